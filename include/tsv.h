@@ -71,7 +71,8 @@ typedef enum {
     TSV_F16 = 0,       /* IEEE binary16 */
     TSV_BF16 = 1,      /* bfloat16 */
     TSV_I8_SCALED = 2, /* int8 code x fp16 per-token scale (KV caches only) */
-    TSV_Q4_G64 = 3     /* 4-bit affine, groups of 64 input features (LM head only) */
+    TSV_Q4_G64 = 3,    /* 4-bit affine, groups of 64 input features (LM head only) */
+    TSV_I4_G64 = 4     /* 4-bit affine, groups of 64 features of a token's row (KV caches only) */
 } tsv_dtype;
 
 /* Device status codes (dev_status word 0). */
@@ -82,6 +83,7 @@ typedef enum {
                                  kept list / kept_len of tsv_gather_positions out of order or range */
 #define TSV_DEV_BAD_KV_LEN 4  /* kv_len[b] < T (< 0 for tsv_gather_positions), or kv_len[b] > capacity */
 #define TSV_DEV_TIMEOUT 5     /* a bounded wait inside a kernel expired (a library bug; outputs unspecified) */
+#define TSV_DEV_BAD_SEQ_LEN 6 /* cu_len not ascending within [0, rows], or a sequence longer than max_len */
 
 #define TSV_MAX_T 64
 #define TSV_MAX_CANDIDATES 1024 /* candidate-tree nodes per sequence for tsv_tree_select */
@@ -194,19 +196,23 @@ tsv_status tsv_tree_select(const int32_t* cand_parents, const int32_t* cand_toke
  *   c > S_b + i - window[l]: the intersection of the tree mask with the
  *   layer's band.  Every node keeps itself.  window[l] == 0 is a full-attention layer.
  *   Accumulation is fp32; O is rounded to bf16 once.
+ *   4-bit caches (TSV_I4_G64, [1185] Phase 3's affine groups of 64 on the cache): byte j of a row holds element 2j in
+ *   its low nibble and 2j + 1 in its high nibble; value = scale * code + bias, with the fp16 pair (scale, bias) of
+ *   its group of 64 features at k_scale[b][h][c][group] (v_scale likewise), 4-byte aligned.
  */
 typedef struct {
     int32_t n_layers;   /* 1 .. TSV_MAX_LAYERS */
     int32_t B, T, HQ, HKV, D; /* HQ % HKV == 0; D in {64, 128, 256} */
     int64_t s_cap;      /* capacity of every cache buffer's sequence axis, in positions */
     int32_t max_kv_len; /* host-known upper bound of every kv_len[b] (<= s_cap); sizes the grid */
-    int32_t kv_dtype;   /* TSV_F16, TSV_BF16 or TSV_I8_SCALED */
+    int32_t kv_dtype;   /* TSV_F16, TSV_BF16, TSV_I8_SCALED or TSV_I4_G64 */
     int32_t splits;     /* key-range splits per (layer, sequence, kv head); 0 = automatic; at most 64 */
     int32_t path;       /* TSV_ATTN_AUTO, TSV_ATTN_SIMT or TSV_ATTN_TCGEN05 */
     const void* q[TSV_MAX_LAYERS];       /* per layer: bf16 [B, T, HQ, D] */
-    const void* k[TSV_MAX_LAYERS];       /* per layer: [B, HKV, s_cap, D] in kv_dtype (int8 codes) */
+    const void* k[TSV_MAX_LAYERS];       /* per layer: [B, HKV, s_cap, D] in kv_dtype (int8 codes; 4-bit: D/2 bytes a row) */
     const void* v[TSV_MAX_LAYERS];       /* per layer: as k */
-    const void* k_scale[TSV_MAX_LAYERS]; /* per layer: fp16 [B, HKV, s_cap] (Int8 only, else NULL) */
+    const void* k_scale[TSV_MAX_LAYERS]; /* per layer: fp16 [B, HKV, s_cap] (Int8), fp16 [B, HKV, s_cap, D/64, 2]
+                                            (4-bit: scale, bias), else NULL */
     const void* v_scale[TSV_MAX_LAYERS]; /* per layer: as k_scale */
     void* o[TSV_MAX_LAYERS];             /* per layer: bf16 [B, T, HQ, D], out */
     const int32_t* kv_len;               /* int32 [B]: S_b + T */
@@ -369,11 +375,11 @@ tsv_status tsv_tree_accept_walk(const int32_t* argmax, const int32_t* tokens, co
 typedef struct {
     int32_t n_layers, B, HKV, D;
     int64_t s_cap;
-    int32_t kv_dtype; /* TSV_F16, TSV_BF16 or TSV_I8_SCALED */
+    int32_t kv_dtype; /* TSV_F16, TSV_BF16, TSV_I8_SCALED or TSV_I4_G64 */
     int32_t reserved;
-    void* k[TSV_MAX_LAYERS];       /* per layer: [B, HKV, s_cap, D] */
+    void* k[TSV_MAX_LAYERS];       /* per layer: [B, HKV, s_cap, D] (4-bit: D/2 bytes a row) */
     void* v[TSV_MAX_LAYERS];
-    void* k_scale[TSV_MAX_LAYERS]; /* per layer: fp16 [B, HKV, s_cap] (Int8 only) */
+    void* k_scale[TSV_MAX_LAYERS]; /* per layer: fp16 [B, HKV, s_cap] (Int8), fp16 [B, HKV, s_cap, D/64, 2] (4-bit) */
     void* v_scale[TSV_MAX_LAYERS];
 } tsv_kv_desc;
 
@@ -427,7 +433,10 @@ tsv_status tsv_gather_positions(const tsv_kv_desc* kv, int32_t* kv_len, const in
  *   per token; a per-token scale maps every single-valued token to the same
  *   code): scale = fp16(absmax / 127) with the division in fp32, code =
  *   round-half-to-even(x / scale) in fp32, clamped to [-127, 127]; a token whose
- *   scale is 0 stores zero codes.  fp16 / bf16 caches store the rotated fp32
+ *   scale is 0 stores zero codes.  4-bit caches: per group of 64 features bias = fp16(minimum), scale =
+ *   fp16((maximum - minimum) / 15) with the division in fp32 (both kept within the finite fp16 range), code =
+ *   round-half-to-even((x - bias) / scale) in fp32, clamped to [0, 15]; a group whose scale is 0 stores zero
+ *   codes.  fp16 / bf16 caches store the rotated fp32
  *   values rounded to nearest even.  Angles are reduced in fp64, so positions
  *   up to 2^31 keep fp32 accuracy.
  *   kv_len: in, S_b per sequence; out, S_b + T.  depth: from tsv_tree_mask.
@@ -439,7 +448,7 @@ typedef struct {
     int32_t n_layers;   /* 1 .. TSV_MAX_LAYERS */
     int32_t B, T, HQ, HKV, D; /* HQ % HKV == 0; D in {64, 128, 256} */
     int64_t s_cap;
-    int32_t kv_dtype;   /* TSV_F16, TSV_BF16 or TSV_I8_SCALED */
+    int32_t kv_dtype;   /* TSV_F16, TSV_BF16, TSV_I8_SCALED or TSV_I4_G64 */
     int32_t rot_dim;    /* even, 2 <= rot_dim <= D; features >= rot_dim are copied */
     int32_t interleaved; /* 0: pairs (j, j + rot_dim/2); 1: pairs (2j, 2j + 1) */
     int32_t reserved;
@@ -456,6 +465,62 @@ typedef struct {
 } tsv_append_desc;
 
 tsv_status tsv_tree_append(const tsv_append_desc* d, int32_t* kv_len, int32_t* dev_status, cudaStream_t stream);
+
+/*
+ * The gated delta rule of a hybrid target's recurrent layers, for n_layers layers at once (three calls).
+ *   [1204] on recurrent layers: recurrent layers cannot take a mask, and a
+ *   flattened tree would leak state between siblings, so every node runs from its own parent's state; [728] "What it
+ *   does": the selected path's recurrent state is the one retained.  The pages do not print the recurrence (reading:
+ *   the published gated delta rule).  For one value head with state S [DV, DK] (fp32), log decay g <= 0, write
+ *   strength beta:
+ *     S <- e^g S;  u = beta (v - S k);  S <- S + u k^T;  o = scale * S q
+ *   Value head h reads key head h / (HV / HK).  With norm_eps > 0 every row of q and k is divided by
+ *   sqrt(sum x^2 + norm_eps) first.  All arithmetic and the state are fp32 (products on the tensor cores take an
+ *   fp32 operand as a sum of bf16 pieces: three for what the state is made of, two for what only reaches o); o is
+ *   rounded to bf16 once.  g may be -infinity (the state is forgotten).
+ *
+ * tsv_gdn_tree_verify - o of every node of each sequence's tree, node i starting from its parent's state and the
+ *   root from state[l][b].  The state is read once and not written (state_out is ignored).  anc: uint64 [B, T] from
+ *   tsv_tree_mask; bits at or above a node's own index are ignored.  A NaN or infinity in one node's inputs reaches
+ *   that node and its descendants only.
+ * tsv_gdn_commit - the state after the accepted path: state_out[l][b] = state[l][b] advanced over the block's rows
+ *   path[b][0 .. path_len[b]).  path and path_len as for tsv_kv_gather_positions (path[b][0] == 0, strictly
+ *   increasing, 1 <= path_len[b] <= T).  q and o are ignored.  Device errors: TSV_DEV_BAD_PATH (that sequence's
+ *   state_out is not written).
+ * tsv_gdn_scan - the state advanced over new tokens (a decoding step, a prompt, or a ragged batch of both), with
+ *   every token's o.  q, k, v, g, beta and o hold T packed rows; sequence b owns rows cu_len[b] .. cu_len[b + 1]
+ *   (int32 [B + 1] on the device, ascending, within [0, T]; a sequence without rows keeps its state, which is copied
+ *   to state_out).  max_len: host-known upper bound of every sequence's rows (<= T); it picks the kernel.  Rows that
+ *   no sequence owns are not read and their o is not written.  Device errors: TSV_DEV_BAD_SEQ_LEN (that sequence's
+ *   o and state_out are not written).
+ *
+ * state_out[l] may equal state[l] (in place); otherwise they must not overlap, nor may o overlap an input.
+ */
+typedef struct {
+    int32_t n_layers;   /* 1 .. TSV_MAX_LAYERS */
+    int32_t B, T;       /* T: nodes per tree (verify, commit: 1 .. 64) or packed rows in all (scan) */
+    int32_t HK, HV;     /* HV % HK == 0 */
+    int32_t DK, DV;     /* each 64 or 128 */
+    float norm_eps;     /* 0: q and k are taken as they are */
+    float scale;        /* on q; 0: 1 / sqrt(DK) */
+    int32_t reserved;
+    const void* q[TSV_MAX_LAYERS];     /* per layer: bf16 [B, T, HK, DK] (scan: [T, HK, DK]) */
+    const void* k[TSV_MAX_LAYERS];     /* per layer: as q */
+    const void* v[TSV_MAX_LAYERS];     /* per layer: bf16 [B, T, HV, DV] */
+    const float* g[TSV_MAX_LAYERS];    /* per layer: fp32 [B, T, HV], log decay */
+    const float* beta[TSV_MAX_LAYERS]; /* per layer: fp32 [B, T, HV] */
+    const float* state[TSV_MAX_LAYERS]; /* per layer: fp32 [B, HV, DV, DK] */
+    float* state_out[TSV_MAX_LAYERS];   /* per layer: as state, out (commit, scan) */
+    void* o[TSV_MAX_LAYERS];            /* per layer: bf16 as v, out (verify, scan) */
+} tsv_gdn_desc;
+
+tsv_status tsv_gdn_tree_verify(const tsv_gdn_desc* d, const uint64_t* anc, int32_t* dev_status, cudaStream_t stream);
+
+tsv_status tsv_gdn_commit(const tsv_gdn_desc* d, const int32_t* path, const int32_t* path_len, int32_t* dev_status,
+                          cudaStream_t stream);
+
+tsv_status tsv_gdn_scan(const tsv_gdn_desc* d, const int32_t* cu_len, int32_t max_len, int32_t* dev_status,
+                        cudaStream_t stream);
 
 #ifdef __cplusplus
 }

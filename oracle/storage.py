@@ -48,14 +48,23 @@ def q4_affine(packed, scale_bits, bias_bits, group: int = 64) -> np.ndarray:
     return s * q + b
 
 
+def int4_affine(packed, pair_bits, group: int = 64) -> np.ndarray:
+    """4-bit cache rows uint8 [..., D/2] with fp16 (scale, bias) pairs [..., D/group, 2] -> fp64 values [..., D]."""
+    q = unpack_q4(packed).astype(np.float64)
+    pair = f16(pair_bits)
+    return q * np.repeat(pair[..., 0], group, axis=-1) + np.repeat(pair[..., 1], group, axis=-1)
+
+
 def kv_values(dtype: int, store, scale_bits=None) -> np.ndarray:
-    """KV storage of format ``dtype`` (0 fp16, 1 bf16, 2 int8+scales) -> fp64."""
+    """KV storage of format ``dtype`` (0 fp16, 1 bf16, 2 int8+scales, 4 affine 4-bit) -> fp64."""
     if dtype == 0:
         return f16(store)
     if dtype == 1:
         return bf16(store)
     if dtype == 2:
         return int8_scaled(store, scale_bits)
+    if dtype == 4:
+        return int4_affine(store, scale_bits)
     raise ValueError(f"not a KV format: {dtype}")
 
 

@@ -1,0 +1,439 @@
+"""GPU parity of the recurrent calls (gated delta rule) against the fp64 recurrence.
+
+Tolerances.  With unit keys and 0 <= beta <= 1 every step multiplies the state by e^g (I - beta k k^T), of norm at
+most 1, so an error made at one token is never amplified by later ones: n tokens add up to n times what one token can
+add.  One token's fp32 products over DK <= 128 terms, its decay (exp within 2 ulp, G from fp64) and its write are each
+within (DK / 8 + 8) * 2^-24 of the magnitudes that enter it, M = max row norm of the state + max |v| along the run.
+Where the tensor cores take an fp32 operand as two bf16 pieces (what only reaches o) its error is 2^-16 of M for each
+of a node's products.  o is rounded to bf16 once: 2^-8 |o|.
+"""
+import numpy as np
+import pytest
+import torch
+
+from oracle import gdn as og
+
+pytestmark = pytest.mark.gpu
+DEV = "cuda"
+
+
+def case(seed, L, B, rows, HK, HV, DK, DV, gate="usual"):
+    """bf16 / fp32 inputs on the device; rows is (B, T) or (n,)."""
+    gen = torch.Generator().manual_seed(seed)
+    n = lambda *s: torch.randn(*s, generator=gen)  # noqa: E731
+    g = -torch.exp(n(L, *rows, HV) - 2.0)
+    if gate == "none":
+        g = torch.zeros_like(g)
+    elif gate == "strong":
+        g = g * 60.0
+    elif gate == "forget":  # some tokens forget everything
+        g[torch.rand(g.shape, generator=gen) < 0.2] = -float("inf")
+    c = dict(q=n(L, *rows, HK, DK).bfloat16(), k=n(L, *rows, HK, DK).bfloat16(), v=n(L, *rows, HV, DV).bfloat16(), g=g,
+             beta=torch.sigmoid(n(L, *rows, HV)), state=0.3 * n(L, B, HV, DV, DK))
+    return {k: v.to(DEV) for k, v in c.items()}
+
+
+def per(x, L):
+    return [x[l] for l in range(L)]
+
+
+def unit(x, eps):
+    x = x.double()
+    return x if eps == 0 else x / torch.sqrt((x * x).sum(-1, keepdim=True) + eps)
+
+
+def ref_run(c, l, rows, parents, state, eps, scale):
+    """fp64 recurrence over the rows `rows` (indices into the layer's rows), node i starting from parents[i]'s state
+    (-1: `state`).  -> (o [n, HV, DV], states [n, HV, DV, DK], M)."""
+    HV = c["v"].shape[-2]
+    flat = lambda x: x[l].reshape(-1, *x.shape[-2:])[rows]  # noqa: E731
+    rep = HV // c["k"].shape[-2]
+    q = unit(flat(c["q"]), eps).repeat_interleave(rep, dim=1)
+    k = unit(flat(c["k"]), eps).repeat_interleave(rep, dim=1)
+    v = flat(c["v"]).double()
+    g, beta = (c[x][l].reshape(-1, HV)[rows].double() for x in ("g", "beta"))
+    states, outs = [], []
+    M = state.norm(dim=-1).max().item()
+    for i, p in enumerate(parents):
+        S = state.double() if p < 0 else states[p]
+        S = torch.exp(g[i])[:, None, None] * S
+        u = beta[i][:, None] * (v[i] - torch.einsum("hvk,hk->hv", S, k[i]))
+        S = S + torch.einsum("hv,hk->hvk", u, k[i])
+        states.append(S)
+        outs.append(torch.einsum("hvk,hk->hv", S, q[i]) * scale)
+        M = max(M, S.norm(dim=-1).max().item())
+    return torch.stack(outs), states, M + v.abs().max().item()
+
+
+def close_o(got, want, M, n, DK, scale, pieces=True):
+    """Every element of o; M and the products' errors carry the factor scale (q is a unit row times it)."""
+    per_node = (DK / 8 + 8) * 2.0 ** -24 + (4 * 2.0 ** -16 if pieces else 0.0)
+    tol = 2.0 ** -8 * want.abs() + n * per_node * M * scale
+    err = (got.double() - want).abs()
+    assert torch.isfinite(got).all()
+    assert (err <= tol).all(), (err - tol).max().item()
+    # half a step of bf16 is at most 2^-8 of each value, so of the norm too; the pieces add well under 2^-11
+    assert err.norm() <= (2.0 ** -8 + 2.0 ** -11) * want.norm() + 1e-30
+
+
+def close_state(got, want, M, n, DK):
+    err = (got.double() - want).abs().max().item()
+    assert err <= n * (DK / 8 + 8) * 2.0 ** -24 * M, (err, M, n)
+    assert (got.double() - want).norm() <= 2.0 ** -18 * want.norm() + 1e-30  # far below the worst case: errors mix signs
+
+
+def tree(rng, T, style):
+    if style == "chain":
+        return [-1] + list(range(T - 1))
+    if style == "star":
+        return [-1] + [0] * (T - 1)
+    return [-1] + [int(rng.integers(max(0, i - 6), i)) for i in range(1, T)]
+
+
+def anc_of(tsv, parents):
+    par = torch.tensor(np.array(parents, dtype=np.int32), device=DEV)
+    B, T = par.shape
+    anc = torch.zeros(B, T, dtype=torch.int64, device=DEV)
+    tsv.tree_mask(par, anc, torch.zeros(B, T, dtype=torch.int32, device=DEV))
+    return anc
+
+
+def verify(tsv, c, parents, eps=1e-6, scale=0.0, anc=None):
+    L = c["k"].shape[0]
+    o = torch.full_like(c["v"], float("nan"))
+    before = c["state"].clone()
+    st = torch.zeros(4, dtype=torch.int32, device=DEV)
+    d = tsv.gdn_desc(*(per(c[x], L) for x in ("q", "k", "v", "g", "beta", "state")), o=per(o, L), norm_eps=eps, scale=scale)
+    tsv.gdn_tree_verify(d, anc_of(tsv, parents) if anc is None else anc, dev_status=st)
+    torch.cuda.synchronize()
+    assert st.tolist() == [0, 0, 0, 0]
+    assert torch.equal(c["state"], before)
+    return o
+
+
+def check_verify(tsv, c, parents, eps=1e-6, scale=0.0):
+    o = verify(tsv, c, parents, eps, scale)
+    L, B, T = c["k"].shape[:3]
+    sc = scale or c["k"].shape[-1] ** -0.5
+    for l in range(L):
+        for b in range(B):
+            want, _, M = ref_run(c, l, slice(b * T, (b + 1) * T), parents[b], c["state"][l, b], eps, sc)
+            close_o(o[l, b], want, M, T, c["k"].shape[-1], sc)
+
+
+@pytest.mark.parametrize("style", ["random", "chain", "star"])
+@pytest.mark.parametrize("T", [1, 2, 3, 5, 8, 9, 15, 16, 17, 24, 31, 32, 33, 48, 49, 63, 64])
+def test_tree_verify_sizes(gpu_lib, T, style):
+    rng = np.random.default_rng(T)
+    check_verify(gpu_lib, case(T, 1, 2, (2, T), 2, 6, 128, 128), [tree(rng, T, style) for _ in range(2)])
+
+
+@pytest.mark.parametrize("DK, DV", [(64, 64), (64, 128), (128, 64), (128, 128)])
+@pytest.mark.parametrize("HK, HV", [(1, 1), (2, 8), (5, 5)])
+@pytest.mark.parametrize("T", [4, 20, 64])
+def test_tree_verify_heads(gpu_lib, T, HK, HV, DK, DV):
+    rng = np.random.default_rng(T + DK)
+    check_verify(gpu_lib, case(T, 3, 1, (1, T), HK, HV, DK, DV), [tree(rng, T, "random")])
+
+
+@pytest.mark.parametrize("gate", ["none", "strong", "forget"])
+@pytest.mark.parametrize("T", [3, 16, 64])
+def test_tree_verify_gates(gpu_lib, T, gate):
+    rng = np.random.default_rng(T)
+    check_verify(gpu_lib, case(T, 1, 2, (2, T), 1, 2, 128, 128, gate), [tree(rng, T, s) for s in ("random", "chain")])
+
+
+@pytest.mark.parametrize("T", [3, 40])
+def test_tree_verify_without_norms_and_with_a_scale(gpu_lib, T):
+    c = case(T, 1, 1, (1, T), 2, 2, 128, 128)
+    for x in "qk":  # already unit rows, rounded to bf16 (norm within 2^-8 of 1)
+        c[x] = unit(c[x], 1e-6).bfloat16()
+    c["k"] = c["k"] * 0.5
+    check_verify(gpu_lib, c, [tree(np.random.default_rng(1), T, "random")], eps=0.0, scale=0.25)
+
+
+@pytest.mark.parametrize("T", [6, 16, 30, 64])
+@pytest.mark.parametrize("what", ["v", "k", "q", "g", "beta", "inf"])
+def test_a_nan_stays_with_its_node_and_descendants(gpu_lib, T, what):
+    rng = np.random.default_rng(T)
+    par = tree(rng, T, "random")
+    j = T // 3
+    below = [i for i in range(T) if j in _path(par, i)]
+    c = case(T, 1, 1, (1, T), 1, 2, 128, 128)
+    clean = verify(gpu_lib, c, [par])
+    x = c["v" if what == "inf" else what]
+    x[0, 0, j] = float("inf") if what == "inf" else float("nan")
+    o = verify(gpu_lib, c, [par])
+    rest = [i for i in range(T) if i not in below]
+    assert torch.isfinite(o[0, 0, rest]).all()
+    # the clean run's values, up to the two ways a tree may be computed
+    err = (o[0, 0, rest].double() - clean[0, 0, rest].double()).abs()
+    assert (err <= 2.0 ** -7 * clean[0, 0, rest].double().abs() + 1e-3).all()
+    assert not torch.isfinite(o[0, 0, j]).any()
+
+
+def _path(par, i):
+    out = [i]
+    while par[out[-1]] >= 0:
+        out.append(par[out[-1]])
+    return out
+
+
+@pytest.mark.parametrize("T", [5, 33])
+def test_ancestor_bits_at_or_above_a_node_are_ignored(gpu_lib, T):
+    rng = np.random.default_rng(T)
+    par = tree(rng, T, "random")
+    c = case(T, 1, 1, (1, T), 1, 1, 128, 128)
+    anc = anc_of(gpu_lib, [par])
+    high = torch.tensor([[-(1 << i) if i < 63 else -(1 << 63) for i in range(T)]], device=DEV)
+    assert torch.equal(verify(gpu_lib, c, [par]), verify(gpu_lib, c, [par], anc=anc | high))
+
+
+def commit(tsv, c, path, path_len, state_out=None, st=None):
+    L = c["k"].shape[0]
+    st = torch.zeros(4, dtype=torch.int32, device=DEV) if st is None else st
+    d = tsv.gdn_desc(None, *(per(c[x], L) for x in ("k", "v", "g", "beta", "state")),
+                     state_out=None if state_out is None else per(state_out, L))
+    tsv.gdn_commit(d, torch.tensor(path, dtype=torch.int32, device=DEV), torch.tensor(path_len, dtype=torch.int32, device=DEV),
+                   dev_status=st)
+    torch.cuda.synchronize()
+    return st
+
+
+@pytest.mark.parametrize("DK, DV, HK, HV", [(128, 128, 2, 6), (64, 64, 1, 2), (64, 128, 3, 3), (128, 64, 1, 4)])
+@pytest.mark.parametrize("T, paths", [(1, [[0]]), (16, [[0, 2, 5, 11, 15], [0], [0, 1, 2, 3]]), (64, [list(range(64)), [0, 63]])])
+def test_commit(gpu_lib, T, paths, DK, DV, HK, HV):
+    B = len(paths)
+    c = case(T, 2, B, (B, T), HK, HV, DK, DV)
+    padded, lens = [p + [-1] * (T - len(p)) for p in paths], [len(p) for p in paths]
+    out = torch.full_like(c["state"], float("nan"))
+    before = c["state"].clone()
+    assert commit(gpu_lib, c, padded, lens, out).tolist() == [0, 0, 0, 0]
+    assert torch.equal(c["state"], before)
+    for l in range(2):
+        for b, p in enumerate(paths):
+            _, S, M = ref_run(c, l, [b * T + j for j in p], list(range(-1, len(p) - 1)), c["state"][l, b], 1e-6, 1.0)
+            close_state(out[l, b], S[-1], M, len(p), DK)
+    assert commit(gpu_lib, c, padded, lens).tolist() == [0, 0, 0, 0]  # in place
+    assert torch.equal(c["state"], out)
+
+
+@pytest.mark.parametrize("path, n", [([1, 2, 3, 3], 2), ([0, 2, 2, 3], 3), ([0, 3, 1, 2], 3), ([0, 4, -1, -1], 2), ([0, 1, 2, 3], 0),
+                                     ([0, 1, 2, 3], 5), ([0, -1, 2, 3], 3), ([0, 1, 2, 3], -7), ([0, 1 << 30, 2, 3], 2)])
+def test_commit_reports_a_bad_path_and_leaves_that_sequence(gpu_lib, path, n):
+    c = case(1, 1, 2, (2, 4), 1, 2, 128, 128)
+    out = torch.full_like(c["state"], 7.0)
+    st = commit(gpu_lib, c, [[0, 1, 2, 3], path], [2, n], out)
+    assert st.tolist()[:2] == [gpu_lib.DEV_BAD_PATH, 1]
+    assert (out[:, 1] == 7.0).all()
+    _, S, M = ref_run(c, 0, [0, 1], [-1, 0], c["state"][0, 0], 1e-6, 1.0)
+    close_state(out[0, 0], S[-1], M, 2, 128)
+
+
+def scan(tsv, c, cu, max_len, state_out=None, o=None, st=None, eps=1e-6, scale=0.0):
+    L = c["k"].shape[0]
+    o = torch.full_like(c["v"], -77.0) if o is None else o
+    st = torch.zeros(4, dtype=torch.int32, device=DEV) if st is None else st
+    d = tsv.gdn_desc(*(per(c[x], L) for x in ("q", "k", "v", "g", "beta", "state")), o=per(o, L),
+                     state_out=None if state_out is None else per(state_out, L), norm_eps=eps, scale=scale)
+    tsv.gdn_scan(d, torch.tensor(cu, dtype=torch.int32, device=DEV), max_len=max_len, dev_status=st)
+    torch.cuda.synchronize()
+    return o, st
+
+
+def check_scan(tsv, c, lens, max_len=None, lead=0, eps=1e-6, scale=0.0, layers=None):
+    """lens: tokens per sequence; `lead` rows ahead of the first sequence and whatever follows the last are no one's."""
+    DK = c["k"].shape[-1]
+    cu = [lead]
+    for n in lens:
+        cu.append(cu[-1] + n)
+    out = torch.full_like(c["state"], float("nan"))
+    before = c["state"].clone()
+    o, st = scan(tsv, c, cu, max(lens) if max_len is None else max_len, out, eps=eps, scale=scale)
+    assert st.tolist() == [0, 0, 0, 0]
+    assert torch.equal(c["state"], before)
+    assert (o[:, :lead] == -77.0).all() and (o[:, cu[-1]:] == -77.0).all()
+    sc = scale or DK ** -0.5
+    for l in range(c["k"].shape[0]):
+        for b, n in enumerate(lens):
+            if n == 0:
+                assert torch.equal(out[l, b], c["state"][l, b])
+                continue
+            want, S, M = ref_run(c, l, slice(cu[b], cu[b + 1]), list(range(-1, n - 1)), c["state"][l, b], eps, sc)
+            close_o(o[l, cu[b]:cu[b + 1]], want, M, n, DK, sc)
+            close_state(out[l, b], S[-1], M, n, DK)
+    return o, out
+
+
+@pytest.mark.parametrize("lens", [[1], [1, 1, 1, 1, 1], [0, 1, 0], [2], [3, 7, 8], [9], [16], [17, 1, 0, 33], [63], [64], [65],
+                                  [127, 128, 129], [200, 0, 5, 64, 1, 190], [500]])
+def test_scan_lengths(gpu_lib, lens):
+    total = sum(lens) + 5
+    check_scan(gpu_lib, case(total, 1, len(lens), (total,), 2, 6, 128, 128), lens, lead=2)
+
+
+@pytest.mark.parametrize("DK, DV", [(64, 64), (64, 128), (128, 64), (128, 128)])
+@pytest.mark.parametrize("HK, HV", [(1, 1), (2, 8), (5, 5)])
+@pytest.mark.parametrize("lens", [[1, 1], [70, 3, 130]])
+def test_scan_heads(gpu_lib, lens, HK, HV, DK, DV):
+    check_scan(gpu_lib, case(7, 2, len(lens), (sum(lens),), HK, HV, DK, DV), lens)
+
+
+@pytest.mark.parametrize("gate", ["none", "strong", "forget"])
+@pytest.mark.parametrize("lens", [[4, 1], [150, 64]])
+def test_scan_gates(gpu_lib, lens, gate):
+    check_scan(gpu_lib, case(8, 1, 2, (sum(lens),), 1, 3, 128, 128, gate), lens)
+
+
+def test_scan_with_equal_keys_and_full_writes(gpu_lib):
+    """Keys all alike and beta = 1: each token overwrites what the one before wrote, the system's worst conditioning."""
+    c = case(9, 1, 1, (200,), 1, 2, 128, 128, "none")
+    c["k"][:] = c["k"][:, :1]
+    c["beta"][:] = 1.0
+    check_scan(gpu_lib, c, [200])
+
+
+def test_scan_without_norms_and_with_a_scale(gpu_lib):
+    c = case(10, 1, 2, (150,), 2, 2, 128, 128)
+    for x in "qk":
+        c[x] = unit(c[x], 1e-6).bfloat16() * 0.5
+    check_scan(gpu_lib, c, [131, 19], eps=0.0, scale=0.25)
+
+
+@pytest.mark.parametrize("lens", [[5, 3], [150, 70]])
+def test_a_max_len_above_the_lengths(gpu_lib, lens):
+    check_scan(gpu_lib, case(11, 1, 2, (300,), 1, 2, 128, 128), lens, max_len=300)
+
+
+def test_scan_in_parts_is_the_whole_scan(gpu_lib):
+    c = case(12, 1, 1, (200,), 1, 4, 128, 128)
+    o, out = check_scan(gpu_lib, c, [200])
+    for parts in ([64, 136], [1, 199], [100, 3, 97]):
+        state, at, rows = c["state"].clone(), 0, []
+        for n in parts:
+            part = {x: c[x][:, at:at + n].contiguous() for x in ("q", "k", "v", "g", "beta")}
+            part["state"] = state
+            rows.append(scan(gpu_lib, part, [0, n], n)[0])  # in place
+            at += n
+        want, S, M = ref_run(c, 0, slice(0, 200), list(range(-1, 199)), c["state"][0, 0], 1e-6, 128 ** -0.5)
+        close_o(torch.cat(rows, dim=1)[0], want, M, 200, 128, 128 ** -0.5)
+        close_state(state[0, 0], S[-1], M, 200, 128)
+
+
+@pytest.mark.parametrize("long", [False, True])
+def test_scan_reports_bad_lengths_and_leaves_those_sequences(gpu_lib, long):
+    """Descending, beyond the rows, below zero, longer than max_len: that sequence is left, the others are computed."""
+    n, top = (90, 90) if long else (4, 4)
+    rows = 2 * n
+    c = case(13, 1, 3, (rows,), 1, 2, 128, 128)
+    for cu, bad, max_len in (([0, n, n - 1, rows], 1, max(n + 1, top)), ([0, n, 2 * n, 2 * n + 1], 2, top), ([-1, n, n, n], 0, n + 1),
+                             ([0, n, n + n, n + n], 0, n - 1)):
+        out = torch.full_like(c["state"], 7.0)
+        o, st = scan(gpu_lib, c, cu, min(max_len, rows), out)
+        assert st.tolist()[0] == gpu_lib.DEV_BAD_SEQ_LEN
+        assert (out[:, bad] == 7.0).all()
+        for b in range(3):
+            if cu[b] >= 0 and 0 < cu[b + 1] - cu[b] <= max_len and cu[b + 1] <= rows and b != bad:
+                _, S, M = ref_run(c, 0, slice(cu[b], cu[b + 1]), list(range(-1, cu[b + 1] - cu[b] - 1)), c["state"][0, b], 1e-6, 1.0)
+                close_state(out[0, b], S[-1], M, cu[b + 1] - cu[b], 128)
+
+
+@pytest.mark.parametrize("n, j", [(5, 2), (150, 70), (150, 149), (150, 64)])
+@pytest.mark.parametrize("what", ["v", "k", "g"])
+def test_a_nan_reaches_later_tokens_only(gpu_lib, n, j, what):
+    c = case(14, 1, 2, (2 * n,), 1, 2, 128, 128)
+    clean, _ = scan(gpu_lib, c, [0, n, 2 * n], n, torch.empty_like(c["state"]))
+    c[what][0, j] = float("nan")
+    o, _ = scan(gpu_lib, c, [0, n, 2 * n], n, torch.empty_like(c["state"]))
+    for rows in (slice(0, j), slice(n, 2 * n)):
+        assert torch.isfinite(o[0, rows]).all()
+        err = (o[0, rows].double() - clean[0, rows].double()).abs()
+        assert (err <= 2.0 ** -7 * clean[0, rows].double().abs() + 1e-3).all()
+    assert not torch.isfinite(o[0, j:n]).any()
+
+
+def test_a_nan_in_one_value_feature_stays_there(gpu_lib):
+    c = case(15, 1, 1, (150,), 1, 1, 128, 128)
+    clean, s0 = scan(gpu_lib, c, [0, 150], 150, torch.empty_like(c["state"]))
+    c["v"][0, 20, 0, 5] = float("nan")
+    out = torch.empty_like(c["state"])
+    o, _ = scan(gpu_lib, c, [0, 150], 150, out)
+    keep = [f for f in range(128) if f != 5]
+    assert torch.isfinite(o[0, :, 0][:, keep]).all() and torch.isfinite(out[0, 0, 0][keep]).all()
+    assert torch.isfinite(o[0, :20]).all() and torch.isnan(o[0, 20:, 0, 5]).all()
+
+
+def test_streams_and_graphs(gpu_lib):
+    """The three calls on a side stream, and captured twice over different buffers and replayed in turn."""
+    L, B, T = 2, 2, 12
+    rng = np.random.default_rng(3)
+    par = [tree(rng, T, "random") for _ in range(B)]
+    anc = anc_of(gpu_lib, par)
+    path = torch.tensor([[0, 2, 7] + [-1] * (T - 3), [0] + [-1] * (T - 1)], dtype=torch.int32, device=DEV)
+    plen = torch.tensor([3, 1], dtype=torch.int32, device=DEV)
+    cu = torch.tensor([0, 100, 130], dtype=torch.int32, device=DEV)
+    sets = []
+    for seed in (1, 2):
+        t, s = case(seed, L, B, (B, T), 2, 4, 128, 128), case(seed + 9, L, B, (130,), 2, 4, 128, 128)
+        o, so = torch.empty_like(t["v"]), torch.empty_like(s["v"])
+        t_out, s_out = torch.empty_like(t["state"]), torch.empty_like(s["state"])
+        f = lambda c, **kw: gpu_lib.gdn_desc(*(per(c[x], L) for x in ("q", "k", "v", "g", "beta", "state")),  # noqa: E731
+                                             **{k: per(v, L) for k, v in kw.items()})
+        dt, ds = f(t, o=o, state_out=t_out), f(s, o=so, state_out=s_out)
+        sets.append((t, s, (o, so, t_out, s_out), dt, ds))
+
+    def calls(dt, ds):
+        gpu_lib.gdn_tree_verify(dt, anc)
+        gpu_lib.gdn_commit(dt, path, plen)
+        gpu_lib.gdn_scan(ds, cu, max_len=100)
+
+    want = []
+    for _, _, outs, dt, ds in sets:
+        calls(dt, ds)
+        torch.cuda.synchronize()
+        want.append([x.clone() for x in outs])
+        for x in outs:
+            x.zero_()
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        calls(sets[0][3], sets[0][4])
+    torch.cuda.synchronize()
+    assert all(torch.equal(a, b) for a, b in zip(sets[0][2], want[0]))
+    graphs = []
+    for _, _, outs, dt, ds in sets:
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            calls(dt, ds)
+        graphs.append(g)
+    for _ in range(2):
+        for s, w, g in zip(sets, want, graphs):
+            for x in s[2]:
+                x.zero_()
+            g.replay()
+        torch.cuda.synchronize()
+        for s, w in zip(sets, want):
+            assert all(torch.equal(a, b) for a, b in zip(s[2], w))
+
+
+def test_the_binding_refuses_the_wrong_layout(gpu_lib):
+    c, p = case(1, 1, 1, (1, 4), 1, 1, 128, 128), case(1, 1, 1, (4,), 1, 1, 128, 128)
+    f = lambda c: gpu_lib.gdn_desc(*(per(c[x], 1) for x in ("q", "k", "v", "g", "beta", "state")), o=per(c["v"].clone(), 1))  # noqa: E731
+    cu = torch.tensor([0, 4], dtype=torch.int32, device=DEV)
+    with pytest.raises(ValueError, match="packed"):
+        gpu_lib.gdn_scan(f(c), cu, max_len=4)
+    with pytest.raises(ValueError, match="tree block"):
+        gpu_lib.gdn_tree_verify(f(p), torch.zeros(1, 4, dtype=torch.int64, device=DEV))
+    with pytest.raises(ValueError, match="contiguous"):
+        gpu_lib.gdn_desc(*(per(c[x], 1) for x in ("q", "k", "v", "g", "beta")), [c["state"][0].transpose(-1, -2)])
+    with pytest.raises(ValueError, match="cu_len"):
+        gpu_lib.gdn_scan(f(p), cu[:1], max_len=4)
+
+
+def test_small_tree_against_the_numpy_oracle(gpu_lib):
+    c = case(4, 1, 1, (1, 7), 2, 4, 64, 64)
+    par = [-1, 0, 0, 1, 1, 2, 2]
+    o = verify(gpu_lib, c, [par])
+    n = {x: c[x][0, 0].double().cpu().numpy() for x in ("q", "k", "v", "g", "beta", "state")}
+    want = og.tree_verify(n["q"], n["k"], n["v"], n["g"], n["beta"], n["state"], par)
+    assert np.abs(o[0, 0].double().cpu().numpy() - want).max() <= 2.0 ** -8 * np.abs(want).max() + 1e-4

@@ -12,8 +12,8 @@ _HERE = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(_HERE, "libtsv.so")
 
 OK, EINVAL, ETOPOLOGY, EUNSUPPORTED, ECAPACITY, ECUDA = range(6)
-F16, BF16, I8_SCALED, Q4_G64 = range(4)
-DEV_OK, DEV_BAD_ROOT, DEV_BAD_PARENT, DEV_BAD_PATH, DEV_BAD_KV_LEN, DEV_TIMEOUT = range(6)
+F16, BF16, I8_SCALED, Q4_G64, I4_G64 = range(5)
+DEV_OK, DEV_BAD_ROOT, DEV_BAD_PARENT, DEV_BAD_PATH, DEV_BAD_KV_LEN, DEV_TIMEOUT, DEV_BAD_SEQ_LEN = range(7)
 ATTN_AUTO, ATTN_SIMT, ATTN_TCGEN05, ATTN_TCGEN05_64, ATTN_TCGEN05_128 = range(5)
 MAX_T = 64
 MAX_CANDIDATES = 1024
@@ -55,6 +55,15 @@ class AppendDesc(C.Structure):
     ]
 
 
+class GdnDesc(C.Structure):
+    _fields_ = [
+        ("n_layers", _i32), ("B", _i32), ("T", _i32), ("HK", _i32), ("HV", _i32), ("DK", _i32), ("DV", _i32),
+        ("norm_eps", C.c_float), ("scale", C.c_float), ("reserved", _i32),
+        ("q", _vp * MAX_LAYERS), ("k", _vp * MAX_LAYERS), ("v", _vp * MAX_LAYERS), ("g", _vp * MAX_LAYERS),
+        ("beta", _vp * MAX_LAYERS), ("state", _vp * MAX_LAYERS), ("state_out", _vp * MAX_LAYERS), ("o", _vp * MAX_LAYERS),
+    ]
+
+
 SIGNATURES = {
     "tsv_last_error": (C.c_char_p, []),
     "tsv_version": (C.c_int, []),
@@ -76,6 +85,9 @@ SIGNATURES = {
     "tsv_kv_gather_positions": (C.c_int, [C.POINTER(KvDesc), _vp, _vp, _vp, _i32, _vp, _vp]),
     "tsv_gather_positions": (C.c_int, [C.POINTER(KvDesc), _vp, _vp, _vp, _i32, _vp, _vp]),
     "tsv_tree_append": (C.c_int, [C.POINTER(AppendDesc), _vp, _vp, _vp]),
+    "tsv_gdn_tree_verify": (C.c_int, [C.POINTER(GdnDesc), _vp, _vp, _vp]),
+    "tsv_gdn_commit": (C.c_int, [C.POINTER(GdnDesc), _vp, _vp, _vp, _vp]),
+    "tsv_gdn_scan": (C.c_int, [C.POINTER(GdnDesc), _vp, _i32, _vp, _vp]),
 }
 
 _lib = None

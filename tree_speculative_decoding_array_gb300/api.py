@@ -13,9 +13,9 @@ from dataclasses import dataclass, field
 import torch
 
 from . import _abi
-from ._abi import BF16, F16, I8_SCALED, MAX_LAYERS, Q4_G64, AppendDesc, AttnDesc, KvDesc, check, load
+from ._abi import BF16, F16, I4_G64, I8_SCALED, MAX_LAYERS, Q4_G64, AppendDesc, AttnDesc, GdnDesc, KvDesc, check, load
 
-KV_TORCH_DTYPE = {F16: torch.float16, BF16: torch.bfloat16, I8_SCALED: torch.int8}
+KV_TORCH_DTYPE = {F16: torch.float16, BF16: torch.bfloat16, I8_SCALED: torch.int8, I4_G64: torch.uint8}
 
 
 def _p(t):
@@ -38,6 +38,26 @@ def _cuda(t, name, dtype=None, shape=None):
         raise ValueError(f"{name} must be {dtype}, got {t.dtype}")
     if shape is not None and tuple(t.shape) != tuple(shape):
         raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
+
+
+def _cache_layer(d, l, k, v, k_scale, v_scale, kv_dtype, shape):
+    """Checks one layer's cache buffers of shape [B, HKV, s_cap, D] and enters them into the descriptor.
+
+    4-bit caches (I4_G64) are uint8 [B, HKV, s_cap, D / 2] with fp16 (scale, bias) pairs [B, HKV, s_cap, D / 64, 2].
+    """
+    B, HKV, s_cap, D = shape
+    kvt = KV_TORCH_DTYPE[kv_dtype]
+    row = D // 2 if kv_dtype == I4_G64 else D
+    _cuda(k[l], "k", kvt, (B, HKV, s_cap, row))
+    _cuda(v[l], "v", kvt, (B, HKV, s_cap, row))
+    d.k[l], d.v[l] = k[l].data_ptr(), v[l].data_ptr()
+    if kv_dtype in (I8_SCALED, I4_G64):
+        if k_scale is None or v_scale is None:
+            raise ValueError("a quantised cache needs k_scale and v_scale")
+        sc = (B, HKV, s_cap) if kv_dtype == I8_SCALED else (B, HKV, s_cap, D // 64, 2)
+        _cuda(k_scale[l], "k_scale", torch.float16, sc)
+        _cuda(v_scale[l], "v_scale", torch.float16, sc)
+        d.k_scale[l], d.v_scale[l] = k_scale[l].data_ptr(), v_scale[l].data_ptr()
 
 
 # ----------------------------------------------------------------------------- a1 tree mask
@@ -96,6 +116,7 @@ def tree_select(cand_parents, cand_tokens, cand_logp, parents, tokens, cand_inde
 def attn_desc(q, k, v, o, kv_len, anc, *, T, HQ, HKV, D, kv_dtype, max_kv_len, k_scale=None, v_scale=None,
               splits=0, path=0, window=None) -> AttnDesc:
     """Descriptor over per-layer lists: q/o bf16 [B,T,HQ,D]; k/v [B,HKV,s_cap,D]; scales fp16 [B,HKV,s_cap].
+    4-bit caches (I4_G64): k/v uint8 [B,HKV,s_cap,D/2], scales fp16 [B,HKV,s_cap,D/64,2] (scale, bias).
 
     window: per-layer sliding windows (0 = full attention), or None for all full-attention layers.
     """
@@ -109,17 +130,11 @@ def attn_desc(q, k, v, o, kv_len, anc, *, T, HQ, HKV, D, kv_dtype, max_kv_len, k
     d = AttnDesc()
     d.n_layers, d.B, d.T, d.HQ, d.HKV, d.D = n, B, T, HQ, HKV, D
     d.s_cap, d.max_kv_len, d.kv_dtype, d.splits, d.path = s_cap, int(max_kv_len), kv_dtype, int(splits), int(path)
-    kvt = KV_TORCH_DTYPE[kv_dtype]
     for l in range(n):
         _cuda(q[l], "q", torch.bfloat16, (B, T, HQ, D))
         _cuda(o[l], "o", torch.bfloat16, (B, T, HQ, D))
-        _cuda(k[l], "k", kvt, (B, HKV, s_cap, D))
-        _cuda(v[l], "v", kvt, (B, HKV, s_cap, D))
-        d.q[l], d.k[l], d.v[l], d.o[l] = q[l].data_ptr(), k[l].data_ptr(), v[l].data_ptr(), o[l].data_ptr()
-        if kv_dtype == I8_SCALED:
-            _cuda(k_scale[l], "k_scale", torch.float16, (B, HKV, s_cap))
-            _cuda(v_scale[l], "v_scale", torch.float16, (B, HKV, s_cap))
-            d.k_scale[l], d.v_scale[l] = k_scale[l].data_ptr(), v_scale[l].data_ptr()
+        d.q[l], d.o[l] = q[l].data_ptr(), o[l].data_ptr()
+        _cache_layer(d, l, k, v, k_scale, v_scale, kv_dtype, (B, HKV, s_cap, D))
     _cuda(kv_len, "kv_len", torch.int32, (B,))
     _cuda(anc, "anc", torch.int64, (B, T))
     d.kv_len, d.anc = kv_len.data_ptr(), anc.data_ptr()
@@ -152,20 +167,14 @@ def append_desc(q_in, q_out, k_new, v_new, k, v, depth, *, T, HQ, HKV, D, kv_dty
     d = AppendDesc()
     d.n_layers, d.B, d.T, d.HQ, d.HKV, d.D, d.s_cap = n, B, T, HQ, HKV, D, s_cap
     d.kv_dtype, d.rot_dim, d.interleaved, d.rope_base = kv_dtype, int(rot_dim), int(bool(interleaved)), float(rope_base)
-    kvt = KV_TORCH_DTYPE[kv_dtype]
     for l in range(n):
         _cuda(q_in[l], "q_in", torch.bfloat16, (B, T, HQ, D))
         _cuda(q_out[l], "q_out", torch.bfloat16, (B, T, HQ, D))
         _cuda(k_new[l], "k_new", torch.bfloat16, (B, T, HKV, D))
         _cuda(v_new[l], "v_new", torch.bfloat16, (B, T, HKV, D))
-        _cuda(k[l], "k", kvt, (B, HKV, s_cap, D))
-        _cuda(v[l], "v", kvt, (B, HKV, s_cap, D))
         d.q_in[l], d.q_out[l] = q_in[l].data_ptr(), q_out[l].data_ptr()
-        d.k_new[l], d.v_new[l], d.k[l], d.v[l] = k_new[l].data_ptr(), v_new[l].data_ptr(), k[l].data_ptr(), v[l].data_ptr()
-        if kv_dtype == I8_SCALED:
-            _cuda(k_scale[l], "k_scale", torch.float16, (B, HKV, s_cap))
-            _cuda(v_scale[l], "v_scale", torch.float16, (B, HKV, s_cap))
-            d.k_scale[l], d.v_scale[l] = k_scale[l].data_ptr(), v_scale[l].data_ptr()
+        d.k_new[l], d.v_new[l] = k_new[l].data_ptr(), v_new[l].data_ptr()
+        _cache_layer(d, l, k, v, k_scale, v_scale, kv_dtype, (B, HKV, s_cap, D))
     _cuda(depth, "depth", torch.int32, (B, T))
     d.depth = depth.data_ptr()
     return d
@@ -250,15 +259,8 @@ def kv_desc(k, v, *, HKV, D, kv_dtype, k_scale=None, v_scale=None) -> KvDesc:
     B, _, s_cap, _ = k[0].shape
     d = KvDesc()
     d.n_layers, d.B, d.HKV, d.D, d.s_cap, d.kv_dtype = n, B, HKV, D, s_cap, kv_dtype
-    kvt = KV_TORCH_DTYPE[kv_dtype]
     for l in range(n):
-        _cuda(k[l], "k", kvt, (B, HKV, s_cap, D))
-        _cuda(v[l], "v", kvt, (B, HKV, s_cap, D))
-        d.k[l], d.v[l] = k[l].data_ptr(), v[l].data_ptr()
-        if kv_dtype == I8_SCALED:
-            _cuda(k_scale[l], "k_scale", torch.float16, (B, HKV, s_cap))
-            _cuda(v_scale[l], "v_scale", torch.float16, (B, HKV, s_cap))
-            d.k_scale[l], d.v_scale[l] = k_scale[l].data_ptr(), v_scale[l].data_ptr()
+        _cache_layer(d, l, k, v, k_scale, v_scale, kv_dtype, (B, HKV, s_cap, D))
     return d
 
 
@@ -285,6 +287,76 @@ def gather_positions(desc: KvDesc, kv_len, kept, kept_len, dev_status=None, stre
         max_kept = kept.shape[1]
     check(load().tsv_gather_positions(C.byref(desc), _p(kv_len), _p(kept), _p(kept_len), int(max_kept), _p(dev_status),
                                       _stream(stream)), "gather_positions")
+
+
+# ----------------------------------------------------------------------------- recurrent layers (gated delta rule)
+def gdn_desc(q, k, v, g, beta, state, *, o=None, state_out=None, norm_eps=1e-6, scale=0.0) -> GdnDesc:
+    """Descriptor over per-layer lists of a recurrent layer's inputs and states.
+
+    q/k bf16 [B,T,HK,DK], v/o bf16 [B,T,HV,DV], g/beta fp32 [B,T,HV] for a tree block (gdn_tree_verify, gdn_commit);
+    the same without the B axis, T packed rows, for gdn_scan.  state/state_out fp32 [B,HV,DV,DK]; state_out None
+    updates the states in place.  q may be None for gdn_commit, o for any call that writes none.  norm_eps > 0
+    divides the rows of q and k by sqrt(sum x^2 + norm_eps); scale 0 is 1 / sqrt(DK).
+    """
+    n = len(k)
+    state_out = state if state_out is None else state_out
+    if not (1 <= n <= MAX_LAYERS) or any(x is not None and len(x) != n for x in (q, v, g, beta, state, state_out, o)):
+        raise ValueError("per-layer lists must have the same length in [1, 64]")
+    if k[0].dim() not in (3, 4) or v[0].dim() != k[0].dim() or state[0].dim() != 4:
+        raise ValueError("k and v must be [B, T, H, D] or [T, H, D] and state [B, HV, DV, DK]")
+    rows, (HK, DK), (HV, DV), B = tuple(k[0].shape[:-2]), k[0].shape[-2:], v[0].shape[-2:], state[0].shape[0]
+    if len(rows) == 2 and rows[0] != B:
+        raise ValueError(f"state must hold B={rows[0]} sequences, got {B}")
+    d = GdnDesc()
+    d.n_layers, d.B, d.T, d.HK, d.HV, d.DK, d.DV = n, B, rows[-1], HK, HV, DK, DV
+    d.norm_eps, d.scale = float(norm_eps), float(scale)
+    d.packed, d.device = len(rows) == 1, k[0].device
+    for l in range(n):
+        for name, x, dt, shape in (("q", q, torch.bfloat16, (HK, DK)), ("k", k, torch.bfloat16, (HK, DK)),
+                                   ("v", v, torch.bfloat16, (HV, DV)), ("g", g, torch.float32, (HV,)),
+                                   ("beta", beta, torch.float32, (HV,)), ("o", o, torch.bfloat16, (HV, DV))):
+            if x is not None:
+                _cuda(x[l], name, dt, rows + shape)
+                if x[l].device != d.device:
+                    raise ValueError(f"{name} is on {x[l].device}, k on {d.device}")
+                getattr(d, name)[l] = x[l].data_ptr()
+        _cuda(state[l], "state", torch.float32, (B, HV, DV, DK))
+        _cuda(state_out[l], "state_out", torch.float32, (B, HV, DV, DK))
+        if state[l].device != d.device or state_out[l].device != d.device:
+            raise ValueError(f"state is on {state[l].device}, k on {d.device}")
+        d.state[l], d.state_out[l] = state[l].data_ptr(), state_out[l].data_ptr()
+    return d
+
+
+def _gdn_rows(desc, packed, name):
+    if desc.packed != packed:
+        raise ValueError(f"{name} takes " + ("packed rows [T, H, D]" if packed else "a tree block [B, T, H, D]"))
+    if desc.device.index != torch.cuda.current_device():
+        raise ValueError(f"{name}: the tensors are on {desc.device}, the current device is "
+                         f"cuda:{torch.cuda.current_device()}")
+
+
+def gdn_tree_verify(desc: GdnDesc, anc, dev_status=None, stream=None):
+    """o of every tree node, each from its own parent's state; the states are only read.  anc int64 [B, T]."""
+    _gdn_rows(desc, False, "gdn_tree_verify")
+    _cuda(anc, "anc", torch.int64, (desc.B, desc.T))
+    check(load().tsv_gdn_tree_verify(C.byref(desc), _p(anc), _p(dev_status), _stream(stream)), "gdn_tree_verify")
+
+
+def gdn_commit(desc: GdnDesc, path, path_len, dev_status=None, stream=None):
+    """State after the accepted path: path int32 [B, T], path_len int32 [B] (tree_accept_walk's outputs)."""
+    _gdn_rows(desc, False, "gdn_commit")
+    _cuda(path, "path", torch.int32, (desc.B, desc.T))
+    _cuda(path_len, "path_len", torch.int32, (desc.B,))
+    check(load().tsv_gdn_commit(C.byref(desc), _p(path), _p(path_len), _p(dev_status), _stream(stream)), "gdn_commit")
+
+
+def gdn_scan(desc: GdnDesc, cu_len, *, max_len, dev_status=None, stream=None):
+    """States advanced over new tokens with every token's o: sequence b owns the packed rows cu_len[b] ..
+    cu_len[b + 1] (int32 [B + 1]), at most max_len of them."""
+    _gdn_rows(desc, True, "gdn_scan")
+    _cuda(cu_len, "cu_len", torch.int32, (desc.B + 1,))
+    check(load().tsv_gdn_scan(C.byref(desc), _p(cu_len), int(max_len), _p(dev_status), _stream(stream)), "gdn_scan")
 
 
 # ----------------------------------------------------------------------------- one verify round
@@ -327,6 +399,8 @@ class VerifyRound:
     rope_base: float = 1e6
     sample: tuple = None   # sampled verification (optional): (temperature, top_k, top_p)
     uniforms: torch.Tensor = None  # fp32 [B * T], one per node
+    gdn: dict = None       # recurrent layers (optional): per-layer lists q, k, v, g, beta, state[, state_out] and
+                           # gdn_desc's norm_eps and scale; outputs in outs["gdn_o"], states advanced by the round
     outs: dict = field(default_factory=dict)
 
     def __post_init__(self):
@@ -355,6 +429,12 @@ class VerifyRound:
             self.apdesc = append_desc(self.q_in, self.q, self.k_new, self.v_new, self.k, self.v, self.outs["depth"], T=T,
                                       HQ=self.HQ, HKV=self.HKV, D=self.D, kv_dtype=self.kv_dtype, rot_dim=self.rot_dim,
                                       rope_base=self.rope_base, k_scale=self.k_scale, v_scale=self.v_scale)
+        self.gdesc = None
+        if self.gdn is not None:
+            self.outs["gdn_o"] = [torch.empty_like(x) for x in self.gdn["v"]]
+            self.gdesc = gdn_desc(o=self.outs["gdn_o"], **self.gdn)
+            if (self.gdesc.B, self.gdesc.T) != (B, T) or self.gdesc.packed:
+                raise ValueError("the recurrent layers' inputs must be [B, T, heads, features] of this round")
         self.attn_ws = torch.empty(max(attention_workspace_size(self.adesc), 256), dtype=torch.uint8, device=dev)
         self.lm_ws = torch.empty(max(lm_head_workspace_size(B * T, self.hidden.shape[1], self.V, self.w_dtype), 256),
                                  dtype=torch.uint8, device=dev)
@@ -363,8 +443,9 @@ class VerifyRound:
             self.sample_ws = torch.empty(max(sample_workspace_size(B * T, self.V, int(self.sample[1])), 256),
                                          dtype=torch.uint8, device=dev)
 
-    def run(self, stream=None, stages=("mask", "append", "attn", "lm", "walk", "gather")):
-        """Issue the round's calls in order; "append" runs only when the round was built with append inputs."""
+    def run(self, stream=None, stages=("mask", "append", "attn", "gdn", "lm", "walk", "gather", "commit")):
+        """Issue the round's calls in order; "append" runs only when the round was built with append inputs, "gdn"
+        and "commit" (the recurrent layers and their states) only when it was built with recurrent layers."""
         o = self.outs
         B, T = self.parents.shape
         if "mask" in stages:
@@ -373,6 +454,8 @@ class VerifyRound:
             tree_append(self.apdesc, self.kv_len, dev_status=o["status"], stream=stream)
         if "attn" in stages:
             tree_verify_attention(self.adesc, self.attn_ws, dev_status=o["status"], stream=stream)
+        if "gdn" in stages and self.gdesc is not None:
+            gdn_tree_verify(self.gdesc, o["anc"], dev_status=o["status"], stream=stream)
         if "lm" in stages and self.sample is None:
             lm_head_argmax(self.hidden, self.W, o["argmax"], w_dtype=self.w_dtype, V=self.V, scales=self.w_scales,
                            biases=self.w_biases, maxlogit=o["maxlogit"], workspace=self.lm_ws, stream=stream)
@@ -388,9 +471,11 @@ class VerifyRound:
         if "gather" in stages:
             kv_gather_positions(self.kdesc, self.kv_len, o["path"], o["path_len"], T, dev_status=o["status"],
                                 stream=stream)
+        if "commit" in stages and self.gdesc is not None:
+            gdn_commit(self.gdesc, o["path"], o["path_len"], dev_status=o["status"], stream=stream)
         return o
 
-    def capture(self, stages=("mask", "append", "attn", "lm", "walk", "gather")):
+    def capture(self, stages=("mask", "append", "attn", "gdn", "lm", "walk", "gather", "commit")):
         """Record ``run(stages)`` once as a CUDA graph over this round's buffers.
 
         Every call reads its per-round inputs (parents, tokens, q, hidden, kv_len, ...) from device memory and

@@ -11,7 +11,8 @@
 // (layer, sequence, kv head) unit - rows are (node i, head g of the GQA group)
 // so every row of the CTA shares one K/V stream - and one key range.  Keys
 // stream through shared memory in tiles of 32, dequantised to fp32 on the way
-// in (Int8 codes times their per-token fp16 scale).  The tree mask is the
+// in (Int8 codes times their per-token fp16 scale,
+// 4-bit codes times their group's scale plus its bias).  The tree mask is the
 // per-node 64-bit ancestor word in shared memory, consulted only for keys at
 // or past the block start S; no dense mask exists anywhere.  Online softmax
 // in the log2 domain keeps fp32 running max / sum per row.  With more than
@@ -108,9 +109,13 @@ __device__ __forceinline__ bool kv_len_ok(int kvl, int T, int max_kv_len, int64_
     return kvl >= T && kvl <= max_kv_len && (int64_t)kvl <= s_cap;
 }
 
-// Loads 8 consecutive stored K/V elements as fp32 (Int8: times the token's scale).
-__device__ __forceinline__ void load8(const void* base, size_t elem, int dtype, float scale, float* out) {
-    if (dtype == TSV_I8_SCALED) {
+// Loads 8 consecutive stored K/V elements as fp32 (Int8: times the token's scale; 4-bit: scale * code + bias).
+__device__ __forceinline__ void load8(const void* base, size_t elem, int dtype, float scale, float bias, float* out) {
+    if (dtype == TSV_I4_G64) {
+        const uint32_t w = *reinterpret_cast<const uint32_t*>(reinterpret_cast<const uint8_t*>(base) + elem / 2);
+#pragma unroll
+        for (int k = 0; k < 8; ++k) out[k] = fmaf((float)((w >> (4 * k)) & 15u), scale, bias);
+    } else if (dtype == TSV_I8_SCALED) {
         const uint2 w = *reinterpret_cast<const uint2*>(reinterpret_cast<const int8_t*>(base) + elem);
         const int8_t* c = reinterpret_cast<const int8_t*>(&w);
 #pragma unroll
@@ -214,10 +219,17 @@ __global__ void __launch_bounds__(kAttThreads) attn_simt_kernel(const __grid_con
             float kf[8], vf[8];
             if (j < nk) {
                 const size_t row = seq0 + kt + j;
-                const float ks = d.kv_dtype == TSV_I8_SCALED ? f16_bits_to_f32(KSc[row]) : 1.f;
-                const float vs = d.kv_dtype == TSV_I8_SCALED ? f16_bits_to_f32(VSc[row]) : 1.f;
-                load8(Kp, row * D + c8, d.kv_dtype, ks, kf);
-                load8(Vp, row * D + c8, d.kv_dtype, vs, vf);
+                float2 ks = make_float2(1.f, 0.f), vs = ks;
+                if (d.kv_dtype == TSV_I8_SCALED) {
+                    ks.x = f16_bits_to_f32(KSc[row]);
+                    vs.x = f16_bits_to_f32(VSc[row]);
+                } else if (d.kv_dtype == TSV_I4_G64) {
+                    const size_t g = row * (D / 64) + c8 / 64;
+                    ks = f16x2_to_f32x2(reinterpret_cast<const uint32_t*>(KSc)[g]);
+                    vs = f16x2_to_f32x2(reinterpret_cast<const uint32_t*>(VSc)[g]);
+                }
+                load8(Kp, row * D + c8, d.kv_dtype, ks.x, ks.y, kf);
+                load8(Vp, row * D + c8, d.kv_dtype, vs.x, vs.y, vf);
             } else {
 #pragma unroll
                 for (int k = 0; k < 8; ++k) kf[k] = vf[k] = 0.f;
@@ -419,8 +431,7 @@ static tsv_status check_desc(const tsv_attn_desc* d) {
         return fail(TSV_EINVAL, "tree_verify_attention: B=%d HQ=%d HKV=%d", d->B, d->HQ, d->HKV);
     if (d->D != 64 && d->D != 128 && d->D != 256)
         return fail(TSV_EUNSUPPORTED, "tree_verify_attention: head dim %d is not 64, 128 or 256", d->D);
-    if (d->kv_dtype != TSV_F16 && d->kv_dtype != TSV_BF16 && d->kv_dtype != TSV_I8_SCALED)
-        return fail(TSV_EUNSUPPORTED, "tree_verify_attention: cache format %d", d->kv_dtype);
+    if (!kv_format_ok(d->kv_dtype)) return fail(TSV_EUNSUPPORTED, "tree_verify_attention: cache format %d", d->kv_dtype);
     if (d->max_kv_len < d->T || (int64_t)d->max_kv_len > d->s_cap)
         return fail(TSV_EINVAL, "tree_verify_attention: max_kv_len=%d must be in [T, s_cap=%lld]", d->max_kv_len,
                     (long long)d->s_cap);
@@ -446,6 +457,12 @@ static tsv_status check_desc(const tsv_attn_desc* d) {
             return fail(TSV_EINVAL, "tree_verify_attention: layer %d Q/K/V/O not 16-byte aligned", l);
         if (d->kv_dtype == TSV_I8_SCALED && (!d->k_scale[l] || !d->v_scale[l]))
             return fail(TSV_EINVAL, "tree_verify_attention: layer %d Int8 cache without scales", l);
+        if (d->kv_dtype == TSV_I4_G64) {
+            if (!d->k_scale[l] || !d->v_scale[l])
+                return fail(TSV_EINVAL, "tree_verify_attention: layer %d 4-bit cache without scales", l);
+            if (((uintptr_t)d->k_scale[l] | (uintptr_t)d->v_scale[l]) & 15)
+                return fail(TSV_EINVAL, "tree_verify_attention: layer %d 4-bit scales not 16-byte aligned", l);
+        }
     }
     return TSV_OK;
 }

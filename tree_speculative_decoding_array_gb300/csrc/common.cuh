@@ -82,6 +82,20 @@ __device__ __forceinline__ unsigned long long pack_best(float v, uint32_t idx) {
     return ((unsigned long long)orderable(v) << 32) | (unsigned long long)(0xFFFFFFFFu - idx);
 }
 
+// Cache formats.
+__host__ __device__ constexpr bool kv_format_ok(int dtype) {
+    return dtype == TSV_F16 || dtype == TSV_BF16 || dtype == TSV_I8_SCALED || dtype == TSV_I4_G64;
+}
+__host__ __device__ constexpr bool kv_has_scales(int dtype) { return dtype == TSV_I8_SCALED || dtype == TSV_I4_G64; }
+// Bytes of one stored row of D features, without its scales.
+__host__ __device__ constexpr int kv_row_bytes(int dtype, int D) {
+    return dtype == TSV_I4_G64 ? D / 2 : dtype == TSV_I8_SCALED ? D : 2 * D;
+}
+// 16-bit words of scales beside each row: one (Int8), or a (scale, bias) pair per 64 features (4-bit).
+__host__ __device__ constexpr int kv_scale_words(int dtype, int D) {
+    return dtype == TSV_I4_G64 ? D / 32 : dtype == TSV_I8_SCALED ? 1 : 0;
+}
+
 // 16-byte streaming load that does not allocate in L1 (weights read once).
 __device__ __forceinline__ uint4 ldg_stream16(const void* p) {
     uint4 r;

@@ -1,0 +1,423 @@
+// The gated delta rule of a hybrid target's recurrent layers: tsv_gdn_tree_verify, tsv_gdn_commit, tsv_gdn_scan.
+//
+// mlxcel issue #1204 and Splash issue #728 ("What it does") name the need: recurrent layers cannot take a mask, a
+// flattened tree would leak state between siblings, so every node has to run from its own parent's state and the
+// accepted path's state is the one that is kept.  The pages do not spell the recurrence out; the arithmetic here is
+// the published gated delta rule.  For one value head with state S [DV, DK], log decay g and write strength beta:
+//
+//     S <- e^g S;   u = beta (v - S k);   S <- S + u k^T;   o = S q * scale
+//
+// This file holds the CUDA-core kernels and the dispatch:
+//   gdn_recur_kernel   token by token (short scans, commits): the state stays in registers, one pass over it
+//   gdn_tree_kernel    a whole tree from one read of the state (small trees, head sizes the tensor-core kernel lacks)
+#include <math.h>
+
+#include "common.cuh"
+
+namespace tsv {
+
+constexpr int kGdnRows = 32;      // state rows (value features) per CTA
+constexpr int kGdnThreads = 128;  // 4 warps of 8 rows; 8 lanes share a row
+constexpr int kGdnBatch = 8;      // tokens whose q and k rows are in shared memory together
+constexpr float kMinLogDecay = -150.f;  // e^-150 is 0 in fp32: a smaller (or infinite) log decay means the same
+
+__device__ __forceinline__ float clamp_decay(float g) { return g < kMinLogDecay ? kMinLogDecay : g; }  // keeps NaN
+
+// One bf16 row of DK features, read by a whole warp, normalised and written to shared memory as fp32.
+template <int DK>
+__device__ __forceinline__ void stage_row(const uint16_t* src, float* dst, float norm_eps, float scale, int lane) {
+    constexpr int E = DK / 32;  // 2 or 4 features per lane
+    float x[E];
+    if constexpr (E == 4) {
+        const uint2 w = *reinterpret_cast<const uint2*>(src + lane * 4);
+        x[0] = bf16_lo(w.x); x[1] = bf16_hi(w.x); x[2] = bf16_lo(w.y); x[3] = bf16_hi(w.y);
+    } else {
+        const uint32_t w = *reinterpret_cast<const uint32_t*>(src + lane * 2);
+        x[0] = bf16_lo(w); x[1] = bf16_hi(w);
+    }
+    float f = scale;
+    if (norm_eps > 0.f) {
+        float ss = 0.f;
+#pragma unroll
+        for (int e = 0; e < E; ++e) ss = fmaf(x[e], x[e], ss);
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) ss += __shfl_xor_sync(0xFFFFFFFFu, ss, o);
+        f = scale / sqrtf(ss + norm_eps);
+    }
+#pragma unroll
+    for (int e = 0; e < E; ++e) dst[lane * E + e] = x[e] * f;
+}
+
+// This lane's part of R state rows: features 4 (lane % 8) + 32 c .. + 3 of rows r * 4 + lane / 8.
+template <int DK, int R>
+__device__ __forceinline__ void load_state(const float* base, float (&s)[R][DK / 8], int lane) {
+#pragma unroll
+    for (int r = 0; r < R; ++r)
+#pragma unroll
+        for (int c = 0; c < DK / 32; ++c) {
+            const float4 w = *reinterpret_cast<const float4*>(base + (size_t)(r * 4 + lane / 8) * DK + 32 * c + 4 * (lane % 8));
+            s[r][4 * c] = w.x; s[r][4 * c + 1] = w.y; s[r][4 * c + 2] = w.z; s[r][4 * c + 3] = w.w;
+        }
+}
+
+// Advances the state token by token; COMMIT takes a tree block's rows along `path` and writes no outputs, otherwise
+// the packed rows cu_len[b] .. cu_len[b + 1].  grid: (layer, sequence, value head, slice of kGdnRows state rows).
+//
+// Per token and state element: one FMA for S k, one for S q, a multiply for the decay and an FMA for the write, with
+// o = e^g (S q) + u (k . q) so that both products read the state before the write.  The state is read and written
+// once per call, so few tokens are bound by HBM (128 KB per 128 x 128 head).
+template <int DK, bool COMMIT>
+__global__ void __launch_bounds__(kGdnThreads) gdn_recur_kernel(const __grid_constant__ tsv_gdn_desc d,
+                                                                const int32_t* __restrict__ cu_len, int max_len,
+                                                                const int32_t* __restrict__ path,
+                                                                const int32_t* __restrict__ path_len, int32_t* status) {
+    griddep_begin();
+    __shared__ float ks[kGdnBatch][DK], qs[kGdnBatch][DK];
+    __shared__ float vs[kGdnBatch][kGdnRows];
+    __shared__ float al[kGdnBatch], be[kGdnBatch], kq[kGdnBatch];
+    __shared__ int row_s[TSV_MAX_T];
+    __shared__ int bad_s;
+    const int slices = d.DV / kGdnRows;
+    int item = blockIdx.x;
+    const int slice = item % slices;
+    item /= slices;
+    const int h = item % d.HV;
+    const int b = (item / d.HV) % d.B;
+    const int layer = item / (d.HV * d.B);
+    const int hk = h / (d.HV / d.HK);
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const bool first_cta = slice == 0 && h == 0 && layer == 0;
+
+    int n;
+    size_t row0;  // first row of this sequence in the [rows, heads, features] inputs
+    if (COMMIT) {
+        n = path_len[b];
+        row0 = (size_t)b * d.T;
+        if (threadIdx.x == 0) bad_s = n < 1 || n > d.T;
+        __syncthreads();
+        if (!bad_s)
+            for (int j = threadIdx.x; j < n; j += kGdnThreads) {
+                const int p = path[(size_t)b * d.T + j];
+                const int before = j > 0 ? path[(size_t)b * d.T + j - 1] : -1;
+                if (p <= before || p >= d.T || (j == 0 && p != 0)) bad_s = 1;
+                row_s[j] = p;
+            }
+        __syncthreads();
+        if (bad_s) {
+            if (first_cta && threadIdx.x == 0) dev_fail(status, TSV_DEV_BAD_PATH, b, 0);
+            return;
+        }
+    } else {
+        const int a = cu_len[b], e = cu_len[b + 1];
+        n = e - a;
+        row0 = (size_t)a;
+        if (a < 0 || e < a || e > d.T || n > max_len) {
+            if (first_cta && threadIdx.x == 0) dev_fail(status, TSV_DEV_BAD_SEQ_LEN, b, e);
+            return;
+        }
+    }
+
+    const size_t s0 = (((size_t)b * d.HV + h) * d.DV + slice * kGdnRows + warp * 8) * DK;
+    float s[2][DK / 8];
+    load_state<DK, 2>(d.state[layer] + s0, s, lane);
+    const uint16_t* Q = reinterpret_cast<const uint16_t*>(d.q[layer]);
+    const uint16_t* K = reinterpret_cast<const uint16_t*>(d.k[layer]);
+    const uint16_t* V = reinterpret_cast<const uint16_t*>(d.v[layer]);
+    __nv_bfloat16* O = reinterpret_cast<__nv_bfloat16*>(d.o[layer]);
+
+    for (int t0 = 0; t0 < n; t0 += kGdnBatch) {
+        const int nt = min(kGdnBatch, n - t0);
+        __syncthreads();
+        for (int j = warp; j < nt; j += kGdnThreads / 32) {
+            const size_t row = row0 + (COMMIT ? row_s[t0 + j] : t0 + j);
+            stage_row<DK>(K + (row * d.HK + hk) * DK, ks[j], d.norm_eps, 1.f, lane);
+            if (!COMMIT) stage_row<DK>(Q + (row * d.HK + hk) * DK, qs[j], d.norm_eps, d.scale, lane);
+            vs[j][lane] = bf16_bits_to_f32(V[(row * d.HV + h) * d.DV + slice * kGdnRows + lane]);
+            if (lane == 0) {
+                al[j] = expf(d.g[layer][row * d.HV + h]);
+                be[j] = d.beta[layer][row * d.HV + h];
+            }
+            if (!COMMIT) {
+                __syncwarp();
+                float p = 0.f;
+#pragma unroll
+                for (int e = lane; e < DK; e += 32) p = fmaf(ks[j][e], qs[j][e], p);
+#pragma unroll
+                for (int o = 16; o > 0; o >>= 1) p += __shfl_xor_sync(0xFFFFFFFFu, p, o);
+                if (lane == 0) kq[j] = p;
+            }
+        }
+        __syncthreads();
+        for (int j = 0; j < nt; ++j) {
+            float sk[2] = {0.f, 0.f}, sq[2] = {0.f, 0.f};
+            float4 kk[DK / 32];
+#pragma unroll
+            for (int c = 0; c < DK / 32; ++c) {
+                kk[c] = *reinterpret_cast<const float4*>(&ks[j][32 * c + 4 * (lane % 8)]);
+#pragma unroll
+                for (int r = 0; r < 2; ++r)
+                    sk[r] = fmaf(s[r][4 * c], kk[c].x, fmaf(s[r][4 * c + 1], kk[c].y,
+                            fmaf(s[r][4 * c + 2], kk[c].z, fmaf(s[r][4 * c + 3], kk[c].w, sk[r]))));
+                if (!COMMIT) {
+                    const float4 qq = *reinterpret_cast<const float4*>(&qs[j][32 * c + 4 * (lane % 8)]);
+#pragma unroll
+                    for (int r = 0; r < 2; ++r)
+                        sq[r] = fmaf(s[r][4 * c], qq.x, fmaf(s[r][4 * c + 1], qq.y,
+                                fmaf(s[r][4 * c + 2], qq.z, fmaf(s[r][4 * c + 3], qq.w, sq[r]))));
+                }
+            }
+#pragma unroll
+            for (int o = 4; o > 0; o >>= 1)
+#pragma unroll
+                for (int r = 0; r < 2; ++r) {
+                    sk[r] += __shfl_xor_sync(0xFFFFFFFFu, sk[r], o);
+                    if (!COMMIT) sq[r] += __shfl_xor_sync(0xFFFFFFFFu, sq[r], o);
+                }
+            const float a = al[j], bt = be[j];
+#pragma unroll
+            for (int r = 0; r < 2; ++r) {
+                const int vr = warp * 8 + r * 4 + lane / 8;
+                const float u = bt * (vs[j][vr] - a * sk[r]);
+#pragma unroll
+                for (int c = 0; c < DK / 32; ++c) {
+                    s[r][4 * c] = fmaf(u, kk[c].x, a * s[r][4 * c]);
+                    s[r][4 * c + 1] = fmaf(u, kk[c].y, a * s[r][4 * c + 1]);
+                    s[r][4 * c + 2] = fmaf(u, kk[c].z, a * s[r][4 * c + 2]);
+                    s[r][4 * c + 3] = fmaf(u, kk[c].w, a * s[r][4 * c + 3]);
+                }
+                if (!COMMIT && lane % 8 == 0)
+                    O[((row0 + t0 + j) * d.HV + h) * d.DV + slice * kGdnRows + vr] = __float2bfloat16(fmaf(a, sq[r], u * kq[j]));
+            }
+        }
+    }
+    float* out = d.state_out[layer] + s0;
+#pragma unroll
+    for (int r = 0; r < 2; ++r)
+#pragma unroll
+        for (int c = 0; c < DK / 32; ++c)
+            *reinterpret_cast<float4*>(out + (size_t)(r * 4 + lane / 8) * DK + 32 * c + 4 * (lane % 8)) =
+                make_float4(s[r][4 * c], s[r][4 * c + 1], s[r][4 * c + 2], s[r][4 * c + 3]);
+}
+
+// The whole tree from one read of the state.  With G_i the log decay summed from the root to node i, the recurrence
+// along i's ancestors unrolls to
+//     u_i = beta_i (v_i - e^{G_i} S k_i - sum_{j strict ancestor} e^{G_i - G_j} (k_j . k_i) u_j)
+//     o_i = e^{G_i} S q_i + sum_{j ancestor or self} e^{G_i - G_j} (k_j . q_i) u_j
+// so S is only needed for the 2 T products S k_i, S q_i, and siblings share nothing but ancestors.  Ancestor words
+// are cut to lower node indices, so that no input can make the substitution read ahead.  G is summed in fp64 (its
+// differences lose nothing however far the decays reach).  Only ancestors are ever read, so a NaN or an infinity in
+// one branch stays in it.
+template <int DK>
+__global__ void __launch_bounds__(kGdnThreads) gdn_tree_kernel(const __grid_constant__ tsv_gdn_desc d,
+                                                               const uint64_t* __restrict__ anc) {
+    griddep_begin();
+    extern __shared__ __align__(16) float smf[];
+    __shared__ double G[TSV_MAX_T];
+    __shared__ uint64_t seen[TSV_MAX_T];  // strict ancestors
+    __shared__ float be[TSV_MAX_T];
+    const int T = d.T;
+    float* ks = smf;                      // [T][DK]
+    float* qs = ks + T * DK;              // [T][DK]
+    float* sk = qs + T * DK;              // [T][kGdnRows] S k_i, then u_i
+    float* sq = sk + T * kGdnRows;        // [T][kGdnRows] S q_i
+    float* A = sq + T * kGdnRows;         // [T][T] e^{G_i - G_j} (k_i . k_j)
+    float* P = A + T * T;                 // [T][T] e^{G_i - G_j} (q_i . k_j)
+    const int slices = d.DV / kGdnRows;
+    int item = blockIdx.x;
+    const int slice = item % slices;
+    item /= slices;
+    const int h = item % d.HV;
+    const int b = (item / d.HV) % d.B;
+    const int layer = item / (d.HV * d.B);
+    const int hk = h / (d.HV / d.HK);
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const size_t row0 = (size_t)b * T;
+
+    const size_t s0 = (((size_t)b * d.HV + h) * d.DV + slice * kGdnRows + warp * 8) * DK;
+    float s[2][DK / 8];
+    load_state<DK, 2>(d.state[layer] + s0, s, lane);
+
+    const uint16_t* Q = reinterpret_cast<const uint16_t*>(d.q[layer]);
+    const uint16_t* K = reinterpret_cast<const uint16_t*>(d.k[layer]);
+    for (int i = warp; i < T; i += kGdnThreads / 32) {
+        stage_row<DK>(K + ((row0 + i) * d.HK + hk) * DK, ks + i * DK, d.norm_eps, 1.f, lane);
+        stage_row<DK>(Q + ((row0 + i) * d.HK + hk) * DK, qs + i * DK, d.norm_eps, d.scale, lane);
+    }
+    for (int i = threadIdx.x; i < T; i += kGdnThreads) {
+        uint64_t a = anc[row0 + i] & ((1ull << i) - 1ull);
+        seen[i] = a;
+        be[i] = d.beta[layer][(row0 + i) * d.HV + h];
+        double sum = (double)clamp_decay(d.g[layer][(row0 + i) * d.HV + h]);
+        for (; a; a &= a - 1) sum += (double)clamp_decay(d.g[layer][(row0 + __ffsll((long long)a) - 1) * d.HV + h]);
+        G[i] = sum;
+    }
+    __syncthreads();
+
+    for (int i = 0; i < T; ++i) {  // S k_i and S q_i
+        float a[2] = {0.f, 0.f}, o[2] = {0.f, 0.f};
+#pragma unroll
+        for (int c = 0; c < DK / 32; ++c) {
+            const float4 kk = *reinterpret_cast<const float4*>(ks + i * DK + 32 * c + 4 * (lane % 8));
+            const float4 qq = *reinterpret_cast<const float4*>(qs + i * DK + 32 * c + 4 * (lane % 8));
+#pragma unroll
+            for (int r = 0; r < 2; ++r) {
+                a[r] = fmaf(s[r][4 * c], kk.x, fmaf(s[r][4 * c + 1], kk.y, fmaf(s[r][4 * c + 2], kk.z, fmaf(s[r][4 * c + 3], kk.w, a[r]))));
+                o[r] = fmaf(s[r][4 * c], qq.x, fmaf(s[r][4 * c + 1], qq.y, fmaf(s[r][4 * c + 2], qq.z, fmaf(s[r][4 * c + 3], qq.w, o[r]))));
+            }
+        }
+#pragma unroll
+        for (int x = 4; x > 0; x >>= 1)
+#pragma unroll
+            for (int r = 0; r < 2; ++r) {
+                a[r] += __shfl_xor_sync(0xFFFFFFFFu, a[r], x);
+                o[r] += __shfl_xor_sync(0xFFFFFFFFu, o[r], x);
+            }
+        if (lane % 8 == 0) {
+#pragma unroll
+            for (int r = 0; r < 2; ++r) {
+                sk[i * kGdnRows + warp * 8 + r * 4 + lane / 8] = a[r];
+                sq[i * kGdnRows + warp * 8 + r * 4 + lane / 8] = o[r];
+            }
+        }
+    }
+    // inner products with the ancestors, one node per warp at a time
+    for (int i = warp; i < T; i += kGdnThreads / 32) {
+        for (uint64_t a = seen[i] | (1ull << i); a; a &= a - 1) {
+            const int j = __ffsll((long long)a) - 1;
+            float kk = 0.f, qk = 0.f;
+#pragma unroll
+            for (int e = lane; e < DK; e += 32) {
+                kk = fmaf(ks[i * DK + e], ks[j * DK + e], kk);
+                qk = fmaf(qs[i * DK + e], ks[j * DK + e], qk);
+            }
+#pragma unroll
+            for (int x = 16; x > 0; x >>= 1) {
+                kk += __shfl_xor_sync(0xFFFFFFFFu, kk, x);
+                qk += __shfl_xor_sync(0xFFFFFFFFu, qk, x);
+            }
+            if (lane == 0) {
+                const float w = expf((float)(G[i] - G[j]));
+                A[i * T + j] = w * kk;
+                P[i * T + j] = w * qk;
+            }
+        }
+    }
+    __syncthreads();
+    if (warp == 0) {  // substitution: lane = value feature of the slice
+        const __nv_bfloat16* V = reinterpret_cast<const __nv_bfloat16*>(d.v[layer]);
+        __nv_bfloat16* O = reinterpret_cast<__nv_bfloat16*>(d.o[layer]);
+        for (int i = 0; i < T; ++i) {
+            const size_t at = ((row0 + i) * d.HV + h) * d.DV + slice * kGdnRows + lane;
+            const float e = expf((float)G[i]);
+            float r = __bfloat162float(V[at]) - e * sk[i * kGdnRows + lane], o = e * sq[i * kGdnRows + lane];
+            for (uint64_t a = seen[i]; a; a &= a - 1) {
+                const int j = __ffsll((long long)a) - 1;
+                const float u = sk[j * kGdnRows + lane];
+                r = fmaf(-A[i * T + j], u, r);
+                o = fmaf(P[i * T + j], u, o);
+            }
+            const float u = be[i] * r;
+            sk[i * kGdnRows + lane] = u;
+            O[at] = __float2bfloat16(fmaf(P[i * T + i], u, o));
+        }
+    }
+}
+
+static size_t tree_smem(const tsv_gdn_desc* d) {
+    return ((size_t)2 * d->T * d->DK + (size_t)2 * d->T * kGdnRows + (size_t)2 * d->T * d->T) * sizeof(float);
+}
+
+enum GdnCall { kGdnVerify, kGdnCommit, kGdnScan };
+
+static tsv_status check_gdn(const tsv_gdn_desc* d, GdnCall call, const char* name) {
+    if (!d) return fail(TSV_EINVAL, "%s: null descriptor", name);
+    if (d->n_layers < 1 || d->n_layers > TSV_MAX_LAYERS)
+        return fail(TSV_ECAPACITY, "%s: n_layers=%d outside [1, %d]", name, d->n_layers, TSV_MAX_LAYERS);
+    if (call == kGdnScan ? d->T < 0 : (d->T < 1 || d->T > TSV_MAX_T))
+        return fail(TSV_ECAPACITY, "%s: T=%d outside [%d, %d]", name, d->T, call == kGdnScan ? 0 : 1,
+                    call == kGdnScan ? 0x7FFFFFFF : TSV_MAX_T);
+    if (d->B < 0 || d->HK < 1 || d->HV < 1 || d->HV % d->HK)
+        return fail(TSV_EINVAL, "%s: B=%d HK=%d HV=%d", name, d->B, d->HK, d->HV);
+    if ((d->DK != 64 && d->DK != 128) || (d->DV != 64 && d->DV != 128))
+        return fail(TSV_EUNSUPPORTED, "%s: head dims DK=%d DV=%d are not 64 or 128", name, d->DK, d->DV);
+    if (!(d->norm_eps >= 0.f) || d->norm_eps > 1e30f) return fail(TSV_EINVAL, "%s: norm_eps=%g", name, (double)d->norm_eps);
+    if (!(fabsf(d->scale) <= 1e30f)) return fail(TSV_EINVAL, "%s: scale=%g", name, (double)d->scale);
+    if ((long long)d->n_layers * d->B * d->HV * (d->DV / kGdnRows) > 0x7FFFFFFFLL)
+        return fail(TSV_ECAPACITY, "%s: too many (layer, sequence, head) units", name);
+    if (d->B == 0) return TSV_OK;  // an empty batch: no pointer is read
+    const bool out = call != kGdnCommit, wr = call != kGdnVerify;
+    for (int l = 0; l < d->n_layers; ++l) {
+        if (!d->state[l] || (wr && !d->state_out[l])) return fail(TSV_EINVAL, "%s: layer %d has a null state", name, l);
+        if (((uintptr_t)d->state[l] | (wr ? (uintptr_t)d->state_out[l] : 0)) & 15)
+            return fail(TSV_EINVAL, "%s: layer %d state not 16-byte aligned", name, l);
+        if (d->T == 0) continue;  // a scan without new rows reads no inputs
+        if (!d->k[l] || !d->v[l] || !d->g[l] || !d->beta[l] || (out && (!d->q[l] || !d->o[l])))
+            return fail(TSV_EINVAL, "%s: layer %d has a null pointer", name, l);
+        if (((uintptr_t)d->k[l] | (uintptr_t)d->v[l] | (out ? (uintptr_t)d->q[l] | (uintptr_t)d->o[l] : 0)) & 15)
+            return fail(TSV_EINVAL, "%s: layer %d q/k/v/o not 16-byte aligned", name, l);
+        if (((uintptr_t)d->g[l] | (uintptr_t)d->beta[l]) & 3)
+            return fail(TSV_EINVAL, "%s: layer %d g/beta not 4-byte aligned", name, l);
+    }
+    return TSV_OK;
+}
+
+// The caller's descriptor with the default scale filled in.
+static tsv_gdn_desc with_scale(const tsv_gdn_desc* d) {
+    tsv_gdn_desc x = *d;
+    if (x.scale == 0.f) x.scale = (float)(1.0 / sqrt((double)d->DK));
+    return x;
+}
+
+}  // namespace tsv
+
+extern "C" tsv_status tsv_gdn_tree_verify(const tsv_gdn_desc* d, const uint64_t* anc, int32_t* dev_status,
+                                          cudaStream_t stream) {
+    using namespace tsv;
+    (void)dev_status;
+    clear_error();
+    tsv_status st = check_gdn(d, kGdnVerify, "gdn_tree_verify");
+    if (st != TSV_OK || d->B == 0) return st;
+    if (!anc) return fail(TSV_EINVAL, "gdn_tree_verify: anc must be non-null");
+    const tsv_gdn_desc x = with_scale(d);
+    const unsigned grid = (unsigned)((long long)d->n_layers * d->B * d->HV * (d->DV / kGdnRows));
+    const size_t sm = tree_smem(d);
+    if (d->DK == 64) {
+        cudaFuncSetAttribute(gdn_tree_kernel<64>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)sm);
+        launch_pdl(gdn_tree_kernel<64>, grid, kGdnThreads, sm, stream, x, anc);
+    } else {
+        cudaFuncSetAttribute(gdn_tree_kernel<128>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)sm);
+        launch_pdl(gdn_tree_kernel<128>, grid, kGdnThreads, sm, stream, x, anc);
+    }
+    return check_launch("gdn_tree_verify");
+}
+
+extern "C" tsv_status tsv_gdn_commit(const tsv_gdn_desc* d, const int32_t* path, const int32_t* path_len,
+                                     int32_t* dev_status, cudaStream_t stream) {
+    using namespace tsv;
+    clear_error();
+    tsv_status st = check_gdn(d, kGdnCommit, "gdn_commit");
+    if (st != TSV_OK || d->B == 0) return st;
+    if (!path || !path_len) return fail(TSV_EINVAL, "gdn_commit: path and path_len must be non-null");
+    const tsv_gdn_desc x = with_scale(d);
+    const unsigned grid = (unsigned)((long long)d->n_layers * d->B * d->HV * (d->DV / kGdnRows));
+    const int32_t* none = nullptr;
+    if (d->DK == 64) launch_pdl(gdn_recur_kernel<64, true>, grid, kGdnThreads, 0, stream, x, none, 0, path, path_len, dev_status);
+    else launch_pdl(gdn_recur_kernel<128, true>, grid, kGdnThreads, 0, stream, x, none, 0, path, path_len, dev_status);
+    return check_launch("gdn_commit");
+}
+
+extern "C" tsv_status tsv_gdn_scan(const tsv_gdn_desc* d, const int32_t* cu_len, int32_t max_len, int32_t* dev_status,
+                                   cudaStream_t stream) {
+    using namespace tsv;
+    clear_error();
+    tsv_status st = check_gdn(d, kGdnScan, "gdn_scan");
+    if (st != TSV_OK || d->B == 0) return st;
+    if (!cu_len) return fail(TSV_EINVAL, "gdn_scan: cu_len must be non-null");
+    if (max_len < 0 || max_len > d->T) return fail(TSV_EINVAL, "gdn_scan: max_len=%d outside [0, T=%d]", max_len, d->T);
+    const tsv_gdn_desc x = with_scale(d);
+    const unsigned grid = (unsigned)((long long)d->n_layers * d->B * d->HV * (d->DV / kGdnRows));
+    const int32_t* none = nullptr;
+    if (d->DK == 64) launch_pdl(gdn_recur_kernel<64, false>, grid, kGdnThreads, 0, stream, x, cu_len, max_len, none, none, dev_status);
+    else launch_pdl(gdn_recur_kernel<128, false>, grid, kGdnThreads, 0, stream, x, cu_len, max_len, none, none, dev_status);
+    return check_launch("gdn_scan");
+}

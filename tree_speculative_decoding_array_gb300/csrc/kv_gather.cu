@@ -57,6 +57,7 @@ __device__ __forceinline__ GatherCheck gather_check(const int32_t* __restrict__ 
 
 constexpr int kGatherThreads = 256;
 constexpr int kMaxRowBytes = 512;  // D = 256 at 2 bytes
+constexpr int kMaxScaleWords = 8;  // D = 256 at 4 bits: four (scale, bias) pairs
 
 __global__ void __launch_bounds__(kGatherThreads) kv_gather_kernel(const __grid_constant__ tsv_kv_desc kv,
                                                                    const int32_t* __restrict__ kv_len,
@@ -65,7 +66,7 @@ __global__ void __launch_bounds__(kGatherThreads) kv_gather_kernel(const __grid_
                                                                    int32_t* status) {
     griddep_begin();
     __shared__ uint4 buf[TSV_MAX_T * kMaxRowBytes / 16];
-    __shared__ uint16_t sbuf[TSV_MAX_T];
+    __shared__ uint16_t sbuf[TSV_MAX_T * kMaxScaleWords];
     __shared__ int sp[TSV_MAX_T];
     __shared__ GatherCheck g;
     const int unit = blockIdx.x;
@@ -80,8 +81,8 @@ __global__ void __launch_bounds__(kGatherThreads) kv_gather_kernel(const __grid_
     __syncthreads();
     if (g.ok < 0 || g.first == g.len) return;  // invalid, or identity selection: nothing moves
 
-    const int elt = kv.kv_dtype == TSV_I8_SCALED ? 1 : 2;
-    const int vpr = kv.D * elt / 16;  // 16-byte vectors per row
+    const int vpr = kv_row_bytes(kv.kv_dtype, kv.D) / 16;  // 16-byte vectors per row
+    const int spr = kv_scale_words(kv.kv_dtype, kv.D);     // 16-bit scale words per row
     const size_t seq_row0 = ((size_t)b * kv.HKV + h) * (size_t)kv.s_cap;
     uint4* base = reinterpret_cast<uint4*>(which ? kv.v[layer] : kv.k[layer]) + seq_row0 * vpr;
     const int first = g.first, n = g.len - g.first, S = g.S;
@@ -90,9 +91,12 @@ __global__ void __launch_bounds__(kGatherThreads) kv_gather_kernel(const __grid_
         buf[e] = base[(size_t)(S + sp[first + r]) * vpr + c];
     }
     uint16_t* sc = nullptr;
-    if (kv.kv_dtype == TSV_I8_SCALED) {
-        sc = reinterpret_cast<uint16_t*>(which ? kv.v_scale[layer] : kv.k_scale[layer]) + seq_row0;
-        for (int r = threadIdx.x; r < n; r += blockDim.x) sbuf[r] = sc[S + sp[first + r]];
+    if (spr > 0) {
+        sc = reinterpret_cast<uint16_t*>(which ? kv.v_scale[layer] : kv.k_scale[layer]) + seq_row0 * spr;
+        for (int e = threadIdx.x; e < n * spr; e += blockDim.x) {
+            const int r = e / spr, c = e % spr;
+            sbuf[e] = sc[(size_t)(S + sp[first + r]) * spr + c];
+        }
     }
     __syncthreads();
     for (int e = threadIdx.x; e < n * vpr; e += blockDim.x) {
@@ -100,7 +104,7 @@ __global__ void __launch_bounds__(kGatherThreads) kv_gather_kernel(const __grid_
         base[(size_t)(S + first + r) * vpr + c] = buf[e];
     }
     if (sc)
-        for (int r = threadIdx.x; r < n; r += blockDim.x) sc[S + first + r] = sbuf[r];
+        for (int e = threadIdx.x; e < n * spr; e += blockDim.x) sc[(size_t)(S + first) * spr + e] = sbuf[e];
 }
 
 __global__ void kv_len_update_kernel(int32_t* __restrict__ kv_len, const int32_t* __restrict__ path,
@@ -128,7 +132,7 @@ extern "C" tsv_status tsv_kv_gather_positions(const tsv_kv_desc* kv, int32_t* kv
     if (kv->B < 0 || kv->HKV < 1) return fail(TSV_EINVAL, "kv_gather_positions: B=%d HKV=%d", kv->B, kv->HKV);
     if (kv->D != 64 && kv->D != 128 && kv->D != 256)
         return fail(TSV_EUNSUPPORTED, "kv_gather_positions: head dim %d is not 64, 128 or 256", kv->D);
-    if (kv->kv_dtype != TSV_F16 && kv->kv_dtype != TSV_BF16 && kv->kv_dtype != TSV_I8_SCALED)
+    if (!kv_format_ok(kv->kv_dtype))
         return fail(TSV_EUNSUPPORTED, "kv_gather_positions: cache format %d has no gather (only fp16, bf16 and "
                                       "Int8 with per-token scales keep all per-token state on the sequence axis)",
                     kv->kv_dtype);
@@ -140,6 +144,12 @@ extern "C" tsv_status tsv_kv_gather_positions(const tsv_kv_desc* kv, int32_t* kv
             return fail(TSV_EINVAL, "kv_gather_positions: layer %d K/V not 16-byte aligned", l);
         if (kv->kv_dtype == TSV_I8_SCALED && (!kv->k_scale[l] || !kv->v_scale[l]))
             return fail(TSV_EINVAL, "kv_gather_positions: layer %d Int8 cache without scale sidecars", l);
+        if (kv->kv_dtype == TSV_I4_G64) {
+            if (!kv->k_scale[l] || !kv->v_scale[l])
+                return fail(TSV_EINVAL, "kv_gather_positions: layer %d 4-bit cache without scale sidecars", l);
+            if (((uintptr_t)kv->k_scale[l] | (uintptr_t)kv->v_scale[l]) & 15)
+                return fail(TSV_EINVAL, "kv_gather_positions: layer %d 4-bit scales not 16-byte aligned", l);
+        }
     }
     const long long units = (long long)kv->n_layers * kv->B * kv->HKV;
     if (units > 0x7FFFFFFFLL) return fail(TSV_ECAPACITY, "kv_gather_positions: too many (layer, seq, head) units");
@@ -167,6 +177,8 @@ namespace tsv {
 
 constexpr int kAbsThreads = 512;
 constexpr int kChunkBytes = 16384;
+// Scale words per chunk: Int8 rows hold one per 64 to 256 bytes, 4-bit rows one per 16 bytes.
+constexpr int kMaxChunkScales = kChunkBytes / 16;
 
 struct KeptCheck {
     int ok, n, first;
@@ -213,7 +225,7 @@ __global__ void __launch_bounds__(kAbsThreads) gather_abs_kernel(const __grid_co
                                                                  int32_t* status) {
     griddep_begin();
     __shared__ uint4 buf[2][kChunkBytes / 16];
-    __shared__ uint16_t sbuf[2][kChunkBytes / 64];  // one scale per row; rows per chunk <= kChunkBytes / 64
+    __shared__ uint16_t sbuf[2][kMaxChunkScales];
     const int unit = blockIdx.x;
     const int h = unit % kv.HKV;
     const int b = (unit / kv.HKV) % kv.B;
@@ -226,13 +238,13 @@ __global__ void __launch_bounds__(kAbsThreads) gather_abs_kernel(const __grid_co
     }
     if (g.first >= g.n) return;  // identity (or prefix) selection: a trim, nothing moves
 
-    const int elt = kv.kv_dtype == TSV_I8_SCALED ? 1 : 2;
-    const int vpr = kv.D * elt / 16;          // 16-byte vectors per row (4 .. 32)
-    const int rows = kChunkBytes / (vpr * 16);  // rows per chunk (32 .. 256)
+    const int vpr = kv_row_bytes(kv.kv_dtype, kv.D) / 16;  // 16-byte vectors per row (2 .. 32)
+    const int spr = kv_scale_words(kv.kv_dtype, kv.D);     // 16-bit scale words per row
+    const int rows = kChunkBytes / (vpr * 16);             // rows per chunk (32 .. 512)
     const size_t seq_row0 = ((size_t)b * kv.HKV + h) * (size_t)kv.s_cap;
     uint4* base = reinterpret_cast<uint4*>(which ? kv.v[layer] : kv.k[layer]) + seq_row0 * vpr;
-    uint16_t* sc = kv.kv_dtype == TSV_I8_SCALED
-                       ? reinterpret_cast<uint16_t*>(which ? kv.v_scale[layer] : kv.k_scale[layer]) + seq_row0
+    uint16_t* sc = spr > 0
+                       ? reinterpret_cast<uint16_t*>(which ? kv.v_scale[layer] : kv.k_scale[layer]) + seq_row0 * spr
                        : nullptr;
     const int32_t* row = kept + (size_t)b * max_kept;
     int s = 0;
@@ -243,14 +255,17 @@ __global__ void __launch_bounds__(kAbsThreads) gather_abs_kernel(const __grid_co
             buf[s][e] = base[(size_t)__ldg(row + j0 + r) * vpr + c];
         }
         if (sc)
-            for (int r = threadIdx.x; r < cnt; r += blockDim.x) sbuf[s][r] = sc[__ldg(row + j0 + r)];
+            for (int e = threadIdx.x; e < cnt * spr; e += blockDim.x) {
+                const int r = e / spr, c = e - r * spr;
+                sbuf[s][e] = sc[(size_t)__ldg(row + j0 + r) * spr + c];
+            }
         __syncthreads();
         for (int e = threadIdx.x; e < cnt * vpr; e += blockDim.x) {
             const int r = e / vpr, c = e - r * vpr;
             base[(size_t)(j0 + r) * vpr + c] = buf[s][e];
         }
         if (sc)
-            for (int r = threadIdx.x; r < cnt; r += blockDim.x) sc[j0 + r] = sbuf[s][r];
+            for (int e = threadIdx.x; e < cnt * spr; e += blockDim.x) sc[(size_t)j0 * spr + e] = sbuf[s][e];
     }
 }
 
@@ -280,7 +295,7 @@ extern "C" tsv_status tsv_gather_positions(const tsv_kv_desc* kv, int32_t* kv_le
         return fail(TSV_ECAPACITY, "gather_positions: n_layers=%d outside [1, %d]", kv->n_layers, TSV_MAX_LAYERS);
     if (kv->D != 64 && kv->D != 128 && kv->D != 256)
         return fail(TSV_EUNSUPPORTED, "gather_positions: head dim %d is not 64, 128 or 256", kv->D);
-    if (kv->kv_dtype != TSV_F16 && kv->kv_dtype != TSV_BF16 && kv->kv_dtype != TSV_I8_SCALED)
+    if (!kv_format_ok(kv->kv_dtype))
         return fail(TSV_EUNSUPPORTED, "gather_positions: cache format %d has no gather (only fp16, bf16 and Int8 "
                                       "with per-token scales keep all per-token state on the sequence axis)",
                     kv->kv_dtype);
@@ -292,6 +307,12 @@ extern "C" tsv_status tsv_gather_positions(const tsv_kv_desc* kv, int32_t* kv_le
             return fail(TSV_EINVAL, "gather_positions: layer %d K/V not 16-byte aligned", l);
         if (kv->kv_dtype == TSV_I8_SCALED && (!kv->k_scale[l] || !kv->v_scale[l]))
             return fail(TSV_EINVAL, "gather_positions: layer %d Int8 cache without scale sidecars", l);
+        if (kv->kv_dtype == TSV_I4_G64) {
+            if (!kv->k_scale[l] || !kv->v_scale[l])
+                return fail(TSV_EINVAL, "gather_positions: layer %d 4-bit cache without scale sidecars", l);
+            if (((uintptr_t)kv->k_scale[l] | (uintptr_t)kv->v_scale[l]) & 15)
+                return fail(TSV_EINVAL, "gather_positions: layer %d 4-bit scales not 16-byte aligned", l);
+        }
     }
     const long long units = (long long)kv->n_layers * kv->B * kv->HKV;
     if (units > 0x7FFFFFFFLL) return fail(TSV_ECAPACITY, "gather_positions: too many (layer, seq, head) units");

@@ -6,7 +6,8 @@
 // S + depth(i), while its K/V rows keep the topological slot S + i.  Q and
 // the new K rows are rotated (rotary embedding of the first rot_dim
 // features); V is not.  Int8 caches (PR #1212, gather_positions commit: one
-// scale per token) quantise every row symmetrically by its absolute maximum.
+// scale per token) quantise every row symmetrically by its absolute maximum; 4-bit
+// caches quantise every group of 64 features between its minimum and maximum.
 //
 // One CTA per (sequence, node, layer): the node's angles (inverse
 // frequencies from the host in fp64, fp64 angle and range reduction, fp32
@@ -52,12 +53,43 @@ __device__ __forceinline__ void store_words(void* dst, const uint32_t* w) {
     else *reinterpret_cast<uint32_t*>(dst) = w[0];
 }
 
-// One row: this lane's E values x (features lane*E ..) -> stored form: bf16 (Q), fp16 / bf16 or Int8 codes
-// + fp16 scale (cache rows).
+// One row: this lane's E values x (features lane*E ..) -> stored form: bf16 (Q), fp16 / bf16, Int8 codes
+// + fp16 scale or 4-bit codes + fp16 (scale, bias) pairs (cache rows).
 template <int E>
 __device__ __forceinline__ void store_row(const float* x, int lane, int dtype, void* dst, size_t e0,
                                           uint16_t* scale_dst) {
-    if (dtype == TSV_I8_SCALED) {
+    if (dtype == TSV_I4_G64) {
+        // Affine codes per group of 64 features: 64 / E consecutive lanes share a group.
+        constexpr int GL = 64 / E;
+        float lo = x[0], hi = x[0];
+#pragma unroll
+        for (int k = 1; k < E; ++k) {
+            lo = fminf(lo, x[k]);
+            hi = fmaxf(hi, x[k]);
+        }
+#pragma unroll
+        for (int o = GL / 2; o > 0; o >>= 1) {
+            lo = fminf(lo, __shfl_xor_sync(0xFFFFFFFFu, lo, o));
+            hi = fmaxf(hi, __shfl_xor_sync(0xFFFFFFFFu, hi, o));
+        }
+        // both stay finite in fp16, whatever a bf16 input holds
+        const __half sh = __float2half_rn(fminf(__fdiv_rn(__fsub_rn(hi, lo), 15.f), 65504.f));
+        const __half bh = __float2half_rn(fminf(fmaxf(lo, -65504.f), 65504.f));
+        const float s = __half2float(sh), b = __half2float(bh);
+        uint32_t w = 0;
+#pragma unroll
+        for (int k = 0; k < E; ++k) {
+            const float q = s != 0.f ? fminf(15.f, fmaxf(0.f, rintf(__fdiv_rn(__fsub_rn(x[k], b), s)))) : 0.f;
+            w |= (uint32_t)(int)q << (4 * k);
+        }
+        uint8_t* out = reinterpret_cast<uint8_t*>(dst) + (e0 + (size_t)lane * E) / 2;
+        if constexpr (E == 8) *reinterpret_cast<uint32_t*>(out) = w;
+        else if constexpr (E == 4) *reinterpret_cast<uint16_t*>(out) = (uint16_t)w;
+        else *out = (uint8_t)w;
+        if (lane % GL == 0)
+            reinterpret_cast<uint32_t*>(scale_dst)[lane / GL] =
+                (uint32_t)__half_as_ushort(sh) | ((uint32_t)__half_as_ushort(bh) << 16);
+    } else if (dtype == TSV_I8_SCALED) {
         float amax = 0.f;
 #pragma unroll
         for (int k = 0; k < E; ++k) amax = fmaxf(amax, fabsf(x[k]));
@@ -179,8 +211,9 @@ __global__ void __launch_bounds__(kApThreads) tree_append_kernel(const __grid_co
             } else {
                 const int kvh = r - d.HQ - (isK ? 0 : d.HKV);
                 const size_t slot = ((size_t)b * d.HKV + kvh) * (size_t)d.s_cap + (size_t)(S + i);
-                uint16_t* sc = d.kv_dtype == TSV_I8_SCALED
-                                   ? reinterpret_cast<uint16_t*>(isK ? d.k_scale[l] : d.v_scale[l]) + slot
+                uint16_t* sc = kv_has_scales(d.kv_dtype)
+                                   ? reinterpret_cast<uint16_t*>(isK ? d.k_scale[l] : d.v_scale[l]) +
+                                         slot * kv_scale_words(d.kv_dtype, D)
                                    : nullptr;
                 store_row<E>(x[u], lane, d.kv_dtype, isK ? d.k[l] : d.v[l], slot * D, sc);
             }
@@ -207,7 +240,7 @@ static tsv_status check_append(const tsv_append_desc* d, const int32_t* kv_len) 
         return fail(TSV_EINVAL, "tree_append: B=%d HQ=%d HKV=%d", d->B, d->HQ, d->HKV);
     if (d->D != 64 && d->D != 128 && d->D != 256)
         return fail(TSV_EUNSUPPORTED, "tree_append: head dim %d is not 64, 128 or 256", d->D);
-    if (d->kv_dtype != TSV_F16 && d->kv_dtype != TSV_BF16 && d->kv_dtype != TSV_I8_SCALED)
+    if (!kv_format_ok(d->kv_dtype))
         return fail(TSV_EUNSUPPORTED, "tree_append: cache format %d", d->kv_dtype);
     if (d->rot_dim < 2 || d->rot_dim > d->D || d->rot_dim % 2)
         return fail(TSV_EINVAL, "tree_append: rot_dim=%d must be even and in [2, D=%d]", d->rot_dim, d->D);
@@ -222,6 +255,12 @@ static tsv_status check_append(const tsv_append_desc* d, const int32_t* kv_len) 
             return fail(TSV_EINVAL, "tree_append: layer %d has a null pointer", l);
         if (d->kv_dtype == TSV_I8_SCALED && (!d->k_scale[l] || !d->v_scale[l]))
             return fail(TSV_EINVAL, "tree_append: layer %d Int8 cache without scales", l);
+        if (d->kv_dtype == TSV_I4_G64) {
+            if (!d->k_scale[l] || !d->v_scale[l])
+                return fail(TSV_EINVAL, "tree_append: layer %d 4-bit cache without scales", l);
+            if (((uintptr_t)d->k_scale[l] | (uintptr_t)d->v_scale[l]) & 15)
+                return fail(TSV_EINVAL, "tree_append: layer %d 4-bit scales not 16-byte aligned", l);
+        }
         if (((uintptr_t)d->q_in[l] | (uintptr_t)d->q_out[l] | (uintptr_t)d->k_new[l] | (uintptr_t)d->v_new[l] |
              (uintptr_t)d->k[l] | (uintptr_t)d->v[l]) & 15)
             return fail(TSV_EINVAL, "tree_append: layer %d buffers not 16-byte aligned", l);
