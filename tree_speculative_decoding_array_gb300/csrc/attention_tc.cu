@@ -191,11 +191,63 @@ __device__ __forceinline__ void convert_i8_tile_scaled(const uint8_t* raw, uint8
     }
 }
 
+// 32 codes of 4 bits (one 16-byte chunk) -> fp16 scale * code + bias, one rounding, 13 instructions per 8 codes: masks
+// give 1024 + q (codes 0, 2 of each 16 bits), exact after one subtraction, and 1024 + 16 q (codes 1, 3), recovered
+// exactly by an fma with 1/16 and -64; then one fma with the group's scale and bias.  The halves of a register are
+// codes k and k + 4 of a word, so every 8 features come out in the order 0 4 1 5 2 6 3 7: Q takes the same order in
+// TMEM, and the columns of O are put back when it is read out, so no instruction is spent on the order.
+__device__ __forceinline__ void i4x8_to_f16x8(uint32_t w, __half2 s2, __half2 b2, uint32_t (&out)[4]) {
+    const __half2 k1024 = __floats2half2_rn(1024.f, 1024.f), k16 = __floats2half2_rn(0.0625f, 0.0625f),
+                  k64 = __floats2half2_rn(-64.f, -64.f);
+    const uint32_t v = w >> 8;
+    uint32_t r[4] = {(w & 0x000F000Fu) | 0x64006400u, (w & 0x00F000F0u) | 0x64006400u, (v & 0x000F000Fu) | 0x64006400u,
+                     (v & 0x00F000F0u) | 0x64006400u};
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+        __half2 x = *reinterpret_cast<__half2*>(&r[k]);
+        x = (k & 1) ? __hfma2(x, k16, k64) : __hsub2(x, k1024);
+        x = __hfma2(x, s2, b2);
+        out[k] = *reinterpret_cast<uint32_t*>(&x);
+    }
+}
+
+// Raw 4-bit tile [64 keys x 128 B], 128-byte swizzled as TMA lands it -> the same fp16 operand tile as
+// convert_i8_tile; `pairs` holds this thread's key's four (scale, bias) pairs.  Keys >= nk become 0 whatever their
+// bytes are.  Thread ct takes key ct & 63 and the chunks 2 s + (ct >> 6): 32 codes each, within one group of 64.
+__device__ __forceinline__ void convert_i4_tile(const uint8_t* raw, uint8_t* dst, int nk, int ct, uint4 pairs) {
+    const int key = ct & 63, k7 = key & 7;
+    const uint32_t pr[4] = {pairs.x, pairs.y, pairs.z, pairs.w};
+    uint4 in[4];
+#pragma unroll
+    for (int s = 0; s < 4; ++s)
+        in[s] = *reinterpret_cast<const uint4*>(raw + key * 128 + (((2 * s + (ct >> 6)) ^ k7) << 4));
+    uint8_t* row = dst + key * 128;
+#pragma unroll
+    for (int s = 0; s < 4; ++s) {
+        const __half2 pair = *reinterpret_cast<const __half2*>(&pr[s]);
+        const __half2 s2 = __low2half2(pair), b2 = __high2half2(pair);
+        const uint32_t w[4] = {in[s].x, in[s].y, in[s].z, in[s].w};
+        // features 32 (2 s + half) .. + 31: 64-feature block s, 16-byte chunks 4 half .. 4 half + 3
+        uint8_t* rb = row + s * 8192;
+#pragma unroll
+        for (int c = 0; c < 4; ++c) {
+            uint32_t o[4];
+            i4x8_to_f16x8(w[c], s2, b2, o);
+            const uint4 v = key < nk ? make_uint4(o[0], o[1], o[2], o[3]) : make_uint4(0, 0, 0, 0);
+            *reinterpret_cast<uint4*>(rb + (((4 * (ct >> 6) + c) ^ k7) << 4)) = v;
+        }
+    }
+}
+
 constexpr int kNS = 3;  // stages of the K ring and of the V ring
 
-template <bool I8>
-__global__ void __launch_bounds__(I8 ? kTcThreadsI8 : kTc64Threads16, 1) attn_tc_kernel(const __grid_constant__ TcParams p) {
+// FMT: 0 16-bit caches, 1 Int8, 2 4-bit.  The quantised formats share one pipeline (converter warps, two issuers) and
+// differ in the raw tile and its conversion.
+template <int FMT>
+__global__ void __launch_bounds__(FMT != 0 ? kTcThreadsI8 : kTc64Threads16, 1) attn_tc_kernel(const __grid_constant__ TcParams p) {
     griddep_begin();
+    constexpr bool I8 = FMT != 0;   // the quantised pipeline
+    constexpr bool I4 = FMT == 2;
     extern __shared__ uint8_t smem_raw[];
     uint8_t* sm = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
     // Q, S and P live in TMEM.  16-bit caches: K stages [3 x 32K] at 0, V stages [3 x 32K] at 96K.
@@ -321,7 +373,10 @@ __global__ void __launch_bounds__(I8 ? kTcThreadsI8 : kTc64Threads16, 1) attn_tc
                 const int st = j % NS;
                 if (j >= NS && !tc::mbar_wait(&emptyb[st], ((j / NS) - 1) & 1, abort_flag, 256)) break;
                 const int row = rowbase + j * kTcBK;
-                if (I8) {  // two 128-byte-wide swizzled halves of the 256-byte rows
+                if (I4) {  // 128-byte rows: one swizzled box
+                    tc::mbar_expect_tx(&fullb[st], kTcBK * kTcD / 2);
+                    tc::tma_load_2d((isK ? sRawK : sRawV) + st * 16384, m, &fullb[st], 0, row);
+                } else if (I8) {  // two 128-byte-wide swizzled halves of the 256-byte rows
                     tc::mbar_expect_tx(&fullb[st], kTcBK * kTcD);
                     uint8_t* dst = (isK ? sRawK : sRawV) + st * 16384;
                     tc::tma_load_2d(dst, m, &fullb[st], 0, row);
@@ -469,20 +524,29 @@ __global__ void __launch_bounds__(I8 ? kTcThreadsI8 : kTc64Threads16, 1) attn_tc
         // each thread converts key ct & 63 of every tile and multiplies its codes by that key's scale; the scale
         // is fetched one tile ahead so that the global load's latency overlaps the previous tile's work
         const int ct = threadIdx.x - 320;
-        const uint16_t* vsrc = p.vs[layer] + ((size_t)b * p.HKV + kvh) * (size_t)p.s_cap + k_begin + (ct & 63);
-        auto vscale = [&](int jj) -> uint16_t {
-            return (jj < ntiles && k_begin + jj * kTcBK + (ct & 63) < k_end) ? vsrc[jj * kTcBK] : (uint16_t)0;
+        const size_t key0 = ((size_t)b * p.HKV + kvh) * (size_t)p.s_cap + k_begin + (ct & 63);
+        auto vscale = [&](int jj) {
+            const bool real = jj < ntiles && k_begin + jj * kTcBK + (ct & 63) < k_end;
+            if constexpr (I4)
+                return real ? reinterpret_cast<const uint4*>(p.vs[layer])[key0 + (size_t)jj * kTcBK] : make_uint4(0, 0, 0, 0);
+            else
+                return real ? p.vs[layer][key0 + (size_t)jj * kTcBK] : (uint16_t)0;
         };
-        uint16_t sc_next = vscale(0);
+        auto sc_next = vscale(0);
         for (int j = 0; j < ntiles; ++j) {
             const int st = j % NS, cb = j & 1;
-            const __half sh = __ushort_as_half(sc_next);
+            const auto sc = sc_next;
             sc_next = vscale(j + 1);
             if (!__all_sync(0xFFFFFFFFu, tc::mbar_wait(&vfull[st], (j / NS) & 1, abort_flag))) break;
             const int nk = min(kTcBK, k_end - (k_begin + j * kTcBK));
             // fp16 V slot cb free once P V of tile j - 2 is done
             if (j >= 2 && !__all_sync(0xFFFFFFFFu, tc::mbar_wait(&sp_free[cb], ((j >> 1) - 1) & 1, abort_flag))) break;
-            convert_i8_tile_scaled(sRawV + st * 16384, sV + cb * kTileBytes, nk, ct, __halves2half2(sh, sh));
+            if constexpr (I4) {
+                convert_i4_tile(sRawV + st * 16384, sV + cb * kTileBytes, nk, ct, sc);
+            } else {
+                const __half sh = __ushort_as_half(sc);
+                convert_i8_tile_scaled(sRawV + st * 16384, sV + cb * kTileBytes, nk, ct, __halves2half2(sh, sh));
+            }
             tc::fence_proxy_async_smem();
             __syncwarp();
             tc::mbar_arrive_one(&vempty[st]);
@@ -492,20 +556,29 @@ __global__ void __launch_bounds__(I8 ? kTcThreadsI8 : kTc64Threads16, 1) attn_tc
         // ------------------------------------------------------------ Int8 K converters
         // as the V converters: key ct & 63 of every tile, times its scale, fetched one tile ahead
         const int ct = threadIdx.x - 192;
-        const uint16_t* ksrc = p.ks[layer] + ((size_t)b * p.HKV + kvh) * (size_t)p.s_cap + k_begin + (ct & 63);
-        auto kscale = [&](int jj) -> uint16_t {
-            return (jj < ntiles && k_begin + jj * kTcBK + (ct & 63) < k_end) ? ksrc[jj * kTcBK] : (uint16_t)0;
+        const size_t key0 = ((size_t)b * p.HKV + kvh) * (size_t)p.s_cap + k_begin + (ct & 63);
+        auto kscale = [&](int jj) {
+            const bool real = jj < ntiles && k_begin + jj * kTcBK + (ct & 63) < k_end;
+            if constexpr (I4)
+                return real ? reinterpret_cast<const uint4*>(p.ks[layer])[key0 + (size_t)jj * kTcBK] : make_uint4(0, 0, 0, 0);
+            else
+                return real ? p.ks[layer][key0 + (size_t)jj * kTcBK] : (uint16_t)0;
         };
-        uint16_t sc_next = kscale(0);
+        auto sc_next = kscale(0);
         for (int j = 0; j < ntiles; ++j) {
             const int st = j % NS, cb = j & 1;
-            const __half sh = __ushort_as_half(sc_next);
+            const auto sc = sc_next;
             sc_next = kscale(j + 1);
             if (!__all_sync(0xFFFFFFFFu, tc::mbar_wait(&kfull[st], (j / NS) & 1, abort_flag))) break;
             const int nk = min(kTcBK, k_end - (k_begin + j * kTcBK));
             // fp16 K slot cb free once Q K^T of tile j - 2 is done
             if (j >= 2 && !__all_sync(0xFFFFFFFFu, tc::mbar_wait(&s_full[cb], ((j >> 1) - 1) & 1, abort_flag))) break;
-            convert_i8_tile_scaled(sRawK + st * 16384, sK + cb * kTileBytes, nk, ct, __halves2half2(sh, sh));
+            if constexpr (I4) {
+                convert_i4_tile(sRawK + st * 16384, sK + cb * kTileBytes, nk, ct, sc);
+            } else {
+                const __half sh = __ushort_as_half(sc);
+                convert_i8_tile_scaled(sRawK + st * 16384, sK + cb * kTileBytes, nk, ct, __halves2half2(sh, sh));
+            }
             tc::fence_proxy_async_smem();
             __syncwarp();
             tc::mbar_arrive_one(&kempty[st]);
@@ -545,6 +618,13 @@ __global__ void __launch_bounds__(I8 ? kTcThreadsI8 : kTc64Threads16, 1) attn_tc
                     for (int i = 0; i < 8; ++i) {
                         uint4 x = v[c2 * 8 + i];
                         if (!bf) x = bf16x8_to_f16x8(x);
+                        if (I4) {  // feature order 0 4 1 5 2 6 3 7
+                            w[4 * i] = __byte_perm(x.x, x.z, 0x5410);
+                            w[4 * i + 1] = __byte_perm(x.x, x.z, 0x7632);
+                            w[4 * i + 2] = __byte_perm(x.y, x.w, 0x5410);
+                            w[4 * i + 3] = __byte_perm(x.y, x.w, 0x7632);
+                            continue;
+                        }
                         w[4 * i] = x.x;
                         w[4 * i + 1] = x.y;
                         w[4 * i + 2] = x.z;
@@ -699,6 +779,19 @@ __global__ void __launch_bounds__(I8 ? kTcThreadsI8 : kTc64Threads16, 1) attn_tc
                 tc::tmem_ld32(tmem + lane_base + kColO + ch * 32, o);
                 tc::tmem_wait_ld();
                 if (!row_ok) continue;
+                if (I4) {  // columns 0 4 1 5 2 6 3 7 of every 8 features back in order
+#pragma unroll
+                    for (int k = 0; k < 4; ++k) {
+                        uint32_t y[8];
+#pragma unroll
+                        for (int e = 0; e < 8; ++e) y[e] = o[8 * k + e];
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) {
+                            o[8 * k + e] = y[2 * e];
+                            o[8 * k + 4 + e] = y[2 * e + 1];
+                        }
+                    }
+                }
                 if (p.splits == 1) {
                     uint4* dst = reinterpret_cast<uint4*>(reinterpret_cast<__nv_bfloat16*>(p.o[layer]) +
                                                           ((size_t)(b * T + node) * p.HQ + head) * kTcD + ch * 32);
@@ -1597,13 +1690,15 @@ static EncodeTiledFn encode_fn() {
 // 64 rows with the 128-byte swizzle the MMA operands use.  Int8 caches:
 // boxes of 128 bytes x 64 rows, 128-byte swizzled too (bank-conflict-free
 // reads for the converter, which re-lays them out as fp16 operand tiles).
+// 4-bit caches: rows of 128 bytes, boxes of 128 bytes x 64 rows.
 // quarters = true (Int8 K for the 128-key kernel): boxes of 64 bytes x 128 rows (one dim quarter of a 128-key
 // tile) with the 64-byte swizzle.
-static bool make_kv_map(CUtensorMap* m, const void* base, long long rows, bool i8, bool quarters = false) {
+static bool make_kv_map(CUtensorMap* m, const void* base, long long rows, int kv_dtype, bool quarters = false) {
     EncodeTiledFn enc = encode_fn();
     if (!enc) return false;
-    cuuint64_t dims[2] = {(cuuint64_t)kTcD, (cuuint64_t)rows};
-    cuuint64_t strides[1] = {(cuuint64_t)kTcD * (i8 ? 1 : 2)};
+    const bool i8 = kv_has_scales(kv_dtype);  // byte elements
+    cuuint64_t dims[2] = {(cuuint64_t)(kv_dtype == TSV_I4_G64 ? kTcD / 2 : kTcD), (cuuint64_t)rows};
+    cuuint64_t strides[1] = {(cuuint64_t)kv_row_bytes(kv_dtype, kTcD)};
     cuuint32_t box[2] = {quarters ? 64u : (i8 ? 128u : 64u), quarters ? (cuuint32_t)kWK : (cuuint32_t)kTcBK};
     cuuint32_t es[2] = {1, 1};
     return enc(m, i8 ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : CU_TENSOR_MAP_DATA_TYPE_UINT16, 2, const_cast<void*>(base), dims,
@@ -1613,7 +1708,7 @@ static bool make_kv_map(CUtensorMap* m, const void* base, long long rows, bool i
 }
 
 bool tc_supported(const tsv_attn_desc* d) {
-    return d->D == kTcD && (d->kv_dtype == TSV_F16 || d->kv_dtype == TSV_BF16 || d->kv_dtype == TSV_I8_SCALED) &&
+    return d->D == kTcD && kv_format_ok(d->kv_dtype) &&
            (long long)d->B * d->HKV * d->s_cap < (1LL << 31) - kTcBK;
 }
 
@@ -1624,7 +1719,7 @@ int tc_mtiles(const tsv_attn_desc* d) { return ((d->HQ / d->HKV) * d->T + kTcRow
 // with a single, mostly empty row tile the deeper 64-key pipeline is faster).  Int8 caches take the 64-key
 // kernel: on the 16- and 64-node workloads the 128-key Int8 kernel measured level with it or up to 2 % slower.
 bool tc_wide(const tsv_attn_desc* d) {
-    if (d->path == TSV_ATTN_TCGEN05_64) return false;
+    if (d->path == TSV_ATTN_TCGEN05_64 || d->kv_dtype == TSV_I4_G64) return false;
     if (d->path == TSV_ATTN_TCGEN05_128) return true;
     return d->kv_dtype != TSV_I8_SCALED && tc_mtiles(d) >= 2;
 }
@@ -1636,7 +1731,8 @@ tsv_status launch_tc(const tsv_attn_desc* d, int splits, int chunk, float* ws_o,
     const bool wide = tc_wide(d);
     const long long rows = (long long)d->B * d->HKV * d->s_cap;
     for (int l = 0; l < d->n_layers; ++l) {
-        if (!make_kv_map(&prm.kmap[l], d->k[l], rows, i8, i8 && wide) || !make_kv_map(&prm.vmap[l], d->v[l], rows, i8))
+        if (!make_kv_map(&prm.kmap[l], d->k[l], rows, d->kv_dtype, i8 && wide) ||
+            !make_kv_map(&prm.vmap[l], d->v[l], rows, d->kv_dtype))
             return fail(TSV_ECUDA, "tree_verify_attention: tensor map encoding failed for layer %d", l);
         prm.q[l] = reinterpret_cast<const uint16_t*>(d->q[l]);
         prm.o[l] = d->o[l];
@@ -1666,15 +1762,18 @@ tsv_status launch_tc(const tsv_attn_desc* d, int splits, int chunk, float* ws_o,
     if (i8 && wide) {
         cudaFuncSetAttribute(attn_tcw8_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kW8Smem);
         launch_pdl(attn_tcw8_kernel, (unsigned)items, kW8Threads, kW8Smem, stream, prm);
+    } else if (d->kv_dtype == TSV_I4_G64) {
+        cudaFuncSetAttribute(attn_tc_kernel<2>, cudaFuncAttributeMaxDynamicSharedMemorySize, kTcSmem);
+        launch_pdl(attn_tc_kernel<2>, (unsigned)items, kTcThreadsI8, kTcSmem, stream, prm);
     } else if (i8) {
-        cudaFuncSetAttribute(attn_tc_kernel<true>, cudaFuncAttributeMaxDynamicSharedMemorySize, kTcSmem);
-        launch_pdl(attn_tc_kernel<true>, (unsigned)items, kTcThreadsI8, kTcSmem, stream, prm);
+        cudaFuncSetAttribute(attn_tc_kernel<1>, cudaFuncAttributeMaxDynamicSharedMemorySize, kTcSmem);
+        launch_pdl(attn_tc_kernel<1>, (unsigned)items, kTcThreadsI8, kTcSmem, stream, prm);
     } else if (wide) {
         cudaFuncSetAttribute(attn_tcw_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kWSmem);
         launch_pdl(attn_tcw_kernel, (unsigned)items, kTcThreads16, kWSmem, stream, prm);
     } else {
-        cudaFuncSetAttribute(attn_tc_kernel<false>, cudaFuncAttributeMaxDynamicSharedMemorySize, kTcSmem);
-        launch_pdl(attn_tc_kernel<false>, (unsigned)items, kTc64Threads16, kTcSmem, stream, prm);
+        cudaFuncSetAttribute(attn_tc_kernel<0>, cudaFuncAttributeMaxDynamicSharedMemorySize, kTcSmem);
+        launch_pdl(attn_tc_kernel<0>, (unsigned)items, kTc64Threads16, kTcSmem, stream, prm);
     }
     return check_launch("tree_verify_attention(tcgen05)");
 }
