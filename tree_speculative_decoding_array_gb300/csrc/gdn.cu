@@ -9,7 +9,6 @@
 //
 // This file holds the CUDA-core kernels and the dispatch:
 //   gdn_recur_kernel   token by token (short scans, commits): the state stays in registers, one pass over it
-//   gdn_tree_kernel    a whole tree from one read of the state (small trees, head sizes the tensor-core kernel lacks)
 #include <math.h>
 
 #include "common.cuh"
@@ -19,9 +18,6 @@ namespace tsv {
 constexpr int kGdnRows = 32;      // state rows (value features) per CTA
 constexpr int kGdnThreads = 128;  // 4 warps of 8 rows; 8 lanes share a row
 constexpr int kGdnBatch = 8;      // tokens whose q and k rows are in shared memory together
-constexpr float kMinLogDecay = -150.f;  // e^-150 is 0 in fp32: a smaller (or infinite) log decay means the same
-
-__device__ __forceinline__ float clamp_decay(float g) { return g < kMinLogDecay ? kMinLogDecay : g; }  // keeps NaN
 
 // One bf16 row of DK features, read by a whole warp, normalised and written to shared memory as fp32.
 template <int DK>
@@ -199,133 +195,8 @@ __global__ void __launch_bounds__(kGdnThreads) gdn_recur_kernel(const __grid_con
                 make_float4(s[r][4 * c], s[r][4 * c + 1], s[r][4 * c + 2], s[r][4 * c + 3]);
 }
 
-// The whole tree from one read of the state.  With G_i the log decay summed from the root to node i, the recurrence
-// along i's ancestors unrolls to
-//     u_i = beta_i (v_i - e^{G_i} S k_i - sum_{j strict ancestor} e^{G_i - G_j} (k_j . k_i) u_j)
-//     o_i = e^{G_i} S q_i + sum_{j ancestor or self} e^{G_i - G_j} (k_j . q_i) u_j
-// so S is only needed for the 2 T products S k_i, S q_i, and siblings share nothing but ancestors.  Ancestor words
-// are cut to lower node indices, so that no input can make the substitution read ahead.  G is summed in fp64 (its
-// differences lose nothing however far the decays reach).  Only ancestors are ever read, so a NaN or an infinity in
-// one branch stays in it.
-template <int DK>
-__global__ void __launch_bounds__(kGdnThreads) gdn_tree_kernel(const __grid_constant__ tsv_gdn_desc d,
-                                                               const uint64_t* __restrict__ anc) {
-    griddep_begin();
-    extern __shared__ __align__(16) float smf[];
-    __shared__ double G[TSV_MAX_T];
-    __shared__ uint64_t seen[TSV_MAX_T];  // strict ancestors
-    __shared__ float be[TSV_MAX_T];
-    const int T = d.T;
-    float* ks = smf;                      // [T][DK]
-    float* qs = ks + T * DK;              // [T][DK]
-    float* sk = qs + T * DK;              // [T][kGdnRows] S k_i, then u_i
-    float* sq = sk + T * kGdnRows;        // [T][kGdnRows] S q_i
-    float* A = sq + T * kGdnRows;         // [T][T] e^{G_i - G_j} (k_i . k_j)
-    float* P = A + T * T;                 // [T][T] e^{G_i - G_j} (q_i . k_j)
-    const int slices = d.DV / kGdnRows;
-    int item = blockIdx.x;
-    const int slice = item % slices;
-    item /= slices;
-    const int h = item % d.HV;
-    const int b = (item / d.HV) % d.B;
-    const int layer = item / (d.HV * d.B);
-    const int hk = h / (d.HV / d.HK);
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const size_t row0 = (size_t)b * T;
-
-    const size_t s0 = (((size_t)b * d.HV + h) * d.DV + slice * kGdnRows + warp * 8) * DK;
-    float s[2][DK / 8];
-    load_state<DK, 2>(d.state[layer] + s0, s, lane);
-
-    const uint16_t* Q = reinterpret_cast<const uint16_t*>(d.q[layer]);
-    const uint16_t* K = reinterpret_cast<const uint16_t*>(d.k[layer]);
-    for (int i = warp; i < T; i += kGdnThreads / 32) {
-        stage_row<DK>(K + ((row0 + i) * d.HK + hk) * DK, ks + i * DK, d.norm_eps, 1.f, lane);
-        stage_row<DK>(Q + ((row0 + i) * d.HK + hk) * DK, qs + i * DK, d.norm_eps, d.scale, lane);
-    }
-    for (int i = threadIdx.x; i < T; i += kGdnThreads) {
-        uint64_t a = anc[row0 + i] & ((1ull << i) - 1ull);
-        seen[i] = a;
-        be[i] = d.beta[layer][(row0 + i) * d.HV + h];
-        double sum = (double)clamp_decay(d.g[layer][(row0 + i) * d.HV + h]);
-        for (; a; a &= a - 1) sum += (double)clamp_decay(d.g[layer][(row0 + __ffsll((long long)a) - 1) * d.HV + h]);
-        G[i] = sum;
-    }
-    __syncthreads();
-
-    for (int i = 0; i < T; ++i) {  // S k_i and S q_i
-        float a[2] = {0.f, 0.f}, o[2] = {0.f, 0.f};
-#pragma unroll
-        for (int c = 0; c < DK / 32; ++c) {
-            const float4 kk = *reinterpret_cast<const float4*>(ks + i * DK + 32 * c + 4 * (lane % 8));
-            const float4 qq = *reinterpret_cast<const float4*>(qs + i * DK + 32 * c + 4 * (lane % 8));
-#pragma unroll
-            for (int r = 0; r < 2; ++r) {
-                a[r] = fmaf(s[r][4 * c], kk.x, fmaf(s[r][4 * c + 1], kk.y, fmaf(s[r][4 * c + 2], kk.z, fmaf(s[r][4 * c + 3], kk.w, a[r]))));
-                o[r] = fmaf(s[r][4 * c], qq.x, fmaf(s[r][4 * c + 1], qq.y, fmaf(s[r][4 * c + 2], qq.z, fmaf(s[r][4 * c + 3], qq.w, o[r]))));
-            }
-        }
-#pragma unroll
-        for (int x = 4; x > 0; x >>= 1)
-#pragma unroll
-            for (int r = 0; r < 2; ++r) {
-                a[r] += __shfl_xor_sync(0xFFFFFFFFu, a[r], x);
-                o[r] += __shfl_xor_sync(0xFFFFFFFFu, o[r], x);
-            }
-        if (lane % 8 == 0) {
-#pragma unroll
-            for (int r = 0; r < 2; ++r) {
-                sk[i * kGdnRows + warp * 8 + r * 4 + lane / 8] = a[r];
-                sq[i * kGdnRows + warp * 8 + r * 4 + lane / 8] = o[r];
-            }
-        }
-    }
-    // inner products with the ancestors, one node per warp at a time
-    for (int i = warp; i < T; i += kGdnThreads / 32) {
-        for (uint64_t a = seen[i] | (1ull << i); a; a &= a - 1) {
-            const int j = __ffsll((long long)a) - 1;
-            float kk = 0.f, qk = 0.f;
-#pragma unroll
-            for (int e = lane; e < DK; e += 32) {
-                kk = fmaf(ks[i * DK + e], ks[j * DK + e], kk);
-                qk = fmaf(qs[i * DK + e], ks[j * DK + e], qk);
-            }
-#pragma unroll
-            for (int x = 16; x > 0; x >>= 1) {
-                kk += __shfl_xor_sync(0xFFFFFFFFu, kk, x);
-                qk += __shfl_xor_sync(0xFFFFFFFFu, qk, x);
-            }
-            if (lane == 0) {
-                const float w = expf((float)(G[i] - G[j]));
-                A[i * T + j] = w * kk;
-                P[i * T + j] = w * qk;
-            }
-        }
-    }
-    __syncthreads();
-    if (warp == 0) {  // substitution: lane = value feature of the slice
-        const __nv_bfloat16* V = reinterpret_cast<const __nv_bfloat16*>(d.v[layer]);
-        __nv_bfloat16* O = reinterpret_cast<__nv_bfloat16*>(d.o[layer]);
-        for (int i = 0; i < T; ++i) {
-            const size_t at = ((row0 + i) * d.HV + h) * d.DV + slice * kGdnRows + lane;
-            const float e = expf((float)G[i]);
-            float r = __bfloat162float(V[at]) - e * sk[i * kGdnRows + lane], o = e * sq[i * kGdnRows + lane];
-            for (uint64_t a = seen[i]; a; a &= a - 1) {
-                const int j = __ffsll((long long)a) - 1;
-                const float u = sk[j * kGdnRows + lane];
-                r = fmaf(-A[i * T + j], u, r);
-                o = fmaf(P[i * T + j], u, o);
-            }
-            const float u = be[i] * r;
-            sk[i * kGdnRows + lane] = u;
-            O[at] = __float2bfloat16(fmaf(P[i * T + i], u, o));
-        }
-    }
-}
-
-static size_t tree_smem(const tsv_gdn_desc* d) {
-    return ((size_t)2 * d->T * d->DK + (size_t)2 * d->T * kGdnRows + (size_t)2 * d->T * d->T) * sizeof(float);
-}
+// Defined in gdn_tree.cu.
+void launch_gdn_tree(const tsv_gdn_desc& d, const uint64_t* anc, cudaStream_t stream);
 
 enum GdnCall { kGdnVerify, kGdnCommit, kGdnScan };
 
@@ -379,15 +250,7 @@ extern "C" tsv_status tsv_gdn_tree_verify(const tsv_gdn_desc* d, const uint64_t*
     if (st != TSV_OK || d->B == 0) return st;
     if (!anc) return fail(TSV_EINVAL, "gdn_tree_verify: anc must be non-null");
     const tsv_gdn_desc x = with_scale(d);
-    const unsigned grid = (unsigned)((long long)d->n_layers * d->B * d->HV * (d->DV / kGdnRows));
-    const size_t sm = tree_smem(d);
-    if (d->DK == 64) {
-        cudaFuncSetAttribute(gdn_tree_kernel<64>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)sm);
-        launch_pdl(gdn_tree_kernel<64>, grid, kGdnThreads, sm, stream, x, anc);
-    } else {
-        cudaFuncSetAttribute(gdn_tree_kernel<128>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)sm);
-        launch_pdl(gdn_tree_kernel<128>, grid, kGdnThreads, sm, stream, x, anc);
-    }
+    launch_gdn_tree(x, anc, stream);
     return check_launch("gdn_tree_verify");
 }
 

@@ -1,0 +1,221 @@
+// Building blocks of the gated delta rule's tensor-core kernels: fp16 fragments of mma.sync, rows staged with an
+// exact power-of-two scale, the block's triangular system.
+//
+// A block of up to 64 rows (a tree's nodes, or consecutive tokens) is one triangular system.  With G_i the log decay
+// summed over i's ancestors and itself, unit rows k_i, q_i and the state S [DV, DK] ahead of the block,
+//     u_i = beta_i (v_i - e^{G_i} S k_i - sum_{j before i} e^{G_i - G_j} (k_i . k_j) u_j)
+//     o_i = e^{G_i} S q_i + sum_{j before i, or i} e^{G_i - G_j} (q_i . k_j) u_j
+// ("before": strict ancestor, or earlier token).  Every value feature (row of S, column of u and o) is a system of
+// its own with the same matrices, so a warp owns 16 features per tile and keeps S, u and o of them in registers as
+// mma fragments; only the matrices, K, Q and V pass through shared memory.  The rows are taken 16 at a time: R_b from
+// S and the blocks before, U_b = (I + A_bb)^-1 R_b with that 16 x 16 inverse, then O_b.
+//
+// Operands are fp16 with power-of-two scales, which cost nothing in accuracy: K and Q rows hold bf16 values (8 bits,
+// exact in fp16 once the row's largest value is scaled to [1, 2); what falls below 2^-24 of it is lost), S, R and U
+// of one value feature share a scale (their equations are linear in them).  An fp16 operand is within 2^-12 of its
+// value; an hi + lo pair within 2^-22 (or 2^-25 of the feature's largest value).  Accumulation is fp32.
+#pragma once
+
+#include "common.cuh"
+#include "tc.cuh"
+
+namespace tsv {
+
+constexpr float kLog2e = 1.4426950408889634f;
+constexpr float kMinLogDecay = -150.f;  // e^-150 is 0 in fp32: a smaller (or infinite) log decay means the same
+
+__device__ __forceinline__ float clamp_decay(float g) { return g < kMinLogDecay ? kMinLogDecay : g; }  // keeps NaN
+
+__device__ __forceinline__ void mma_16816(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+    asm volatile(
+        "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+        : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+        : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+__device__ __forceinline__ void ldsm4(uint32_t (&r)[4], uint32_t addr) {
+    asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0,%1,%2,%3}, [%4];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+                 : "r"(addr)
+                 : "memory");
+}
+__device__ __forceinline__ void ldsm4_t(uint32_t (&r)[4], uint32_t addr) {
+    asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0,%1,%2,%3}, [%4];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+                 : "r"(addr)
+                 : "memory");
+}
+__device__ __forceinline__ void stsm4_t(uint32_t addr, const uint32_t (&r)[4]) {
+    asm volatile("stmatrix.sync.aligned.m8n8.x4.trans.shared.b16 [%0], {%1,%2,%3,%4};" ::"r"(addr), "r"(r[0]), "r"(r[1]),
+                 "r"(r[2]), "r"(r[3])
+                 : "memory");
+}
+__device__ __forceinline__ uint32_t f16x2(float a, float b) {
+    const __half2 h = __floats2half2_rn(a, b);
+    return *reinterpret_cast<const uint32_t*>(&h);
+}
+__device__ __forceinline__ uint32_t bf16x2(float a, float b) {
+    const __nv_bfloat162 h = __floats2bfloat162_rn(a, b);
+    return *reinterpret_cast<const uint32_t*>(&h);
+}
+// hi + lo fp16 pieces of two values.
+__device__ __forceinline__ void split2(float a, float b, uint32_t& hi, uint32_t& lo) {
+    hi = f16x2(a, b);
+    const float2 h = f16x2_to_f32x2(hi);
+    lo = f16x2(a - h.x, b - h.y);
+}
+// NaN in `flag` once any half of x is an infinity or a NaN.
+__device__ __forceinline__ void watch(uint32_t& flag, uint32_t x) {
+    const __half2 z = __floats2half2_rn(0.f, 0.f);
+    const __half2 f = __hfma2(*reinterpret_cast<const __half2*>(&x), z, *reinterpret_cast<const __half2*>(&flag));
+    flag = *reinterpret_cast<const uint32_t*>(&f);
+}
+__device__ __forceinline__ bool watched(uint32_t flag) {
+    const float2 f = f16x2_to_f32x2(flag);
+    return !(f.x == 0.f && f.y == 0.f);
+}
+// 2^-e and 2^e for m in [2^e, 2^(e+1)); 1 for 0, infinities and NaN.
+__device__ __forceinline__ void pow2_scale(float m, float& down, float& up) {
+    uint32_t e = (__float_as_uint(m) >> 23) & 255u;
+    if (e == 255u || m == 0.f) e = 127u;
+    e = min(max(e, 1u), 253u);
+    down = __uint_as_float((254u - e) << 23);
+    up = __uint_as_float(e << 23);
+}
+
+// Shared-memory tiles: rows of BYTES bytes, 16-byte chunk c of row r at chunk c ^ (r & 7), so that the 8 rows of an
+// ldmatrix fall into different banks.
+template <int BYTES>
+__device__ __forceinline__ uint32_t tile_at(uint32_t base, int row, int chunk) {
+    return base + (uint32_t)(row * BYTES + ((chunk ^ (row & 7)) << 4));
+}
+
+// Per-row scalars of a block.
+struct GdnRows {
+    float g_hi[64], g_lo[64];  // G in units of ln 2, as hi + lo (differences of far sums keep fp32 accuracy)
+    float fk[64], fq[64];      // what a staged row's products are multiplied with: its scale and norm (and q's scale)
+    float beta[64];
+    float ck[64], cq[64];      // 2^G fk, 2^G fq
+    uint64_t before[64];       // rows ahead of i in its system (strict ancestors, or earlier tokens)
+};
+
+// One bf16 row chunk of 8 values -> fp16 scaled by the row's power of two; DK / 8 consecutive lanes share a row.
+// Returns the factor that products with the staged row need.
+template <int DK>
+__device__ __forceinline__ float stage_chunk(uint4 w, float norm_eps, uint4& out) {
+    float x[8] = {bf16_lo(w.x), bf16_hi(w.x), bf16_lo(w.y), bf16_hi(w.y), bf16_lo(w.z), bf16_hi(w.z), bf16_lo(w.w), bf16_hi(w.w)};
+    float ss = 0.f, mx = 0.f;
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+        ss = fmaf(x[e], x[e], ss);
+        mx = fmaxf(mx, fabsf(x[e]));
+    }
+#pragma unroll
+    for (int o = DK / 16; o > 0; o >>= 1) {
+        ss += __shfl_xor_sync(0xFFFFFFFFu, ss, o);
+        mx = fmaxf(mx, __shfl_xor_sync(0xFFFFFFFFu, mx, o));
+    }
+    float down, up;
+    pow2_scale(mx, down, up);
+    out = make_uint4(f16x2(x[0] * down, x[1] * down), f16x2(x[2] * down, x[3] * down), f16x2(x[4] * down, x[5] * down),
+                     f16x2(x[6] * down, x[7] * down));
+    return norm_eps > 0.f ? up / sqrtf(ss + norm_eps) : up;
+}
+
+// Products of one 16-row block with the K rows of its own and the blocks before, decayed and masked:
+//   q == false: rows K_b; -A (fp16 pieces) for the blocks before, A itself (fp32) for the block's own
+//   q == true:  rows Q_b; P (fp16)
+// kq: K rows [T] then Q rows [T]; a16 / p16: [T rows][128 B] tiles; diag: this block's [16][17] fp32.
+template <int DK, int NB, int PIECES>
+__device__ __forceinline__ void block_products(bool q, int b, uint32_t kq, char* a16, char* p16, float* diag,
+                                               const GdnRows& rw, uint32_t& flag, int lane) {
+    constexpr int KB = DK * 2;  // bytes per row
+    constexpr int T = 16 * NB;
+    float acc[NB][2][4];
+#pragma unroll
+    for (int c = 0; c < NB; ++c)
+#pragma unroll
+        for (int n = 0; n < 2; ++n) acc[c][n][0] = acc[c][n][1] = acc[c][n][2] = acc[c][n][3] = 0.f;
+    const int arow = (q ? T : 0) + b * 16 + (lane & 15);
+    const int brow = ((lane >> 4) << 3) + (lane & 7);
+#pragma unroll
+    for (int ks = 0; ks < DK / 16; ++ks) {
+        uint32_t a[4];
+        ldsm4(a, tile_at<KB>(kq, arow, 2 * ks + (lane >> 4)));
+#pragma unroll
+        for (int c = 0; c < NB; ++c) {
+            if (c > b) break;
+            uint32_t w[4];
+            ldsm4(w, tile_at<KB>(kq, c * 16 + brow, 2 * ks + ((lane >> 3) & 1)));
+            mma_16816(acc[c][0], a, w[0], w[1]);
+            mma_16816(acc[c][1], a, w[2], w[3]);
+        }
+    }
+    const int g = lane >> 2, t = lane & 3;
+#pragma unroll
+    for (int c = 0; c < NB; ++c) {
+        if (c > b) break;
+#pragma unroll
+        for (int half = 0; half < 2; ++half) {
+            const int il = g + 8 * half, i = b * 16 + il;
+            const uint64_t seen = q ? rw.before[i] | (1ull << i) : rw.before[i];
+            const float gh = rw.g_hi[i], gl = rw.g_lo[i];
+            const float f = q ? rw.fq[i] : rw.beta[i] * rw.fk[i];
+#pragma unroll
+            for (int n = 0; n < 2; ++n) {
+                float y[2];
+#pragma unroll
+                for (int e = 0; e < 2; ++e) {
+                    const int j = c * 16 + n * 8 + 2 * t + e;
+                    const float w = tc::ex2_approx((gh - rw.g_hi[j]) + (gl - rw.g_lo[j]));
+                    const float x = acc[c][n][2 * half + e] * (f * rw.fk[j]) * w;
+                    y[e] = ((seen >> j) & 1ull) ? x : 0.f;
+                }
+                const int jl = n * 8 + 2 * t;
+                if (q) {
+                    const uint32_t h = f16x2(y[0], y[1]);
+                    watch(flag, h);
+                    *reinterpret_cast<uint32_t*>(p16 + tile_at<128>(0, i, 2 * c + n) + 4 * t) = h;
+                } else if (c == b) {
+                    diag[il * 17 + jl] = y[0];
+                    diag[il * 17 + jl + 1] = y[1];
+                } else {
+                    uint32_t hi, lo;
+                    split2(-y[0], -y[1], hi, lo);
+                    watch(flag, hi);
+                    *reinterpret_cast<uint32_t*>(a16 + tile_at<128>(0, i, 2 * c + n) + 4 * t) = hi;
+                    if (PIECES == 2) *reinterpret_cast<uint32_t*>(a16 + T * 128 + tile_at<128>(0, i, 2 * c + n) + 4 * t) = lo;
+                }
+            }
+        }
+    }
+}
+
+// (I + A_bb)^-1 of one block by forward substitution, a column per lane (both half-warps do the same), stored over
+// block (b, b) of the a16 tile.
+template <int NB, int PIECES>
+__device__ __forceinline__ void block_inverse(int b, char* a16, const float* diag, uint32_t& flag, int lane) {
+    constexpr int T = 16 * NB;
+    const int c = lane & 15;
+    float x[16];
+#pragma unroll
+    for (int i = 0; i < 16; ++i) {
+        float s = i == c ? 1.f : 0.f;
+#pragma unroll
+        for (int j = 0; j < i; ++j) s = fmaf(-diag[i * 17 + j], x[j], s);
+        x[i] = s;
+    }
+    if (lane < 16) {
+#pragma unroll
+        for (int i = 0; i < 16; ++i) {
+            const int row = b * 16 + i, col = b * 16 + c;
+            uint32_t hi, lo;
+            split2(x[i], 0.f, hi, lo);
+            watch(flag, hi);
+            char* at = a16 + tile_at<128>(0, row, col >> 3) + 2 * (col & 7);
+            *reinterpret_cast<uint16_t*>(at) = (uint16_t)hi;
+            if (PIECES == 2) *reinterpret_cast<uint16_t*>(at + T * 128) = (uint16_t)lo;
+        }
+    }
+}
+
+}  // namespace tsv

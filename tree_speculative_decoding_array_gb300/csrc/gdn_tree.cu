@@ -1,0 +1,406 @@
+// tsv_gdn_tree_verify: every node of a draft tree through the recurrent layers, from one read of the state.
+//
+// mlxcel issue #1204 and Splash issue #728 ("What it does"): recurrent layers cannot take a mask and a flattened tree
+// would leak state between siblings, so each node runs from its own parent's state.  The recurrence along a node's
+// ancestors unrolls into one triangular system over the tree (gdn_tc.cuh), in which the state appears only in the
+// products S k_i and S q_i: no node's state is ever formed.
+//
+// One CTA of 4 warps per (layer, sequence, value head): a warp owns DV / 4 value features and holds their rows of S
+// as fp16 fragments.  The state's loads are issued first and land while K, Q and V are staged and the system's
+// matrices are built.
+#include <math.h>
+
+#include "gdn_tc.cuh"
+
+namespace tsv {
+
+constexpr int kTreeThreads = 128;
+
+template <int DK, int DV, int NB>
+struct TreeSmem {
+    static constexpr int T = 16 * NB;
+    static constexpr int kq = 0;                       // K rows [T], Q rows [T], DK fp16 each
+    static constexpr int v = kq + 2 * T * DK * 2;      // V rows [T], DV bf16 each; o over them
+    static constexpr int a16 = v + T * DV * 2;         // [T][64] fp16: -A below the diagonal blocks, inverses on them
+    static constexpr int p16 = a16 + T * 128;          // [T][64] fp16: P
+    static constexpr int diag = p16 + T * 128;         // [NB][16][17] fp32: A of the diagonal blocks
+    static constexpr int rows = (diag + NB * 16 * 17 * 4 + 15) / 16 * 16;
+    static constexpr int total = rows + (int)sizeof(GdnRows);
+    // the fp32 path: u [T][DV] over kq and v, one node's k and q over a16, its ancestors' products over p16
+    static_assert(T * DV * 4 <= a16 && 2 * DK * 4 <= T * 128 && 2 * 64 * 4 <= T * 128, "fp32 path does not fit");
+};
+
+// One bf16 row of DK features, read by a whole warp, normalised: this lane's DK / 32 values.
+template <int DK>
+__device__ __forceinline__ void unit_row(const uint16_t* src, float norm_eps, float scale, int lane, float (&x)[DK / 32]) {
+    float ss = 0.f;
+#pragma unroll
+    for (int e = 0; e < DK / 32; ++e) {
+        x[e] = bf16_bits_to_f32(src[lane + 32 * e]);
+        ss = fmaf(x[e], x[e], ss);
+    }
+    float f = scale;
+    if (norm_eps > 0.f) {
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) ss += __shfl_xor_sync(0xFFFFFFFFu, ss, o);
+        f = scale / sqrtf(ss + norm_eps);
+    }
+#pragma unroll
+    for (int e = 0; e < DK / 32; ++e) x[e] *= f;
+}
+
+// The whole tree of one head in fp32, node by node: taken when an operand left fp16's range (an infinity or a NaN in
+// the inputs, keys that are not of unit length with large writes).  Only a node's ancestors are ever read, so what is
+// not finite stays with its node and the node's descendants.  Thread = value feature.
+template <int DK, int DV, int NB>
+__device__ __noinline__ void tree_fp32(const tsv_gdn_desc& d, const uint64_t* anc, int layer, int b, int h, char* sm) {
+    using M = TreeSmem<DK, DV, NB>;
+    float* u = reinterpret_cast<float*>(sm);
+    float* kk = reinterpret_cast<float*>(sm + M::a16);   // k_i, then q_i
+    float* wk = reinterpret_cast<float*>(sm + M::p16);   // e^{G_i - G_j} (k_i . k_j), then (q_i . k_j)
+    const GdnRows& rw = *reinterpret_cast<const GdnRows*>(sm + M::rows);
+    const int T = d.T, hk = h / (d.HV / d.HK), warp = threadIdx.x >> 5, lane = threadIdx.x & 31, r = threadIdx.x;
+    const uint16_t* K = reinterpret_cast<const uint16_t*>(d.k[layer]);
+    const uint16_t* Q = reinterpret_cast<const uint16_t*>(d.q[layer]);
+    for (int i = 0; i < T; ++i) {
+        const size_t row = (size_t)b * T + i;
+        float ki[DK / 32], qi[DK / 32];
+        unit_row<DK>(K + (row * d.HK + hk) * DK, d.norm_eps, 1.f, lane, ki);
+        unit_row<DK>(Q + (row * d.HK + hk) * DK, d.norm_eps, d.scale, lane, qi);
+        __syncthreads();  // the node before is done with kk and wk
+        if (warp == 0)
+#pragma unroll
+            for (int e = 0; e < DK / 32; ++e) {
+                kk[lane + 32 * e] = ki[e];
+                kk[DK + lane + 32 * e] = qi[e];
+            }
+        int at = 0;
+        for (uint64_t a = rw.before[i] | (1ull << i); a; a &= a - 1, ++at) {
+            if ((at & 3) != warp) continue;
+            const int j = __ffsll((long long)a) - 1;
+            float kj[DK / 32], x = 0.f, y = 0.f;
+            unit_row<DK>(K + (((size_t)b * T + j) * d.HK + hk) * DK, d.norm_eps, 1.f, lane, kj);
+#pragma unroll
+            for (int e = 0; e < DK / 32; ++e) {
+                x = fmaf(ki[e], kj[e], x);
+                y = fmaf(qi[e], kj[e], y);
+            }
+#pragma unroll
+            for (int o = 16; o > 0; o >>= 1) {
+                x += __shfl_xor_sync(0xFFFFFFFFu, x, o);
+                y += __shfl_xor_sync(0xFFFFFFFFu, y, o);
+            }
+            const float w = exp2f((rw.g_hi[i] - rw.g_hi[j]) + (rw.g_lo[i] - rw.g_lo[j]));
+            if (lane == 0) {
+                wk[j] = w * x;
+                wk[64 + j] = w * y;
+            }
+        }
+        __syncthreads();
+        if (r < DV) {
+            const float* S = d.state[layer] + (((size_t)b * d.HV + h) * DV + r) * DK;
+            float sk = 0.f, sq = 0.f;
+            for (int e = 0; e < DK; ++e) {
+                sk = fmaf(S[e], kk[e], sk);
+                sq = fmaf(S[e], kk[DK + e], sq);
+            }
+            const float w = exp2f(rw.g_hi[i] + rw.g_lo[i]);
+            const size_t ov = (row * d.HV + h) * DV + r;
+            float x = bf16_bits_to_f32(reinterpret_cast<const uint16_t*>(d.v[layer])[ov]) - w * sk, y = w * sq;
+            for (uint64_t a = rw.before[i]; a; a &= a - 1) {
+                const int j = __ffsll((long long)a) - 1;
+                x = fmaf(-wk[j], u[j * DV + r], x);
+                y = fmaf(wk[64 + j], u[j * DV + r], y);
+            }
+            x *= rw.beta[i];
+            u[i * DV + r] = x;
+            reinterpret_cast<__nv_bfloat16*>(d.o[layer])[ov] = __float2bfloat16(fmaf(wk[64 + i], x, y));
+        }
+    }
+}
+
+template <int DK, int DV, int NB>
+__global__ void __launch_bounds__(kTreeThreads, 2) gdn_tree_kernel(const __grid_constant__ tsv_gdn_desc d,
+                                                                   const uint64_t* __restrict__ anc) {
+    griddep_begin();
+    using M = TreeSmem<DK, DV, NB>;
+    constexpr int MT = DV / 64;  // 16-feature tiles per warp
+    constexpr int KS = DK / 16;
+    constexpr int T16 = M::T;
+    extern __shared__ __align__(1024) char sm[];
+    GdnRows& rw = *reinterpret_cast<GdnRows*>(sm + M::rows);
+    const uint32_t s0 = tc::smem_u32(sm);
+    const int T = d.T;
+    int item = blockIdx.x;
+    const int h = item % d.HV;
+    item /= d.HV;
+    const int b = item % d.B, layer = item / d.B;
+    const int hk = h / (d.HV / d.HK);
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int g = lane >> 2, t = lane & 3;
+    const size_t row0 = (size_t)b * T;
+
+    // the state's loads: features (rows) f and f + 8 of each tile, columns 8 n + 2 t, + 1
+    const int f0 = warp * (DV / 4) + g;
+    const float* S = d.state[layer] + ((size_t)b * d.HV + h) * DV * DK + 2 * t;
+    float2 raw[MT][2][2 * KS];
+#pragma unroll
+    for (int m = 0; m < MT; ++m)
+#pragma unroll
+        for (int half = 0; half < 2; ++half)
+#pragma unroll
+            for (int n = 0; n < 2 * KS; ++n)
+                raw[m][half][n] = __ldcs(reinterpret_cast<const float2*>(S + (size_t)(f0 + m * 16 + half * 8) * DK + 8 * n));
+
+    // K, Q and V rows; rows beyond T are zero
+    {
+        constexpr int LPR = DK / 8;               // lanes per row
+        constexpr int RPP = kTreeThreads / LPR;   // rows per pass
+        const int c = threadIdx.x % LPR;
+#pragma unroll 4
+        for (int r0 = 0; r0 < 2 * T16; r0 += RPP) {
+            const int r = r0 + threadIdx.x / LPR;
+            const bool isq = r >= T16;
+            const int i = isq ? r - T16 : r;
+            const uint16_t* src = reinterpret_cast<const uint16_t*>(isq ? d.q[layer] : d.k[layer]);
+            const uint4 w = i < T ? *reinterpret_cast<const uint4*>(src + ((row0 + i) * d.HK + hk) * DK + c * 8) : make_uint4(0, 0, 0, 0);
+            uint4 x;
+            const float f = stage_chunk<DK>(w, d.norm_eps, x);
+            *reinterpret_cast<uint4*>(sm + tile_at<DK * 2>(M::kq, r, c)) = x;
+            if (c == 0) {
+                if (isq) rw.fq[i] = f * d.scale;
+                else rw.fk[i] = f;
+            }
+        }
+        constexpr int CPR = DV / 8;
+        for (int e = threadIdx.x; e < T16 * CPR; e += kTreeThreads) {
+            const int i = e / CPR, cc = e % CPR;
+            const uint4 w = i < T ? *reinterpret_cast<const uint4*>(reinterpret_cast<const uint16_t*>(d.v[layer]) + ((row0 + i) * d.HV + h) * DV + cc * 8)
+                                  : make_uint4(0, 0, 0, 0);
+            *reinterpret_cast<uint4*>(sm + tile_at<DV * 2>(M::v, i, cc)) = w;
+        }
+    }
+    // G by pointer doubling over the parents (the highest strict ancestor), two nodes per lane of warp 0
+    if (warp == 0) {
+        double G[2];
+        int p[2];
+#pragma unroll
+        for (int x = 0; x < 2; ++x) {
+            const int i = lane + 32 * x;
+            uint64_t a = 0;
+            float gi = 0.f, bi = 0.f;
+            if (i < T) {
+                a = anc[row0 + i] & ((1ull << i) - 1ull);
+                gi = d.g[layer][(row0 + i) * d.HV + h];
+                bi = d.beta[layer][(row0 + i) * d.HV + h];
+            }
+            rw.before[i] = a;
+            rw.beta[i] = bi;
+            G[x] = (double)clamp_decay(gi) * 1.4426950408889634;
+            p[x] = a ? 63 - __clzll((long long)a) : -1;
+        }
+        while (__any_sync(0xFFFFFFFFu, p[0] >= 0 || p[1] >= 0)) {  // each round halves every remaining chain
+            double add[2];
+            int np[2];
+#pragma unroll
+            for (int x = 0; x < 2; ++x) {
+                const int src = p[x] & 31;
+                const double g0 = __shfl_sync(0xFFFFFFFFu, G[0], src), g1 = __shfl_sync(0xFFFFFFFFu, G[1], src);
+                const int p0 = __shfl_sync(0xFFFFFFFFu, p[0], src), p1 = __shfl_sync(0xFFFFFFFFu, p[1], src);
+                add[x] = p[x] < 0 ? 0.0 : (p[x] >= 32 ? g1 : g0);
+                np[x] = p[x] < 0 ? -1 : (p[x] >= 32 ? p1 : p0);
+            }
+#pragma unroll
+            for (int x = 0; x < 2; ++x) {
+                G[x] += add[x];
+                p[x] = np[x];
+            }
+        }
+#pragma unroll
+        for (int x = 0; x < 2; ++x) {
+            const int i = lane + 32 * x;
+            const float hi = (float)G[x];
+            rw.g_hi[i] = hi;
+            rw.g_lo[i] = (float)(G[x] - (double)hi);
+        }
+    }
+    __syncthreads();
+    if (threadIdx.x < T16) {
+        const int i = threadIdx.x;
+        const float e = tc::ex2_approx(rw.g_hi[i] + rw.g_lo[i]);
+        rw.ck[i] = e * rw.fk[i];
+        rw.cq[i] = e * rw.fq[i];
+    }
+    uint32_t flag = 0;
+    float* diag = reinterpret_cast<float*>(sm + M::diag);
+    if (warp < NB) {  // K block w with Q block NB - 1 - w: the same number of products for every warp
+        block_products<DK, NB, 1>(false, warp, s0 + M::kq, sm + M::a16, sm + M::p16, diag + warp * 272, rw, flag, lane);
+        __syncwarp();
+        block_inverse<NB, 1>(warp, sm + M::a16, diag + warp * 272, flag, lane);
+        block_products<DK, NB, 1>(true, NB - 1 - warp, s0 + M::kq, sm + M::a16, sm + M::p16, nullptr, rw, flag, lane);
+    }
+    __syncthreads();
+
+    // this warp's features: a power-of-two scale each, from the largest of the state's row and of v
+    const int vrow = ((lane >> 4) << 3) + (lane & 7), vchunk = warp * (DV / 32) + ((lane >> 3) & 1);
+    float down[MT][2], up[MT][2];
+    uint32_t Sf[MT][KS][4];
+#pragma unroll
+    for (int m = 0; m < MT; ++m) {
+        float mx[2] = {0.f, 0.f};
+#pragma unroll
+        for (int bb = 0; bb < NB; ++bb) {
+            uint32_t w[4];
+            ldsm4_t(w, tile_at<DV * 2>(s0 + M::v, bb * 16 + vrow, vchunk + 2 * m));
+#pragma unroll
+            for (int x = 0; x < 4; ++x)
+                mx[x & 1] = fmaxf(mx[x & 1], fmaxf(fabsf(bf16_lo(w[x])), fabsf(bf16_hi(w[x]))));
+        }
+#pragma unroll
+        for (int half = 0; half < 2; ++half) {
+            float sx = 0.f;
+#pragma unroll
+            for (int n = 0; n < 2 * KS; ++n) sx = fmaxf(sx, fmaxf(fabsf(raw[m][half][n].x), fabsf(raw[m][half][n].y)));
+            sx = fmaxf(8.f * sx, mx[half]);
+            sx = fmaxf(sx, __shfl_xor_sync(0xFFFFFFFFu, sx, 1));
+            sx = fmaxf(sx, __shfl_xor_sync(0xFFFFFFFFu, sx, 2));
+            pow2_scale(sx, down[m][half], up[m][half]);
+#pragma unroll
+            for (int n = 0; n < 2 * KS; ++n) {
+                const uint32_t x = f16x2(raw[m][half][n].x * down[m][half], raw[m][half][n].y * down[m][half]);
+                Sf[m][n >> 1][(n & 1) * 2 + half] = x;
+                watch(flag, x);
+            }
+        }
+    }
+
+    const int brow = ((lane >> 4) << 3) + (lane & 7), bch = (lane >> 3) & 1;
+    uint32_t Uf[NB][MT][4];
+#pragma unroll
+    for (int bb = 0; bb < NB; ++bb) {
+        float ak[MT][2][4], aq[MT][2][4];
+#pragma unroll
+        for (int m = 0; m < MT; ++m)
+#pragma unroll
+            for (int n = 0; n < 2; ++n)
+#pragma unroll
+                for (int e = 0; e < 4; ++e) ak[m][n][e] = aq[m][n][e] = 0.f;
+#pragma unroll
+        for (int ks = 0; ks < KS; ++ks) {
+            uint32_t wk[4], wq[4];
+            ldsm4(wk, tile_at<DK * 2>(s0 + M::kq, bb * 16 + brow, 2 * ks + bch));
+            ldsm4(wq, tile_at<DK * 2>(s0 + M::kq, T16 + bb * 16 + brow, 2 * ks + bch));
+#pragma unroll
+            for (int m = 0; m < MT; ++m) {
+                mma_16816(ak[m][0], Sf[m][ks], wk[0], wk[1]);
+                mma_16816(ak[m][1], Sf[m][ks], wk[2], wk[3]);
+                mma_16816(aq[m][0], Sf[m][ks], wq[0], wq[1]);
+                mma_16816(aq[m][1], Sf[m][ks], wq[2], wq[3]);
+            }
+        }
+        // R_b, then U_b
+#pragma unroll
+        for (int m = 0; m < MT; ++m) {
+            uint32_t w[4];
+            ldsm4_t(w, tile_at<DV * 2>(s0 + M::v, bb * 16 + vrow, vchunk + 2 * m));
+#pragma unroll
+            for (int n = 0; n < 2; ++n) {
+                const int i = bb * 16 + n * 8 + 2 * t;
+                const float2 be = *reinterpret_cast<const float2*>(&rw.beta[i]), ck = *reinterpret_cast<const float2*>(&rw.ck[i]),
+                             cq = *reinterpret_cast<const float2*>(&rw.cq[i]);
+#pragma unroll
+                for (int half = 0; half < 2; ++half) {
+                    const uint32_t v2 = w[2 * n + half];
+                    ak[m][n][2 * half] = be.x * (bf16_lo(v2) * down[m][half] - ck.x * ak[m][n][2 * half]);
+                    ak[m][n][2 * half + 1] = be.y * (bf16_hi(v2) * down[m][half] - ck.y * ak[m][n][2 * half + 1]);
+                    aq[m][n][2 * half] *= cq.x;
+                    aq[m][n][2 * half + 1] *= cq.y;
+                }
+            }
+        }
+#pragma unroll
+        for (int c = 0; c < bb; ++c) {
+            uint32_t wa[4];
+            ldsm4(wa, tile_at<128>(s0 + M::a16, bb * 16 + brow, 2 * c + bch));
+#pragma unroll
+            for (int m = 0; m < MT; ++m) {
+                mma_16816(ak[m][0], Uf[c][m], wa[0], wa[1]);
+                mma_16816(ak[m][1], Uf[c][m], wa[2], wa[3]);
+            }
+        }
+        uint32_t wt[4];
+        ldsm4(wt, tile_at<128>(s0 + M::a16, bb * 16 + brow, 2 * bb + bch));
+#pragma unroll
+        for (int m = 0; m < MT; ++m) {
+            uint32_t r[4];
+#pragma unroll
+            for (int x = 0; x < 4; ++x) {
+                r[x] = f16x2(ak[m][x >> 1][2 * (x & 1)], ak[m][x >> 1][2 * (x & 1) + 1]);
+                watch(flag, r[x]);
+            }
+            float u[2][4] = {};
+            mma_16816(u[0], r, wt[0], wt[1]);
+            mma_16816(u[1], r, wt[2], wt[3]);
+#pragma unroll
+            for (int x = 0; x < 4; ++x) {
+                Uf[bb][m][x] = f16x2(u[x >> 1][2 * (x & 1)], u[x >> 1][2 * (x & 1) + 1]);
+                watch(flag, Uf[bb][m][x]);
+            }
+        }
+#pragma unroll
+        for (int c = 0; c <= bb; ++c) {
+            uint32_t wp[4];
+            ldsm4(wp, tile_at<128>(s0 + M::p16, bb * 16 + brow, 2 * c + bch));
+#pragma unroll
+            for (int m = 0; m < MT; ++m) {
+                mma_16816(aq[m][0], Uf[c][m], wp[0], wp[1]);
+                mma_16816(aq[m][1], Uf[c][m], wp[2], wp[3]);
+            }
+        }
+        // o over v's place
+#pragma unroll
+        for (int m = 0; m < MT; ++m) {
+            uint32_t w[4];
+#pragma unroll
+            for (int n = 0; n < 2; ++n)
+#pragma unroll
+                for (int half = 0; half < 2; ++half)
+                    w[2 * n + half] = bf16x2(aq[m][n][2 * half] * up[m][half], aq[m][n][2 * half + 1] * up[m][half]);
+            stsm4_t(tile_at<DV * 2>(s0 + M::v, bb * 16 + vrow, vchunk + 2 * m), w);
+        }
+    }
+    if (__syncthreads_or(watched(flag))) {
+        tree_fp32<DK, DV, NB>(d, anc, layer, b, h, sm);
+        return;
+    }
+    constexpr int CPR = DV / 8;
+    for (int e = threadIdx.x; e < T * CPR; e += kTreeThreads) {
+        const int i = e / CPR, c = e % CPR;
+        *reinterpret_cast<uint4*>(reinterpret_cast<uint16_t*>(d.o[layer]) + ((row0 + i) * d.HV + h) * DV + c * 8) =
+            *reinterpret_cast<const uint4*>(sm + tile_at<DV * 2>(M::v, i, c));
+    }
+}
+
+template <int DK, int DV, int NB>
+static void launch_tree_nb(const tsv_gdn_desc& d, const uint64_t* anc, cudaStream_t stream) {
+    constexpr int sm = TreeSmem<DK, DV, NB>::total;
+    cudaFuncSetAttribute(gdn_tree_kernel<DK, DV, NB>, cudaFuncAttributeMaxDynamicSharedMemorySize, sm);
+    launch_pdl(gdn_tree_kernel<DK, DV, NB>, (unsigned)((long long)d.n_layers * d.B * d.HV), kTreeThreads, sm, stream, d, anc);
+}
+
+template <int DK, int DV>
+static void launch_tree_dims(const tsv_gdn_desc& d, const uint64_t* anc, cudaStream_t stream) {
+    if (d.T <= 16) launch_tree_nb<DK, DV, 1>(d, anc, stream);
+    else if (d.T <= 32) launch_tree_nb<DK, DV, 2>(d, anc, stream);
+    else if (d.T <= 48) launch_tree_nb<DK, DV, 3>(d, anc, stream);
+    else launch_tree_nb<DK, DV, 4>(d, anc, stream);
+}
+
+void launch_gdn_tree(const tsv_gdn_desc& d, const uint64_t* anc, cudaStream_t stream) {
+    if (d.DK == 64 && d.DV == 64) launch_tree_dims<64, 64>(d, anc, stream);
+    else if (d.DK == 64) launch_tree_dims<64, 128>(d, anc, stream);
+    else if (d.DV == 64) launch_tree_dims<128, 64>(d, anc, stream);
+    else launch_tree_dims<128, 128>(d, anc, stream);
+}
+
+}  // namespace tsv
