@@ -82,6 +82,36 @@ __device__ __forceinline__ void pow2_scale(float m, float& down, float& up) {
     up = __uint_as_float(e << 23);
 }
 
+// 16 bytes from global to shared memory, asynchronously; zeros when !real (src is then not read).
+__device__ __forceinline__ void cp16(uint32_t dst, const void* src, bool real) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(real ? 16 : 0) : "memory");
+}
+__device__ __forceinline__ void cp_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void cp_wait() {
+    asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
+
+// A sum of log decays in units of ln 2 as an unevaluated pair: differences of far sums keep fp32 accuracy.
+struct Pair {
+    float hi, lo;
+};
+__device__ __forceinline__ Pair log2_decay(float g) {
+    const float c = clamp_decay(g);
+    Pair p;
+    p.hi = c * kLog2e;
+    p.lo = fmaf(c, kLog2e, -p.hi) + c * 1.925963033500e-8f;  // log2(e) - fp32(log2(e))
+    return p;
+}
+__device__ __forceinline__ Pair add(Pair a, Pair b) {  // two-sum, then renormalised
+    const float s = a.hi + b.hi, z = s - a.hi;
+    const float e = ((a.hi - (s - z)) + (b.hi - z)) + (a.lo + b.lo);
+    Pair p;
+    p.hi = s + e;
+    p.lo = e - (p.hi - s);
+    return p;
+}
+
 // Shared-memory tiles: rows of BYTES bytes, 16-byte chunk c of row r at chunk c ^ (r & 7), so that the 8 rows of an
 // ldmatrix fall into different banks.
 template <int BYTES>
@@ -158,18 +188,19 @@ __device__ __forceinline__ void block_products(bool q, int b, uint32_t kq, char*
         for (int half = 0; half < 2; ++half) {
             const int il = g + 8 * half, i = b * 16 + il;
             const uint64_t seen = q ? rw.before[i] | (1ull << i) : rw.before[i];
+            const uint32_t bits = (uint32_t)(seen >> (c * 16)) >> (2 * t);
             const float gh = rw.g_hi[i], gl = rw.g_lo[i];
             const float f = q ? rw.fq[i] : rw.beta[i] * rw.fk[i];
 #pragma unroll
             for (int n = 0; n < 2; ++n) {
+                const int j0 = c * 16 + n * 8 + 2 * t;
+                const float2 jh = *reinterpret_cast<const float2*>(&rw.g_hi[j0]), jl2 = *reinterpret_cast<const float2*>(&rw.g_lo[j0]),
+                             jf = *reinterpret_cast<const float2*>(&rw.fk[j0]);
                 float y[2];
+                y[0] = acc[c][n][2 * half] * jf.x * (f * tc::ex2_approx((gh - jh.x) + (gl - jl2.x)));
+                y[1] = acc[c][n][2 * half + 1] * jf.y * (f * tc::ex2_approx((gh - jh.y) + (gl - jl2.y)));
 #pragma unroll
-                for (int e = 0; e < 2; ++e) {
-                    const int j = c * 16 + n * 8 + 2 * t + e;
-                    const float w = tc::ex2_approx((gh - rw.g_hi[j]) + (gl - rw.g_lo[j]));
-                    const float x = acc[c][n][2 * half + e] * (f * rw.fk[j]) * w;
-                    y[e] = ((seen >> j) & 1ull) ? x : 0.f;
-                }
+                for (int e = 0; e < 2; ++e) y[e] = (bits & (1u << (n * 8 + e))) ? y[e] : 0.f;
                 const int jl = n * 8 + 2 * t;
                 if (q) {
                     const uint32_t h = f16x2(y[0], y[1]);

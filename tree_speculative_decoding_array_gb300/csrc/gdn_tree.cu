@@ -5,16 +5,14 @@
 // ancestors unrolls into one triangular system over the tree (gdn_tc.cuh), in which the state appears only in the
 // products S k_i and S q_i: no node's state is ever formed.
 //
-// One CTA of 4 warps per (layer, sequence, value head): a warp owns DV / 4 value features and holds their rows of S
-// as fp16 fragments.  The state's loads are issued first and land while K, Q and V are staged and the system's
-// matrices are built.
+// One CTA per (layer, sequence, value head): each warp owns 16 value features and holds their rows of S as fp16
+// fragments.  K, Q and V are fetched asynchronously, the state's loads are issued behind them and land while the rows
+// are staged and the system's matrices are built.
 #include <math.h>
 
 #include "gdn_tc.cuh"
 
 namespace tsv {
-
-constexpr int kTreeThreads = 128;
 
 template <int DK, int DV, int NB>
 struct TreeSmem {
@@ -76,7 +74,7 @@ __device__ __noinline__ void tree_fp32(const tsv_gdn_desc& d, const uint64_t* an
             }
         int at = 0;
         for (uint64_t a = rw.before[i] | (1ull << i); a; a &= a - 1, ++at) {
-            if ((at & 3) != warp) continue;
+            if (at % (DV / 16) != warp) continue;
             const int j = __ffsll((long long)a) - 1;
             float kj[DK / 32], x = 0.f, y = 0.f;
             unit_row<DK>(K + (((size_t)b * T + j) * d.HK + hk) * DK, d.norm_eps, 1.f, lane, kj);
@@ -120,11 +118,11 @@ __device__ __noinline__ void tree_fp32(const tsv_gdn_desc& d, const uint64_t* an
 }
 
 template <int DK, int DV, int NB>
-__global__ void __launch_bounds__(kTreeThreads, 2) gdn_tree_kernel(const __grid_constant__ tsv_gdn_desc d,
+__global__ void __launch_bounds__(2 * DV, 2) gdn_tree_kernel(const __grid_constant__ tsv_gdn_desc d,
                                                                    const uint64_t* __restrict__ anc) {
     griddep_begin();
     using M = TreeSmem<DK, DV, NB>;
-    constexpr int MT = DV / 64;  // 16-feature tiles per warp
+    constexpr int kThreads = 2 * DV, kWarps = DV / 16;
     constexpr int KS = DK / 16;
     constexpr int T16 = M::T;
     extern __shared__ __align__(1024) char sm[];
@@ -140,90 +138,102 @@ __global__ void __launch_bounds__(kTreeThreads, 2) gdn_tree_kernel(const __grid_
     const int g = lane >> 2, t = lane & 3;
     const size_t row0 = (size_t)b * T;
 
-    // the state's loads: features (rows) f and f + 8 of each tile, columns 8 n + 2 t, + 1
-    const int f0 = warp * (DV / 4) + g;
-    const float* S = d.state[layer] + ((size_t)b * d.HV + h) * DV * DK + 2 * t;
-    float2 raw[MT][2][2 * KS];
-#pragma unroll
-    for (int m = 0; m < MT; ++m)
-#pragma unroll
-        for (int half = 0; half < 2; ++half)
-#pragma unroll
-            for (int n = 0; n < 2 * KS; ++n)
-                raw[m][half][n] = __ldcs(reinterpret_cast<const float2*>(S + (size_t)(f0 + m * 16 + half * 8) * DK + 8 * n));
-
     // K, Q and V rows; rows beyond T are zero
-    {
-        constexpr int LPR = DK / 8;               // lanes per row
-        constexpr int RPP = kTreeThreads / LPR;   // rows per pass
-        const int c = threadIdx.x % LPR;
-#pragma unroll 4
-        for (int r0 = 0; r0 < 2 * T16; r0 += RPP) {
-            const int r = r0 + threadIdx.x / LPR;
-            const bool isq = r >= T16;
-            const int i = isq ? r - T16 : r;
-            const uint16_t* src = reinterpret_cast<const uint16_t*>(isq ? d.q[layer] : d.k[layer]);
-            const uint4 w = i < T ? *reinterpret_cast<const uint4*>(src + ((row0 + i) * d.HK + hk) * DK + c * 8) : make_uint4(0, 0, 0, 0);
-            uint4 x;
-            const float f = stage_chunk<DK>(w, d.norm_eps, x);
-            *reinterpret_cast<uint4*>(sm + tile_at<DK * 2>(M::kq, r, c)) = x;
-            if (c == 0) {
-                if (isq) rw.fq[i] = f * d.scale;
-                else rw.fk[i] = f;
-            }
-        }
-        constexpr int CPR = DV / 8;
-        for (int e = threadIdx.x; e < T16 * CPR; e += kTreeThreads) {
-            const int i = e / CPR, cc = e % CPR;
-            const uint4 w = i < T ? *reinterpret_cast<const uint4*>(reinterpret_cast<const uint16_t*>(d.v[layer]) + ((row0 + i) * d.HV + h) * DV + cc * 8)
-                                  : make_uint4(0, 0, 0, 0);
-            *reinterpret_cast<uint4*>(sm + tile_at<DV * 2>(M::v, i, cc)) = w;
-        }
+    constexpr int LPR = DK / 8;                      // lanes that share a K or Q row
+    constexpr int KQ = 2 * T16 * LPR / kThreads;     // its chunks per thread
+    static_assert(KQ * kThreads == 2 * T16 * LPR, "uneven staging");
+    const int chunk = threadIdx.x % LPR;
+#pragma unroll
+    for (int x = 0; x < KQ; ++x) {
+        const int r = threadIdx.x / LPR + x * (kThreads / LPR), i = r >= T16 ? r - T16 : r;
+        const uint16_t* src = reinterpret_cast<const uint16_t*>(r >= T16 ? d.q[layer] : d.k[layer]);
+        cp16(tile_at<DK * 2>(s0 + M::kq, r, chunk), src + ((row0 + (i < T ? i : 0)) * d.HK + hk) * DK + chunk * 8, i < T);
     }
-    // G by pointer doubling over the parents (the highest strict ancestor), two nodes per lane of warp 0
+    cp_commit();
+    constexpr int CPR = DV / 8;
+    for (int e = threadIdx.x; e < T16 * CPR; e += kThreads) {
+        const int i = e / CPR, cc = e % CPR;
+        cp16(tile_at<DV * 2>(s0 + M::v, i, cc),
+             reinterpret_cast<const uint16_t*>(d.v[layer]) + ((row0 + (i < T ? i : 0)) * d.HV + h) * DV + cc * 8, i < T);
+    }
+    cp_commit();
+    // warp 0: two nodes' gates per lane
+    uint64_t before[2] = {0, 0};
+    float gi[2] = {0.f, 0.f}, bi[2] = {0.f, 0.f};
     if (warp == 0) {
-        double G[2];
-        int p[2];
 #pragma unroll
         for (int x = 0; x < 2; ++x) {
             const int i = lane + 32 * x;
-            uint64_t a = 0;
-            float gi = 0.f, bi = 0.f;
             if (i < T) {
-                a = anc[row0 + i] & ((1ull << i) - 1ull);
-                gi = d.g[layer][(row0 + i) * d.HV + h];
-                bi = d.beta[layer][(row0 + i) * d.HV + h];
+                before[x] = anc[row0 + i] & ((1ull << i) - 1ull);
+                gi[x] = d.g[layer][(row0 + i) * d.HV + h];
+                bi[x] = d.beta[layer][(row0 + i) * d.HV + h];
             }
-            rw.before[i] = a;
-            rw.beta[i] = bi;
-            G[x] = (double)clamp_decay(gi) * 1.4426950408889634;
-            p[x] = a ? 63 - __clzll((long long)a) : -1;
+        }
+    }
+    // the state's loads: features (rows) f0 and f0 + 8, columns 8 n + 2 t, + 1
+    const int f0 = warp * 16 + g;
+    const float* S = d.state[layer] + (((size_t)b * d.HV + h) * DV + f0) * DK + 2 * t;
+    float2 raw[2][2 * KS];
+#pragma unroll
+    for (int half = 0; half < 2; ++half)
+#pragma unroll
+        for (int n = 0; n < 2 * KS; ++n) raw[half][n] = __ldcs(reinterpret_cast<const float2*>(S + half * 8 * DK + 8 * n));
+
+    if (warp == 0) {  // G by pointer doubling over the parents (the highest strict ancestor)
+        Pair G[2];
+        int p[2];
+#pragma unroll
+        for (int x = 0; x < 2; ++x) {
+            rw.before[lane + 32 * x] = before[x];
+            rw.beta[lane + 32 * x] = bi[x];
+            G[x] = log2_decay(gi[x]);
+            p[x] = before[x] ? 63 - __clzll((long long)before[x]) : -1;
         }
         while (__any_sync(0xFFFFFFFFu, p[0] >= 0 || p[1] >= 0)) {  // each round halves every remaining chain
-            double add[2];
+            Pair more[2];
             int np[2];
 #pragma unroll
             for (int x = 0; x < 2; ++x) {
                 const int src = p[x] & 31;
-                const double g0 = __shfl_sync(0xFFFFFFFFu, G[0], src), g1 = __shfl_sync(0xFFFFFFFFu, G[1], src);
-                const int p0 = __shfl_sync(0xFFFFFFFFu, p[0], src), p1 = __shfl_sync(0xFFFFFFFFu, p[1], src);
-                add[x] = p[x] < 0 ? 0.0 : (p[x] >= 32 ? g1 : g0);
-                np[x] = p[x] < 0 ? -1 : (p[x] >= 32 ? p1 : p0);
+                Pair q[2];
+                int pp[2];
+#pragma unroll
+                for (int y = 0; y < 2; ++y) {
+                    q[y].hi = __shfl_sync(0xFFFFFFFFu, G[y].hi, src);
+                    q[y].lo = __shfl_sync(0xFFFFFFFFu, G[y].lo, src);
+                    pp[y] = __shfl_sync(0xFFFFFFFFu, p[y], src);
+                }
+                more[x] = p[x] >= 32 ? q[1] : q[0];
+                np[x] = p[x] >= 32 ? pp[1] : pp[0];
             }
 #pragma unroll
-            for (int x = 0; x < 2; ++x) {
-                G[x] += add[x];
-                p[x] = np[x];
-            }
+            for (int x = 0; x < 2; ++x)
+                if (p[x] >= 0) {
+                    G[x] = add(G[x], more[x]);
+                    p[x] = np[x];
+                }
         }
 #pragma unroll
         for (int x = 0; x < 2; ++x) {
-            const int i = lane + 32 * x;
-            const float hi = (float)G[x];
-            rw.g_hi[i] = hi;
-            rw.g_lo[i] = (float)(G[x] - (double)hi);
+            rw.g_hi[lane + 32 * x] = G[x].hi;
+            rw.g_lo[lane + 32 * x] = G[x].lo;
         }
     }
+    cp_wait<1>();  // this thread's own chunks of K and Q: converted in place
+#pragma unroll
+    for (int x = 0; x < KQ; ++x) {
+        const int r = threadIdx.x / LPR + x * (kThreads / LPR);
+        char* at = sm + tile_at<DK * 2>(M::kq, r, chunk);
+        uint4 y;
+        const float f = stage_chunk<DK>(*reinterpret_cast<const uint4*>(at), d.norm_eps, y);
+        *reinterpret_cast<uint4*>(at) = y;
+        if (chunk == 0) {
+            if (r >= T16) rw.fq[r - T16] = f * d.scale;
+            else rw.fk[r] = f;
+        }
+    }
+    cp_wait<0>();
     __syncthreads();
     if (threadIdx.x < T16) {
         const int i = threadIdx.x;
@@ -233,25 +243,27 @@ __global__ void __launch_bounds__(kTreeThreads, 2) gdn_tree_kernel(const __grid_
     }
     uint32_t flag = 0;
     float* diag = reinterpret_cast<float*>(sm + M::diag);
-    if (warp < NB) {  // K block w with Q block NB - 1 - w: the same number of products for every warp
-        block_products<DK, NB, 1>(false, warp, s0 + M::kq, sm + M::a16, sm + M::p16, diag + warp * 272, rw, flag, lane);
-        __syncwarp();
-        block_inverse<NB, 1>(warp, sm + M::a16, diag + warp * 272, flag, lane);
-        block_products<DK, NB, 1>(true, NB - 1 - warp, s0 + M::kq, sm + M::a16, sm + M::p16, nullptr, rw, flag, lane);
+    for (int x = warp; x < 2 * NB; x += kWarps) {  // K blocks (each with its inverse), then Q blocks, the longest first
+        const bool q = x >= NB;
+        const int bb = q ? 2 * NB - 1 - x : NB - 1 - x;
+        block_products<DK, NB, 1>(q, bb, s0 + M::kq, sm + M::a16, sm + M::p16, diag + bb * 272, rw, flag, lane);
+        if (!q) {
+            __syncwarp();
+            block_inverse<NB, 1>(bb, sm + M::a16, diag + bb * 272, flag, lane);
+        }
     }
     __syncthreads();
 
     // this warp's features: a power-of-two scale each, from the largest of the state's row and of v
-    const int vrow = ((lane >> 4) << 3) + (lane & 7), vchunk = warp * (DV / 32) + ((lane >> 3) & 1);
-    float down[MT][2], up[MT][2];
-    uint32_t Sf[MT][KS][4];
-#pragma unroll
-    for (int m = 0; m < MT; ++m) {
+    const int vrow = ((lane >> 4) << 3) + (lane & 7), vchunk = warp * 2 + ((lane >> 3) & 1);
+    float down[2], up[2];
+    uint32_t Sf[KS][4];
+    {
         float mx[2] = {0.f, 0.f};
 #pragma unroll
         for (int bb = 0; bb < NB; ++bb) {
             uint32_t w[4];
-            ldsm4_t(w, tile_at<DV * 2>(s0 + M::v, bb * 16 + vrow, vchunk + 2 * m));
+            ldsm4_t(w, tile_at<DV * 2>(s0 + M::v, bb * 16 + vrow, vchunk));
 #pragma unroll
             for (int x = 0; x < 4; ++x)
                 mx[x & 1] = fmaxf(mx[x & 1], fmaxf(fabsf(bf16_lo(w[x])), fabsf(bf16_hi(w[x]))));
@@ -260,121 +272,94 @@ __global__ void __launch_bounds__(kTreeThreads, 2) gdn_tree_kernel(const __grid_
         for (int half = 0; half < 2; ++half) {
             float sx = 0.f;
 #pragma unroll
-            for (int n = 0; n < 2 * KS; ++n) sx = fmaxf(sx, fmaxf(fabsf(raw[m][half][n].x), fabsf(raw[m][half][n].y)));
+            for (int n = 0; n < 2 * KS; ++n) sx = fmaxf(sx, fmaxf(fabsf(raw[half][n].x), fabsf(raw[half][n].y)));
             sx = fmaxf(8.f * sx, mx[half]);
             sx = fmaxf(sx, __shfl_xor_sync(0xFFFFFFFFu, sx, 1));
             sx = fmaxf(sx, __shfl_xor_sync(0xFFFFFFFFu, sx, 2));
-            pow2_scale(sx, down[m][half], up[m][half]);
+            pow2_scale(sx, down[half], up[half]);
 #pragma unroll
             for (int n = 0; n < 2 * KS; ++n) {
-                const uint32_t x = f16x2(raw[m][half][n].x * down[m][half], raw[m][half][n].y * down[m][half]);
-                Sf[m][n >> 1][(n & 1) * 2 + half] = x;
+                const uint32_t x = f16x2(raw[half][n].x * down[half], raw[half][n].y * down[half]);
+                Sf[n >> 1][(n & 1) * 2 + half] = x;
                 watch(flag, x);
             }
         }
     }
 
     const int brow = ((lane >> 4) << 3) + (lane & 7), bch = (lane >> 3) & 1;
-    uint32_t Uf[NB][MT][4];
+    uint32_t Uf[NB][4];
 #pragma unroll
     for (int bb = 0; bb < NB; ++bb) {
-        float ak[MT][2][4], aq[MT][2][4];
-#pragma unroll
-        for (int m = 0; m < MT; ++m)
-#pragma unroll
-            for (int n = 0; n < 2; ++n)
-#pragma unroll
-                for (int e = 0; e < 4; ++e) ak[m][n][e] = aq[m][n][e] = 0.f;
+        float ak[2][4] = {}, aq[2][4] = {};
 #pragma unroll
         for (int ks = 0; ks < KS; ++ks) {
             uint32_t wk[4], wq[4];
             ldsm4(wk, tile_at<DK * 2>(s0 + M::kq, bb * 16 + brow, 2 * ks + bch));
             ldsm4(wq, tile_at<DK * 2>(s0 + M::kq, T16 + bb * 16 + brow, 2 * ks + bch));
-#pragma unroll
-            for (int m = 0; m < MT; ++m) {
-                mma_16816(ak[m][0], Sf[m][ks], wk[0], wk[1]);
-                mma_16816(ak[m][1], Sf[m][ks], wk[2], wk[3]);
-                mma_16816(aq[m][0], Sf[m][ks], wq[0], wq[1]);
-                mma_16816(aq[m][1], Sf[m][ks], wq[2], wq[3]);
-            }
+            mma_16816(ak[0], Sf[ks], wk[0], wk[1]);
+            mma_16816(ak[1], Sf[ks], wk[2], wk[3]);
+            mma_16816(aq[0], Sf[ks], wq[0], wq[1]);
+            mma_16816(aq[1], Sf[ks], wq[2], wq[3]);
         }
         // R_b, then U_b
+        uint32_t w[4];
+        ldsm4_t(w, tile_at<DV * 2>(s0 + M::v, bb * 16 + vrow, vchunk));
 #pragma unroll
-        for (int m = 0; m < MT; ++m) {
-            uint32_t w[4];
-            ldsm4_t(w, tile_at<DV * 2>(s0 + M::v, bb * 16 + vrow, vchunk + 2 * m));
+        for (int n = 0; n < 2; ++n) {
+            const int i = bb * 16 + n * 8 + 2 * t;
+            const float2 be = *reinterpret_cast<const float2*>(&rw.beta[i]), ck = *reinterpret_cast<const float2*>(&rw.ck[i]),
+                         cq = *reinterpret_cast<const float2*>(&rw.cq[i]);
 #pragma unroll
-            for (int n = 0; n < 2; ++n) {
-                const int i = bb * 16 + n * 8 + 2 * t;
-                const float2 be = *reinterpret_cast<const float2*>(&rw.beta[i]), ck = *reinterpret_cast<const float2*>(&rw.ck[i]),
-                             cq = *reinterpret_cast<const float2*>(&rw.cq[i]);
-#pragma unroll
-                for (int half = 0; half < 2; ++half) {
-                    const uint32_t v2 = w[2 * n + half];
-                    ak[m][n][2 * half] = be.x * (bf16_lo(v2) * down[m][half] - ck.x * ak[m][n][2 * half]);
-                    ak[m][n][2 * half + 1] = be.y * (bf16_hi(v2) * down[m][half] - ck.y * ak[m][n][2 * half + 1]);
-                    aq[m][n][2 * half] *= cq.x;
-                    aq[m][n][2 * half + 1] *= cq.y;
-                }
+            for (int half = 0; half < 2; ++half) {
+                const uint32_t v2 = w[2 * n + half];
+                ak[n][2 * half] = be.x * (bf16_lo(v2) * down[half] - ck.x * ak[n][2 * half]);
+                ak[n][2 * half + 1] = be.y * (bf16_hi(v2) * down[half] - ck.y * ak[n][2 * half + 1]);
+                aq[n][2 * half] *= cq.x;
+                aq[n][2 * half + 1] *= cq.y;
             }
         }
 #pragma unroll
         for (int c = 0; c < bb; ++c) {
             uint32_t wa[4];
             ldsm4(wa, tile_at<128>(s0 + M::a16, bb * 16 + brow, 2 * c + bch));
-#pragma unroll
-            for (int m = 0; m < MT; ++m) {
-                mma_16816(ak[m][0], Uf[c][m], wa[0], wa[1]);
-                mma_16816(ak[m][1], Uf[c][m], wa[2], wa[3]);
-            }
+            mma_16816(ak[0], Uf[c], wa[0], wa[1]);
+            mma_16816(ak[1], Uf[c], wa[2], wa[3]);
         }
-        uint32_t wt[4];
+        uint32_t wt[4], r[4];
         ldsm4(wt, tile_at<128>(s0 + M::a16, bb * 16 + brow, 2 * bb + bch));
 #pragma unroll
-        for (int m = 0; m < MT; ++m) {
-            uint32_t r[4];
+        for (int x = 0; x < 4; ++x) {
+            r[x] = f16x2(ak[x >> 1][2 * (x & 1)], ak[x >> 1][2 * (x & 1) + 1]);
+            watch(flag, r[x]);
+        }
+        float u[2][4] = {};
+        mma_16816(u[0], r, wt[0], wt[1]);
+        mma_16816(u[1], r, wt[2], wt[3]);
 #pragma unroll
-            for (int x = 0; x < 4; ++x) {
-                r[x] = f16x2(ak[m][x >> 1][2 * (x & 1)], ak[m][x >> 1][2 * (x & 1) + 1]);
-                watch(flag, r[x]);
-            }
-            float u[2][4] = {};
-            mma_16816(u[0], r, wt[0], wt[1]);
-            mma_16816(u[1], r, wt[2], wt[3]);
-#pragma unroll
-            for (int x = 0; x < 4; ++x) {
-                Uf[bb][m][x] = f16x2(u[x >> 1][2 * (x & 1)], u[x >> 1][2 * (x & 1) + 1]);
-                watch(flag, Uf[bb][m][x]);
-            }
+        for (int x = 0; x < 4; ++x) {
+            Uf[bb][x] = f16x2(u[x >> 1][2 * (x & 1)], u[x >> 1][2 * (x & 1) + 1]);
+            watch(flag, Uf[bb][x]);
         }
 #pragma unroll
         for (int c = 0; c <= bb; ++c) {
             uint32_t wp[4];
             ldsm4(wp, tile_at<128>(s0 + M::p16, bb * 16 + brow, 2 * c + bch));
-#pragma unroll
-            for (int m = 0; m < MT; ++m) {
-                mma_16816(aq[m][0], Uf[c][m], wp[0], wp[1]);
-                mma_16816(aq[m][1], Uf[c][m], wp[2], wp[3]);
-            }
+            mma_16816(aq[0], Uf[c], wp[0], wp[1]);
+            mma_16816(aq[1], Uf[c], wp[2], wp[3]);
         }
         // o over v's place
 #pragma unroll
-        for (int m = 0; m < MT; ++m) {
-            uint32_t w[4];
+        for (int n = 0; n < 2; ++n)
 #pragma unroll
-            for (int n = 0; n < 2; ++n)
-#pragma unroll
-                for (int half = 0; half < 2; ++half)
-                    w[2 * n + half] = bf16x2(aq[m][n][2 * half] * up[m][half], aq[m][n][2 * half + 1] * up[m][half]);
-            stsm4_t(tile_at<DV * 2>(s0 + M::v, bb * 16 + vrow, vchunk + 2 * m), w);
-        }
+            for (int half = 0; half < 2; ++half)
+                w[2 * n + half] = bf16x2(aq[n][2 * half] * up[half], aq[n][2 * half + 1] * up[half]);
+        stsm4_t(tile_at<DV * 2>(s0 + M::v, bb * 16 + vrow, vchunk), w);
     }
     if (__syncthreads_or(watched(flag))) {
         tree_fp32<DK, DV, NB>(d, anc, layer, b, h, sm);
         return;
     }
-    constexpr int CPR = DV / 8;
-    for (int e = threadIdx.x; e < T * CPR; e += kTreeThreads) {
+    for (int e = threadIdx.x; e < T * CPR; e += kThreads) {
         const int i = e / CPR, c = e % CPR;
         *reinterpret_cast<uint4*>(reinterpret_cast<uint16_t*>(d.o[layer]) + ((row0 + i) * d.HV + h) * DV + c * 8) =
             *reinterpret_cast<const uint4*>(sm + tile_at<DV * 2>(M::v, i, c));
@@ -385,7 +370,7 @@ template <int DK, int DV, int NB>
 static void launch_tree_nb(const tsv_gdn_desc& d, const uint64_t* anc, cudaStream_t stream) {
     constexpr int sm = TreeSmem<DK, DV, NB>::total;
     cudaFuncSetAttribute(gdn_tree_kernel<DK, DV, NB>, cudaFuncAttributeMaxDynamicSharedMemorySize, sm);
-    launch_pdl(gdn_tree_kernel<DK, DV, NB>, (unsigned)((long long)d.n_layers * d.B * d.HV), kTreeThreads, sm, stream, d, anc);
+    launch_pdl(gdn_tree_kernel<DK, DV, NB>, (unsigned)((long long)d.n_layers * d.B * d.HV), 2 * DV, sm, stream, d, anc);
 }
 
 template <int DK, int DV>
