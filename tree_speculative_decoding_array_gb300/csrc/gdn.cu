@@ -196,7 +196,7 @@ __global__ void __launch_bounds__(kGdnThreads) gdn_recur_kernel(const __grid_con
 }
 
 // Defined in gdn_tree.cu.
-void launch_gdn_tree(const tsv_gdn_desc& d, const uint64_t* anc, cudaStream_t stream);
+void launch_gdn_tree(const tsv_gdn_desc& d, const uint64_t* anc, int32_t* status, cudaStream_t stream);
 
 enum GdnCall { kGdnVerify, kGdnCommit, kGdnScan };
 
@@ -244,13 +244,12 @@ static tsv_gdn_desc with_scale(const tsv_gdn_desc* d) {
 extern "C" tsv_status tsv_gdn_tree_verify(const tsv_gdn_desc* d, const uint64_t* anc, int32_t* dev_status,
                                           cudaStream_t stream) {
     using namespace tsv;
-    (void)dev_status;
     clear_error();
     tsv_status st = check_gdn(d, kGdnVerify, "gdn_tree_verify");
     if (st != TSV_OK || d->B == 0) return st;
     if (!anc) return fail(TSV_EINVAL, "gdn_tree_verify: anc must be non-null");
     const tsv_gdn_desc x = with_scale(d);
-    launch_gdn_tree(x, anc, stream);
+    launch_gdn_tree(x, anc, dev_status, stream);
     return check_launch("gdn_tree_verify");
 }
 

@@ -6,14 +6,16 @@
 //     u_i = beta_i (v_i - e^{G_i} S k_i - sum_{j before i} e^{G_i - G_j} (k_i . k_j) u_j)
 //     o_i = e^{G_i} S q_i + sum_{j before i, or i} e^{G_i - G_j} (q_i . k_j) u_j
 // ("before": strict ancestor, or earlier token).  Every value feature (row of S, column of u and o) is a system of
-// its own with the same matrices, so a warp owns 16 features per tile and keeps S, u and o of them in registers as
-// mma fragments; only the matrices, K, Q and V pass through shared memory.  The rows are taken 16 at a time: R_b from
-// S and the blocks before, U_b = (I + A_bb)^-1 R_b with that 16 x 16 inverse, then O_b.
+// its own with the same matrices.  The large products run on the 5th-generation tensor cores: [K; Q] K^T (rows in the
+// TMEM lanes) and S [K; Q]^T (value features in the lanes, S as fp16 pairs in TMEM).  Both are read back from TMEM in
+// the layout of mma.sync fragments, in which a warp owns 16 value features and solves their systems in registers, 16
+// rows of the block at a time: R_b from S and the blocks before, U_b = (I + A_bb)^-1 R_b with that 16 x 16 inverse,
+// then O_b.  Only the matrices, K, Q and V pass through shared memory.
 //
 // Operands are fp16 with power-of-two scales, which cost nothing in accuracy: K and Q rows hold bf16 values (8 bits,
-// exact in fp16 once the row's largest value is scaled to [1, 2); what falls below 2^-24 of it is lost), S, R and U
-// of one value feature share a scale (their equations are linear in them).  An fp16 operand is within 2^-12 of its
-// value; an hi + lo pair within 2^-22 (or 2^-25 of the feature's largest value).  Accumulation is fp32.
+// exact in fp16 once the row's norm is scaled to about 1; what falls below 2^-24 of it is lost), S, R and U of one
+// value feature share a scale (their equations are linear in them).  An fp16 operand is within 2^-12 of its value; an
+// hi + lo pair within 2^-22 (or 2^-25 of the feature's largest value).  Accumulation is fp32.
 #pragma once
 
 #include "common.cuh"
@@ -73,6 +75,22 @@ __device__ __forceinline__ bool watched(uint32_t flag) {
     const float2 f = f16x2_to_f32x2(flag);
     return !(f.x == 0.f && f.y == 0.f);
 }
+// Two fp32 products or sums per instruction.
+__device__ __forceinline__ float2 mul2(float2 a, float2 b) {
+    float2 c;
+    asm("{\n .reg .b64 x, y, z;\n mov.b64 x, {%2, %3};\n mov.b64 y, {%4, %5};\n mul.rn.f32x2 z, x, y;\n mov.b64 {%0, %1}, z;\n}"
+        : "=f"(c.x), "=f"(c.y)
+        : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
+    return c;
+}
+__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 d) {
+    float2 c;
+    asm("{\n .reg .b64 x, y, z;\n mov.b64 x, {%2, %3};\n mov.b64 y, {%4, %5};\n mov.b64 z, {%6, %7};\n fma.rn.f32x2 z, x, y, z;\n"
+        " mov.b64 {%0, %1}, z;\n}"
+        : "=f"(c.x), "=f"(c.y)
+        : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y), "f"(d.x), "f"(d.y));
+    return c;
+}
 // 2^-e and 2^e for m in [2^e, 2^(e+1)); 1 for 0, infinities and NaN.
 __device__ __forceinline__ void pow2_scale(float m, float& down, float& up) {
     uint32_t e = (__float_as_uint(m) >> 23) & 255u;
@@ -128,87 +146,77 @@ struct GdnRows {
     uint64_t before[64];       // rows ahead of i in its system (strict ancestors, or earlier tokens)
 };
 
-// One bf16 row chunk of 8 values -> fp16 scaled by the row's power of two; DK / 8 consecutive lanes share a row.
-// Returns the factor that products with the staged row need.
+// One chunk of 8 bf16 values of a K or Q row -> fp16, scaled by a power of two that brings the row's norm to [1, 2);
+// DK / 8 consecutive lanes share a row.  ss: the row's sum of squares; up: what the scaling divided by.
 template <int DK>
-__device__ __forceinline__ float stage_chunk(uint4 w, float norm_eps, uint4& out) {
-    float x[8] = {bf16_lo(w.x), bf16_hi(w.x), bf16_lo(w.y), bf16_hi(w.y), bf16_lo(w.z), bf16_hi(w.z), bf16_lo(w.w), bf16_hi(w.w)};
-    float ss = 0.f, mx = 0.f;
+__device__ __forceinline__ uint4 stage_chunk(uint4 w, float& ss, float& up, uint32_t& flag) {
+    float2 x[4] = {{bf16_lo(w.x), bf16_hi(w.x)}, {bf16_lo(w.y), bf16_hi(w.y)}, {bf16_lo(w.z), bf16_hi(w.z)}, {bf16_lo(w.w), bf16_hi(w.w)}};
+    float2 s2 = mul2(x[0], x[0]);
 #pragma unroll
-    for (int e = 0; e < 8; ++e) {
-        ss = fmaf(x[e], x[e], ss);
-        mx = fmaxf(mx, fabsf(x[e]));
-    }
+    for (int e = 1; e < 4; ++e) s2 = fma2(x[e], x[e], s2);
+    ss = s2.x + s2.y;
 #pragma unroll
-    for (int o = DK / 16; o > 0; o >>= 1) {
-        ss += __shfl_xor_sync(0xFFFFFFFFu, ss, o);
-        mx = fmaxf(mx, __shfl_xor_sync(0xFFFFFFFFu, mx, o));
-    }
-    float down, up;
-    pow2_scale(mx, down, up);
-    out = make_uint4(f16x2(x[0] * down, x[1] * down), f16x2(x[2] * down, x[3] * down), f16x2(x[4] * down, x[5] * down),
-                     f16x2(x[6] * down, x[7] * down));
-    return norm_eps > 0.f ? up / sqrtf(ss + norm_eps) : up;
+    for (int o = DK / 16; o > 0; o >>= 1) ss += __shfl_xor_sync(0xFFFFFFFFu, ss, o);
+    const int es = (int)(__float_as_uint(ss) >> 23) & 255;
+    const int e = es == 0 || es == 255 ? 0 : (es - 127) >> 1;
+    const float down = __uint_as_float((uint32_t)(127 - e) << 23);
+    up = __uint_as_float((uint32_t)(127 + e) << 23);
+    // squares that underflowed: the fp32 path
+    if (ss < 1e-30f && ((w.x | w.y | w.z | w.w) & 0x7FFF7FFFu)) flag = 0x7FFF7FFFu;
+    const float2 d2 = make_float2(down, down);
+#pragma unroll
+    for (int k = 0; k < 4; ++k) x[k] = mul2(x[k], d2);
+    return make_uint4(f16x2(x[0].x, x[0].y), f16x2(x[1].x, x[1].y), f16x2(x[2].x, x[2].y), f16x2(x[3].x, x[3].y));
 }
 
-// Products of one 16-row block with the K rows of its own and the blocks before, decayed and masked:
+// K and Q as operand tiles: DK / 64 blocks of [ROWS][128 B], 128-byte swizzled; chunk 0 .. DK / 8 - 1 of a row.
+template <int ROWS>
+__device__ __forceinline__ uint32_t kq_at(uint32_t base, int row, int chunk) {
+    return base + (uint32_t)((chunk >> 3) * ROWS * 128 + row * 128 + (((chunk & 7) ^ (row & 7)) << 4));
+}
+
+// One 16-row block's products with the K rows of its own and the blocks before (TMEM columns c * 16 of `taddr`, the
+// block's rows in its lanes), decayed and masked:
 //   q == false: rows K_b; -A (fp16 pieces) for the blocks before, A itself (fp32) for the block's own
 //   q == true:  rows Q_b; P (fp16)
-// kq: K rows [T] then Q rows [T]; a16 / p16: [T rows][128 B] tiles; diag: this block's [16][17] fp32.
-template <int DK, int NB, int PIECES>
-__device__ __forceinline__ void block_products(bool q, int b, uint32_t kq, char* a16, char* p16, float* diag,
+// a16 / p16: [T rows][128 B] tiles; diag: this block's [16][kDiag] fp32.
+constexpr int kDiag = 20;  // fp32 row stride of a diagonal block: 16-byte aligned, rows in different banks
+template <int NB, int PIECES>
+__device__ __forceinline__ void block_matrices(bool q, int b, uint32_t taddr, char* a16, char* p16, float* diag,
                                                const GdnRows& rw, uint32_t& flag, int lane) {
-    constexpr int KB = DK * 2;  // bytes per row
     constexpr int T = 16 * NB;
-    float acc[NB][2][4];
+    float acc[NB][8];
 #pragma unroll
     for (int c = 0; c < NB; ++c)
+        if (c <= b) tc::tmem_ld_frag2(taddr + c * 16, acc[c]);
+    tc::tmem_wait_ld();
+    const int g = lane >> 2, t = lane & 3;
 #pragma unroll
-        for (int n = 0; n < 2; ++n) acc[c][n][0] = acc[c][n][1] = acc[c][n][2] = acc[c][n][3] = 0.f;
-    const int arow = (q ? T : 0) + b * 16 + (lane & 15);
-    const int brow = ((lane >> 4) << 3) + (lane & 7);
-#pragma unroll
-    for (int ks = 0; ks < DK / 16; ++ks) {
-        uint32_t a[4];
-        ldsm4(a, tile_at<KB>(kq, arow, 2 * ks + (lane >> 4)));
+    for (int half = 0; half < 2; ++half) {
+        const int il = g + 8 * half, i = b * 16 + il;
+        const uint64_t seen = (q ? rw.before[i] | (1ull << i) : rw.before[i]) >> (2 * t);
+        const float gh = rw.g_hi[i], gl = rw.g_lo[i];
+        const float f = q ? rw.fq[i] : rw.beta[i] * rw.fk[i];
 #pragma unroll
         for (int c = 0; c < NB; ++c) {
             if (c > b) break;
-            uint32_t w[4];
-            ldsm4(w, tile_at<KB>(kq, c * 16 + brow, 2 * ks + ((lane >> 3) & 1)));
-            mma_16816(acc[c][0], a, w[0], w[1]);
-            mma_16816(acc[c][1], a, w[2], w[3]);
-        }
-    }
-    const int g = lane >> 2, t = lane & 3;
-#pragma unroll
-    for (int c = 0; c < NB; ++c) {
-        if (c > b) break;
-#pragma unroll
-        for (int half = 0; half < 2; ++half) {
-            const int il = g + 8 * half, i = b * 16 + il;
-            const uint64_t seen = q ? rw.before[i] | (1ull << i) : rw.before[i];
-            const uint32_t bits = (uint32_t)(seen >> (c * 16)) >> (2 * t);
-            const float gh = rw.g_hi[i], gl = rw.g_lo[i];
-            const float f = q ? rw.fq[i] : rw.beta[i] * rw.fk[i];
+            const uint32_t bits = (uint32_t)(seen >> (c * 16));
 #pragma unroll
             for (int n = 0; n < 2; ++n) {
                 const int j0 = c * 16 + n * 8 + 2 * t;
                 const float2 jh = *reinterpret_cast<const float2*>(&rw.g_hi[j0]), jl2 = *reinterpret_cast<const float2*>(&rw.g_lo[j0]),
                              jf = *reinterpret_cast<const float2*>(&rw.fk[j0]);
                 float y[2];
-                y[0] = acc[c][n][2 * half] * jf.x * (f * tc::ex2_approx((gh - jh.x) + (gl - jl2.x)));
-                y[1] = acc[c][n][2 * half + 1] * jf.y * (f * tc::ex2_approx((gh - jh.y) + (gl - jl2.y)));
+                y[0] = acc[c][4 * n + 2 * half] * jf.x * (f * tc::ex2_approx((gh - jh.x) + (gl - jl2.x)));
+                y[1] = acc[c][4 * n + 2 * half + 1] * jf.y * (f * tc::ex2_approx((gh - jh.y) + (gl - jl2.y)));
 #pragma unroll
                 for (int e = 0; e < 2; ++e) y[e] = (bits & (1u << (n * 8 + e))) ? y[e] : 0.f;
-                const int jl = n * 8 + 2 * t;
                 if (q) {
                     const uint32_t h = f16x2(y[0], y[1]);
                     watch(flag, h);
                     *reinterpret_cast<uint32_t*>(p16 + tile_at<128>(0, i, 2 * c + n) + 4 * t) = h;
                 } else if (c == b) {
-                    diag[il * 17 + jl] = y[0];
-                    diag[il * 17 + jl + 1] = y[1];
+                    *reinterpret_cast<float2*>(diag + il * kDiag + n * 8 + 2 * t) = make_float2(y[0], y[1]);
                 } else {
                     uint32_t hi, lo;
                     split2(-y[0], -y[1], hi, lo);
@@ -230,21 +238,30 @@ __device__ __forceinline__ void block_inverse(int b, char* a16, const float* dia
     float x[16];
 #pragma unroll
     for (int i = 0; i < 16; ++i) {
-        float s = i == c ? 1.f : 0.f;
+        float s0 = i == c ? 1.f : 0.f, s1 = 0.f;
 #pragma unroll
-        for (int j = 0; j < i; ++j) s = fmaf(-diag[i * 17 + j], x[j], s);
-        x[i] = s;
+        for (int j = 0; j < i; j += 4) {
+            const float4 a = *reinterpret_cast<const float4*>(diag + i * kDiag + j);
+            s0 = fmaf(-a.x, x[j], s0);
+            if (j + 1 < i) s1 = fmaf(-a.y, x[j + 1], s1);
+            if (j + 2 < i) s0 = fmaf(-a.z, x[j + 2], s0);
+            if (j + 3 < i) s1 = fmaf(-a.w, x[j + 3], s1);
+        }
+        x[i] = s0 + s1;
     }
     if (lane < 16) {
 #pragma unroll
-        for (int i = 0; i < 16; ++i) {
-            const int row = b * 16 + i, col = b * 16 + c;
+        for (int i = 0; i < 16; i += 2) {
             uint32_t hi, lo;
-            split2(x[i], 0.f, hi, lo);
+            split2(x[i], x[i + 1], hi, lo);
             watch(flag, hi);
-            char* at = a16 + tile_at<128>(0, row, col >> 3) + 2 * (col & 7);
-            *reinterpret_cast<uint16_t*>(at) = (uint16_t)hi;
-            if (PIECES == 2) *reinterpret_cast<uint16_t*>(at + T * 128) = (uint16_t)lo;
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+                const int row = b * 16 + i + e, col = b * 16 + c;
+                char* at = a16 + tile_at<128>(0, row, col >> 3) + 2 * (col & 7);
+                *reinterpret_cast<uint16_t*>(at) = (uint16_t)(hi >> (16 * e));
+                if (PIECES == 2) *reinterpret_cast<uint16_t*>(at + T * 128) = (uint16_t)(lo >> (16 * e));
+            }
         }
     }
 }

@@ -5,9 +5,9 @@
 // ancestors unrolls into one triangular system over the tree (gdn_tc.cuh), in which the state appears only in the
 // products S k_i and S q_i: no node's state is ever formed.
 //
-// One CTA per (layer, sequence, value head): each warp owns 16 value features and holds their rows of S as fp16
-// fragments.  K, Q and V are fetched asynchronously, the state's loads are issued behind them and land while the rows
-// are staged and the system's matrices are built.
+// One CTA per (layer, sequence, value head): each warp owns 16 value features and takes their rows of S from global
+// memory to fp16 pairs in TMEM.  K, Q and V are fetched asynchronously, the state's loads are issued behind them and
+// land while the rows are staged; the matrices are built while the tensor cores work on S [K; Q]^T.
 #include <math.h>
 
 #include "gdn_tc.cuh"
@@ -21,9 +21,15 @@ struct TreeSmem {
     static constexpr int v = kq + 2 * T * DK * 2;      // V rows [T], DV bf16 each; o over them
     static constexpr int a16 = v + T * DV * 2;         // [T][64] fp16: -A below the diagonal blocks, inverses on them
     static constexpr int p16 = a16 + T * 128;          // [T][64] fp16: P
-    static constexpr int diag = p16 + T * 128;         // [NB][16][17] fp32: A of the diagonal blocks
-    static constexpr int rows = (diag + NB * 16 * 17 * 4 + 15) / 16 * 16;
-    static constexpr int total = rows + (int)sizeof(GdnRows);
+    static constexpr int diag = p16 + T * 128;         // [NB][16][kDiag] fp32: A of the diagonal blocks
+    static constexpr int rows = diag + NB * 16 * kDiag * 4;
+    static constexpr int bars = rows + (int)sizeof(GdnRows);  // two barriers, TMEM address, abort flag
+    // [K; Q] K^T takes 128 rows of the K and Q tile, whatever lies behind them
+    static constexpr int reach = (DK / 64 - 1) * 2 * T * 128 + 128 * 128;
+    static constexpr int total = bars + 32 > reach ? bars + 32 : reach;
+    // TMEM columns: S as fp16 pairs, S [K; Q]^T, [K; Q] K^T
+    static constexpr int col_s = 0, col_d = DK / 2, col_g = col_d + 2 * T, cols_used = col_g + T;
+    static constexpr int cols = cols_used <= 64 ? 64 : cols_used <= 128 ? 128 : 256;
     // the fp32 path: u [T][DV] over kq and v, one node's k and q over a16, its ancestors' products over p16
     static_assert(T * DV * 4 <= a16 && 2 * DK * 4 <= T * 128 && 2 * 64 * 4 <= T * 128, "fp32 path does not fit");
 };
@@ -119,7 +125,7 @@ __device__ __noinline__ void tree_fp32(const tsv_gdn_desc& d, const uint64_t* an
 
 template <int DK, int DV, int NB>
 __global__ void __launch_bounds__(2 * DV, 2) gdn_tree_kernel(const __grid_constant__ tsv_gdn_desc d,
-                                                                   const uint64_t* __restrict__ anc) {
+                                                             const uint64_t* __restrict__ anc, int32_t* status) {
     griddep_begin();
     using M = TreeSmem<DK, DV, NB>;
     constexpr int kThreads = 2 * DV, kWarps = DV / 16;
@@ -137,6 +143,22 @@ __global__ void __launch_bounds__(2 * DV, 2) gdn_tree_kernel(const __grid_consta
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int g = lane >> 2, t = lane & 3;
     const size_t row0 = (size_t)b * T;
+    // this warp's TMEM lanes and value features (16 of each); 64 features leave the upper half of each quarter unused
+    const int lane0 = (warp & 3) * 32 + (warp >> 2) * 16, fb = DV == 128 ? lane0 : warp * 16;
+
+    uint64_t* bars = reinterpret_cast<uint64_t*>(sm + M::bars);  // [K; Q] K^T done, S [K; Q]^T done
+    uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + 2);
+    volatile int* abort_flag = reinterpret_cast<volatile int*>(bars + 3);
+    if (threadIdx.x == 0) {
+        tc::mbar_init(&bars[0], 1);
+        tc::mbar_init(&bars[1], 1);
+        *abort_flag = 0;
+        tc::fence_mbar_init();
+    }
+    if (warp == 1) {
+        tc::tmem_alloc(tmem_slot, M::cols);
+        tc::tmem_relinquish();
+    }
 
     // K, Q and V rows; rows beyond T are zero
     constexpr int LPR = DK / 8;                      // lanes that share a K or Q row
@@ -147,7 +169,7 @@ __global__ void __launch_bounds__(2 * DV, 2) gdn_tree_kernel(const __grid_consta
     for (int x = 0; x < KQ; ++x) {
         const int r = threadIdx.x / LPR + x * (kThreads / LPR), i = r >= T16 ? r - T16 : r;
         const uint16_t* src = reinterpret_cast<const uint16_t*>(r >= T16 ? d.q[layer] : d.k[layer]);
-        cp16(tile_at<DK * 2>(s0 + M::kq, r, chunk), src + ((row0 + (i < T ? i : 0)) * d.HK + hk) * DK + chunk * 8, i < T);
+        cp16(kq_at<2 * T16>(s0 + M::kq, r, chunk), src + ((row0 + (i < T ? i : 0)) * d.HK + hk) * DK + chunk * 8, i < T);
     }
     cp_commit();
     constexpr int CPR = DV / 8;
@@ -172,7 +194,7 @@ __global__ void __launch_bounds__(2 * DV, 2) gdn_tree_kernel(const __grid_consta
         }
     }
     // the state's loads: features (rows) f0 and f0 + 8, columns 8 n + 2 t, + 1
-    const int f0 = warp * 16 + g;
+    const int f0 = fb + g;
     const float* S = d.state[layer] + (((size_t)b * d.HV + h) * DV + f0) * DK + 2 * t;
     float2 raw[2][2 * KS];
 #pragma unroll
@@ -220,44 +242,50 @@ __global__ void __launch_bounds__(2 * DV, 2) gdn_tree_kernel(const __grid_consta
             rw.g_lo[lane + 32 * x] = G[x].lo;
         }
     }
+    uint32_t flag = 0;
     cp_wait<1>();  // this thread's own chunks of K and Q: converted in place
 #pragma unroll
     for (int x = 0; x < KQ; ++x) {
         const int r = threadIdx.x / LPR + x * (kThreads / LPR);
-        char* at = sm + tile_at<DK * 2>(M::kq, r, chunk);
-        uint4 y;
-        const float f = stage_chunk<DK>(*reinterpret_cast<const uint4*>(at), d.norm_eps, y);
-        *reinterpret_cast<uint4*>(at) = y;
-        if (chunk == 0) {
-            if (r >= T16) rw.fq[r - T16] = f * d.scale;
-            else rw.fk[r] = f;
+        char* at = sm + kq_at<2 * T16>(M::kq, r, chunk);
+        float ss, upr;
+        *reinterpret_cast<uint4*>(at) = stage_chunk<DK>(*reinterpret_cast<const uint4*>(at), ss, upr, flag);
+        if (chunk == 0) {  // the row's factor is finished below
+            const int i = r >= T16 ? r - T16 : r;
+            (r >= T16 ? rw.fq : rw.fk)[i] = upr;
+            (r >= T16 ? rw.cq : rw.ck)[i] = ss;
         }
     }
     cp_wait<0>();
+    tc::fence_proxy_async_smem();
+    tc::tc_fence_before();
     __syncthreads();
-    if (threadIdx.x < T16) {
-        const int i = threadIdx.x;
-        const float e = tc::ex2_approx(rw.g_hi[i] + rw.g_lo[i]);
-        rw.ck[i] = e * rw.fk[i];
-        rw.cq[i] = e * rw.fq[i];
-    }
-    uint32_t flag = 0;
-    float* diag = reinterpret_cast<float*>(sm + M::diag);
-    for (int x = warp; x < 2 * NB; x += kWarps) {  // K blocks (each with its inverse), then Q blocks, the longest first
-        const bool q = x >= NB;
-        const int bb = q ? 2 * NB - 1 - x : NB - 1 - x;
-        block_products<DK, NB, 1>(q, bb, s0 + M::kq, sm + M::a16, sm + M::p16, diag + bb * 272, rw, flag, lane);
-        if (!q) {
-            __syncwarp();
-            block_inverse<NB, 1>(bb, sm + M::a16, diag + bb * 272, flag, lane);
+    tc::tc_fence_after();
+    const uint32_t tmem = *tmem_slot;
+    const uint32_t lane_addr = tmem + ((uint32_t)lane0 << 16);
+    const uint64_t kq_desc = tc::sdesc_sw128(s0 + M::kq, 16, 1024);
+    if (threadIdx.x == 0) {  // [K; Q] K^T
+        const uint32_t id = tc::idesc_f16(false, false, false, 128, T16);
+#pragma unroll
+        for (int ks = 0; ks < KS; ++ks) {
+            const uint64_t at = tc::sdesc_add(kq_desc, (ks >> 2) * 2 * T16 * 128 + (ks & 3) * 32);
+            tc::mma_f16(tmem + M::col_g, at, at, id, ks > 0);
         }
+        tc::mma_commit(&bars[0]);
     }
-    __syncthreads();
-
+    if (threadIdx.x < 2 * T16) {
+        const int r = threadIdx.x, i = r >= T16 ? r - T16 : r;
+        const float e = tc::ex2_approx(rw.g_hi[i] + rw.g_lo[i]);
+        float* f = r >= T16 ? rw.fq : rw.fk;
+        float* c = r >= T16 ? rw.cq : rw.ck;
+        float x = f[i] * (r >= T16 ? d.scale : 1.f);
+        if (d.norm_eps > 0.f) x /= sqrtf(c[i] + d.norm_eps);
+        f[i] = x;
+        c[i] = e * x;
+    }
     // this warp's features: a power-of-two scale each, from the largest of the state's row and of v
-    const int vrow = ((lane >> 4) << 3) + (lane & 7), vchunk = warp * 2 + ((lane >> 3) & 1);
+    const int vrow = ((lane >> 4) << 3) + (lane & 7), vchunk = fb / 8 + ((lane >> 3) & 1);
     float down[2], up[2];
-    uint32_t Sf[KS][4];
     {
         float mx[2] = {0.f, 0.f};
 #pragma unroll
@@ -268,6 +296,7 @@ __global__ void __launch_bounds__(2 * DV, 2) gdn_tree_kernel(const __grid_consta
             for (int x = 0; x < 4; ++x)
                 mx[x & 1] = fmaxf(mx[x & 1], fmaxf(fabsf(bf16_lo(w[x])), fabsf(bf16_hi(w[x]))));
         }
+        uint32_t Sf[4 * KS];
 #pragma unroll
         for (int half = 0; half < 2; ++half) {
             float sx = 0.f;
@@ -277,29 +306,65 @@ __global__ void __launch_bounds__(2 * DV, 2) gdn_tree_kernel(const __grid_consta
             sx = fmaxf(sx, __shfl_xor_sync(0xFFFFFFFFu, sx, 1));
             sx = fmaxf(sx, __shfl_xor_sync(0xFFFFFFFFu, sx, 2));
             pow2_scale(sx, down[half], up[half]);
+            const float2 d2 = make_float2(down[half], down[half]);
 #pragma unroll
             for (int n = 0; n < 2 * KS; ++n) {
-                const uint32_t x = f16x2(raw[half][n].x * down[half], raw[half][n].y * down[half]);
-                Sf[n >> 1][(n & 1) * 2 + half] = x;
-                watch(flag, x);
+                const float2 x = mul2(raw[half][n], d2);
+                Sf[2 * n + half] = f16x2(x.x, x.y);
+                watch(flag, Sf[2 * n + half]);
             }
         }
+#pragma unroll
+        for (int x = 0; x < KS / 4; ++x) tc::tmem_st_frag8(lane_addr + M::col_s + x * 32, Sf + 16 * x);
+        tc::tmem_wait_st();
     }
+    tc::tc_fence_before();
+    __syncthreads();
+    tc::tc_fence_after();
+    if (threadIdx.x == 0) {  // S [K; Q]^T
+        const uint32_t id = tc::idesc_f16(false, false, false, 128, 2 * T16);
+#pragma unroll
+        for (int ks = 0; ks < KS; ++ks)
+            tc::mma_f16_ts(tmem + M::col_d, tmem + M::col_s + ks * 8,
+                           tc::sdesc_add(kq_desc, (ks >> 2) * 2 * T16 * 128 + (ks & 3) * 32), id, ks > 0);
+        tc::mma_commit(&bars[1]);
+    }
+    __syncwarp();
+    // the system's matrices: 16-row block x of [K; Q] sits in lanes 16 x ..
+    float* diag = reinterpret_cast<float*>(sm + M::diag);
+    bool ok = __all_sync(0xFFFFFFFFu, tc::mbar_wait(&bars[0], 0, abort_flag));
+    tc::tc_fence_after();
+    if (ok) {
+        for (int hf = warp >> 2; hf < 2; hf += kWarps / 4) {
+            const int x = 2 * (warp & 3) + hf;
+            if (x >= 2 * NB) continue;
+            const bool q = x >= NB;
+            const int bb = q ? x - NB : x;
+            block_matrices<NB, 1>(q, bb, tmem + M::col_g + ((uint32_t)(16 * x) << 16), sm + M::a16, sm + M::p16,
+                                  diag + bb * 16 * kDiag, rw, flag, lane);
+            if (!q) {
+                __syncwarp();
+                block_inverse<NB, 1>(bb, sm + M::a16, diag + bb * 16 * kDiag, flag, lane);
+            }
+        }
+        ok = __all_sync(0xFFFFFFFFu, tc::mbar_wait(&bars[1], 0, abort_flag));
+    }
+    ok = __syncthreads_and(ok);
+    tc::tc_fence_after();
 
     const int brow = ((lane >> 4) << 3) + (lane & 7), bch = (lane >> 3) & 1;
     uint32_t Uf[NB][4];
 #pragma unroll
     for (int bb = 0; bb < NB; ++bb) {
-        float ak[2][4] = {}, aq[2][4] = {};
+        if (!ok) break;
+        float dk[8], dq[8], ak[2][4], aq[2][4];  // this block's columns of S K^T and S Q^T
+        tc::tmem_ld_frag2(lane_addr + M::col_d + bb * 16, dk);
+        tc::tmem_ld_frag2(lane_addr + M::col_d + T16 + bb * 16, dq);
+        tc::tmem_wait_ld();
 #pragma unroll
-        for (int ks = 0; ks < KS; ++ks) {
-            uint32_t wk[4], wq[4];
-            ldsm4(wk, tile_at<DK * 2>(s0 + M::kq, bb * 16 + brow, 2 * ks + bch));
-            ldsm4(wq, tile_at<DK * 2>(s0 + M::kq, T16 + bb * 16 + brow, 2 * ks + bch));
-            mma_16816(ak[0], Sf[ks], wk[0], wk[1]);
-            mma_16816(ak[1], Sf[ks], wk[2], wk[3]);
-            mma_16816(aq[0], Sf[ks], wq[0], wq[1]);
-            mma_16816(aq[1], Sf[ks], wq[2], wq[3]);
+        for (int x = 0; x < 8; ++x) {
+            ak[x >> 2][x & 3] = dk[x];
+            aq[x >> 2][x & 3] = dq[x];
         }
         // R_b, then U_b
         uint32_t w[4];
@@ -355,7 +420,19 @@ __global__ void __launch_bounds__(2 * DV, 2) gdn_tree_kernel(const __grid_consta
                 w[2 * n + half] = bf16x2(aq[n][2 * half] * up[half], aq[n][2 * half + 1] * up[half]);
         stsm4_t(tile_at<DV * 2>(s0 + M::v, bb * 16 + vrow, vchunk), w);
     }
-    if (__syncthreads_or(watched(flag))) {
+    tc::tc_fence_before();
+    const bool redo = __syncthreads_or(watched(flag));
+    if (warp == 1) {
+        tc::tc_fence_after();
+        if (!ok)  // let the MMAs end before their TMEM goes
+            for (int x = 0; x < 2; ++x) tc::mbar_drain(&bars[x], 0);
+        tc::tmem_dealloc(tmem, M::cols);
+    }
+    if (!ok) {
+        if (threadIdx.x == 0) dev_fail(status, TSV_DEV_TIMEOUT, b, h);
+        return;
+    }
+    if (redo) {
         tree_fp32<DK, DV, NB>(d, anc, layer, b, h, sm);
         return;
     }
@@ -367,25 +444,25 @@ __global__ void __launch_bounds__(2 * DV, 2) gdn_tree_kernel(const __grid_consta
 }
 
 template <int DK, int DV, int NB>
-static void launch_tree_nb(const tsv_gdn_desc& d, const uint64_t* anc, cudaStream_t stream) {
+static void launch_tree_nb(const tsv_gdn_desc& d, const uint64_t* anc, int32_t* status, cudaStream_t stream) {
     constexpr int sm = TreeSmem<DK, DV, NB>::total;
     cudaFuncSetAttribute(gdn_tree_kernel<DK, DV, NB>, cudaFuncAttributeMaxDynamicSharedMemorySize, sm);
-    launch_pdl(gdn_tree_kernel<DK, DV, NB>, (unsigned)((long long)d.n_layers * d.B * d.HV), 2 * DV, sm, stream, d, anc);
+    launch_pdl(gdn_tree_kernel<DK, DV, NB>, (unsigned)((long long)d.n_layers * d.B * d.HV), 2 * DV, sm, stream, d, anc, status);
 }
 
 template <int DK, int DV>
-static void launch_tree_dims(const tsv_gdn_desc& d, const uint64_t* anc, cudaStream_t stream) {
-    if (d.T <= 16) launch_tree_nb<DK, DV, 1>(d, anc, stream);
-    else if (d.T <= 32) launch_tree_nb<DK, DV, 2>(d, anc, stream);
-    else if (d.T <= 48) launch_tree_nb<DK, DV, 3>(d, anc, stream);
-    else launch_tree_nb<DK, DV, 4>(d, anc, stream);
+static void launch_tree_dims(const tsv_gdn_desc& d, const uint64_t* anc, int32_t* status, cudaStream_t stream) {
+    if (d.T <= 16) launch_tree_nb<DK, DV, 1>(d, anc, status, stream);
+    else if (d.T <= 32) launch_tree_nb<DK, DV, 2>(d, anc, status, stream);
+    else if (d.T <= 48) launch_tree_nb<DK, DV, 3>(d, anc, status, stream);
+    else launch_tree_nb<DK, DV, 4>(d, anc, status, stream);
 }
 
-void launch_gdn_tree(const tsv_gdn_desc& d, const uint64_t* anc, cudaStream_t stream) {
-    if (d.DK == 64 && d.DV == 64) launch_tree_dims<64, 64>(d, anc, stream);
-    else if (d.DK == 64) launch_tree_dims<64, 128>(d, anc, stream);
-    else if (d.DV == 64) launch_tree_dims<128, 64>(d, anc, stream);
-    else launch_tree_dims<128, 128>(d, anc, stream);
+void launch_gdn_tree(const tsv_gdn_desc& d, const uint64_t* anc, int32_t* status, cudaStream_t stream) {
+    if (d.DK == 64 && d.DV == 64) launch_tree_dims<64, 64>(d, anc, status, stream);
+    else if (d.DK == 64) launch_tree_dims<64, 128>(d, anc, status, stream);
+    else if (d.DV == 64) launch_tree_dims<128, 64>(d, anc, status, stream);
+    else launch_tree_dims<128, 128>(d, anc, status, stream);
 }
 
 }  // namespace tsv

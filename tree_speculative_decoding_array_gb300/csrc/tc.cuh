@@ -90,6 +90,13 @@ __device__ __forceinline__ bool mbar_wait(uint64_t* bar, uint32_t parity, volati
     }
 }
 
+// Bounded wait that ignores the abort flag: lets work in flight end before its memory is given back.
+__device__ __forceinline__ void mbar_drain(uint64_t* bar, uint32_t parity) {
+    const uint64_t t0 = globaltimer();
+    while (!mbar_try_wait(bar, parity))
+        if (globaltimer() - t0 > 200000000ull) break;  // 200 ms
+}
+
 // The MMA-issuing thread polls without sleeping: its reaction time is on the critical path of every MMA.
 __device__ __forceinline__ bool mbar_wait_spin(uint64_t* bar, uint32_t parity, volatile int* abort) {
     if (mbar_test(bar, parity)) return true;
@@ -243,6 +250,27 @@ __device__ __forceinline__ void tmem_st32(uint32_t taddr, const uint32_t (&r)[32
 
 __device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t (&r)[16]) {
     asm volatile("tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16};"
+                 :
+                 : "r"(taddr), "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]),
+                   "r"(r[8]), "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
+                 : "memory");
+}
+
+// Loads and stores in the layout of mma.sync fragments, for 16 lanes (an address' lane field is a multiple of 16
+// within the warp's quarter; both layouts checked on this part against 32x32b accesses).
+// 16 fp32 columns as two m16n8 accumulator tiles: r[4 n + e] is (lane / 4 + 8 (e / 2), 8 n + 2 (lane % 4) + e % 2).
+__device__ __forceinline__ void tmem_ld_frag2(uint32_t taddr, float (&r)[8]) {
+    uint32_t x[8];
+    asm volatile("tcgen05.ld.sync.aligned.16x256b.x2.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];"
+                 : "=r"(x[0]), "=r"(x[1]), "=r"(x[2]), "=r"(x[3]), "=r"(x[4]), "=r"(x[5]), "=r"(x[6]), "=r"(x[7])
+                 : "r"(taddr));
+#pragma unroll
+    for (int k = 0; k < 8; ++k) r[k] = __uint_as_float(x[k]);
+}
+// 32 32-bit columns: r[2 n + h] goes to (lane / 4 + 8 h, 4 n + lane % 4).  With r[2 n], r[2 n + 1] the 16-bit pairs of
+// an m16n8 tile's rows, 64 values of each row in order: an A operand of the MMA.
+__device__ __forceinline__ void tmem_st_frag8(uint32_t taddr, const uint32_t* r) {
+    asm volatile("tcgen05.st.sync.aligned.16x128b.x8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16};"
                  :
                  : "r"(taddr), "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]),
                    "r"(r[8]), "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
