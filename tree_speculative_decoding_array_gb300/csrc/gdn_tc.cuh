@@ -137,13 +137,16 @@ __device__ __forceinline__ uint32_t tile_at(uint32_t base, int row, int chunk) {
     return base + (uint32_t)(row * BYTES + ((chunk ^ (row & 7)) << 4));
 }
 
-// Per-row scalars of a block.
+// Per-row scalars of a block: those of the key head, and those of one value head.
+struct GdnKeys {
+    uint64_t before[64];   // rows ahead of i in its system (strict ancestors, or earlier tokens)
+    float fk[64], fq[64];  // what a staged row's products are multiplied with: its scale and norm (and q's scale)
+    float sk[64], sq[64];  // sums of squares
+};
 struct GdnRows {
     float g_hi[64], g_lo[64];  // G in units of ln 2, as hi + lo (differences of far sums keep fp32 accuracy)
-    float fk[64], fq[64];      // what a staged row's products are multiplied with: its scale and norm (and q's scale)
     float beta[64];
     float ck[64], cq[64];      // 2^G fk, 2^G fq
-    uint64_t before[64];       // rows ahead of i in its system (strict ancestors, or earlier tokens)
 };
 
 // One chunk of 8 bf16 values of a K or Q row -> fp16, scaled by a power of two that brings the row's norm to [1, 2);
@@ -183,32 +186,33 @@ __device__ __forceinline__ uint32_t kq_at(uint32_t base, int row, int chunk) {
 constexpr int kDiag = 20;  // fp32 row stride of a diagonal block: 16-byte aligned, rows in different banks
 template <int NB, int PIECES>
 __device__ __forceinline__ void block_matrices(bool q, int b, uint32_t taddr, char* a16, char* p16, float* diag,
-                                               const GdnRows& rw, uint32_t& flag, int lane) {
+                                               const GdnKeys& ky, const GdnRows& rw, uint32_t& flag, int lane) {
     constexpr int T = 16 * NB;
-    float acc[NB][8];
-#pragma unroll
-    for (int c = 0; c < NB; ++c)
-        if (c <= b) tc::tmem_ld_frag2(taddr + c * 16, acc[c]);
-    tc::tmem_wait_ld();
     const int g = lane >> 2, t = lane & 3;
+    float acc[2][8];
+    tc::tmem_ld_frag2(taddr, acc[0]);
 #pragma unroll
-    for (int half = 0; half < 2; ++half) {
-        const int il = g + 8 * half, i = b * 16 + il;
-        const uint64_t seen = (q ? rw.before[i] | (1ull << i) : rw.before[i]) >> (2 * t);
-        const float gh = rw.g_hi[i], gl = rw.g_lo[i];
-        const float f = q ? rw.fq[i] : rw.beta[i] * rw.fk[i];
+    for (int c = 0; c < NB; ++c) {
+        if (c > b) break;
+        tc::tmem_wait_ld();
+        if (c < b) tc::tmem_ld_frag2(taddr + (c + 1) * 16, acc[(c + 1) & 1]);
+        const float(&x)[8] = acc[c & 1];
 #pragma unroll
-        for (int c = 0; c < NB; ++c) {
-            if (c > b) break;
-            const uint32_t bits = (uint32_t)(seen >> (c * 16));
+        for (int half = 0; half < 2; ++half) {
+            const int il = g + 8 * half, i = b * 16 + il;
+            uint32_t bits = (uint32_t)(ky.before[i] >> (c * 16));
+            if (q && c == b) bits |= 1u << il;
+            bits >>= 2 * t;
+            const float gh = rw.g_hi[i], gl = rw.g_lo[i];
+            const float f = q ? ky.fq[i] : rw.beta[i] * ky.fk[i];
 #pragma unroll
             for (int n = 0; n < 2; ++n) {
                 const int j0 = c * 16 + n * 8 + 2 * t;
                 const float2 jh = *reinterpret_cast<const float2*>(&rw.g_hi[j0]), jl2 = *reinterpret_cast<const float2*>(&rw.g_lo[j0]),
-                             jf = *reinterpret_cast<const float2*>(&rw.fk[j0]);
+                             jf = *reinterpret_cast<const float2*>(&ky.fk[j0]);
                 float y[2];
-                y[0] = acc[c][4 * n + 2 * half] * jf.x * (f * tc::ex2_approx((gh - jh.x) + (gl - jl2.x)));
-                y[1] = acc[c][4 * n + 2 * half + 1] * jf.y * (f * tc::ex2_approx((gh - jh.y) + (gl - jl2.y)));
+                y[0] = x[4 * n + 2 * half] * jf.x * (f * tc::ex2_approx((gh - jh.x) + (gl - jl2.x)));
+                y[1] = x[4 * n + 2 * half + 1] * jf.y * (f * tc::ex2_approx((gh - jh.y) + (gl - jl2.y)));
 #pragma unroll
                 for (int e = 0; e < 2; ++e) y[e] = (bits & (1u << (n * 8 + e))) ? y[e] : 0.f;
                 if (q) {

@@ -5,33 +5,37 @@
 // ancestors unrolls into one triangular system over the tree (gdn_tc.cuh), in which the state appears only in the
 // products S k_i and S q_i: no node's state is ever formed.
 //
-// One CTA per (layer, sequence, value head): each warp owns 16 value features and takes their rows of S from global
-// memory to fp16 pairs in TMEM.  K, Q and V are fetched asynchronously, the state's loads are issued behind them and
-// land while the rows are staged; the matrices are built while the tensor cores work on S [K; Q]^T.
+// One CTA per (layer, sequence, some value heads of one key head): K and Q are staged and [K; Q] K^T taken once, then
+// the value heads follow one another.  Each warp owns 16 value features and takes their rows of S from global memory
+// to fp16 pairs in TMEM; the next head's state and V are fetched while this head is computed, and a head's matrices
+// are built while the tensor cores work on its S [K; Q]^T.
 #include <math.h>
 
 #include "gdn_tc.cuh"
 
 namespace tsv {
 
+constexpr int kMaxHeads = 4;  // value heads of one CTA
+
 template <int DK, int DV, int NB>
 struct TreeSmem {
     static constexpr int T = 16 * NB;
     static constexpr int kq = 0;                       // K rows [T], Q rows [T], DK fp16 each
-    static constexpr int v = kq + 2 * T * DK * 2;      // V rows [T], DV bf16 each; o over them
-    static constexpr int a16 = v + T * DV * 2;         // [T][64] fp16: -A below the diagonal blocks, inverses on them
+    static constexpr int v = kq + 2 * T * DK * 2;      // two buffers of V rows [T], DV bf16 each; o over them
+    static constexpr int a16 = v + 2 * T * DV * 2;     // [T][64] fp16: -A below the diagonal blocks, inverses on them
     static constexpr int p16 = a16 + T * 128;          // [T][64] fp16: P
     static constexpr int diag = p16 + T * 128;         // [NB][16][kDiag] fp32: A of the diagonal blocks
-    static constexpr int rows = diag + NB * 16 * kDiag * 4;
-    static constexpr int bars = rows + (int)sizeof(GdnRows);  // two barriers, TMEM address, abort flag
+    static constexpr int keys = diag + NB * 16 * kDiag * 4;
+    static constexpr int rows = keys + (int)sizeof(GdnKeys);  // per value head
+    static constexpr int bars = rows + kMaxHeads * (int)sizeof(GdnRows);  // two barriers, TMEM address, abort flag
     // [K; Q] K^T takes 128 rows of the K and Q tile, whatever lies behind them
     static constexpr int reach = (DK / 64 - 1) * 2 * T * 128 + 128 * 128;
     static constexpr int total = bars + 32 > reach ? bars + 32 : reach;
     // TMEM columns: S as fp16 pairs, S [K; Q]^T, [K; Q] K^T
     static constexpr int col_s = 0, col_d = DK / 2, col_g = col_d + 2 * T, cols_used = col_g + T;
     static constexpr int cols = cols_used <= 64 ? 64 : cols_used <= 128 ? 128 : 256;
-    // the fp32 path: u [T][DV] over kq and v, one node's k and q over a16, its ancestors' products over p16
-    static_assert(T * DV * 4 <= a16 && 2 * DK * 4 <= T * 128 && 2 * 64 * 4 <= T * 128, "fp32 path does not fit");
+    // the fp32 path: u [T][DV] over v, one node's k and q over a16, its ancestors' products over p16
+    static_assert(T * DV * 4 <= a16 - v && 2 * DK * 4 <= T * 128 && 2 * 64 * 4 <= T * 128, "fp32 path does not fit");
 };
 
 // One bf16 row of DK features, read by a whole warp, normalised: this lane's DK / 32 values.
@@ -57,12 +61,12 @@ __device__ __forceinline__ void unit_row(const uint16_t* src, float norm_eps, fl
 // the inputs, keys that are not of unit length with large writes).  Only a node's ancestors are ever read, so what is
 // not finite stays with its node and the node's descendants.  Thread = value feature.
 template <int DK, int DV, int NB>
-__device__ __noinline__ void tree_fp32(const tsv_gdn_desc& d, const uint64_t* anc, int layer, int b, int h, char* sm) {
+__device__ __noinline__ void tree_fp32(const tsv_gdn_desc& d, const uint64_t* anc, int layer, int b, int h, char* sm, const GdnRows& rw) {
     using M = TreeSmem<DK, DV, NB>;
-    float* u = reinterpret_cast<float*>(sm);
+    float* u = reinterpret_cast<float*>(sm + M::v);
     float* kk = reinterpret_cast<float*>(sm + M::a16);   // k_i, then q_i
     float* wk = reinterpret_cast<float*>(sm + M::p16);   // e^{G_i - G_j} (k_i . k_j), then (q_i . k_j)
-    const GdnRows& rw = *reinterpret_cast<const GdnRows*>(sm + M::rows);
+    const GdnKeys& ky = *reinterpret_cast<const GdnKeys*>(sm + M::keys);
     const int T = d.T, hk = h / (d.HV / d.HK), warp = threadIdx.x >> 5, lane = threadIdx.x & 31, r = threadIdx.x;
     const uint16_t* K = reinterpret_cast<const uint16_t*>(d.k[layer]);
     const uint16_t* Q = reinterpret_cast<const uint16_t*>(d.q[layer]);
@@ -79,7 +83,7 @@ __device__ __noinline__ void tree_fp32(const tsv_gdn_desc& d, const uint64_t* an
                 kk[DK + lane + 32 * e] = qi[e];
             }
         int at = 0;
-        for (uint64_t a = rw.before[i] | (1ull << i); a; a &= a - 1, ++at) {
+        for (uint64_t a = ky.before[i] | (1ull << i); a; a &= a - 1, ++at) {
             if (at % (DV / 16) != warp) continue;
             const int j = __ffsll((long long)a) - 1;
             float kj[DK / 32], x = 0.f, y = 0.f;
@@ -111,7 +115,7 @@ __device__ __noinline__ void tree_fp32(const tsv_gdn_desc& d, const uint64_t* an
             const float w = exp2f(rw.g_hi[i] + rw.g_lo[i]);
             const size_t ov = (row * d.HV + h) * DV + r;
             float x = bf16_bits_to_f32(reinterpret_cast<const uint16_t*>(d.v[layer])[ov]) - w * sk, y = w * sq;
-            for (uint64_t a = rw.before[i]; a; a &= a - 1) {
+            for (uint64_t a = ky.before[i]; a; a &= a - 1) {
                 const int j = __ffsll((long long)a) - 1;
                 x = fmaf(-wk[j], u[j * DV + r], x);
                 y = fmaf(wk[64 + j], u[j * DV + r], y);
@@ -125,21 +129,22 @@ __device__ __noinline__ void tree_fp32(const tsv_gdn_desc& d, const uint64_t* an
 
 template <int DK, int DV, int NB>
 __global__ void __launch_bounds__(2 * DV, 2) gdn_tree_kernel(const __grid_constant__ tsv_gdn_desc d,
-                                                             const uint64_t* __restrict__ anc, int32_t* status) {
+                                                             const uint64_t* __restrict__ anc, int heads, int32_t* status) {
     griddep_begin();
     using M = TreeSmem<DK, DV, NB>;
     constexpr int kThreads = 2 * DV, kWarps = DV / 16;
     constexpr int KS = DK / 16;
     constexpr int T16 = M::T;
     extern __shared__ __align__(1024) char sm[];
-    GdnRows& rw = *reinterpret_cast<GdnRows*>(sm + M::rows);
+    GdnKeys& ky = *reinterpret_cast<GdnKeys*>(sm + M::keys);
+    GdnRows* rows = reinterpret_cast<GdnRows*>(sm + M::rows);
     const uint32_t s0 = tc::smem_u32(sm);
     const int T = d.T;
     int item = blockIdx.x;
-    const int h = item % d.HV;
-    item /= d.HV;
+    const int h0 = item % (d.HV / heads) * heads;
+    item /= d.HV / heads;
     const int b = item % d.B, layer = item / d.B;
-    const int hk = h / (d.HV / d.HK);
+    const int hk = h0 / (d.HV / d.HK);
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int g = lane >> 2, t = lane & 3;
     const size_t row0 = (size_t)b * T;
@@ -160,7 +165,7 @@ __global__ void __launch_bounds__(2 * DV, 2) gdn_tree_kernel(const __grid_consta
         tc::tmem_relinquish();
     }
 
-    // K, Q and V rows; rows beyond T are zero
+    // K, Q and the first V rows; rows beyond T are zero
     constexpr int LPR = DK / 8;                      // lanes that share a K or Q row
     constexpr int KQ = 2 * T16 * LPR / kThreads;     // its chunks per thread
     static_assert(KQ * kThreads == 2 * T16 * LPR, "uneven staging");
@@ -173,44 +178,43 @@ __global__ void __launch_bounds__(2 * DV, 2) gdn_tree_kernel(const __grid_consta
     }
     cp_commit();
     constexpr int CPR = DV / 8;
-    for (int e = threadIdx.x; e < T16 * CPR; e += kThreads) {
-        const int i = e / CPR, cc = e % CPR;
-        cp16(tile_at<DV * 2>(s0 + M::v, i, cc),
-             reinterpret_cast<const uint16_t*>(d.v[layer]) + ((row0 + (i < T ? i : 0)) * d.HV + h) * DV + cc * 8, i < T);
-    }
-    cp_commit();
-    // warp 0: two nodes' gates per lane
-    uint64_t before[2] = {0, 0};
-    float gi[2] = {0.f, 0.f}, bi[2] = {0.f, 0.f};
-    if (warp == 0) {
-#pragma unroll
-        for (int x = 0; x < 2; ++x) {
-            const int i = lane + 32 * x;
-            if (i < T) {
-                before[x] = anc[row0 + i] & ((1ull << i) - 1ull);
-                gi[x] = d.g[layer][(row0 + i) * d.HV + h];
-                bi[x] = d.beta[layer][(row0 + i) * d.HV + h];
-            }
+    auto fetch_v = [&](int k) {
+        for (int e = threadIdx.x; e < T16 * CPR; e += kThreads) {
+            const int i = e / CPR, cc = e % CPR;
+            cp16(tile_at<DV * 2>(s0 + M::v + (k & 1) * T16 * DV * 2, i, cc),
+                 reinterpret_cast<const uint16_t*>(d.v[layer]) + ((row0 + (i < T ? i : 0)) * d.HV + h0 + k) * DV + cc * 8, i < T);
         }
-    }
-    // the state's loads: features (rows) f0 and f0 + 8, columns 8 n + 2 t, + 1
-    const int f0 = fb + g;
-    const float* S = d.state[layer] + (((size_t)b * d.HV + h) * DV + f0) * DK + 2 * t;
+        cp_commit();
+    };
+    fetch_v(0);
+    // the state's loads: features (rows) fb + g and fb + g + 8, columns 8 n + 2 t, + 1
+    const float* S = d.state[layer] + (((size_t)b * d.HV + h0) * DV + fb + g) * DK + 2 * t;
     float2 raw[2][2 * KS];
+    auto fetch_s = [&](int k) {
 #pragma unroll
-    for (int half = 0; half < 2; ++half)
+        for (int half = 0; half < 2; ++half)
 #pragma unroll
-        for (int n = 0; n < 2 * KS; ++n) raw[half][n] = __ldcs(reinterpret_cast<const float2*>(S + half * 8 * DK + 8 * n));
-
-    if (warp == 0) {  // G by pointer doubling over the parents (the highest strict ancestor)
+            for (int n = 0; n < 2 * KS; ++n)
+                raw[half][n] = __ldcs(reinterpret_cast<const float2*>(S + (size_t)k * DV * DK + half * 8 * DK + 8 * n));
+    };
+    // G of every head, a warp each, two nodes per lane: pointer doubling over the parents (the highest strict ancestor)
+    for (int k = warp; k < heads; k += kWarps) {
         Pair G[2];
         int p[2];
 #pragma unroll
         for (int x = 0; x < 2; ++x) {
-            rw.before[lane + 32 * x] = before[x];
-            rw.beta[lane + 32 * x] = bi[x];
-            G[x] = log2_decay(gi[x]);
-            p[x] = before[x] ? 63 - __clzll((long long)before[x]) : -1;
+            const int i = lane + 32 * x;
+            uint64_t before = 0;
+            float gi = 0.f, bi = 0.f;
+            if (i < T) {
+                before = anc[row0 + i] & ((1ull << i) - 1ull);
+                gi = d.g[layer][(row0 + i) * d.HV + h0 + k];
+                bi = d.beta[layer][(row0 + i) * d.HV + h0 + k];
+            }
+            if (k == 0) ky.before[i] = before;
+            rows[k].beta[i] = bi;
+            G[x] = log2_decay(gi);
+            p[x] = before ? 63 - __clzll((long long)before) : -1;
         }
         while (__any_sync(0xFFFFFFFFu, p[0] >= 0 || p[1] >= 0)) {  // each round halves every remaining chain
             Pair more[2];
@@ -238,190 +242,212 @@ __global__ void __launch_bounds__(2 * DV, 2) gdn_tree_kernel(const __grid_consta
         }
 #pragma unroll
         for (int x = 0; x < 2; ++x) {
-            rw.g_hi[lane + 32 * x] = G[x].hi;
-            rw.g_lo[lane + 32 * x] = G[x].lo;
+            rows[k].g_hi[lane + 32 * x] = G[x].hi;
+            rows[k].g_lo[lane + 32 * x] = G[x].lo;
         }
     }
-    uint32_t flag = 0;
+    fetch_s(0);
+    uint32_t flag_kq = 0;
     cp_wait<1>();  // this thread's own chunks of K and Q: converted in place
 #pragma unroll
     for (int x = 0; x < KQ; ++x) {
         const int r = threadIdx.x / LPR + x * (kThreads / LPR);
         char* at = sm + kq_at<2 * T16>(M::kq, r, chunk);
         float ss, upr;
-        *reinterpret_cast<uint4*>(at) = stage_chunk<DK>(*reinterpret_cast<const uint4*>(at), ss, upr, flag);
+        *reinterpret_cast<uint4*>(at) = stage_chunk<DK>(*reinterpret_cast<const uint4*>(at), ss, upr, flag_kq);
         if (chunk == 0) {  // the row's factor is finished below
             const int i = r >= T16 ? r - T16 : r;
-            (r >= T16 ? rw.fq : rw.fk)[i] = upr;
-            (r >= T16 ? rw.cq : rw.ck)[i] = ss;
+            (r >= T16 ? ky.fq : ky.fk)[i] = upr;
+            (r >= T16 ? ky.sq : ky.sk)[i] = ss;
+        }
+    }
+    tc::fence_proxy_async_smem();
+    tc::tc_fence_before();
+
+    const uint64_t kq_desc = tc::sdesc_sw128(s0 + M::kq, 16, 1024);
+    const int vrow = ((lane >> 4) << 3) + (lane & 7), vchunk = fb / 8 + ((lane >> 3) & 1);
+    const int brow = ((lane >> 4) << 3) + (lane & 7), bch = (lane >> 3) & 1;
+    float* diag = reinterpret_cast<float*>(sm + M::diag);
+    uint32_t tmem = 0, redo = 0;
+    bool ok = true;
+    for (int k = 0; k < heads; ++k) {
+        const GdnRows& rw = rows[k];
+        const int vt = M::v + (k & 1) * T16 * DV * 2;
+        uint32_t flag = flag_kq;
+        cp_wait<0>();
+        __syncthreads();  // V is here; the head before is done with shared memory and TMEM
+        tc::tc_fence_after();
+        if (k == 0) {
+            tmem = *tmem_slot;
+            if (threadIdx.x == 0) {  // [K; Q] K^T
+                const uint32_t id = tc::idesc_f16(false, false, false, 128, T16);
+#pragma unroll
+                for (int ks = 0; ks < KS; ++ks) {
+                    const uint64_t at = tc::sdesc_add(kq_desc, (ks >> 2) * 2 * T16 * 128 + (ks & 3) * 32);
+                    tc::mma_f16(tmem + M::col_g, at, at, id, ks > 0);
+                }
+                tc::mma_commit(&bars[0]);
+            }
+            if (threadIdx.x < 2 * T16) {
+                const int r = threadIdx.x, i = r >= T16 ? r - T16 : r;
+                float* f = r >= T16 ? ky.fq : ky.fk;
+                float x = f[i] * (r >= T16 ? d.scale : 1.f);
+                if (d.norm_eps > 0.f) x /= sqrtf((r >= T16 ? ky.sq : ky.sk)[i] + d.norm_eps);
+                f[i] = x;
+                for (int y = 0; y < heads; ++y)
+                    (r >= T16 ? rows[y].cq : rows[y].ck)[i] = tc::ex2_approx(rows[y].g_hi[i] + rows[y].g_lo[i]) * x;
+            }
+        }
+        if (k + 1 < heads) fetch_v(k + 1);
+        // this warp's features: a power-of-two scale each, from the largest of the state's row and of v
+        float down[2], up[2];
+        {
+            float mx[2] = {0.f, 0.f};
+#pragma unroll
+            for (int bb = 0; bb < NB; ++bb) {
+                uint32_t w[4];
+                ldsm4_t(w, tile_at<DV * 2>(s0 + vt, bb * 16 + vrow, vchunk));
+#pragma unroll
+                for (int x = 0; x < 4; ++x)
+                    mx[x & 1] = fmaxf(mx[x & 1], fmaxf(fabsf(bf16_lo(w[x])), fabsf(bf16_hi(w[x]))));
+            }
+            uint32_t Sf[4 * KS];
+#pragma unroll
+            for (int half = 0; half < 2; ++half) {
+                float sx = 0.f;
+#pragma unroll
+                for (int n = 0; n < 2 * KS; ++n) sx = fmaxf(sx, fmaxf(fabsf(raw[half][n].x), fabsf(raw[half][n].y)));
+                sx = fmaxf(8.f * sx, mx[half]);
+                sx = fmaxf(sx, __shfl_xor_sync(0xFFFFFFFFu, sx, 1));
+                sx = fmaxf(sx, __shfl_xor_sync(0xFFFFFFFFu, sx, 2));
+                pow2_scale(sx, down[half], up[half]);
+                const float2 d2 = make_float2(down[half], down[half]);
+#pragma unroll
+                for (int n = 0; n < 2 * KS; ++n) {
+                    const float2 x = mul2(raw[half][n], d2);
+                    Sf[2 * n + half] = f16x2(x.x, x.y);
+                    watch(flag, Sf[2 * n + half]);
+                }
+            }
+#pragma unroll
+            for (int x = 0; x < KS / 4; ++x)
+                tc::tmem_st_frag8(tmem + ((uint32_t)lane0 << 16) + M::col_s + x * 32, Sf + 16 * x);
+            tc::tmem_wait_st();
+        }
+        if (k + 1 < heads) fetch_s(k + 1);
+        tc::tc_fence_before();
+        __syncthreads();
+        tc::tc_fence_after();
+        if (threadIdx.x == 0) {  // S [K; Q]^T
+            const uint32_t id = tc::idesc_f16(false, false, false, 128, 2 * T16);
+#pragma unroll
+            for (int ks = 0; ks < KS; ++ks)
+                tc::mma_f16_ts(tmem + M::col_d, tmem + M::col_s + ks * 8,
+                               tc::sdesc_add(kq_desc, (ks >> 2) * 2 * T16 * 128 + (ks & 3) * 32), id, ks > 0);
+            tc::mma_commit(&bars[1]);
+        }
+        __syncwarp();
+        // the system's matrices: 16-row block x of [K; Q] sits in lanes 16 x ..
+        ok = __all_sync(0xFFFFFFFFu, tc::mbar_wait(&bars[0], 0, abort_flag));
+        tc::tc_fence_after();
+        if (ok) {
+            for (int hf = warp >> 2; hf < 2; hf += kWarps / 4) {
+                const int x = 2 * (warp & 3) + hf;
+                if (x >= 2 * NB) continue;
+                const bool q = x >= NB;
+                const int bb = q ? x - NB : x;
+                block_matrices<NB, 1>(q, bb, tmem + M::col_g + ((uint32_t)(16 * x) << 16), sm + M::a16, sm + M::p16,
+                                      diag + bb * 16 * kDiag, ky, rw, flag, lane);
+                if (!q) {
+                    __syncwarp();
+                    block_inverse<NB, 1>(bb, sm + M::a16, diag + bb * 16 * kDiag, flag, lane);
+                }
+            }
+            ok = __all_sync(0xFFFFFFFFu, tc::mbar_wait(&bars[1], k & 1, abort_flag));
+        }
+        ok = __syncthreads_and(ok);
+        tc::tc_fence_after();
+        if (!ok) break;
+
+        uint32_t Uf[NB][4];
+#pragma unroll
+        for (int bb = 0; bb < NB; ++bb) {
+            float dk[8], dq[8], ak[2][4], aq[2][4];  // this block's columns of S K^T and S Q^T
+            tc::tmem_ld_frag2(tmem + ((uint32_t)lane0 << 16) + M::col_d + bb * 16, dk);
+            tc::tmem_ld_frag2(tmem + ((uint32_t)lane0 << 16) + M::col_d + T16 + bb * 16, dq);
+            tc::tmem_wait_ld();
+#pragma unroll
+            for (int x = 0; x < 8; ++x) {
+                ak[x >> 2][x & 3] = dk[x];
+                aq[x >> 2][x & 3] = dq[x];
+            }
+            // R_b, then U_b
+            uint32_t w[4];
+            ldsm4_t(w, tile_at<DV * 2>(s0 + vt, bb * 16 + vrow, vchunk));
+#pragma unroll
+            for (int n = 0; n < 2; ++n) {
+                const int i = bb * 16 + n * 8 + 2 * t;
+                const float2 be = *reinterpret_cast<const float2*>(&rw.beta[i]), ck = *reinterpret_cast<const float2*>(&rw.ck[i]),
+                             cq = *reinterpret_cast<const float2*>(&rw.cq[i]);
+#pragma unroll
+                for (int half = 0; half < 2; ++half) {
+                    const uint32_t v2 = w[2 * n + half];
+                    ak[n][2 * half] = be.x * (bf16_lo(v2) * down[half] - ck.x * ak[n][2 * half]);
+                    ak[n][2 * half + 1] = be.y * (bf16_hi(v2) * down[half] - ck.y * ak[n][2 * half + 1]);
+                    aq[n][2 * half] *= cq.x;
+                    aq[n][2 * half + 1] *= cq.y;
+                }
+            }
+#pragma unroll
+            for (int c = 0; c < bb; ++c) {
+                uint32_t wa[4];
+                ldsm4(wa, tile_at<128>(s0 + M::a16, bb * 16 + brow, 2 * c + bch));
+                mma_16816(ak[0], Uf[c], wa[0], wa[1]);
+                mma_16816(ak[1], Uf[c], wa[2], wa[3]);
+            }
+            uint32_t wt[4], r[4];
+            ldsm4(wt, tile_at<128>(s0 + M::a16, bb * 16 + brow, 2 * bb + bch));
+#pragma unroll
+            for (int x = 0; x < 4; ++x) {
+                r[x] = f16x2(ak[x >> 1][2 * (x & 1)], ak[x >> 1][2 * (x & 1) + 1]);
+                watch(flag, r[x]);
+            }
+            float u[2][4] = {};
+            mma_16816(u[0], r, wt[0], wt[1]);
+            mma_16816(u[1], r, wt[2], wt[3]);
+#pragma unroll
+            for (int x = 0; x < 4; ++x) {
+                Uf[bb][x] = f16x2(u[x >> 1][2 * (x & 1)], u[x >> 1][2 * (x & 1) + 1]);
+                watch(flag, Uf[bb][x]);
+            }
+#pragma unroll
+            for (int c = 0; c <= bb; ++c) {
+                uint32_t wp[4];
+                ldsm4(wp, tile_at<128>(s0 + M::p16, bb * 16 + brow, 2 * c + bch));
+                mma_16816(aq[0], Uf[c], wp[0], wp[1]);
+                mma_16816(aq[1], Uf[c], wp[2], wp[3]);
+            }
+            // o over v's place
+#pragma unroll
+            for (int n = 0; n < 2; ++n)
+#pragma unroll
+                for (int half = 0; half < 2; ++half)
+                    w[2 * n + half] = bf16x2(aq[n][2 * half] * up[half], aq[n][2 * half + 1] * up[half]);
+            stsm4_t(tile_at<DV * 2>(s0 + vt, bb * 16 + vrow, vchunk), w);
+        }
+        tc::tc_fence_before();
+        if (__syncthreads_or(watched(flag))) {
+            redo |= 1u << k;
+            continue;
+        }
+        for (int e = threadIdx.x; e < T * CPR; e += kThreads) {
+            const int i = e / CPR, c = e % CPR;
+            *reinterpret_cast<uint4*>(reinterpret_cast<uint16_t*>(d.o[layer]) + ((row0 + i) * d.HV + h0 + k) * DV + c * 8) =
+                *reinterpret_cast<const uint4*>(sm + tile_at<DV * 2>(vt, i, c));
         }
     }
     cp_wait<0>();
-    tc::fence_proxy_async_smem();
-    tc::tc_fence_before();
     __syncthreads();
-    tc::tc_fence_after();
-    const uint32_t tmem = *tmem_slot;
-    const uint32_t lane_addr = tmem + ((uint32_t)lane0 << 16);
-    const uint64_t kq_desc = tc::sdesc_sw128(s0 + M::kq, 16, 1024);
-    if (threadIdx.x == 0) {  // [K; Q] K^T
-        const uint32_t id = tc::idesc_f16(false, false, false, 128, T16);
-#pragma unroll
-        for (int ks = 0; ks < KS; ++ks) {
-            const uint64_t at = tc::sdesc_add(kq_desc, (ks >> 2) * 2 * T16 * 128 + (ks & 3) * 32);
-            tc::mma_f16(tmem + M::col_g, at, at, id, ks > 0);
-        }
-        tc::mma_commit(&bars[0]);
-    }
-    if (threadIdx.x < 2 * T16) {
-        const int r = threadIdx.x, i = r >= T16 ? r - T16 : r;
-        const float e = tc::ex2_approx(rw.g_hi[i] + rw.g_lo[i]);
-        float* f = r >= T16 ? rw.fq : rw.fk;
-        float* c = r >= T16 ? rw.cq : rw.ck;
-        float x = f[i] * (r >= T16 ? d.scale : 1.f);
-        if (d.norm_eps > 0.f) x /= sqrtf(c[i] + d.norm_eps);
-        f[i] = x;
-        c[i] = e * x;
-    }
-    // this warp's features: a power-of-two scale each, from the largest of the state's row and of v
-    const int vrow = ((lane >> 4) << 3) + (lane & 7), vchunk = fb / 8 + ((lane >> 3) & 1);
-    float down[2], up[2];
-    {
-        float mx[2] = {0.f, 0.f};
-#pragma unroll
-        for (int bb = 0; bb < NB; ++bb) {
-            uint32_t w[4];
-            ldsm4_t(w, tile_at<DV * 2>(s0 + M::v, bb * 16 + vrow, vchunk));
-#pragma unroll
-            for (int x = 0; x < 4; ++x)
-                mx[x & 1] = fmaxf(mx[x & 1], fmaxf(fabsf(bf16_lo(w[x])), fabsf(bf16_hi(w[x]))));
-        }
-        uint32_t Sf[4 * KS];
-#pragma unroll
-        for (int half = 0; half < 2; ++half) {
-            float sx = 0.f;
-#pragma unroll
-            for (int n = 0; n < 2 * KS; ++n) sx = fmaxf(sx, fmaxf(fabsf(raw[half][n].x), fabsf(raw[half][n].y)));
-            sx = fmaxf(8.f * sx, mx[half]);
-            sx = fmaxf(sx, __shfl_xor_sync(0xFFFFFFFFu, sx, 1));
-            sx = fmaxf(sx, __shfl_xor_sync(0xFFFFFFFFu, sx, 2));
-            pow2_scale(sx, down[half], up[half]);
-            const float2 d2 = make_float2(down[half], down[half]);
-#pragma unroll
-            for (int n = 0; n < 2 * KS; ++n) {
-                const float2 x = mul2(raw[half][n], d2);
-                Sf[2 * n + half] = f16x2(x.x, x.y);
-                watch(flag, Sf[2 * n + half]);
-            }
-        }
-#pragma unroll
-        for (int x = 0; x < KS / 4; ++x) tc::tmem_st_frag8(lane_addr + M::col_s + x * 32, Sf + 16 * x);
-        tc::tmem_wait_st();
-    }
-    tc::tc_fence_before();
-    __syncthreads();
-    tc::tc_fence_after();
-    if (threadIdx.x == 0) {  // S [K; Q]^T
-        const uint32_t id = tc::idesc_f16(false, false, false, 128, 2 * T16);
-#pragma unroll
-        for (int ks = 0; ks < KS; ++ks)
-            tc::mma_f16_ts(tmem + M::col_d, tmem + M::col_s + ks * 8,
-                           tc::sdesc_add(kq_desc, (ks >> 2) * 2 * T16 * 128 + (ks & 3) * 32), id, ks > 0);
-        tc::mma_commit(&bars[1]);
-    }
-    __syncwarp();
-    // the system's matrices: 16-row block x of [K; Q] sits in lanes 16 x ..
-    float* diag = reinterpret_cast<float*>(sm + M::diag);
-    bool ok = __all_sync(0xFFFFFFFFu, tc::mbar_wait(&bars[0], 0, abort_flag));
-    tc::tc_fence_after();
-    if (ok) {
-        for (int hf = warp >> 2; hf < 2; hf += kWarps / 4) {
-            const int x = 2 * (warp & 3) + hf;
-            if (x >= 2 * NB) continue;
-            const bool q = x >= NB;
-            const int bb = q ? x - NB : x;
-            block_matrices<NB, 1>(q, bb, tmem + M::col_g + ((uint32_t)(16 * x) << 16), sm + M::a16, sm + M::p16,
-                                  diag + bb * 16 * kDiag, rw, flag, lane);
-            if (!q) {
-                __syncwarp();
-                block_inverse<NB, 1>(bb, sm + M::a16, diag + bb * 16 * kDiag, flag, lane);
-            }
-        }
-        ok = __all_sync(0xFFFFFFFFu, tc::mbar_wait(&bars[1], 0, abort_flag));
-    }
-    ok = __syncthreads_and(ok);
-    tc::tc_fence_after();
-
-    const int brow = ((lane >> 4) << 3) + (lane & 7), bch = (lane >> 3) & 1;
-    uint32_t Uf[NB][4];
-#pragma unroll
-    for (int bb = 0; bb < NB; ++bb) {
-        if (!ok) break;
-        float dk[8], dq[8], ak[2][4], aq[2][4];  // this block's columns of S K^T and S Q^T
-        tc::tmem_ld_frag2(lane_addr + M::col_d + bb * 16, dk);
-        tc::tmem_ld_frag2(lane_addr + M::col_d + T16 + bb * 16, dq);
-        tc::tmem_wait_ld();
-#pragma unroll
-        for (int x = 0; x < 8; ++x) {
-            ak[x >> 2][x & 3] = dk[x];
-            aq[x >> 2][x & 3] = dq[x];
-        }
-        // R_b, then U_b
-        uint32_t w[4];
-        ldsm4_t(w, tile_at<DV * 2>(s0 + M::v, bb * 16 + vrow, vchunk));
-#pragma unroll
-        for (int n = 0; n < 2; ++n) {
-            const int i = bb * 16 + n * 8 + 2 * t;
-            const float2 be = *reinterpret_cast<const float2*>(&rw.beta[i]), ck = *reinterpret_cast<const float2*>(&rw.ck[i]),
-                         cq = *reinterpret_cast<const float2*>(&rw.cq[i]);
-#pragma unroll
-            for (int half = 0; half < 2; ++half) {
-                const uint32_t v2 = w[2 * n + half];
-                ak[n][2 * half] = be.x * (bf16_lo(v2) * down[half] - ck.x * ak[n][2 * half]);
-                ak[n][2 * half + 1] = be.y * (bf16_hi(v2) * down[half] - ck.y * ak[n][2 * half + 1]);
-                aq[n][2 * half] *= cq.x;
-                aq[n][2 * half + 1] *= cq.y;
-            }
-        }
-#pragma unroll
-        for (int c = 0; c < bb; ++c) {
-            uint32_t wa[4];
-            ldsm4(wa, tile_at<128>(s0 + M::a16, bb * 16 + brow, 2 * c + bch));
-            mma_16816(ak[0], Uf[c], wa[0], wa[1]);
-            mma_16816(ak[1], Uf[c], wa[2], wa[3]);
-        }
-        uint32_t wt[4], r[4];
-        ldsm4(wt, tile_at<128>(s0 + M::a16, bb * 16 + brow, 2 * bb + bch));
-#pragma unroll
-        for (int x = 0; x < 4; ++x) {
-            r[x] = f16x2(ak[x >> 1][2 * (x & 1)], ak[x >> 1][2 * (x & 1) + 1]);
-            watch(flag, r[x]);
-        }
-        float u[2][4] = {};
-        mma_16816(u[0], r, wt[0], wt[1]);
-        mma_16816(u[1], r, wt[2], wt[3]);
-#pragma unroll
-        for (int x = 0; x < 4; ++x) {
-            Uf[bb][x] = f16x2(u[x >> 1][2 * (x & 1)], u[x >> 1][2 * (x & 1) + 1]);
-            watch(flag, Uf[bb][x]);
-        }
-#pragma unroll
-        for (int c = 0; c <= bb; ++c) {
-            uint32_t wp[4];
-            ldsm4(wp, tile_at<128>(s0 + M::p16, bb * 16 + brow, 2 * c + bch));
-            mma_16816(aq[0], Uf[c], wp[0], wp[1]);
-            mma_16816(aq[1], Uf[c], wp[2], wp[3]);
-        }
-        // o over v's place
-#pragma unroll
-        for (int n = 0; n < 2; ++n)
-#pragma unroll
-            for (int half = 0; half < 2; ++half)
-                w[2 * n + half] = bf16x2(aq[n][2 * half] * up[half], aq[n][2 * half + 1] * up[half]);
-        stsm4_t(tile_at<DV * 2>(s0 + M::v, bb * 16 + vrow, vchunk), w);
-    }
-    tc::tc_fence_before();
-    const bool redo = __syncthreads_or(watched(flag));
     if (warp == 1) {
         tc::tc_fence_after();
         if (!ok)  // let the MMAs end before their TMEM goes
@@ -429,25 +455,25 @@ __global__ void __launch_bounds__(2 * DV, 2) gdn_tree_kernel(const __grid_consta
         tc::tmem_dealloc(tmem, M::cols);
     }
     if (!ok) {
-        if (threadIdx.x == 0) dev_fail(status, TSV_DEV_TIMEOUT, b, h);
+        if (threadIdx.x == 0) dev_fail(status, TSV_DEV_TIMEOUT, b, h0);
         return;
     }
-    if (redo) {
-        tree_fp32<DK, DV, NB>(d, anc, layer, b, h, sm);
-        return;
-    }
-    for (int e = threadIdx.x; e < T * CPR; e += kThreads) {
-        const int i = e / CPR, c = e % CPR;
-        *reinterpret_cast<uint4*>(reinterpret_cast<uint16_t*>(d.o[layer]) + ((row0 + i) * d.HV + h) * DV + c * 8) =
-            *reinterpret_cast<const uint4*>(sm + tile_at<DV * 2>(M::v, i, c));
-    }
+    for (int k = 0; k < heads; ++k)
+        if (redo & (1u << k)) tree_fp32<DK, DV, NB>(d, anc, layer, b, h0 + k, sm, rows[k]);
 }
 
 template <int DK, int DV, int NB>
 static void launch_tree_nb(const tsv_gdn_desc& d, const uint64_t* anc, int32_t* status, cudaStream_t stream) {
     constexpr int sm = TreeSmem<DK, DV, NB>::total;
     cudaFuncSetAttribute(gdn_tree_kernel<DK, DV, NB>, cudaFuncAttributeMaxDynamicSharedMemorySize, sm);
-    launch_pdl(gdn_tree_kernel<DK, DV, NB>, (unsigned)((long long)d.n_layers * d.B * d.HV), 2 * DV, sm, stream, d, anc, status);
+    // Value heads per CTA: as many as share a key head (up to kMaxHeads) as long as every SM gets CTAs for two rounds;
+    // fewer, larger CTAs save the staging but leave SMs idle on small batches.
+    const int per = d.HV / d.HK;
+    int heads = 1;
+    for (int x = 2; x <= kMaxHeads; ++x)
+        if (per % x == 0 && (long long)d.n_layers * d.B * d.HV / x >= 4LL * sm_count()) heads = x;
+    launch_pdl(gdn_tree_kernel<DK, DV, NB>, (unsigned)((long long)d.n_layers * d.B * d.HV / heads), 2 * DV, sm, stream, d, anc,
+               heads, status);
 }
 
 template <int DK, int DV>
