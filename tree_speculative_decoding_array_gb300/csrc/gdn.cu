@@ -195,8 +195,12 @@ __global__ void __launch_bounds__(kGdnThreads) gdn_recur_kernel(const __grid_con
                 make_float4(s[r][4 * c], s[r][4 * c + 1], s[r][4 * c + 2], s[r][4 * c + 3]);
 }
 
-// Defined in gdn_tree.cu.
+// Defined in gdn_tree.cu and gdn_scan.cu.
 void launch_gdn_tree(const tsv_gdn_desc& d, const uint64_t* anc, int32_t* status, cudaStream_t stream);
+void launch_gdn_scan(const tsv_gdn_desc& d, const int32_t* cu_len, int max_len, int32_t* status, cudaStream_t stream);
+
+// Sequences of up to this many tokens are advanced token by token, longer ones in chunks.
+constexpr int kRecurMax = 16;
 
 enum GdnCall { kGdnVerify, kGdnCommit, kGdnScan };
 
@@ -277,6 +281,10 @@ extern "C" tsv_status tsv_gdn_scan(const tsv_gdn_desc* d, const int32_t* cu_len,
     if (!cu_len) return fail(TSV_EINVAL, "gdn_scan: cu_len must be non-null");
     if (max_len < 0 || max_len > d->T) return fail(TSV_EINVAL, "gdn_scan: max_len=%d outside [0, T=%d]", max_len, d->T);
     const tsv_gdn_desc x = with_scale(d);
+    if (max_len > kRecurMax) {
+        launch_gdn_scan(x, cu_len, max_len, dev_status, stream);
+        return check_launch("gdn_scan");
+    }
     const unsigned grid = (unsigned)((long long)d->n_layers * d->B * d->HV * (d->DV / kGdnRows));
     const int32_t* none = nullptr;
     if (d->DK == 64) launch_pdl(gdn_recur_kernel<64, false>, grid, kGdnThreads, 0, stream, x, cu_len, max_len, none, none, dev_status);

@@ -1,0 +1,543 @@
+// tsv_gdn_scan over many tokens: the gated delta rule in chunks of 64.
+//
+// A chunk is one triangular system (gdn_tc.cuh) whose rows are consecutive tokens, and the state moves on by
+//     S <- e^{G_n} S + sum_j e^{G_n - G_j} u_j k_j^T        (n: the chunk's last token)
+// One persistent CTA per (layer, sequence, value head) walks its chunks.  Two groups of warps work a chunk apart:
+//   8 preparing warps   stage K, Q, V and the gates of a chunk, take [K; Q] K^T on the tensor cores and build the
+//                       system's matrices; two buffers, so they run up to two chunks ahead.  A chunk's global loads
+//                       are issued while the one before is prepared.
+//   DV / 16 state warps 16 value features each: split the state into fp16 hi + lo pairs (TMEM), S [K; Q]^T on the
+//                       tensor cores (the lo pieces for K only: what reaches o alone is rounded to bf16 anyway), solve
+//                       the system in mma fragments, write u as hi + lo pairs to TMEM, and let the tensor cores add
+//                       their product with K onto the decayed state, which stays in TMEM in fp32.
+// What reaches the state is kept to 2^-22 (fp16 pairs; K's values are exact), what reaches o alone to 2^-12.
+#include <math.h>
+
+#include "gdn_tc.cuh"
+
+namespace tsv {
+
+constexpr int kScanPrep = 8;  // preparing warps
+constexpr int kScanT = 64;    // tokens per chunk
+constexpr int kScanNB = 4;
+
+template <int DK, int DV>
+struct ScanSmem {
+    static constexpr int T = kScanT;
+    // per buffer
+    static constexpr int kq = 0;                    // K rows [64], Q rows [64], DK fp16 each
+    static constexpr int v = kq + 2 * T * DK * 2;   // V rows [64], DV bf16 each; o over them
+    static constexpr int a16 = v + T * DV * 2;      // hi and lo tiles of -A and the diagonal blocks' inverses
+    static constexpr int p16 = a16 + 2 * T * 128;   // P
+    static constexpr int keys = p16 + T * 128;
+    static constexpr int rows = keys + (int)sizeof(GdnKeys);
+    static constexpr int dj = rows + (int)sizeof(GdnRows);  // e^{G_n - G_j} times k_j's factor, then e^{G_n}
+    static constexpr int buffer = (dj + 65 * 4 + 1023) / 1024 * 1024;
+    static constexpr int diag = 2 * buffer;                        // [4][16][kDiag] fp32
+    static constexpr int slow = diag + kScanNB * 16 * kDiag * 4;   // fp32 path: one token's k and q, and k . q
+    static constexpr int bars = slow + (2 * 128 + 4) * 4;
+    static constexpr int total = bars + 16 * 8;
+    // [K; Q] K^T reads 128 rows per 64-feature block: exactly the tile
+    // TMEM columns: the state (fp32), its hi and lo pieces (then u's), S [K; Q]^T, [K; Q] K^T
+    static constexpr int col_s = 0, col_hi = DK, col_lo = col_hi + DK / 2, col_d = col_lo + DK / 2, col_g = col_d + 128;
+    static constexpr int cols = 512;
+    static_assert(col_g + T <= 512, "TMEM");
+};
+
+// Barriers of one CTA.
+struct ScanBars {
+    uint64_t full[2], empty[2], gram, prod, state, ssync, psync, drain_s, drain_p;
+    uint32_t tmem;
+    int abort, bad[2];
+};
+
+template <int DK, int DV>
+__global__ void __launch_bounds__((kScanPrep + DV / 16) * 32, 1)
+    gdn_scan_kernel(const __grid_constant__ tsv_gdn_desc d, const int32_t* __restrict__ cu_len, int max_len, int32_t* status) {
+    griddep_begin();
+    using M = ScanSmem<DK, DV>;
+    constexpr int SW = DV / 16;  // state warps
+    constexpr int KS = DK / 16;
+    constexpr int NB = kScanNB;
+    extern __shared__ __align__(1024) char sm[];
+    ScanBars& br = *reinterpret_cast<ScanBars*>(sm + M::bars);
+    static_assert(sizeof(ScanBars) <= 128, "barriers");
+    volatile int* abort_flag = &br.abort;
+    const uint32_t s0 = tc::smem_u32(sm);
+    int item = blockIdx.x;
+    const int h = item % d.HV;
+    item /= d.HV;
+    const int b = item % d.B, layer = item / d.B;
+    const int hk = h / (d.HV / d.HK);
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int g = lane >> 2, t = lane & 3;
+
+    const int row0 = cu_len[b], row1 = cu_len[b + 1];
+    const int n = row1 - row0;
+    if (row0 < 0 || row1 < row0 || row1 > d.T || n > max_len) {
+        if (h == 0 && layer == 0 && threadIdx.x == 0) dev_fail(status, TSV_DEV_BAD_SEQ_LEN, b, row1);
+        return;
+    }
+    const size_t state0 = ((size_t)b * d.HV + h) * DV * DK;
+    if (n == 0) {  // the state as it was
+        if (d.state_out[layer] != d.state[layer])
+            for (int e = threadIdx.x; e < DV * DK / 4; e += blockDim.x)
+                reinterpret_cast<float4*>(d.state_out[layer] + state0)[e] = reinterpret_cast<const float4*>(d.state[layer] + state0)[e];
+        return;
+    }
+    const int chunks = (n + kScanT - 1) / kScanT;
+
+    if (threadIdx.x == 0) {
+        for (int x = 0; x < 2; ++x) {
+            tc::mbar_init(&br.full[x], kScanPrep);
+            tc::mbar_init(&br.empty[x], SW);
+            br.bad[x] = 0;
+        }
+        tc::mbar_init(&br.gram, 1);
+        tc::mbar_init(&br.prod, 1);
+        tc::mbar_init(&br.state, 1);
+        tc::mbar_init(&br.ssync, SW);
+        tc::mbar_init(&br.psync, kScanPrep);
+        tc::mbar_init(&br.drain_s, 1);
+        tc::mbar_init(&br.drain_p, 1);
+        br.abort = 0;
+        tc::fence_mbar_init();
+    }
+    if (warp == 1) {
+        tc::tmem_alloc(&br.tmem, M::cols);
+        tc::tmem_relinquish();
+    }
+    tc::tc_fence_before();
+    __syncthreads();
+    tc::tc_fence_after();
+    const uint32_t tmem = br.tmem;
+
+    if (warp >= SW) {
+        // ------------------------------------------------------------ preparing warps
+        const int pw = warp - SW, pt = threadIdx.x - SW * 32;
+        constexpr int PT = kScanPrep * 32;
+        constexpr int LPR = DK / 8, CPR = DV / 8;
+        constexpr int KQ = 2 * kScanT * LPR / PT, VC = kScanT * CPR / PT;
+        const int chunk = pt % LPR;
+        uint4 kq[KQ], vv[VC];
+        float gi[2] = {0.f, 0.f}, bi[2] = {0.f, 0.f};
+        auto fetch = [&](int c) {
+            const int t0 = c * kScanT;
+            const uint4 zero = make_uint4(0, 0, 0, 0);
+#pragma unroll
+            for (int x = 0; x < KQ; ++x) {
+                const int r = pt / LPR + x * (PT / LPR), i = t0 + (r & 63);
+                const uint16_t* src = reinterpret_cast<const uint16_t*>(r >= kScanT ? d.q[layer] : d.k[layer]);
+                kq[x] = i < n ? *reinterpret_cast<const uint4*>(src + ((size_t)(row0 + i) * d.HK + hk) * DK + chunk * 8) : zero;
+            }
+#pragma unroll
+            for (int x = 0; x < VC; ++x) {
+                const int e = pt + x * PT, i = t0 + e / CPR;
+                vv[x] = i < n ? *reinterpret_cast<const uint4*>(reinterpret_cast<const uint16_t*>(d.v[layer]) +
+                                                                 ((size_t)(row0 + i) * d.HV + h) * DV + e % CPR * 8) : zero;
+            }
+            if (pw == 0) {
+#pragma unroll
+                for (int x = 0; x < 2; ++x) {
+                    const int i = t0 + 2 * lane + x;
+                    gi[x] = i < n ? d.g[layer][(size_t)(row0 + i) * d.HV + h] : 0.f;
+                    bi[x] = i < n ? d.beta[layer][(size_t)(row0 + i) * d.HV + h] : 0.f;
+                }
+            }
+        };
+        uint32_t ps = 0;  // phases of psync
+        auto sync = [&]() -> bool {
+            __syncwarp();
+            tc::mbar_arrive_one(&br.psync);
+            return __all_sync(0xFFFFFFFFu, tc::mbar_wait(&br.psync, ps++ & 1, abort_flag));
+        };
+        fetch(0);
+        bool ok = true;
+        for (int c = 0; c < chunks; ++c) {
+            const int buf = c & 1;
+            char* bs = sm + buf * M::buffer;
+            const uint32_t bs32 = s0 + buf * M::buffer;
+            GdnKeys& ky = *reinterpret_cast<GdnKeys*>(bs + M::keys);
+            GdnRows& rw = *reinterpret_cast<GdnRows*>(bs + M::rows);
+            float* dj = reinterpret_cast<float*>(bs + M::dj);
+            if (c >= 2 && !__all_sync(0xFFFFFFFFu, tc::mbar_wait(&br.empty[buf], ((c >> 1) - 1) & 1, abort_flag))) {
+                ok = false;
+                break;
+            }
+            if (pt == 0) br.bad[buf] = 0;  // read by the state warps before they gave the buffer back; set again after sync()
+            uint32_t flag = 0;
+#pragma unroll
+            for (int x = 0; x < KQ; ++x) {
+                const int r = pt / LPR + x * (PT / LPR);
+                float ss, up;
+                *reinterpret_cast<uint4*>(bs + kq_at<2 * kScanT>(M::kq, r, chunk)) = stage_chunk<DK>(kq[x], ss, up, flag);
+                if (chunk == 0) {
+                    (r >= kScanT ? ky.fq : ky.fk)[r & 63] = up;
+                    (r >= kScanT ? ky.sq : ky.sk)[r & 63] = ss;
+                }
+            }
+#pragma unroll
+            for (int x = 0; x < VC; ++x) {
+                const int e = pt + x * PT;
+                *reinterpret_cast<uint4*>(bs + tile_at<DV * 2>(M::v, e / CPR, e % CPR)) = vv[x];
+            }
+            if (pw == 0) {  // G: tokens 2 lane, 2 lane + 1; inclusive scan over the lanes
+                Pair a = log2_decay(gi[0]), s = add(a, log2_decay(gi[1])), run = s;
+#pragma unroll
+                for (int o = 1; o < 32; o <<= 1) {
+                    Pair y;
+                    y.hi = __shfl_up_sync(0xFFFFFFFFu, run.hi, o);
+                    y.lo = __shfl_up_sync(0xFFFFFFFFu, run.lo, o);
+                    if (lane >= o) run = add(run, y);
+                }
+                Pair before;
+                before.hi = __shfl_up_sync(0xFFFFFFFFu, run.hi, 1);
+                before.lo = __shfl_up_sync(0xFFFFFFFFu, run.lo, 1);
+                if (lane > 0) a = add(a, before);
+                *reinterpret_cast<float2*>(&rw.g_hi[2 * lane]) = make_float2(a.hi, run.hi);
+                *reinterpret_cast<float2*>(&rw.g_lo[2 * lane]) = make_float2(a.lo, run.lo);
+                *reinterpret_cast<float2*>(&rw.beta[2 * lane]) = make_float2(bi[0], bi[1]);
+                ky.before[2 * lane] = (1ull << (2 * lane)) - 1ull;
+                ky.before[2 * lane + 1] = (1ull << (2 * lane + 1)) - 1ull;
+            }
+            if (c + 1 < chunks) fetch(c + 1);
+            tc::fence_proxy_async_smem();
+            tc::tc_fence_before();
+            if (!sync()) {
+                ok = false;
+                break;
+            }
+            tc::tc_fence_after();
+            if (pt == 0) {  // [K; Q] K^T
+                const uint32_t id = tc::idesc_f16(false, false, false, 128, kScanT);
+                const uint64_t desc = tc::sdesc_sw128(bs32 + M::kq, 16, 1024);
+#pragma unroll
+                for (int ks = 0; ks < KS; ++ks) {
+                    const uint64_t at = tc::sdesc_add(desc, (ks >> 2) * 2 * kScanT * 128 + (ks & 3) * 32);
+                    tc::mma_f16(tmem + M::col_g, at, at, id, ks > 0);
+                }
+                tc::mma_commit(&br.gram);
+            }
+            if (pt < 2 * kScanT) {
+                const int i = pt & 63;
+                const bool q = pt >= kScanT;
+                float* f = q ? ky.fq : ky.fk;
+                float x = f[i] * (q ? d.scale : 1.f);
+                if (d.norm_eps > 0.f) x /= sqrtf((q ? ky.sq : ky.sk)[i] + d.norm_eps);
+                f[i] = x;
+                const float gh = rw.g_hi[i], gl = rw.g_lo[i];
+                (q ? rw.cq : rw.ck)[i] = tc::ex2_approx(gh + gl) * x;
+                if (!q) dj[i] = tc::ex2_approx((rw.g_hi[63] - gh) + (rw.g_lo[63] - gl)) * x;
+                else if (i == 63) dj[64] = tc::ex2_approx(gh + gl);
+            }
+            __syncwarp();
+            if (!sync()) {
+                ok = false;
+                break;
+            }
+            if (!__all_sync(0xFFFFFFFFu, tc::mbar_wait(&br.gram, c & 1, abort_flag))) {
+                ok = false;
+                break;
+            }
+            tc::tc_fence_after();
+            const int x = 2 * (pw & 3) + (pw >> 2);  // 16-row block x of [K; Q] sits in lanes 16 x ..
+            const bool q = x >= NB;
+            const int bb = q ? x - NB : x;
+            float* diag = reinterpret_cast<float*>(sm + M::diag) + bb * 16 * kDiag;
+            block_matrices<NB, 2>(q, bb, tmem + M::col_g + ((uint32_t)(16 * x) << 16), bs + M::a16, bs + M::p16, diag, ky, rw, flag, lane);
+            if (!q) {
+                __syncwarp();
+                block_inverse<NB, 2>(bb, bs + M::a16, diag, flag, lane);
+            }
+            if (watched(flag)) br.bad[buf] = 1;
+            tc::tc_fence_before();
+            __syncwarp();
+            tc::mbar_arrive_one(&br.full[buf]);
+        }
+        if (!ok && pt == 0) {  // let this thread's MMAs end
+            tc::mma_commit(&br.drain_p);
+            tc::mbar_drain(&br.drain_p, 0);
+        }
+    } else {
+        // ------------------------------------------------------------ state warps
+        const int lane0 = DV == 128 ? (warp & 3) * 32 + (warp >> 2) * 16 : warp * 32;  // TMEM lanes (16 of them)
+        const int fb = DV == 128 ? lane0 : warp * 16;                                  // value features
+        const uint32_t la = tmem + ((uint32_t)lane0 << 16);
+        const int vrow = ((lane >> 4) << 3) + (lane & 7), vchunk = fb / 8 + ((lane >> 3) & 1);
+        uint32_t ss = 0;  // phases of ssync
+        auto sync = [&]() -> bool {
+            __syncwarp();
+            tc::mbar_arrive_one(&br.ssync);
+            return __all_sync(0xFFFFFFFFu, tc::mbar_wait(&br.ssync, ss++ & 1, abort_flag));
+        };
+        // 64 columns of the state at a time: r[4 n + 2 half + e] = S[fb + g + 8 half][64 x + 8 n + 2 t + e]
+        float r[32];
+        const float* S = d.state[layer] + state0 + (size_t)(fb + g) * DK + 2 * t;
+#pragma unroll 1
+        for (int x = 0; x < DK / 64; ++x) {
+#pragma unroll
+            for (int nn = 0; nn < 8; ++nn)
+#pragma unroll
+                for (int half = 0; half < 2; ++half) {
+                    const float2 y = __ldcs(reinterpret_cast<const float2*>(S + half * 8 * DK + 64 * x + 8 * nn));
+                    r[4 * nn + 2 * half] = y.x;
+                    r[4 * nn + 2 * half + 1] = y.y;
+                }
+            tc::tmem_st_frag8f(la + M::col_s + 64 * x, r);
+        }
+        tc::tmem_wait_st();
+        float up[2] = {1.f, 1.f};  // the state is what TMEM holds times up
+        bool ok = true;
+        for (int c = 0; c < chunks; ++c) {
+            const int buf = c & 1;
+            char* bs = sm + buf * M::buffer;
+            const uint32_t bs32 = s0 + buf * M::buffer;
+            const GdnRows& rw = *reinterpret_cast<const GdnRows*>(bs + M::rows);
+            const float* dj = reinterpret_cast<const float*>(bs + M::dj);
+            const int nt = min(kScanT, n - c * kScanT);
+            uint32_t flag = 0;
+            if (!__all_sync(0xFFFFFFFFu, tc::mbar_wait(&br.full[buf], (c >> 1) & 1, abort_flag))) { ok = false; break; }
+            if (c > 0) {  // the state of the chunk before, whose buffer is then free
+                if (!__all_sync(0xFFFFFFFFu, tc::mbar_wait(&br.state, (c - 1) & 1, abort_flag))) { ok = false; break; }
+                __syncwarp();
+                tc::mbar_arrive_one(&br.empty[buf ^ 1]);
+            }
+            tc::tc_fence_after();
+            // each feature's power-of-two scale from the largest of its state row and v; the state's hi and lo pieces
+            float mx[2] = {0.f, 0.f}, sx[2] = {0.f, 0.f}, down[2], sc[2];
+#pragma unroll
+            for (int bb = 0; bb < NB; ++bb) {
+                uint32_t w[4];
+                ldsm4_t(w, tile_at<DV * 2>(bs32 + M::v, bb * 16 + vrow, vchunk));
+#pragma unroll
+                for (int x = 0; x < 4; ++x)
+                    mx[x & 1] = fmaxf(mx[x & 1], fmaxf(fabsf(bf16_lo(w[x])), fabsf(bf16_hi(w[x]))));
+            }
+            float S2[DK / 2];  // this thread's part of the state
+#pragma unroll
+            for (int x = 0; x < DK / 64; ++x) tc::tmem_ld_frag8(la + M::col_s + 64 * x, S2 + 32 * x);
+            tc::tmem_wait_ld();
+#pragma unroll
+            for (int x = 0; x < DK / 2; x += 4)
+#pragma unroll
+                for (int half = 0; half < 2; ++half)
+                    sx[half] = fmaxf(sx[half], fmaxf(fabsf(S2[x + 2 * half]), fabsf(S2[x + 2 * half + 1])));
+#pragma unroll
+            for (int half = 0; half < 2; ++half) {
+                float m = fmaxf(8.f * sx[half] * up[half], mx[half]), up_new;
+                m = fmaxf(m, __shfl_xor_sync(0xFFFFFFFFu, m, 1));
+                m = fmaxf(m, __shfl_xor_sync(0xFFFFFFFFu, m, 2));
+                pow2_scale(m, down[half], up_new);
+                sc[half] = up[half] * down[half];
+                up[half] = up_new;
+            }
+#pragma unroll
+            for (int x = 0; x < DK / 64; ++x) {
+                uint32_t hi[16], lo[16];
+#pragma unroll
+                for (int y = 0; y < 16; ++y) {  // y = 2 n + half
+                    const float2 z = mul2(make_float2(S2[32 * x + 2 * y], S2[32 * x + 2 * y + 1]), make_float2(sc[y & 1], sc[y & 1]));
+                    split2(z.x, z.y, hi[y], lo[y]);
+                    watch(flag, hi[y]);
+                }
+                tc::tmem_st_frag8(la + M::col_hi + 32 * x, hi);
+                tc::tmem_st_frag8(la + M::col_lo + 32 * x, lo);
+            }
+            tc::tmem_wait_st();
+            tc::tc_fence_before();
+            if (!sync()) { ok = false; break; }
+            const uint64_t desc = tc::sdesc_sw128(bs32 + M::kq, 16, 1024);
+            if (threadIdx.x == 0) {  // S [K; Q]^T
+                tc::tc_fence_after();
+                const uint32_t id = tc::idesc_f16(false, false, false, 128, 2 * kScanT), idk = tc::idesc_f16(false, false, false, 128, kScanT);
+#pragma unroll
+                for (int ks = 0; ks < KS; ++ks)
+                    tc::mma_f16_ts(tmem + M::col_d, tmem + M::col_hi + ks * 8,
+                                   tc::sdesc_add(desc, (ks >> 2) * 2 * kScanT * 128 + (ks & 3) * 32), id, ks > 0);
+#pragma unroll
+                for (int ks = 0; ks < KS; ++ks)
+                    tc::mma_f16_ts(tmem + M::col_d, tmem + M::col_lo + ks * 8,
+                                   tc::sdesc_add(desc, (ks >> 2) * 2 * kScanT * 128 + (ks & 3) * 32), idk, 1);
+                tc::mma_commit(&br.prod);
+            }
+            __syncwarp();
+            if (!__all_sync(0xFFFFFFFFu, tc::mbar_wait(&br.prod, c & 1, abort_flag))) { ok = false; break; }
+            tc::tc_fence_after();
+
+            uint32_t Uf[NB][2][4];
+#pragma unroll
+            for (int bb = 0; bb < NB; ++bb) {
+                float x8[8], y8[8], ak[2][4], aq[2][4], u[2][4];
+                tc::tmem_ld_frag2(la + M::col_d + bb * 16, x8);
+                tc::tmem_ld_frag2(la + M::col_d + kScanT + bb * 16, y8);
+                tc::tmem_wait_ld();
+#pragma unroll
+                for (int x = 0; x < 8; ++x) {
+                    ak[x >> 2][x & 3] = x8[x];
+                    aq[x >> 2][x & 3] = y8[x];
+                }
+                uint32_t w[4];
+                ldsm4_t(w, tile_at<DV * 2>(bs32 + M::v, bb * 16 + vrow, vchunk));
+                block_rhs(bb, ak, aq, w, down, rw, t);
+                block_solve<NB, 2>(bb, ak, aq, Uf, u, bs32 + M::a16, bs32 + M::p16, flag, lane);
+                // o over v's place; u for the state, over the state's pieces
+                uint32_t hi[4], lo[4];
+#pragma unroll
+                for (int nn = 0; nn < 2; ++nn) {
+                    const float2 z = *reinterpret_cast<const float2*>(&dj[bb * 16 + nn * 8 + 2 * t]);
+#pragma unroll
+                    for (int half = 0; half < 2; ++half) {
+                        w[2 * nn + half] = bf16x2(aq[nn][2 * half] * up[half], aq[nn][2 * half + 1] * up[half]);
+                        split2(u[nn][2 * half] * z.x, u[nn][2 * half + 1] * z.y, hi[2 * nn + half], lo[2 * nn + half]);
+                        watch(flag, hi[2 * nn + half]);
+                    }
+                }
+                stsm4_t(tile_at<DV * 2>(bs32 + M::v, bb * 16 + vrow, vchunk), w);
+                tc::tmem_st_frag2(la + M::col_hi + bb * 8, hi);
+                tc::tmem_st_frag2(la + M::col_lo + bb * 8, lo);
+            }
+            if (watched(flag)) br.bad[buf] = 1;
+            tc::tmem_wait_st();
+            if (!sync()) { ok = false; break; }
+            const bool bad = *reinterpret_cast<volatile int*>(&br.bad[buf]) != 0;
+#pragma unroll
+            for (int x = 0; x < DK / 64; ++x) tc::tmem_ld_frag8(la + M::col_s + 64 * x, S2 + 32 * x);
+            tc::tmem_wait_ld();
+            if (!bad) {
+                const float e = dj[64];
+                const float2 f[2] = {make_float2(sc[0] * e, sc[0] * e), make_float2(sc[1] * e, sc[1] * e)};
+#pragma unroll
+                for (int x = 0; x < DK / 2; x += 2) {
+                    const float2 z = mul2(make_float2(S2[x], S2[x + 1]), f[(x >> 1) & 1]);
+                    S2[x] = z.x;
+                    S2[x + 1] = z.y;
+                }
+            } else {
+                // fp32, token by token: an operand left fp16's range.  Not finite inputs then reach what the recurrence
+                // lets them reach: later tokens, and with v only their own feature.
+                float* tk = reinterpret_cast<float*>(sm + M::slow);
+                const float un[2] = {sc[0] * up[0], sc[1] * up[1]};  // what TMEM holds times the scale before this chunk's
+#pragma unroll
+                for (int x = 0; x < DK / 2; ++x) S2[x] *= un[(x >> 1) & 1];
+                for (int i = 0; i < nt && ok; ++i) {
+                    const size_t row = (size_t)row0 + c * kScanT + i;
+                    if (warp == 0) {
+                        float kx[DK / 32], qx[DK / 32], kq = 0.f;
+                        unit_row<DK>(reinterpret_cast<const uint16_t*>(d.k[layer]) + (row * d.HK + hk) * DK, d.norm_eps, 1.f, lane, kx);
+                        unit_row<DK>(reinterpret_cast<const uint16_t*>(d.q[layer]) + (row * d.HK + hk) * DK, d.norm_eps, d.scale, lane, qx);
+#pragma unroll
+                        for (int e = 0; e < DK / 32; ++e) {
+                            tk[lane + 32 * e] = kx[e];
+                            tk[128 + lane + 32 * e] = qx[e];
+                            kq = fmaf(kx[e], qx[e], kq);
+                        }
+#pragma unroll
+                        for (int o = 16; o > 0; o >>= 1) kq += __shfl_xor_sync(0xFFFFFFFFu, kq, o);
+                        if (lane == 0) tk[256] = kq;
+                    }
+                    if (!sync()) { ok = false; break; }
+                    const float a = expf(d.g[layer][row * d.HV + h]), be = d.beta[layer][row * d.HV + h];
+                    float sk[2] = {0.f, 0.f}, sq[2] = {0.f, 0.f};
+#pragma unroll
+                    for (int x = 0; x < DK / 2; ++x) {
+                        const int e = (x >> 5) * 64 + ((x & 31) >> 2) * 8 + 2 * t + (x & 1);
+                        sk[(x >> 1) & 1] = fmaf(S2[x], tk[e], sk[(x >> 1) & 1]);
+                        sq[(x >> 1) & 1] = fmaf(S2[x], tk[128 + e], sq[(x >> 1) & 1]);
+                    }
+#pragma unroll
+                    for (int half = 0; half < 2; ++half) {
+#pragma unroll
+                        for (int o = 1; o < 4; o <<= 1) {
+                            sk[half] += __shfl_xor_sync(0xFFFFFFFFu, sk[half], o);
+                            sq[half] += __shfl_xor_sync(0xFFFFFFFFu, sq[half], o);
+                        }
+                        const size_t at = (row * d.HV + h) * DV + fb + g + 8 * half;
+                        const float u = be * (bf16_bits_to_f32(reinterpret_cast<const uint16_t*>(d.v[layer])[at]) - a * sk[half]);
+                        if (t == 0) reinterpret_cast<__nv_bfloat16*>(d.o[layer])[at] = __float2bfloat16(fmaf(a, sq[half], u * tk[256]));
+                        sk[half] = u;
+                    }
+#pragma unroll
+                    for (int x = 0; x < DK / 2; ++x) {
+                        const int e = (x >> 5) * 64 + ((x & 31) >> 2) * 8 + 2 * t + (x & 1);
+                        S2[x] = fmaf(sk[(x >> 1) & 1], tk[e], a * S2[x]);
+                    }
+                    if (!sync()) { ok = false; break; }
+                }
+                if (!ok) break;
+                up[0] = up[1] = 1.f;
+            }
+#pragma unroll
+            for (int x = 0; x < DK / 64; ++x) tc::tmem_st_frag8f(la + M::col_s + 64 * x, S2 + 32 * x);
+            tc::tmem_wait_st();
+            tc::tc_fence_before();
+            if (!sync()) { ok = false; break; }
+            if (threadIdx.x == 0) {  // S += U'^T K
+                tc::tc_fence_after();
+                if (!bad) {
+                    const uint32_t id = tc::idesc_f16(false, false, true, 128, DK);
+                    const uint64_t kd = tc::sdesc_sw128(bs32 + M::kq, 2 * kScanT * 128, 1024);
+#pragma unroll
+                    for (int ks = 0; ks < kScanT / 16; ++ks)
+                        tc::mma_f16_ts(tmem + M::col_s, tmem + M::col_hi + ks * 8, tc::sdesc_add(kd, ks * 2048), id, 1);
+#pragma unroll
+                    for (int ks = 0; ks < kScanT / 16; ++ks)
+                        tc::mma_f16_ts(tmem + M::col_s, tmem + M::col_lo + ks * 8, tc::sdesc_add(kd, ks * 2048), id, 1);
+                }
+                tc::mma_commit(&br.state);
+            }
+            __syncwarp();
+            if (!bad) {  // o, gathered from every warp's features
+                constexpr int CPR = DV / 8;
+                for (int e = threadIdx.x; e < nt * CPR; e += SW * 32) {
+                    const int i = e / CPR, cc = e % CPR;
+                    *reinterpret_cast<uint4*>(reinterpret_cast<uint16_t*>(d.o[layer]) +
+                                              ((size_t)(row0 + c * kScanT + i) * d.HV + h) * DV + cc * 8) =
+                        *reinterpret_cast<const uint4*>(bs + tile_at<DV * 2>(M::v, i, cc));
+                }
+            }
+        }
+        if (ok) ok = __all_sync(0xFFFFFFFFu, tc::mbar_wait(&br.state, (chunks - 1) & 1, abort_flag));
+        if (ok) {
+            tc::tc_fence_after();
+            float* out = d.state_out[layer] + state0 + (size_t)(fb + g) * DK + 2 * t;
+#pragma unroll 1
+            for (int x = 0; x < DK / 64; ++x) {
+                tc::tmem_ld_frag8(la + M::col_s + 64 * x, r);
+                tc::tmem_wait_ld();
+#pragma unroll
+                for (int nn = 0; nn < 8; ++nn)
+#pragma unroll
+                    for (int half = 0; half < 2; ++half)
+                        *reinterpret_cast<float2*>(out + half * 8 * DK + 64 * x + 8 * nn) =
+                            make_float2(r[4 * nn + 2 * half] * up[half], r[4 * nn + 2 * half + 1] * up[half]);
+            }
+        } else if (threadIdx.x == 0) {  // let this thread's MMAs end
+            tc::mma_commit(&br.drain_s);
+            tc::mbar_drain(&br.drain_s, 0);
+        }
+    }
+    tc::tc_fence_before();
+    __syncthreads();
+    if (*abort_flag && threadIdx.x == 0) dev_fail(status, TSV_DEV_TIMEOUT, b, h);
+    if (warp == 1) {
+        tc::tc_fence_after();
+        tc::tmem_dealloc(tmem, M::cols);
+    }
+}
+
+template <int DK, int DV>
+static void launch_scan_dims(const tsv_gdn_desc& d, const int32_t* cu_len, int max_len, int32_t* status, cudaStream_t stream) {
+    constexpr int sm = ScanSmem<DK, DV>::total;
+    cudaFuncSetAttribute(gdn_scan_kernel<DK, DV>, cudaFuncAttributeMaxDynamicSharedMemorySize, sm);
+    launch_pdl(gdn_scan_kernel<DK, DV>, (unsigned)((long long)d.n_layers * d.B * d.HV), (kScanPrep + DV / 16) * 32, sm, stream, d,
+               cu_len, max_len, status);
+}
+
+void launch_gdn_scan(const tsv_gdn_desc& d, const int32_t* cu_len, int max_len, int32_t* status, cudaStream_t stream) {
+    if (d.DK == 64 && d.DV == 64) launch_scan_dims<64, 64>(d, cu_len, max_len, status, stream);
+    else if (d.DK == 64) launch_scan_dims<64, 128>(d, cu_len, max_len, status, stream);
+    else if (d.DV == 64) launch_scan_dims<128, 64>(d, cu_len, max_len, status, stream);
+    else launch_scan_dims<128, 128>(d, cu_len, max_len, status, stream);
+}
+
+}  // namespace tsv

@@ -270,4 +270,102 @@ __device__ __forceinline__ void block_inverse(int b, char* a16, const float* dia
     }
 }
 
+// Scaled sums of one block and value feature pair in mma fragments (features g, g + 8; rows 8 n + 2 t, + 1):
+// in, ak = S k_i and aq = S q_i; out, ak = R_b (before the blocks ahead of b) and aq = e^{G_i} S q_i.
+__device__ __forceinline__ void block_rhs(int bb, float (&ak)[2][4], float (&aq)[2][4], const uint32_t (&v)[4], const float (&down)[2],
+                                          const GdnRows& rw, int t) {
+#pragma unroll
+    for (int n = 0; n < 2; ++n) {
+        const int i = bb * 16 + n * 8 + 2 * t;
+        const float2 be = *reinterpret_cast<const float2*>(&rw.beta[i]), ck = *reinterpret_cast<const float2*>(&rw.ck[i]),
+                     cq = *reinterpret_cast<const float2*>(&rw.cq[i]);
+#pragma unroll
+        for (int half = 0; half < 2; ++half) {
+            const uint32_t v2 = v[2 * n + half];
+            ak[n][2 * half] = be.x * (bf16_lo(v2) * down[half] - ck.x * ak[n][2 * half]);
+            ak[n][2 * half + 1] = be.y * (bf16_hi(v2) * down[half] - ck.y * ak[n][2 * half + 1]);
+            aq[n][2 * half] *= cq.x;
+            aq[n][2 * half + 1] *= cq.y;
+        }
+    }
+}
+
+// R_b -> U_b (kept as fragments in Uf, fp32 in u) and o_b (in aq).  a16, p16: shared addresses of the tiles.
+template <int NB, int PIECES>
+__device__ __forceinline__ void block_solve(int bb, float (&ak)[2][4], float (&aq)[2][4], uint32_t (&Uf)[NB][PIECES][4],
+                                            float (&u)[2][4], uint32_t a16, uint32_t p16, uint32_t& flag, int lane) {
+    const int brow = ((lane >> 4) << 3) + (lane & 7), bch = (lane >> 3) & 1;
+    constexpr int kLo = 16 * NB * 128;  // the lo pieces' tile
+    uint32_t w[4], w2[4];
+#pragma unroll
+    for (int c = 0; c < NB; ++c) {
+        if (c >= bb) break;
+        ldsm4(w, tile_at<128>(a16, bb * 16 + brow, 2 * c + bch));
+        mma_16816(ak[0], Uf[c][0], w[0], w[1]);
+        mma_16816(ak[1], Uf[c][0], w[2], w[3]);
+        if constexpr (PIECES == 2) {
+            ldsm4(w2, tile_at<128>(a16 + kLo, bb * 16 + brow, 2 * c + bch));
+            mma_16816(ak[0], Uf[c][1], w[0], w[1]);
+            mma_16816(ak[1], Uf[c][1], w[2], w[3]);
+            mma_16816(ak[0], Uf[c][0], w2[0], w2[1]);
+            mma_16816(ak[1], Uf[c][0], w2[2], w2[3]);
+        }
+    }
+    uint32_t r[PIECES][4];
+#pragma unroll
+    for (int x = 0; x < 4; ++x) {
+        const float a = ak[x >> 1][2 * (x & 1)], b = ak[x >> 1][2 * (x & 1) + 1];
+        if constexpr (PIECES == 2) split2(a, b, r[0][x], r[1][x]);
+        else r[0][x] = f16x2(a, b);
+        watch(flag, r[0][x]);
+    }
+#pragma unroll
+    for (int n = 0; n < 2; ++n)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) u[n][e] = 0.f;
+    ldsm4(w, tile_at<128>(a16, bb * 16 + brow, 2 * bb + bch));
+    mma_16816(u[0], r[0], w[0], w[1]);
+    mma_16816(u[1], r[0], w[2], w[3]);
+    if constexpr (PIECES == 2) {
+        ldsm4(w2, tile_at<128>(a16 + kLo, bb * 16 + brow, 2 * bb + bch));
+        mma_16816(u[0], r[1], w[0], w[1]);
+        mma_16816(u[1], r[1], w[2], w[3]);
+        mma_16816(u[0], r[0], w2[0], w2[1]);
+        mma_16816(u[1], r[0], w2[2], w2[3]);
+    }
+#pragma unroll
+    for (int x = 0; x < 4; ++x) {
+        const float a = u[x >> 1][2 * (x & 1)], b = u[x >> 1][2 * (x & 1) + 1];
+        if constexpr (PIECES == 2) split2(a, b, Uf[bb][0][x], Uf[bb][1][x]);
+        else Uf[bb][0][x] = f16x2(a, b);
+        watch(flag, Uf[bb][0][x]);
+    }
+#pragma unroll
+    for (int c = 0; c < NB; ++c) {
+        if (c > bb) break;
+        ldsm4(w, tile_at<128>(p16, bb * 16 + brow, 2 * c + bch));
+        mma_16816(aq[0], Uf[c][0], w[0], w[1]);
+        mma_16816(aq[1], Uf[c][0], w[2], w[3]);
+    }
+}
+
+// One bf16 row of DK features, read by a whole warp, normalised: this lane's values of features lane + 32 e.
+template <int DK>
+__device__ __forceinline__ void unit_row(const uint16_t* src, float norm_eps, float scale, int lane, float (&x)[DK / 32]) {
+    float ss = 0.f;
+#pragma unroll
+    for (int e = 0; e < DK / 32; ++e) {
+        x[e] = bf16_bits_to_f32(src[lane + 32 * e]);
+        ss = fmaf(x[e], x[e], ss);
+    }
+    float f = scale;
+    if (norm_eps > 0.f) {
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) ss += __shfl_xor_sync(0xFFFFFFFFu, ss, o);
+        f = scale / sqrtf(ss + norm_eps);
+    }
+#pragma unroll
+    for (int e = 0; e < DK / 32; ++e) x[e] *= f;
+}
+
 }  // namespace tsv

@@ -38,25 +38,6 @@ struct TreeSmem {
     static_assert(T * DV * 4 <= a16 - v && 2 * DK * 4 <= T * 128 && 2 * 64 * 4 <= T * 128, "fp32 path does not fit");
 };
 
-// One bf16 row of DK features, read by a whole warp, normalised: this lane's DK / 32 values.
-template <int DK>
-__device__ __forceinline__ void unit_row(const uint16_t* src, float norm_eps, float scale, int lane, float (&x)[DK / 32]) {
-    float ss = 0.f;
-#pragma unroll
-    for (int e = 0; e < DK / 32; ++e) {
-        x[e] = bf16_bits_to_f32(src[lane + 32 * e]);
-        ss = fmaf(x[e], x[e], ss);
-    }
-    float f = scale;
-    if (norm_eps > 0.f) {
-#pragma unroll
-        for (int o = 16; o > 0; o >>= 1) ss += __shfl_xor_sync(0xFFFFFFFFu, ss, o);
-        f = scale / sqrtf(ss + norm_eps);
-    }
-#pragma unroll
-    for (int e = 0; e < DK / 32; ++e) x[e] *= f;
-}
-
 // The whole tree of one head in fp32, node by node: taken when an operand left fp16's range (an infinity or a NaN in
 // the inputs, keys that are not of unit length with large writes).  Only a node's ancestors are ever read, so what is
 // not finite stays with its node and the node's descendants.  Thread = value feature.
@@ -266,7 +247,6 @@ __global__ void __launch_bounds__(2 * DV, 2) gdn_tree_kernel(const __grid_consta
 
     const uint64_t kq_desc = tc::sdesc_sw128(s0 + M::kq, 16, 1024);
     const int vrow = ((lane >> 4) << 3) + (lane & 7), vchunk = fb / 8 + ((lane >> 3) & 1);
-    const int brow = ((lane >> 4) << 3) + (lane & 7), bch = (lane >> 3) & 1;
     float* diag = reinterpret_cast<float*>(sm + M::diag);
     uint32_t tmem = 0, redo = 0;
     bool ok = true;
@@ -369,7 +349,7 @@ __global__ void __launch_bounds__(2 * DV, 2) gdn_tree_kernel(const __grid_consta
         tc::tc_fence_after();
         if (!ok) break;
 
-        uint32_t Uf[NB][4];
+        uint32_t Uf[NB][1][4];
 #pragma unroll
         for (int bb = 0; bb < NB; ++bb) {
             float dk[8], dq[8], ak[2][4], aq[2][4];  // this block's columns of S K^T and S Q^T
@@ -381,52 +361,11 @@ __global__ void __launch_bounds__(2 * DV, 2) gdn_tree_kernel(const __grid_consta
                 ak[x >> 2][x & 3] = dk[x];
                 aq[x >> 2][x & 3] = dq[x];
             }
-            // R_b, then U_b
             uint32_t w[4];
+            float u[2][4];
             ldsm4_t(w, tile_at<DV * 2>(s0 + vt, bb * 16 + vrow, vchunk));
-#pragma unroll
-            for (int n = 0; n < 2; ++n) {
-                const int i = bb * 16 + n * 8 + 2 * t;
-                const float2 be = *reinterpret_cast<const float2*>(&rw.beta[i]), ck = *reinterpret_cast<const float2*>(&rw.ck[i]),
-                             cq = *reinterpret_cast<const float2*>(&rw.cq[i]);
-#pragma unroll
-                for (int half = 0; half < 2; ++half) {
-                    const uint32_t v2 = w[2 * n + half];
-                    ak[n][2 * half] = be.x * (bf16_lo(v2) * down[half] - ck.x * ak[n][2 * half]);
-                    ak[n][2 * half + 1] = be.y * (bf16_hi(v2) * down[half] - ck.y * ak[n][2 * half + 1]);
-                    aq[n][2 * half] *= cq.x;
-                    aq[n][2 * half + 1] *= cq.y;
-                }
-            }
-#pragma unroll
-            for (int c = 0; c < bb; ++c) {
-                uint32_t wa[4];
-                ldsm4(wa, tile_at<128>(s0 + M::a16, bb * 16 + brow, 2 * c + bch));
-                mma_16816(ak[0], Uf[c], wa[0], wa[1]);
-                mma_16816(ak[1], Uf[c], wa[2], wa[3]);
-            }
-            uint32_t wt[4], r[4];
-            ldsm4(wt, tile_at<128>(s0 + M::a16, bb * 16 + brow, 2 * bb + bch));
-#pragma unroll
-            for (int x = 0; x < 4; ++x) {
-                r[x] = f16x2(ak[x >> 1][2 * (x & 1)], ak[x >> 1][2 * (x & 1) + 1]);
-                watch(flag, r[x]);
-            }
-            float u[2][4] = {};
-            mma_16816(u[0], r, wt[0], wt[1]);
-            mma_16816(u[1], r, wt[2], wt[3]);
-#pragma unroll
-            for (int x = 0; x < 4; ++x) {
-                Uf[bb][x] = f16x2(u[x >> 1][2 * (x & 1)], u[x >> 1][2 * (x & 1) + 1]);
-                watch(flag, Uf[bb][x]);
-            }
-#pragma unroll
-            for (int c = 0; c <= bb; ++c) {
-                uint32_t wp[4];
-                ldsm4(wp, tile_at<128>(s0 + M::p16, bb * 16 + brow, 2 * c + bch));
-                mma_16816(aq[0], Uf[c], wp[0], wp[1]);
-                mma_16816(aq[1], Uf[c], wp[2], wp[3]);
-            }
+            block_rhs(bb, ak, aq, w, down, rw, t);
+            block_solve<NB, 1>(bb, ak, aq, Uf, u, s0 + M::a16, s0 + M::p16, flag, lane);
             // o over v's place
 #pragma unroll
             for (int n = 0; n < 2; ++n)
