@@ -10,6 +10,8 @@
 //                       tensor cores (the lo pieces for K only: what reaches o alone is rounded to bf16 anyway), solve
 //                       the system in mma fragments, write u as hi + lo pairs to TMEM, and let the tensor cores add
 //                       their product with K onto the decayed state, which stays in TMEM in fp32.
+// The system is solved right-looking: U_b is applied to every block after b at once, so that the products of different
+// blocks are independent.
 // What reaches the state is kept to 2^-22 (fp16 pairs; K's values are exact), what reaches o alone to 2^-12.
 #include <math.h>
 
@@ -50,6 +52,72 @@ struct ScanBars {
     uint32_t tmem;
     int abort, bad[2];
 };
+
+// A chunk token by token in fp32, by the state warps: the state in TMEM times un0 / un1 (features g, g + 8 of the warp's
+// 16) is advanced over rows row .. row + nt - 1 and written back unscaled; o goes to global memory.  phase: the state
+// warps' barrier count.
+template <int DK, int DV>
+__device__ __noinline__ bool chunk_fp32(const tsv_gdn_desc& d, int layer, int h, size_t row, int nt, uint32_t state, int fb, float un0,
+                                        float un1, float* tk, uint64_t* bar, uint32_t& phase, volatile int* abort_flag) {
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3, hk = h / (d.HV / d.HK);
+    auto sync = [&]() -> bool {
+        __syncwarp();
+        tc::mbar_arrive_one(bar);
+        return warp_wait(bar, phase++ & 1, abort_flag);
+    };
+    float S[DK / 2];  // S[32 x + 4 n + 2 half + e]: feature fb + g + 8 half, column 64 x + 8 n + 2 t + e
+#pragma unroll
+    for (int x = 0; x < DK / 64; ++x) tc::tmem_ld_frag8(state + 64 * x, S + 32 * x);
+    tc::tmem_wait_ld();
+#pragma unroll
+    for (int x = 0; x < DK / 2; ++x) S[x] *= (x >> 1) & 1 ? un1 : un0;
+    for (int i = 0; i < nt; ++i, ++row) {
+        if (warp == 0) {
+            float kx[DK / 32], qx[DK / 32], kq = 0.f;
+            unit_row<DK>(reinterpret_cast<const uint16_t*>(d.k[layer]) + (row * d.HK + hk) * DK, d.norm_eps, 1.f, lane, kx);
+            unit_row<DK>(reinterpret_cast<const uint16_t*>(d.q[layer]) + (row * d.HK + hk) * DK, d.norm_eps, d.scale, lane, qx);
+#pragma unroll
+            for (int e = 0; e < DK / 32; ++e) {
+                tk[lane + 32 * e] = kx[e];
+                tk[128 + lane + 32 * e] = qx[e];
+                kq = fmaf(kx[e], qx[e], kq);
+            }
+#pragma unroll
+            for (int o = 16; o > 0; o >>= 1) kq += __shfl_xor_sync(0xFFFFFFFFu, kq, o);
+            if (lane == 0) tk[256] = kq;
+        }
+        if (!sync()) return false;
+        const float a = expf(d.g[layer][row * d.HV + h]), be = d.beta[layer][row * d.HV + h];
+        float sk[2] = {0.f, 0.f}, sq[2] = {0.f, 0.f};
+#pragma unroll
+        for (int x = 0; x < DK / 2; ++x) {
+            const int e = (x >> 5) * 64 + ((x & 31) >> 2) * 8 + 2 * t + (x & 1);
+            sk[(x >> 1) & 1] = fmaf(S[x], tk[e], sk[(x >> 1) & 1]);
+            sq[(x >> 1) & 1] = fmaf(S[x], tk[128 + e], sq[(x >> 1) & 1]);
+        }
+#pragma unroll
+        for (int half = 0; half < 2; ++half) {
+#pragma unroll
+            for (int o = 1; o < 4; o <<= 1) {
+                sk[half] += __shfl_xor_sync(0xFFFFFFFFu, sk[half], o);
+                sq[half] += __shfl_xor_sync(0xFFFFFFFFu, sq[half], o);
+            }
+            const size_t at = (row * d.HV + h) * DV + fb + g + 8 * half;
+            const float u = be * (bf16_bits_to_f32(reinterpret_cast<const uint16_t*>(d.v[layer])[at]) - a * sk[half]);
+            if (t == 0) reinterpret_cast<__nv_bfloat16*>(d.o[layer])[at] = __float2bfloat16(fmaf(a, sq[half], u * tk[256]));
+            sk[half] = u;
+        }
+#pragma unroll
+        for (int x = 0; x < DK / 2; ++x) {
+            const int e = (x >> 5) * 64 + ((x & 31) >> 2) * 8 + 2 * t + (x & 1);
+            S[x] = fmaf(sk[(x >> 1) & 1], tk[e], a * S[x]);
+        }
+        if (!sync()) return false;
+    }
+#pragma unroll
+    for (int x = 0; x < DK / 64; ++x) tc::tmem_st_frag8f(state + 64 * x, S + 32 * x);
+    return true;
+}
 
 template <int DK, int DV>
 __global__ void __launch_bounds__((kScanPrep + DV / 16) * 32, 1)
@@ -103,6 +171,8 @@ __global__ void __launch_bounds__((kScanPrep + DV / 16) * 32, 1)
         br.abort = 0;
         tc::fence_mbar_init();
     }
+    for (int e = threadIdx.x; e < 2 * kScanT * 8; e += blockDim.x)  // P above its diagonal blocks, in both buffers
+        *reinterpret_cast<uint4*>(sm + (e >> 9) * M::buffer + M::p16 + (e & 511) * 16) = make_uint4(0, 0, 0, 0);
     if (warp == 1) {
         tc::tmem_alloc(&br.tmem, M::cols);
         tc::tmem_relinquish();
@@ -149,9 +219,27 @@ __global__ void __launch_bounds__((kScanPrep + DV / 16) * 32, 1)
         auto sync = [&]() -> bool {
             __syncwarp();
             tc::mbar_arrive_one(&br.psync);
-            return __all_sync(0xFFFFFFFFu, tc::mbar_wait(&br.psync, ps++ & 1, abort_flag));
+            return warp_wait(&br.psync, ps++ & 1, abort_flag);
+        };
+        // G of the fetched chunk: tokens 2 lane, 2 lane + 1 of the first warp; inclusive scan over the lanes
+        Pair G[2];
+        auto sum_gates = [&]() {
+            G[0] = log2_decay(gi[0]);
+            Pair run = add(G[0], log2_decay(gi[1])), before;
+#pragma unroll
+            for (int o = 1; o < 32; o <<= 1) {
+                Pair y;
+                y.hi = __shfl_up_sync(0xFFFFFFFFu, run.hi, o);
+                y.lo = __shfl_up_sync(0xFFFFFFFFu, run.lo, o);
+                if (lane >= o) run = add(run, y);
+            }
+            before.hi = __shfl_up_sync(0xFFFFFFFFu, run.hi, 1);
+            before.lo = __shfl_up_sync(0xFFFFFFFFu, run.lo, 1);
+            if (lane > 0) G[0] = add(G[0], before);
+            G[1] = run;
         };
         fetch(0);
+        if (pw == 0) sum_gates();
         bool ok = true;
         for (int c = 0; c < chunks; ++c) {
             const int buf = c & 1;
@@ -160,7 +248,7 @@ __global__ void __launch_bounds__((kScanPrep + DV / 16) * 32, 1)
             GdnKeys& ky = *reinterpret_cast<GdnKeys*>(bs + M::keys);
             GdnRows& rw = *reinterpret_cast<GdnRows*>(bs + M::rows);
             float* dj = reinterpret_cast<float*>(bs + M::dj);
-            if (c >= 2 && !__all_sync(0xFFFFFFFFu, tc::mbar_wait(&br.empty[buf], ((c >> 1) - 1) & 1, abort_flag))) {
+            if (c >= 2 && !warp_wait(&br.empty[buf], ((c >> 1) - 1) & 1, abort_flag)) {
                 ok = false;
                 break;
             }
@@ -168,39 +256,25 @@ __global__ void __launch_bounds__((kScanPrep + DV / 16) * 32, 1)
             uint32_t flag = 0;
 #pragma unroll
             for (int x = 0; x < KQ; ++x) {
-                const int r = pt / LPR + x * (PT / LPR);
-                float ss, up;
-                *reinterpret_cast<uint4*>(bs + kq_at<2 * kScanT>(M::kq, r, chunk)) = stage_chunk<DK>(kq[x], ss, up, flag);
-                if (chunk == 0) {
-                    (r >= kScanT ? ky.fq : ky.fk)[r & 63] = up;
-                    (r >= kScanT ? ky.sq : ky.sk)[r & 63] = ss;
-                }
+                const int r = pt / LPR + x * (PT / LPR), i = r & 63;
+                float ss, f;
+                *reinterpret_cast<uint4*>(bs + kq_at<2 * kScanT>(M::kq, (r & 64) + 16 * block_pos<NB>(i >> 4) + (i & 15), chunk)) =
+                    stage_chunk<DK>(kq[x], ss, f, flag);
+                if (d.norm_eps > 0.f) f *= rsqrtf(ss + d.norm_eps);
+                if (chunk == 0) (r >= kScanT ? ky.fq : ky.fk)[i] = r >= kScanT ? f * d.scale : f;
             }
 #pragma unroll
             for (int x = 0; x < VC; ++x) {
                 const int e = pt + x * PT;
                 *reinterpret_cast<uint4*>(bs + tile_at<DV * 2>(M::v, e / CPR, e % CPR)) = vv[x];
             }
-            if (pw == 0) {  // G: tokens 2 lane, 2 lane + 1; inclusive scan over the lanes
-                Pair a = log2_decay(gi[0]), s = add(a, log2_decay(gi[1])), run = s;
-#pragma unroll
-                for (int o = 1; o < 32; o <<= 1) {
-                    Pair y;
-                    y.hi = __shfl_up_sync(0xFFFFFFFFu, run.hi, o);
-                    y.lo = __shfl_up_sync(0xFFFFFFFFu, run.lo, o);
-                    if (lane >= o) run = add(run, y);
-                }
-                Pair before;
-                before.hi = __shfl_up_sync(0xFFFFFFFFu, run.hi, 1);
-                before.lo = __shfl_up_sync(0xFFFFFFFFu, run.lo, 1);
-                if (lane > 0) a = add(a, before);
-                *reinterpret_cast<float2*>(&rw.g_hi[2 * lane]) = make_float2(a.hi, run.hi);
-                *reinterpret_cast<float2*>(&rw.g_lo[2 * lane]) = make_float2(a.lo, run.lo);
+            if (pw == 0) {
+                *reinterpret_cast<float2*>(&rw.g_hi[2 * lane]) = make_float2(G[0].hi, G[1].hi);
+                *reinterpret_cast<float2*>(&rw.g_lo[2 * lane]) = make_float2(G[0].lo, G[1].lo);
                 *reinterpret_cast<float2*>(&rw.beta[2 * lane]) = make_float2(bi[0], bi[1]);
                 ky.before[2 * lane] = (1ull << (2 * lane)) - 1ull;
                 ky.before[2 * lane + 1] = (1ull << (2 * lane + 1)) - 1ull;
             }
-            if (c + 1 < chunks) fetch(c + 1);
             tc::fence_proxy_async_smem();
             tc::tc_fence_before();
             if (!sync()) {
@@ -218,41 +292,29 @@ __global__ void __launch_bounds__((kScanPrep + DV / 16) * 32, 1)
                 }
                 tc::mma_commit(&br.gram);
             }
-            if (pt < 2 * kScanT) {
+            __syncwarp();
+            if (c + 1 < chunks) fetch(c + 1);
+            if (pt < 2 * kScanT) {  // for the state warps
                 const int i = pt & 63;
                 const bool q = pt >= kScanT;
-                float* f = q ? ky.fq : ky.fk;
-                float x = f[i] * (q ? d.scale : 1.f);
-                if (d.norm_eps > 0.f) x /= sqrtf((q ? ky.sq : ky.sk)[i] + d.norm_eps);
-                f[i] = x;
-                const float gh = rw.g_hi[i], gl = rw.g_lo[i];
+                const float x = (q ? ky.fq : ky.fk)[i], gh = rw.g_hi[i], gl = rw.g_lo[i];
                 (q ? rw.cq : rw.ck)[i] = tc::ex2_approx(gh + gl) * x;
                 if (!q) dj[i] = tc::ex2_approx((rw.g_hi[63] - gh) + (rw.g_lo[63] - gl)) * x;
                 else if (i == 63) dj[64] = tc::ex2_approx(gh + gl);
             }
             __syncwarp();
-            if (!sync()) {
-                ok = false;
-                break;
-            }
-            if (!__all_sync(0xFFFFFFFFu, tc::mbar_wait(&br.gram, c & 1, abort_flag))) {
+            if (!warp_wait(&br.gram, c & 1, abort_flag)) {
                 ok = false;
                 break;
             }
             tc::tc_fence_after();
-            const int x = 2 * (pw & 3) + (pw >> 2);  // 16-row block x of [K; Q] sits in lanes 16 x ..
-            const bool q = x >= NB;
-            const int bb = q ? x - NB : x;
-            float* diag = reinterpret_cast<float*>(sm + M::diag) + bb * 16 * kDiag;
-            block_matrices<NB, 2>(q, bb, tmem + M::col_g + ((uint32_t)(16 * x) << 16), bs + M::a16, bs + M::p16, diag, ky, rw, flag, lane);
-            if (!q) {
-                __syncwarp();
-                block_inverse<NB, 2>(bb, bs + M::a16, diag, flag, lane);
-            }
+            warp_matrices<NB, 2>(pw & 3, pw >> 2, tmem + M::col_g, bs + M::a16, bs + M::p16, reinterpret_cast<float*>(sm + M::diag), ky, rw, flag,
+                                 lane);
             if (watched(flag)) br.bad[buf] = 1;
             tc::tc_fence_before();
             __syncwarp();
             tc::mbar_arrive_one(&br.full[buf]);
+            if (pw == 0) sum_gates();
         }
         if (!ok && pt == 0) {  // let this thread's MMAs end
             tc::mma_commit(&br.drain_p);
@@ -268,7 +330,7 @@ __global__ void __launch_bounds__((kScanPrep + DV / 16) * 32, 1)
         auto sync = [&]() -> bool {
             __syncwarp();
             tc::mbar_arrive_one(&br.ssync);
-            return __all_sync(0xFFFFFFFFu, tc::mbar_wait(&br.ssync, ss++ & 1, abort_flag));
+            return warp_wait(&br.ssync, ss++ & 1, abort_flag);
         };
         // 64 columns of the state at a time: r[4 n + 2 half + e] = S[fb + g + 8 half][64 x + 8 n + 2 t + e]
         float r[32];
@@ -296,23 +358,27 @@ __global__ void __launch_bounds__((kScanPrep + DV / 16) * 32, 1)
             const float* dj = reinterpret_cast<const float*>(bs + M::dj);
             const int nt = min(kScanT, n - c * kScanT);
             uint32_t flag = 0;
-            if (!__all_sync(0xFFFFFFFFu, tc::mbar_wait(&br.full[buf], (c >> 1) & 1, abort_flag))) { ok = false; break; }
+            if (!warp_wait(&br.full[buf], (c >> 1) & 1, abort_flag)) { ok = false; break; }
+            // each feature's power-of-two scale from the largest of its state row and v
+            float mx[2] = {0.f, 0.f}, sx[2] = {0.f, 0.f}, down[2], sc[2];
+            uint32_t vf[NB][4];
+#pragma unroll
+            for (int bb = 0; bb < NB; ++bb) {
+                ldsm4_t(vf[bb], tile_at<DV * 2>(bs32 + M::v, bb * 16 + vrow, vchunk));
+#pragma unroll
+                for (int x = 0; x < 4; ++x)
+                    mx[x & 1] = fmaxf(mx[x & 1], fmaxf(fabsf(bf16_lo(vf[bb][x])), fabsf(bf16_hi(vf[bb][x]))));
+            }
+            const float e_n = dj[64];
+            // The decay over the chunk.  Unless it is next to nothing the state is decayed (and scaled) in TMEM at once:
+            // should the chunk have to be done again in fp32, the state can be had back.
+            const bool early = e_n >= 0x1p-60f;
             if (c > 0) {  // the state of the chunk before, whose buffer is then free
-                if (!__all_sync(0xFFFFFFFFu, tc::mbar_wait(&br.state, (c - 1) & 1, abort_flag))) { ok = false; break; }
+                if (!warp_wait(&br.state, (c - 1) & 1, abort_flag)) { ok = false; break; }
                 __syncwarp();
                 tc::mbar_arrive_one(&br.empty[buf ^ 1]);
             }
             tc::tc_fence_after();
-            // each feature's power-of-two scale from the largest of its state row and v; the state's hi and lo pieces
-            float mx[2] = {0.f, 0.f}, sx[2] = {0.f, 0.f}, down[2], sc[2];
-#pragma unroll
-            for (int bb = 0; bb < NB; ++bb) {
-                uint32_t w[4];
-                ldsm4_t(w, tile_at<DV * 2>(bs32 + M::v, bb * 16 + vrow, vchunk));
-#pragma unroll
-                for (int x = 0; x < 4; ++x)
-                    mx[x & 1] = fmaxf(mx[x & 1], fmaxf(fabsf(bf16_lo(w[x])), fabsf(bf16_hi(w[x]))));
-            }
             float S2[DK / 2];  // this thread's part of the state
 #pragma unroll
             for (int x = 0; x < DK / 64; ++x) tc::tmem_ld_frag8(la + M::col_s + 64 * x, S2 + 32 * x);
@@ -338,8 +404,13 @@ __global__ void __launch_bounds__((kScanPrep + DV / 16) * 32, 1)
                 for (int y = 0; y < 16; ++y) {  // y = 2 n + half
                     const float2 z = mul2(make_float2(S2[32 * x + 2 * y], S2[32 * x + 2 * y + 1]), make_float2(sc[y & 1], sc[y & 1]));
                     split2(z.x, z.y, hi[y], lo[y]);
-                    watch(flag, hi[y]);
+                    if (early) {
+                        const float2 ze = mul2(z, make_float2(e_n, e_n));
+                        S2[32 * x + 2 * y] = ze.x;
+                        S2[32 * x + 2 * y + 1] = ze.y;
+                    }
                 }
+                if (early) tc::tmem_st_frag8f(la + M::col_s + 64 * x, S2 + 32 * x);
                 tc::tmem_st_frag8(la + M::col_hi + 32 * x, hi);
                 tc::tmem_st_frag8(la + M::col_lo + 32 * x, lo);
             }
@@ -361,116 +432,104 @@ __global__ void __launch_bounds__((kScanPrep + DV / 16) * 32, 1)
                 tc::mma_commit(&br.prod);
             }
             __syncwarp();
-            if (!__all_sync(0xFFFFFFFFu, tc::mbar_wait(&br.prod, c & 1, abort_flag))) { ok = false; break; }
+            if (!warp_wait(&br.prod, c & 1, abort_flag)) { ok = false; break; }
             tc::tc_fence_after();
 
-            uint32_t Uf[NB][2][4];
+            float ak[NB][2][4];
 #pragma unroll
             for (int bb = 0; bb < NB; ++bb) {
-                float x8[8], y8[8], ak[2][4], aq[2][4], u[2][4];
-                tc::tmem_ld_frag2(la + M::col_d + bb * 16, x8);
-                tc::tmem_ld_frag2(la + M::col_d + kScanT + bb * 16, y8);
-                tc::tmem_wait_ld();
+                float x8[8];
+                tc::tmem_ld_frag2(la + M::col_d + 16 * block_pos<NB>(bb), x8);
 #pragma unroll
-                for (int x = 0; x < 8; ++x) {
-                    ak[x >> 2][x & 3] = x8[x];
-                    aq[x >> 2][x & 3] = y8[x];
-                }
-                uint32_t w[4];
-                ldsm4_t(w, tile_at<DV * 2>(bs32 + M::v, bb * 16 + vrow, vchunk));
-                block_rhs(bb, ak, aq, w, down, rw, t);
-                block_solve<NB, 2>(bb, ak, aq, Uf, u, bs32 + M::a16, bs32 + M::p16, flag, lane);
-                // o over v's place; u for the state, over the state's pieces
+                for (int x = 0; x < 8; ++x) ak[bb][x >> 2][x & 3] = x8[x];
+            }
+            tc::tmem_wait_ld();
+#pragma unroll
+            for (int bb = 0; bb < NB; ++bb) {
+                ldsm4_t(vf[bb], tile_at<DV * 2>(bs32 + M::v, bb * 16 + vrow, vchunk));
+                block_rhs(bb, ak[bb], vf[bb], down, rw, t);
+            }
+            uint32_t Uh[NB][4];  // rolled loops: the block in turn is ak[0], and Uh fills up from its end
+#pragma unroll 1
+            for (int bb = 0; bb < NB; ++bb) {
+                uint32_t Uf[2][4];
+                float u[2][4];
+                block_solve<NB, 2>(bb, ak[0], Uf, u, bs32 + M::a16, flag, lane);
+#pragma unroll
+                for (int bn = 1; bn < NB; ++bn)
+                    if (bb + bn < NB) block_update<NB, 2>(bb + bn, bb, ak[bn], Uf, bs32 + M::a16, lane);
+#pragma unroll
+                for (int bn = 0; bn < NB - 1; ++bn)
+#pragma unroll
+                    for (int x = 0; x < 4; ++x) {
+                        ak[bn][0][x] = ak[bn + 1][0][x];
+                        ak[bn][1][x] = ak[bn + 1][1][x];
+                        Uh[bn][x] = Uh[bn + 1][x];
+                    }
+                // u for the state, over the state's pieces
                 uint32_t hi[4], lo[4];
+#pragma unroll
+                for (int x = 0; x < 4; ++x) Uh[NB - 1][x] = Uf[0][x];
 #pragma unroll
                 for (int nn = 0; nn < 2; ++nn) {
                     const float2 z = *reinterpret_cast<const float2*>(&dj[bb * 16 + nn * 8 + 2 * t]);
 #pragma unroll
                     for (int half = 0; half < 2; ++half) {
-                        w[2 * nn + half] = bf16x2(aq[nn][2 * half] * up[half], aq[nn][2 * half + 1] * up[half]);
                         split2(u[nn][2 * half] * z.x, u[nn][2 * half + 1] * z.y, hi[2 * nn + half], lo[2 * nn + half]);
                         watch(flag, hi[2 * nn + half]);
                     }
                 }
+                tc::tmem_st_frag2(la + M::col_hi + 8 * block_pos<NB>(bb), hi);
+                tc::tmem_st_frag2(la + M::col_lo + 8 * block_pos<NB>(bb), lo);
+            }
+            // o over v's place; P is zero above its diagonal blocks
+#pragma unroll 1
+            for (int bb = 0; bb < NB; ++bb) {
+                float x8[8], aq[2][4];
+                uint32_t w[4];
+                tc::tmem_ld_frag2(la + M::col_d + kScanT + 16 * block_pos<NB>(bb), x8);
+                tc::tmem_wait_ld();
+#pragma unroll
+                for (int x = 0; x < 8; ++x) aq[x >> 2][x & 3] = x8[x];
+                block_rhs_q(bb, aq, rw, t);
+#pragma unroll
+                for (int cc = 0; cc < NB; ++cc) block_out(bb, cc, aq, Uh[cc], bs32 + M::p16, lane);
+#pragma unroll
+                for (int nn = 0; nn < 2; ++nn)
+#pragma unroll
+                    for (int half = 0; half < 2; ++half)
+                        w[2 * nn + half] = bf16x2(aq[nn][2 * half] * up[half], aq[nn][2 * half + 1] * up[half]);
                 stsm4_t(tile_at<DV * 2>(bs32 + M::v, bb * 16 + vrow, vchunk), w);
-                tc::tmem_st_frag2(la + M::col_hi + bb * 8, hi);
-                tc::tmem_st_frag2(la + M::col_lo + bb * 8, lo);
             }
             if (watched(flag)) br.bad[buf] = 1;
             tc::tmem_wait_st();
-            if (!sync()) { ok = false; break; }
-            const bool bad = *reinterpret_cast<volatile int*>(&br.bad[buf]) != 0;
-#pragma unroll
-            for (int x = 0; x < DK / 64; ++x) tc::tmem_ld_frag8(la + M::col_s + 64 * x, S2 + 32 * x);
-            tc::tmem_wait_ld();
-            if (!bad) {
-                const float e = dj[64];
-                const float2 f[2] = {make_float2(sc[0] * e, sc[0] * e), make_float2(sc[1] * e, sc[1] * e)};
-#pragma unroll
-                for (int x = 0; x < DK / 2; x += 2) {
-                    const float2 z = mul2(make_float2(S2[x], S2[x + 1]), f[(x >> 1) & 1]);
-                    S2[x] = z.x;
-                    S2[x + 1] = z.y;
-                }
-            } else {
-                // fp32, token by token: an operand left fp16's range.  Not finite inputs then reach what the recurrence
-                // lets them reach: later tokens, and with v only their own feature.
-                float* tk = reinterpret_cast<float*>(sm + M::slow);
-                const float un[2] = {sc[0] * up[0], sc[1] * up[1]};  // what TMEM holds times the scale before this chunk's
-#pragma unroll
-                for (int x = 0; x < DK / 2; ++x) S2[x] *= un[(x >> 1) & 1];
-                for (int i = 0; i < nt && ok; ++i) {
-                    const size_t row = (size_t)row0 + c * kScanT + i;
-                    if (warp == 0) {
-                        float kx[DK / 32], qx[DK / 32], kq = 0.f;
-                        unit_row<DK>(reinterpret_cast<const uint16_t*>(d.k[layer]) + (row * d.HK + hk) * DK, d.norm_eps, 1.f, lane, kx);
-                        unit_row<DK>(reinterpret_cast<const uint16_t*>(d.q[layer]) + (row * d.HK + hk) * DK, d.norm_eps, d.scale, lane, qx);
-#pragma unroll
-                        for (int e = 0; e < DK / 32; ++e) {
-                            tk[lane + 32 * e] = kx[e];
-                            tk[128 + lane + 32 * e] = qx[e];
-                            kq = fmaf(kx[e], qx[e], kq);
-                        }
-#pragma unroll
-                        for (int o = 16; o > 0; o >>= 1) kq += __shfl_xor_sync(0xFFFFFFFFu, kq, o);
-                        if (lane == 0) tk[256] = kq;
-                    }
-                    if (!sync()) { ok = false; break; }
-                    const float a = expf(d.g[layer][row * d.HV + h]), be = d.beta[layer][row * d.HV + h];
-                    float sk[2] = {0.f, 0.f}, sq[2] = {0.f, 0.f};
-#pragma unroll
-                    for (int x = 0; x < DK / 2; ++x) {
-                        const int e = (x >> 5) * 64 + ((x & 31) >> 2) * 8 + 2 * t + (x & 1);
-                        sk[(x >> 1) & 1] = fmaf(S2[x], tk[e], sk[(x >> 1) & 1]);
-                        sq[(x >> 1) & 1] = fmaf(S2[x], tk[128 + e], sq[(x >> 1) & 1]);
-                    }
-#pragma unroll
-                    for (int half = 0; half < 2; ++half) {
-#pragma unroll
-                        for (int o = 1; o < 4; o <<= 1) {
-                            sk[half] += __shfl_xor_sync(0xFFFFFFFFu, sk[half], o);
-                            sq[half] += __shfl_xor_sync(0xFFFFFFFFu, sq[half], o);
-                        }
-                        const size_t at = (row * d.HV + h) * DV + fb + g + 8 * half;
-                        const float u = be * (bf16_bits_to_f32(reinterpret_cast<const uint16_t*>(d.v[layer])[at]) - a * sk[half]);
-                        if (t == 0) reinterpret_cast<__nv_bfloat16*>(d.o[layer])[at] = __float2bfloat16(fmaf(a, sq[half], u * tk[256]));
-                        sk[half] = u;
-                    }
-#pragma unroll
-                    for (int x = 0; x < DK / 2; ++x) {
-                        const int e = (x >> 5) * 64 + ((x & 31) >> 2) * 8 + 2 * t + (x & 1);
-                        S2[x] = fmaf(sk[(x >> 1) & 1], tk[e], a * S2[x]);
-                    }
-                    if (!sync()) { ok = false; break; }
-                }
-                if (!ok) break;
-                up[0] = up[1] = 1.f;
-            }
-#pragma unroll
-            for (int x = 0; x < DK / 64; ++x) tc::tmem_st_frag8f(la + M::col_s + 64 * x, S2 + 32 * x);
-            tc::tmem_wait_st();
             tc::tc_fence_before();
             if (!sync()) { ok = false; break; }
+            const bool bad = *reinterpret_cast<volatile int*>(&br.bad[buf]) != 0;
+            if (bad) {
+                // fp32, token by token: an operand left fp16's range.  Not finite inputs then reach what the recurrence
+                // lets them reach: later tokens, and with v only their own feature.  What TMEM holds times un is the
+                // state ahead of the chunk.
+                const float un0 = early ? up[0] / e_n : sc[0] * up[0], un1 = early ? up[1] / e_n : sc[1] * up[1];
+                ok = chunk_fp32<DK, DV>(d, layer, h, (size_t)row0 + (size_t)c * kScanT, nt, la + M::col_s, fb, un0, un1,
+                                        reinterpret_cast<float*>(sm + M::slow), &br.ssync, ss, abort_flag);
+                if (!ok) break;
+                up[0] = up[1] = 1.f;
+            } else if (!early) {
+#pragma unroll 1
+                for (int x = 0; x < DK / 64; ++x) {
+                    tc::tmem_ld_frag8(la + M::col_s + 64 * x, S2);
+                    tc::tmem_wait_ld();
+#pragma unroll
+                    for (int y = 0; y < 32; ++y) S2[y] *= sc[(y >> 1) & 1] * e_n;
+                    tc::tmem_st_frag8f(la + M::col_s + 64 * x, S2);
+                }
+            }
+            if (bad || !early) {
+                tc::tmem_wait_st();
+                tc::tc_fence_before();
+                if (!sync()) { ok = false; break; }
+            }
             if (threadIdx.x == 0) {  // S += U'^T K
                 tc::tc_fence_after();
                 if (!bad) {
@@ -496,7 +555,7 @@ __global__ void __launch_bounds__((kScanPrep + DV / 16) * 32, 1)
                 }
             }
         }
-        if (ok) ok = __all_sync(0xFFFFFFFFu, tc::mbar_wait(&br.state, (chunks - 1) & 1, abort_flag));
+        if (ok) ok = warp_wait(&br.state, (chunks - 1) & 1, abort_flag);
         if (ok) {
             tc::tc_fence_after();
             float* out = d.state_out[layer] + state0 + (size_t)(fb + g) * DK + 2 * t;

@@ -29,7 +29,7 @@ constexpr float kMinLogDecay = -150.f;  // e^-150 is 0 in fp32: a smaller (or in
 __device__ __forceinline__ float clamp_decay(float g) { return g < kMinLogDecay ? kMinLogDecay : g; }  // keeps NaN
 
 __device__ __forceinline__ void mma_16816(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
-    asm volatile(
+    asm(
         "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
         : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
         : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
@@ -98,6 +98,15 @@ __device__ __forceinline__ void pow2_scale(float m, float& down, float& up) {
     e = min(max(e, 1u), 253u);
     down = __uint_as_float((254u - e) << 23);
     up = __uint_as_float(e << 23);
+}
+
+// A whole warp's bounded wait: the poll inline, the sleeping loop (tc::mbar_wait) out of line, once per kernel.
+static __device__ __noinline__ bool wait_out_of_line(uint64_t* bar, uint32_t parity, volatile int* abort) {
+    return __all_sync(0xFFFFFFFFu, tc::mbar_wait(bar, parity, abort));
+}
+__device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity, volatile int* abort) {
+    if (__all_sync(0xFFFFFFFFu, tc::mbar_test(bar, parity))) return true;
+    return wait_out_of_line(bar, parity, abort);
 }
 
 // 16 bytes from global to shared memory, asynchronously; zeros when !real (src is then not read).
@@ -178,65 +187,88 @@ __device__ __forceinline__ uint32_t kq_at(uint32_t base, int row, int chunk) {
     return base + (uint32_t)((chunk >> 3) * ROWS * 128 + row * 128 + (((chunk & 7) ^ (row & 7)) << 4));
 }
 
-// One 16-row block's products with the K rows of its own and the blocks before (TMEM columns c * 16 of `taddr`, the
-// block's rows in its lanes), decayed and masked:
+// Where 16-row block b of K (and of Q, NB blocks on) sits in the tile, its TMEM lanes and the products' columns.  A
+// quarter of the TMEM lanes belongs to two warps; four blocks in the order 0 3 1 2 give every quarter five block
+// products (block b has b + 1).
+template <int NB>
+__host__ __device__ constexpr int block_pos(int b) {
+    return NB == 4 ? (b == 0 ? 0 : b == 3 ? 1 : b + 1) : b;
+}
+
+// Products of one 16-row block with the K rows of blocks c0 .. c1 - 1, none of them after its own (TMEM columns
+// 16 block_pos(c) of `taddr`, the block's rows in its lanes), decayed and masked:
 //   q == false: rows K_b; -A (fp16 pieces) for the blocks before, A itself (fp32) for the block's own
 //   q == true:  rows Q_b; P (fp16)
 // a16 / p16: [T rows][128 B] tiles; diag: this block's [16][kDiag] fp32.
 constexpr int kDiag = 20;  // fp32 row stride of a diagonal block: 16-byte aligned, rows in different banks
 template <int NB, int PIECES>
-__device__ __forceinline__ void block_matrices(bool q, int b, uint32_t taddr, char* a16, char* p16, float* diag,
+__device__ __forceinline__ void block_matrices(bool q, int b, int c0, int c1, uint32_t taddr, char* a16, char* p16, float* diag,
                                                const GdnKeys& ky, const GdnRows& rw, uint32_t& flag, int lane) {
     constexpr int T = 16 * NB;
     const int g = lane >> 2, t = lane & 3;
-    float acc[2][8];
-    tc::tmem_ld_frag2(taddr, acc[0]);
+    float gh[2], gl[2], f[2];
+    uint64_t seen[2];
 #pragma unroll
-    for (int c = 0; c < NB; ++c) {
-        if (c > b) break;
+    for (int half = 0; half < 2; ++half) {
+        const int i = b * 16 + g + 8 * half;
+        gh[half] = rw.g_hi[i];
+        gl[half] = rw.g_lo[i];
+        f[half] = q ? ky.fq[i] : rw.beta[i] * ky.fk[i];
+        seen[half] = q ? ky.before[i] | (1ull << i) : ky.before[i];
+    }
+#pragma unroll 1
+    for (int c = c0; c < c1; ++c) {  // rolled: a kernel's warps run different parts at once and share the instruction cache
+        float x[8];
+        tc::tmem_ld_frag2(taddr + 16 * block_pos<NB>(c), x);
+        float2 jh[2], jl[2], jf[2];
+#pragma unroll
+        for (int n = 0; n < 2; ++n) {
+            const int j0 = c * 16 + n * 8 + 2 * t;
+            jh[n] = *reinterpret_cast<const float2*>(&rw.g_hi[j0]);
+            jl[n] = *reinterpret_cast<const float2*>(&rw.g_lo[j0]);
+            jf[n] = *reinterpret_cast<const float2*>(&ky.fk[j0]);
+        }
         tc::tmem_wait_ld();
-        if (c < b) tc::tmem_ld_frag2(taddr + (c + 1) * 16, acc[(c + 1) & 1]);
-        const float(&x)[8] = acc[c & 1];
+        float y[2][2][2];
 #pragma unroll
         for (int half = 0; half < 2; ++half) {
-            const int il = g + 8 * half, i = b * 16 + il;
-            uint32_t bits = (uint32_t)(ky.before[i] >> (c * 16));
-            if (q && c == b) bits |= 1u << il;
-            bits >>= 2 * t;
-            const float gh = rw.g_hi[i], gl = rw.g_lo[i];
-            const float f = q ? ky.fq[i] : rw.beta[i] * ky.fk[i];
+            const uint32_t bits = (uint32_t)(seen[half] >> (c * 16)) >> (2 * t);
 #pragma unroll
             for (int n = 0; n < 2; ++n) {
-                const int j0 = c * 16 + n * 8 + 2 * t;
-                const float2 jh = *reinterpret_cast<const float2*>(&rw.g_hi[j0]), jl2 = *reinterpret_cast<const float2*>(&rw.g_lo[j0]),
-                             jf = *reinterpret_cast<const float2*>(&ky.fk[j0]);
-                float y[2];
-                y[0] = x[4 * n + 2 * half] * jf.x * (f * tc::ex2_approx((gh - jh.x) + (gl - jl2.x)));
-                y[1] = x[4 * n + 2 * half + 1] * jf.y * (f * tc::ex2_approx((gh - jh.y) + (gl - jl2.y)));
+                const float w0 = tc::ex2_approx((gh[half] - jh[n].x) + (gl[half] - jl[n].x));
+                const float w1 = tc::ex2_approx((gh[half] - jh[n].y) + (gl[half] - jl[n].y));
+                const float y0 = x[4 * n + 2 * half] * jf[n].x * (f[half] * w0);
+                const float y1 = x[4 * n + 2 * half + 1] * jf[n].y * (f[half] * w1);
+                y[half][n][0] = (bits & (1u << (n * 8))) ? y0 : 0.f;
+                y[half][n][1] = (bits & (2u << (n * 8))) ? y1 : 0.f;
+            }
+        }
 #pragma unroll
-                for (int e = 0; e < 2; ++e) y[e] = (bits & (1u << (n * 8 + e))) ? y[e] : 0.f;
+        for (int half = 0; half < 2; ++half)
+#pragma unroll
+            for (int n = 0; n < 2; ++n) {
+                const int il = g + 8 * half, i = b * 16 + il;
+                const float y0 = y[half][n][0], y1 = y[half][n][1];
                 if (q) {
-                    const uint32_t h = f16x2(y[0], y[1]);
+                    const uint32_t h = f16x2(y0, y1);
                     watch(flag, h);
                     *reinterpret_cast<uint32_t*>(p16 + tile_at<128>(0, i, 2 * c + n) + 4 * t) = h;
                 } else if (c == b) {
-                    *reinterpret_cast<float2*>(diag + il * kDiag + n * 8 + 2 * t) = make_float2(y[0], y[1]);
+                    *reinterpret_cast<float2*>(diag + il * kDiag + n * 8 + 2 * t) = make_float2(y0, y1);
                 } else {
                     uint32_t hi, lo;
-                    split2(-y[0], -y[1], hi, lo);
-                    watch(flag, hi);
+                    split2(-y0, -y1, hi, lo);
                     *reinterpret_cast<uint32_t*>(a16 + tile_at<128>(0, i, 2 * c + n) + 4 * t) = hi;
                     if (PIECES == 2) *reinterpret_cast<uint32_t*>(a16 + T * 128 + tile_at<128>(0, i, 2 * c + n) + 4 * t) = lo;
                 }
             }
-        }
     }
 }
 
 // (I + A_bb)^-1 of one block by forward substitution, a column per lane (both half-warps do the same), stored over
 // block (b, b) of the a16 tile.
 template <int NB, int PIECES>
-__device__ __forceinline__ void block_inverse(int b, char* a16, const float* diag, uint32_t& flag, int lane) {
+__device__ __forceinline__ void block_inverse(int b, char* a16, const float* diag, int lane) {
     constexpr int T = 16 * NB;
     const int c = lane & 15;
     float x[16];
@@ -258,7 +290,6 @@ __device__ __forceinline__ void block_inverse(int b, char* a16, const float* dia
         for (int i = 0; i < 16; i += 2) {
             uint32_t hi, lo;
             split2(x[i], x[i + 1], hi, lo);
-            watch(flag, hi);
 #pragma unroll
             for (int e = 0; e < 2; ++e) {
                 const int row = b * 16 + i + e, col = b * 16 + c;
@@ -270,54 +301,75 @@ __device__ __forceinline__ void block_inverse(int b, char* a16, const float* dia
     }
 }
 
-// Scaled sums of one block and value feature pair in mma fragments (features g, g + 8; rows 8 n + 2 t, + 1):
-// in, ak = S k_i and aq = S q_i; out, ak = R_b (before the blocks ahead of b) and aq = e^{G_i} S q_i.
-__device__ __forceinline__ void block_rhs(int bb, float (&ak)[2][4], float (&aq)[2][4], const uint32_t (&v)[4], const float (&down)[2],
-                                          const GdnRows& rw, int t) {
+// One warp's share of a block's matrices: quarter qt of the TMEM lanes, its first or second warp m.  gram: TMEM address
+// of [K; Q] K^T.
+template <int NB, int PIECES>
+__device__ __forceinline__ void warp_matrices(int qt, int m, uint32_t gram, char* a16, char* p16, float* diag, const GdnKeys& ky,
+                                              const GdnRows& rw, uint32_t& flag, int lane) {
+    const bool q = NB == 4 ? qt >= 2 : 2 * qt + m >= NB;
+    int b, c0 = 0, c1, parts = 1;
+    if constexpr (NB == 4) {
+        b = qt & 1 ? m + 1 : (m == 0 ? 0 : 3);  // blocks 1 and 2, or 0 with half of 3 and the rest of 3
+        c0 = b == 3 ? 2 : 0;
+        parts = b == 0 ? 2 : 1;
+    } else {
+        b = q ? 2 * qt + m - NB : 2 * qt + m;
+        if (b >= NB) return;
+    }
+    c1 = b + 1;
+#pragma unroll 1
+    for (int p = 0; p < parts; ++p) {
+        const int row = 16 * ((q ? NB : 0) + block_pos<NB>(b));
+        block_matrices<NB, PIECES>(q, b, c0, c1, gram + ((uint32_t)row << 16), a16, p16, diag + b * 16 * kDiag, ky, rw, flag, lane);
+        if (!q && p == 0) {
+            __syncwarp();
+            block_inverse<NB, PIECES>(b, a16, diag + b * 16 * kDiag, lane);
+        }
+        b = 3;  // the second part: the first half of block 3
+        c0 = 0;
+        c1 = 2;
+    }
+}
+
+// One block and value feature pair in mma fragments (features g, g + 8; rows 8 n + 2 t, + 1): S k_i -> R_b ahead of
+// the blocks before, from v's fragments and the features' scales; and S q_i -> e^{G_i} S q_i.
+__device__ __forceinline__ void block_rhs(int bb, float (&ak)[2][4], const uint32_t (&v)[4], const float (&down)[2], const GdnRows& rw, int t) {
 #pragma unroll
     for (int n = 0; n < 2; ++n) {
         const int i = bb * 16 + n * 8 + 2 * t;
-        const float2 be = *reinterpret_cast<const float2*>(&rw.beta[i]), ck = *reinterpret_cast<const float2*>(&rw.ck[i]),
-                     cq = *reinterpret_cast<const float2*>(&rw.cq[i]);
+        const float2 be = *reinterpret_cast<const float2*>(&rw.beta[i]), ck = *reinterpret_cast<const float2*>(&rw.ck[i]);
 #pragma unroll
         for (int half = 0; half < 2; ++half) {
             const uint32_t v2 = v[2 * n + half];
             ak[n][2 * half] = be.x * (bf16_lo(v2) * down[half] - ck.x * ak[n][2 * half]);
             ak[n][2 * half + 1] = be.y * (bf16_hi(v2) * down[half] - ck.y * ak[n][2 * half + 1]);
+        }
+    }
+}
+__device__ __forceinline__ void block_rhs_q(int bb, float (&aq)[2][4], const GdnRows& rw, int t) {
+#pragma unroll
+    for (int n = 0; n < 2; ++n) {
+        const float2 cq = *reinterpret_cast<const float2*>(&rw.cq[bb * 16 + n * 8 + 2 * t]);
+#pragma unroll
+        for (int half = 0; half < 2; ++half) {
             aq[n][2 * half] *= cq.x;
             aq[n][2 * half + 1] *= cq.y;
         }
     }
 }
 
-// R_b -> U_b (kept as fragments in Uf, fp32 in u) and o_b (in aq).  a16, p16: shared addresses of the tiles.
+// R_b -> U_b: pieces in Uf, fp32 in u.  a16: shared address of the tiles.
 template <int NB, int PIECES>
-__device__ __forceinline__ void block_solve(int bb, float (&ak)[2][4], float (&aq)[2][4], uint32_t (&Uf)[NB][PIECES][4],
-                                            float (&u)[2][4], uint32_t a16, uint32_t p16, uint32_t& flag, int lane) {
+__device__ __forceinline__ void block_solve(int bb, const float (&ak)[2][4], uint32_t (&Uf)[PIECES][4], float (&u)[2][4], uint32_t a16,
+                                            uint32_t& flag, int lane) {
     const int brow = ((lane >> 4) << 3) + (lane & 7), bch = (lane >> 3) & 1;
     constexpr int kLo = 16 * NB * 128;  // the lo pieces' tile
-    uint32_t w[4], w2[4];
-#pragma unroll
-    for (int c = 0; c < NB; ++c) {
-        if (c >= bb) break;
-        ldsm4(w, tile_at<128>(a16, bb * 16 + brow, 2 * c + bch));
-        mma_16816(ak[0], Uf[c][0], w[0], w[1]);
-        mma_16816(ak[1], Uf[c][0], w[2], w[3]);
-        if constexpr (PIECES == 2) {
-            ldsm4(w2, tile_at<128>(a16 + kLo, bb * 16 + brow, 2 * c + bch));
-            mma_16816(ak[0], Uf[c][1], w[0], w[1]);
-            mma_16816(ak[1], Uf[c][1], w[2], w[3]);
-            mma_16816(ak[0], Uf[c][0], w2[0], w2[1]);
-            mma_16816(ak[1], Uf[c][0], w2[2], w2[3]);
-        }
-    }
-    uint32_t r[PIECES][4];
+    uint32_t w[4], r[PIECES][4];
 #pragma unroll
     for (int x = 0; x < 4; ++x) {
         const float a = ak[x >> 1][2 * (x & 1)], b = ak[x >> 1][2 * (x & 1) + 1];
         if constexpr (PIECES == 2) split2(a, b, r[0][x], r[1][x]);
         else r[0][x] = f16x2(a, b);
-        watch(flag, r[0][x]);
     }
 #pragma unroll
     for (int n = 0; n < 2; ++n)
@@ -327,26 +379,50 @@ __device__ __forceinline__ void block_solve(int bb, float (&ak)[2][4], float (&a
     mma_16816(u[0], r[0], w[0], w[1]);
     mma_16816(u[1], r[0], w[2], w[3]);
     if constexpr (PIECES == 2) {
+        float v[2][4] = {};
+        uint32_t w2[4];
         ldsm4(w2, tile_at<128>(a16 + kLo, bb * 16 + brow, 2 * bb + bch));
-        mma_16816(u[0], r[1], w[0], w[1]);
-        mma_16816(u[1], r[1], w[2], w[3]);
-        mma_16816(u[0], r[0], w2[0], w2[1]);
-        mma_16816(u[1], r[0], w2[2], w2[3]);
+        mma_16816(v[0], r[1], w[0], w[1]);
+        mma_16816(v[1], r[1], w[2], w[3]);
+        mma_16816(v[0], r[0], w2[0], w2[1]);
+        mma_16816(v[1], r[0], w2[2], w2[3]);
+#pragma unroll
+        for (int n = 0; n < 2; ++n)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) u[n][e] += v[n][e];
     }
 #pragma unroll
     for (int x = 0; x < 4; ++x) {
         const float a = u[x >> 1][2 * (x & 1)], b = u[x >> 1][2 * (x & 1) + 1];
-        if constexpr (PIECES == 2) split2(a, b, Uf[bb][0][x], Uf[bb][1][x]);
-        else Uf[bb][0][x] = f16x2(a, b);
-        watch(flag, Uf[bb][0][x]);
+        if constexpr (PIECES == 2) split2(a, b, Uf[0][x], Uf[1][x]);
+        else Uf[0][x] = f16x2(a, b);
+        watch(flag, Uf[0][x]);  // an R, A or inverse that is not finite ends here
     }
-#pragma unroll
-    for (int c = 0; c < NB; ++c) {
-        if (c > bb) break;
-        ldsm4(w, tile_at<128>(p16, bb * 16 + brow, 2 * c + bch));
-        mma_16816(aq[0], Uf[c][0], w[0], w[1]);
-        mma_16816(aq[1], Uf[c][0], w[2], w[3]);
+}
+// acc -= A_bc U_c for a block b after c (the tile holds -A).
+template <int NB, int PIECES>
+__device__ __forceinline__ void block_update(int b, int c, float (&acc)[2][4], const uint32_t (&Uf)[PIECES][4], uint32_t a16, int lane) {
+    const int brow = ((lane >> 4) << 3) + (lane & 7), bch = (lane >> 3) & 1;
+    constexpr int kLo = 16 * NB * 128;
+    uint32_t w[4];
+    ldsm4(w, tile_at<128>(a16, b * 16 + brow, 2 * c + bch));
+    mma_16816(acc[0], Uf[0], w[0], w[1]);
+    mma_16816(acc[1], Uf[0], w[2], w[3]);
+    if constexpr (PIECES == 2) {
+        uint32_t w2[4];
+        ldsm4(w2, tile_at<128>(a16 + kLo, b * 16 + brow, 2 * c + bch));
+        mma_16816(acc[0], Uf[1], w[0], w[1]);
+        mma_16816(acc[1], Uf[1], w[2], w[3]);
+        mma_16816(acc[0], Uf[0], w2[0], w2[1]);
+        mma_16816(acc[1], Uf[0], w2[2], w2[3]);
     }
+}
+// acc += P_bc U_c.
+__device__ __forceinline__ void block_out(int b, int c, float (&acc)[2][4], const uint32_t (&U)[4], uint32_t p16, int lane) {
+    uint32_t w[4];
+    ldsm4(w, tile_at<128>(p16, b * 16 + ((lane >> 4) << 3) + (lane & 7), 2 * c + ((lane >> 3) & 1)));
+    mma_16816(acc[0], U, w[0], w[1]);
+    mma_16816(acc[1], U, w[2], w[3]);
 }
 
 // One bf16 row of DK features, read by a whole warp, normalised: this lane's values of features lane + 32 e.

@@ -108,6 +108,13 @@ __device__ __noinline__ void tree_fp32(const tsv_gdn_desc& d, const uint64_t* an
     }
 }
 
+// Row of the K and Q tile that holds row r of [K; Q].
+template <int NB>
+__device__ __forceinline__ int row_pos(int r) {
+    const int q = r >= 16 * NB ? 16 * NB : 0, i = r - q;
+    return q + 16 * block_pos<NB>(i >> 4) + (i & 15);
+}
+
 template <int DK, int DV, int NB>
 __global__ void __launch_bounds__(2 * DV, 2) gdn_tree_kernel(const __grid_constant__ tsv_gdn_desc d,
                                                              const uint64_t* __restrict__ anc, int heads, int32_t* status) {
@@ -155,7 +162,7 @@ __global__ void __launch_bounds__(2 * DV, 2) gdn_tree_kernel(const __grid_consta
     for (int x = 0; x < KQ; ++x) {
         const int r = threadIdx.x / LPR + x * (kThreads / LPR), i = r >= T16 ? r - T16 : r;
         const uint16_t* src = reinterpret_cast<const uint16_t*>(r >= T16 ? d.q[layer] : d.k[layer]);
-        cp16(kq_at<2 * T16>(s0 + M::kq, r, chunk), src + ((row0 + (i < T ? i : 0)) * d.HK + hk) * DK + chunk * 8, i < T);
+        cp16(kq_at<2 * T16>(s0 + M::kq, row_pos<NB>(r), chunk), src + ((row0 + (i < T ? i : 0)) * d.HK + hk) * DK + chunk * 8, i < T);
     }
     cp_commit();
     constexpr int CPR = DV / 8;
@@ -233,7 +240,7 @@ __global__ void __launch_bounds__(2 * DV, 2) gdn_tree_kernel(const __grid_consta
 #pragma unroll
     for (int x = 0; x < KQ; ++x) {
         const int r = threadIdx.x / LPR + x * (kThreads / LPR);
-        char* at = sm + kq_at<2 * T16>(M::kq, r, chunk);
+        char* at = sm + kq_at<2 * T16>(M::kq, row_pos<NB>(r), chunk);
         float ss, upr;
         *reinterpret_cast<uint4*>(at) = stage_chunk<DK>(*reinterpret_cast<const uint4*>(at), ss, upr, flag_kq);
         if (chunk == 0) {  // the row's factor is finished below
@@ -306,7 +313,6 @@ __global__ void __launch_bounds__(2 * DV, 2) gdn_tree_kernel(const __grid_consta
                 for (int n = 0; n < 2 * KS; ++n) {
                     const float2 x = mul2(raw[half][n], d2);
                     Sf[2 * n + half] = f16x2(x.x, x.y);
-                    watch(flag, Sf[2 * n + half]);
                 }
             }
 #pragma unroll
@@ -327,23 +333,13 @@ __global__ void __launch_bounds__(2 * DV, 2) gdn_tree_kernel(const __grid_consta
             tc::mma_commit(&bars[1]);
         }
         __syncwarp();
-        // the system's matrices: 16-row block x of [K; Q] sits in lanes 16 x ..
-        ok = __all_sync(0xFFFFFFFFu, tc::mbar_wait(&bars[0], 0, abort_flag));
+        // the system's matrices
+        ok = warp_wait(&bars[0], 0, abort_flag);
         tc::tc_fence_after();
         if (ok) {
-            for (int hf = warp >> 2; hf < 2; hf += kWarps / 4) {
-                const int x = 2 * (warp & 3) + hf;
-                if (x >= 2 * NB) continue;
-                const bool q = x >= NB;
-                const int bb = q ? x - NB : x;
-                block_matrices<NB, 1>(q, bb, tmem + M::col_g + ((uint32_t)(16 * x) << 16), sm + M::a16, sm + M::p16,
-                                      diag + bb * 16 * kDiag, ky, rw, flag, lane);
-                if (!q) {
-                    __syncwarp();
-                    block_inverse<NB, 1>(bb, sm + M::a16, diag + bb * 16 * kDiag, flag, lane);
-                }
-            }
-            ok = __all_sync(0xFFFFFFFFu, tc::mbar_wait(&bars[1], k & 1, abort_flag));
+            for (int hf = warp >> 2; hf < 2; hf += kWarps / 4)
+                warp_matrices<NB, 1>(warp & 3, hf, tmem + M::col_g, sm + M::a16, sm + M::p16, diag, ky, rw, flag, lane);
+            ok = warp_wait(&bars[1], k & 1, abort_flag);
         }
         ok = __syncthreads_and(ok);
         tc::tc_fence_after();
@@ -352,20 +348,24 @@ __global__ void __launch_bounds__(2 * DV, 2) gdn_tree_kernel(const __grid_consta
         uint32_t Uf[NB][1][4];
 #pragma unroll
         for (int bb = 0; bb < NB; ++bb) {
-            float dk[8], dq[8], ak[2][4], aq[2][4];  // this block's columns of S K^T and S Q^T
-            tc::tmem_ld_frag2(tmem + ((uint32_t)lane0 << 16) + M::col_d + bb * 16, dk);
-            tc::tmem_ld_frag2(tmem + ((uint32_t)lane0 << 16) + M::col_d + T16 + bb * 16, dq);
+            float dk[8], dq[8], ak[2][4], aq[2][4], u[2][4];  // this block's columns of S K^T and S Q^T
+            tc::tmem_ld_frag2(tmem + ((uint32_t)lane0 << 16) + M::col_d + 16 * block_pos<NB>(bb), dk);
+            tc::tmem_ld_frag2(tmem + ((uint32_t)lane0 << 16) + M::col_d + T16 + 16 * block_pos<NB>(bb), dq);
+            uint32_t w[4];
+            ldsm4_t(w, tile_at<DV * 2>(s0 + vt, bb * 16 + vrow, vchunk));
             tc::tmem_wait_ld();
 #pragma unroll
             for (int x = 0; x < 8; ++x) {
                 ak[x >> 2][x & 3] = dk[x];
                 aq[x >> 2][x & 3] = dq[x];
             }
-            uint32_t w[4];
-            float u[2][4];
-            ldsm4_t(w, tile_at<DV * 2>(s0 + vt, bb * 16 + vrow, vchunk));
-            block_rhs(bb, ak, aq, w, down, rw, t);
-            block_solve<NB, 1>(bb, ak, aq, Uf, u, s0 + M::a16, s0 + M::p16, flag, lane);
+            block_rhs(bb, ak, w, down, rw, t);
+#pragma unroll
+            for (int c = 0; c < bb; ++c) block_update<NB, 1>(bb, c, ak, Uf[c], s0 + M::a16, lane);
+            block_solve<NB, 1>(bb, ak, Uf[bb], u, s0 + M::a16, flag, lane);
+            block_rhs_q(bb, aq, rw, t);
+#pragma unroll
+            for (int c = 0; c <= bb; ++c) block_out(bb, c, aq, Uf[c][0], s0 + M::p16, lane);
             // o over v's place
 #pragma unroll
             for (int n = 0; n < 2; ++n)
