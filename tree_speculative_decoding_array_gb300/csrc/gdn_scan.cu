@@ -48,23 +48,38 @@ struct ScanSmem {
 
 // Barriers of one CTA.
 struct ScanBars {
-    uint64_t full[2], empty[2], gram, prod, state, ssync, psync, drain_s, drain_p;
+    uint64_t full[2], empty[2], gram, prod, state, drain_s, drain_p;
     uint32_t tmem;
-    int abort, bad[2];
+    int abort, bad[2], said[2][2];
+};
+
+// One of the CTA's two groups of warps (hardware barrier 1 + which, `threads` threads).  Only the group's first warp
+// polls a barrier; the others wait for it at the group's own barrier and take its answer, so every warp of a group
+// takes the same decisions, always meets the others, and waits without spending issue slots.
+struct Group {
+    int which, threads;
+    bool lead;
+    volatile int* said;  // [2]
+    volatile int* abort;
+    uint32_t turn;
+    __device__ __forceinline__ void sync() { asm volatile("bar.sync %0, %1;" ::"r"(1 + which), "r"(threads) : "memory"); }
+    __device__ __forceinline__ bool wait(uint64_t* bar, uint32_t parity) {
+        const int slot = turn++ & 1;
+        if (lead) {
+            const bool ok = warp_wait(bar, parity, abort);
+            if ((threadIdx.x & 31) == 0) said[slot] = ok;
+        }
+        sync();
+        return said[slot] != 0;
+    }
 };
 
 // A chunk token by token in fp32, by the state warps: the state in TMEM times un0 / un1 (features g, g + 8 of the warp's
-// 16) is advanced over rows row .. row + nt - 1 and written back unscaled; o goes to global memory.  phase: the state
-// warps' barrier count.
+// 16) is advanced over rows row .. row + nt - 1 and written back unscaled; o goes to global memory.
 template <int DK, int DV>
-__device__ __noinline__ bool chunk_fp32(const tsv_gdn_desc& d, int layer, int h, size_t row, int nt, uint32_t state, int fb, float un0,
-                                        float un1, float* tk, uint64_t* bar, uint32_t& phase, volatile int* abort_flag) {
+__device__ __noinline__ void chunk_fp32(const tsv_gdn_desc& d, int layer, int h, size_t row, int nt, uint32_t state, int fb, float un0,
+                                        float un1, float* tk, Group& group) {
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3, hk = h / (d.HV / d.HK);
-    auto sync = [&]() -> bool {
-        __syncwarp();
-        tc::mbar_arrive_one(bar);
-        return warp_wait(bar, phase++ & 1, abort_flag);
-    };
     float S[DK / 2];  // S[32 x + 4 n + 2 half + e]: feature fb + g + 8 half, column 64 x + 8 n + 2 t + e
 #pragma unroll
     for (int x = 0; x < DK / 64; ++x) tc::tmem_ld_frag8(state + 64 * x, S + 32 * x);
@@ -86,7 +101,7 @@ __device__ __noinline__ bool chunk_fp32(const tsv_gdn_desc& d, int layer, int h,
             for (int o = 16; o > 0; o >>= 1) kq += __shfl_xor_sync(0xFFFFFFFFu, kq, o);
             if (lane == 0) tk[256] = kq;
         }
-        if (!sync()) return false;
+        group.sync();
         const float a = expf(d.g[layer][row * d.HV + h]), be = d.beta[layer][row * d.HV + h];
         float sk[2] = {0.f, 0.f}, sq[2] = {0.f, 0.f};
 #pragma unroll
@@ -112,11 +127,10 @@ __device__ __noinline__ bool chunk_fp32(const tsv_gdn_desc& d, int layer, int h,
             const int e = (x >> 5) * 64 + ((x & 31) >> 2) * 8 + 2 * t + (x & 1);
             S[x] = fmaf(sk[(x >> 1) & 1], tk[e], a * S[x]);
         }
-        if (!sync()) return false;
+        group.sync();
     }
 #pragma unroll
     for (int x = 0; x < DK / 64; ++x) tc::tmem_st_frag8f(state + 64 * x, S + 32 * x);
-    return true;
 }
 
 template <int DK, int DV>
@@ -157,22 +171,18 @@ __global__ void __launch_bounds__((kScanPrep + DV / 16) * 32, 1)
 
     if (threadIdx.x == 0) {
         for (int x = 0; x < 2; ++x) {
-            tc::mbar_init(&br.full[x], kScanPrep);
-            tc::mbar_init(&br.empty[x], SW);
+            tc::mbar_init(&br.full[x], 1);
+            tc::mbar_init(&br.empty[x], 1);
             br.bad[x] = 0;
         }
         tc::mbar_init(&br.gram, 1);
         tc::mbar_init(&br.prod, 1);
         tc::mbar_init(&br.state, 1);
-        tc::mbar_init(&br.ssync, SW);
-        tc::mbar_init(&br.psync, kScanPrep);
         tc::mbar_init(&br.drain_s, 1);
         tc::mbar_init(&br.drain_p, 1);
         br.abort = 0;
         tc::fence_mbar_init();
     }
-    for (int e = threadIdx.x; e < 2 * kScanT * 8; e += blockDim.x)  // P above its diagonal blocks, in both buffers
-        *reinterpret_cast<uint4*>(sm + (e >> 9) * M::buffer + M::p16 + (e & 511) * 16) = make_uint4(0, 0, 0, 0);
     if (warp == 1) {
         tc::tmem_alloc(&br.tmem, M::cols);
         tc::tmem_relinquish();
@@ -189,7 +199,7 @@ __global__ void __launch_bounds__((kScanPrep + DV / 16) * 32, 1)
         constexpr int LPR = DK / 8, CPR = DV / 8;
         constexpr int KQ = 2 * kScanT * LPR / PT, VC = kScanT * CPR / PT;
         const int chunk = pt % LPR;
-        uint4 kq[KQ], vv[VC];
+        uint4 kq[KQ];
         float gi[2] = {0.f, 0.f}, bi[2] = {0.f, 0.f};
         auto fetch = [&](int c) {
             const int t0 = c * kScanT;
@@ -200,13 +210,7 @@ __global__ void __launch_bounds__((kScanPrep + DV / 16) * 32, 1)
                 const uint16_t* src = reinterpret_cast<const uint16_t*>(r >= kScanT ? d.q[layer] : d.k[layer]);
                 kq[x] = i < n ? *reinterpret_cast<const uint4*>(src + ((size_t)(row0 + i) * d.HK + hk) * DK + chunk * 8) : zero;
             }
-#pragma unroll
-            for (int x = 0; x < VC; ++x) {
-                const int e = pt + x * PT, i = t0 + e / CPR;
-                vv[x] = i < n ? *reinterpret_cast<const uint4*>(reinterpret_cast<const uint16_t*>(d.v[layer]) +
-                                                                 ((size_t)(row0 + i) * d.HV + h) * DV + e % CPR * 8) : zero;
-            }
-            if (pw == 0) {
+            if (pw == 1) {
 #pragma unroll
                 for (int x = 0; x < 2; ++x) {
                     const int i = t0 + 2 * lane + x;
@@ -215,13 +219,8 @@ __global__ void __launch_bounds__((kScanPrep + DV / 16) * 32, 1)
                 }
             }
         };
-        uint32_t ps = 0;  // phases of psync
-        auto sync = [&]() -> bool {
-            __syncwarp();
-            tc::mbar_arrive_one(&br.psync);
-            return warp_wait(&br.psync, ps++ & 1, abort_flag);
-        };
-        // G of the fetched chunk: tokens 2 lane, 2 lane + 1 of the first warp; inclusive scan over the lanes
+        Group group = {1, PT, pw == 0, br.said[1], abort_flag, 0};
+        // G of the fetched chunk: tokens 2 lane, 2 lane + 1 of one warp; inclusive scan over the lanes
         Pair G[2];
         auto sum_gates = [&]() {
             G[0] = log2_decay(gi[0]);
@@ -239,7 +238,7 @@ __global__ void __launch_bounds__((kScanPrep + DV / 16) * 32, 1)
             G[1] = run;
         };
         fetch(0);
-        if (pw == 0) sum_gates();
+        if (pw == 1) sum_gates();
         bool ok = true;
         for (int c = 0; c < chunks; ++c) {
             const int buf = c & 1;
@@ -248,27 +247,32 @@ __global__ void __launch_bounds__((kScanPrep + DV / 16) * 32, 1)
             GdnKeys& ky = *reinterpret_cast<GdnKeys*>(bs + M::keys);
             GdnRows& rw = *reinterpret_cast<GdnRows*>(bs + M::rows);
             float* dj = reinterpret_cast<float*>(bs + M::dj);
-            if (c >= 2 && !warp_wait(&br.empty[buf], ((c >> 1) - 1) & 1, abort_flag)) {
-                ok = false;
-                break;
-            }
+            if (c >= 2 && !(ok = group.wait(&br.empty[buf], ((c >> 1) - 1) & 1))) break;
             if (pt == 0) br.bad[buf] = 0;  // read by the state warps before they gave the buffer back; set again after sync()
             uint32_t flag = 0;
 #pragma unroll
-            for (int x = 0; x < KQ; ++x) {
-                const int r = pt / LPR + x * (PT / LPR), i = r & 63;
-                float ss, f;
-                *reinterpret_cast<uint4*>(bs + kq_at<2 * kScanT>(M::kq, (r & 64) + 16 * block_pos<NB>(i >> 4) + (i & 15), chunk)) =
-                    stage_chunk<DK>(kq[x], ss, f, flag);
-                if (d.norm_eps > 0.f) f *= rsqrtf(ss + d.norm_eps);
-                if (chunk == 0) (r >= kScanT ? ky.fq : ky.fk)[i] = r >= kScanT ? f * d.scale : f;
-            }
-#pragma unroll
             for (int x = 0; x < VC; ++x) {
-                const int e = pt + x * PT;
-                *reinterpret_cast<uint4*>(bs + tile_at<DV * 2>(M::v, e / CPR, e % CPR)) = vv[x];
+                const int e = pt + x * PT, i = c * kScanT + e / CPR;
+                cp16(bs32 + tile_at<DV * 2>(M::v, e / CPR, e % CPR),
+                     reinterpret_cast<const uint16_t*>(d.v[layer]) + ((size_t)(row0 + min(i, n - 1)) * d.HV + h) * DV + e % CPR * 8, i < n);
             }
-            if (pw == 0) {
+            cp_commit();
+            constexpr int KH = KQ / 2;  // half of a thread's chunks at a time
+#pragma unroll
+            for (int x0 = 0; x0 < KQ; x0 += KH) {
+                uint4 w[KH];
+                float f[KH];
+#pragma unroll
+                for (int x = 0; x < KH; ++x) w[x] = kq[x0 + x];
+                stage_chunks<DK, KH>(w, f, d.norm_eps, flag);
+#pragma unroll
+                for (int x = 0; x < KH; ++x) {
+                    const int r = pt / LPR + (x0 + x) * (PT / LPR), i = r & 63;
+                    *reinterpret_cast<uint4*>(bs + kq_at<2 * kScanT>(M::kq, (r & 64) + 16 * block_pos<NB>(i >> 4) + (i & 15), chunk)) = w[x];
+                    if (chunk == 0) (r >= kScanT ? ky.fq : ky.fk)[i] = r >= kScanT ? f[x] * d.scale : f[x];
+                }
+            }
+            if (pw == 1) {
                 *reinterpret_cast<float2*>(&rw.g_hi[2 * lane]) = make_float2(G[0].hi, G[1].hi);
                 *reinterpret_cast<float2*>(&rw.g_lo[2 * lane]) = make_float2(G[0].lo, G[1].lo);
                 *reinterpret_cast<float2*>(&rw.beta[2 * lane]) = make_float2(bi[0], bi[1]);
@@ -277,12 +281,9 @@ __global__ void __launch_bounds__((kScanPrep + DV / 16) * 32, 1)
             }
             tc::fence_proxy_async_smem();
             tc::tc_fence_before();
-            if (!sync()) {
-                ok = false;
-                break;
-            }
+            group.sync();
             tc::tc_fence_after();
-            if (pt == 0) {  // [K; Q] K^T
+            if (pt == 6 * 32) {  // [K; Q] K^T, by a warp with a small share of the matrices
                 const uint32_t id = tc::idesc_f16(false, false, false, 128, kScanT);
                 const uint64_t desc = tc::sdesc_sw128(bs32 + M::kq, 16, 1024);
 #pragma unroll
@@ -294,29 +295,27 @@ __global__ void __launch_bounds__((kScanPrep + DV / 16) * 32, 1)
             }
             __syncwarp();
             if (c + 1 < chunks) fetch(c + 1);
-            if (pt < 2 * kScanT) {  // for the state warps
+            if (pt >= 2 * kScanT) {  // for the state warps
                 const int i = pt & 63;
-                const bool q = pt >= kScanT;
+                const bool q = pt >= 3 * kScanT;
                 const float x = (q ? ky.fq : ky.fk)[i], gh = rw.g_hi[i], gl = rw.g_lo[i];
                 (q ? rw.cq : rw.ck)[i] = tc::ex2_approx(gh + gl) * x;
                 if (!q) dj[i] = tc::ex2_approx((rw.g_hi[63] - gh) + (rw.g_lo[63] - gl)) * x;
                 else if (i == 63) dj[64] = tc::ex2_approx(gh + gl);
             }
             __syncwarp();
-            if (!warp_wait(&br.gram, c & 1, abort_flag)) {
-                ok = false;
-                break;
-            }
+            if (!(ok = group.wait(&br.gram, c & 1))) break;
             tc::tc_fence_after();
             warp_matrices<NB, 2>(pw & 3, pw >> 2, tmem + M::col_g, bs + M::a16, bs + M::p16, reinterpret_cast<float*>(sm + M::diag), ky, rw, flag,
                                  lane);
             if (watched(flag)) br.bad[buf] = 1;
             tc::tc_fence_before();
-            __syncwarp();
-            tc::mbar_arrive_one(&br.full[buf]);
-            if (pw == 0) sum_gates();
+            cp_wait<0>();  // V
+            group.sync();
+            if (pt == 0) tc::mbar_arrive(&br.full[buf]);
+            if (pw == 1) sum_gates();
         }
-        if (!ok && pt == 0) {  // let this thread's MMAs end
+        if (!ok && pt == 6 * 32) {  // let this thread's MMAs end
             tc::mma_commit(&br.drain_p);
             tc::mbar_drain(&br.drain_p, 0);
         }
@@ -326,12 +325,7 @@ __global__ void __launch_bounds__((kScanPrep + DV / 16) * 32, 1)
         const int fb = DV == 128 ? lane0 : warp * 16;                                  // value features
         const uint32_t la = tmem + ((uint32_t)lane0 << 16);
         const int vrow = ((lane >> 4) << 3) + (lane & 7), vchunk = fb / 8 + ((lane >> 3) & 1);
-        uint32_t ss = 0;  // phases of ssync
-        auto sync = [&]() -> bool {
-            __syncwarp();
-            tc::mbar_arrive_one(&br.ssync);
-            return warp_wait(&br.ssync, ss++ & 1, abort_flag);
-        };
+        Group group = {0, SW * 32, warp == 0, br.said[0], abort_flag, 0};
         // 64 columns of the state at a time: r[4 n + 2 half + e] = S[fb + g + 8 half][64 x + 8 n + 2 t + e]
         float r[32];
         const float* S = d.state[layer] + state0 + (size_t)(fb + g) * DK + 2 * t;
@@ -358,7 +352,7 @@ __global__ void __launch_bounds__((kScanPrep + DV / 16) * 32, 1)
             const float* dj = reinterpret_cast<const float*>(bs + M::dj);
             const int nt = min(kScanT, n - c * kScanT);
             uint32_t flag = 0;
-            if (!warp_wait(&br.full[buf], (c >> 1) & 1, abort_flag)) { ok = false; break; }
+            if (!(ok = group.wait(&br.full[buf], (c >> 1) & 1))) break;
             // each feature's power-of-two scale from the largest of its state row and v
             float mx[2] = {0.f, 0.f}, sx[2] = {0.f, 0.f}, down[2], sc[2];
             uint32_t vf[NB][4];
@@ -373,11 +367,6 @@ __global__ void __launch_bounds__((kScanPrep + DV / 16) * 32, 1)
             // The decay over the chunk.  Unless it is next to nothing the state is decayed (and scaled) in TMEM at once:
             // should the chunk have to be done again in fp32, the state can be had back.
             const bool early = e_n >= 0x1p-60f;
-            if (c > 0) {  // the state of the chunk before, whose buffer is then free
-                if (!warp_wait(&br.state, (c - 1) & 1, abort_flag)) { ok = false; break; }
-                __syncwarp();
-                tc::mbar_arrive_one(&br.empty[buf ^ 1]);
-            }
             tc::tc_fence_after();
             float S2[DK / 2];  // this thread's part of the state
 #pragma unroll
@@ -416,7 +405,7 @@ __global__ void __launch_bounds__((kScanPrep + DV / 16) * 32, 1)
             }
             tc::tmem_wait_st();
             tc::tc_fence_before();
-            if (!sync()) { ok = false; break; }
+            group.sync();
             const uint64_t desc = tc::sdesc_sw128(bs32 + M::kq, 16, 1024);
             if (threadIdx.x == 0) {  // S [K; Q]^T
                 tc::tc_fence_after();
@@ -432,7 +421,7 @@ __global__ void __launch_bounds__((kScanPrep + DV / 16) * 32, 1)
                 tc::mma_commit(&br.prod);
             }
             __syncwarp();
-            if (!warp_wait(&br.prod, c & 1, abort_flag)) { ok = false; break; }
+            if (!(ok = group.wait(&br.prod, c & 1))) break;
             tc::tc_fence_after();
 
             float ak[NB][2][4];
@@ -449,27 +438,18 @@ __global__ void __launch_bounds__((kScanPrep + DV / 16) * 32, 1)
                 ldsm4_t(vf[bb], tile_at<DV * 2>(bs32 + M::v, bb * 16 + vrow, vchunk));
                 block_rhs(bb, ak[bb], vf[bb], down, rw, t);
             }
-            uint32_t Uh[NB][4];  // rolled loops: the block in turn is ak[0], and Uh fills up from its end
-#pragma unroll 1
+            uint32_t Uh[NB][4];
+#pragma unroll
             for (int bb = 0; bb < NB; ++bb) {
                 uint32_t Uf[2][4];
                 float u[2][4];
-                block_solve<NB, 2>(bb, ak[0], Uf, u, bs32 + M::a16, flag, lane);
+                block_solve<NB, 2>(bb, ak[bb], Uf, u, bs32 + M::a16, flag, lane);
 #pragma unroll
-                for (int bn = 1; bn < NB; ++bn)
-                    if (bb + bn < NB) block_update<NB, 2>(bb + bn, bb, ak[bn], Uf, bs32 + M::a16, lane);
-#pragma unroll
-                for (int bn = 0; bn < NB - 1; ++bn)
-#pragma unroll
-                    for (int x = 0; x < 4; ++x) {
-                        ak[bn][0][x] = ak[bn + 1][0][x];
-                        ak[bn][1][x] = ak[bn + 1][1][x];
-                        Uh[bn][x] = Uh[bn + 1][x];
-                    }
+                for (int bn = bb + 1; bn < NB; ++bn) block_update<NB, 2>(bn, bb, ak[bn], Uf, bs32 + M::a16, lane);
                 // u for the state, over the state's pieces
                 uint32_t hi[4], lo[4];
 #pragma unroll
-                for (int x = 0; x < 4; ++x) Uh[NB - 1][x] = Uf[0][x];
+                for (int x = 0; x < 4; ++x) Uh[bb][x] = Uf[0][x];
 #pragma unroll
                 for (int nn = 0; nn < 2; ++nn) {
                     const float2 z = *reinterpret_cast<const float2*>(&dj[bb * 16 + nn * 8 + 2 * t]);
@@ -482,8 +462,8 @@ __global__ void __launch_bounds__((kScanPrep + DV / 16) * 32, 1)
                 tc::tmem_st_frag2(la + M::col_hi + 8 * block_pos<NB>(bb), hi);
                 tc::tmem_st_frag2(la + M::col_lo + 8 * block_pos<NB>(bb), lo);
             }
-            // o over v's place; P is zero above its diagonal blocks
-#pragma unroll 1
+            // o over v's place
+#pragma unroll
             for (int bb = 0; bb < NB; ++bb) {
                 float x8[8], aq[2][4];
                 uint32_t w[4];
@@ -493,7 +473,7 @@ __global__ void __launch_bounds__((kScanPrep + DV / 16) * 32, 1)
                 for (int x = 0; x < 8; ++x) aq[x >> 2][x & 3] = x8[x];
                 block_rhs_q(bb, aq, rw, t);
 #pragma unroll
-                for (int cc = 0; cc < NB; ++cc) block_out(bb, cc, aq, Uh[cc], bs32 + M::p16, lane);
+                for (int cc = 0; cc <= bb; ++cc) block_out(bb, cc, aq, Uh[cc], bs32 + M::p16, lane);
 #pragma unroll
                 for (int nn = 0; nn < 2; ++nn)
 #pragma unroll
@@ -504,16 +484,15 @@ __global__ void __launch_bounds__((kScanPrep + DV / 16) * 32, 1)
             if (watched(flag)) br.bad[buf] = 1;
             tc::tmem_wait_st();
             tc::tc_fence_before();
-            if (!sync()) { ok = false; break; }
+            group.sync();
             const bool bad = *reinterpret_cast<volatile int*>(&br.bad[buf]) != 0;
             if (bad) {
                 // fp32, token by token: an operand left fp16's range.  Not finite inputs then reach what the recurrence
                 // lets them reach: later tokens, and with v only their own feature.  What TMEM holds times un is the
                 // state ahead of the chunk.
                 const float un0 = early ? up[0] / e_n : sc[0] * up[0], un1 = early ? up[1] / e_n : sc[1] * up[1];
-                ok = chunk_fp32<DK, DV>(d, layer, h, (size_t)row0 + (size_t)c * kScanT, nt, la + M::col_s, fb, un0, un1,
-                                        reinterpret_cast<float*>(sm + M::slow), &br.ssync, ss, abort_flag);
-                if (!ok) break;
+                chunk_fp32<DK, DV>(d, layer, h, (size_t)row0 + (size_t)c * kScanT, nt, la + M::col_s, fb, un0, un1,
+                                   reinterpret_cast<float*>(sm + M::slow), group);
                 up[0] = up[1] = 1.f;
             } else if (!early) {
 #pragma unroll 1
@@ -528,7 +507,7 @@ __global__ void __launch_bounds__((kScanPrep + DV / 16) * 32, 1)
             if (bad || !early) {
                 tc::tmem_wait_st();
                 tc::tc_fence_before();
-                if (!sync()) { ok = false; break; }
+                group.sync();
             }
             if (threadIdx.x == 0) {  // S += U'^T K
                 tc::tc_fence_after();
@@ -554,8 +533,10 @@ __global__ void __launch_bounds__((kScanPrep + DV / 16) * 32, 1)
                         *reinterpret_cast<const uint4*>(bs + tile_at<DV * 2>(M::v, i, cc));
                 }
             }
+            // the new state, with which the buffer is free
+            if (!(ok = group.wait(&br.state, c & 1))) break;
+            if (threadIdx.x == 0) tc::mbar_arrive(&br.empty[buf]);
         }
-        if (ok) ok = warp_wait(&br.state, (chunks - 1) & 1, abort_flag);
         if (ok) {
             tc::tc_fence_after();
             float* out = d.state_out[layer] + state0 + (size_t)(fb + g) * DK + 2 * t;

@@ -150,7 +150,6 @@ __device__ __forceinline__ uint32_t tile_at(uint32_t base, int row, int chunk) {
 struct GdnKeys {
     uint64_t before[64];   // rows ahead of i in its system (strict ancestors, or earlier tokens)
     float fk[64], fq[64];  // what a staged row's products are multiplied with: its scale and norm (and q's scale)
-    float sk[64], sq[64];  // sums of squares
 };
 struct GdnRows {
     float g_hi[64], g_lo[64];  // G in units of ln 2, as hi + lo (differences of far sums keep fp32 accuracy)
@@ -158,27 +157,44 @@ struct GdnRows {
     float ck[64], cq[64];      // 2^G fk, 2^G fq
 };
 
-// One chunk of 8 bf16 values of a K or Q row -> fp16, scaled by a power of two that brings the row's norm to [1, 2);
-// DK / 8 consecutive lanes share a row.  ss: the row's sum of squares; up: what the scaling divided by.
-template <int DK>
-__device__ __forceinline__ uint4 stage_chunk(uint4 w, float& ss, float& up, uint32_t& flag) {
-    float2 x[4] = {{bf16_lo(w.x), bf16_hi(w.x)}, {bf16_lo(w.y), bf16_hi(w.y)}, {bf16_lo(w.z), bf16_hi(w.z)}, {bf16_lo(w.w), bf16_hi(w.w)}};
-    float2 s2 = mul2(x[0], x[0]);
+// N chunks of 8 bf16 values, each of a K or Q row of its own -> fp16 in place, scaled by a power of two that brings the
+// row's norm to [1, 2); DK / 8 consecutive lanes share a row.  f: what the row's products are to be multiplied with,
+// its scale over its norm.  The chunks go through each step together: their shuffles overlap, and there is no branch.
+template <int DK, int N>
+__device__ __forceinline__ void stage_chunks(uint4 (&w)[N], float (&f)[N], float norm_eps, uint32_t& flag) {
+    float ss[N];
 #pragma unroll
-    for (int e = 1; e < 4; ++e) s2 = fma2(x[e], x[e], s2);
-    ss = s2.x + s2.y;
+    for (int x = 0; x < N; ++x) {
+        const uint32_t y[4] = {w[x].x, w[x].y, w[x].z, w[x].w};
+        float2 s2 = make_float2(0.f, 0.f);
 #pragma unroll
-    for (int o = DK / 16; o > 0; o >>= 1) ss += __shfl_xor_sync(0xFFFFFFFFu, ss, o);
-    const int es = (int)(__float_as_uint(ss) >> 23) & 255;
-    const int e = es == 0 || es == 255 ? 0 : (es - 127) >> 1;
-    const float down = __uint_as_float((uint32_t)(127 - e) << 23);
-    up = __uint_as_float((uint32_t)(127 + e) << 23);
-    // squares that underflowed: the fp32 path
-    if (ss < 1e-30f && ((w.x | w.y | w.z | w.w) & 0x7FFF7FFFu)) flag = 0x7FFF7FFFu;
-    const float2 d2 = make_float2(down, down);
+        for (int e = 0; e < 4; ++e) {
+            const float2 z = make_float2(bf16_lo(y[e]), bf16_hi(y[e]));
+            s2 = fma2(z, z, s2);
+        }
+        ss[x] = s2.x + s2.y;
+    }
 #pragma unroll
-    for (int k = 0; k < 4; ++k) x[k] = mul2(x[k], d2);
-    return make_uint4(f16x2(x[0].x, x[0].y), f16x2(x[1].x, x[1].y), f16x2(x[2].x, x[2].y), f16x2(x[3].x, x[3].y));
+    for (int o = DK / 16; o > 0; o >>= 1)
+#pragma unroll
+        for (int x = 0; x < N; ++x) ss[x] += __shfl_xor_sync(0xFFFFFFFFu, ss[x], o);
+#pragma unroll
+    for (int x = 0; x < N; ++x) {
+        const int es = (int)(__float_as_uint(ss[x]) >> 23);
+        const int e = es == 0 || es >= 255 ? 0 : (es - 127) >> 1;
+        const float down = __uint_as_float((uint32_t)(127 - e) << 23), up = __uint_as_float((uint32_t)(127 + e) << 23);
+        // squares that underflowed: the fp32 path
+        flag = ss[x] < 1e-30f && ((w[x].x | w[x].y | w[x].z | w[x].w) & 0x7FFF7FFFu) ? 0x7FFF7FFFu : flag;
+        f[x] = norm_eps > 0.f ? up * rsqrtf(ss[x] + norm_eps) : up;
+        const uint32_t y[4] = {w[x].x, w[x].y, w[x].z, w[x].w};
+        uint32_t z[4];
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+            const float2 a = mul2(make_float2(bf16_lo(y[k]), bf16_hi(y[k])), make_float2(down, down));
+            z[k] = f16x2(a.x, a.y);
+        }
+        w[x] = make_uint4(z[0], z[1], z[2], z[3]);
+    }
 }
 
 // K and Q as operand tiles: DK / 64 blocks of [ROWS][128 B], 128-byte swizzled; chunk 0 .. DK / 8 - 1 of a row.
@@ -309,8 +325,8 @@ __device__ __forceinline__ void warp_matrices(int qt, int m, uint32_t gram, char
     const bool q = NB == 4 ? qt >= 2 : 2 * qt + m >= NB;
     int b, c0 = 0, c1, parts = 1;
     if constexpr (NB == 4) {
-        b = qt & 1 ? m + 1 : (m == 0 ? 0 : 3);  // blocks 1 and 2, or 0 with half of 3 and the rest of 3
-        c0 = b == 3 ? 2 : 0;
+        b = qt & 1 ? m + 1 : (m == 0 ? 0 : 3);  // blocks 1 and 2, or 0 with the first product of 3 and the rest of 3
+        c0 = b == 3 ? 1 : 0;
         parts = b == 0 ? 2 : 1;
     } else {
         b = q ? 2 * qt + m - NB : 2 * qt + m;
@@ -325,9 +341,9 @@ __device__ __forceinline__ void warp_matrices(int qt, int m, uint32_t gram, char
             __syncwarp();
             block_inverse<NB, PIECES>(b, a16, diag + b * 16 * kDiag, lane);
         }
-        b = 3;  // the second part: the first half of block 3
+        b = 3;  // the second part: the first product of block 3
         c0 = 0;
-        c1 = 2;
+        c1 = 1;
     }
 }
 

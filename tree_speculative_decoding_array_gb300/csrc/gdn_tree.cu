@@ -237,16 +237,20 @@ __global__ void __launch_bounds__(2 * DV, 2) gdn_tree_kernel(const __grid_consta
     fetch_s(0);
     uint32_t flag_kq = 0;
     cp_wait<1>();  // this thread's own chunks of K and Q: converted in place
+    constexpr int KH = KQ >= 4 ? KQ / 4 : 1;
 #pragma unroll
-    for (int x = 0; x < KQ; ++x) {
-        const int r = threadIdx.x / LPR + x * (kThreads / LPR);
-        char* at = sm + kq_at<2 * T16>(M::kq, row_pos<NB>(r), chunk);
-        float ss, upr;
-        *reinterpret_cast<uint4*>(at) = stage_chunk<DK>(*reinterpret_cast<const uint4*>(at), ss, upr, flag_kq);
-        if (chunk == 0) {  // the row's factor is finished below
-            const int i = r >= T16 ? r - T16 : r;
-            (r >= T16 ? ky.fq : ky.fk)[i] = upr;
-            (r >= T16 ? ky.sq : ky.sk)[i] = ss;
+    for (int x0 = 0; x0 < KQ; x0 += KH) {
+        uint4 w[KH];
+        float f[KH];
+#pragma unroll
+        for (int x = 0; x < KH; ++x)
+            w[x] = *reinterpret_cast<const uint4*>(sm + kq_at<2 * T16>(M::kq, row_pos<NB>(threadIdx.x / LPR + (x0 + x) * (kThreads / LPR)), chunk));
+        stage_chunks<DK, KH>(w, f, d.norm_eps, flag_kq);
+#pragma unroll
+        for (int x = 0; x < KH; ++x) {
+            const int r = threadIdx.x / LPR + (x0 + x) * (kThreads / LPR);
+            *reinterpret_cast<uint4*>(sm + kq_at<2 * T16>(M::kq, row_pos<NB>(r), chunk)) = w[x];
+            if (chunk == 0) (r >= T16 ? ky.fq : ky.fk)[r >= T16 ? r - T16 : r] = r >= T16 ? f[x] * d.scale : f[x];
         }
     }
     tc::fence_proxy_async_smem();
@@ -277,10 +281,7 @@ __global__ void __launch_bounds__(2 * DV, 2) gdn_tree_kernel(const __grid_consta
             }
             if (threadIdx.x < 2 * T16) {
                 const int r = threadIdx.x, i = r >= T16 ? r - T16 : r;
-                float* f = r >= T16 ? ky.fq : ky.fk;
-                float x = f[i] * (r >= T16 ? d.scale : 1.f);
-                if (d.norm_eps > 0.f) x /= sqrtf((r >= T16 ? ky.sq : ky.sk)[i] + d.norm_eps);
-                f[i] = x;
+                const float x = (r >= T16 ? ky.fq : ky.fk)[i];
                 for (int y = 0; y < heads; ++y)
                     (r >= T16 ? rows[y].cq : rows[y].ck)[i] = tc::ex2_approx(rows[y].g_hi[i] + rows[y].g_lo[i]) * x;
             }
