@@ -39,11 +39,47 @@ bool tc_wide(const tsv_attn_desc* d);
 tsv_status launch_tc(const tsv_attn_desc* d, int splits, int chunk, float* ws_o, float* ws_ml, int32_t* status,
                      cudaStream_t stream);
 
+// Defined in attention_i4.cu.
+int few_rows(const tsv_attn_desc* d);
+void launch_few(const tsv_attn_desc* d, int splits, int chunk, float* ws_o, float* ws_ml, int32_t* status, cudaStream_t stream);
+
+constexpr int kPathFew = 100;  // the few-row kernel of 4-bit caches, chosen by AUTO alone
+
+// 4-bit caches take the few-row kernel up to 16 query rows per K/V stream, and wherever the tcgen05 kernel does not apply.
+static bool few_applies(const tsv_attn_desc* d) {
+    return d->kv_dtype == TSV_I4_G64 && d->path == TSV_ATTN_AUTO && ((d->HQ / d->HKV) * d->T <= 16 || !tc_supported(d));
+}
+
 static AttnGeom attn_geom(const tsv_attn_desc* d) {
     AttnGeom g;
     g.rows_unit = (d->HQ / d->HKV) * d->T;
     g.units = d->n_layers * d->B * d->HKV;
     g.rgs = (g.rows_unit + kRB - 1) / kRB;
+    if (few_applies(d)) {
+        // 64 keys (four warps' steps) are a unit of work.  Enough splits for `slots` CTAs at a time; the time of s splits
+        // is waves(s) x (fixed CTA cost, worth about 6 units: Q, the first loads, the merge) + units per split).
+        g.path = kPathFew;
+        g.rgs = (g.rows_unit + few_rows(d) - 1) / few_rows(d);
+        const long long base = (long long)g.units * g.rgs, slots = (long long)sm_count() * (few_rows(d) == 8 ? 3 : 2);
+        const long long tiles = (d->max_kv_len + 63) / 64;
+        const int cap_s = tiles < 64 ? (int)tiles : 64;
+        int s = d->splits;
+        if (s <= 0) {
+            double best = 1e300;
+            s = 1;
+            for (int c = 1; c <= cap_s; ++c) {
+                const long long waves = (base * c + slots - 1) / slots;
+                const double time = (double)waves * (6.0 + (double)((tiles + c - 1) / c)) + (c > 1 ? 2.0 : 0.0);
+                if (time < best * 0.98) {
+                    best = time;
+                    s = c;
+                }
+            }
+        }
+        g.splits = s;
+        g.chunk = (int)(((d->max_kv_len + s - 1) / s + 63) / 64 * 64);
+        return g;
+    }
     g.path = (d->path >= TSV_ATTN_TCGEN05 || (d->path == TSV_ATTN_AUTO && tc_supported(d))) ? TSV_ATTN_TCGEN05
                                                                                            : TSV_ATTN_SIMT;
     // key tiles: 128 for the tcgen05 128-key kernel, 64 for its 64-key kernels, kBK for the CUDA cores
@@ -488,6 +524,14 @@ extern "C" tsv_status tsv_tree_verify_attention(const tsv_attn_desc* d, void* wo
         return fail(TSV_ECAPACITY, "tree_verify_attention: workspace %zu < %zu bytes", ws_bytes, need);
     float* ws_o = (float*)workspace;
     float* ws_ml = need ? (float*)((char*)workspace + ((((size_t)g.units * g.splits * g.rows_unit) * d->D * 4 + 255) & ~(size_t)255)) : nullptr;
+    if (g.path == kPathFew) {
+        launch_few(d, g.splits, g.chunk, ws_o, ws_ml, dev_status, stream);
+        st = check_launch("tree_verify_attention(4-bit)");
+        if (st != TSV_OK || g.splits == 1) return st;
+        dim3 cg((g.rows_unit + kCombRows - 1) / kCombRows, g.units);
+        launch_pdl(attn_combine_kernel, cg, kCombRows * 32, 0, stream, *d, g.splits, ws_o, ws_ml);
+        return check_launch("tree_verify_attention(combine)");
+    }
     if (g.path == TSV_ATTN_TCGEN05) {
         st = launch_tc(d, g.splits, g.chunk, ws_o, ws_ml, dev_status, stream);
         if (st != TSV_OK || g.splits == 1) return st;
