@@ -212,9 +212,9 @@ __device__ __forceinline__ void i4x8_to_f16x8(uint32_t w, __half2 s2, __half2 b2
 }
 
 // Raw 4-bit tile [64 keys x 128 B], 128-byte swizzled as TMA lands it -> the same fp16 operand tile as
-// convert_i8_tile; `pairs` holds this thread's key's four (scale, bias) pairs.  Keys >= nk become 0 whatever their
-// bytes are.  Thread ct takes key ct & 63 and the chunks 2 s + (ct >> 6): 32 codes each, within one group of 64.
-__device__ __forceinline__ void convert_i4_tile(const uint8_t* raw, uint8_t* dst, int nk, int ct, uint4 pairs) {
+// convert_i8_tile; `pairs` holds this thread's key's four (scale, bias) pairs, zeros past the key range (any code then
+// gives 0).  Thread ct takes key ct & 63 and the chunks 2 s + (ct >> 6): 32 codes each, within one group of 64.
+__device__ __forceinline__ void convert_i4_tile(const uint8_t* raw, uint8_t* dst, int ct, uint4 pairs) {
     const int key = ct & 63, k7 = key & 7;
     const uint32_t pr[4] = {pairs.x, pairs.y, pairs.z, pairs.w};
     uint4 in[4];
@@ -233,8 +233,7 @@ __device__ __forceinline__ void convert_i4_tile(const uint8_t* raw, uint8_t* dst
         for (int c = 0; c < 4; ++c) {
             uint32_t o[4];
             i4x8_to_f16x8(w[c], s2, b2, o);
-            const uint4 v = key < nk ? make_uint4(o[0], o[1], o[2], o[3]) : make_uint4(0, 0, 0, 0);
-            *reinterpret_cast<uint4*>(rb + (((4 * (ct >> 6) + c) ^ k7) << 4)) = v;
+            *reinterpret_cast<uint4*>(rb + (((4 * (ct >> 6) + c) ^ k7) << 4)) = make_uint4(o[0], o[1], o[2], o[3]);
         }
     }
 }
@@ -519,66 +518,75 @@ __global__ void __launch_bounds__(FMT != 0 ? kTcThreadsI8 : kTc64Threads16, 1) a
                 drain_wait(drain, 0);
             }
         }
-    } else if (I8 && warp >= 10 && warp < 14) {
+    } else if (I4 && warp >= 6 && warp < 14) {
+        // ------------------------------------------------------------ 4-bit converters: warps 6-9 K, 10-13 V
+        // (one piece of code for both: the kernel's roles share the instruction cache).  As the Int8 converters: key
+        // ct & 63 of every tile, its (scale, bias) pairs fetched one tile ahead.  An fp16 K slot is free once Q K^T of
+        // tile j - 2 is done, an fp16 V slot once P V of tile j - 2 is.
+        const bool isK = warp < 10;
+        const int ct = (threadIdx.x - 192) & 127;
+        const uint4* src = reinterpret_cast<const uint4*>(isK ? p.ks[layer] : p.vs[layer]) + ((size_t)b * p.HKV + kvh) * (size_t)p.s_cap + k_begin + (ct & 63);
+        uint64_t *full = isK ? kfull : vfull, *empty = isK ? kempty : vempty, *slot_free = isK ? s_full : sp_free, *done = isK ? kc_full : vc_full;
+        const uint8_t* raw = isK ? sRawK : sRawV;
+        uint8_t* dst = isK ? sK : sV;
+        auto pairs = [&](int jj) {
+            return jj < ntiles && k_begin + jj * kTcBK + (ct & 63) < k_end ? src[(size_t)jj * kTcBK] : make_uint4(0, 0, 0, 0);
+        };
+        uint4 next = pairs(0);
+        for (int j = 0; j < ntiles; ++j) {
+            const int st = j % NS, cb = j & 1;
+            const uint4 sc = next;
+            next = pairs(j + 1);
+            if (!__all_sync(0xFFFFFFFFu, tc::mbar_wait(&full[st], (j / NS) & 1, abort_flag))) break;
+            if (j >= 2 && !__all_sync(0xFFFFFFFFu, tc::mbar_wait(&slot_free[cb], ((j >> 1) - 1) & 1, abort_flag))) break;
+            convert_i4_tile(raw + st * 16384, dst + cb * kTileBytes, ct, sc);
+            tc::fence_proxy_async_smem();
+            __syncwarp();
+            tc::mbar_arrive_one(&empty[st]);
+            tc::mbar_arrive_one(&done[cb]);
+        }
+    } else if (I8 && !I4 && warp >= 10 && warp < 14) {
         // ------------------------------------------------------------ Int8 V converters
         // each thread converts key ct & 63 of every tile and multiplies its codes by that key's scale; the scale
         // is fetched one tile ahead so that the global load's latency overlaps the previous tile's work
         const int ct = threadIdx.x - 320;
-        const size_t key0 = ((size_t)b * p.HKV + kvh) * (size_t)p.s_cap + k_begin + (ct & 63);
-        auto vscale = [&](int jj) {
-            const bool real = jj < ntiles && k_begin + jj * kTcBK + (ct & 63) < k_end;
-            if constexpr (I4)
-                return real ? reinterpret_cast<const uint4*>(p.vs[layer])[key0 + (size_t)jj * kTcBK] : make_uint4(0, 0, 0, 0);
-            else
-                return real ? p.vs[layer][key0 + (size_t)jj * kTcBK] : (uint16_t)0;
+        const uint16_t* vsrc = p.vs[layer] + ((size_t)b * p.HKV + kvh) * (size_t)p.s_cap + k_begin + (ct & 63);
+        auto vscale = [&](int jj) -> uint16_t {
+            return (jj < ntiles && k_begin + jj * kTcBK + (ct & 63) < k_end) ? vsrc[jj * kTcBK] : (uint16_t)0;
         };
-        auto sc_next = vscale(0);
+        uint16_t sc_next = vscale(0);
         for (int j = 0; j < ntiles; ++j) {
             const int st = j % NS, cb = j & 1;
-            const auto sc = sc_next;
+            const __half sh = __ushort_as_half(sc_next);
             sc_next = vscale(j + 1);
             if (!__all_sync(0xFFFFFFFFu, tc::mbar_wait(&vfull[st], (j / NS) & 1, abort_flag))) break;
             const int nk = min(kTcBK, k_end - (k_begin + j * kTcBK));
             // fp16 V slot cb free once P V of tile j - 2 is done
             if (j >= 2 && !__all_sync(0xFFFFFFFFu, tc::mbar_wait(&sp_free[cb], ((j >> 1) - 1) & 1, abort_flag))) break;
-            if constexpr (I4) {
-                convert_i4_tile(sRawV + st * 16384, sV + cb * kTileBytes, nk, ct, sc);
-            } else {
-                const __half sh = __ushort_as_half(sc);
-                convert_i8_tile_scaled(sRawV + st * 16384, sV + cb * kTileBytes, nk, ct, __halves2half2(sh, sh));
-            }
+            convert_i8_tile_scaled(sRawV + st * 16384, sV + cb * kTileBytes, nk, ct, __halves2half2(sh, sh));
             tc::fence_proxy_async_smem();
             __syncwarp();
             tc::mbar_arrive_one(&vempty[st]);
             tc::mbar_arrive_one(&vc_full[cb]);
         }
-    } else if (I8 && warp >= 6 && warp < 10) {
+    } else if (I8 && !I4 && warp >= 6 && warp < 10) {
         // ------------------------------------------------------------ Int8 K converters
         // as the V converters: key ct & 63 of every tile, times its scale, fetched one tile ahead
         const int ct = threadIdx.x - 192;
-        const size_t key0 = ((size_t)b * p.HKV + kvh) * (size_t)p.s_cap + k_begin + (ct & 63);
-        auto kscale = [&](int jj) {
-            const bool real = jj < ntiles && k_begin + jj * kTcBK + (ct & 63) < k_end;
-            if constexpr (I4)
-                return real ? reinterpret_cast<const uint4*>(p.ks[layer])[key0 + (size_t)jj * kTcBK] : make_uint4(0, 0, 0, 0);
-            else
-                return real ? p.ks[layer][key0 + (size_t)jj * kTcBK] : (uint16_t)0;
+        const uint16_t* ksrc = p.ks[layer] + ((size_t)b * p.HKV + kvh) * (size_t)p.s_cap + k_begin + (ct & 63);
+        auto kscale = [&](int jj) -> uint16_t {
+            return (jj < ntiles && k_begin + jj * kTcBK + (ct & 63) < k_end) ? ksrc[jj * kTcBK] : (uint16_t)0;
         };
-        auto sc_next = kscale(0);
+        uint16_t sc_next = kscale(0);
         for (int j = 0; j < ntiles; ++j) {
             const int st = j % NS, cb = j & 1;
-            const auto sc = sc_next;
+            const __half sh = __ushort_as_half(sc_next);
             sc_next = kscale(j + 1);
             if (!__all_sync(0xFFFFFFFFu, tc::mbar_wait(&kfull[st], (j / NS) & 1, abort_flag))) break;
             const int nk = min(kTcBK, k_end - (k_begin + j * kTcBK));
             // fp16 K slot cb free once Q K^T of tile j - 2 is done
             if (j >= 2 && !__all_sync(0xFFFFFFFFu, tc::mbar_wait(&s_full[cb], ((j >> 1) - 1) & 1, abort_flag))) break;
-            if constexpr (I4) {
-                convert_i4_tile(sRawK + st * 16384, sK + cb * kTileBytes, nk, ct, sc);
-            } else {
-                const __half sh = __ushort_as_half(sc);
-                convert_i8_tile_scaled(sRawK + st * 16384, sK + cb * kTileBytes, nk, ct, __halves2half2(sh, sh));
-            }
+            convert_i8_tile_scaled(sRawK + st * 16384, sK + cb * kTileBytes, nk, ct, __halves2half2(sh, sh));
             tc::fence_proxy_async_smem();
             __syncwarp();
             tc::mbar_arrive_one(&kempty[st]);
@@ -653,10 +661,19 @@ __global__ void __launch_bounds__(FMT != 0 ? kTcThreadsI8 : kTc64Threads16, 1) a
         const float qk_scale = 1.4426950408889634f * 0.0625f;  // log2(e) / sqrt(256)
         float m_ref = -INFINITY, l = 0.f;
         bool ok = true;
+        // 4-bit caches: two warps whose 32 rows are all padding leave S and P as they are (a row of P only reaches its
+        // own row of O, which nobody reads) and the issue slots to the converters.
+        const bool idle = I4 && row0 + qd * 32 >= p.R;
         for (int j = 0; j < ntiles; ++j) {
             const int sb = j & 1;
-            if (!__all_sync(0xFFFFFFFFu, tc::mbar_wait(&s_full[sb], (j >> 1) & 1, abort_flag))) { ok = false; break; }
+            if (!__all_sync(0xFFFFFFFFu, tc::mbar_wait(&s_full[sb], (j >> 1) & 1, abort_flag, idle ? 256 : 32))) { ok = false; break; }
             tc::tc_fence_after();
+            if (idle) {
+                __syncwarp();
+                tc::mbar_arrive_one(s_free);
+                tc::mbar_arrive_one(&p_full[sb]);
+                continue;
+            }
             uint32_t sc[32];
             tc::tmem_ld32(tmem + lane_base + kColS + (I8 ? 0 : sb * kTcBK) + h * 32, sc);
             tc::tmem_wait_ld();
@@ -764,7 +781,7 @@ __global__ void __launch_bounds__(FMT != 0 ? kTcThreadsI8 : kTc64Threads16, 1) a
             __syncwarp();
             tc::mbar_arrive_one(&p_full[sb]);
         }
-        if (ok) {  // the row sum of both halves
+        if (ok && !idle) {  // the row sum of both halves
             float lo;
             if (exchange(ntiles, l, lo)) l += lo;
             else ok = false;
