@@ -200,7 +200,7 @@ void launch_gdn_tree(const tsv_gdn_desc& d, const uint64_t* anc, int32_t* status
 void launch_gdn_scan(const tsv_gdn_desc& d, const int32_t* cu_len, int max_len, int32_t* status, cudaStream_t stream);
 
 // Sequences of up to this many tokens are advanced token by token, longer ones in chunks.
-constexpr int kRecurMax = 16;
+constexpr int kRecurMax = 14;
 
 enum GdnCall { kGdnVerify, kGdnCommit, kGdnScan };
 

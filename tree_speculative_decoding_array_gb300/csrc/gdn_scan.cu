@@ -2,7 +2,8 @@
 //
 // A chunk is one triangular system (gdn_tc.cuh) whose rows are consecutive tokens, and the state moves on by
 //     S <- e^{G_n} S + sum_j e^{G_n - G_j} u_j k_j^T        (n: the chunk's last token)
-// One persistent CTA per (layer, sequence, value head) walks its chunks.  Two groups of warps work a chunk apart:
+// One persistent CTA per (layer, sequence, value head) walks its chunks - or two, of half the value features each, where
+// the heads alone would leave half of the SMs idle.  Two groups of warps work a chunk apart:
 //   8 preparing warps   stage K, Q, V and the gates of a chunk, take [K; Q] K^T on the tensor cores and build the
 //                       system's matrices; two buffers, so they run up to two chunks ahead.  A chunk's global loads
 //                       are issued while the one before is prepared.
@@ -22,6 +23,7 @@ namespace tsv {
 constexpr int kScanPrep = 8;  // preparing warps
 constexpr int kScanT = 64;    // tokens per chunk
 constexpr int kScanNB = 4;
+constexpr int kScanSort = 256;  // batches up to this size are started longest sequence first
 
 template <int DK, int DV>
 struct ScanSmem {
@@ -76,7 +78,7 @@ struct Group {
 
 // A chunk token by token in fp32, by the state warps: the state in TMEM times un0 / un1 (features g, g + 8 of the warp's
 // 16) is advanced over rows row .. row + nt - 1 and written back unscaled; o goes to global memory.
-template <int DK, int DV>
+template <int DK>
 __device__ __noinline__ void chunk_fp32(const tsv_gdn_desc& d, int layer, int h, size_t row, int nt, uint32_t state, int fb, float un0,
                                         float un1, float* tk, Group& group) {
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3, hk = h / (d.HV / d.HK);
@@ -117,7 +119,7 @@ __device__ __noinline__ void chunk_fp32(const tsv_gdn_desc& d, int layer, int h,
                 sk[half] += __shfl_xor_sync(0xFFFFFFFFu, sk[half], o);
                 sq[half] += __shfl_xor_sync(0xFFFFFFFFu, sq[half], o);
             }
-            const size_t at = (row * d.HV + h) * DV + fb + g + 8 * half;
+            const size_t at = (row * d.HV + h) * d.DV + fb + g + 8 * half;
             const float u = be * (bf16_bits_to_f32(reinterpret_cast<const uint16_t*>(d.v[layer])[at]) - a * sk[half]);
             if (t == 0) reinterpret_cast<__nv_bfloat16*>(d.o[layer])[at] = __float2bfloat16(fmaf(a, sq[half], u * tk[256]));
             sk[half] = u;
@@ -133,6 +135,7 @@ __device__ __noinline__ void chunk_fp32(const tsv_gdn_desc& d, int layer, int h,
     for (int x = 0; x < DK / 64; ++x) tc::tmem_st_frag8f(state + 64 * x, S + 32 * x);
 }
 
+// DV: value features of one CTA, d.DV or half of it.
 template <int DK, int DV>
 __global__ void __launch_bounds__((kScanPrep + DV / 16) * 32, 1)
     gdn_scan_kernel(const __grid_constant__ tsv_gdn_desc d, const int32_t* __restrict__ cu_len, int max_len, int32_t* status) {
@@ -146,10 +149,27 @@ __global__ void __launch_bounds__((kScanPrep + DV / 16) * 32, 1)
     static_assert(sizeof(ScanBars) <= 128, "barriers");
     volatile int* abort_flag = &br.abort;
     const uint32_t s0 = tc::smem_u32(sm);
+    const int slices = d.DV / DV;
     int item = blockIdx.x;
+    const int f0 = item % slices * DV;  // this CTA's first value feature
+    item /= slices;
     const int h = item % d.HV;
     item /= d.HV;
-    const int b = item % d.B, layer = item / d.B;
+    const int layer = item % d.n_layers;
+    int b = item / d.n_layers;
+    if (d.B > 1 && d.B <= kScanSort) {  // CTAs start in the order of their index: the longest sequences first
+        int* lens = reinterpret_cast<int*>(sm + M::diag);
+        int* pick = lens + kScanSort;
+        int mine = 0, rank = 0;
+        if (threadIdx.x < d.B) lens[threadIdx.x] = mine = cu_len[threadIdx.x + 1] - cu_len[threadIdx.x];
+        __syncthreads();
+        if (threadIdx.x < d.B) {
+            for (int x = 0; x < d.B; ++x) rank += lens[x] > mine || (lens[x] == mine && x < (int)threadIdx.x);
+            if (rank == b) *pick = threadIdx.x;
+        }
+        __syncthreads();
+        b = *pick;
+    }
     const int hk = h / (d.HV / d.HK);
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int g = lane >> 2, t = lane & 3;
@@ -157,10 +177,10 @@ __global__ void __launch_bounds__((kScanPrep + DV / 16) * 32, 1)
     const int row0 = cu_len[b], row1 = cu_len[b + 1];
     const int n = row1 - row0;
     if (row0 < 0 || row1 < row0 || row1 > d.T || n > max_len) {
-        if (h == 0 && layer == 0 && threadIdx.x == 0) dev_fail(status, TSV_DEV_BAD_SEQ_LEN, b, row1);
+        if (h == 0 && layer == 0 && f0 == 0 && threadIdx.x == 0) dev_fail(status, TSV_DEV_BAD_SEQ_LEN, b, row1);
         return;
     }
-    const size_t state0 = ((size_t)b * d.HV + h) * DV * DK;
+    const size_t state0 = (((size_t)b * d.HV + h) * d.DV + f0) * DK;
     if (n == 0) {  // the state as it was
         if (d.state_out[layer] != d.state[layer])
             for (int e = threadIdx.x; e < DV * DK / 4; e += blockDim.x)
@@ -254,7 +274,7 @@ __global__ void __launch_bounds__((kScanPrep + DV / 16) * 32, 1)
             for (int x = 0; x < VC; ++x) {
                 const int e = pt + x * PT, i = c * kScanT + e / CPR;
                 cp16(bs32 + tile_at<DV * 2>(M::v, e / CPR, e % CPR),
-                     reinterpret_cast<const uint16_t*>(d.v[layer]) + ((size_t)(row0 + min(i, n - 1)) * d.HV + h) * DV + e % CPR * 8, i < n);
+                     reinterpret_cast<const uint16_t*>(d.v[layer]) + ((size_t)(row0 + min(i, n - 1)) * d.HV + h) * d.DV + f0 + e % CPR * 8, i < n);
             }
             cp_commit();
             constexpr int KH = KQ / 2;  // half of a thread's chunks at a time
@@ -462,25 +482,6 @@ __global__ void __launch_bounds__((kScanPrep + DV / 16) * 32, 1)
                 tc::tmem_st_frag2(la + M::col_hi + 8 * block_pos<NB>(bb), hi);
                 tc::tmem_st_frag2(la + M::col_lo + 8 * block_pos<NB>(bb), lo);
             }
-            // o over v's place
-#pragma unroll
-            for (int bb = 0; bb < NB; ++bb) {
-                float x8[8], aq[2][4];
-                uint32_t w[4];
-                tc::tmem_ld_frag2(la + M::col_d + kScanT + 16 * block_pos<NB>(bb), x8);
-                tc::tmem_wait_ld();
-#pragma unroll
-                for (int x = 0; x < 8; ++x) aq[x >> 2][x & 3] = x8[x];
-                block_rhs_q(bb, aq, rw, t);
-#pragma unroll
-                for (int cc = 0; cc <= bb; ++cc) block_out(bb, cc, aq, Uh[cc], bs32 + M::p16, lane);
-#pragma unroll
-                for (int nn = 0; nn < 2; ++nn)
-#pragma unroll
-                    for (int half = 0; half < 2; ++half)
-                        w[2 * nn + half] = bf16x2(aq[nn][2 * half] * up[half], aq[nn][2 * half + 1] * up[half]);
-                stsm4_t(tile_at<DV * 2>(bs32 + M::v, bb * 16 + vrow, vchunk), w);
-            }
             if (watched(flag)) br.bad[buf] = 1;
             tc::tmem_wait_st();
             tc::tc_fence_before();
@@ -491,8 +492,8 @@ __global__ void __launch_bounds__((kScanPrep + DV / 16) * 32, 1)
                 // lets them reach: later tokens, and with v only their own feature.  What TMEM holds times un is the
                 // state ahead of the chunk.
                 const float un0 = early ? up[0] / e_n : sc[0] * up[0], un1 = early ? up[1] / e_n : sc[1] * up[1];
-                chunk_fp32<DK, DV>(d, layer, h, (size_t)row0 + (size_t)c * kScanT, nt, la + M::col_s, fb, un0, un1,
-                                   reinterpret_cast<float*>(sm + M::slow), group);
+                chunk_fp32<DK>(d, layer, h, (size_t)row0 + (size_t)c * kScanT, nt, la + M::col_s, f0 + fb, un0, un1,
+                               reinterpret_cast<float*>(sm + M::slow), group);
                 up[0] = up[1] = 1.f;
             } else if (!early) {
 #pragma unroll 1
@@ -524,12 +525,32 @@ __global__ void __launch_bounds__((kScanPrep + DV / 16) * 32, 1)
                 tc::mma_commit(&br.state);
             }
             __syncwarp();
-            if (!bad) {  // o, gathered from every warp's features
+            if (!bad) {  // o while the tensor cores work on the state
+                // o over v's place
+#pragma unroll
+                for (int bb = 0; bb < NB; ++bb) {
+                    float x8[8], aq[2][4];
+                    uint32_t w[4];
+                    tc::tmem_ld_frag2(la + M::col_d + kScanT + 16 * block_pos<NB>(bb), x8);
+                    tc::tmem_wait_ld();
+#pragma unroll
+                    for (int x = 0; x < 8; ++x) aq[x >> 2][x & 3] = x8[x];
+                    block_rhs_q(bb, aq, rw, t);
+#pragma unroll
+                    for (int cc = 0; cc <= bb; ++cc) block_out(bb, cc, aq, Uh[cc], bs32 + M::p16, lane);
+#pragma unroll
+                    for (int nn = 0; nn < 2; ++nn)
+#pragma unroll
+                        for (int half = 0; half < 2; ++half)
+                            w[2 * nn + half] = bf16x2(aq[nn][2 * half] * up[half], aq[nn][2 * half + 1] * up[half]);
+                    stsm4_t(tile_at<DV * 2>(bs32 + M::v, bb * 16 + vrow, vchunk), w);
+                }
+                group.sync();
                 constexpr int CPR = DV / 8;
                 for (int e = threadIdx.x; e < nt * CPR; e += SW * 32) {
                     const int i = e / CPR, cc = e % CPR;
                     *reinterpret_cast<uint4*>(reinterpret_cast<uint16_t*>(d.o[layer]) +
-                                              ((size_t)(row0 + c * kScanT + i) * d.HV + h) * DV + cc * 8) =
+                                              ((size_t)(row0 + c * kScanT + i) * d.HV + h) * d.DV + f0 + cc * 8) =
                         *reinterpret_cast<const uint4*>(bs + tile_at<DV * 2>(M::v, i, cc));
                 }
             }
@@ -569,15 +590,16 @@ template <int DK, int DV>
 static void launch_scan_dims(const tsv_gdn_desc& d, const int32_t* cu_len, int max_len, int32_t* status, cudaStream_t stream) {
     constexpr int sm = ScanSmem<DK, DV>::total;
     cudaFuncSetAttribute(gdn_scan_kernel<DK, DV>, cudaFuncAttributeMaxDynamicSharedMemorySize, sm);
-    launch_pdl(gdn_scan_kernel<DK, DV>, (unsigned)((long long)d.n_layers * d.B * d.HV), (kScanPrep + DV / 16) * 32, sm, stream, d,
-               cu_len, max_len, status);
+    launch_pdl(gdn_scan_kernel<DK, DV>, (unsigned)((long long)d.n_layers * d.B * d.HV * (d.DV / DV)), (kScanPrep + DV / 16) * 32, sm,
+               stream, d, cu_len, max_len, status);
 }
 
 void launch_gdn_scan(const tsv_gdn_desc& d, const int32_t* cu_len, int max_len, int32_t* status, cudaStream_t stream) {
-    if (d.DK == 64 && d.DV == 64) launch_scan_dims<64, 64>(d, cu_len, max_len, status, stream);
-    else if (d.DK == 64) launch_scan_dims<64, 128>(d, cu_len, max_len, status, stream);
-    else if (d.DV == 64) launch_scan_dims<128, 64>(d, cu_len, max_len, status, stream);
-    else launch_scan_dims<128, 128>(d, cu_len, max_len, status, stream);
+    // Half heads while both halves of every head find an SM: the preparation is done twice, but a half's warps have more
+    // of their SM to themselves.
+    const bool half = d.DV == 64 || 2LL * d.n_layers * d.B * d.HV <= sm_count();
+    if (d.DK == 64) half ? launch_scan_dims<64, 64>(d, cu_len, max_len, status, stream) : launch_scan_dims<64, 128>(d, cu_len, max_len, status, stream);
+    else half ? launch_scan_dims<128, 64>(d, cu_len, max_len, status, stream) : launch_scan_dims<128, 128>(d, cu_len, max_len, status, stream);
 }
 
 }  // namespace tsv

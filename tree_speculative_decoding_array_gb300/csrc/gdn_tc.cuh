@@ -232,10 +232,11 @@ __device__ __forceinline__ void block_matrices(bool q, int b, int c0, int c1, ui
         f[half] = q ? ky.fq[i] : rw.beta[i] * ky.fk[i];
         seen[half] = q ? ky.before[i] | (1ull << i) : ky.before[i];
     }
+    float next[8];
+    tc::tmem_ld_frag2(taddr + 16 * block_pos<NB>(c0), next);
 #pragma unroll 1
     for (int c = c0; c < c1; ++c) {  // rolled: a kernel's warps run different parts at once and share the instruction cache
         float x[8];
-        tc::tmem_ld_frag2(taddr + 16 * block_pos<NB>(c), x);
         float2 jh[2], jl[2], jf[2];
 #pragma unroll
         for (int n = 0; n < 2; ++n) {
@@ -245,6 +246,9 @@ __device__ __forceinline__ void block_matrices(bool q, int b, int c0, int c1, ui
             jf[n] = *reinterpret_cast<const float2*>(&ky.fk[j0]);
         }
         tc::tmem_wait_ld();
+#pragma unroll
+        for (int e = 0; e < 8; ++e) x[e] = next[e];
+        if (c + 1 < c1) tc::tmem_ld_frag2(taddr + 16 * block_pos<NB>(c + 1), next);
         float y[2][2][2];
 #pragma unroll
         for (int half = 0; half < 2; ++half) {
