@@ -7,8 +7,10 @@
 //
 // One CTA per (layer, sequence, some value heads of one key head): K and Q are staged and [K; Q] K^T taken once, then
 // the value heads follow one another.  Each warp owns 16 value features and takes their rows of S from global memory
-// to fp16 pairs in TMEM; the next head's state and V are fetched while this head is computed, and a head's matrices
-// are built while the tensor cores work on its S [K; Q]^T.
+// to fp16 pairs in TMEM, fetches their columns of V and writes their columns of o; the next head's state and V are
+// fetched while this head is computed, and a head's matrices are built while the tensor cores work on its S [K; Q]^T.
+// The warps of a head only meet to hand over S and the matrices.  K, Q and S are kept with the columns of every 16 in the
+// order 0 1 4 5 8 9 12 13 2 3 6 7 10 11 14 15, in which a thread's four values of a fragment are neighbours in memory.
 #include <math.h>
 
 #include "gdn_tc.cuh"
@@ -142,10 +144,12 @@ __global__ void __launch_bounds__(2 * DV, 2) gdn_tree_kernel(const __grid_consta
     uint64_t* bars = reinterpret_cast<uint64_t*>(sm + M::bars);  // [K; Q] K^T done, S [K; Q]^T done
     uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + 2);
     volatile int* abort_flag = reinterpret_cast<volatile int*>(bars + 3);
+    int* redo_s = reinterpret_cast<int*>(bars + 3) + 1;
     if (threadIdx.x == 0) {
         tc::mbar_init(&bars[0], 1);
         tc::mbar_init(&bars[1], 1);
         *abort_flag = 0;
+        *redo_s = 0;
         tc::fence_mbar_init();
     }
     if (warp == 1) {
@@ -165,25 +169,28 @@ __global__ void __launch_bounds__(2 * DV, 2) gdn_tree_kernel(const __grid_consta
         cp16(kq_at<2 * T16>(s0 + M::kq, row_pos<NB>(r), chunk), src + ((row0 + (i < T ? i : 0)) * d.HK + hk) * DK + chunk * 8, i < T);
     }
     cp_commit();
-    constexpr int CPR = DV / 8;
+    // this warp's columns of V, and of o over them: 32 bytes of every row, a 16-byte chunk per lane and NB
+    const int vc = fb / 8 + (lane & 1), vr = lane >> 1;
+    const size_t vo0 = (row0 * d.HV + h0) * DV + vc * 8;  // + (row * HV + head) * DV
     auto fetch_v = [&](int k) {
-        for (int e = threadIdx.x; e < T16 * CPR; e += kThreads) {
-            const int i = e / CPR, cc = e % CPR;
-            cp16(tile_at<DV * 2>(s0 + M::v + (k & 1) * T16 * DV * 2, i, cc),
-                 reinterpret_cast<const uint16_t*>(d.v[layer]) + ((row0 + (i < T ? i : 0)) * d.HV + h0 + k) * DV + cc * 8, i < T);
+#pragma unroll
+        for (int x = 0; x < NB; ++x) {
+            const int i = vr + 16 * x;
+            cp16(tile_at<DV * 2>(s0 + M::v + (k & 1) * T16 * DV * 2, i, vc),
+                 reinterpret_cast<const uint16_t*>(d.v[layer]) + vo0 + ((size_t)(i < T ? i : 0) * d.HV + k) * DV, i < T);
         }
         cp_commit();
     };
     fetch_v(0);
-    // the state's loads: features (rows) fb + g and fb + g + 8, columns 8 n + 2 t, + 1
-    const float* S = d.state[layer] + (((size_t)b * d.HV + h0) * DV + fb + g) * DK + 2 * t;
-    float2 raw[2][2 * KS];
+    // the state's loads: features (rows) fb + g and fb + g + 8, columns 16 j + 4 t .. + 3
+    const float* S = d.state[layer] + (((size_t)b * d.HV + h0) * DV + fb + g) * DK + 4 * t;
+    float4 raw[2][KS];
     auto fetch_s = [&](int k) {
 #pragma unroll
         for (int half = 0; half < 2; ++half)
 #pragma unroll
-            for (int n = 0; n < 2 * KS; ++n)
-                raw[half][n] = __ldcs(reinterpret_cast<const float2*>(S + (size_t)k * DV * DK + half * 8 * DK + 8 * n));
+            for (int j = 0; j < KS; ++j)
+                raw[half][j] = __ldcs(reinterpret_cast<const float4*>(S + (size_t)k * DV * DK + half * 8 * DK + 16 * j));
     };
     // G of every head, a warp each, two nodes per lane: pointer doubling over the parents (the highest strict ancestor)
     for (int k = warp; k < heads; k += kWarps) {
@@ -249,7 +256,10 @@ __global__ void __launch_bounds__(2 * DV, 2) gdn_tree_kernel(const __grid_consta
 #pragma unroll
         for (int x = 0; x < KH; ++x) {
             const int r = threadIdx.x / LPR + (x0 + x) * (kThreads / LPR);
-            *reinterpret_cast<uint4*>(sm + kq_at<2 * T16>(M::kq, row_pos<NB>(r), chunk)) = w[x];
+            // columns 0 1 4 5 (or 8 9 12 13) of the 16 to their first chunk, 2 3 6 7 (10 11 14 15) to the second
+            const int p = row_pos<NB>(r), at = 8 * (chunk & 1);
+            *reinterpret_cast<uint2*>(sm + kq_at<2 * T16>(M::kq, p, chunk & ~1) + at) = make_uint2(w[x].x, w[x].z);
+            *reinterpret_cast<uint2*>(sm + kq_at<2 * T16>(M::kq, p, chunk | 1) + at) = make_uint2(w[x].y, w[x].w);
             if (chunk == 0) (r >= T16 ? ky.fq : ky.fk)[r >= T16 ? r - T16 : r] = r >= T16 ? f[x] * d.scale : f[x];
         }
     }
@@ -259,33 +269,32 @@ __global__ void __launch_bounds__(2 * DV, 2) gdn_tree_kernel(const __grid_consta
     const uint64_t kq_desc = tc::sdesc_sw128(s0 + M::kq, 16, 1024);
     const int vrow = ((lane >> 4) << 3) + (lane & 7), vchunk = fb / 8 + ((lane >> 3) & 1);
     float* diag = reinterpret_cast<float*>(sm + M::diag);
-    uint32_t tmem = 0, redo = 0;
+    __syncthreads();
+    tc::tc_fence_after();
+    const uint32_t tmem = *tmem_slot;
+    if (threadIdx.x == 0) {  // [K; Q] K^T
+        const uint32_t id = tc::idesc_f16(false, false, false, 128, T16);
+#pragma unroll
+        for (int ks = 0; ks < KS; ++ks) {
+            const uint64_t at = tc::sdesc_add(kq_desc, (ks >> 2) * 2 * T16 * 128 + (ks & 3) * 32);
+            tc::mma_f16(tmem + M::col_g, at, at, id, ks > 0);
+        }
+        tc::mma_commit(&bars[0]);
+    }
+    if (threadIdx.x < 2 * T16) {
+        const int r = threadIdx.x, i = r >= T16 ? r - T16 : r;
+        const float x = (r >= T16 ? ky.fq : ky.fk)[i];
+        for (int y = 0; y < heads; ++y)
+            (r >= T16 ? rows[y].cq : rows[y].ck)[i] = tc::ex2_approx(rows[y].g_hi[i] + rows[y].g_lo[i]) * x;
+    }
+    uint32_t redo = 0;  // heads in which this thread saw an operand that is not finite
     bool ok = true;
     for (int k = 0; k < heads; ++k) {
         const GdnRows& rw = rows[k];
         const int vt = M::v + (k & 1) * T16 * DV * 2;
         uint32_t flag = flag_kq;
         cp_wait<0>();
-        __syncthreads();  // V is here; the head before is done with shared memory and TMEM
-        tc::tc_fence_after();
-        if (k == 0) {
-            tmem = *tmem_slot;
-            if (threadIdx.x == 0) {  // [K; Q] K^T
-                const uint32_t id = tc::idesc_f16(false, false, false, 128, T16);
-#pragma unroll
-                for (int ks = 0; ks < KS; ++ks) {
-                    const uint64_t at = tc::sdesc_add(kq_desc, (ks >> 2) * 2 * T16 * 128 + (ks & 3) * 32);
-                    tc::mma_f16(tmem + M::col_g, at, at, id, ks > 0);
-                }
-                tc::mma_commit(&bars[0]);
-            }
-            if (threadIdx.x < 2 * T16) {
-                const int r = threadIdx.x, i = r >= T16 ? r - T16 : r;
-                const float x = (r >= T16 ? ky.fq : ky.fk)[i];
-                for (int y = 0; y < heads; ++y)
-                    (r >= T16 ? rows[y].cq : rows[y].ck)[i] = tc::ex2_approx(rows[y].g_hi[i] + rows[y].g_lo[i]) * x;
-            }
-        }
+        __syncwarp();  // this warp's V is here
         if (k + 1 < heads) fetch_v(k + 1);
         // this warp's features: a power-of-two scale each, from the largest of the state's row and of v
         float down[2], up[2];
@@ -304,16 +313,18 @@ __global__ void __launch_bounds__(2 * DV, 2) gdn_tree_kernel(const __grid_consta
             for (int half = 0; half < 2; ++half) {
                 float sx = 0.f;
 #pragma unroll
-                for (int n = 0; n < 2 * KS; ++n) sx = fmaxf(sx, fmaxf(fabsf(raw[half][n].x), fabsf(raw[half][n].y)));
+                for (int j = 0; j < KS; ++j)
+                    sx = fmaxf(fmaxf(sx, fmaxf(fabsf(raw[half][j].x), fabsf(raw[half][j].y))), fmaxf(fabsf(raw[half][j].z), fabsf(raw[half][j].w)));
                 sx = fmaxf(8.f * sx, mx[half]);
                 sx = fmaxf(sx, __shfl_xor_sync(0xFFFFFFFFu, sx, 1));
                 sx = fmaxf(sx, __shfl_xor_sync(0xFFFFFFFFu, sx, 2));
                 pow2_scale(sx, down[half], up[half]);
                 const float2 d2 = make_float2(down[half], down[half]);
 #pragma unroll
-                for (int n = 0; n < 2 * KS; ++n) {
-                    const float2 x = mul2(raw[half][n], d2);
-                    Sf[2 * n + half] = f16x2(x.x, x.y);
+                for (int j = 0; j < KS; ++j) {
+                    const float2 x = mul2(make_float2(raw[half][j].x, raw[half][j].y), d2), y = mul2(make_float2(raw[half][j].z, raw[half][j].w), d2);
+                    Sf[4 * j + half] = f16x2(x.x, x.y);
+                    Sf[4 * j + 2 + half] = f16x2(y.x, y.y);
                 }
             }
 #pragma unroll
@@ -376,18 +387,21 @@ __global__ void __launch_bounds__(2 * DV, 2) gdn_tree_kernel(const __grid_consta
             stsm4_t(tile_at<DV * 2>(s0 + vt, bb * 16 + vrow, vchunk), w);
         }
         tc::tc_fence_before();
-        if (__syncthreads_or(watched(flag))) {
-            redo |= 1u << k;
-            continue;
+        redo |= (uint32_t)watched(flag) << k;
+        __syncwarp();
+#pragma unroll
+        for (int x = 0; x < NB; ++x) {
+            const int i = vr + 16 * x;
+            if (i < T)
+                *reinterpret_cast<uint4*>(reinterpret_cast<uint16_t*>(d.o[layer]) + vo0 + ((size_t)i * d.HV + k) * DV) =
+                    *reinterpret_cast<const uint4*>(sm + tile_at<DV * 2>(vt, i, vc));
         }
-        for (int e = threadIdx.x; e < T * CPR; e += kThreads) {
-            const int i = e / CPR, c = e % CPR;
-            *reinterpret_cast<uint4*>(reinterpret_cast<uint16_t*>(d.o[layer]) + ((row0 + i) * d.HV + h0 + k) * DV + c * 8) =
-                *reinterpret_cast<const uint4*>(sm + tile_at<DV * 2>(vt, i, c));
-        }
+        __syncwarp();  // before V is fetched over it
     }
+    if (redo) atomicOr(redo_s, (int)redo);
     cp_wait<0>();
     __syncthreads();
+    redo = *redo_s;
     if (warp == 1) {
         tc::tc_fence_after();
         if (!ok)  // let the MMAs end before their TMEM goes
