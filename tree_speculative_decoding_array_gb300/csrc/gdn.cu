@@ -11,12 +11,13 @@
 //   gdn_recur_kernel   token by token (short scans, commits): the state stays in registers, one pass over it
 #include <math.h>
 
-#include "common.cuh"
+#include "gdn_tc.cuh"
 
 namespace tsv {
 
-constexpr int kGdnRows = 32;      // state rows (value features) per CTA
-constexpr int kGdnThreads = 128;  // 4 warps of 8 rows; 8 lanes share a row
+constexpr int kGdnRows = 64;      // state rows (value features) per CTA
+constexpr int kGdnThreads = 128;  // 4 warps of 16 rows; 8 lanes share a row, 4 rows to a lane
+constexpr int kGdnR = 4;
 constexpr int kGdnBatch = 8;      // tokens whose q and k rows are in shared memory together
 
 // One bf16 row of DK features, read by a whole warp, normalised and written to shared memory as fp32.
@@ -44,24 +45,25 @@ __device__ __forceinline__ void stage_row(const uint16_t* src, float* dst, float
     for (int e = 0; e < E; ++e) dst[lane * E + e] = x[e] * f;
 }
 
-// This lane's part of R state rows: features 4 (lane % 8) + 32 c .. + 3 of rows r * 4 + lane / 8.
-template <int DK, int R>
-__device__ __forceinline__ void load_state(const float* base, float (&s)[R][DK / 8], int lane) {
+// This lane's part of kGdnR state rows: features 4 (lane % 8) + 32 c .. + 3 of rows 4 r + lane / 8, as pairs.
+template <int DK>
+__device__ __forceinline__ void load_state(const float* base, float2 (&s)[kGdnR][DK / 16], int lane) {
 #pragma unroll
-    for (int r = 0; r < R; ++r)
+    for (int r = 0; r < kGdnR; ++r)
 #pragma unroll
         for (int c = 0; c < DK / 32; ++c) {
-            const float4 w = *reinterpret_cast<const float4*>(base + (size_t)(r * 4 + lane / 8) * DK + 32 * c + 4 * (lane % 8));
-            s[r][4 * c] = w.x; s[r][4 * c + 1] = w.y; s[r][4 * c + 2] = w.z; s[r][4 * c + 3] = w.w;
+            const float4 w = __ldcs(reinterpret_cast<const float4*>(base + (size_t)(r * 4 + lane / 8) * DK + 32 * c + 4 * (lane % 8)));
+            s[r][2 * c] = make_float2(w.x, w.y);
+            s[r][2 * c + 1] = make_float2(w.z, w.w);
         }
 }
 
 // Advances the state token by token; COMMIT takes a tree block's rows along `path` and writes no outputs, otherwise
 // the packed rows cu_len[b] .. cu_len[b + 1].  grid: (layer, sequence, value head, slice of kGdnRows state rows).
 //
-// Per token and state element: one FMA for S k, one for S q, a multiply for the decay and an FMA for the write, with
-// o = e^g (S q) + u (k . q) so that both products read the state before the write.  The state is read and written
-// once per call, so few tokens are bound by HBM (128 KB per 128 x 128 head).
+// Per token and state element: one FMA for S k, one for S q, a multiply for the decay and an FMA for the write, two
+// elements to an instruction, with o = e^g (S q) + u (k . q) so that both products read the state before the write.  The
+// state is read and written once per call, so few tokens are bound by HBM (128 KB per 128 x 128 head).
 template <int DK, bool COMMIT>
 __global__ void __launch_bounds__(kGdnThreads) gdn_recur_kernel(const __grid_constant__ tsv_gdn_desc d,
                                                                 const int32_t* __restrict__ cu_len, int max_len,
@@ -113,9 +115,9 @@ __global__ void __launch_bounds__(kGdnThreads) gdn_recur_kernel(const __grid_con
         }
     }
 
-    const size_t s0 = (((size_t)b * d.HV + h) * d.DV + slice * kGdnRows + warp * 8) * DK;
-    float s[2][DK / 8];
-    load_state<DK, 2>(d.state[layer] + s0, s, lane);
+    const size_t s0 = (((size_t)b * d.HV + h) * d.DV + slice * kGdnRows + warp * 4 * kGdnR) * DK;
+    float2 s[kGdnR][DK / 16];
+    load_state<DK>(d.state[layer] + s0, s, lane);
     const uint16_t* Q = reinterpret_cast<const uint16_t*>(d.q[layer]);
     const uint16_t* K = reinterpret_cast<const uint16_t*>(d.k[layer]);
     const uint16_t* V = reinterpret_cast<const uint16_t*>(d.v[layer]);
@@ -128,7 +130,8 @@ __global__ void __launch_bounds__(kGdnThreads) gdn_recur_kernel(const __grid_con
             const size_t row = row0 + (COMMIT ? row_s[t0 + j] : t0 + j);
             stage_row<DK>(K + (row * d.HK + hk) * DK, ks[j], d.norm_eps, 1.f, lane);
             if (!COMMIT) stage_row<DK>(Q + (row * d.HK + hk) * DK, qs[j], d.norm_eps, d.scale, lane);
-            vs[j][lane] = bf16_bits_to_f32(V[(row * d.HV + h) * d.DV + slice * kGdnRows + lane]);
+            const uint32_t v2 = *reinterpret_cast<const uint32_t*>(V + (row * d.HV + h) * d.DV + slice * kGdnRows + 2 * lane);
+            *reinterpret_cast<float2*>(&vs[j][2 * lane]) = make_float2(bf16_lo(v2), bf16_hi(v2));
             if (lane == 0) {
                 al[j] = expf(d.g[layer][row * d.HV + h]);
                 be[j] = d.beta[layer][row * d.HV + h];
@@ -145,42 +148,43 @@ __global__ void __launch_bounds__(kGdnThreads) gdn_recur_kernel(const __grid_con
         }
         __syncthreads();
         for (int j = 0; j < nt; ++j) {
-            float sk[2] = {0.f, 0.f}, sq[2] = {0.f, 0.f};
-            float4 kk[DK / 32];
+            float2 kk[DK / 16], sk2[kGdnR], sq2[kGdnR];
+#pragma unroll
+            for (int r = 0; r < kGdnR; ++r) sk2[r] = sq2[r] = make_float2(0.f, 0.f);
 #pragma unroll
             for (int c = 0; c < DK / 32; ++c) {
-                kk[c] = *reinterpret_cast<const float4*>(&ks[j][32 * c + 4 * (lane % 8)]);
+                const float4 w = *reinterpret_cast<const float4*>(&ks[j][32 * c + 4 * (lane % 8)]);
+                kk[2 * c] = make_float2(w.x, w.y);
+                kk[2 * c + 1] = make_float2(w.z, w.w);
 #pragma unroll
-                for (int r = 0; r < 2; ++r)
-                    sk[r] = fmaf(s[r][4 * c], kk[c].x, fmaf(s[r][4 * c + 1], kk[c].y,
-                            fmaf(s[r][4 * c + 2], kk[c].z, fmaf(s[r][4 * c + 3], kk[c].w, sk[r]))));
+                for (int r = 0; r < kGdnR; ++r) sk2[r] = fma2(s[r][2 * c], kk[2 * c], fma2(s[r][2 * c + 1], kk[2 * c + 1], sk2[r]));
                 if (!COMMIT) {
-                    const float4 qq = *reinterpret_cast<const float4*>(&qs[j][32 * c + 4 * (lane % 8)]);
+                    const float4 y = *reinterpret_cast<const float4*>(&qs[j][32 * c + 4 * (lane % 8)]);
 #pragma unroll
-                    for (int r = 0; r < 2; ++r)
-                        sq[r] = fmaf(s[r][4 * c], qq.x, fmaf(s[r][4 * c + 1], qq.y,
-                                fmaf(s[r][4 * c + 2], qq.z, fmaf(s[r][4 * c + 3], qq.w, sq[r]))));
+                    for (int r = 0; r < kGdnR; ++r)
+                        sq2[r] = fma2(s[r][2 * c], make_float2(y.x, y.y), fma2(s[r][2 * c + 1], make_float2(y.z, y.w), sq2[r]));
                 }
+            }
+            float sk[kGdnR], sq[kGdnR];
+#pragma unroll
+            for (int r = 0; r < kGdnR; ++r) {
+                sk[r] = sk2[r].x + sk2[r].y;
+                sq[r] = sq2[r].x + sq2[r].y;
             }
 #pragma unroll
             for (int o = 4; o > 0; o >>= 1)
 #pragma unroll
-                for (int r = 0; r < 2; ++r) {
+                for (int r = 0; r < kGdnR; ++r) {
                     sk[r] += __shfl_xor_sync(0xFFFFFFFFu, sk[r], o);
                     if (!COMMIT) sq[r] += __shfl_xor_sync(0xFFFFFFFFu, sq[r], o);
                 }
             const float a = al[j], bt = be[j];
 #pragma unroll
-            for (int r = 0; r < 2; ++r) {
-                const int vr = warp * 8 + r * 4 + lane / 8;
+            for (int r = 0; r < kGdnR; ++r) {
+                const int vr = warp * 4 * kGdnR + r * 4 + lane / 8;
                 const float u = bt * (vs[j][vr] - a * sk[r]);
 #pragma unroll
-                for (int c = 0; c < DK / 32; ++c) {
-                    s[r][4 * c] = fmaf(u, kk[c].x, a * s[r][4 * c]);
-                    s[r][4 * c + 1] = fmaf(u, kk[c].y, a * s[r][4 * c + 1]);
-                    s[r][4 * c + 2] = fmaf(u, kk[c].z, a * s[r][4 * c + 2]);
-                    s[r][4 * c + 3] = fmaf(u, kk[c].w, a * s[r][4 * c + 3]);
-                }
+                for (int c = 0; c < DK / 16; ++c) s[r][c] = fma2(make_float2(u, u), kk[c], mul2(make_float2(a, a), s[r][c]));
                 if (!COMMIT && lane % 8 == 0)
                     O[((row0 + t0 + j) * d.HV + h) * d.DV + slice * kGdnRows + vr] = __float2bfloat16(fmaf(a, sq[r], u * kq[j]));
             }
@@ -188,11 +192,11 @@ __global__ void __launch_bounds__(kGdnThreads) gdn_recur_kernel(const __grid_con
     }
     float* out = d.state_out[layer] + s0;
 #pragma unroll
-    for (int r = 0; r < 2; ++r)
+    for (int r = 0; r < kGdnR; ++r)
 #pragma unroll
         for (int c = 0; c < DK / 32; ++c)
-            *reinterpret_cast<float4*>(out + (size_t)(r * 4 + lane / 8) * DK + 32 * c + 4 * (lane % 8)) =
-                make_float4(s[r][4 * c], s[r][4 * c + 1], s[r][4 * c + 2], s[r][4 * c + 3]);
+            __stcs(reinterpret_cast<float4*>(out + (size_t)(r * 4 + lane / 8) * DK + 32 * c + 4 * (lane % 8)),
+                   make_float4(s[r][2 * c].x, s[r][2 * c].y, s[r][2 * c + 1].x, s[r][2 * c + 1].y));
 }
 
 // Defined in gdn_tree.cu and gdn_scan.cu.
@@ -200,7 +204,7 @@ void launch_gdn_tree(const tsv_gdn_desc& d, const uint64_t* anc, int32_t* status
 void launch_gdn_scan(const tsv_gdn_desc& d, const int32_t* cu_len, int max_len, int32_t* status, cudaStream_t stream);
 
 // Sequences of up to this many tokens are advanced token by token, longer ones in chunks.
-constexpr int kRecurMax = 14;
+constexpr int kRecurMax = 16;
 
 enum GdnCall { kGdnVerify, kGdnCommit, kGdnScan };
 
