@@ -65,7 +65,7 @@ __device__ __forceinline__ void load_state(const float* base, float2 (&s)[kGdnR]
 // elements to an instruction, with o = e^g (S q) + u (k . q) so that both products read the state before the write.  The
 // state is read and written once per call, so few tokens are bound by HBM (128 KB per 128 x 128 head).
 template <int DK, bool COMMIT>
-__global__ void __launch_bounds__(kGdnThreads) gdn_recur_kernel(const __grid_constant__ tsv_gdn_desc d,
+__global__ void __launch_bounds__(kGdnThreads, 5) gdn_recur_kernel(const __grid_constant__ tsv_gdn_desc d,
                                                                 const int32_t* __restrict__ cu_len, int max_len,
                                                                 const int32_t* __restrict__ path,
                                                                 const int32_t* __restrict__ path_len, int32_t* status) {
