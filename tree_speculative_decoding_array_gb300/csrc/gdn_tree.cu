@@ -241,7 +241,17 @@ __global__ void __launch_bounds__(2 * DV, 2) gdn_tree_kernel(const __grid_consta
             rows[k].g_lo[lane + 32 * x] = G[x].lo;
         }
     }
-    fetch_s(0);
+    // The next head's state is fetched ahead: to registers where they are free (one block), else to L2, 128 bytes per
+    // prefetch.
+    constexpr bool kAhead = NB == 1;
+    auto ahead_s = [&](int k) {
+        const char* p = reinterpret_cast<const char*>(d.state[layer] + ((size_t)b * d.HV + h0 + k) * DV * DK);
+#pragma unroll
+        for (int x = 0; x < DV * DK * 4 / 128 / kThreads; ++x)
+            asm volatile("prefetch.global.L2 [%0];" ::"l"(p + (threadIdx.x + x * kThreads) * 128));
+    };
+    if (kAhead) fetch_s(0);
+    else ahead_s(0);
     uint32_t flag_kq = 0;
     cp_wait<1>();  // this thread's own chunks of K and Q: converted in place
     constexpr int KH = KQ >= 4 ? KQ / 4 : 1;
@@ -293,6 +303,10 @@ __global__ void __launch_bounds__(2 * DV, 2) gdn_tree_kernel(const __grid_consta
         const GdnRows& rw = rows[k];
         const int vt = M::v + (k & 1) * T16 * DV * 2;
         uint32_t flag = flag_kq;
+        if (!kAhead) {
+            fetch_s(k);
+            if (k + 1 < heads) ahead_s(k + 1);
+        }
         cp_wait<0>();
         __syncwarp();  // this warp's V is here
         if (k + 1 < heads) fetch_v(k + 1);
@@ -332,7 +346,7 @@ __global__ void __launch_bounds__(2 * DV, 2) gdn_tree_kernel(const __grid_consta
                 tc::tmem_st_frag8(tmem + ((uint32_t)lane0 << 16) + M::col_s + x * 32, Sf + 16 * x);
             tc::tmem_wait_st();
         }
-        if (k + 1 < heads) fetch_s(k + 1);
+        if (kAhead && k + 1 < heads) fetch_s(k + 1);
         tc::tc_fence_before();
         __syncthreads();
         tc::tc_fence_after();
