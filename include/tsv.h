@@ -198,7 +198,9 @@ tsv_status tsv_tree_select(const int32_t* cand_parents, const int32_t* cand_toke
  *   Accumulation is fp32; O is rounded to bf16 once.
  *   4-bit caches (TSV_I4_G64, [1185] Phase 3's affine groups of 64 on the cache): byte j of a row holds element 2j in
  *   its low nibble and 2j + 1 in its high nibble; value = scale * code + bias, with the fp16 pair (scale, bias) of
- *   its group of 64 features at k_scale[b][h][c][group] (v_scale likewise), 4-byte aligned.
+ *   its group of 64 features at k_scale[b][h][c][group] (v_scale likewise; the buffers 16-byte aligned).  Pairs of
+ *   positions below kv_len[b] have to be finite and to stand for values within fp16's range, as tsv_tree_append writes
+ *   them; what lies behind is not looked at.
  */
 typedef struct {
     int32_t n_layers;   /* 1 .. TSV_MAX_LAYERS */
@@ -434,10 +436,10 @@ tsv_status tsv_gather_positions(const tsv_kv_desc* kv, int32_t* kv_len, const in
  *   per token; a per-token scale maps every single-valued token to the same
  *   code): scale = fp16(absmax / 127) with the division in fp32, code =
  *   round-half-to-even(x / scale) in fp32, clamped to [-127, 127]; a token whose
- *   scale is 0 stores zero codes.  4-bit caches: per group of 64 features bias = fp16(minimum), scale =
- *   fp16((maximum - minimum) / 15) with the division in fp32 (both kept within the finite fp16 range), code =
- *   round-half-to-even((x - bias) / scale) in fp32, clamped to [0, 15]; a group whose scale is 0 stores zero
- *   codes.  fp16 / bf16 caches store the rotated fp32
+ *   scale is 0 stores zero codes.  4-bit caches: per group of 64 features, with its minimum and maximum (over what is
+ *   not NaN) cut to [-65000, 65000], bias = fp16(minimum), scale = fp16((maximum - minimum) / 15) with the division in
+ *   fp32, code = round-half-to-even((x - bias) / scale) in fp32, clamped to [0, 15] (0 for NaN); a group whose scale is 0
+ *   stores zero codes.  fp16 / bf16 caches store the rotated fp32
  *   values rounded to nearest even.  Angles are reduced in fp64, so positions
  *   up to 2^31 keep fp32 accuracy.
  *   kv_len: in, S_b per sequence; out, S_b + T.  depth: from tsv_tree_mask.

@@ -75,17 +75,19 @@ def quantize_token4(x, group: int = 64):
     """One token's affine 4-bit quantisation per group of 64 features (the 4-bit format of issue #1185's Phase 3, on
     a cache row): (codes uint8 [D], (scale, bias) pairs as fp16 bits uint16 [D/group, 2]).
 
-    bias = fp16(minimum), scale = fp16((maximum - minimum) / 15), both held within the finite fp16 range; code =
-    round-half-to-even((x - bias) / scale) clamped to [0, 15], decisions in fp32; a group of scale 0 has codes 0.
+    With the minimum and maximum (over what is not NaN) cut to [-65000, 65000]: bias = fp16(minimum), scale =
+    fp16((maximum - minimum) / 15); code = round-half-to-even((x - bias) / scale) clamped to [0, 15], decisions in fp32;
+    NaN and groups of scale 0 have codes 0.
     """
     x32 = np.asarray(x, dtype=np.float64).astype(np.float32).reshape(-1, group)
-    lo, hi = x32.min(axis=1), x32.max(axis=1)
-    big = np.float32(65504.0)
-    scale = np.minimum((hi - lo) / np.float32(15.0), big).astype(np.float16)
-    bias = np.clip(lo, -big, big).astype(np.float16)
+    big = np.float32(65000.0)
+    lo = np.fmin(np.fmax(np.fmin.reduce(x32, axis=1), -big), big)
+    hi = np.fmin(np.fmax(np.fmax.reduce(x32, axis=1), -big), big)
+    scale = ((hi - lo) / np.float32(15.0)).astype(np.float16)
+    bias = lo.astype(np.float16)
     s32, b32 = scale.astype(np.float32)[:, None], bias.astype(np.float32)[:, None]
     safe = np.where(s32 == 0, np.float32(1.0), s32)
-    q = np.where(s32 == 0, np.float32(0.0), np.clip(np.rint((x32 - b32) / safe), 0, 15))
+    q = np.where(s32 == 0, np.float32(0.0), np.fmin(np.float32(15.0), np.fmax(np.float32(0.0), np.rint((x32 - b32) / safe))))
     return q.astype(np.uint8).reshape(-1), np.stack([scale, bias], axis=-1).view(np.uint16)
 
 

@@ -98,7 +98,15 @@ def test_four_bit_quantisation_by_hand():
     codes, pair = oap.quantize_token4(np.full(64, 3.0))  # a single value: scale 0, the bias holds it
     assert codes.tolist() == [0] * 64 and pair.tolist() == [[0, 0x4200]]
     codes, pair = oap.quantize_token4(np.concatenate([np.full(32, -1e30), np.full(32, 1e30)]))
-    assert pair.tolist() == [[0x7BFF, 0xFBFF]] and codes[0] == 0 and codes[63] == 15  # finite, whatever comes
+    # cut to +-65000: 8666.67 to the nearest 8, -65000 to the nearest 32 (to even); every value is finite in fp16
+    assert osd.f16(pair).tolist() == [[8664.0, -64992.0]] and codes[0] == 0 and codes[63] == 15
+    assert -64992.0 + 15 * 8664.0 < 65504.0
+    x = np.full(64, np.nan)
+    x[5], x[9] = np.inf, 1.0
+    codes, pair = oap.quantize_token4(x)
+    assert osd.f16(pair).tolist()[0][1] == 1.0 and codes[5] == 15 and codes[9] == 0 and codes[0] == 0
+    codes, pair = oap.quantize_token4(np.full(64, np.nan))
+    assert np.isfinite(osd.f16(pair)).all() and codes.tolist() == [0] * 64
 
 
 @pytest.mark.parametrize("seed", range(3))

@@ -72,9 +72,13 @@ __device__ __forceinline__ void store_row(const float* x, int lane, int dtype, v
             lo = fminf(lo, __shfl_xor_sync(0xFFFFFFFFu, lo, o));
             hi = fmaxf(hi, __shfl_xor_sync(0xFFFFFFFFu, hi, o));
         }
-        // both stay finite in fp16, whatever a bf16 input holds
-        const __half sh = __float2half_rn(fminf(__fdiv_rn(__fsub_rn(hi, lo), 15.f), 65504.f));
-        const __half bh = __float2half_rn(fminf(fmaxf(lo, -65504.f), 65504.f));
+        // The range is cut to +-65000, so that the pair and every value it stands for are finite in fp16 whatever a bf16
+        // input holds (fminf and fmaxf pass over NaN): a row that is not finite cannot reach, through a zero weight, the
+        // nodes that do not attend to it.
+        lo = fminf(fmaxf(lo, -65000.f), 65000.f);
+        hi = fminf(fmaxf(hi, -65000.f), 65000.f);
+        const __half sh = __float2half_rn(__fdiv_rn(__fsub_rn(hi, lo), 15.f));
+        const __half bh = __float2half_rn(lo);
         const float s = __half2float(sh), b = __half2float(bh);
         uint32_t w = 0;
 #pragma unroll
