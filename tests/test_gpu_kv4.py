@@ -387,3 +387,100 @@ def test_hybrid_round(gpu_lib, captured):
         lens = [n + len(p) for n, p in zip(lens, plan)]
         assert vr.kv_len.tolist() == lens
         states = [s.clone() for s in gdn["state"]]
+
+
+def test_rows_that_are_not_finite_stay_with_the_nodes_that_see_them(gpu_lib):
+    """A branch whose K and V rows hold NaN, infinities or values beyond fp16 is appended to the 4-bit cache; every node
+    that does not attend to it computes what it computes without it."""
+    tsv, T, HQ, HKV, D, S = gpu_lib, 7, 6, 1, 256, 90
+    par = [-1, 0, 0, 1, 2, 4, 3]  # node 2 and its descendants 4, 5 are the bad branch
+    anc, depth = masks(tsv, [par])
+    for head_rows in (1, 6):  # few query rows and many
+        out = []
+        for bad in (False, True):
+            gen = torch.Generator().manual_seed(3)
+            kc, vc = ([t.to(DEV) for t in random_cache(gen, 1, HKV, S + T, D)] for _ in "kv")
+            q, kn, vn = (torch.randn(1, T, n, D, generator=gen).bfloat16().to(DEV) for n in (head_rows, HKV, HKV))
+            if bad:
+                for x in (kn, vn):
+                    x[0, 2], x[0, 4, 0, ::3], x[0, 5, 0, ::2] = float("nan"), float("inf"), 1e30
+            o, qo = torch.empty_like(q), torch.empty_like(q)
+            d = tsv.append_desc([q], [qo], [kn], [vn], [kc[0]], [vc[0]], depth, T=T, HQ=head_rows, HKV=HKV, D=D, kv_dtype=tsv.I4_G64,
+                                rot_dim=64, rope_base=1e4, k_scale=[kc[1]], v_scale=[vc[1]])
+            kv_len = torch.tensor([S], dtype=torch.int32, device=DEV)
+            tsv.tree_append(d, kv_len)
+            assert torch.isfinite(kc[1]).all() and torch.isfinite(vc[1]).all()
+            assert values(vc[0], vc[1]).abs().max() < 65520
+            a = tsv.attn_desc([qo], [kc[0]], [vc[0]], [o], kv_len, anc, T=T, HQ=head_rows, HKV=HKV, D=D, kv_dtype=tsv.I4_G64,
+                              max_kv_len=S + T, k_scale=[kc[1]], v_scale=[vc[1]])
+            ws = torch.empty(max(tsv.attention_workspace_size(a), 16), dtype=torch.uint8, device=DEV)
+            tsv.tree_verify_attention(a, ws)
+            torch.cuda.synchronize()
+            out.append(o.clone())
+        clear = [0, 1, 3, 6]
+        assert torch.equal(out[0][0, clear], out[1][0, clear])
+
+
+@pytest.mark.parametrize("T", [1, 20])
+def test_offsets_beyond_32_bits(gpu_lib, T):
+    """The second sequence of a cache whose buffers pass 2^31 bytes and 2^32 codes."""
+    tsv, HQ, HKV, D, S = gpu_lib, 6, 1, 256, 500
+    cap = (1 << 31) // (D // 2) + 1000
+    gen = torch.Generator().manual_seed(1)
+    q = torch.randn(2, T, HQ, D, generator=gen).bfloat16()
+    parts = [[random_cache(gen, HKV, S + T, D) for _ in "kv"] for _ in range(2)]
+    k, v = (torch.empty(2, HKV, cap, D // 2, dtype=torch.uint8, device=DEV) for _ in "kv")
+    ks, vs = (torch.empty(2, HKV, cap, D // 64, 2, dtype=torch.float16, device=DEV) for _ in "kv")
+    for b in range(2):
+        for (codes, pair), c, s in zip(parts[b], (k, v), (ks, vs)):
+            c[b, :, :S + T], s[b, :, :S + T] = codes.to(DEV), pair.to(DEV)
+    par = [random_tree(np.random.default_rng(T), T) for _ in range(2)]
+    anc, _ = masks(tsv, par)
+    o = torch.empty(2, T, HQ, D, dtype=torch.bfloat16, device=DEV)
+    kv_len = torch.full((2,), S + T, dtype=torch.int32, device=DEV)
+    d = tsv.attn_desc([q.to(DEV)], [k], [v], [o], kv_len, anc, T=T, HQ=HQ, HKV=HKV, D=D, kv_dtype=tsv.I4_G64, max_kv_len=S + T,
+                      k_scale=[ks], v_scale=[vs])
+    ws = torch.empty(max(tsv.attention_workspace_size(d), 16), dtype=torch.uint8, device=DEV)
+    tsv.tree_verify_attention(d, ws)
+    for b in range(2):
+        want, tol = ref_attention(q[b].double(), *(values(*x) for x in parts[b]), par[b], S)
+        assert ((o[b].double().cpu() - want).abs() <= tol).all()
+    # and the gather of the block behind it
+    if T > 1:
+        path = torch.tensor([[0, 2, 5] + [-1] * (T - 3)] * 2, dtype=torch.int32, device=DEV)
+        tsv.kv_gather_positions(tsv.kv_desc([k], [v], HKV=HKV, D=D, kv_dtype=tsv.I4_G64, k_scale=[ks], v_scale=[vs]), kv_len, path,
+                                torch.full((2,), 3, dtype=torch.int32, device=DEV), T)
+        for (codes, pair), c, s in zip(parts[1], (k, v), (ks, vs)):
+            assert torch.equal(c[1, :, S + 2].cpu(), codes[:, S + 5]) and torch.equal(s[1, :, S + 1].cpu(), pair[:, S + 2])
+
+
+@pytest.mark.parametrize("big", [False, True])
+@pytest.mark.parametrize("at", [0, 9000])
+@pytest.mark.parametrize("T, D", [(1, 256), (2, 256), (20, 256), (1, 128), (3, 64)])
+def test_small_values_behind_a_key_that_draws_most_of_the_weight(gpu_lib, T, D, at, big):
+    """16000 keys of values up to 15 * 2^-9, each e^-11 behind one key whose values are 0: together a fifth of the
+    weight.  With `big`, values of one late key reach 15 * 100."""
+    tsv, HQ, S = gpu_lib, 6, 16000
+    gen = torch.Generator().manual_seed(T)
+    pair = lambda s, b: torch.tensor([s, b]).half()  # noqa: E731
+    k, v = ([torch.zeros(1, S + T, D // 2, dtype=torch.uint8), torch.zeros(1, S + T, D // 64, 2, dtype=torch.float16)] for _ in "kv")
+    k[1][0, at] = pair(0.0, 11.0 / D ** 0.5)
+    v[0][:] = torch.randint(0, 256, v[0].shape, generator=gen)
+    v[1][:] = pair(2.0 ** -9, 0.0)
+    v[1][0, at] = 0.0
+    if big:
+        v[1][0, S - 10] = pair(100.0, 0.0)
+    q = torch.ones(1, T, HQ, D).bfloat16()
+    par = [list(range(-1, T - 1))]
+    anc, _ = masks(tsv, par)
+    o = torch.empty(1, T, HQ, D, dtype=torch.bfloat16, device=DEV)
+    dev = [[x[None].to(DEV) for x in y] for y in (k, v)]
+    d = tsv.attn_desc([q.to(DEV)], [dev[0][0]], [dev[1][0]], [o], torch.tensor([S + T], dtype=torch.int32, device=DEV), anc, T=T, HQ=HQ,
+                      HKV=1, D=D, kv_dtype=tsv.I4_G64, max_kv_len=S + T, k_scale=[dev[0][1]], v_scale=[dev[1][1]], splits=1)
+    ws = torch.empty(max(tsv.attention_workspace_size(d), 16), dtype=torch.uint8, device=DEV)
+    tsv.tree_verify_attention(d, ws)
+    want, _ = ref_attention(q[0].double(), values(*k), values(*v), par[0], S)
+    # P (times a scale) in fp16 is off by 2^-11 of itself and 2^-25 absolutely, relative to the largest P of 1 / 4 or more
+    # (one of 2^-8 on the tiles of 128 rows): 16000 such keys add up to 2^-9 of the weight.  The bias sum is zero here.
+    tol = 2.0 ** -8 * want.abs() + (2.0 ** -10 + 16000 * 2.0 ** -25 * 4) * 15 * 2.0 ** -9 + (2.0 ** -9 * want.abs() if big else 0)
+    assert ((o[0].double().cpu() - want).abs() <= tol).all()

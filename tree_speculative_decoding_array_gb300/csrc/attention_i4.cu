@@ -23,6 +23,10 @@ namespace tsv {
 
 constexpr int kFewWarps = 4;
 constexpr int kFewKeys = 16;  // keys per warp and step
+// P s_g goes through fp16, whose smallest value is 2^-24: with scales of 2^-7 (values of 0.06) a key 2^17 behind the
+// maximum would be lost, and a long cache holds many such keys behind an early one that draws most of the weight.  So P
+// is lifted by 2^12 until a scale above 3.9 comes by (4 x 2^12 x 3.9 < 65504), which takes the lift off again.
+constexpr float kFewLift = 4096.f;
 
 template <int D>
 struct FewTile {
@@ -191,6 +195,7 @@ __global__ void __launch_bounds__(kFewWarps * 32, NT == 1 ? 3 : 2)
 #pragma unroll
             for (int nt = 0; nt < NT; ++nt) o[j][i][nt][0] = o[j][i][nt][1] = o[j][i][nt][2] = o[j][i][nt][3] = 0.f;
 
+    float lift = kFewLift;
     const int mine = steps > warp ? (steps - warp + kFewWarps - 1) / kFewWarps : 0;
 #pragma unroll
     for (int i = 0; i < ST - 1; ++i) fetch(i, i);
@@ -251,7 +256,12 @@ __global__ void __launch_bounds__(kFewWarps * 32, NT == 1 ? 3 : 2)
         }
         const float up = qscale * 16777216.f;  // 2^24
         const bool plain = kt + kFewKeys <= k_end && kt + kFewKeys <= S && kt >= lo_last;
-        bool grow = false;
+        bool grow = false, wide = false;
+        const uint32_t* pairs = reinterpret_cast<const uint32_t*>(st + F::vs);
+#pragma unroll
+        for (int y = 0; y < (NG > 2 ? NG / 2 : 1); ++y)
+            wide = wide || fabsf(f16x2_to_f32x2(pairs[(lane + 32 * y) & (kFewKeys * NG - 1)]).x) > 3.9f;
+        wide = wide && lift != 1.f;
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
@@ -268,7 +278,9 @@ __global__ void __launch_bounds__(kFewWarps * 32, NT == 1 ? 3 : 2)
             }
         // The reference follows a row's maximum only when it is exceeded by more than 2 (p <= 4): then the sums and O are
         // brought to the new one.
-        if (__any_sync(0xFFFFFFFFu, grow)) {
+        if (__any_sync(0xFFFFFFFFu, grow || wide)) {
+            const float drop = __any_sync(0xFFFFFFFFu, wide) ? 1.f / kFewLift : 1.f;
+            lift *= drop;
 #pragma unroll
             for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
@@ -276,9 +288,11 @@ __global__ void __launch_bounds__(kFewWarps * 32, NT == 1 ? 3 : 2)
                     float y = fmaxf(x[nt][e], x[nt][e + 2]);
 #pragma unroll
                     for (int z = 4; z < 32; z <<= 1) y = fmaxf(y, __shfl_xor_sync(0xFFFFFFFFu, y, z));
-                    if (y > m[nt][e]) {
-                        const float a = tc::ex2_approx(m[nt][e] - y);
-                        m[nt][e] = y;
+                    // by the row alone: its result does not depend on its neighbours
+                    const bool rise = y > m[nt][e] + 2.f;
+                    if (rise || drop != 1.f) {
+                        const float a = (rise ? tc::ex2_approx(m[nt][e] - y) : 1.f) * drop;
+                        if (rise) m[nt][e] = y;
                         l[nt][e] *= a;
 #pragma unroll
                         for (int j = 0; j < NG; ++j) {
@@ -298,9 +312,15 @@ __global__ void __launch_bounds__(kFewWarps * 32, NT == 1 ? 3 : 2)
             for (int e = 0; e < 4; ++e) {
                 const float mr = m[nt][e & 1];
                 x[nt][e] = mr == -INFINITY ? 0.f : tc::ex2_approx(x[nt][e] - mr);  // every key masked so far: nothing
-                l[nt][e & 1] += x[nt][e];
             }
         // O^T += V^T P^T
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                x[nt][e] *= lift;
+                l[nt][e & 1] += x[nt][e];
+            }
 #pragma unroll
         for (int j = 0; j < NG; ++j) {
             uint32_t p[NT][2];
@@ -353,7 +373,7 @@ __global__ void __launch_bounds__(kFewWarps * 32, NT == 1 ? 3 : 2)
 #pragma unroll
             for (int e = 0; e < 2; ++e) {
                 ml[0][warp][8 * nt + 2 * t + e] = m[nt][e];
-                ml[1][warp][8 * nt + 2 * t + e] = l[nt][e];
+                ml[1][warp][8 * nt + 2 * t + e] = l[nt][e] / lift;
             }
     __syncthreads();  // and the rings are free
     float* part = reinterpret_cast<float*>(sm);  // [warp][row][D + 4]
@@ -365,7 +385,7 @@ __global__ void __launch_bounds__(kFewWarps * 32, NT == 1 ? 3 : 2)
             float top = ml[0][0][r];
 #pragma unroll
             for (int w = 1; w < kFewWarps; ++w) top = fmaxf(top, ml[0][w][r]);
-            const float f = m[nt][e] == -INFINITY ? 0.f : tc::ex2_approx(m[nt][e] - top);
+            const float f = m[nt][e] == -INFINITY ? 0.f : tc::ex2_approx(m[nt][e] - top) / lift;
             float* dst = part + ((size_t)warp * 8 * NT + r) * (D + 4) + 8 * g;
 #pragma unroll
             for (int j = 0; j < NG; ++j) {
