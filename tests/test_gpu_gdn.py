@@ -467,3 +467,140 @@ def test_small_tree_against_the_numpy_oracle(gpu_lib):
     n = {x: c[x][0, 0].double().cpu().numpy() for x in ("q", "k", "v", "g", "beta", "state")}
     want = og.tree_verify(n["q"], n["k"], n["v"], n["g"], n["beta"], n["state"], par)
     assert np.abs(o[0, 0].double().cpu().numpy() - want).max() <= 2.0 ** -8 * np.abs(want).max() + 1e-4
+
+
+# ----------------------------------------------------------------------------- the grids that large batches take
+@pytest.mark.parametrize("T", [5, 16, 20, 48, 64])
+@pytest.mark.parametrize("HK, HV", [(4, 4), (2, 4), (2, 6), (2, 8), (1, 5)])
+def test_tree_verify_of_large_batches(gpu_lib, T, HK, HV):
+    """Enough heads that the value heads of one key head share a CTA (two, three or four of them; five do not split);
+    one head's operands leave fp16's range, one holds a NaN: the others of their CTA are as without them."""
+    L, B = 40, 16
+    rng = np.random.default_rng(T)
+    par = [tree(rng, T, "random") for _ in range(B)]
+    c = case(T, L, B, (B, T), HK, HV, 128, 128)
+    clean = verify(gpu_lib, c, par)
+    for l, b in ((0, 0), (L - 1, B - 1), (17, 5)):
+        want, _, M = ref_run(c, l, slice(b * T, (b + 1) * T), par[b], c["state"][l, b], 1e-6, 128 ** -0.5)
+        close_o(clean[l, b], want, M, T, 128, 128 ** -0.5)
+    c["v"][3, 2, T - 1, HV - 1] = float("nan")
+    c["v"][3, 2, :, 0, 7] *= 1e30
+    c["state"][3, 2, 0, 9] = 1e25
+    o = verify(gpu_lib, c, par)
+    keep = torch.ones_like(o, dtype=torch.bool)
+    keep[3, 2, :, 0] = False
+    keep[3, 2, :, HV - 1] = False
+    assert torch.equal(o[keep], clean[keep])
+    assert not torch.isfinite(o[3, 2, T - 1, HV - 1]).any()
+    if HV > 1:  # features of very different size in one head: each is as exact as alone
+        want, _, _ = ref_run(c, 3, slice(2 * T, 3 * T), par[2], c["state"][3, 2], 1e-6, 128 ** -0.5)
+        for f in (7, 9, 20):
+            x, y = o[3, 2, :, 0, f].double(), want[:, 0, f]
+            assert (x - y).norm() <= (2.0 ** -8 + 2.0 ** -9) * y.norm()
+
+
+@pytest.mark.parametrize("DK, DV", [(64, 64), (64, 128), (128, 128)])
+@pytest.mark.parametrize("what", ["clean", "v", "k", "wide"])
+def test_scan_of_large_batches(gpu_lib, what, DK, DV):
+    """Whole heads per CTA (many of them), sequences started in another order than theirs, bad values in one."""
+    lens = [70, 0, 200, 17, 64, 129, 33]
+    c = case(21, 1, len(lens), (sum(lens) + 4,), 4, 16, DK, DV)
+    at = lens[0] + 100  # token 100 of the third sequence
+    if what in ("v", "k"):
+        clean, s0 = scan(gpu_lib, c, np.cumsum([2] + lens).tolist(), max(lens), torch.empty_like(c["state"]))
+        c[what][0, 2 + at, 1] = float("nan")
+        o, _ = scan(gpu_lib, c, np.cumsum([2] + lens).tolist(), max(lens), torch.empty_like(c["state"]))
+        hit = torch.zeros(o.shape[1:3], dtype=torch.bool, device=DEV)
+        heads = [1] if what == "v" else [4, 5, 6, 7]
+        hit[2 + at:2 + lens[0] + lens[2], heads] = True
+        assert not torch.isfinite(o[0][hit]).any()
+        # the chunk ahead of the NaN is done again token by token: the same values up to bf16's rounding of either
+        x, y = o[0][~hit].double(), clean[0][~hit].double()
+        assert ((x - y).abs() <= 2.0 ** -7 * y.abs() + 1e-3).all()
+        return
+    if what == "wide":  # v's features 2^80 apart
+        c["v"][..., ::2] *= 2.0 ** -80
+        c["state"][:, :, :, ::2] *= 2.0 ** -80
+        cu = np.cumsum([2] + lens).tolist()
+        out = torch.empty_like(c["state"])
+        o, st = scan(gpu_lib, c, cu, max(lens), out)
+        want, S, _ = ref_run(c, 0, slice(cu[2], cu[3]), list(range(-1, lens[2] - 1)), c["state"][0, 2], 1e-6, DK ** -0.5)
+        for half in (slice(0, None, 2), slice(1, None, 2)):
+            assert (o[0, cu[2]:cu[3]][..., half].double() - want[..., half]).norm() <= (2.0 ** -8 + 2.0 ** -9) * want[..., half].norm()
+            assert (out[0, 2][:, half].double() - S[-1][:, half]).norm() <= 2.0 ** -18 * S[-1][:, half].norm()
+        return
+    check_scan(gpu_lib, c, lens, lead=2)
+
+
+def test_scan_of_more_sequences_than_are_sorted(gpu_lib):
+    rng = np.random.default_rng(0)
+    lens = [int(x) for x in rng.integers(0, 40, 300)]
+    check_scan(gpu_lib, case(22, 1, 300, (sum(lens),), 1, 1, 128, 128), lens)
+
+
+def test_scan_beyond_fp16(gpu_lib):
+    """Keys far from unit length: the recurrence grows beyond fp16's range, token by token in fp32 then, and stays exact
+    where it still is finite."""
+    for n in (40, 150):
+        c = case(23, 1, 1, (n,), 1, 2, 128, 128, "none")
+        c["k"] = c["k"] * (0.5 if n == 40 else 0.35)
+        o, st = scan(gpu_lib, c, [0, n], n, torch.empty_like(c["state"]), eps=0.0)
+        want, S, _ = ref_run(c, 0, slice(0, n), list(range(-1, n - 1)), c["state"][0, 0], 0.0, 128 ** -0.5)
+        assert want.abs().max() > 65504
+        # every step multiplies a direction by up to |1 - beta |k|^2|: errors grow as the values do
+        assert (o[0].double() - want).norm() <= (2.0 ** -8 + 2.0 ** -10) * want.norm()
+
+
+def test_scan_without_rows(gpu_lib):
+    c = case(24, 2, 3, (0,), 1, 2, 128, 128)
+    out = torch.full_like(c["state"], 7.0)
+    o, st = scan(gpu_lib, c, [0, 0, 0, 0], 0, out)
+    assert st.tolist() == [0, 0, 0, 0] and torch.equal(out, c["state"])
+
+
+def test_scan_rows_beyond_32_bits(gpu_lib):
+    """Rows whose v and o lie past 2^31 bytes."""
+    HV, rows, n = 64, (1 << 31) // (64 * 128 * 2) + 300, 100
+    gen = torch.Generator().manual_seed(4)
+    r = lambda *s: torch.randn(*s, generator=gen).to(DEV)  # noqa: E731
+    c = dict(q=torch.empty(1, rows, 1, 128, dtype=torch.bfloat16, device=DEV), k=torch.empty(1, rows, 1, 128, dtype=torch.bfloat16, device=DEV),
+             v=torch.empty(1, rows, HV, 128, dtype=torch.bfloat16, device=DEV), g=torch.empty(1, rows, HV, device=DEV),
+             beta=torch.empty(1, rows, HV, device=DEV), state=0.3 * r(1, 1, HV, 128, 128))
+    at = rows - n
+    c["q"][0, at:], c["k"][0, at:], c["v"][0, at:] = r(n, 1, 128).bfloat16(), r(n, 1, 128).bfloat16(), r(n, HV, 128).bfloat16()
+    c["g"][0, at:], c["beta"][0, at:] = -r(n, HV).abs(), torch.sigmoid(r(n, HV))
+    o = torch.empty_like(c["v"])
+    out = torch.empty_like(c["state"])
+    for m in (n, 5):  # in chunks, token by token
+        scan(gpu_lib, c, [rows - m, rows], m, out, o=o)
+        want, S, M = ref_run(c, 0, slice(rows - m, rows), list(range(-1, m - 1)), c["state"][0, 0], 1e-6, 128 ** -0.5)
+        close_o(o[0, rows - m:], want, M, m, 128, 128 ** -0.5)
+        close_state(out[0, 0], S[-1], M, m, 128)
+
+
+@pytest.mark.parametrize("T", [1, 9, 64])
+def test_two_calls_at_once(gpu_lib, T):
+    """The calls on two streams at a time, over their own outputs, give what they give one after the other."""
+    rng = np.random.default_rng(T)
+    L, B = 4, 8
+    par = [tree(rng, T, "random") for _ in range(B)]
+    anc = anc_of(gpu_lib, par)
+    cu = torch.arange(0, 30 * (B + 1), 30, dtype=torch.int32, device=DEV)
+    t, s = case(1, L, B, (B, T), 2, 8, 128, 128), case(2, L, B, (30 * B,), 2, 8, 128, 128)
+    outs = [[torch.empty_like(t["v"]), torch.empty_like(s["v"]), torch.empty_like(s["state"])] for _ in range(3)]
+
+    def calls(x):
+        gpu_lib.gdn_tree_verify(gpu_lib.gdn_desc(*(per(t[y], L) for y in ("q", "k", "v", "g", "beta", "state")), o=per(x[0], L)), anc)
+        gpu_lib.gdn_scan(gpu_lib.gdn_desc(*(per(s[y], L) for y in ("q", "k", "v", "g", "beta", "state")), o=per(x[1], L),
+                                          state_out=per(x[2], L)), cu, max_len=30)
+
+    calls(outs[0])
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    for _ in range(5):
+        for st, x in zip(streams, outs[1:]):
+            with torch.cuda.stream(st):
+                calls(x)
+    torch.cuda.synchronize()
+    for x in outs[1:]:
+        assert all(torch.equal(a, b) for a, b in zip(x, outs[0]))
