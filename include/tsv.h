@@ -223,13 +223,15 @@ typedef struct {
 } tsv_attn_desc;
 
 /* Kernel choice.  AUTO takes the tensor-core (tcgen05) kernel where it applies
- * (D == 256) and the CUDA-core kernel elsewhere.
+ * (D == 256) and the CUDA-core kernel elsewhere; 4-bit caches of up to 16 query
+ * rows per K/V head, or of other head dimensions, take a kernel of their own.
  * TCGEN05 lets the library pick the tensor-core kernel's score-tile width (128
  * keys for Int8 caches and for units of more than 128 query rows, else 64);
  * TCGEN05_64 and TCGEN05_128 force one (both compute the same result; 4-bit
- * caches have 64-key tiles only).
+ * caches have 128-key tiles only).
  * On the tensor-core path Q is rounded to the cache's 16-bit type for the
- * Q K^T product (exact for bf16; for fp16 caches |q| must lie in fp16 range)
+ * Q K^T product (exact for bf16; for fp16, Int8 and 4-bit caches, whose products
+ * are fp16, |q| must lie in fp16 range)
  * and the softmax weights P enter P V as 16-bit values. */
 #define TSV_ATTN_AUTO 0
 #define TSV_ATTN_SIMT 1
@@ -478,9 +480,10 @@ tsv_status tsv_tree_append(const tsv_append_desc* d, int32_t* kv_len, int32_t* d
  *   strength beta:
  *     S <- e^g S;  u = beta (v - S k);  S <- S + u k^T;  o = scale * S q
  *   Value head h reads key head h / (HV / HK).  With norm_eps > 0 every row of q and k is divided by
- *   sqrt(sum x^2 + norm_eps) first.  All arithmetic and the state are fp32 (products on the tensor cores take an
- *   fp32 operand as a sum of bf16 pieces: three for what the state is made of, two for what only reaches o); o is
- *   rounded to bf16 once.  g may be -infinity (the state is forgotten).
+ *   sqrt(sum x^2 + norm_eps) first.  Sums and the state are fp32.  Products on the tensor cores take their operands as
+ *   fp16 with power-of-two scales: an hi + lo pair (within 2^-22 of the value) for what reaches the state, one fp16
+ *   (2^-12) for what reaches o alone; a block whose operands leave fp16's range is computed in fp32.  o is rounded to
+ *   bf16 once.  g may be -infinity (the state is forgotten).
  *
  * tsv_gdn_tree_verify - o of every node of each sequence's tree, node i starting from its parent's state and the
  *   root from state[l][b].  The state is read once and not written (state_out is ignored).  anc: uint64 [B, T] from
@@ -497,7 +500,8 @@ tsv_status tsv_tree_append(const tsv_append_desc* d, int32_t* kv_len, int32_t* d
  *   no sequence owns are not read and their o is not written.  Device errors: TSV_DEV_BAD_SEQ_LEN (that sequence's
  *   o and state_out are not written).
  *
- * state_out[l] may equal state[l] (in place); otherwise they must not overlap, nor may o overlap an input.
+ * state_out[l] may equal state[l] (in place); otherwise they must not overlap, nor may o overlap an input, nor the
+ * outputs of two layers each other.
  */
 typedef struct {
     int32_t n_layers;   /* 1 .. TSV_MAX_LAYERS */

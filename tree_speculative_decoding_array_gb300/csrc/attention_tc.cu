@@ -41,6 +41,8 @@
 // thread owns one key of every tile and writes its codes times its scale
 // (fp16, one rounding; the scale fetched a tile ahead) into 2-stage operand
 // rings, so the softmax does no scale work.
+// 4-bit caches (TSV_I4_G64) have one kernel, the 128-key one of the byte caches
+// (attn_tcw8_kernel<true>, below).
 // Warp-collective roles take every wait decision warp-uniformly (__all_sync),
 // so that tcgen05.ld / __syncwarp never see a partial warp.
 // Every mbarrier wait is bounded in time: on expiry the CTA raises a shared
@@ -211,42 +213,34 @@ __device__ __forceinline__ void i4x8_to_f16x8(uint32_t w, __half2 s2, __half2 b2
     }
 }
 
-// Raw 4-bit tile [64 keys x 128 B], 128-byte swizzled as TMA lands it -> the same fp16 operand tile as
-// convert_i8_tile; `pairs` holds this thread's key's four (scale, bias) pairs, zeros past the key range (any code then
-// gives 0).  Thread ct takes key ct & 63 and the chunks 2 s + (ct >> 6): 32 codes each, within one group of 64.
-__device__ __forceinline__ void convert_i4_tile(const uint8_t* raw, uint8_t* dst, int ct, uint4 pairs) {
-    const int key = ct & 63, k7 = key & 7;
-    const uint32_t pr[4] = {pairs.x, pairs.y, pairs.z, pairs.w};
-    uint4 in[4];
+// W words of one key's codes, within one group of 64 features -> its fp16 operand row, the 16-byte chunks
+// c0 .. c0 + W - 1 (chunk c at ((c ^ (key & 7)) << 4)).
+template <int W>
+__device__ __forceinline__ void convert_i4(const uint32_t (&w)[W], uint32_t pair, uint8_t* row, int c0, int k7) {
+    const __half2 sb = *reinterpret_cast<const __half2*>(&pair);
+    const __half2 s2 = __low2half2(sb), b2 = __high2half2(sb);
 #pragma unroll
-    for (int s = 0; s < 4; ++s)
-        in[s] = *reinterpret_cast<const uint4*>(raw + key * 128 + (((2 * s + (ct >> 6)) ^ k7) << 4));
-    uint8_t* row = dst + key * 128;
-#pragma unroll
-    for (int s = 0; s < 4; ++s) {
-        const __half2 pair = *reinterpret_cast<const __half2*>(&pr[s]);
-        const __half2 s2 = __low2half2(pair), b2 = __high2half2(pair);
-        const uint32_t w[4] = {in[s].x, in[s].y, in[s].z, in[s].w};
-        // features 32 (2 s + half) .. + 31: 64-feature block s, 16-byte chunks 4 half .. 4 half + 3
-        uint8_t* rb = row + s * 8192;
-#pragma unroll
-        for (int c = 0; c < 4; ++c) {
-            uint32_t o[4];
-            i4x8_to_f16x8(w[c], s2, b2, o);
-            *reinterpret_cast<uint4*>(rb + (((4 * (ct >> 6) + c) ^ k7) << 4)) = make_uint4(o[0], o[1], o[2], o[3]);
-        }
+    for (int c = 0; c < W; ++c) {
+        uint32_t o[4];
+        i4x8_to_f16x8(w[c], s2, b2, o);
+        *reinterpret_cast<uint4*>(row + (((c0 + c) ^ k7) << 4)) = make_uint4(o[0], o[1], o[2], o[3]);
     }
+}
+
+// Two fp32 sums per instruction.
+__device__ __forceinline__ float2 add2(float2 a, float2 b) {
+    float2 c;
+    asm("{\n .reg .b64 x, y, z;\n mov.b64 x, {%2, %3};\n mov.b64 y, {%4, %5};\n add.rn.f32x2 z, x, y;\n mov.b64 {%0, %1}, z;\n}"
+        : "=f"(c.x), "=f"(c.y)
+        : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
+    return c;
 }
 
 constexpr int kNS = 3;  // stages of the K ring and of the V ring
 
-// FMT: 0 16-bit caches, 1 Int8, 2 4-bit.  The quantised formats share one pipeline (converter warps, two issuers) and
-// differ in the raw tile and its conversion.
-template <int FMT>
-__global__ void __launch_bounds__(FMT != 0 ? kTcThreadsI8 : kTc64Threads16, 1) attn_tc_kernel(const __grid_constant__ TcParams p) {
+template <bool I8>
+__global__ void __launch_bounds__(I8 ? kTcThreadsI8 : kTc64Threads16, 1) attn_tc_kernel(const __grid_constant__ TcParams p) {
     griddep_begin();
-    constexpr bool I8 = FMT != 0;   // the quantised pipeline
-    constexpr bool I4 = FMT == 2;
     extern __shared__ uint8_t smem_raw[];
     uint8_t* sm = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
     // Q, S and P live in TMEM.  16-bit caches: K stages [3 x 32K] at 0, V stages [3 x 32K] at 96K.
@@ -372,10 +366,7 @@ __global__ void __launch_bounds__(FMT != 0 ? kTcThreadsI8 : kTc64Threads16, 1) a
                 const int st = j % NS;
                 if (j >= NS && !tc::mbar_wait(&emptyb[st], ((j / NS) - 1) & 1, abort_flag, 256)) break;
                 const int row = rowbase + j * kTcBK;
-                if (I4) {  // 128-byte rows: one swizzled box
-                    tc::mbar_expect_tx(&fullb[st], kTcBK * kTcD / 2);
-                    tc::tma_load_2d((isK ? sRawK : sRawV) + st * 16384, m, &fullb[st], 0, row);
-                } else if (I8) {  // two 128-byte-wide swizzled halves of the 256-byte rows
+                if (I8) {  // two 128-byte-wide swizzled halves of the 256-byte rows
                     tc::mbar_expect_tx(&fullb[st], kTcBK * kTcD);
                     uint8_t* dst = (isK ? sRawK : sRawV) + st * 16384;
                     tc::tma_load_2d(dst, m, &fullb[st], 0, row);
@@ -518,34 +509,7 @@ __global__ void __launch_bounds__(FMT != 0 ? kTcThreadsI8 : kTc64Threads16, 1) a
                 drain_wait(drain, 0);
             }
         }
-    } else if (I4 && warp >= 6 && warp < 14) {
-        // ------------------------------------------------------------ 4-bit converters: warps 6-9 K, 10-13 V
-        // (one piece of code for both: the kernel's roles share the instruction cache).  As the Int8 converters: key
-        // ct & 63 of every tile, its (scale, bias) pairs fetched one tile ahead.  An fp16 K slot is free once Q K^T of
-        // tile j - 2 is done, an fp16 V slot once P V of tile j - 2 is.
-        const bool isK = warp < 10;
-        const int ct = (threadIdx.x - 192) & 127;
-        const uint4* src = reinterpret_cast<const uint4*>(isK ? p.ks[layer] : p.vs[layer]) + ((size_t)b * p.HKV + kvh) * (size_t)p.s_cap + k_begin + (ct & 63);
-        uint64_t *full = isK ? kfull : vfull, *empty = isK ? kempty : vempty, *slot_free = isK ? s_full : sp_free, *done = isK ? kc_full : vc_full;
-        const uint8_t* raw = isK ? sRawK : sRawV;
-        uint8_t* dst = isK ? sK : sV;
-        auto pairs = [&](int jj) {
-            return jj < ntiles && k_begin + jj * kTcBK + (ct & 63) < k_end ? src[(size_t)jj * kTcBK] : make_uint4(0, 0, 0, 0);
-        };
-        uint4 next = pairs(0);
-        for (int j = 0; j < ntiles; ++j) {
-            const int st = j % NS, cb = j & 1;
-            const uint4 sc = next;
-            next = pairs(j + 1);
-            if (!__all_sync(0xFFFFFFFFu, tc::mbar_wait(&full[st], (j / NS) & 1, abort_flag))) break;
-            if (j >= 2 && !__all_sync(0xFFFFFFFFu, tc::mbar_wait(&slot_free[cb], ((j >> 1) - 1) & 1, abort_flag))) break;
-            convert_i4_tile(raw + st * 16384, dst + cb * kTileBytes, ct, sc);
-            tc::fence_proxy_async_smem();
-            __syncwarp();
-            tc::mbar_arrive_one(&empty[st]);
-            tc::mbar_arrive_one(&done[cb]);
-        }
-    } else if (I8 && !I4 && warp >= 10 && warp < 14) {
+    } else if (I8 && warp >= 10 && warp < 14) {
         // ------------------------------------------------------------ Int8 V converters
         // each thread converts key ct & 63 of every tile and multiplies its codes by that key's scale; the scale
         // is fetched one tile ahead so that the global load's latency overlaps the previous tile's work
@@ -569,7 +533,7 @@ __global__ void __launch_bounds__(FMT != 0 ? kTcThreadsI8 : kTc64Threads16, 1) a
             tc::mbar_arrive_one(&vempty[st]);
             tc::mbar_arrive_one(&vc_full[cb]);
         }
-    } else if (I8 && !I4 && warp >= 6 && warp < 10) {
+    } else if (I8 && warp >= 6 && warp < 10) {
         // ------------------------------------------------------------ Int8 K converters
         // as the V converters: key ct & 63 of every tile, times its scale, fetched one tile ahead
         const int ct = threadIdx.x - 192;
@@ -626,13 +590,6 @@ __global__ void __launch_bounds__(FMT != 0 ? kTcThreadsI8 : kTc64Threads16, 1) a
                     for (int i = 0; i < 8; ++i) {
                         uint4 x = v[c2 * 8 + i];
                         if (!bf) x = bf16x8_to_f16x8(x);
-                        if (I4) {  // feature order 0 4 1 5 2 6 3 7
-                            w[4 * i] = __byte_perm(x.x, x.z, 0x5410);
-                            w[4 * i + 1] = __byte_perm(x.x, x.z, 0x7632);
-                            w[4 * i + 2] = __byte_perm(x.y, x.w, 0x5410);
-                            w[4 * i + 3] = __byte_perm(x.y, x.w, 0x7632);
-                            continue;
-                        }
                         w[4 * i] = x.x;
                         w[4 * i + 1] = x.y;
                         w[4 * i + 2] = x.z;
@@ -661,19 +618,10 @@ __global__ void __launch_bounds__(FMT != 0 ? kTcThreadsI8 : kTc64Threads16, 1) a
         const float qk_scale = 1.4426950408889634f * 0.0625f;  // log2(e) / sqrt(256)
         float m_ref = -INFINITY, l = 0.f;
         bool ok = true;
-        // 4-bit caches: two warps whose 32 rows are all padding leave S and P as they are (a row of P only reaches its
-        // own row of O, which nobody reads) and the issue slots to the converters.
-        const bool idle = I4 && row0 + qd * 32 >= p.R;
         for (int j = 0; j < ntiles; ++j) {
             const int sb = j & 1;
-            if (!__all_sync(0xFFFFFFFFu, tc::mbar_wait(&s_full[sb], (j >> 1) & 1, abort_flag, idle ? 256 : 32))) { ok = false; break; }
+            if (!__all_sync(0xFFFFFFFFu, tc::mbar_wait(&s_full[sb], (j >> 1) & 1, abort_flag))) { ok = false; break; }
             tc::tc_fence_after();
-            if (idle) {
-                __syncwarp();
-                tc::mbar_arrive_one(s_free);
-                tc::mbar_arrive_one(&p_full[sb]);
-                continue;
-            }
             uint32_t sc[32];
             tc::tmem_ld32(tmem + lane_base + kColS + (I8 ? 0 : sb * kTcBK) + h * 32, sc);
             tc::tmem_wait_ld();
@@ -781,7 +729,7 @@ __global__ void __launch_bounds__(FMT != 0 ? kTcThreadsI8 : kTc64Threads16, 1) a
             __syncwarp();
             tc::mbar_arrive_one(&p_full[sb]);
         }
-        if (ok && !idle) {  // the row sum of both halves
+        if (ok) {  // the row sum of both halves
             float lo;
             if (exchange(ntiles, l, lo)) l += lo;
             else ok = false;
@@ -796,19 +744,6 @@ __global__ void __launch_bounds__(FMT != 0 ? kTcThreadsI8 : kTc64Threads16, 1) a
                 tc::tmem_ld32(tmem + lane_base + kColO + ch * 32, o);
                 tc::tmem_wait_ld();
                 if (!row_ok) continue;
-                if (I4) {  // columns 0 4 1 5 2 6 3 7 of every 8 features back in order
-#pragma unroll
-                    for (int k = 0; k < 4; ++k) {
-                        uint32_t y[8];
-#pragma unroll
-                        for (int e = 0; e < 8; ++e) y[e] = o[8 * k + e];
-#pragma unroll
-                        for (int e = 0; e < 4; ++e) {
-                            o[8 * k + e] = y[2 * e];
-                            o[8 * k + 4 + e] = y[2 * e + 1];
-                        }
-                    }
-                }
                 if (p.splits == 1) {
                     uint4* dst = reinterpret_cast<uint4*>(reinterpret_cast<__nv_bfloat16*>(p.o[layer]) +
                                                           ((size_t)(b * T + node) * p.HQ + head) * kTcD + ch * 32);
@@ -1215,7 +1150,7 @@ __global__ void __launch_bounds__(kTcThreads16, 1) attn_tcw_kernel(const __grid_
     }
 }
 
-// ------------------------------------------------------------------ Int8 caches: 128-key score tiles
+// ------------------------------------------------------------------ Int8 and 4-bit caches: 128-key score tiles
 // The same 128-key Q K^T (N = 128) for Int8 caches.  TMEM as in attn_tcw_kernel: Q [0, 128), S [128, 256) (one
 // buffer, freed as soon as the softmax has read it), O [256, 512).  An fp16 K tile of 128 keys (64 KB) does
 // not fit twice beside the other rings, so K moves in dim quarters (128 keys x 64 dims): TMA lands a raw quarter
@@ -1237,6 +1172,13 @@ __global__ void __launch_bounds__(kTcThreads16, 1) attn_tcw_kernel(const __grid_
 //   warps 11-14      K converters (thread = key of the quarter)
 //   warps 15-18      V converters
 //   warp 19          the P V issuer
+// 4-bit caches (I4): the same roles and rings.  A raw K quarter is one group of 64 features (32 bytes a key), a key's
+// four (scale, bias) pairs are one 16-byte load, a tile ahead; the halved raw bytes leave room for two P buffers.  Not
+// bound by HBM (9 % of it at 64-node trees) but by the instructions and hand-offs of the 16 converting and softmax warps
+// beside the MMAs: 384 rows over 2 x 4 layers x 32768 keys take 468 us (880 TFLOP/s), 385 without either conversion,
+// 437 without the softmax, 340 without all three.  Measured against it at those sizes: 64-key tiles with two or three
+// fp16 slots 490 and 475 us, the converters reading their codes from global memory themselves 534 us, one P buffer
+// and six K slots (the same way) 524 us.
 constexpr int kW8Threads = 640;
 
 // Keys c0 .. c0 + 63 as a bit mask (bit c = key c0 + c) of what one query row sees: keys below k_end and at or
@@ -1261,32 +1203,44 @@ constexpr uint32_t kW8OffP = 188416;              // 2 x 16 KB P halves [128 row
 constexpr uint32_t kW8OffX = 221184;              // softmax halves' exchange [2 slots][2 halves][128 rows] fp32
 constexpr uint32_t kW8OffBar = 223232;            // barriers, TMEM slot, abort flag
 constexpr int kW8Smem = 1024 + 223232 + 512;
+// 4-bit caches
+constexpr int kW4KR = 4;
+constexpr uint32_t kW4OffKr = 65536;                       // 4 x 4 KB raw K quarters [128 keys][32 B]
+constexpr uint32_t kW4OffVh = kW4OffKr + kW4KR * 4096;     // 2 x 32 KB
+constexpr uint32_t kW4OffVr = kW4OffVh + 65536;            // 2 x 8 KB raw V halves [64 keys][128 B]
+constexpr uint32_t kW4OffP = kW4OffVr + 16384;             // 2 x 2 x 16 KB
+constexpr uint32_t kW4OffX = kW4OffP + 65536;
+constexpr uint32_t kW4OffBar = kW4OffX + 2048;
+constexpr int kW4Smem = kW4OffBar + 512;
 constexpr float kLog2eOverSqrtD = 1.4426950408889634f * 0.0625f;
 
 
+template <bool I4>
 __global__ void __launch_bounds__(kW8Threads, 1) attn_tcw8_kernel(const __grid_constant__ TcParams p) {
     griddep_begin();
-    extern __shared__ uint8_t smem_raw[];
-    uint8_t* sm = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+    extern __shared__ __align__(1024) uint8_t smem_raw[];
+    uint8_t* sm = I4 ? smem_raw : reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+    constexpr int KR = I4 ? kW4KR : kW8KR;
+    constexpr uint32_t kKrBytes = I4 ? 4096 : 8192, kVrBytes = I4 ? 8192 : 16384;
     uint8_t* sKh = sm + kW8OffKh;
-    uint8_t* sKr = sm + kW8OffKr;
-    uint8_t* sVh = sm + kW8OffVh;
-    uint8_t* sVr = sm + kW8OffVr;
-    uint8_t* sP = sm + kW8OffP;
-    float* xv = reinterpret_cast<float*>(sm + kW8OffX);
-    uint64_t* bars = reinterpret_cast<uint64_t*>(sm + kW8OffBar);
-    uint64_t* kr_full = bars + 0;    // [3] raw K quarter landed
-    uint64_t* kr_empty = bars + 3;   // [3] the K converters are done with it
-    uint64_t* kq_full = bars + 6;    // [4] fp16 K quarter written
-    uint64_t* kq_empty = bars + 10;  // [4] Q K^T done with it
-    uint64_t* vr_full = bars + 14;   // [2] raw V half landed
-    uint64_t* vr_empty = bars + 16;  // [2] the V converters are done with it
-    uint64_t* vh_full = bars + 18;   // [2] fp16 V half written
-    uint64_t* vh_empty = bars + 20;  // [2] P V done with it
-    uint64_t* s_full = bars + 22;    // Q K^T of a tile done
-    uint64_t* s_free = bars + 23;    // both softmax halves read S (8 warps)
-    uint64_t* p_full = bars + 24;    // [2] P half written (4 warps)
-    uint64_t* p_free = bars + 26;    // [2] P V done with the P half
+    uint8_t* sKr = sm + (I4 ? kW4OffKr : kW8OffKr);
+    uint8_t* sVh = sm + (I4 ? kW4OffVh : kW8OffVh);
+    uint8_t* sVr = sm + (I4 ? kW4OffVr : kW8OffVr);
+    uint8_t* sP = sm + (I4 ? kW4OffP : kW8OffP);
+    float* xv = reinterpret_cast<float*>(sm + (I4 ? kW4OffX : kW8OffX));
+    uint64_t* bars = reinterpret_cast<uint64_t*>(sm + (I4 ? kW4OffBar : kW8OffBar));
+    uint64_t* kr_full = bars + 0;                  // [KR] raw K quarter landed
+    uint64_t* kr_empty = bars + (I4 ? 4 : 3);      // [KR] the K converters are done with it
+    uint64_t* kq_full = bars + (I4 ? 8 : 6);       // [4] fp16 K quarter written
+    uint64_t* kq_empty = bars + (I4 ? 12 : 10);    // [4] Q K^T done with it
+    uint64_t* vr_full = bars + (I4 ? 16 : 14);     // [2] raw V half landed
+    uint64_t* vr_empty = bars + (I4 ? 18 : 16);    // [2] the V converters are done with it
+    uint64_t* vh_full = bars + (I4 ? 20 : 18);     // [2] fp16 V half written
+    uint64_t* vh_empty = bars + (I4 ? 22 : 20);    // [2] P V done with it
+    uint64_t* s_full = bars + (I4 ? 42 : 22);      // Q K^T of a tile done
+    uint64_t* s_free = bars + (I4 ? 43 : 23);      // both softmax halves read S (8 warps)
+    uint64_t* p_full = bars + (I4 ? 44 : 24);      // [2] P half written (4 warps); 4-bit: [2][2], of either buffer
+    uint64_t* p_free = bars + (I4 ? 24 : 26);      // [2] P V done with the P half; 4-bit: with both halves of a buffer
     uint64_t* xch = bars + 28;       // [4 lane quarters][2 parities] both halves posted their value
     uint64_t* q_full = bars + 36;
     uint64_t* o_done = bars + 37;
@@ -1334,7 +1288,7 @@ __global__ void __launch_bounds__(kW8Threads, 1) attn_tcw8_kernel(const __grid_c
     }
 
     if (threadIdx.x == 0) {
-        for (int s = 0; s < kW8KR; ++s) {
+        for (int s = 0; s < KR; ++s) {
             tc::mbar_init(&kr_full[s], 1);
             tc::mbar_init(&kr_empty[s], 4);
         }
@@ -1348,6 +1302,7 @@ __global__ void __launch_bounds__(kW8Threads, 1) attn_tcw8_kernel(const __grid_c
             tc::mbar_init(&vh_full[s], 4);
             tc::mbar_init(&vh_empty[s], 1);
             tc::mbar_init(&p_full[s], 4);
+            if (I4) tc::mbar_init(&p_full[2 + s], 4);
             tc::mbar_init(&p_free[s], 1);
         }
         for (int s = 0; s < 8; ++s) tc::mbar_init(&xch[s], 2);
@@ -1377,16 +1332,19 @@ __global__ void __launch_bounds__(kW8Threads, 1) attn_tcw8_kernel(const __grid_c
             const CUtensorMap* m = isK ? &p.kmap[layer] : &p.vmap[layer];
             tc::tma_prefetch_desc(m);
             const int n = isK ? 4 * ntiles : nhalves;
-            const int NS = isK ? kW8KR : 2;
+            const int NS = isK ? KR : 2;
             uint64_t* fullb = isK ? kr_full : vr_full;
             uint64_t* emptyb = isK ? kr_empty : vr_empty;
             int issued = 0;
             for (int g = 0; g < n; ++g) {
                 const int st = g % NS;
                 if (g >= NS && !tc::mbar_wait(&emptyb[st], ((g / NS) - 1) & 1, abort_flag, 256)) break;
-                if (isK) {  // quarter g & 3 of tile g >> 2: 128 keys x 64 bytes
+                if (isK) {  // quarter g & 3 of tile g >> 2: 128 keys x 64 (4-bit: 32) bytes
+                    tc::mbar_expect_tx(&fullb[st], kKrBytes);
+                    tc::tma_load_2d(sKr + st * kKrBytes, m, &fullb[st], (g & 3) * (I4 ? 32 : 64), rowbase + (g >> 2) * kWK);
+                } else if (I4) {  // 64 keys x 128 bytes
                     tc::mbar_expect_tx(&fullb[st], 8192);
-                    tc::tma_load_2d(sKr + st * 8192, m, &fullb[st], (g & 3) * 64, rowbase + (g >> 2) * kWK);
+                    tc::tma_load_2d(sVr + st * 8192, m, &fullb[st], 0, rowbase + g * kTcBK);
                 } else {    // 64 keys x 256 bytes as two 128-byte-wide halves
                     tc::mbar_expect_tx(&fullb[st], 16384);
                     uint8_t* dst = sVr + st * 16384;
@@ -1430,16 +1388,18 @@ __global__ void __launch_bounds__(kW8Threads, 1) attn_tcw8_kernel(const __grid_c
             } else {
                 for (int pq = 0; ok && pq < nhalves; ++pq) {  // P V of half pq: P written, fp16 V half there
                     const int h = pq & 1, jt = pq >> 1;
-                    ok = tc::mbar_wait(&p_full[h], jt & 1, abort_flag, 32, 64);
+                    const int pb = I4 ? jt & 1 : 0;  // P buffer
+                    ok = tc::mbar_wait(&p_full[2 * pb + h], (I4 ? jt >> 1 : jt) & 1, abort_flag, 32, 64);
                     if (ok) ok = tc::mbar_wait(&vh_full[h], jt & 1, abort_flag, 32, 64);
                     if (!ok) break;
                     tc::tc_fence_after();
-                    const uint64_t a = tc::sdesc_add(dP, h * 16384), bv = tc::sdesc_add(dV, h * 32768);
+                    const uint64_t a = tc::sdesc_add(dP, pb * 32768 + h * 16384), bv = tc::sdesc_add(dV, h * 32768);
                     tc::mma_f16(tO, a, bv, id_pv, pq > 0 ? 1u : 0u);
                     tc::mma_f16(tO, tc::sdesc_add(a, 32), tc::sdesc_add(bv, 2048), id_pv, 1u);
                     tc::mma_f16(tO, tc::sdesc_add(a, 64), tc::sdesc_add(bv, 4096), id_pv, 1u);
                     tc::mma_f16(tO, tc::sdesc_add(a, 96), tc::sdesc_add(bv, 6144), id_pv, 1u);
-                    tc::mma_commit(&p_free[h]);
+                    if (!I4) tc::mma_commit(&p_free[h]);
+                    else if (h == 1) tc::mma_commit(&p_free[pb]);
                     tc::mma_commit(&vh_empty[h]);
                 }
             }
@@ -1451,7 +1411,65 @@ __global__ void __launch_bounds__(kW8Threads, 1) attn_tcw8_kernel(const __grid_c
                 drain_wait(dr, 0);
             }
         }
-    } else if (warp >= 11 && warp < 15) {
+    } else if (I4 && warp >= 11 && warp < 15) {
+        // ------------------------------------------------------------ 4-bit K converters: thread = key of the quarter, a
+        // quarter = a group of 64 features; the key's (scale, bias) pairs are fetched a tile ahead, zeros past the range
+        const int key = threadIdx.x - 352, k7 = key & 7;
+        const uint4* pairs = reinterpret_cast<const uint4*>(p.ks[layer]) + seq_row + k_begin + key;
+        auto pair_of = [&](int jj) { return jj < ntiles && k_begin + jj * kWK + key < k_end ? pairs[(size_t)jj * kWK] : make_uint4(0, 0, 0, 0); };
+        uint4 pr = make_uint4(0, 0, 0, 0), next = pair_of(0);
+        for (int g = 0; g < 4 * ntiles; ++g) {
+            const int rs = g % KR, q = g & 3;
+            if (q == 0) {
+                pr = next;
+                next = pair_of((g >> 2) + 1);
+            }
+            if (!__all_sync(0xFFFFFFFFu, tc::mbar_wait(&kr_full[rs], (g / KR) & 1, abort_flag, 128, 0))) break;
+            // raw row: 32 bytes, 16-byte chunk c at ((c ^ ((key >> 2) & 1)) << 4) (32-byte swizzle)
+            const uint8_t* raw = sKr + rs * kKrBytes + key * 32;
+            uint32_t w[8];
+#pragma unroll
+            for (int c = 0; c < 2; ++c) {
+                const uint4 x = *reinterpret_cast<const uint4*>(raw + ((c ^ ((key >> 2) & 1)) << 4));
+                w[4 * c] = x.x; w[4 * c + 1] = x.y; w[4 * c + 2] = x.z; w[4 * c + 3] = x.w;
+            }
+            if (g >= 4 && !__all_sync(0xFFFFFFFFu, tc::mbar_wait(&kq_empty[q], ((g >> 2) - 1) & 1, abort_flag, 64, 0))) break;
+            convert_i4<8>(w, pr.x, sKh + q * 16384 + key * 128, 0, k7);
+            pr = make_uint4(pr.y, pr.z, pr.w, 0);
+            tc::fence_proxy_async_smem();
+            __syncwarp();
+            tc::mbar_arrive_one(&kr_empty[rs]);
+            tc::mbar_arrive_one(&kq_full[q]);
+        }
+    } else if (I4 && warp >= 15 && warp < 19) {
+        // ------------------------------------------------------------ 4-bit V converters: key ct & 63 of every half; of each
+        // group of 64 features its first or second 32 (ct >> 6)
+        const int ct = threadIdx.x - 480, key = ct & 63, k7 = key & 7, side = ct >> 6;
+        const uint4* pairs = reinterpret_cast<const uint4*>(p.vs[layer]) + seq_row + k_begin + key;
+        auto pair_of = [&](int hh) { return hh < nhalves && k_begin + hh * kTcBK + key < k_end ? pairs[(size_t)hh * kTcBK] : make_uint4(0, 0, 0, 0); };
+        uint4 next = pair_of(0);
+        for (int hh = 0; hh < nhalves; ++hh) {
+            const int st = hh & 1;
+            const uint32_t sb[4] = {next.x, next.y, next.z, next.w};
+            next = pair_of(hh + 1);
+            if (!__all_sync(0xFFFFFFFFu, tc::mbar_wait(&vr_full[st], (hh >> 1) & 1, abort_flag, 128, 0))) break;
+            uint4 in[4];
+#pragma unroll
+            for (int s = 0; s < 4; ++s)
+                in[s] = *reinterpret_cast<const uint4*>(sVr + st * kVrBytes + key * 128 + (((2 * s + side) ^ k7) << 4));
+            if (hh >= 2 && !__all_sync(0xFFFFFFFFu, tc::mbar_wait(&vh_empty[st], ((hh >> 1) - 1) & 1, abort_flag, 64, 0))) break;
+            uint8_t* row = sVh + st * 32768 + key * 128;
+#pragma unroll
+            for (int s = 0; s < 4; ++s) {
+                const uint32_t w[4] = {in[s].x, in[s].y, in[s].z, in[s].w};
+                convert_i4<4>(w, sb[s], row + s * 8192, 4 * side, k7);
+            }
+            tc::fence_proxy_async_smem();
+            __syncwarp();
+            tc::mbar_arrive_one(&vr_empty[st]);
+            tc::mbar_arrive_one(&vh_full[st]);
+        }
+    } else if (!I4 && warp >= 11 && warp < 15) {
         // ------------------------------------------------------------ K converters: thread = key of the quarter
         const int key = threadIdx.x - 352;
         const uint16_t* ksg = p.ks[layer] + seq_row;
@@ -1490,7 +1508,7 @@ __global__ void __launch_bounds__(kW8Threads, 1) attn_tcw8_kernel(const __grid_c
             tc::mbar_arrive_one(&kq_full[q]);
             if (q == 3) sc_cur = sc_nxt;
         }
-    } else if (warp >= 15 && warp < 19) {
+    } else if (!I4 && warp >= 15 && warp < 19) {
         // ------------------------------------------------------------ V converters: 64-key halves
         const int ct = threadIdx.x - 480;
         const uint16_t* vsg = p.vs[layer] + seq_row;
@@ -1542,6 +1560,13 @@ __global__ void __launch_bounds__(kW8Threads, 1) attn_tcw8_kernel(const __grid_c
                                                              bf16_hi(in[e]) * kLog2eOverSqrtD);
                         w[4 * i + e] = *reinterpret_cast<const uint32_t*>(&hh2);
                     }
+                    if (I4) {  // feature order 0 4 1 5 2 6 3 7
+                        const uint32_t x0 = w[4 * i], x1 = w[4 * i + 1], x2 = w[4 * i + 2], x3 = w[4 * i + 3];
+                        w[4 * i] = __byte_perm(x0, x2, 0x5410);
+                        w[4 * i + 1] = __byte_perm(x0, x2, 0x7632);
+                        w[4 * i + 2] = __byte_perm(x1, x3, 0x5410);
+                        w[4 * i + 3] = __byte_perm(x1, x3, 0x7632);
+                    }
                 }
                 tc::tmem_st32(tmem + lane_base + kColQ + c4 * 32, w);
             }
@@ -1561,9 +1586,18 @@ __global__ void __launch_bounds__(kW8Threads, 1) attn_tcw8_kernel(const __grid_c
         };
         float m_ref = -INFINITY, l = 0.f;
         bool ok = true;
+        // 4-bit caches: two warps whose 32 rows are all padding leave P as it is (a row of P only reaches its own row of
+        // O, which nobody reads) and the issue slots to the converters.
+        const bool idle = I4 && row0 + qd * 32 >= p.R;
         for (int j = 0; j < ntiles; ++j) {
-            if (!__all_sync(0xFFFFFFFFu, tc::mbar_wait(s_full, j & 1, abort_flag))) { ok = false; break; }
+            if (!__all_sync(0xFFFFFFFFu, (I4 ? tc::mbar_wait(s_full, j & 1, abort_flag, idle ? 256 : 64, 0) : tc::mbar_wait(s_full, j & 1, abort_flag)))) { ok = false; break; }
             tc::tc_fence_after();
+            if (idle) {
+                __syncwarp();
+                tc::mbar_arrive_one(s_free);
+                tc::mbar_arrive_one(&p_full[2 * (j & 1) + h]);
+                continue;
+            }
             float x[64];  // scores of this half, already in the log2 domain
 #pragma unroll
             for (int c2 = 0; c2 < 2; ++c2) {
@@ -1584,8 +1618,19 @@ __global__ void __launch_bounds__(kW8Threads, 1) attn_tcw8_kernel(const __grid_c
                 for (int c = 0; c < 64; ++c) x[c] = ((vis >> c) & 1ull) ? x[c] : -INFINITY;
             }
             float mx = x[0];
+            if constexpr (I4) {  // four chains of three-input maxima
+                float m4[4];
 #pragma unroll
-            for (int c = 1; c < 64; ++c) mx = fmaxf(mx, x[c]);
+                for (int c = 0; c < 4; ++c) {
+                    m4[c] = fmaxf(x[16 * c], x[16 * c + 1]);
+#pragma unroll
+                    for (int e = 2; e < 16; e += 2) m4[c] = fmaxf(fmaxf(x[16 * c + e], x[16 * c + e + 1]), m4[c]);
+                }
+                mx = fmaxf(fmaxf(m4[0], m4[1]), fmaxf(m4[2], m4[3]));
+            } else {
+#pragma unroll
+                for (int c = 1; c < 64; ++c) mx = fmaxf(mx, x[c]);
+            }
             float mo;
             if (!exchange(j, mx, mo)) { ok = false; break; }
             const float mt_ = fmaxf(mx, mo);
@@ -1597,18 +1642,31 @@ __global__ void __launch_bounds__(kW8Threads, 1) attn_tcw8_kernel(const __grid_c
                 resc = true;
             }
             const float msub = m_ref == -INFINITY ? 0.f : m_ref;
-            if (j >= 1) {  // P V of the previous tile done: the P halves are free again and O is stable
+            const int pb = I4 ? j & 1 : 0;
+            if (I4 && j >= 2) {  // P V of the tile that used this buffer before is done
+                if (!__all_sync(0xFFFFFFFFu, tc::mbar_wait(&p_free[pb], ((j >> 1) - 1) & 1, abort_flag))) { ok = false; break; }
+                tc::tc_fence_after();
+            }
+            if (!I4 && j >= 1) {  // P V of the previous tile done: the P halves are free again and O is stable
                 if (!__all_sync(0xFFFFFFFFu, tc::mbar_wait(&p_free[1], (j - 1) & 1, abort_flag))) { ok = false; break; }
                 tc::tc_fence_after();
             }
             float ps = 0.f;
-            uint8_t* prow = sP + h * 16384 + r * 128;
+            float2 ps2 = make_float2(0.f, 0.f);
+            uint8_t* prow = sP + pb * 32768 + h * 16384 + r * 128;
 #pragma unroll
             for (int ch = 0; ch < 8; ++ch) {  // 8 keys per 16-byte chunk of this row's P half
                 uint32_t pk[4];
 #pragma unroll
                 for (int e = 0; e < 4; ++e) {
                     const int c = ch * 8 + 2 * e;
+                    if constexpr (I4) {
+                        const float2 y = add2(make_float2(x[c], x[c + 1]), make_float2(-msub, -msub));
+                        const float2 z = make_float2(tc::ex2_approx(y.x), tc::ex2_approx(y.y));
+                        ps2 = add2(ps2, z);
+                        pk[e] = pack2(z.x, z.y, false);
+                        continue;
+                    }
                     const float p0 = tc::ex2_approx(x[c] - msub);
                     const float p1 = tc::ex2_approx(x[c + 1] - msub);
                     ps += p0 + p1;
@@ -1619,6 +1677,10 @@ __global__ void __launch_bounds__(kW8Threads, 1) attn_tcw8_kernel(const __grid_c
             // O *= alpha, all 256 columns, by half 0 alone: the P V over the first 64 keys, which writes every
             // column of O, waits only for half 0's P (both halves take the same rescale decision)
             if (h == 0 && j >= 1 && __any_sync(0xFFFFFFFFu, resc)) {
+                if (I4) {  // P V of the previous tile is done with O
+                    if (!__all_sync(0xFFFFFFFFu, tc::mbar_wait(&p_free[pb ^ 1], ((j - 1) >> 1) & 1, abort_flag))) { ok = false; break; }
+                    tc::tc_fence_after();
+                }
 #pragma unroll 1
                 for (int ch = 0; ch < 8; ++ch) {
                     uint32_t o[32];
@@ -1633,10 +1695,10 @@ __global__ void __launch_bounds__(kW8Threads, 1) attn_tcw8_kernel(const __grid_c
             tc::fence_proxy_async_smem();
             tc::tc_fence_before();
             __syncwarp();
-            tc::mbar_arrive_one(&p_full[h]);
-            l = l * alpha + ps;
+            tc::mbar_arrive_one(&p_full[2 * pb + h]);
+            l = l * alpha + (I4 ? ps2.x + ps2.y : ps);
         }
-        if (ok) {  // the row sum of both halves
+        if (ok && !idle) {  // the row sum of both halves
             float lo;
             if (exchange(ntiles, l, lo)) l += lo;
             else ok = false;
@@ -1651,6 +1713,19 @@ __global__ void __launch_bounds__(kW8Threads, 1) attn_tcw8_kernel(const __grid_c
                 tc::tmem_ld32(tmem + lane_base + kColO + ch * 32, o);
                 tc::tmem_wait_ld();
                 if (!row_ok) continue;
+                if (I4) {  // columns 0 4 1 5 2 6 3 7 of every 8 features back in order
+#pragma unroll
+                    for (int x = 0; x < 4; ++x) {
+                        uint32_t y[8];
+#pragma unroll
+                        for (int e = 0; e < 8; ++e) y[e] = o[8 * x + e];
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) {
+                            o[8 * x + e] = y[2 * e];
+                            o[8 * x + 4 + e] = y[2 * e + 1];
+                        }
+                    }
+                }
                 if (p.splits == 1) {
                     uint4* dst = reinterpret_cast<uint4*>(reinterpret_cast<__nv_bfloat16*>(p.o[layer]) +
                                                           ((size_t)(b * T + node) * p.HQ + head) * kTcD + ch * 32);
@@ -1708,19 +1783,20 @@ static EncodeTiledFn encode_fn() {
 // boxes of 128 bytes x 64 rows, 128-byte swizzled too (bank-conflict-free
 // reads for the converter, which re-lays them out as fp16 operand tiles).
 // 4-bit caches: rows of 128 bytes, boxes of 128 bytes x 64 rows.
-// quarters = true (Int8 K for the 128-key kernel): boxes of 64 bytes x 128 rows (one dim quarter of a 128-key
-// tile) with the 64-byte swizzle.
+// quarters = true (K for the 128-key kernels of byte caches): boxes of 64 bytes x 128 rows (one dim quarter of a
+// 128-key tile) with the 64-byte swizzle; 4-bit: 32 bytes, 32-byte swizzle.
 static bool make_kv_map(CUtensorMap* m, const void* base, long long rows, int kv_dtype, bool quarters = false) {
     EncodeTiledFn enc = encode_fn();
     if (!enc) return false;
-    const bool i8 = kv_has_scales(kv_dtype);  // byte elements
-    cuuint64_t dims[2] = {(cuuint64_t)(kv_dtype == TSV_I4_G64 ? kTcD / 2 : kTcD), (cuuint64_t)rows};
+    const bool bytes = kv_has_scales(kv_dtype);  // byte elements
+    const cuuint32_t width = (cuuint32_t)kv_row_bytes(kv_dtype, kTcD) / (bytes ? 1 : 2);
+    cuuint64_t dims[2] = {width, (cuuint64_t)rows};
     cuuint64_t strides[1] = {(cuuint64_t)kv_row_bytes(kv_dtype, kTcD)};
-    cuuint32_t box[2] = {quarters ? 64u : (i8 ? 128u : 64u), quarters ? (cuuint32_t)kWK : (cuuint32_t)kTcBK};
+    cuuint32_t box[2] = {quarters ? width / 4 : (bytes ? 128u : 64u), quarters ? (cuuint32_t)kWK : (cuuint32_t)kTcBK};
     cuuint32_t es[2] = {1, 1};
-    return enc(m, i8 ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : CU_TENSOR_MAP_DATA_TYPE_UINT16, 2, const_cast<void*>(base), dims,
-               strides, box, es, CU_TENSOR_MAP_INTERLEAVE_NONE,
-               quarters ? CU_TENSOR_MAP_SWIZZLE_64B : CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+    const CUtensorMapSwizzle swizzle = !quarters ? CU_TENSOR_MAP_SWIZZLE_128B : width == 256 ? CU_TENSOR_MAP_SWIZZLE_64B : CU_TENSOR_MAP_SWIZZLE_32B;
+    return enc(m, bytes ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : CU_TENSOR_MAP_DATA_TYPE_UINT16, 2, const_cast<void*>(base), dims,
+               strides, box, es, CU_TENSOR_MAP_INTERLEAVE_NONE, swizzle, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
                CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
@@ -1735,8 +1811,10 @@ int tc_mtiles(const tsv_attn_desc* d) { return ((d->HQ / d->HKV) * d->T + kTcRow
 // 16-bit caches when a unit has more than one 128-row tile of query rows (there the halved Q K^T issue cost wins;
 // with a single, mostly empty row tile the deeper 64-key pipeline is faster).  Int8 caches take the 64-key
 // kernel: on the 16- and 64-node workloads the 128-key Int8 kernel measured level with it or up to 2 % slower.
+// 4-bit caches have the 128-key kernel only.
 bool tc_wide(const tsv_attn_desc* d) {
-    if (d->path == TSV_ATTN_TCGEN05_64 || d->kv_dtype == TSV_I4_G64) return false;
+    if (d->kv_dtype == TSV_I4_G64) return true;
+    if (d->path == TSV_ATTN_TCGEN05_64) return false;
     if (d->path == TSV_ATTN_TCGEN05_128) return true;
     return d->kv_dtype != TSV_I8_SCALED && tc_mtiles(d) >= 2;
 }
@@ -1744,12 +1822,11 @@ bool tc_wide(const tsv_attn_desc* d) {
 tsv_status launch_tc(const tsv_attn_desc* d, int splits, int chunk, float* ws_o, float* ws_ml, int32_t* status,
                      cudaStream_t stream) {
     static thread_local TcParams prm;
-    const bool i8 = d->kv_dtype == TSV_I8_SCALED;
+    const bool i8 = d->kv_dtype == TSV_I8_SCALED, i4 = d->kv_dtype == TSV_I4_G64, is16 = !i8 && !i4;
     const bool wide = tc_wide(d);
     const long long rows = (long long)d->B * d->HKV * d->s_cap;
     for (int l = 0; l < d->n_layers; ++l) {
-        if (!make_kv_map(&prm.kmap[l], d->k[l], rows, d->kv_dtype, i8 && wide) ||
-            !make_kv_map(&prm.vmap[l], d->v[l], rows, d->kv_dtype))
+        if (!make_kv_map(&prm.kmap[l], d->k[l], rows, d->kv_dtype, !is16 && wide) || !make_kv_map(&prm.vmap[l], d->v[l], rows, d->kv_dtype))
             return fail(TSV_ECUDA, "tree_verify_attention: tensor map encoding failed for layer %d", l);
         prm.q[l] = reinterpret_cast<const uint16_t*>(d->q[l]);
         prm.o[l] = d->o[l];
@@ -1776,21 +1853,21 @@ tsv_status launch_tc(const tsv_attn_desc* d, int splits, int chunk, float* ws_o,
     prm.mma_bf16 = d->kv_dtype == TSV_BF16;
     const long long items = (long long)d->n_layers * d->B * d->HKV * splits * prm.mtiles;
     if (items > 0x7FFFFFFFLL) return fail(TSV_ECAPACITY, "tree_verify_attention: too many work items");
-    if (i8 && wide) {
-        cudaFuncSetAttribute(attn_tcw8_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kW8Smem);
-        launch_pdl(attn_tcw8_kernel, (unsigned)items, kW8Threads, kW8Smem, stream, prm);
-    } else if (d->kv_dtype == TSV_I4_G64) {
-        cudaFuncSetAttribute(attn_tc_kernel<2>, cudaFuncAttributeMaxDynamicSharedMemorySize, kTcSmem);
-        launch_pdl(attn_tc_kernel<2>, (unsigned)items, kTcThreadsI8, kTcSmem, stream, prm);
+    if (i4) {
+        cudaFuncSetAttribute(attn_tcw8_kernel<true>, cudaFuncAttributeMaxDynamicSharedMemorySize, kW4Smem);
+        launch_pdl(attn_tcw8_kernel<true>, (unsigned)items, kW8Threads, kW4Smem, stream, prm);
+    } else if (i8 && wide) {
+        cudaFuncSetAttribute(attn_tcw8_kernel<false>, cudaFuncAttributeMaxDynamicSharedMemorySize, kW8Smem);
+        launch_pdl(attn_tcw8_kernel<false>, (unsigned)items, kW8Threads, kW8Smem, stream, prm);
     } else if (i8) {
-        cudaFuncSetAttribute(attn_tc_kernel<1>, cudaFuncAttributeMaxDynamicSharedMemorySize, kTcSmem);
-        launch_pdl(attn_tc_kernel<1>, (unsigned)items, kTcThreadsI8, kTcSmem, stream, prm);
+        cudaFuncSetAttribute(attn_tc_kernel<true>, cudaFuncAttributeMaxDynamicSharedMemorySize, kTcSmem);
+        launch_pdl(attn_tc_kernel<true>, (unsigned)items, kTcThreadsI8, kTcSmem, stream, prm);
     } else if (wide) {
         cudaFuncSetAttribute(attn_tcw_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kWSmem);
         launch_pdl(attn_tcw_kernel, (unsigned)items, kTcThreads16, kWSmem, stream, prm);
     } else {
-        cudaFuncSetAttribute(attn_tc_kernel<0>, cudaFuncAttributeMaxDynamicSharedMemorySize, kTcSmem);
-        launch_pdl(attn_tc_kernel<0>, (unsigned)items, kTc64Threads16, kTcSmem, stream, prm);
+        cudaFuncSetAttribute(attn_tc_kernel<false>, cudaFuncAttributeMaxDynamicSharedMemorySize, kTcSmem);
+        launch_pdl(attn_tc_kernel<false>, (unsigned)items, kTc64Threads16, kTcSmem, stream, prm);
     }
     return check_launch("tree_verify_attention(tcgen05)");
 }

@@ -13,6 +13,9 @@
 //                       their product with K onto the decayed state, which stays in TMEM in fp32.
 // The system is solved right-looking: U_b is applied to every block after b at once, so that the products of different
 // blocks are independent.
+// 16391 tokens, 48 heads of 128 x 128: 1.24 to 1.34 ms, about 4.9 us a chunk, where reading and writing everything once would
+// take 81 us: bound by the two groups' chains of steps (state: split 1.0 us, product 0.6, solve 1.5, o and the new state
+// 1.2; preparation: staging 1.4, product 0.6, matrices 2), which are of equal length.  24 prompts of 5 to 4001 tokens 0.44 ms.
 // What reaches the state is kept to 2^-22 (fp16 pairs; K's values are exact), what reaches o alone to 2^-12.
 #include <math.h>
 
@@ -23,7 +26,9 @@ namespace tsv {
 constexpr int kScanPrep = 8;  // preparing warps
 constexpr int kScanT = 64;    // tokens per chunk
 constexpr int kScanNB = 4;
-constexpr int kScanSort = 256;  // batches up to this size are started longest sequence first
+// Batches up to this size are started longest sequence first (a rank by counting, in every CTA: quadratic).  24 prompts of 5
+// to 4001 tokens: 0.44 ms; in the order given 0.48.
+constexpr int kScanSort = 256;
 
 template <int DK, int DV>
 struct ScanSmem {
@@ -384,7 +389,7 @@ __global__ void __launch_bounds__((kScanPrep + DV / 16) * 32, 1)
                     mx[x & 1] = fmaxf(mx[x & 1], fmaxf(fabsf(bf16_lo(vf[bb][x])), fabsf(bf16_hi(vf[bb][x]))));
             }
             const float e_n = dj[64];
-            // The decay over the chunk.  Unless it is next to nothing the state is decayed (and scaled) in TMEM at once:
+            // The decay over the chunk.  Unless it is next to nothing (its inverse then still is far inside fp32) the state is decayed (and scaled) in TMEM at once:
             // should the chunk have to be done again in fp32, the state can be had back.
             const bool early = e_n >= 0x1p-60f;
             tc::tc_fence_after();
@@ -596,7 +601,7 @@ static void launch_scan_dims(const tsv_gdn_desc& d, const int32_t* cu_len, int m
 
 void launch_gdn_scan(const tsv_gdn_desc& d, const int32_t* cu_len, int max_len, int32_t* status, cudaStream_t stream) {
     // Half heads while both halves of every head find an SM: the preparation is done twice, but a half's warps have more
-    // of their SM to themselves.
+    // of their SM to themselves.  16391 tokens, 48 heads: 1.24 ms alone, whole heads 1.40.
     const bool half = d.DV == 64 || 2LL * d.n_layers * d.B * d.HV <= sm_count();
     if (d.DK == 64) half ? launch_scan_dims<64, 64>(d, cu_len, max_len, status, stream) : launch_scan_dims<64, 128>(d, cu_len, max_len, status, stream);
     else half ? launch_scan_dims<128, 64>(d, cu_len, max_len, status, stream) : launch_scan_dims<128, 128>(d, cu_len, max_len, status, stream);
