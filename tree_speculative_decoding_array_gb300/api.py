@@ -23,8 +23,11 @@ def _p(t):
 
 
 def _stream(stream):
-    s = stream if stream is not None else torch.cuda.current_stream()
-    return C.c_void_p(s.cuda_stream)
+    """The stream's handle; None: the current stream's, without building a Stream object around it (2 of a small call's
+    9 us on the host)."""
+    if stream is None:
+        return C.c_void_p(torch._C._cuda_getCurrentRawStream(torch.cuda.current_device()))
+    return C.c_void_p(stream.cuda_stream)
 
 
 def _cuda(t, name, dtype=None, shape=None):
@@ -331,9 +334,9 @@ def gdn_desc(q, k, v, g, beta, state, *, o=None, state_out=None, norm_eps=1e-6, 
 def _gdn_rows(desc, packed, name):
     if desc.packed != packed:
         raise ValueError(f"{name} takes " + ("packed rows [T, H, D]" if packed else "a tree block [B, T, H, D]"))
-    if desc.device.index != torch.cuda.current_device():
-        raise ValueError(f"{name}: the tensors are on {desc.device}, the current device is "
-                         f"cuda:{torch.cuda.current_device()}")
+    device = torch.cuda.current_device()
+    if desc.device.index != device:
+        raise ValueError(f"{name}: the tensors are on {desc.device}, the current device is cuda:{device}")
 
 
 def gdn_tree_verify(desc: GdnDesc, anc, dev_status=None, stream=None):
