@@ -421,6 +421,41 @@ def test_rows_that_are_not_finite_stay_with_the_nodes_that_see_them(gpu_lib):
         assert torch.equal(out[0][0, clear], out[1][0, clear])
 
 
+@pytest.mark.parametrize("D", [64, 128, 256])
+def test_append_of_rows_that_are_not_finite(gpu_lib, D):
+    """The stored form of NaN, infinities and values beyond fp16, as the oracle's (V rows are not rotated)."""
+    tsv, rows = gpu_lib, []
+    for what in range(7):
+        x = torch.randn(D, generator=torch.Generator().manual_seed(what))
+        if what == 0:
+            x[:] = float("nan")
+        elif what == 1:
+            x[::3] = float("nan")
+        elif what == 2:
+            x[5], x[6] = float("inf"), -float("inf")
+        elif what == 3:
+            x[:] = float("inf")
+        elif what == 4:
+            x[:] = 1e30
+            x[::2] = -3e4
+        elif what == 5:
+            x[:64] = -float("inf")
+        rows.append(x)
+    T = len(rows)
+    vn = torch.stack(rows)[None, :, None].bfloat16().to(DEV)
+    kc, vc = ([torch.zeros(1, 1, T, D // 2, dtype=torch.uint8, device=DEV), torch.zeros(1, 1, T, D // 64, 2, dtype=torch.float16, device=DEV)]
+              for _ in "kv")
+    q = torch.zeros(1, T, 1, D, dtype=torch.bfloat16, device=DEV)
+    d = tsv.append_desc([q], [torch.empty_like(q)], [torch.zeros_like(vn)], [vn], [kc[0]], [vc[0]], torch.zeros(1, T, dtype=torch.int32, device=DEV),
+                        T=T, HQ=1, HKV=1, D=D, kv_dtype=tsv.I4_G64, rot_dim=32, rope_base=1e4, k_scale=[kc[1]], v_scale=[vc[1]])
+    tsv.tree_append(d, torch.zeros(1, dtype=torch.int32, device=DEV))
+    for i in range(T):
+        codes, pair = oap.quantize_token4(vn[0, i, 0].double().cpu().numpy())
+        got = vc[0][0, 0, i].cpu().numpy()
+        assert (np.stack([got & 15, got >> 4], -1).reshape(-1) == codes).all(), i
+        assert (vc[1][0, 0, i].cpu().numpy().view(np.uint16) == pair).all(), i
+
+
 @pytest.mark.parametrize("T", [1, 20])
 def test_offsets_beyond_32_bits(gpu_lib, T):
     """The second sequence of a cache whose buffers pass 2^31 bytes and 2^32 codes."""

@@ -46,8 +46,8 @@ void launch_few(const tsv_attn_desc* d, int splits, int chunk, float* ws_o, floa
 constexpr int kPathFew = 100;  // the few-row kernel of 4-bit caches, chosen by AUTO alone
 
 // 4-bit caches take the few-row kernel up to 16 query rows per K/V stream, and wherever the tcgen05 kernel does not apply.
-// 16 layers x 4 heads x 8192 keys, few-row against tcgen05: 12 rows 63 and 100 us, 18 rows 107 and 100; x 131072 keys 6
-// rows 649 and 1236.
+// 16 layers x 4 heads x 8192 keys, few-row against tcgen05: 6 rows 46 and 97 us, 12 rows 66 and 98, 18 rows 107 and 99;
+// x 131072 keys 6 rows 439 and 1123.
 static bool few_applies(const tsv_attn_desc* d) {
     return d->kv_dtype == TSV_I4_G64 && d->path == TSV_ATTN_AUTO && ((d->HQ / d->HKV) * d->T <= 16 || !tc_supported(d));
 }

@@ -12,8 +12,9 @@
 // Q takes the order and the power of two of the masks when it is loaded, the output's when it is written.
 //
 // A warp takes 16 keys at a time through a private ring of cp.async stages, all rows, all features; the four warps of a
-// CTA interleave over one key range and merge their partials through shared memory at its end.  Bound by HBM; what is
-// not its traffic is about 25 instructions per key and warp.
+// CTA interleave over one key range and merge their partials through shared memory at its end.  32 tokens over up to 32768
+// keys, 4 layers x 4 heads of 256: 684 us, 5.2 TB/s; about 25 instructions per key and warp take 60 % of the issue slots,
+// half of them masks on the half-rate integer pipe.
 #include <math.h>
 
 #include "common.cuh"
