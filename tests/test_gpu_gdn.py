@@ -538,6 +538,29 @@ def test_scan_of_more_sequences_than_are_sorted(gpu_lib):
     check_scan(gpu_lib, case(22, 1, 300, (sum(lens),), 1, 1, 128, 128), lens)
 
 
+@pytest.mark.parametrize("lens", [[0] * 299 + [500], [int(x) for x in np.random.default_rng(5).integers(0, 200, 384)],
+                                  [int(x) for x in np.random.default_rng(6).integers(0, 200, 385)],
+                                  [65, 64, 128, 129, 0, 65, 64, 129, 1, 192, 193, 65], [64] * 33 + [65], [300, 0]])
+def test_scan_in_the_order_of_lengths(gpu_lib, lens):
+    """Every sequence is taken by exactly one CTA per head, whatever the order: many equal ones, a long one at the end,
+    as many as there are threads, one more."""
+    B = len(lens)
+    check_scan(gpu_lib, case(25, 1, B, (sum(lens) + 3,), 1, 1, 64, 64), lens, lead=1)
+    c = case(26, 1, B, (sum(lens),), 1, 2, 128, 128)
+    cu = np.cumsum([0] + lens).tolist()
+    bad = int(np.argmax(lens))  # the longest does not fit max_len: reported, the others as they are
+    out, ref = torch.full_like(c["state"], 7.0), torch.full_like(c["state"], 7.0)
+    scan(gpu_lib, c, cu, max(lens), ref)
+    _, st = scan(gpu_lib, c, cu, max(lens) - 1, out)
+    assert st.tolist()[0] == gpu_lib.DEV_BAD_SEQ_LEN
+    for b in range(B):
+        if lens[b] == max(lens):
+            assert (out[:, b] == 7.0).all()
+        else:
+            assert torch.equal(out[:, b], ref[:, b])
+    assert st.tolist()[1] < B and lens[st.tolist()[1]] == lens[bad]
+
+
 def test_scan_beyond_fp16(gpu_lib):
     """Keys far from unit length: the recurrence grows beyond fp16's range, token by token in fp32 then, and stays exact
     where it still is finite."""

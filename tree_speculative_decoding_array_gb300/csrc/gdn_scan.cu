@@ -26,9 +26,7 @@ namespace tsv {
 constexpr int kScanPrep = 8;  // preparing warps
 constexpr int kScanT = 64;    // tokens per chunk
 constexpr int kScanNB = 4;
-// Batches up to this size are started longest sequence first (a rank by counting, in every CTA: quadratic).  24 prompts of 5
-// to 4001 tokens: 0.44 ms; in the order given 0.48.
-constexpr int kScanSort = 256;
+constexpr int kScanSort = 32 * (kScanPrep + 4);  // sequences that can be sorted: a thread each
 
 template <int DK, int DV>
 struct ScanSmem {
@@ -143,7 +141,7 @@ __device__ __noinline__ void chunk_fp32(const tsv_gdn_desc& d, int layer, int h,
 // DV: value features of one CTA, d.DV or half of it.
 template <int DK, int DV>
 __global__ void __launch_bounds__((kScanPrep + DV / 16) * 32, 1)
-    gdn_scan_kernel(const __grid_constant__ tsv_gdn_desc d, const int32_t* __restrict__ cu_len, int max_len, int32_t* status) {
+    gdn_scan_kernel(const __grid_constant__ tsv_gdn_desc d, const int32_t* __restrict__ cu_len, int max_len, int sorted, int32_t* status) {
     griddep_begin();
     using M = ScanSmem<DK, DV>;
     constexpr int SW = DV / 16;  // state warps
@@ -162,29 +160,51 @@ __global__ void __launch_bounds__((kScanPrep + DV / 16) * 32, 1)
     item /= d.HV;
     const int layer = item % d.n_layers;
     int b = item / d.n_layers;
-    if (d.B > 1 && d.B <= kScanSort) {  // CTAs start in the order of their index: the longest sequences first
-        int* lens = reinterpret_cast<int*>(sm + M::diag);
-        int* pick = lens + kScanSort;
-        int mine = 0, rank = 0;
-        if (threadIdx.x < d.B) lens[threadIdx.x] = mine = cu_len[threadIdx.x + 1] - cu_len[threadIdx.x];
-        __syncthreads();
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    int row0, row1;
+    if (sorted) {
+        // CTAs start in the order of their index: this one takes the sequence of b-th most chunks (ties by index), its
+        // number of chunks found bit by bit, a count of the batch each.
+        int* equal = reinterpret_cast<int*>(sm + M::diag);
+        int* pick = equal + 32;
+        int mine = -1;
+        row0 = row1 = 0;
         if (threadIdx.x < d.B) {
-            for (int x = 0; x < d.B; ++x) rank += lens[x] > mine || (lens[x] == mine && x < (int)threadIdx.x);
-            if (rank == b) *pick = threadIdx.x;
+            row0 = cu_len[threadIdx.x];
+            row1 = cu_len[threadIdx.x + 1];
+            const long long len = (long long)row1 - row0;
+            mine = len < 0 ? 0 : (int)((len > max_len ? max_len : len) + kScanT - 1) / kScanT;
+        }
+        int want = 0;
+        for (int bit = 31 - __clz((max_len - 1) / kScanT + 1); bit >= 0; --bit)
+            if (__syncthreads_count(mine >= (want | 1 << bit)) > b) want |= 1 << bit;
+        const int more = __syncthreads_count(mine > want);
+        const uint32_t same = __ballot_sync(0xFFFFFFFFu, mine == want);
+        if (lane == 0) equal[warp] = __popc(same);
+        __syncthreads();
+        int before = more + __popc(same & ((1u << lane) - 1u));
+        for (int w = 0; w < warp; ++w) before += equal[w];
+        if (mine == want && before == b) {
+            pick[0] = threadIdx.x;
+            pick[1] = row0;
+            pick[2] = row1;
         }
         __syncthreads();
-        b = *pick;
+        b = pick[0];
+        row0 = pick[1];
+        row1 = pick[2];
+    } else {
+        row0 = cu_len[b];
+        row1 = cu_len[b + 1];
     }
     const int hk = h / (d.HV / d.HK);
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int g = lane >> 2, t = lane & 3;
 
-    const int row0 = cu_len[b], row1 = cu_len[b + 1];
-    const int n = row1 - row0;
-    if (row0 < 0 || row1 < row0 || row1 > d.T || n > max_len) {
+    if (row0 < 0 || row1 < row0 || row1 > d.T || row1 - row0 > max_len) {
         if (h == 0 && layer == 0 && f0 == 0 && threadIdx.x == 0) dev_fail(status, TSV_DEV_BAD_SEQ_LEN, b, row1);
         return;
     }
+    const int n = row1 - row0;
     const size_t state0 = (((size_t)b * d.HV + h) * d.DV + f0) * DK;
     if (n == 0) {  // the state as it was
         if (d.state_out[layer] != d.state[layer])
@@ -595,13 +615,20 @@ template <int DK, int DV>
 static void launch_scan_dims(const tsv_gdn_desc& d, const int32_t* cu_len, int max_len, int32_t* status, cudaStream_t stream) {
     constexpr int sm = ScanSmem<DK, DV>::total;
     cudaFuncSetAttribute(gdn_scan_kernel<DK, DV>, cudaFuncAttributeMaxDynamicSharedMemorySize, sm);
+    // The longest sequences first, where one of the longest, started last, would add more than a sixteenth to the whole
+    // (max_len rows of one head against every SM's share of all rows).  24 prompts of 5 to 4001 tokens: 0.44 ms, in the
+    // order given 0.48; finding its place costs a CTA up to 0.9 us: 256 prompts of 17 to 400 tokens 1.68 ms, in the order
+    // given 1.61.
+    const int sorted = d.B > 1 && d.B <= kScanSort && max_len > kScanT &&
+                       16LL * max_len * sm_count() > (long long)d.T * d.n_layers * d.HV;
     launch_pdl(gdn_scan_kernel<DK, DV>, (unsigned)((long long)d.n_layers * d.B * d.HV * (d.DV / DV)), (kScanPrep + DV / 16) * 32, sm,
-               stream, d, cu_len, max_len, status);
+               stream, d, cu_len, max_len, sorted, status);
 }
 
 void launch_gdn_scan(const tsv_gdn_desc& d, const int32_t* cu_len, int max_len, int32_t* status, cudaStream_t stream) {
     // Half heads while both halves of every head find an SM: the preparation is done twice, but a half's warps have more
-    // of their SM to themselves.  16391 tokens, 48 heads: 1.24 ms alone, whole heads 1.40.
+    // of their SM to themselves.  48 heads, 16391 tokens alone: 1.24 ms, whole heads 1.40; two prompts of 4096: 0.62 ms, whole
+    // heads 0.36.
     const bool half = d.DV == 64 || 2LL * d.n_layers * d.B * d.HV <= sm_count();
     if (d.DK == 64) half ? launch_scan_dims<64, 64>(d, cu_len, max_len, status, stream) : launch_scan_dims<64, 128>(d, cu_len, max_len, status, stream);
     else half ? launch_scan_dims<128, 64>(d, cu_len, max_len, status, stream) : launch_scan_dims<128, 128>(d, cu_len, max_len, status, stream);

@@ -244,9 +244,10 @@ __global__ void __launch_bounds__(2 * DV, 2) gdn_tree_kernel(const __grid_consta
             rows[k].g_lo[lane + 32 * x] = G[x].lo;
         }
     }
-    // The next head's state is fetched ahead: to registers where they are free (one block), else to L2, 128 bytes per
-    // prefetch.
-    constexpr bool kAhead = NB == 1;
+    // The next head's state is fetched ahead: to registers where they are free, else (four blocks) to L2, 128 bytes per
+    // prefetch.  48 layers, registers against L2: 3 nodes 38 and 42 us, 16 nodes 39 and 44, 4 trees of 20 nodes 163 and 174,
+    // of 40 nodes 211 and 214; 8 trees of 64 nodes 508 and 500.
+    constexpr bool kAhead = NB < 4;
     auto ahead_s = [&](int k) {
         const char* p = reinterpret_cast<const char*>(d.state[layer] + ((size_t)b * d.HV + h0 + k) * DV * DK);
 #pragma unroll
