@@ -538,6 +538,12 @@ def test_scan_of_more_sequences_than_are_sorted(gpu_lib):
     check_scan(gpu_lib, case(22, 1, 300, (sum(lens),), 1, 1, 128, 128), lens)
 
 
+def test_scan_token_by_token_of_many_heads(gpu_lib):
+    """Up to 17 tokens a call go token by token when there are this many heads."""
+    lens = [17] * 20 + [12, 1, 0, 16, 9, 17]
+    check_scan(gpu_lib, case(27, 1, len(lens), (sum(lens),), 16, 48, 64, 64), lens)
+
+
 @pytest.mark.parametrize("lens", [[0] * 299 + [500], [int(x) for x in np.random.default_rng(5).integers(0, 200, 384)],
                                   [int(x) for x in np.random.default_rng(6).integers(0, 200, 385)],
                                   [65, 64, 128, 129, 0, 65, 64, 129, 1, 192, 193, 65], [64] * 33 + [65], [300, 0]])

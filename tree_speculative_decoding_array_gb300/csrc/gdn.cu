@@ -207,10 +207,14 @@ __global__ void __launch_bounds__(kGdnThreads, 5) gdn_recur_kernel(const __grid_
 void launch_gdn_tree(const tsv_gdn_desc& d, const uint64_t* anc, int32_t* status, cudaStream_t stream);
 void launch_gdn_scan(const tsv_gdn_desc& d, const int32_t* cu_len, int max_len, int32_t* status, cudaStream_t stream);
 
-// Sequences of up to this many tokens are advanced token by token, longer ones in chunks of 64.  48 heads, token by token
-// against in chunks: 64 sequences of 14 tokens 190 and 266 us, 16 tokens 215 and 266; 8 sequences of 14 tokens 31 and 38;
-// one sequence of 14 tokens 12.7 and 11.7.  (The time in chunks hardly depends on the length up to 64.)
-constexpr int kRecurMax = 16;
+// Sequences of up to this many tokens are advanced token by token, longer ones in chunks of 64 (whose time hardly depends on
+// the length up to 64; the more heads there are, the better the recurrence hides its latency).  48 heads, token by token
+// against in chunks: 1 sequence of 8 tokens 11.7 and 13.3 us, of 12 15.2 and 13.4; 8 sequences of 12 tokens 33.9 and 38.6, of
+// 16 42.2 and 38.4; 64 sequences of 16 tokens 223 and 253, of 18 255 and 253.
+static int recur_max(const tsv_gdn_desc* d) {
+    const long long units = (long long)d->n_layers * d->B * d->HV;
+    return units < 2LL * sm_count() ? 10 : units < 8LL * sm_count() ? 14 : 17;
+}
 
 enum GdnCall { kGdnVerify, kGdnCommit, kGdnScan };
 
@@ -291,7 +295,7 @@ extern "C" tsv_status tsv_gdn_scan(const tsv_gdn_desc* d, const int32_t* cu_len,
     if (!cu_len) return fail(TSV_EINVAL, "gdn_scan: cu_len must be non-null");
     if (max_len < 0 || max_len > d->T) return fail(TSV_EINVAL, "gdn_scan: max_len=%d outside [0, T=%d]", max_len, d->T);
     const tsv_gdn_desc x = with_scale(d);
-    if (max_len > kRecurMax) {
+    if (max_len > recur_max(d)) {
         launch_gdn_scan(x, cu_len, max_len, dev_status, stream);
         return check_launch("gdn_scan");
     }
