@@ -9,11 +9,11 @@
 // the value heads follow one another.  Each warp owns 16 value features and takes their rows of S from global memory
 // to fp16 pairs in TMEM, fetches their columns of V and writes their columns of o; the next head's state and V are
 // fetched while this head is computed, and a head's matrices are built while the tensor cores work on its S [K; Q]^T.
-// The warps of a head only meet to hand over S and the matrices.  48 layers x 48 heads of 128 x 128: trees of 3 nodes 36 us,
-// of 16 nodes 38 us (4.6 TB/s of the 4.8 to 6.8 that reading the state alone would reach), 32 trees of 64 nodes 1.93 ms
-// (4.2 TB/s): two CTAs fit an SM, so what bounds it is the chain of a head's steps, and at 64 nodes its 15,000 warp
-// instructions (the counters show 45 % of the issue slots, 37 % of HBM).  K, Q and S are kept with the columns of every 16 in the
-// order 0 1 4 5 8 9 12 13 2 3 6 7 10 11 14 15, in which a thread's four values of a fragment are neighbours in memory.
+// The warps of a head only meet to hand over S and the matrices.  48 layers x 48 heads of 128 x 128: trees of 3 nodes 34 us,
+// of 16 nodes 36 us (4.9 TB/s), 32 trees of 64 nodes 1.93 ms (4.2 TB/s): two CTAs fit an SM, so what bounds it is the chain
+// of a head's steps, and at 64 nodes its 15,000 warp instructions (45 % of the issue slots).
+//
+// K, Q and S are kept with the columns of every 16 in the order 0 1 4 5 8 9 12 13 2 3 6 7 10 11 14 15, in which a thread's four values of a fragment are neighbours in memory.
 #include <math.h>
 
 #include "gdn_tc.cuh"
@@ -122,7 +122,7 @@ __device__ __forceinline__ int row_pos(int r) {
 
 template <int DK, int DV, int NB>
 __global__ void __launch_bounds__(2 * DV, 2) gdn_tree_kernel(const __grid_constant__ tsv_gdn_desc d,
-                                                             const uint64_t* __restrict__ anc, int heads, int32_t* status) {
+                                                             const uint64_t* __restrict__ anc, int heads, int big, int32_t* status) {
     griddep_begin();
     using M = TreeSmem<DK, DV, NB>;
     constexpr int kThreads = 2 * DV, kWarps = DV / 16;
@@ -134,8 +134,14 @@ __global__ void __launch_bounds__(2 * DV, 2) gdn_tree_kernel(const __grid_consta
     const uint32_t s0 = tc::smem_u32(sm);
     const int T = d.T;
     int item = blockIdx.x;
-    const int h0 = item % (d.HV / heads) * heads;
-    item /= d.HV / heads;
+    if (item < big) {  // CTAs of `heads` heads, then of one
+        item *= heads;
+    } else {
+        item = big * heads + (item - big);
+        heads = 1;
+    }
+    const int h0 = item % d.HV;
+    item /= d.HV;
     const int b = item % d.B, layer = item / d.B;
     const int hk = h0 / (d.HV / d.HK);
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -445,8 +451,11 @@ static void launch_tree_nb(const tsv_gdn_desc& d, const uint64_t* anc, int32_t* 
     int heads = 1;
     for (int x = 2; x <= kMaxHeads; ++x)
         if (per % x == 0 && (long long)d.n_layers * d.B * d.HV / x >= 4LL * sm_count()) heads = x;
-    launch_pdl(gdn_tree_kernel<DK, DV, NB>, (unsigned)((long long)d.n_layers * d.B * d.HV / heads), 2 * DV, sm, stream, d, anc,
-               heads, status);
+    // The last heads, four for every three SMs, have a CTA each: the call ends sooner than with large CTAs alone (3 nodes 34.1
+    // against 36.3 us, 16 nodes 36.3 against 38.2; twice as many 34.7 and 36.7, half as many 34.5 and 36.8).
+    const long long all = (long long)d.n_layers * d.B * d.HV;
+    const long long big = heads > 1 ? (all - sm_count() * 4 / 3) / heads : all;
+    launch_pdl(gdn_tree_kernel<DK, DV, NB>, (unsigned)(big + (all - big * heads)), 2 * DV, sm, stream, d, anc, heads, (int)big, status);
 }
 
 template <int DK, int DV>
