@@ -13,7 +13,8 @@
 // of 16 nodes 36 us (4.9 TB/s), 32 trees of 64 nodes 1.93 ms (4.2 TB/s): two CTAs fit an SM, so what bounds it is the chain
 // of a head's steps, and at 64 nodes its 15,000 warp instructions (45 % of the issue slots).
 //
-// K, Q and S are kept with the columns of every 16 in the order 0 1 4 5 8 9 12 13 2 3 6 7 10 11 14 15, in which a thread's four values of a fragment are neighbours in memory.
+// K, Q and S are kept with the columns of every 16 in the order 0 1 4 5 8 9 12 13 2 3 6 7 10 11 14 15, in which a thread's four
+// values of a fragment are neighbours in memory.
 #include <math.h>
 
 #include "gdn_tc.cuh"
