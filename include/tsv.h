@@ -20,7 +20,10 @@
  *   says "host", it is DEVICE memory of the current CUDA device.  The library
  *   keeps no pointer after a call returns and allocates no device memory;
  *   scratch comes from a caller-provided workspace whose size the matching
- *   *_workspace_size() call returns.
+ *   *_workspace_size() call returns.  Workspaces are 16-byte aligned, and each
+ *   belongs to one call until that has run on the device: calls that may overlap
+ *   (on several streams, or in graphs that are replayed at the same time) need
+ *   one each.
  * Streams: every call only enqueues work on `stream` (0 = legacy default
  *   stream) and returns without synchronising.  Results are ready when the
  *   stream reaches them.  Calls are capturable in CUDA graphs.  Every kernel

@@ -99,6 +99,22 @@ def test_four_bit_caches_need_their_scales():
         assert lib.tsv_tree_append(C.byref(ap), vp, None, None) == _abi.EUNSUPPORTED
 
 
+@pytest.mark.parametrize("D, HQ, path", [(256, 4, 0), (256, 64, 0), (256, 64, 2), (128, 4, 1)])
+def test_four_bit_attention_needs_an_aligned_workspace(D, HQ, path):
+    lib = tsv.load()
+    a = _abi.AttnDesc()
+    a.n_layers, a.B, a.T, a.HQ, a.HKV, a.D, a.kv_dtype, a.s_cap, a.max_kv_len = 1, 1, 2, HQ, 2, D, tsv.I4_G64, 4096, 4096
+    a.splits, a.path = 4, path
+    for f in ("q", "k", "v", "o", "k_scale", "v_scale"):
+        getattr(a, f)[0] = PTR
+    a.kv_len = a.anc = PTR
+    need = lib.tsv_attention_workspace_size(C.byref(a))
+    assert need > 0
+    assert lib.tsv_tree_verify_attention(C.byref(a), C.c_void_p(PTR), need - 1, None, None) == _abi.ECAPACITY
+    assert lib.tsv_tree_verify_attention(C.byref(a), C.c_void_p(PTR + 8), need, None, None) == _abi.EINVAL
+    assert b"aligned" in lib.tsv_last_error()
+
+
 def test_the_binding_checks_its_tensors():
     bf = lambda *s: torch.zeros(*s, dtype=torch.bfloat16)  # noqa: E731
     f = lambda *s: torch.zeros(*s)  # noqa: E731

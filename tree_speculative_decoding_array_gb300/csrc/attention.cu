@@ -524,6 +524,8 @@ extern "C" tsv_status tsv_tree_verify_attention(const tsv_attn_desc* d, void* wo
     const size_t need = ws_bytes_for(d, g);
     if (need > 0 && (!workspace || ws_bytes < need))
         return fail(TSV_ECAPACITY, "tree_verify_attention: workspace %zu < %zu bytes", ws_bytes, need);
+    if (need > 0 && d->kv_dtype == TSV_I4_G64 && ((uintptr_t)workspace & 15))
+        return fail(TSV_EINVAL, "tree_verify_attention: workspace not 16-byte aligned");
     float* ws_o = (float*)workspace;
     float* ws_ml = need ? (float*)((char*)workspace + ((((size_t)g.units * g.splits * g.rows_unit) * d->D * 4 + 255) & ~(size_t)255)) : nullptr;
     if (g.path == kPathFew) {
