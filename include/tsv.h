@@ -234,7 +234,7 @@ typedef struct {
  * caches have 128-key tiles only).
  * On the tensor-core path Q is rounded to the cache's 16-bit type for the
  * Q K^T product (exact for bf16; for fp16, Int8 and 4-bit caches, whose products
- * are fp16, |q| must lie in fp16 range)
+ * are fp16, |q| must lie in fp16 range; there a row of q that is NaN or beyond it gives a row of NaN)
  * and the softmax weights P enter P V as 16-bit values. */
 #define TSV_ATTN_AUTO 0
 #define TSV_ATTN_SIMT 1

@@ -519,3 +519,64 @@ def test_small_values_behind_a_key_that_draws_most_of_the_weight(gpu_lib, T, D, 
     # (one of 2^-8 on the tiles of 128 rows): 16000 such keys add up to 2^-9 of the weight.  The bias sum is zero here.
     tol = 2.0 ** -8 * want.abs() + (2.0 ** -10 + 16000 * 2.0 ** -25 * 4) * 15 * 2.0 ** -9 + (2.0 ** -9 * want.abs() if big else 0)
     assert ((o[0].double().cpu() - want).abs() <= tol).all()
+
+
+@pytest.mark.parametrize("splits", [0, 1, 3])
+@pytest.mark.parametrize("T, HQ, HKV, D, path", [(1, 6, 1, 256, 0), (5, 4, 2, 256, 0), (16, 24, 4, 256, 0), (1, 8, 2, 128, 0), (20, 6, 1, 64, 0),
+                                                 (4, 6, 2, 128, 0)])
+def test_a_query_row_that_is_not_finite(gpu_lib, T, HQ, HKV, D, path, splits):
+    """NaN in one row of q (all of it, or one feature), infinities and values beyond fp16: NaN comes out of that row (zeros
+    would hide a broken model), the other rows are bit for bit as without it."""
+    tsv, B, S = gpu_lib, 2, 300
+    gen = torch.Generator().manual_seed(T + D)
+    k, v = ([t.to(DEV) for t in random_cache(gen, B, HKV, S + T, D)] for _ in "kv")
+    anc, _ = masks(tsv, [random_tree(np.random.default_rng(b), T) for b in range(B)])
+    clean = torch.randn(B, T, HQ, D, generator=gen).bfloat16().to(DEV)
+    kv_len = torch.tensor([S + T, S + T - 100], dtype=torch.int32, device=DEV)
+
+    def run(q):
+        o = torch.full((B, T, HQ, D), 7.0, dtype=torch.bfloat16, device=DEV)
+        d = tsv.attn_desc([q], [k[0]], [v[0]], [o], kv_len, anc, T=T, HQ=HQ, HKV=HKV, D=D, kv_dtype=tsv.I4_G64, max_kv_len=S + T,
+                          k_scale=[k[1]], v_scale=[v[1]], splits=splits, path=path)
+        ws = torch.empty(max(tsv.attention_workspace_size(d), 16), dtype=torch.uint8, device=DEV)
+        tsv.tree_verify_attention(d, ws)
+        torch.cuda.synchronize()
+        return o
+
+    want = run(clean)
+    b, i, h = 1, T // 2, HQ - 1
+    for bad in (float("nan"), "one nan", float("inf"), -float("inf"), 1e30):
+        q = clean.clone()
+        if bad == "one nan":
+            q[b, i, h, 5] = float("nan")
+        else:
+            q[b, i, h] = bad
+        o = run(q)
+        assert torch.isnan(o[b, i, h]).all(), bad
+        o[b, i, h] = want[b, i, h]
+        assert torch.equal(o, want), bad
+
+
+@pytest.mark.parametrize("T, HQ", [(7, 1), (7, 6)])
+def test_a_nan_in_a_row_that_is_masked(gpu_lib, T, HQ):
+    """Pairs of rows behind kv_len may be NaN; q rows of another sequence may be; neither reaches a row that does not see
+    them, in the kernels of few and of many query rows."""
+    tsv, HKV, D, S, B = gpu_lib, 1, 256, 90, 2
+    gen = torch.Generator().manual_seed(T)
+    k, v = ([t.to(DEV) for t in random_cache(gen, B, HKV, S + T + 40, D)] for _ in "kv")
+    anc, _ = masks(tsv, [[-1, 0, 0, 1, 2, 4, 3]] * B)
+    q = torch.randn(B, T, HQ, D, generator=gen).bfloat16().to(DEV)
+    outs = []
+    for bad in (False, True):
+        if bad:
+            q[1] = float("nan")
+            for x in (k, v):
+                x[1][:, :, S + T:] = float("nan")
+        o = torch.empty(B, T, HQ, D, dtype=torch.bfloat16, device=DEV)
+        d = tsv.attn_desc([q], [k[0]], [v[0]], [o], torch.full((B,), S + T, dtype=torch.int32, device=DEV), anc, T=T, HQ=HQ, HKV=HKV, D=D,
+                          kv_dtype=tsv.I4_G64, max_kv_len=S + T, k_scale=[k[1]], v_scale=[v[1]])
+        ws = torch.empty(max(tsv.attention_workspace_size(d), 16), dtype=torch.uint8, device=DEV)
+        tsv.tree_verify_attention(d, ws)
+        torch.cuda.synchronize()
+        outs.append(o.clone())
+    assert torch.equal(outs[0][0], outs[1][0]) and torch.isnan(outs[1][1]).all()

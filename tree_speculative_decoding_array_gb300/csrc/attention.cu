@@ -413,7 +413,7 @@ __global__ void __launch_bounds__(kCombRows * 32) attn_combine_kernel(const __gr
 #pragma unroll
     for (int o = 16; o >= 1; o >>= 1) L += __shfl_xor_sync(0xFFFFFFFFu, L, o);
     __syncwarp();
-    const float inv = L > 0.f ? 1.f / L : 0.f;
+    const float inv = L == 0.f ? 0.f : 1.f / L;  // a split whose sum is NaN makes the row NaN
     const int i = gr / G, h = kvh * G + gr % G;
     __nv_bfloat16* O = reinterpret_cast<__nv_bfloat16*>(d.o[layer]) + ((size_t)(b * d.T + i) * d.HQ + h) * D;
     for (int c = lane * 4; c < D; c += 128) {

@@ -311,8 +311,9 @@ __global__ void __launch_bounds__(kFewWarps * 32, NT == 1 ? 3 : 2)
         for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
             for (int e = 0; e < 4; ++e) {
+                // every key masked so far: nothing; a score that is NaN (q is, or left fp16's range) stays NaN
                 const float mr = m[nt][e & 1];
-                x[nt][e] = mr == -INFINITY ? 0.f : tc::ex2_approx(x[nt][e] - mr);  // every key masked so far: nothing
+                x[nt][e] = tc::ex2_approx(x[nt][e] - (mr == -INFINITY ? 0.f : mr));
             }
         // O^T += V^T P^T
 #pragma unroll
@@ -415,9 +416,10 @@ __global__ void __launch_bounds__(kFewWarps * 32, NT == 1 ? 3 : 2)
 #pragma unroll
         for (int w = 1; w < kFewWarps; ++w) top = fmaxf(top, ml[0][w][r]);
 #pragma unroll
-        for (int w = 0; w < kFewWarps; ++w) sum += ml[0][w][r] == -INFINITY ? 0.f : tc::ex2_approx(ml[0][w][r] - top) * ml[1][w][r];
+        for (int w = 0; w < kFewWarps; ++w)  // no maximum: the sum is 0, or NaN
+            sum += ml[0][w][r] == -INFINITY ? ml[1][w][r] : tc::ex2_approx(ml[0][w][r] - top) * ml[1][w][r];
         if (splits == 1) {
-            const float inv = sum > 0.f ? 1.f / sum : 0.f;
+            const float inv = sum == 0.f ? 0.f : 1.f / sum;
             *reinterpret_cast<uint2*>(reinterpret_cast<uint16_t*>(d.o[layer]) + ((size_t)(b * T + gr / G) * d.HQ + kvh * G + gr % G) * D + c) =
                 make_uint2(bf16x2(y.x * inv, y.y * inv), bf16x2(y.z * inv, y.w * inv));
         } else {
