@@ -633,3 +633,45 @@ def test_two_calls_at_once(gpu_lib, T):
     torch.cuda.synchronize()
     for x in outs[1:]:
         assert all(torch.equal(a, b) for a, b in zip(x, outs[0]))
+
+
+@pytest.mark.parametrize("scale", [1e-9, 2.0 ** -20, 1e-4, 3e4, 1e12])
+@pytest.mark.parametrize("empty", [False, True])
+def test_any_scale(gpu_lib, scale, empty):
+    """o is as exact under a small or large scale as under the usual one, also where it comes from the block's own writes
+    alone (empty states)."""
+    rng = np.random.default_rng(1)
+    for T in (3, 16, 40, 64):
+        c = case(T, 1, 2, (2, T), 2, 4, 128, 128)
+        if empty:
+            c["state"].zero_()
+        check_verify(gpu_lib, c, [tree(rng, T, "random") for _ in range(2)], scale=scale)
+    c = case(5, 1, 2, (150,), 2, 4, 128, 128)
+    if empty:
+        c["state"].zero_()
+    check_scan(gpu_lib, c, [100, 50], scale=scale)
+
+
+@pytest.mark.parametrize("mq, mk", [(2.0 ** -12, 1.0), (2.0 ** -7, 2.0 ** -7), (2.0 ** -10, 2.0 ** -10), (2.0 ** -30, 2.0 ** -4), (1.0, 2.0 ** -12),
+                                    (200.0, 1.0), (2000.0, 1.0)])
+def test_rows_far_from_unit_length(gpu_lib, mq, mk):
+    """norm_eps 0 with short or long rows of q and k over empty states: o is as small as their product, as exact as ever
+    relative to itself."""
+    rng = np.random.default_rng(2)
+    for T in (5, 40, 64):
+        c = case(T, 1, 1, (1, T), 1, 2, 128, 128)
+        c["q"], c["k"] = unit(c["q"], 1e-6).bfloat16() * mq, unit(c["k"], 1e-6).bfloat16() * mk
+        c["state"].zero_()
+        par = tree(rng, T, "random")
+        o = verify(gpu_lib, c, [par], eps=0.0, scale=1.0)
+        want, _, _ = ref_run(c, 0, slice(0, T), par, c["state"][0, 0], 0.0, 1.0)
+        # a bf16 rounding and fp16 operands (2^-12 each, mixing signs), relative to o itself
+        assert (o[0, 0].double() - want).norm() <= (2.0 ** -8 + 2.0 ** -10) * want.norm()
+    c = case(6, 1, 1, (150,), 1, 2, 128, 128)
+    c["q"], c["k"] = unit(c["q"], 1e-6).bfloat16() * mq, unit(c["k"], 1e-6).bfloat16() * mk
+    c["state"].zero_()
+    out = torch.empty_like(c["state"])
+    o, _ = scan(gpu_lib, c, [0, 150], 150, out, eps=0.0, scale=1.0)
+    want, S, _ = ref_run(c, 0, slice(0, 150), list(range(-1, 149)), c["state"][0, 0], 0.0, 1.0)
+    assert (o[0].double() - want).norm() <= (2.0 ** -8 + 2.0 ** -10) * want.norm()
+    assert (out[0, 0].double() - S[-1]).norm() <= 2.0 ** -18 * S[-1].norm()  # as close_state's bound on the norm

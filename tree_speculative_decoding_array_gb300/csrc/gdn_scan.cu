@@ -314,7 +314,7 @@ __global__ void __launch_bounds__((kScanPrep + DV / 16) * 32, 1)
                 for (int x = 0; x < KH; ++x) {
                     const int r = pt / LPR + (x0 + x) * (PT / LPR), i = r & 63;
                     *reinterpret_cast<uint4*>(bs + kq_at<2 * kScanT>(M::kq, (r & 64) + 16 * block_pos<NB>(i >> 4) + (i & 15), chunk)) = w[x];
-                    if (chunk == 0) (r >= kScanT ? ky.fq : ky.fk)[i] = r >= kScanT ? f[x] * d.scale : f[x];
+                    if (chunk == 0) (r >= kScanT ? ky.fq : ky.fk)[i] = r >= kScanT ? f[x] * kOutLift : f[x];
                 }
             }
             if (pw == 1) {
@@ -427,7 +427,7 @@ __global__ void __launch_bounds__((kScanPrep + DV / 16) * 32, 1)
                 float m = fmaxf(8.f * sx[half] * up[half], mx[half]), up_new;
                 m = fmaxf(m, __shfl_xor_sync(0xFFFFFFFFu, m, 1));
                 m = fmaxf(m, __shfl_xor_sync(0xFFFFFFFFu, m, 2));
-                pow2_scale(m, down[half], up_new);
+                pow2_scale(m * (1.f / kLift), down[half], up_new);
                 sc[half] = up[half] * down[half];
                 up[half] = up_new;
             }
@@ -551,6 +551,7 @@ __global__ void __launch_bounds__((kScanPrep + DV / 16) * 32, 1)
             }
             __syncwarp();
             if (!bad) {  // o while the tensor cores work on the state
+                const float oscale = d.scale / kOutLift, uo[2] = {up[0] * oscale, up[1] * oscale};
                 // o over v's place
 #pragma unroll
                 for (int bb = 0; bb < NB; ++bb) {
@@ -567,7 +568,7 @@ __global__ void __launch_bounds__((kScanPrep + DV / 16) * 32, 1)
                     for (int nn = 0; nn < 2; ++nn)
 #pragma unroll
                         for (int half = 0; half < 2; ++half)
-                            w[2 * nn + half] = bf16x2(aq[nn][2 * half] * up[half], aq[nn][2 * half + 1] * up[half]);
+                            w[2 * nn + half] = bf16x2(aq[nn][2 * half] * uo[half], aq[nn][2 * half + 1] * uo[half]);
                     stsm4_t(tile_at<DV * 2>(bs32 + M::v, bb * 16 + vrow, vchunk), w);
                 }
                 group.sync();

@@ -25,6 +25,13 @@ namespace tsv {
 
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kMinLogDecay = -150.f;  // e^-150 is 0 in fp32: a smaller (or infinite) log decay means the same
+// P and e^G S q are computed without q's scale and times this, and o is multiplied with scale / kOutLift in fp32: an fp16
+// P then holds weights down to 2^-33 whatever the scale, and q rows of up to 2^8 times unit length.
+constexpr float kOutLift = 256.f;
+// A feature's S, R and U are scaled until the largest of 8 max |S row| and max |v| is in [2^12, 2^13): fp16 then holds them
+// down to 2^-37 of it.  Room above: with unit keys and 0 <= beta <= 1 a write v adds at most v^2 to |S row|^2, so 64 writes
+// reach 2^16 only where each is orthogonal to those before; what does leave the range is seen (watch()).
+constexpr float kLift = 4096.f;
 
 __device__ __forceinline__ float clamp_decay(float g) { return g < kMinLogDecay ? kMinLogDecay : g; }  // keeps NaN
 
@@ -149,7 +156,7 @@ __device__ __forceinline__ uint32_t tile_at(uint32_t base, int row, int chunk) {
 // Per-row scalars of a block: those of the key head, and those of one value head.
 struct GdnKeys {
     uint64_t before[64];   // rows ahead of i in its system (strict ancestors, or earlier tokens)
-    float fk[64], fq[64];  // what a staged row's products are multiplied with: its scale and norm (and q's scale)
+    float fk[64], fq[64];  // what a staged row's products are multiplied with: its scale and norm (q: and kOutLift)
 };
 struct GdnRows {
     float g_hi[64], g_lo[64];  // G in units of ln 2, as hi + lo (differences of far sums keep fp32 accuracy)
@@ -183,9 +190,9 @@ __device__ __forceinline__ void stage_chunks(uint4 (&w)[N], float (&f)[N], float
         const int es = (int)(__float_as_uint(ss[x]) >> 23);
         const int e = es == 0 || es >= 255 ? 0 : (es - 127) >> 1;
         const float down = __uint_as_float((uint32_t)(127 - e) << 23), up = __uint_as_float((uint32_t)(127 + e) << 23);
-        // squares that underflowed: the fp32 path
-        flag = ss[x] < 1e-30f && ((w[x].x | w[x].y | w[x].z | w[x].w) & 0x7FFF7FFFu) ? 0x7FFF7FFFu : flag;
         f[x] = norm_eps > 0.f ? up * rsqrtf(ss[x] + norm_eps) : up;
+        // squares that underflowed, or a row so short (norm_eps 0, or far above its squares) that P would be: the fp32 path
+        flag = (ss[x] < 1e-30f || f[x] < 0x1p-8f) && ((w[x].x | w[x].y | w[x].z | w[x].w) & 0x7FFF7FFFu) ? 0x7FFF7FFFu : flag;
         const uint32_t y[4] = {w[x].x, w[x].y, w[x].z, w[x].w};
         uint32_t z[4];
 #pragma unroll

@@ -281,7 +281,7 @@ __global__ void __launch_bounds__(2 * DV, 2) gdn_tree_kernel(const __grid_consta
             const int p = row_pos<NB>(r), at = 8 * (chunk & 1);
             *reinterpret_cast<uint2*>(sm + kq_at<2 * T16>(M::kq, p, chunk & ~1) + at) = make_uint2(w[x].x, w[x].z);
             *reinterpret_cast<uint2*>(sm + kq_at<2 * T16>(M::kq, p, chunk | 1) + at) = make_uint2(w[x].y, w[x].w);
-            if (chunk == 0) (r >= T16 ? ky.fq : ky.fk)[r >= T16 ? r - T16 : r] = r >= T16 ? f[x] * d.scale : f[x];
+            if (chunk == 0) (r >= T16 ? ky.fq : ky.fk)[r >= T16 ? r - T16 : r] = r >= T16 ? f[x] * kOutLift : f[x];
         }
     }
     tc::fence_proxy_async_smem();
@@ -322,7 +322,7 @@ __global__ void __launch_bounds__(2 * DV, 2) gdn_tree_kernel(const __grid_consta
         __syncwarp();  // this warp's V is here
         if (k + 1 < heads) fetch_v(k + 1);
         // this warp's features: a power-of-two scale each, from the largest of the state's row and of v
-        float down[2], up[2];
+        float down[2], up[2];  // up: with o's scale
         {
             float mx[2] = {0.f, 0.f};
 #pragma unroll
@@ -343,7 +343,8 @@ __global__ void __launch_bounds__(2 * DV, 2) gdn_tree_kernel(const __grid_consta
                 sx = fmaxf(8.f * sx, mx[half]);
                 sx = fmaxf(sx, __shfl_xor_sync(0xFFFFFFFFu, sx, 1));
                 sx = fmaxf(sx, __shfl_xor_sync(0xFFFFFFFFu, sx, 2));
-                pow2_scale(sx, down[half], up[half]);
+                pow2_scale(sx * (1.f / kLift), down[half], up[half]);
+                up[half] *= d.scale / kOutLift;
                 const float2 d2 = make_float2(down[half], down[half]);
 #pragma unroll
                 for (int j = 0; j < KS; ++j) {
