@@ -675,3 +675,112 @@ def test_rows_far_from_unit_length(gpu_lib, mq, mk):
     want, S, _ = ref_run(c, 0, slice(0, 150), list(range(-1, 149)), c["state"][0, 0], 0.0, 1.0)
     assert (o[0].double() - want).norm() <= (2.0 ** -8 + 2.0 ** -10) * want.norm()
     assert (out[0, 0].double() - S[-1]).norm() <= 2.0 ** -18 * S[-1].norm()  # as close_state's bound on the norm
+
+
+# ----------------------------------------------------------------------------- values of very different size in one block
+def rows_close(got, want, rel=2.0 ** -8 + 2.0 ** -9):
+    """Every row (last axis) relative to its own norm: bf16's rounding is within 2^-8 of each value, so of the norm."""
+    err, size = (got.double() - want).norm(dim=-1), want.norm(dim=-1)
+    assert (err <= rel * size + 1e-37).all(), (err / size.clamp_min(1e-37)).max().item()
+
+
+def within_o(got, want, MW, n, DK, scale):
+    """close_o's bound per element, of the module's derivation, without the one on the norm."""
+    M, W = MW
+    tol = 2.0 ** -8 * want.abs() + scale * (n * (DK / 8 + 8) * 2.0 ** -24 * M + (min(n, 64) + 1) * (2.0 ** -12 * M + 2.0 ** -11 * W))
+    assert ((got.double() - want).abs() <= tol).all()
+
+
+def within_state(got, want, MW, n, DK):
+    """close_state's bound per element."""
+    M, W = MW
+    assert (got.double() - want).abs().max() <= n * ((DK / 8 + 8) * 2.0 ** -24 * M + 2.0 ** -22 * M + 2.0 ** -21 * W)
+
+
+def enlarge(x, power, what):
+    """Rows x [HV, DV] of one node or token: all of it, or one value feature of the last head, 2^power times as large."""
+    if what == "row":
+        x *= 2.0 ** power
+    else:
+        x[-1, 37] = 1.5 * 2.0 ** power
+
+
+@pytest.mark.parametrize("what", ["row", "feature"])
+@pytest.mark.parametrize("power", [10, 16, 19, 22, 24, 26, 28, 31, 60, 100])
+@pytest.mark.parametrize("T, j", [(2, 1), (4, 2), (16, 9), (17, 1), (40, 30), (64, 5), (64, 63)])
+def test_a_large_value_stays_with_its_node_and_descendants(gpu_lib, T, j, power, what):
+    """One node's v 2^power times the others': nodes that do not see it are as exact as without it."""
+    par = tree(np.random.default_rng(T + j), T, "random")
+    below = [i for i in range(T) if j in _path(par, i)]
+    rest = [i for i in range(T) if i not in below]
+    for fresh in (False, True):
+        c = case(T + power, 1, 1, (1, T), 1, 3, 128, 128)
+        if fresh:
+            c["state"].zero_()
+        want, _, MW = ref_run(c, 0, slice(0, T), par, c["state"][0, 0], 1e-6, 128 ** -0.5)
+        enlarge(c["v"][0, 0, j], power, what)
+        o = verify(gpu_lib, c, [par])[0, 0]
+        close_o(o[rest], want[rest], MW, T, 128, 128 ** -0.5)
+        rows_close(o[rest], want[rest])
+        if what == "feature":
+            rows_close(o[rest, -1, 37].unsqueeze(0), want[rest, -1, 37].unsqueeze(0))
+            others = [f for f in range(128) if f != 37]
+            close_o(o[..., others], want[..., others], MW, T, 128, 128 ** -0.5)
+        # what sees it is as exact as the largest values it is summed from
+        want, _, MW = ref_run(c, 0, slice(0, T), par, c["state"][0, 0], 1e-6, 128 ** -0.5)
+        within_o(o[below], want[below], MW, T, 128, 128 ** -0.5)
+
+
+@pytest.mark.parametrize("power", [-10, -20, -24, -26, -30, -40, -90])
+@pytest.mark.parametrize("T", [2, 16, 33, 64])
+def test_a_small_root_before_larger_nodes(gpu_lib, T, power):
+    """The root of an empty state sees itself alone: its o is exact relative to its own size."""
+    par = tree(np.random.default_rng(T), T, "random")
+    c = case(T, 1, 1, (1, T), 1, 2, 128, 128)
+    c["state"].zero_()
+    c["v"][0, 0, 0] *= 2.0 ** power
+    o = verify(gpu_lib, c, [par])[0, 0]
+    want, _, _ = ref_run(c, 0, slice(0, T), par, c["state"][0, 0], 1e-6, 128 ** -0.5)
+    rows_close(o, want)
+
+
+@pytest.mark.parametrize("what", ["row", "feature"])
+@pytest.mark.parametrize("power", [10, 16, 19, 22, 24, 26, 28, 31, 60, 100])
+@pytest.mark.parametrize("n, j", [(24, 20), (64, 63), (150, 40), (150, 64), (150, 149)])
+def test_a_large_value_reaches_later_tokens_only(gpu_lib, n, j, power, what):
+    """One token's v 2^power times the others': earlier tokens are as exact as without it, the state relative to its rows."""
+    for fresh in (False, True):
+        c = case(n + power, 1, 2, (2 * n,), 1, 3, 128, 128)
+        if fresh:
+            c["state"].zero_()
+        want, S, MW = ref_run(c, 0, slice(0, n), list(range(-1, n - 1)), c["state"][0, 0], 1e-6, 128 ** -0.5)
+        enlarge(c["v"][0, j], power, what)
+        out = torch.empty_like(c["state"])
+        o, _ = scan(gpu_lib, c, [0, n, 2 * n], n, out)
+        close_o(o[0, :j], want[:j], MW, n, 128, 128 ** -0.5)
+        rows_close(o[0, :j], want[:j])
+        if what == "feature":
+            rows_close(o[0, :j, -1, 37].unsqueeze(0), want[:j, -1, 37].unsqueeze(0))
+            others = [f for f in range(128) if f != 37]
+            close_o(o[0, :n][..., others], want[..., others], MW, n, 128, 128 ** -0.5)
+            close_state(out[0, 0][:, others], S[-1][:, others], MW, n, 128)
+        # what sees it is as exact as the largest values it is summed from
+        want, S, MW = ref_run(c, 0, slice(0, n), list(range(-1, n - 1)), c["state"][0, 0], 1e-6, 128 ** -0.5)
+        within_o(o[0, j:n], want[j:], MW, n, 128, 128 ** -0.5)
+        within_state(out[0, 0], S[-1], MW, n, 128)
+        want, S, MW = ref_run(c, 0, slice(n, 2 * n), list(range(-1, n - 1)), c["state"][0, 1], 1e-6, 128 ** -0.5)
+        close_o(o[0, n:], want, MW, n, 128, 128 ** -0.5)
+        close_state(out[0, 1], S[-1], MW, n, 128)
+
+
+@pytest.mark.parametrize("power", [-10, -20, -24, -26, -30, -40, -90])
+@pytest.mark.parametrize("n", [30, 64, 130])
+def test_small_first_tokens_before_larger_ones(gpu_lib, n, power):
+    c = case(n, 1, 1, (n,), 1, 2, 128, 128)
+    c["state"].zero_()
+    c["v"][0, :3] *= 2.0 ** power
+    out = torch.empty_like(c["state"])
+    o, _ = scan(gpu_lib, c, [0, n], n, out)
+    want, S, _ = ref_run(c, 0, slice(0, n), list(range(-1, n - 1)), c["state"][0, 0], 1e-6, 128 ** -0.5)
+    rows_close(o[0], want)
+    rows_close(out[0, 0], S[-1], 2.0 ** -18)

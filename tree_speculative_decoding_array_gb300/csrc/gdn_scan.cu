@@ -347,6 +347,9 @@ __global__ void __launch_bounds__((kScanPrep + DV / 16) * 32, 1)
                 (q ? rw.cq : rw.ck)[i] = tc::ex2_approx(gh + gl) * x;
                 if (!q) dj[i] = tc::ex2_approx((rw.g_hi[63] - gh) + (rw.g_lo[63] - gl)) * x;
                 else if (i == 63) dj[64] = tc::ex2_approx(gh + gl);
+            } else if (pw == 2) {
+                const float write = least_write(rw, min(kScanT, n - c * kScanT), lane);
+                if (lane == 0) rw.write = write;
             }
             __syncwarp();
             if (!(ok = group.wait(&br.gram, c & 1))) break;
@@ -393,25 +396,25 @@ __global__ void __launch_bounds__((kScanPrep + DV / 16) * 32, 1)
             const int buf = c & 1;
             char* bs = sm + buf * M::buffer;
             const uint32_t bs32 = s0 + buf * M::buffer;
+            const GdnKeys& ky = *reinterpret_cast<const GdnKeys*>(bs + M::keys);
             const GdnRows& rw = *reinterpret_cast<const GdnRows*>(bs + M::rows);
             const float* dj = reinterpret_cast<const float*>(bs + M::dj);
             const int nt = min(kScanT, n - c * kScanT);
             uint32_t flag = 0;
             if (!(ok = group.wait(&br.full[buf], (c >> 1) & 1))) break;
             // each feature's power-of-two scale from the largest of its state row and v
-            float mx[2] = {0.f, 0.f}, sx[2] = {0.f, 0.f}, down[2], sc[2];
-            uint32_t vf[NB][4];
+            float sx[2] = {0.f, 0.f}, down[2], sc[2];
+            uint32_t vf[NB][4], top[2] = {0, 0}, low[2] = {kInf2, kInf2};
 #pragma unroll
             for (int bb = 0; bb < NB; ++bb) {
                 ldsm4_t(vf[bb], tile_at<DV * 2>(bs32 + M::v, bb * 16 + vrow, vchunk));
 #pragma unroll
-                for (int x = 0; x < 4; ++x)
-                    mx[x & 1] = fmaxf(mx[x & 1], fmaxf(fabsf(bf16_lo(vf[bb][x])), fabsf(bf16_hi(vf[bb][x]))));
+                for (int x = 0; x < 4; ++x) {
+                    top[x & 1] = abs_max2(top[x & 1], vf[bb][x]);
+                    low[x & 1] = abs_min2(low[x & 1], vf[bb][x]);
+                }
             }
             const float e_n = dj[64];
-            // The decay over the chunk.  Unless it is next to nothing (its inverse then still is far inside fp32) the state is decayed (and scaled) in TMEM at once:
-            // should the chunk have to be done again in fp32, the state can be had back.
-            const bool early = e_n >= 0x1p-60f;
             tc::tc_fence_after();
             float S2[DK / 2];  // this thread's part of the state
 #pragma unroll
@@ -422,15 +425,48 @@ __global__ void __launch_bounds__((kScanPrep + DV / 16) * 32, 1)
 #pragma unroll
                 for (int half = 0; half < 2; ++half)
                     sx[half] = fmaxf(sx[half], fmaxf(fabsf(S2[x + 2 * half]), fabsf(S2[x + 2 * half + 1])));
+            float up_new[2], sd[2], least = INFINITY;  // the feature's largest state, scaled; the smallest v
 #pragma unroll
             for (int half = 0; half < 2; ++half) {
-                float m = fmaxf(8.f * sx[half] * up[half], mx[half]), up_new;
-                m = fmaxf(m, __shfl_xor_sync(0xFFFFFFFFu, m, 1));
-                m = fmaxf(m, __shfl_xor_sync(0xFFFFFFFFu, m, 2));
-                pow2_scale(m * (1.f / kLift), down[half], up_new);
+                float m = fmaxf(bf16_lo(top[half]), bf16_hi(top[half]));
+                sx[half] *= up[half];
+#pragma unroll
+                for (int x = 1; x < 4; x <<= 1) {
+                    sx[half] = fmaxf(sx[half], __shfl_xor_sync(0xFFFFFFFFu, sx[half], x));
+                    m = fmaxf(m, __shfl_xor_sync(0xFFFFFFFFu, m, x));
+                }
+                pow2_scale(fmaxf(8.f * sx[half], m) * (1.f / kLift), down[half], up_new[half]);
+                sd[half] = sx[half] * down[half];
                 sc[half] = up[half] * down[half];
-                up[half] = up_new;
+                least = fminf(least, fminf(bf16_lo(low[half]), bf16_hi(low[half])) * down[half]);
             }
+            // Where the state fades out of sight, and where next to v it cannot be held in fp32 at v's scale.
+            bool redo = false;
+            const float sd_min = fminf(sd[0], sd[1]);
+            if (__any_sync(0xFFFFFFFFu, (sd_min * e_n < kFaint && least * rw.write < kFaint) ||
+                                            !(sd_min >= 0x1p-40f && fminf(sc[0], sc[1]) >= 0x1p-100f && fmaxf(sc[0], sc[1]) <= 0x1p100f))) {
+                redo = faint_rows<DV * 2>(bs + M::v, fb, down[0], down[1], sd[0], sd[1], rw, ky, nt);
+#pragma unroll
+                for (int half = 0; half < 2; ++half) {
+                    if (sx[half] == 0.f) sc[half] = 1.f;
+                    else redo = redo || !(sd[half] >= 0x1p-40f && sc[half] >= 0x1p-100f && sc[half] <= 0x1p100f);
+                }
+                redo = __any_sync(0xFFFFFFFFu, redo);
+                if (redo) {  // this chunk is for the fp32 path: the state stays as it is
+                    flag = 0x7FFF7FFFu;
+#pragma unroll
+                    for (int half = 0; half < 2; ++half) {
+                        up_new[half] = up[half];
+                        down[half] = 1.f / up[half];
+                        sc[half] = 1.f;
+                    }
+                }
+            }
+            up[0] = up_new[0];
+            up[1] = up_new[1];
+            // Unless the decay over the chunk is next to nothing (its inverse then still is far inside fp32) the state is decayed
+            // (and scaled) in TMEM at once: should the chunk have to be done again in fp32, the state can be had back.
+            const bool early = e_n >= 0x1p-60f && !redo;
 #pragma unroll
             for (int x = 0; x < DK / 64; ++x) {
                 uint32_t hi[16], lo[16];

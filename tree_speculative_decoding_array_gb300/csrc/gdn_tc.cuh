@@ -162,6 +162,8 @@ struct GdnRows {
     float g_hi[64], g_lo[64];  // G in units of ln 2, as hi + lo (differences of far sums keep fp32 accuracy)
     float beta[64];
     float ck[64], cq[64];      // 2^G fk, 2^G fq
+    float seen, write;         // smallest 2^G (rounded down) and |beta| of the rows
+    float unused[2];
 };
 
 // N chunks of 8 bf16 values, each of a K or Q row of its own -> fp16 in place, scaled by a power of two that brings the
@@ -202,6 +204,57 @@ __device__ __forceinline__ void stage_chunks(uint4 (&w)[N], float (&f)[N], float
         }
         w[x] = make_uint4(z[0], z[1], z[2], z[3]);
     }
+}
+
+// Largest (smallest) |v| as pairs of bf16, NaN passed over, two values of v at a time.
+constexpr uint32_t kInf2 = 0x7F807F80u;
+__device__ __forceinline__ uint32_t abs_max2(uint32_t top, uint32_t v) {
+    const uint32_t a = v & 0x7FFF7FFFu;
+    const __nv_bfloat162 x = __hmax2(*reinterpret_cast<const __nv_bfloat162*>(&top), *reinterpret_cast<const __nv_bfloat162*>(&a));
+    return *reinterpret_cast<const uint32_t*>(&x);
+}
+__device__ __forceinline__ uint32_t abs_min2(uint32_t low, uint32_t v) {
+    const uint32_t a = v & 0x7FFF7FFFu;
+    const __nv_bfloat162 x = __hmin2(*reinterpret_cast<const __nv_bfloat162*>(&low), *reinterpret_cast<const __nv_bfloat162*>(&a));
+    return *reinterpret_cast<const uint32_t*>(&x);
+}
+
+// Smallest |beta| of a block's first n rows, by one warp.
+__device__ __forceinline__ float least_write(const GdnRows& rw, int n, int lane) {
+    uint32_t x = lane < n ? __float_as_uint(fabsf(rw.beta[lane])) : 0x7F800000u;
+    if (lane + 32 < n) x = min(x, __float_as_uint(fabsf(rw.beta[lane + 32])));
+    return __uint_as_float(__reduce_min_sync(0xFFFFFFFFu, x));
+}
+
+// What fp16 loses at its lower end.  S, R and U of a feature share a scale, so next to a value at the scale's top (2^13) a
+// value below kFaint = 2^-12 is held by its last 13 bits or fewer, and next to a far larger one it is 0.  That only matters
+// where a row sees nothing larger.  True if one of the block's first n rows sees less than kFaint in one of this thread's
+// features f and f + 8, and not nothing: for what it sees this takes its own write, that of the row just before it (its
+// parent) and the state, decayed to it.  The block is then for the fp32 path.
+// Called where the state fades below kFaint (s * rw.seen) and so do the smallest v and beta (low, rw.write): the product of
+// two minima, in a block of ordinary values hardly ever.  v: V tile, rows of BYTES bytes; d: what v is scaled with; s: the
+// largest of the state's row, scaled.  Rows 8 m + 2 t, + 1 are this thread's.
+constexpr float kFaint = 0x1p-12f;
+template <int BYTES>
+__device__ __noinline__ bool faint_rows(const char* v, int fb, float d0, float d1, float s0, float s1, const GdnRows& rw, const GdnKeys& ky,
+                                        int n) {
+    const int lane = threadIdx.x & 31;
+    const int f = fb + (lane >> 2);
+    bool faint = false;
+    for (int j = 2 * (lane & 3); j < n; j += (j & 1) ? 7 : 1) {
+        const float G = rw.g_hi[j], W = tc::ex2_approx(G);
+        const int p = ky.before[j] ? 63 - __clzll((long long)ky.before[j]) : -1;
+        const float be = fabsf(rw.beta[j]), bp = p < 0 ? 0.f : fabsf(rw.beta[p]) * tc::ex2_approx(G - rw.g_hi[p]);
+#pragma unroll
+        for (int half = 0; half < 2; ++half) {
+            const int at = (f >> 3) + half;
+            const float x = bf16_bits_to_f32(*reinterpret_cast<const uint16_t*>(v + tile_at<BYTES>(0, j, at) + 2 * (f & 7)));
+            const float y = bf16_bits_to_f32(*reinterpret_cast<const uint16_t*>(v + tile_at<BYTES>(0, p < 0 ? j : p, at) + 2 * (f & 7)));
+            const float sees = fmaxf(fmaxf(be * fabsf(x), bp * fabsf(y)) * (half ? d1 : d0), (half ? s1 : s0) * W);
+            faint = faint || (sees > 0.f && sees < kFaint);
+        }
+    }
+    return faint;
 }
 
 // K and Q as operand tiles: DK / 64 blocks of [ROWS][128 B], 128-byte swizzled; chunk 0 .. DK / 8 - 1 of a row.

@@ -45,7 +45,7 @@ struct TreeSmem {
 };
 
 // The whole tree of one head in fp32, node by node: taken when an operand left fp16's range (an infinity or a NaN in
-// the inputs, keys that are not of unit length with large writes).  Only a node's ancestors are ever read, so what is
+// the inputs, keys that are not of unit length with large writes, values far above those that another node sees).  Only a node's ancestors are ever read, so what is
 // not finite stays with its node and the node's descendants.  Thread = value feature.
 template <int DK, int DV, int NB>
 __device__ __noinline__ void tree_fp32(const tsv_gdn_desc& d, const uint64_t* anc, int layer, int b, int h, char* sm, const GdnRows& rw) {
@@ -308,6 +308,16 @@ __global__ void __launch_bounds__(2 * DV, 2) gdn_tree_kernel(const __grid_consta
         for (int y = 0; y < heads; ++y)
             (r >= T16 ? rows[y].cq : rows[y].ck)[i] = tc::ex2_approx(rows[y].g_hi[i] + rows[y].g_lo[i]) * x;
     }
+    for (int y = kWarps - 1 - warp; y < heads; y += kWarps) {  // the smallest decay and write, by the warps with less to do
+        float least = lane < T ? rows[y].g_hi[lane] : 0.f;
+        if (lane + 32 < T) least = fminf(least, rows[y].g_hi[lane + 32]);
+        const int floor = __reduce_min_sync(0xFFFFFFFFu, __float2int_rd(least));
+        const float write = least_write(rows[y], T, lane);
+        if (lane == 0) {
+            rows[y].seen = tc::ex2_approx((float)floor);
+            rows[y].write = write;
+        }
+    }
     uint32_t redo = 0;  // heads in which this thread saw an operand that is not finite
     bool ok = true;
     for (int k = 0; k < heads; ++k) {
@@ -322,28 +332,34 @@ __global__ void __launch_bounds__(2 * DV, 2) gdn_tree_kernel(const __grid_consta
         __syncwarp();  // this warp's V is here
         if (k + 1 < heads) fetch_v(k + 1);
         // this warp's features: a power-of-two scale each, from the largest of the state's row and of v
-        float down[2], up[2];  // up: with o's scale
+        float down[2], up[2], sd[2], low[2];  // up: with o's scale; the feature's largest state and smallest v, scaled
         {
-            float mx[2] = {0.f, 0.f};
+            uint32_t top[2] = {0, 0}, low2[2] = {kInf2, kInf2};
 #pragma unroll
             for (int bb = 0; bb < NB; ++bb) {
                 uint32_t w[4];
                 ldsm4_t(w, tile_at<DV * 2>(s0 + vt, bb * 16 + vrow, vchunk));
 #pragma unroll
-                for (int x = 0; x < 4; ++x)
-                    mx[x & 1] = fmaxf(mx[x & 1], fmaxf(fabsf(bf16_lo(w[x])), fabsf(bf16_hi(w[x]))));
+                for (int x = 0; x < 4; ++x) {
+                    top[x & 1] = abs_max2(top[x & 1], w[x]);
+                    low2[x & 1] = abs_min2(low2[x & 1], w[x]);
+                }
             }
             uint32_t Sf[4 * KS];
 #pragma unroll
             for (int half = 0; half < 2; ++half) {
-                float sx = 0.f;
+                float sx = 0.f, mx = fmaxf(bf16_lo(top[half]), bf16_hi(top[half]));
 #pragma unroll
                 for (int j = 0; j < KS; ++j)
                     sx = fmaxf(fmaxf(sx, fmaxf(fabsf(raw[half][j].x), fabsf(raw[half][j].y))), fmaxf(fabsf(raw[half][j].z), fabsf(raw[half][j].w)));
-                sx = fmaxf(8.f * sx, mx[half]);
-                sx = fmaxf(sx, __shfl_xor_sync(0xFFFFFFFFu, sx, 1));
-                sx = fmaxf(sx, __shfl_xor_sync(0xFFFFFFFFu, sx, 2));
-                pow2_scale(sx * (1.f / kLift), down[half], up[half]);
+#pragma unroll
+                for (int x = 1; x < 4; x <<= 1) {
+                    sx = fmaxf(sx, __shfl_xor_sync(0xFFFFFFFFu, sx, x));
+                    mx = fmaxf(mx, __shfl_xor_sync(0xFFFFFFFFu, mx, x));
+                }
+                pow2_scale(fmaxf(8.f * sx, mx) * (1.f / kLift), down[half], up[half]);
+                sd[half] = sx * down[half];
+                low[half] = fminf(bf16_lo(low2[half]), bf16_hi(low2[half])) * down[half];
                 up[half] *= d.scale / kOutLift;
                 const float2 d2 = make_float2(down[half], down[half]);
 #pragma unroll
@@ -370,6 +386,9 @@ __global__ void __launch_bounds__(2 * DV, 2) gdn_tree_kernel(const __grid_consta
                                tc::sdesc_add(kq_desc, (ks >> 2) * 2 * T16 * 128 + (ks & 3) * 32), id, ks > 0);
             tc::mma_commit(&bars[1]);
         }
+        __syncwarp();
+        if (fminf(sd[0], sd[1]) * rw.seen < kFaint && fminf(low[0], low[1]) * rw.write < kFaint)
+            if (faint_rows<DV * 2>(sm + vt, fb, down[0], down[1], sd[0], sd[1], rw, ky, T)) flag = 0x7FFF7FFFu;
         __syncwarp();
         // the system's matrices
         ok = warp_wait(&bars[0], 0, abort_flag);
