@@ -485,10 +485,12 @@ tsv_status tsv_tree_append(const tsv_append_desc* d, int32_t* kv_len, int32_t* d
  *   Value head h reads key head h / (HV / HK).  With norm_eps > 0 every row of q and k is divided by
  *   sqrt(sum x^2 + norm_eps) first.  Sums and the state are fp32.  Products on the tensor cores take their operands as
  *   fp16 with power-of-two scales: an hi + lo pair (within 2^-22 of the value) for what reaches the state, one fp16
- *   (2^-12) for what reaches o alone.  The scales are a value feature's, over a block (a tree, or 64 tokens): v and the
- *   state's row are held down to 2^-37 of the largest of them.  A block is computed in fp32 where its operands leave
- *   fp16's range, and where a node or token sees (in its own v, the one before it and the state, times their beta and
- *   decay) less than 2^-24 of that largest: values that a row does not see do not reach it.  o is rounded to
+ *   (2^-12) for what reaches o alone.  The scales are a value feature's, over a block (a tree, or 64 tokens): v, and the
+ *   state's row as the block's first row leaves it (decayed), are held down to 2^-37 of the largest of them; so is the
+ *   weight of one row's write in a later row (in o: 2^-33).  A block is computed in fp32 where its operands leave fp16's
+ *   range, where a row of q or k is shorter than 2^-8, where a node or token sees (in its own v, the one before it and the
+ *   state, times their beta and decay) less than 2^-24 of that largest, and where the new state is less than 2^-18 of it:
+ *   values that a row does not see, or that were forgotten ahead of it, do not reach it.  o is rounded to
  *   bf16 once.  g may be -infinity (the state is forgotten).
  *
  * tsv_gdn_tree_verify - o of every node of each sequence's tree, node i starting from its parent's state and the

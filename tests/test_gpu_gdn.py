@@ -784,3 +784,83 @@ def test_small_first_tokens_before_larger_ones(gpu_lib, n, power):
     want, S, _ = ref_run(c, 0, slice(0, n), list(range(-1, n - 1)), c["state"][0, 0], 1e-6, 128 ** -0.5)
     rows_close(o[0], want)
     rows_close(out[0, 0], S[-1], 2.0 ** -18)
+
+
+@pytest.mark.parametrize("power", [0, 7, 10, 14, 20, 40, 90])
+@pytest.mark.parametrize("g", [-float("inf"), -45.0, -20.0, -16.0, -11.0])
+@pytest.mark.parametrize("T, j", [(3, 0), (16, 0), (40, 0), (64, 0), (16, 3), (64, 9)])
+def test_a_forgotten_state_leaves_the_tree_exact(gpu_lib, T, j, g, power):
+    """Node j forgets a state 2^power times its usual size: what j and its descendants give is as exact as from the state
+    that is left (e^g of it), however large the forgotten one was."""
+    par = tree(np.random.default_rng(T + j), T, "random")
+    below = [i for i in range(T) if j in _path(par, i)]
+    c = case(T + power, 1, 1, (1, T), 1, 2, 128, 128)
+    c["state"] *= 2.0 ** power
+    c["g"][0, 0, j] = g
+    o = verify(gpu_lib, c, [par])[0, 0]
+    want, states, MW = ref_run(c, 0, slice(0, T), par, c["state"][0, 0], 1e-6, 128 ** -0.5)
+    within_o(o, want, MW, T, 128, 128 ** -0.5)
+    # the same nodes from the state that j leaves behind: their own magnitudes, not those of what was forgotten
+    before = c["state"][0, 0].double() if j == 0 else states[par[j]]
+    part = {x: c[x][:, 0, below] for x in ("q", "k", "v", "g", "beta")}
+    part["g"] = part["g"].clone()
+    part["g"][0, 0] = 0.0
+    sub = [below.index(par[i]) if i != j else -1 for i in below]
+    want2, _, MW = ref_run(part, 0, slice(0, len(below)), sub, torch.exp(torch.tensor(g, dtype=torch.float64, device=DEV)) * before, 1e-6, 128 ** -0.5)
+    assert (want2 - want[below]).norm() <= 1e-9 * want2.norm()
+    close_o(o[below], want[below], MW, T, 128, 128 ** -0.5)
+
+
+@pytest.mark.parametrize("what", ["state", "tokens"])
+@pytest.mark.parametrize("power", [0, 7, 10, 14, 20, 40, 90])
+@pytest.mark.parametrize("g", [-float("inf"), -45.0, -20.0, -16.0, -11.0])
+@pytest.mark.parametrize("n, j", [(24, 0), (24, 11), (64, 63), (150, 0), (150, 64), (150, 100)])
+def test_a_forgotten_state_leaves_the_scan_exact(gpu_lib, n, j, g, power, what):
+    """Token j forgets a state, or the writes of the tokens before it, 2^power times the usual size: o and the state from j on
+    are as exact as from what is left of it."""
+    c = case(n + power, 1, 1, (n,), 1, 2, 128, 128)
+    if what == "state":
+        c["state"] *= 2.0 ** power
+    else:
+        c["v"][0, :j] *= 2.0 ** power
+    c["g"][0, j] = g
+    out = torch.empty_like(c["state"])
+    o, _ = scan(gpu_lib, c, [0, n], n, out)
+    want, states, MW = ref_run(c, 0, slice(0, n), list(range(-1, n - 1)), c["state"][0, 0], 1e-6, 128 ** -0.5)
+    within_o(o[0], want, MW, n, 128, 128 ** -0.5)
+    before = c["state"][0, 0].double() if j == 0 else states[j - 1]
+    part = {x: c[x][:, j:] for x in ("q", "k", "v", "g", "beta")}
+    part["g"] = part["g"].clone()
+    part["g"][0, 0] = 0.0
+    m = n - j
+    want, S, MW = ref_run(part, 0, slice(0, m), list(range(-1, m - 1)), torch.exp(torch.tensor(g, dtype=torch.float64, device=DEV)) * before,
+                          1e-6, 128 ** -0.5)
+    assert (S[-1] - states[-1]).norm() <= 1e-9 * S[-1].norm()
+    # beside the products' errors of close_o and close_state: the weight of an earlier write of the same block is held
+    # down to 2^-37, once in the matrix and once in its inverse (P: 2^-33), so 64 of them leave at most
+    M0, W0 = MW
+    big = 0.0 if g == -float("inf") else 64 * c["v"][0, :j].double().abs().max().item() if j else 0.0
+    close_o(o[0, j:], want, (M0 + 2.0 ** 12 * 2.0 ** -33 * big, W0), n, 128, 128 ** -0.5)
+    err = (out[0, 0].double() - S[-1]).abs().max().item()
+    assert err <= n * ((128 / 8 + 8) * 2.0 ** -24 * M0 + 2.0 ** -22 * M0 + 2.0 ** -21 * W0) + 2.0 ** -36 * big
+    if g == -float("inf") or what == "state":
+        close_state(out[0, 0], S[-1], MW, n, 128)
+
+
+@pytest.mark.parametrize("n", [30, 64, 150])
+def test_a_state_that_only_decays(gpu_lib, n):
+    """Without writes (beta 0, or v and the state's product with k 0) the state is its decayed self, also where the decay of a
+    block passes what fp16 holds; after large writes that are forgotten, small ones are not lost."""
+    c = case(n, 1, 1, (n,), 1, 2, 128, 128)
+    c["beta"].zero_()
+    c["g"][:] = -0.9
+    out = torch.empty_like(c["state"])
+    scan(gpu_lib, c, [0, n], n, out)
+    want = c["state"].double() * torch.exp(c["g"].double().sum(1))[:, None, :, None, None]
+    assert ((out.double() - want).abs() <= n * 2.0 ** -22 * want.abs() + 1e-40).all()  # a rounding and an exp (2 ulp) per token
+    c = case(n, 1, 1, (n,), 1, 2, 128, 128)  # writes, then none while what was written decays by e^-27
+    c["beta"][0, n - 30:] = 0.0
+    c["g"][0, n - 30:] = -0.9
+    scan(gpu_lib, c, [0, n], n, out)
+    _, S, _ = ref_run(c, 0, slice(0, n), list(range(-1, n - 1)), c["state"][0, 0], 1e-6, 1.0)
+    assert (out[0, 0].double() - S[-1]).norm() <= 2.0 ** -18 * S[-1].norm()

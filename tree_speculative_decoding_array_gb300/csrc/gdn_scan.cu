@@ -26,6 +26,7 @@ namespace tsv {
 constexpr int kScanPrep = 8;  // preparing warps
 constexpr int kScanT = 64;    // tokens per chunk
 constexpr int kScanNB = 4;
+constexpr float kFaintState = 0x1p-6f;  // a write's pair holds 2^-25 of the scale, 2^-19 of this
 constexpr int kScanSort = 32 * (kScanPrep + 4);  // sequences that can be sorted: a thread each
 
 template <int DK, int DV>
@@ -136,6 +137,17 @@ __device__ __noinline__ void chunk_fp32(const tsv_gdn_desc& d, int layer, int h,
     }
 #pragma unroll
     for (int x = 0; x < DK / 64; ++x) tc::tmem_st_frag8f(state + 64 * x, S + 32 * x);
+}
+
+// Whether one of this warp's features needs the fp32 path for a chunk: for what faint_rows() says, or because the state (x:
+// the largest of its row) lies outside what fp32 holds at the chunk's scale (d; c: from the scale that it is held at).
+constexpr float kScaleMax = 0x1p100f, kStateMin = 0x1p-40f;
+template <int BYTES, int NB>
+__device__ __noinline__ bool scan_redo(const char* v, int fb, float d0, float d1, float s0, float s1, float x0, float x1, float c0, float c1,
+                                       const GdnRows& rw, const GdnKeys& ky, int n) {
+    bool redo = faint_rows<BYTES, NB>(v, fb, d0, d1, s0, s1, rw, ky, n);
+    redo = redo || (x0 > 0.f && !(x0 * d0 >= kStateMin && c0 <= kScaleMax)) || (x1 > 0.f && !(x1 * d1 >= kStateMin && c1 <= kScaleMax));
+    return __any_sync(0xFFFFFFFFu, redo);
 }
 
 // DV: value features of one CTA, d.DV or half of it.
@@ -344,12 +356,17 @@ __global__ void __launch_bounds__((kScanPrep + DV / 16) * 32, 1)
                 const int i = pt & 63;
                 const bool q = pt >= 3 * kScanT;
                 const float x = (q ? ky.fq : ky.fk)[i], gh = rw.g_hi[i], gl = rw.g_lo[i];
-                (q ? rw.cq : rw.ck)[i] = tc::ex2_approx(gh + gl) * x;
+                (q ? rw.cq : rw.ck)[i] = tc::ex2_approx((gh - floorf(rw.g_hi[0])) + gl) * x;
                 if (!q) dj[i] = tc::ex2_approx((rw.g_hi[63] - gh) + (rw.g_lo[63] - gl)) * x;
                 else if (i == 63) dj[64] = tc::ex2_approx(gh + gl);
             } else if (pw == 2) {
-                const float write = least_write(rw, min(kScanT, n - c * kScanT), lane);
-                if (lane == 0) rw.write = write;
+                const float write = least_write(rw, min(kScanT, n - c * kScanT), lane), e = floorf(rw.g_hi[0]);
+                if (lane == 0) {  // G falls from token to token
+                    rw.e = e;
+                    rw.fade = pow2_floor((int)e);
+                    rw.seen = tc::ex2_approx(rw.g_hi[63] - e);
+                    rw.write = write;
+                }
             }
             __syncwarp();
             if (!(ok = group.wait(&br.gram, c & 1))) break;
@@ -425,7 +442,10 @@ __global__ void __launch_bounds__((kScanPrep + DV / 16) * 32, 1)
 #pragma unroll
                 for (int half = 0; half < 2; ++half)
                     sx[half] = fmaxf(sx[half], fmaxf(fabsf(S2[x + 2 * half]), fabsf(S2[x + 2 * half + 1])));
-            float up_new[2], sd[2], least = INFINITY;  // the feature's largest state, scaled; the smallest v
+            const float fade = rw.fade, seen = rw.seen;
+            // sd: the feature's largest state, faded and scaled; the smaller of both features' (fade_s), of the state as it is
+            // (full_s) and of all v (least), where a feature is not empty
+            float up_new[2], sd[2], fade_s = INFINITY, full_s = INFINITY, least = INFINITY;
 #pragma unroll
             for (int half = 0; half < 2; ++half) {
                 float m = fmaxf(bf16_lo(top[half]), bf16_hi(top[half]));
@@ -435,31 +455,27 @@ __global__ void __launch_bounds__((kScanPrep + DV / 16) * 32, 1)
                     sx[half] = fmaxf(sx[half], __shfl_xor_sync(0xFFFFFFFFu, sx[half], x));
                     m = fmaxf(m, __shfl_xor_sync(0xFFFFFFFFu, m, x));
                 }
-                pow2_scale(fmaxf(8.f * sx[half], m) * (1.f / kLift), down[half], up_new[half]);
-                sd[half] = sx[half] * down[half];
-                sc[half] = up[half] * down[half];
-                least = fminf(least, fminf(bf16_lo(low[half]), bf16_hi(low[half])) * down[half]);
+                m = fmaxf(8.f * (sx[half] * fade), m);
+                pow2_scale(m * (1.f / kLift), down[half], up_new[half]);
+                sd[half] = sx[half] * fade * down[half];
+                sc[half] = fminf(up[half] * down[half], 2.f * kScaleMax);
+                const float empty = m == 0.f ? INFINITY : 0.f;
+                fade_s = fminf(fade_s, sd[half] + empty);
+                full_s = fminf(full_s, sx[half] * down[half] + empty);
+                least = fminf(least, fminf(bf16_lo(low[half]), bf16_hi(low[half])) * down[half] + empty);
             }
-            // Where the state fades out of sight, and where next to v it cannot be held in fp32 at v's scale.
+            // hardly ever: where the state fades out of sight, and where it cannot be held in fp32 at v's scale
+            const bool check = (fade_s * seen < kFaint && (least * rw.write < kFaint || full_s < kStateMin)) || !(fmaxf(sc[0], sc[1]) <= kScaleMax);
             bool redo = false;
-            const float sd_min = fminf(sd[0], sd[1]);
-            if (__any_sync(0xFFFFFFFFu, (sd_min * e_n < kFaint && least * rw.write < kFaint) ||
-                                            !(sd_min >= 0x1p-40f && fminf(sc[0], sc[1]) >= 0x1p-100f && fmaxf(sc[0], sc[1]) <= 0x1p100f))) {
-                redo = faint_rows<DV * 2>(bs + M::v, fb, down[0], down[1], sd[0], sd[1], rw, ky, nt);
+            if (__any_sync(0xFFFFFFFFu, check))
+                redo = scan_redo<DV * 2, NB>(bs + M::v, fb, down[0], down[1], sd[0], sd[1], sx[0], sx[1], sc[0], sc[1], rw, ky, nt);
+            if (redo) {  // this chunk is for the fp32 path: the state stays as it is
+                flag = 0x7FFF7FFFu;
 #pragma unroll
                 for (int half = 0; half < 2; ++half) {
-                    if (sx[half] == 0.f) sc[half] = 1.f;
-                    else redo = redo || !(sd[half] >= 0x1p-40f && sc[half] >= 0x1p-100f && sc[half] <= 0x1p100f);
-                }
-                redo = __any_sync(0xFFFFFFFFu, redo);
-                if (redo) {  // this chunk is for the fp32 path: the state stays as it is
-                    flag = 0x7FFF7FFFu;
-#pragma unroll
-                    for (int half = 0; half < 2; ++half) {
-                        up_new[half] = up[half];
-                        down[half] = 1.f / up[half];
-                        sc[half] = 1.f;
-                    }
+                    up_new[half] = up[half];
+                    down[half] = 1.f / up[half];
+                    sc[half] = 1.f;
                 }
             }
             up[0] = up_new[0];
@@ -467,15 +483,18 @@ __global__ void __launch_bounds__((kScanPrep + DV / 16) * 32, 1)
             // Unless the decay over the chunk is next to nothing (its inverse then still is far inside fp32) the state is decayed
             // (and scaled) in TMEM at once: should the chunk have to be done again in fp32, the state can be had back.
             const bool early = e_n >= 0x1p-60f && !redo;
+            const float se[2] = {sc[0] * e_n, sc[1] * e_n}, sf[2] = {sc[0] * fade, sc[1] * fade};
+            float last[2] = {sd[0] * seen, sd[1] * seen};  // what the feature's new state is made of, its largest
 #pragma unroll
             for (int x = 0; x < DK / 64; ++x) {
                 uint32_t hi[16], lo[16];
 #pragma unroll
                 for (int y = 0; y < 16; ++y) {  // y = 2 n + half
-                    const float2 z = mul2(make_float2(S2[32 * x + 2 * y], S2[32 * x + 2 * y + 1]), make_float2(sc[y & 1], sc[y & 1]));
+                    const float2 s = make_float2(S2[32 * x + 2 * y], S2[32 * x + 2 * y + 1]);
+                    const float2 z = mul2(s, make_float2(sf[y & 1], sf[y & 1]));
                     split2(z.x, z.y, hi[y], lo[y]);
                     if (early) {
-                        const float2 ze = mul2(z, make_float2(e_n, e_n));
+                        const float2 ze = mul2(s, make_float2(se[y & 1], se[y & 1]));
                         S2[32 * x + 2 * y] = ze.x;
                         S2[32 * x + 2 * y + 1] = ze.y;
                     }
@@ -517,7 +536,7 @@ __global__ void __launch_bounds__((kScanPrep + DV / 16) * 32, 1)
 #pragma unroll
             for (int bb = 0; bb < NB; ++bb) {
                 ldsm4_t(vf[bb], tile_at<DV * 2>(bs32 + M::v, bb * 16 + vrow, vchunk));
-                block_rhs(bb, ak[bb], vf[bb], down, rw, t);
+                block_rhs<2>(bb, ak[bb], vf[bb], down, rw, t);
             }
             uint32_t Uh[NB][4];
 #pragma unroll
@@ -536,12 +555,23 @@ __global__ void __launch_bounds__((kScanPrep + DV / 16) * 32, 1)
                     const float2 z = *reinterpret_cast<const float2*>(&dj[bb * 16 + nn * 8 + 2 * t]);
 #pragma unroll
                     for (int half = 0; half < 2; ++half) {
-                        split2(u[nn][2 * half] * z.x, u[nn][2 * half + 1] * z.y, hi[2 * nn + half], lo[2 * nn + half]);
+                        const float2 y = mul2(make_float2(u[nn][2 * half], u[nn][2 * half + 1]), z);
+                        split2(y.x, y.y, hi[2 * nn + half], lo[2 * nn + half]);
+                        last[half] = fmaxf(fmaxf(last[half], fabsf(y.x)), fabsf(y.y));
                         watch(flag, hi[2 * nn + half]);
                     }
                 }
                 tc::tmem_st_frag2(la + M::col_hi + 8 * block_pos<NB>(bb), hi);
                 tc::tmem_st_frag2(la + M::col_lo + 8 * block_pos<NB>(bb), lo);
+            }
+            // a new state whose every part fp16 holds by its last bits only
+            if (__any_sync(0xFFFFFFFFu, fminf(last[0], last[1]) < kFaintState)) {
+#pragma unroll
+                for (int half = 0; half < 2; ++half) {
+#pragma unroll
+                    for (int x = 1; x < 4; x <<= 1) last[half] = fmaxf(last[half], __shfl_xor_sync(0xFFFFFFFFu, last[half], x));
+                    if (last[half] > 0.f && last[half] < kFaintState) flag = 0x7FFF7FFFu;
+                }
             }
             if (watched(flag)) br.bad[buf] = 1;
             tc::tmem_wait_st();

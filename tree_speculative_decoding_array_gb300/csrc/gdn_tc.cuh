@@ -32,6 +32,13 @@ constexpr float kOutLift = 256.f;
 // down to 2^-37 of it.  Room above: with unit keys and 0 <= beta <= 1 a write v adds at most v^2 to |S row|^2, so 64 writes
 // reach 2^16 only where each is orthogonal to those before; what does leave the range is seen (watch()).
 constexpr float kLift = 4096.f;
+// The system's matrix (its blocks ahead of the diagonal and the inverses on it) is held down to 2^-37, so that a large write
+// which decays by much is as exact as what it is added to.  One piece: the matrix is held times kMatLift, with room for keys
+// of up to four times unit length, and R on its way to U as well.  Two pieces: the lo piece is held times kMatLift and meets
+// the operand divided by it.
+constexpr float kMatLift = 4096.f;
+template <int PIECES>
+constexpr float kHiLift = PIECES == 1 ? kMatLift : 1.f;
 
 __device__ __forceinline__ float clamp_decay(float g) { return g < kMinLogDecay ? kMinLogDecay : g; }  // keeps NaN
 
@@ -98,6 +105,17 @@ __device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 d) {
         : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y), "f"(d.x), "f"(d.y));
     return c;
 }
+// hi + lo fp16 pieces of two values, lo times kMatLift.
+__device__ __forceinline__ void split2_lifted(float a, float b, uint32_t& hi, uint32_t& lo) {
+    hi = f16x2(a, b);
+    const float2 y = fma2(f16x2_to_f32x2(hi), make_float2(-kMatLift, -kMatLift), mul2(make_float2(a, b), make_float2(kMatLift, kMatLift)));
+    lo = f16x2(y.x, y.y);
+}
+// An operand for a lifted lo piece.
+__device__ __forceinline__ uint32_t lowered(uint32_t x) {
+    const __half2 y = __hmul2(*reinterpret_cast<const __half2*>(&x), __floats2half2_rn(1.f / kMatLift, 1.f / kMatLift));
+    return *reinterpret_cast<const uint32_t*>(&y);
+}
 // 2^-e and 2^e for m in [2^e, 2^(e+1)); 1 for 0, infinities and NaN.
 __device__ __forceinline__ void pow2_scale(float m, float& down, float& up) {
     uint32_t e = (__float_as_uint(m) >> 23) & 255u;
@@ -161,9 +179,10 @@ struct GdnKeys {
 struct GdnRows {
     float g_hi[64], g_lo[64];  // G in units of ln 2, as hi + lo (differences of far sums keep fp32 accuracy)
     float beta[64];
-    float ck[64], cq[64];      // 2^G fk, 2^G fq
-    float seen, write;         // smallest 2^G (rounded down) and |beta| of the rows
-    float unused[2];
+    float ck[64], cq[64];      // 2^(G - e) fk, 2^(G - e) fq
+    // e: the floor of the largest G.  The state enters as 2^e S (fade = 2^e), so that what no row sees of it - a state that
+    // the block's first row forgets - has no part in the scale.  seen, write: smallest 2^(G - e) (rounded down) and |beta|.
+    float e, fade, seen, write;
 };
 
 // N chunks of 8 bf16 values, each of a K or Q row of its own -> fp16 in place, scaled by a power of two that brings the
@@ -219,6 +238,8 @@ __device__ __forceinline__ uint32_t abs_min2(uint32_t low, uint32_t v) {
     return *reinterpret_cast<const uint32_t*>(&x);
 }
 
+__device__ __forceinline__ float pow2_floor(int e) { return __uint_as_float((uint32_t)(min(max(e, -127), 127) + 127) << 23); }  // 0 below 2^-126
+
 // Smallest |beta| of a block's first n rows, by one warp.
 __device__ __forceinline__ float least_write(const GdnRows& rw, int n, int lane) {
     uint32_t x = lane < n ? __float_as_uint(fabsf(rw.beta[lane])) : 0x7F800000u;
@@ -231,18 +252,27 @@ __device__ __forceinline__ float least_write(const GdnRows& rw, int n, int lane)
 // where a row sees nothing larger.  True if one of the block's first n rows sees less than kFaint in one of this thread's
 // features f and f + 8, and not nothing: for what it sees this takes its own write, that of the row just before it (its
 // parent) and the state, decayed to it.  The block is then for the fp32 path.
-// Called where the state fades below kFaint (s * rw.seen) and so do the smallest v and beta (low, rw.write): the product of
-// two minima, in a block of ordinary values hardly ever.  v: V tile, rows of BYTES bytes; d: what v is scaled with; s: the
-// largest of the state's row, scaled.  Rows 8 m + 2 t, + 1 are this thread's.
+// Called by whole warps, where the state fades below kFaint (s * rw.seen).  Rows 8 m + 2 t, + 1 are this thread's, and the
+// product of their smallest v and the smallest beta is looked at first: in a block of ordinary values it is hardly ever
+// faint.  v: V tile, rows of BYTES bytes; d: what v is scaled with; s: the largest of the state's row, faded and scaled.
 constexpr float kFaint = 0x1p-12f;
-template <int BYTES>
+template <int BYTES, int NB>
 __device__ __noinline__ bool faint_rows(const char* v, int fb, float d0, float d1, float s0, float s1, const GdnRows& rw, const GdnKeys& ky,
                                         int n) {
     const int lane = threadIdx.x & 31;
+    uint32_t low[2] = {kInf2, kInf2};
+#pragma unroll
+    for (int bb = 0; bb < NB; ++bb) {
+        uint32_t w[4];
+        ldsm4_t(w, tile_at<BYTES>(tc::smem_u32(v), bb * 16 + ((lane >> 4) << 3) + (lane & 7), fb / 8 + ((lane >> 3) & 1)));
+#pragma unroll
+        for (int x = 0; x < 4; ++x) low[x & 1] = abs_min2(low[x & 1], w[x]);
+    }
+    if (fminf(fminf(bf16_lo(low[0]), bf16_hi(low[0])) * d0, fminf(bf16_lo(low[1]), bf16_hi(low[1])) * d1) * rw.write >= kFaint) return false;
     const int f = fb + (lane >> 2);
     bool faint = false;
     for (int j = 2 * (lane & 3); j < n; j += (j & 1) ? 7 : 1) {
-        const float G = rw.g_hi[j], W = tc::ex2_approx(G);
+        const float G = rw.g_hi[j], W = tc::ex2_approx(G - rw.e);
         const int p = ky.before[j] ? 63 - __clzll((long long)ky.before[j]) : -1;
         const float be = fabsf(rw.beta[j]), bp = p < 0 ? 0.f : fabsf(rw.beta[p]) * tc::ex2_approx(G - rw.g_hi[p]);
 #pragma unroll
@@ -273,7 +303,7 @@ __host__ __device__ constexpr int block_pos(int b) {
 
 // Products of one 16-row block with the K rows of blocks c0 .. c1 - 1, none of them after its own (TMEM columns
 // 16 block_pos(c) of `taddr`, the block's rows in its lanes), decayed and masked:
-//   q == false: rows K_b; -A (fp16 pieces) for the blocks before, A itself (fp32) for the block's own
+//   q == false: rows K_b; -A kHiLift (fp16 pieces) for the blocks before, A itself (fp32) for the block's own
 //   q == true:  rows Q_b; P (fp16)
 // a16 / p16: [T rows][128 B] tiles; diag: this block's [16][kDiag] fp32.
 constexpr int kDiag = 20;  // fp32 row stride of a diagonal block: 16-byte aligned, rows in different banks
@@ -312,13 +342,14 @@ __device__ __forceinline__ void block_matrices(bool q, int b, int c0, int c1, ui
         float y[2][2][2];
 #pragma unroll
         for (int half = 0; half < 2; ++half) {
+            const float fc = q || c == b ? f[half] : -kHiLift<PIECES> * f[half];
             const uint32_t bits = (uint32_t)(seen[half] >> (c * 16)) >> (2 * t);
 #pragma unroll
             for (int n = 0; n < 2; ++n) {
                 const float w0 = tc::ex2_approx((gh[half] - jh[n].x) + (gl[half] - jl[n].x));
                 const float w1 = tc::ex2_approx((gh[half] - jh[n].y) + (gl[half] - jl[n].y));
-                const float y0 = x[4 * n + 2 * half] * jf[n].x * (f[half] * w0);
-                const float y1 = x[4 * n + 2 * half + 1] * jf[n].y * (f[half] * w1);
+                const float y0 = x[4 * n + 2 * half] * jf[n].x * (fc * w0);
+                const float y1 = x[4 * n + 2 * half + 1] * jf[n].y * (fc * w1);
                 y[half][n][0] = (bits & (1u << (n * 8))) ? y0 : 0.f;
                 y[half][n][1] = (bits & (2u << (n * 8))) ? y1 : 0.f;
             }
@@ -337,7 +368,7 @@ __device__ __forceinline__ void block_matrices(bool q, int b, int c0, int c1, ui
                     *reinterpret_cast<float2*>(diag + il * kDiag + n * 8 + 2 * t) = make_float2(y0, y1);
                 } else {
                     uint32_t hi, lo;
-                    split2(-y0, -y1, hi, lo);
+                    split2_lifted(y0, y1, hi, lo);
                     *reinterpret_cast<uint32_t*>(a16 + tile_at<128>(0, i, 2 * c + n) + 4 * t) = hi;
                     if (PIECES == 2) *reinterpret_cast<uint32_t*>(a16 + T * 128 + tile_at<128>(0, i, 2 * c + n) + 4 * t) = lo;
                 }
@@ -345,7 +376,7 @@ __device__ __forceinline__ void block_matrices(bool q, int b, int c0, int c1, ui
     }
 }
 
-// (I + A_bb)^-1 of one block by forward substitution, a column per lane (both half-warps do the same), stored over
+// kHiLift (I + A_bb)^-1 of one block by forward substitution, a column per lane (both half-warps do the same), stored over
 // block (b, b) of the a16 tile.
 template <int NB, int PIECES>
 __device__ __forceinline__ void block_inverse(int b, char* a16, const float* diag, int lane) {
@@ -354,7 +385,7 @@ __device__ __forceinline__ void block_inverse(int b, char* a16, const float* dia
     float x[16];
 #pragma unroll
     for (int i = 0; i < 16; ++i) {
-        float s0 = i == c ? 1.f : 0.f, s1 = 0.f;
+        float s0 = i == c ? kHiLift<PIECES> : 0.f, s1 = 0.f;
 #pragma unroll
         for (int j = 0; j < i; j += 4) {
             const float4 a = *reinterpret_cast<const float4*>(diag + i * kDiag + j);
@@ -369,7 +400,7 @@ __device__ __forceinline__ void block_inverse(int b, char* a16, const float* dia
 #pragma unroll
         for (int i = 0; i < 16; i += 2) {
             uint32_t hi, lo;
-            split2(x[i], x[i + 1], hi, lo);
+            split2_lifted(x[i], x[i + 1], hi, lo);
 #pragma unroll
             for (int e = 0; e < 2; ++e) {
                 const int row = b * 16 + i + e, col = b * 16 + c;
@@ -411,13 +442,16 @@ __device__ __forceinline__ void warp_matrices(int qt, int m, uint32_t gram, char
     }
 }
 
-// One block and value feature pair in mma fragments (features g, g + 8; rows 8 n + 2 t, + 1): S k_i -> R_b ahead of
-// the blocks before, from v's fragments and the features' scales; and S q_i -> e^{G_i} S q_i.
+// One block and value feature pair in mma fragments (features g, g + 8; rows 8 n + 2 t, + 1): S k_i -> kHiLift R_b ahead
+// of the blocks before, from v's fragments and the features' scales; and S q_i -> e^{G_i} S q_i.
+template <int PIECES>
 __device__ __forceinline__ void block_rhs(int bb, float (&ak)[2][4], const uint32_t (&v)[4], const float (&down)[2], const GdnRows& rw, int t) {
 #pragma unroll
     for (int n = 0; n < 2; ++n) {
         const int i = bb * 16 + n * 8 + 2 * t;
-        const float2 be = *reinterpret_cast<const float2*>(&rw.beta[i]), ck = *reinterpret_cast<const float2*>(&rw.ck[i]);
+        float2 be = *reinterpret_cast<const float2*>(&rw.beta[i]);
+        if constexpr (PIECES == 1) be = mul2(be, make_float2(kMatLift, kMatLift));
+        const float2 ck = *reinterpret_cast<const float2*>(&rw.ck[i]);
 #pragma unroll
         for (int half = 0; half < 2; ++half) {
             const uint32_t v2 = v[2 * n + half];
@@ -438,7 +472,7 @@ __device__ __forceinline__ void block_rhs_q(int bb, float (&aq)[2][4], const Gdn
     }
 }
 
-// R_b -> U_b: pieces in Uf, fp32 in u.  a16: shared address of the tiles.
+// kHiLift R_b -> U_b: pieces in Uf, fp32 in u.  a16: shared address of the tiles.
 template <int NB, int PIECES>
 __device__ __forceinline__ void block_solve(int bb, const float (&ak)[2][4], uint32_t (&Uf)[PIECES][4], float (&u)[2][4], uint32_t a16,
                                             uint32_t& flag, int lane) {
@@ -449,7 +483,7 @@ __device__ __forceinline__ void block_solve(int bb, const float (&ak)[2][4], uin
     for (int x = 0; x < 4; ++x) {
         const float a = ak[x >> 1][2 * (x & 1)], b = ak[x >> 1][2 * (x & 1) + 1];
         if constexpr (PIECES == 2) split2(a, b, r[0][x], r[1][x]);
-        else r[0][x] = f16x2(a, b);
+        else r[0][x] = f16x2(a * (1.f / kMatLift), b * (1.f / kMatLift));
     }
 #pragma unroll
     for (int n = 0; n < 2; ++n)
@@ -464,6 +498,8 @@ __device__ __forceinline__ void block_solve(int bb, const float (&ak)[2][4], uin
         ldsm4(w2, tile_at<128>(a16 + kLo, bb * 16 + brow, 2 * bb + bch));
         mma_16816(v[0], r[1], w[0], w[1]);
         mma_16816(v[1], r[1], w[2], w[3]);
+#pragma unroll
+        for (int x = 0; x < 4; ++x) r[0][x] = lowered(r[0][x]);
         mma_16816(v[0], r[0], w2[0], w2[1]);
         mma_16816(v[1], r[0], w2[2], w2[3]);
 #pragma unroll
@@ -475,11 +511,11 @@ __device__ __forceinline__ void block_solve(int bb, const float (&ak)[2][4], uin
     for (int x = 0; x < 4; ++x) {
         const float a = u[x >> 1][2 * (x & 1)], b = u[x >> 1][2 * (x & 1) + 1];
         if constexpr (PIECES == 2) split2(a, b, Uf[0][x], Uf[1][x]);
-        else Uf[0][x] = f16x2(a, b);
+        else Uf[0][x] = f16x2(a * (1.f / kMatLift), b * (1.f / kMatLift));
         watch(flag, Uf[0][x]);  // an R, A or inverse that is not finite ends here
     }
 }
-// acc -= A_bc U_c for a block b after c (the tile holds -A).
+// acc -= kHiLift A_bc U_c for a block b after c (the tile holds -kHiLift A).
 template <int NB, int PIECES>
 __device__ __forceinline__ void block_update(int b, int c, float (&acc)[2][4], const uint32_t (&Uf)[PIECES][4], uint32_t a16, int lane) {
     const int brow = ((lane >> 4) << 3) + (lane & 7), bch = (lane >> 3) & 1;
@@ -493,8 +529,11 @@ __device__ __forceinline__ void block_update(int b, int c, float (&acc)[2][4], c
         ldsm4(w2, tile_at<128>(a16 + kLo, b * 16 + brow, 2 * c + bch));
         mma_16816(acc[0], Uf[1], w[0], w[1]);
         mma_16816(acc[1], Uf[1], w[2], w[3]);
-        mma_16816(acc[0], Uf[0], w2[0], w2[1]);
-        mma_16816(acc[1], Uf[0], w2[2], w2[3]);
+        uint32_t y[4];
+#pragma unroll
+        for (int x = 0; x < 4; ++x) y[x] = lowered(Uf[0][x]);
+        mma_16816(acc[0], y, w2[0], w2[1]);
+        mma_16816(acc[1], y, w2[2], w2[3]);
     }
 }
 // acc += P_bc U_c.

@@ -203,7 +203,8 @@ __global__ void __launch_bounds__(2 * DV, 2) gdn_tree_kernel(const __grid_consta
                 raw[half][j] = __ldcs(reinterpret_cast<const float4*>(S + (size_t)k * DV * DK + half * 8 * DK + 16 * j));
     };
     // G of every head, a warp each, two nodes per lane: pointer doubling over the parents (the highest strict ancestor)
-    for (int k = warp; k < heads; k += kWarps) {
+    static_assert(kMaxHeads <= kWarps, "a warp per head");
+    if (const int k = warp; k < heads) {
         Pair G[2];
         int p[2];
 #pragma unroll
@@ -250,6 +251,7 @@ __global__ void __launch_bounds__(2 * DV, 2) gdn_tree_kernel(const __grid_consta
             rows[k].g_hi[lane + 32 * x] = G[x].hi;
             rows[k].g_lo[lane + 32 * x] = G[x].lo;
         }
+        __syncwarp();
     }
     // The next head's state is fetched ahead: to registers where they are free, else (four blocks) to L2, 128 bytes per
     // prefetch.  48 layers, registers against L2: 3 nodes 38 and 42 us, 16 nodes 39 and 44, 4 trees of 20 nodes 163 and 174,
@@ -263,6 +265,19 @@ __global__ void __launch_bounds__(2 * DV, 2) gdn_tree_kernel(const __grid_consta
     };
     if (kAhead) fetch_s(0);
     else ahead_s(0);
+    if (warp < heads) {  // the largest and smallest G and the smallest write, while K and Q arrive
+        GdnRows& rw = rows[warp];
+        const float g0 = lane < T ? rw.g_hi[lane] : rw.g_hi[0], g1 = lane + 32 < T ? rw.g_hi[lane + 32] : g0;
+        const int most = __reduce_max_sync(0xFFFFFFFFu, __float2int_rd(fmaxf(g0, g1)));
+        const int least = __reduce_min_sync(0xFFFFFFFFu, __float2int_rd(fminf(g0, g1)));
+        const float write = least_write(rw, T, lane);
+        if (lane == 0) {
+            rw.e = (float)most;
+            rw.fade = pow2_floor(most);
+            rw.seen = tc::ex2_approx((float)(least - most));
+            rw.write = write;
+        }
+    }
     uint32_t flag_kq = 0;
     cp_wait<1>();  // this thread's own chunks of K and Q: converted in place
     constexpr int KH = KQ >= 4 ? KQ / 4 : 1;
@@ -306,17 +321,7 @@ __global__ void __launch_bounds__(2 * DV, 2) gdn_tree_kernel(const __grid_consta
         const int r = threadIdx.x, i = r >= T16 ? r - T16 : r;
         const float x = (r >= T16 ? ky.fq : ky.fk)[i];
         for (int y = 0; y < heads; ++y)
-            (r >= T16 ? rows[y].cq : rows[y].ck)[i] = tc::ex2_approx(rows[y].g_hi[i] + rows[y].g_lo[i]) * x;
-    }
-    for (int y = kWarps - 1 - warp; y < heads; y += kWarps) {  // the smallest decay and write, by the warps with less to do
-        float least = lane < T ? rows[y].g_hi[lane] : 0.f;
-        if (lane + 32 < T) least = fminf(least, rows[y].g_hi[lane + 32]);
-        const int floor = __reduce_min_sync(0xFFFFFFFFu, __float2int_rd(least));
-        const float write = least_write(rows[y], T, lane);
-        if (lane == 0) {
-            rows[y].seen = tc::ex2_approx((float)floor);
-            rows[y].write = write;
-        }
+            (r >= T16 ? rows[y].cq : rows[y].ck)[i] = tc::ex2_approx((rows[y].g_hi[i] - rows[y].e) + rows[y].g_lo[i]) * x;
     }
     uint32_t redo = 0;  // heads in which this thread saw an operand that is not finite
     bool ok = true;
@@ -332,18 +337,15 @@ __global__ void __launch_bounds__(2 * DV, 2) gdn_tree_kernel(const __grid_consta
         __syncwarp();  // this warp's V is here
         if (k + 1 < heads) fetch_v(k + 1);
         // this warp's features: a power-of-two scale each, from the largest of the state's row and of v
-        float down[2], up[2], sd[2], low[2];  // up: with o's scale; the feature's largest state and smallest v, scaled
+        float down[2], up[2], sd = INFINITY;  // up: with o's scale
         {
-            uint32_t top[2] = {0, 0}, low2[2] = {kInf2, kInf2};
+            uint32_t top[2] = {0, 0};
 #pragma unroll
             for (int bb = 0; bb < NB; ++bb) {
                 uint32_t w[4];
                 ldsm4_t(w, tile_at<DV * 2>(s0 + vt, bb * 16 + vrow, vchunk));
 #pragma unroll
-                for (int x = 0; x < 4; ++x) {
-                    top[x & 1] = abs_max2(top[x & 1], w[x]);
-                    low2[x & 1] = abs_min2(low2[x & 1], w[x]);
-                }
+                for (int x = 0; x < 4; ++x) top[x & 1] = abs_max2(top[x & 1], w[x]);
             }
             uint32_t Sf[4 * KS];
 #pragma unroll
@@ -357,11 +359,13 @@ __global__ void __launch_bounds__(2 * DV, 2) gdn_tree_kernel(const __grid_consta
                     sx = fmaxf(sx, __shfl_xor_sync(0xFFFFFFFFu, sx, x));
                     mx = fmaxf(mx, __shfl_xor_sync(0xFFFFFFFFu, mx, x));
                 }
-                pow2_scale(fmaxf(8.f * sx, mx) * (1.f / kLift), down[half], up[half]);
-                sd[half] = sx * down[half];
-                low[half] = fminf(bf16_lo(low2[half]), bf16_hi(low2[half])) * down[half];
+                sx *= rw.fade;
+                mx = fmaxf(8.f * sx, mx);
+                pow2_scale(mx * (1.f / kLift), down[half], up[half]);
+                // the smaller of the two features' largest state, faded and scaled, where a feature is not empty
+                sd = fminf(sd, mx == 0.f ? INFINITY : sx * down[half]);
                 up[half] *= d.scale / kOutLift;
-                const float2 d2 = make_float2(down[half], down[half]);
+                const float2 d2 = make_float2(rw.fade * down[half], rw.fade * down[half]);
 #pragma unroll
                 for (int j = 0; j < KS; ++j) {
                     const float2 x = mul2(make_float2(raw[half][j].x, raw[half][j].y), d2), y = mul2(make_float2(raw[half][j].z, raw[half][j].w), d2);
@@ -387,8 +391,8 @@ __global__ void __launch_bounds__(2 * DV, 2) gdn_tree_kernel(const __grid_consta
             tc::mma_commit(&bars[1]);
         }
         __syncwarp();
-        if (fminf(sd[0], sd[1]) * rw.seen < kFaint && fminf(low[0], low[1]) * rw.write < kFaint)
-            if (faint_rows<DV * 2>(sm + vt, fb, down[0], down[1], sd[0], sd[1], rw, ky, T)) flag = 0x7FFF7FFFu;
+        if (__any_sync(0xFFFFFFFFu, sd * rw.seen < kFaint))
+            if (faint_rows<DV * 2, NB>(sm + vt, fb, down[0], down[1], sd, sd, rw, ky, T)) flag = 0x7FFF7FFFu;
         __syncwarp();
         // the system's matrices
         ok = warp_wait(&bars[0], 0, abort_flag);
@@ -416,7 +420,7 @@ __global__ void __launch_bounds__(2 * DV, 2) gdn_tree_kernel(const __grid_consta
                 ak[x >> 2][x & 3] = dk[x];
                 aq[x >> 2][x & 3] = dq[x];
             }
-            block_rhs(bb, ak, w, down, rw, t);
+            block_rhs<1>(bb, ak, w, down, rw, t);
 #pragma unroll
             for (int c = 0; c < bb; ++c) block_update<NB, 1>(bb, c, ak, Uf[c], s0 + M::a16, lane);
             block_solve<NB, 1>(bb, ak, Uf[bb], u, s0 + M::a16, flag, lane);
