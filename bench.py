@@ -40,20 +40,20 @@ DEFAULT_ROUND = {"chain3_27b_bf16": 2}  # the round that accepts the whole chain
 
 # ncu dram bytes (read + write) per launch of a workload's dominant kernel, with the sources that kernel is built
 # from and their hash when it was measured (a changed source makes the number stale and it is reported as null).
-# The 64-node workload's attention was captured on 1 layer x 4 sequences (1.0867 GB read + 2.978 MB written); a
+# The 64-node workload's attention was captured on 1 layer x 4 sequences (1.0861 GB read + 3.100 MB written); a
 # launch over 16 layers x 32 sequences reads and writes 128 times that (every unit streams its own keys).
 TRAFFIC = {
     # the chain's bf16 LM head (the CUDA-core GEMV), one launch at full size
-    "chain3_27b_bf16": {"kernel": "lm", "src": ("lm_head.cu", "common.cuh"), "hash": "46f6f865d5feba27",
-                        "bytes": 2543127040 + 2785024},
+    "chain3_27b_bf16": {"kernel": "lm", "src": ("lm_head.cu", "common.cuh"), "hash": "dc5931748b5bca73",
+                        "bytes": 2542929920 + 2681344},
     # the 16-node workload's 4-bit LM head (lm_q4s_kernel, 16 rows), one launch at full size
     "specinfer16_27b_i8": {"kernel": "lm", "src": ("lm_head.cu", "lm_head_tc.cu", "common.cuh", "tc.cuh"),
-                           "hash": "07d6b485b4e260fc", "bytes": 715418368 + 3241984},
+                           "hash": "68fc16daddd0db99", "bytes": 715406592 + 3024384},
     # the 32-node workload's attention (attn_tcw_kernel, 16 layers x 8 sequences), one launch at full size
     "eagle32x8_27b_f16": {"kernel": "attn", "src": ("attention.cu", "attention_tc.cu", "common.cuh", "tc.cuh"),
-                          "hash": "af0faa37c76ef2ad", "bytes": 17298162176 + 49117952},
+                          "hash": "deff46faf224d23d", "bytes": 17298016256 + 48260352},
     "eagle64x32_27b_i8": {"kernel": "attn", "src": ("attention.cu", "attention_tc.cu", "common.cuh", "tc.cuh"),
-                          "hash": "af0faa37c76ef2ad", "bytes": (1086705920 + 2978048) * 128},
+                          "hash": "deff46faf224d23d", "bytes": (1086094080 + 3099648) * 128},
 }
 
 
