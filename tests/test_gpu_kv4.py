@@ -580,3 +580,52 @@ def test_a_nan_in_a_row_that_is_masked(gpu_lib, T, HQ):
         torch.cuda.synchronize()
         outs.append(o.clone())
     assert torch.equal(outs[0][0], outs[1][0]) and torch.isnan(outs[1][1]).all()
+
+
+@pytest.mark.parametrize("wide", ["early key", "one group of every key", "one group of every third step", "all groups of every key"])
+@pytest.mark.parametrize("T, D", [(1, 256), (2, 256), (1, 128), (3, 128), (1, 64)])
+def test_small_values_beside_wide_ones(gpu_lib, T, D, wide):
+    """60000 keys of values up to 15 * 2^-9, each e^-12 behind one key whose values are 0, in every group of 64 features that is
+    not wide; `wide` groups or keys have values up to 15 * 100.  A group's small values are as exact as without them."""
+    tsv, HQ, S = gpu_lib, 4, 60000
+    gen = torch.Generator().manual_seed(T)
+    pair = lambda s, b: torch.tensor([s, b]).half()  # noqa: E731
+    k, v = ([torch.zeros(1, S + T, D // 2, dtype=torch.uint8), torch.zeros(1, S + T, D // 64, 2, dtype=torch.float16)] for _ in "kv")
+    k[1][0, 0] = pair(0.0, 12.0 / D ** 0.5)
+    v[0][:] = torch.randint(0, 256, v[0].shape, generator=gen)
+    v[1][:] = pair(2.0 ** -9, 0.0)
+    last = D // 64 - 1
+    if wide == "early key":
+        v[1][0, 20, last] = pair(100.0, -750.0)
+    elif wide == "one group of every key":
+        v[1][0, :, last] = pair(100.0, -750.0)
+    elif wide == "one group of every third step":
+        v[1][0, ::48, last] = pair(100.0, -750.0)
+    else:
+        v[1][:] = pair(100.0, -750.0)
+    v[1][0, 0] = 0.0
+    q = torch.ones(1, T, HQ, D).bfloat16()
+    par = [list(range(-1, T - 1))]
+    anc, _ = masks(tsv, par)
+    o = torch.empty(1, T, HQ, D, dtype=torch.bfloat16, device=DEV)
+    dev, qd = [[x[None].to(DEV) for x in y] for y in (k, v)], q.to(DEV)
+    kv_len = torch.tensor([S + T], dtype=torch.int32, device=DEV)  # (a descriptor holds addresses)
+    d = tsv.attn_desc([qd], [dev[0][0]], [dev[1][0]], [o], kv_len, anc, T=T, HQ=HQ,
+                      HKV=1, D=D, kv_dtype=tsv.I4_G64, max_kv_len=S + T, k_scale=[dev[0][1]], v_scale=[dev[1][1]], splits=2)
+    ws = torch.empty(max(tsv.attention_workspace_size(d), 16), dtype=torch.uint8, device=DEV)
+    tsv.tree_verify_attention(d, ws)
+    want, _ = ref_attention(q[0].double(), values(*k), values(*v), par[0], S)
+    err = (o[0].double().cpu() - want).abs()
+    # scores are exact in fp32; P times a scale is rounded once to fp16, 2^-11 of each term (all of one sign in a narrow group),
+    # exp and the sums add 2^-20 of them; o is rounded to bf16 once.  Terms of a wide group: code * scale and bias apart,
+    # each below 15 * 100 times the weight
+    weight = 60000 * math.exp(-12) / (1 + 60000 * math.exp(-12))
+    tol = (2.0 ** -8 + 2.0 ** -10) * want.abs()
+    if wide in ("one group of every key", "all groups of every key"):
+        g = slice(64 * last, None) if wide.startswith("one") else slice(None)
+        tol[..., g] += 2.0 ** -10 * 2250 * weight
+    elif D == 64 or wide.startswith("one"):
+        tol[..., 64 * last:] += 2.0 ** -10 * 2250 * weight
+    else:
+        tol[..., 64 * last:] += 2.0 ** -10 * 2250 * math.exp(-12)
+    assert (err <= tol).all(), (err / tol).max().item()

@@ -13,7 +13,7 @@
 //
 // A warp takes 16 keys at a time through a private ring of cp.async stages, all rows, all features; the four warps of a
 // CTA interleave over one key range and merge their partials through shared memory at its end.  32 tokens over up to 32768
-// keys, 4 layers x 4 heads of 256: 684 us, 5.2 TB/s; about 25 instructions per key and warp take 60 % of the issue slots,
+// keys, 4 layers x 4 heads of 256: 668 us, 5.4 TB/s (720 us where scales are above 3.9); about 25 instructions per key and warp take 60 % of the issue slots,
 // half of them masks on the half-rate integer pipe.
 #include <math.h>
 
@@ -25,9 +25,20 @@ namespace tsv {
 constexpr int kFewWarps = 4;
 constexpr int kFewKeys = 16;  // keys per warp and step
 // P s_g goes through fp16, whose smallest value is 2^-24: with scales of 2^-7 (values of 0.06) a key 2^17 behind the
-// maximum would be lost, and a long cache holds many such keys behind an early one that draws most of the weight.  So P
-// is lifted by 2^12 until a scale above 3.9 comes by (4 x 2^12 x 3.9 < 65504), which takes the lift off again.
+// maximum would be lost, and a long cache holds many such keys behind an early one that draws most of the weight.  So the
+// P is lifted by 2^12, but for a group in steps where one of its scales is above 3.9 (4 x 2^12 x 3.9 < 65504): its part of O
+// is brought to the other unit where such steps begin and end, and the other groups keep their lift.
 constexpr float kFewLift = 4096.f;
+
+// Lanes whose group (lane % NG) is 0; what takes the lift off group j, given the lanes that saw a large scale of theirs.
+template <int NG>
+constexpr uint32_t few_lanes() {
+    return NG == 4 ? 0x11111111u : NG == 2 ? 0x55555555u : 0xFFFFFFFFu;
+}
+template <int NG>
+__device__ __forceinline__ float few_unit(uint32_t wide, int j) {
+    return wide & (few_lanes<NG>() << j) ? 1.f / kFewLift : 1.f;
+}
 
 template <int D>
 struct FewTile {
@@ -196,7 +207,7 @@ __global__ void __launch_bounds__(kFewWarps * 32, NT == 1 ? 3 : 2)
 #pragma unroll
             for (int nt = 0; nt < NT; ++nt) o[j][i][nt][0] = o[j][i][nt][1] = o[j][i][nt][2] = o[j][i][nt][3] = 0.f;
 
-    float lift = kFewLift;
+    uint32_t wide = 0;  // lanes' groups with a scale above 3.9 in the step before: O of such a group is not lifted
     const int mine = steps > warp ? (steps - warp + kFewWarps - 1) / kFewWarps : 0;
 #pragma unroll
     for (int i = 0; i < ST - 1; ++i) fetch(i, i);
@@ -257,12 +268,11 @@ __global__ void __launch_bounds__(kFewWarps * 32, NT == 1 ? 3 : 2)
         }
         const float up = qscale * 16777216.f;  // 2^24
         const bool plain = kt + kFewKeys <= k_end && kt + kFewKeys <= S && kt >= lo_last;
-        bool grow = false, wide = false;
+        bool grow = false, large = false;  // large: a scale of this lane's group, lane % NG
         const uint32_t* pairs = reinterpret_cast<const uint32_t*>(st + F::vs);
 #pragma unroll
         for (int y = 0; y < (NG > 2 ? NG / 2 : 1); ++y)
-            wide = wide || fabsf(f16x2_to_f32x2(pairs[(lane + 32 * y) & (kFewKeys * NG - 1)]).x) > 3.9f;
-        wide = wide && lift != 1.f;
+            large = large || fabsf(f16x2_to_f32x2(pairs[(lane + 32 * y) & (kFewKeys * NG - 1)]).x) > 3.9f;
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
@@ -279,33 +289,48 @@ __global__ void __launch_bounds__(kFewWarps * 32, NT == 1 ? 3 : 2)
             }
         // The reference follows a row's maximum only when it is exceeded by more than 2 (p <= 4): then the sums and O are
         // brought to the new one.
-        if (__any_sync(0xFFFFFFFFu, grow || wide)) {
-            const float drop = __any_sync(0xFFFFFFFFu, wide) ? 1.f / kFewLift : 1.f;
-            lift *= drop;
+        if (__any_sync(0xFFFFFFFFu, grow || large || wide != 0)) {
+            const uint32_t now = __ballot_sync(0xFFFFFFFFu, large);
 #pragma unroll
-            for (int nt = 0; nt < NT; ++nt)
+            for (int j = 0; j < NG; ++j) {
+                constexpr uint32_t kLanes = few_lanes<NG>();
+                const uint32_t lanes = kLanes << j;
+                if (((now & lanes) != 0) != ((wide & lanes) != 0)) {
+                    const float f = (now & lanes) != 0 ? 1.f / kFewLift : kFewLift;
 #pragma unroll
-                for (int e = 0; e < 2; ++e) {
-                    float y = fmaxf(x[nt][e], x[nt][e + 2]);
+                    for (int z = 0; z < 4; ++z)
 #pragma unroll
-                    for (int z = 4; z < 32; z <<= 1) y = fmaxf(y, __shfl_xor_sync(0xFFFFFFFFu, y, z));
-                    // by the row alone: its result does not depend on its neighbours
-                    const bool rise = y > m[nt][e] + 2.f;
-                    if (rise || drop != 1.f) {
-                        const float a = (rise ? tc::ex2_approx(m[nt][e] - y) : 1.f) * drop;
-                        if (rise) m[nt][e] = y;
-                        l[nt][e] *= a;
+                        for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-                        for (int j = 0; j < NG; ++j) {
-                            ob[j][nt][e] *= a;
+                            for (int e = 0; e < 4; ++e) o[j][z][nt][e] *= f;
+                }
+            }
+            wide = now;
+            if (__any_sync(0xFFFFFFFFu, grow)) {
 #pragma unroll
-                            for (int z = 0; z < 4; ++z) {
-                                o[j][z][nt][e] *= a;
-                                o[j][z][nt][e + 2] *= a;
+                for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                    for (int e = 0; e < 2; ++e) {
+                        float y = fmaxf(x[nt][e], x[nt][e + 2]);
+#pragma unroll
+                        for (int z = 4; z < 32; z <<= 1) y = fmaxf(y, __shfl_xor_sync(0xFFFFFFFFu, y, z));
+                        // by the row alone: its result does not depend on its neighbours
+                        if (y > m[nt][e] + 2.f) {
+                            const float a = tc::ex2_approx(m[nt][e] - y);
+                            m[nt][e] = y;
+                            l[nt][e] *= a;
+#pragma unroll
+                            for (int j = 0; j < NG; ++j) {
+                                ob[j][nt][e] *= a;
+#pragma unroll
+                                for (int z = 0; z < 4; ++z) {
+                                    o[j][z][nt][e] *= a;
+                                    o[j][z][nt][e + 2] *= a;
+                                }
                             }
                         }
                     }
-                }
+            }
         }
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt)
@@ -320,40 +345,45 @@ __global__ void __launch_bounds__(kFewWarps * 32, NT == 1 ? 3 : 2)
         for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
             for (int e = 0; e < 4; ++e) {
-                x[nt][e] *= lift;
+                x[nt][e] *= kFewLift;
                 l[nt][e & 1] += x[nt][e];
             }
+        auto add_values = [&](auto any_wide) {
 #pragma unroll
-        for (int j = 0; j < NG; ++j) {
-            uint32_t p[NT][2];
+            for (int j = 0; j < NG; ++j) {
+                uint32_t p[NT][2];
 #pragma unroll
-            for (int half = 0; half < 2; ++half) {
-                const float2 sb = f16x2_to_f32x2(*reinterpret_cast<const uint32_t*>(st + F::vs + (g + 8 * half) * F::pairs + 4 * j));
+                for (int half = 0; half < 2; ++half) {
+                    float2 sb = f16x2_to_f32x2(*reinterpret_cast<const uint32_t*>(st + F::vs + (g + 8 * half) * F::pairs + 4 * j));
+                    if constexpr (decltype(any_wide)::value) sb.x *= few_unit<NG>(wide, j);
 #pragma unroll
-                for (int nt = 0; nt < NT; ++nt) {
-                    p[nt][half] = transposed(f16x2(x[nt][2 * half] * sb.x, x[nt][2 * half + 1] * sb.x));
-                    ob[j][nt][0] = fmaf(x[nt][2 * half], sb.y, ob[j][nt][0]);
-                    ob[j][nt][1] = fmaf(x[nt][2 * half + 1], sb.y, ob[j][nt][1]);
+                    for (int nt = 0; nt < NT; ++nt) {
+                        p[nt][half] = transposed(f16x2(x[nt][2 * half] * sb.x, x[nt][2 * half + 1] * sb.x));
+                        ob[j][nt][0] = fmaf(x[nt][2 * half], sb.y, ob[j][nt][0]);
+                        ob[j][nt][1] = fmaf(x[nt][2 * half + 1], sb.y, ob[j][nt][1]);
+                    }
+                }
+                // features 64 j + 8 g .. + 7 of keys 2 t, 2 t + 1 (first) and 2 t + 8, 2 t + 9 (second), keys side by side
+                uint32_t c[2][2];
+#pragma unroll
+                for (int half = 0; half < 2; ++half) {
+                    const int key = 2 * t + 8 * half;
+                    const char* at = st + F::v + key * F::row + (((2 * j + (g >> 2)) ^ F::v_swizzle(key)) << 4) + 4 * (g & 3);
+                    const uint32_t w0 = *reinterpret_cast<const uint32_t*>(at), w1 = *reinterpret_cast<const uint32_t*>(at + F::row);
+                    c[half][0] = __byte_perm(w0, w1, 0x5410);
+                    c[half][1] = __byte_perm(w0, w1, 0x7632);
+                }
+#pragma unroll
+                for (int z = 0; z < 4; ++z) {  // features 2 z (rows g) and 2 z + 1 (rows g + 8, times 16) of the 8
+                    const uint32_t c0 = c[0][z >> 1] >> (8 * (z & 1)), c1 = c[1][z >> 1] >> (8 * (z & 1));
+                    const uint32_t a[4] = {c0 & 0x000F000Fu, c0 & 0x00F000F0u, c1 & 0x000F000Fu, c1 & 0x00F000F0u};
+#pragma unroll
+                    for (int nt = 0; nt < NT; ++nt) mma_16816(o[j][z][nt], a, p[nt][0], p[nt][1]);
                 }
             }
-            // features 64 j + 8 g .. + 7 of keys 2 t, 2 t + 1 (first) and 2 t + 8, 2 t + 9 (second), keys side by side
-            uint32_t c[2][2];
-#pragma unroll
-            for (int half = 0; half < 2; ++half) {
-                const int key = 2 * t + 8 * half;
-                const char* at = st + F::v + key * F::row + (((2 * j + (g >> 2)) ^ F::v_swizzle(key)) << 4) + 4 * (g & 3);
-                const uint32_t w0 = *reinterpret_cast<const uint32_t*>(at), w1 = *reinterpret_cast<const uint32_t*>(at + F::row);
-                c[half][0] = __byte_perm(w0, w1, 0x5410);
-                c[half][1] = __byte_perm(w0, w1, 0x7632);
-            }
-#pragma unroll
-            for (int z = 0; z < 4; ++z) {  // features 2 z (rows g) and 2 z + 1 (rows g + 8, times 16) of the 8
-                const uint32_t c0 = c[0][z >> 1] >> (8 * (z & 1)), c1 = c[1][z >> 1] >> (8 * (z & 1));
-                const uint32_t a[4] = {c0 & 0x000F000Fu, c0 & 0x00F000F0u, c1 & 0x000F000Fu, c1 & 0x00F000F0u};
-#pragma unroll
-                for (int nt = 0; nt < NT; ++nt) mma_16816(o[j][z][nt], a, p[nt][0], p[nt][1]);
-            }
-        }
+        };
+        if (wide == 0) add_values(std::false_type{});
+        else add_values(std::true_type{});
     }
     cp_wait<0>();
 
@@ -375,7 +405,7 @@ __global__ void __launch_bounds__(kFewWarps * 32, NT == 1 ? 3 : 2)
 #pragma unroll
             for (int e = 0; e < 2; ++e) {
                 ml[0][warp][8 * nt + 2 * t + e] = m[nt][e];
-                ml[1][warp][8 * nt + 2 * t + e] = l[nt][e] / lift;
+                ml[1][warp][8 * nt + 2 * t + e] = l[nt][e] / kFewLift;
             }
     __syncthreads();  // and the rings are free
     float* part = reinterpret_cast<float*>(sm);  // [warp][row][D + 4]
@@ -387,15 +417,16 @@ __global__ void __launch_bounds__(kFewWarps * 32, NT == 1 ? 3 : 2)
             float top = ml[0][0][r];
 #pragma unroll
             for (int w = 1; w < kFewWarps; ++w) top = fmaxf(top, ml[0][w][r]);
-            const float f = m[nt][e] == -INFINITY ? 0.f : tc::ex2_approx(m[nt][e] - top) / lift;
+            const float f = m[nt][e] == -INFINITY ? 0.f : tc::ex2_approx(m[nt][e] - top) / kFewLift;
             float* dst = part + ((size_t)warp * 8 * NT + r) * (D + 4) + 8 * g;
 #pragma unroll
             for (int j = 0; j < NG; ++j) {
                 float y[8];
+                const float unit = 1.f / few_unit<NG>(wide, j);
 #pragma unroll
                 for (int z = 0; z < 4; ++z) {
-                    y[2 * z] = f * fmaf(o[j][z][nt][e], 16777216.f, ob[j][nt][e]);
-                    y[2 * z + 1] = f * fmaf(o[j][z][nt][e + 2], 1048576.f, ob[j][nt][e]);
+                    y[2 * z] = f * fmaf(o[j][z][nt][e], 16777216.f * unit, ob[j][nt][e]);
+                    y[2 * z + 1] = f * fmaf(o[j][z][nt][e + 2], 1048576.f * unit, ob[j][nt][e]);
                 }
                 *reinterpret_cast<float4*>(dst + 64 * j) = make_float4(y[0], y[1], y[2], y[3]);
                 *reinterpret_cast<float4*>(dst + 64 * j + 4) = make_float4(y[4], y[5], y[6], y[7]);
