@@ -864,3 +864,32 @@ def test_a_state_that_only_decays(gpu_lib, n):
     scan(gpu_lib, c, [0, n], n, out)
     _, S, _ = ref_run(c, 0, slice(0, n), list(range(-1, n - 1)), c["state"][0, 0], 1e-6, 1.0)
     assert (out[0, 0].double() - S[-1]).norm() <= 2.0 ** -18 * S[-1].norm()
+
+
+@pytest.mark.parametrize("log_s, g", [(120, -84.0), (124, -88.0), (126, -87.5), (40, -20.0), (-100, 0.0)])
+def test_a_state_at_the_ends_of_fp32(gpu_lib, log_s, g):
+    """A state near fp32's largest that a first decay brings to ordinary size, and one near its smallest."""
+    rng = np.random.default_rng(5)
+    for T in (3, 64):
+        c = case(T, 1, 1, (1, T), 1, 2, 128, 128)
+        c["state"] = torch.sign(c["state"]) * 2.0 ** (log_s - 1) * (1 + torch.rand_like(c["state"]))
+        c["g"][0, 0, 0] = g
+        par = tree(rng, T, "random")
+        o = verify(gpu_lib, c, [par])[0, 0]
+        want, _, _ = ref_run(c, 0, slice(0, T), par, c["state"][0, 0], 1e-6, 128 ** -0.5)
+        after = {x: c[x].clone() for x in c}
+        after["g"][0, 0, 0] = 0.0
+        left = c["state"][0, 0].double() * np.exp(g)
+        _, _, MW = ref_run(after, 0, slice(0, T), par, left, 1e-6, 128 ** -0.5)
+        close_o(o, want, MW, T, 128, 128 ** -0.5)
+    n = 100
+    c = case(n, 1, 1, (n,), 1, 2, 128, 128)
+    c["state"] = torch.sign(c["state"]) * 2.0 ** (log_s - 1) * (1 + torch.rand_like(c["state"]))
+    c["g"][0, 0] = g
+    out = torch.empty_like(c["state"])
+    o, _ = scan(gpu_lib, c, [0, n], n, out)
+    want, S, _ = ref_run(c, 0, slice(0, n), list(range(-1, n - 1)), c["state"][0, 0], 1e-6, 128 ** -0.5)
+    c["g"][0, 0] = 0.0
+    _, _, MW = ref_run(c, 0, slice(0, n), list(range(-1, n - 1)), c["state"][0, 0].double() * np.exp(g), 1e-6, 128 ** -0.5)
+    close_o(o[0], want, MW, n, 128, 128 ** -0.5)
+    close_state(out[0, 0], S[-1], MW, n, 128)

@@ -356,14 +356,14 @@ __global__ void __launch_bounds__((kScanPrep + DV / 16) * 32, 1)
                 const int i = pt & 63;
                 const bool q = pt >= 3 * kScanT;
                 const float x = (q ? ky.fq : ky.fk)[i], gh = rw.g_hi[i], gl = rw.g_lo[i];
-                (q ? rw.cq : rw.ck)[i] = tc::ex2_approx((gh - floorf(rw.g_hi[0])) + gl) * x;
+                (q ? rw.cq : rw.ck)[i] = tc::ex2_approx((gh - fade_exponent(rw.g_hi[0])) + gl) * x;
                 if (!q) dj[i] = tc::ex2_approx((rw.g_hi[63] - gh) + (rw.g_lo[63] - gl)) * x;
                 else if (i == 63) dj[64] = tc::ex2_approx(gh + gl);
             } else if (pw == 2) {
-                const float write = least_write(rw, min(kScanT, n - c * kScanT), lane), e = floorf(rw.g_hi[0]);
+                const float write = least_write(rw, min(kScanT, n - c * kScanT), lane), e = fade_exponent(rw.g_hi[0]);
                 if (lane == 0) {  // G falls from token to token
                     rw.e = e;
-                    rw.fade = pow2_floor((int)e);
+                    rw.fade = pow2_of(e);
                     rw.seen = tc::ex2_approx(rw.g_hi[63] - e);
                     rw.write = write;
                 }

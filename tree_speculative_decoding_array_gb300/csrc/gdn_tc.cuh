@@ -180,7 +180,7 @@ struct GdnRows {
     float g_hi[64], g_lo[64];  // G in units of ln 2, as hi + lo (differences of far sums keep fp32 accuracy)
     float beta[64];
     float ck[64], cq[64];      // 2^(G - e) fk, 2^(G - e) fq
-    // e: the floor of the largest G.  The state enters as 2^e S (fade = 2^e), so that what no row sees of it - a state that
+    // e: the floor of the largest G (within fp32's exponents).  The state enters as 2^e S (fade = 2^e), so that what no row sees of it - a state that
     // the block's first row forgets - has no part in the scale.  seen, write: smallest 2^(G - e) (rounded down) and |beta|.
     float e, fade, seen, write;
 };
@@ -238,7 +238,9 @@ __device__ __forceinline__ uint32_t abs_min2(uint32_t low, uint32_t v) {
     return *reinterpret_cast<const uint32_t*>(&x);
 }
 
-__device__ __forceinline__ float pow2_floor(int e) { return __uint_as_float((uint32_t)(min(max(e, -127), 127) + 127) << 23); }  // 0 below 2^-126
+// The exponent that the state enters a block with, from the largest G, and its power of two.
+__device__ __forceinline__ float fade_exponent(float g) { return fminf(fmaxf(floorf(g), -126.f), 127.f); }
+__device__ __forceinline__ float pow2_of(float e) { return __uint_as_float((uint32_t)((int)e + 127) << 23); }
 
 // Smallest |beta| of a block's first n rows, by one warp.
 __device__ __forceinline__ float least_write(const GdnRows& rw, int n, int lane) {

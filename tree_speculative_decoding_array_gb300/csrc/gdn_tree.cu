@@ -268,13 +268,13 @@ __global__ void __launch_bounds__(2 * DV, 2) gdn_tree_kernel(const __grid_consta
     if (warp < heads) {  // the largest and smallest G and the smallest write, while K and Q arrive
         GdnRows& rw = rows[warp];
         const float g0 = lane < T ? rw.g_hi[lane] : rw.g_hi[0], g1 = lane + 32 < T ? rw.g_hi[lane + 32] : g0;
-        const int most = __reduce_max_sync(0xFFFFFFFFu, __float2int_rd(fmaxf(g0, g1)));
+        const float e = fade_exponent((float)__reduce_max_sync(0xFFFFFFFFu, __float2int_rd(fmaxf(g0, g1))));
         const int least = __reduce_min_sync(0xFFFFFFFFu, __float2int_rd(fminf(g0, g1)));
         const float write = least_write(rw, T, lane);
         if (lane == 0) {
-            rw.e = (float)most;
-            rw.fade = pow2_floor(most);
-            rw.seen = tc::ex2_approx((float)(least - most));
+            rw.e = e;
+            rw.fade = pow2_of(e);
+            rw.seen = tc::ex2_approx((float)least - e);
             rw.write = write;
         }
     }
