@@ -13,9 +13,9 @@
 //                       their product with K onto the decayed state, which stays in TMEM in fp32.
 // The system is solved right-looking: U_b is applied to every block after b at once, so that the products of different
 // blocks are independent.
-// 16391 tokens, 48 heads of 128 x 128: 1.24 to 1.34 ms, about 4.9 us a chunk, where reading and writing everything once would
-// take 81 us: bound by the two groups' chains of steps (state: split 1.0 us, product 0.6, solve 1.5, o and the new state
-// 1.2; preparation: staging 1.4, product 0.6, matrices 2), which are of equal length.  24 prompts of 5 to 4001 tokens 0.44 ms.
+// 16391 tokens, 48 heads of 128 x 128: 1.21 ms alone, 1.34 among others, about 5 us a chunk, where reading and writing
+// everything once would take 81 us: bound by the two groups' chains of steps (split, product, solve, o and the new state;
+// staging, product, matrices), which are of equal length.  24 prompts of 5 to 4001 tokens 0.47 ms.
 // What reaches the state is kept to 2^-22 (fp16 pairs; K's values are exact), what reaches o alone to 2^-12.
 #include <math.h>
 
@@ -433,15 +433,17 @@ __global__ void __launch_bounds__((kScanPrep + DV / 16) * 32, 1)
             }
             const float e_n = dj[64];
             tc::tc_fence_after();
-            float S2[DK / 2];  // this thread's part of the state
+            float S2[32];  // 64 columns of this thread's part of the state (all of it would crowd registers and instruction cache)
+#pragma unroll 1
+            for (int x = 0; x < DK / 64; ++x) {
+                tc::tmem_ld_frag8(la + M::col_s + 64 * x, S2);
+                tc::tmem_wait_ld();
 #pragma unroll
-            for (int x = 0; x < DK / 64; ++x) tc::tmem_ld_frag8(la + M::col_s + 64 * x, S2 + 32 * x);
-            tc::tmem_wait_ld();
+                for (int y = 0; y < 32; y += 4)
 #pragma unroll
-            for (int x = 0; x < DK / 2; x += 4)
-#pragma unroll
-                for (int half = 0; half < 2; ++half)
-                    sx[half] = fmaxf(sx[half], fmaxf(fabsf(S2[x + 2 * half]), fabsf(S2[x + 2 * half + 1])));
+                    for (int half = 0; half < 2; ++half)
+                        sx[half] = fmaxf(sx[half], fmaxf(fabsf(S2[y + 2 * half]), fabsf(S2[y + 2 * half + 1])));
+            }
             const float fade = rw.fade, seen = rw.seen;
             // sd: the feature's largest state, faded and scaled; the smaller of both features' (fade_s), of the state as it is
             // (full_s) and of all v (least), where a feature is not empty
@@ -485,21 +487,25 @@ __global__ void __launch_bounds__((kScanPrep + DV / 16) * 32, 1)
             const bool early = e_n >= 0x1p-60f && !redo;
             const float se[2] = {sc[0] * e_n, sc[1] * e_n}, sf[2] = {sc[0] * fade, sc[1] * fade};
             float last[2] = {sd[0] * seen, sd[1] * seen};  // what the feature's new state is made of, its largest
-#pragma unroll
-            for (int x = 0; x < DK / 64; ++x) {
+#pragma unroll 1
+            for (int x = DK / 64 - 1; x >= 0; --x) {
                 uint32_t hi[16], lo[16];
+                if (x != DK / 64 - 1) {
+                    tc::tmem_ld_frag8(la + M::col_s + 64 * x, S2);
+                    tc::tmem_wait_ld();
+                }
 #pragma unroll
                 for (int y = 0; y < 16; ++y) {  // y = 2 n + half
-                    const float2 s = make_float2(S2[32 * x + 2 * y], S2[32 * x + 2 * y + 1]);
+                    const float2 s = make_float2(S2[2 * y], S2[2 * y + 1]);
                     const float2 z = mul2(s, make_float2(sf[y & 1], sf[y & 1]));
                     split2(z.x, z.y, hi[y], lo[y]);
                     if (early) {
                         const float2 ze = mul2(s, make_float2(se[y & 1], se[y & 1]));
-                        S2[32 * x + 2 * y] = ze.x;
-                        S2[32 * x + 2 * y + 1] = ze.y;
+                        S2[2 * y] = ze.x;
+                        S2[2 * y + 1] = ze.y;
                     }
                 }
-                if (early) tc::tmem_st_frag8f(la + M::col_s + 64 * x, S2 + 32 * x);
+                if (early) tc::tmem_st_frag8f(la + M::col_s + 64 * x, S2);
                 tc::tmem_st_frag8(la + M::col_hi + 32 * x, hi);
                 tc::tmem_st_frag8(la + M::col_lo + 32 * x, lo);
             }
@@ -683,9 +689,9 @@ static void launch_scan_dims(const tsv_gdn_desc& d, const int32_t* cu_len, int m
     constexpr int sm = ScanSmem<DK, DV>::total;
     cudaFuncSetAttribute(gdn_scan_kernel<DK, DV>, cudaFuncAttributeMaxDynamicSharedMemorySize, sm);
     // The longest sequences first, where one of the longest, started last, would add more than a sixteenth to the whole
-    // (max_len rows of one head against every SM's share of all rows).  24 prompts of 5 to 4001 tokens: 0.44 ms, in the
-    // order given 0.48; finding its place costs a CTA up to 0.9 us: 256 prompts of 17 to 400 tokens 1.68 ms, in the order
-    // given 1.61.
+    // (max_len rows of one head against every SM's share of all rows).  24 prompts of 5 to 4001 tokens: 0.465 ms, in the
+    // order given 0.516; finding its place costs a CTA up to 0.9 us: 256 prompts of 17 to 400 tokens 1.77 ms, in the order
+    // given 1.73.
     const int sorted = d.B > 1 && d.B <= kScanSort && max_len > kScanT &&
                        16LL * max_len * sm_count() > (long long)d.T * d.n_layers * d.HV;
     launch_pdl(gdn_scan_kernel<DK, DV>, (unsigned)((long long)d.n_layers * d.B * d.HV * (d.DV / DV)), (kScanPrep + DV / 16) * 32, sm,
@@ -694,8 +700,8 @@ static void launch_scan_dims(const tsv_gdn_desc& d, const int32_t* cu_len, int m
 
 void launch_gdn_scan(const tsv_gdn_desc& d, const int32_t* cu_len, int max_len, int32_t* status, cudaStream_t stream) {
     // Half heads while both halves of every head find an SM: the preparation is done twice, but a half's warps have more
-    // of their SM to themselves.  48 heads, 16391 tokens alone: 1.24 ms, whole heads 1.40; two prompts of 4096: 0.62 ms, whole
-    // heads 0.36.
+    // of their SM to themselves.  48 heads, 16391 tokens: 1.33 ms, whole heads 1.42 (alone 1.20 and 1.42); two prompts of 4096:
+    // 0.61 ms, whole heads 0.39.
     const bool half = d.DV == 64 || 2LL * d.n_layers * d.B * d.HV <= sm_count();
     if (d.DK == 64) half ? launch_scan_dims<64, 64>(d, cu_len, max_len, status, stream) : launch_scan_dims<64, 128>(d, cu_len, max_len, status, stream);
     else half ? launch_scan_dims<128, 64>(d, cu_len, max_len, status, stream) : launch_scan_dims<128, 128>(d, cu_len, max_len, status, stream);
