@@ -122,6 +122,7 @@ def attn_desc(q, k, v, o, kv_len, anc, *, T, HQ, HKV, D, kv_dtype, max_kv_len, k
     4-bit caches (I4_G64): k/v uint8 [B,HKV,s_cap,D/2], scales fp16 [B,HKV,s_cap,D/64,2] (scale, bias).
 
     window: per-layer sliding windows (0 = full attention), or None for all full-attention layers.
+    A descriptor holds addresses: its tensors (kv_len and anc among them) have to live as long as it is used.
     """
     n = len(q)
     if not (1 <= n <= MAX_LAYERS) or not (len(k) == len(v) == len(o) == n):
@@ -299,7 +300,8 @@ def gdn_desc(q, k, v, g, beta, state, *, o=None, state_out=None, norm_eps=1e-6, 
     q/k bf16 [B,T,HK,DK], v/o bf16 [B,T,HV,DV], g/beta fp32 [B,T,HV] for a tree block (gdn_tree_verify, gdn_commit);
     the same without the B axis, T packed rows, for gdn_scan.  state/state_out fp32 [B,HV,DV,DK]; state_out None
     updates the states in place.  q may be None for gdn_commit, o for any call that writes none.  norm_eps > 0
-    divides the rows of q and k by sqrt(sum x^2 + norm_eps); scale 0 is 1 / sqrt(DK).
+    divides the rows of q and k by sqrt(sum x^2 + norm_eps); scale 0 is 1 / sqrt(DK).  The descriptor holds addresses:
+    its tensors have to live as long as it is used.
     """
     n = len(k)
     state_out = state if state_out is None else state_out

@@ -13,8 +13,8 @@
 //
 // A warp takes 16 keys at a time through a private ring of cp.async stages, all rows, all features; the four warps of a
 // CTA interleave over one key range and merge their partials through shared memory at its end.  32 tokens over up to 32768
-// keys, 4 layers x 4 heads of 256: 668 us, 5.4 TB/s (720 us where scales are above 3.9); about 25 instructions per key and warp take 60 % of the issue slots,
-// half of them masks on the half-rate integer pipe.
+// keys, 4 layers x 4 heads of 256: 668 us, 5.4 TB/s (720 us with scales above 3.9 in every step); about 25 instructions per
+// key and warp take 62 % of the issue slots, half of them masks on the half-rate integer pipe.
 #include <math.h>
 
 #include "common.cuh"
@@ -25,7 +25,7 @@ namespace tsv {
 constexpr int kFewWarps = 4;
 constexpr int kFewKeys = 16;  // keys per warp and step
 // P s_g goes through fp16, whose smallest value is 2^-24: with scales of 2^-7 (values of 0.06) a key 2^17 behind the
-// maximum would be lost, and a long cache holds many such keys behind an early one that draws most of the weight.  So the
+// maximum would be lost, and a long cache holds many such keys behind an early one that draws most of the weight.  So
 // P is lifted by 2^12, but for a group in steps where one of its scales is above 3.9 (4 x 2^12 x 3.9 < 65504): its part of O
 // is brought to the other unit where such steps begin and end, and the other groups keep their lift.
 constexpr float kFewLift = 4096.f;

@@ -208,9 +208,9 @@ void launch_gdn_tree(const tsv_gdn_desc& d, const uint64_t* anc, int32_t* status
 void launch_gdn_scan(const tsv_gdn_desc& d, const int32_t* cu_len, int max_len, int32_t* status, cudaStream_t stream);
 
 // Sequences of up to this many tokens are advanced token by token, longer ones in chunks of 64 (whose time hardly depends on
-// the length up to 64; the more heads there are, the better the recurrence hides its latency).  48 heads, token by token
-// against in chunks: 1 sequence of 8 tokens 11.7 and 13.3 us, of 12 15.2 and 13.4; 8 sequences of 12 tokens 33.9 and 38.6, of
-// 16 42.2 and 38.4; 64 sequences of 16 tokens 223 and 253, of 18 255 and 253.
+// the length up to 64; the more heads there are, the better the recurrence hides its latency).  48 heads of 128, token by token
+// against in chunks: 1 sequence of 8 tokens 10.2 and 12.0 us, of 12 13.9 and 12.0; 8 sequences of 12 tokens 34.9 and 38.1, of
+// 16 44.2 and 38.2; 64 sequences of 16 tokens 233 and 256, of 18 268 and 256.
 static int recur_max(const tsv_gdn_desc* d) {
     const long long units = (long long)d->n_layers * d->B * d->HV;
     return units < 2LL * sm_count() ? 10 : units < 8LL * sm_count() ? 14 : 17;

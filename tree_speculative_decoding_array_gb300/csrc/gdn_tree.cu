@@ -9,8 +9,8 @@
 // the value heads follow one another.  Each warp owns 16 value features and takes their rows of S from global memory
 // to fp16 pairs in TMEM, fetches their columns of V and writes their columns of o; the next head's state and V are
 // fetched while this head is computed, and a head's matrices are built while the tensor cores work on its S [K; Q]^T.
-// The warps of a head only meet to hand over S and the matrices.  48 layers x 48 heads of 128 x 128: trees of 3 nodes 34 us,
-// of 16 nodes 36 us (4.9 TB/s), 32 trees of 64 nodes 1.93 ms (4.2 TB/s): two CTAs fit an SM, so what bounds it is the chain
+// The warps of a head only meet to hand over S and the matrices.  48 layers x 48 heads of 128 x 128: trees of 3 nodes 35 us,
+// of 16 nodes 37 us (4.7 TB/s), 32 trees of 64 nodes 1.98 ms (4.1 TB/s): two CTAs fit an SM, so what bounds it is the chain
 // of a head's steps, and at 64 nodes its 15,000 warp instructions (45 % of the issue slots).
 //
 // K, Q and S are kept with the columns of every 16 in the order 0 1 4 5 8 9 12 13 2 3 6 7 10 11 14 15, in which a thread's four
@@ -254,8 +254,8 @@ __global__ void __launch_bounds__(2 * DV, 2) gdn_tree_kernel(const __grid_consta
         __syncwarp();
     }
     // The next head's state is fetched ahead: to registers where they are free, else (four blocks) to L2, 128 bytes per
-    // prefetch.  48 layers, registers against L2: 3 nodes 38 and 42 us, 16 nodes 39 and 44, 4 trees of 20 nodes 163 and 174,
-    // of 40 nodes 211 and 214; 8 trees of 64 nodes 508 and 500.
+    // prefetch.  48 layers, registers against L2: 3 nodes 35.3 and 38.9 us, 16 nodes 38.9 and 41.5, 4 trees of 20 nodes 166 and
+    // 171, of 40 nodes 215 and 213; 8 trees of 64 nodes 514 and 509.
     constexpr bool kAhead = NB < 4;
     auto ahead_s = [&](int k) {
         const char* p = reinterpret_cast<const char*>(d.state[layer] + ((size_t)b * d.HV + h0 + k) * DV * DK);
@@ -471,13 +471,13 @@ static void launch_tree_nb(const tsv_gdn_desc& d, const uint64_t* anc, int32_t* 
     cudaFuncSetAttribute(gdn_tree_kernel<DK, DV, NB>, cudaFuncAttributeMaxDynamicSharedMemorySize, sm);
     // Value heads per CTA: as many as share a key head (up to kMaxHeads) as long as every SM gets CTAs for two rounds;
     // fewer, larger CTAs save the staging but leave SMs idle on small batches.  48 layers x 48 heads, one tree of 3 nodes:
-    // three heads per CTA 44.5 us, one 54.4.
+    // three heads per CTA 35.4 us, one 50.0.
     const int per = d.HV / d.HK;
     int heads = 1;
     for (int x = 2; x <= kMaxHeads; ++x)
         if (per % x == 0 && (long long)d.n_layers * d.B * d.HV / x >= 4LL * sm_count()) heads = x;
-    // The last heads, four for every three SMs, have a CTA each: the call ends sooner than with large CTAs alone (3 nodes 34.1
-    // against 36.3 us, 16 nodes 36.3 against 38.2; twice as many 34.7 and 36.7, half as many 34.5 and 36.8).
+    // The last heads, four for every three SMs, have a CTA each: the call ends sooner than with large CTAs alone (3 nodes 35.4
+    // against 37.6 us, 16 nodes 38.8 against 40.6; twice as many 36.9 and 40.5, half as many 35.5 and 38.9).
     const long long all = (long long)d.n_layers * d.B * d.HV;
     const long long big = heads > 1 ? (all - sm_count() * 4 / 3) / heads : all;
     launch_pdl(gdn_tree_kernel<DK, DV, NB>, (unsigned)(big + (all - big * heads)), 2 * DV, sm, stream, d, anc, heads, (int)big, status);

@@ -133,8 +133,8 @@ extern "C" tsv_status tsv_kv_gather_positions(const tsv_kv_desc* kv, int32_t* kv
     if (kv->D != 64 && kv->D != 128 && kv->D != 256)
         return fail(TSV_EUNSUPPORTED, "kv_gather_positions: head dim %d is not 64, 128 or 256", kv->D);
     if (!kv_format_ok(kv->kv_dtype))
-        return fail(TSV_EUNSUPPORTED, "kv_gather_positions: cache format %d has no gather (only fp16, bf16 and "
-                                      "Int8 with per-token scales keep all per-token state on the sequence axis)",
+        return fail(TSV_EUNSUPPORTED, "kv_gather_positions: cache format %d has no gather (only fp16, bf16, "
+                                      "Int8 and 4-bit caches keep all per-token state on the sequence axis)",
                     kv->kv_dtype);
     if (kv->s_cap < T) return fail(TSV_EINVAL, "kv_gather_positions: s_cap=%lld < T", (long long)kv->s_cap);
     if (kv->B == 0) return TSV_OK;
@@ -296,8 +296,8 @@ extern "C" tsv_status tsv_gather_positions(const tsv_kv_desc* kv, int32_t* kv_le
     if (kv->D != 64 && kv->D != 128 && kv->D != 256)
         return fail(TSV_EUNSUPPORTED, "gather_positions: head dim %d is not 64, 128 or 256", kv->D);
     if (!kv_format_ok(kv->kv_dtype))
-        return fail(TSV_EUNSUPPORTED, "gather_positions: cache format %d has no gather (only fp16, bf16 and Int8 "
-                                      "with per-token scales keep all per-token state on the sequence axis)",
+        return fail(TSV_EUNSUPPORTED, "gather_positions: cache format %d has no gather (only fp16, bf16, Int8 "
+                                      "and 4-bit caches keep all per-token state on the sequence axis)",
                     kv->kv_dtype);
     if (kv->s_cap < 1 || kv->s_cap > 0x7FFFFFFFLL)
         return fail(TSV_EINVAL, "gather_positions: s_cap=%lld outside [1, 2^31)", (long long)kv->s_cap);
