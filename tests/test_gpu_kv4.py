@@ -629,3 +629,46 @@ def test_small_values_beside_wide_ones(gpu_lib, T, D, wide):
     else:
         tol[..., 64 * last:] += 2.0 ** -10 * 2250 * math.exp(-12)
     assert (err <= tol).all(), (err / tol).max().item()
+
+
+@pytest.mark.parametrize("splits", [0, 1, 3])
+@pytest.mark.parametrize("path", [0, 3, 4])
+@pytest.mark.parametrize("fmt", ["f16", "bf16", "i8"])
+def test_a_query_row_that_is_not_finite_over_other_caches(gpu_lib, fmt, path, splits):
+    """The same on the tensor-core kernels of the other formats, whose splits are merged by the same kernel."""
+    tsv, B, T, HQ, HKV, D, S = gpu_lib, 1, 16, 24, 4, 256, 500
+    gen = torch.Generator().manual_seed(path)
+    r = lambda *s: torch.randn(*s, generator=gen).to(DEV)  # noqa: E731
+    if fmt == "i8":
+        k, v = (torch.randint(-127, 128, (B, HKV, S + T, D), generator=gen, dtype=torch.int8).to(DEV) for _ in "kv")
+        scales = dict(k_scale=[(0.01 * r(B, HKV, S + T).abs()).half()], v_scale=[(0.01 * r(B, HKV, S + T).abs()).half()])
+    else:
+        k, v = (r(B, HKV, S + T, D).to(torch.float16 if fmt == "f16" else torch.bfloat16) for _ in "kv")
+        scales = {}
+    kv_dtype = dict(f16=tsv.F16, bf16=tsv.BF16, i8=tsv.I8_SCALED)[fmt]
+    anc, _ = masks(tsv, [random_tree(np.random.default_rng(1), T)])
+    kv_len = torch.tensor([S + T], dtype=torch.int32, device=DEV)
+    clean = r(B, T, HQ, D).bfloat16()
+
+    def run(q):
+        o = torch.full((B, T, HQ, D), 7.0, dtype=torch.bfloat16, device=DEV)
+        d = tsv.attn_desc([q], [k], [v], [o], kv_len, anc, T=T, HQ=HQ, HKV=HKV, D=D, kv_dtype=kv_dtype, max_kv_len=S + T, splits=splits,
+                          path=path, **scales)
+        ws = torch.empty(max(tsv.attention_workspace_size(d), 16), dtype=torch.uint8, device=DEV)
+        tsv.tree_verify_attention(d, ws)
+        torch.cuda.synchronize()
+        return o
+
+    want = run(clean)
+    for bad in (float("nan"), "one nan", 1e30):
+        if fmt == "bf16" and bad == 1e30:
+            continue  # within bf16: a finite, one-hot softmax
+        q = clean.clone()
+        if bad == "one nan":
+            q[0, 5, 7, 9] = float("nan")
+        else:
+            q[0, 5, 7] = bad
+        o = run(q)
+        assert torch.isnan(o[0, 5, 7]).all(), bad
+        o[0, 5, 7] = want[0, 5, 7]
+        assert torch.equal(o, want), bad
