@@ -15,7 +15,7 @@
 // Operands are fp16 with power-of-two scales, which cost nothing in accuracy: K and Q rows hold bf16 values (8 bits,
 // exact in fp16 once the row's norm is scaled to about 1; what falls below 2^-24 of it is lost), S, R and U of one
 // value feature share a scale (their equations are linear in them).  An fp16 operand is within 2^-12 of its value; an
-// hi + lo pair within 2^-22 (or 2^-25 of the feature's largest value).  Accumulation is fp32.
+// hi + lo pair within 2^-22 (either: or 2^-37 of the feature's largest value).  Accumulation is fp32.
 #pragma once
 
 #include "common.cuh"
@@ -180,8 +180,9 @@ struct GdnRows {
     float g_hi[64], g_lo[64];  // G in units of ln 2, as hi + lo (differences of far sums keep fp32 accuracy)
     float beta[64];
     float ck[64], cq[64];      // 2^(G - e) fk, 2^(G - e) fq
-    // e: the floor of the largest G (within fp32's exponents).  The state enters as 2^e S (fade = 2^e), so that what no row sees of it - a state that
-    // the block's first row forgets - has no part in the scale.  seen, write: smallest 2^(G - e) (rounded down) and |beta|.
+    // e: the floor of the largest G (within fp32's exponents).  The state enters as 2^e S (fade = 2^e), so that what no row
+    // sees of it - a state that the block's first row forgets - has no part in the scale.  seen, write: smallest 2^(G - e)
+    // (rounded down) and |beta|.
     float e, fade, seen, write;
 };
 

@@ -10,7 +10,7 @@
 // to fp16 pairs in TMEM, fetches their columns of V and writes their columns of o; the next head's state and V are
 // fetched while this head is computed, and a head's matrices are built while the tensor cores work on its S [K; Q]^T.
 // The warps of a head only meet to hand over S and the matrices.  48 layers x 48 heads of 128 x 128: trees of 3 nodes 35 us,
-// of 16 nodes 37 us (4.7 TB/s), 32 trees of 64 nodes 1.98 ms (4.1 TB/s): two CTAs fit an SM, so what bounds it is the chain
+// of 16 nodes 37 us (4.7 TB/s), 32 trees of 64 nodes 1.99 ms (4.1 TB/s): two CTAs fit an SM, so what bounds it is the chain
 // of a head's steps, and at 64 nodes its 15,000 warp instructions (45 % of the issue slots).
 //
 // K, Q and S are kept with the columns of every 16 in the order 0 1 4 5 8 9 12 13 2 3 6 7 10 11 14 15, in which a thread's four
@@ -45,8 +45,9 @@ struct TreeSmem {
 };
 
 // The whole tree of one head in fp32, node by node: taken when an operand left fp16's range (an infinity or a NaN in
-// the inputs, keys that are not of unit length with large writes, values far above those that another node sees).  Only a node's ancestors are ever read, so what is
-// not finite stays with its node and the node's descendants.  Thread = value feature.
+// the inputs, keys that are not of unit length with large writes, values far above those that another node sees).  Only a
+// node's ancestors are ever read, so what is not finite stays with its node and the node's descendants.  Thread = value
+// feature.
 template <int DK, int DV, int NB>
 __device__ __noinline__ void tree_fp32(const tsv_gdn_desc& d, const uint64_t* anc, int layer, int b, int h, char* sm, const GdnRows& rw) {
     using M = TreeSmem<DK, DV, NB>;
