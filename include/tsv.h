@@ -75,7 +75,9 @@ typedef enum {
     TSV_BF16 = 1,      /* bfloat16 */
     TSV_I8_SCALED = 2, /* int8 code x fp16 per-token scale (KV caches only) */
     TSV_Q4_G64 = 3,    /* 4-bit affine, groups of 64 input features (LM head only) */
-    TSV_I4_G64 = 4     /* 4-bit affine, groups of 64 features of a token's row (KV caches only) */
+    TSV_I4_G64 = 4,    /* 4-bit affine, groups of 64 features of a token's row (KV caches only) */
+    TSV_E4M3_B128 = 5, /* e4m3 codes x fp32 scales, one per block of 128 x 128 (LM head, matmul weights) */
+    TSV_F32 = 6        /* IEEE binary32 (norm rows, logits, products) */
 } tsv_dtype;
 
 /* Device status codes (dev_status word 0). */
@@ -536,6 +538,74 @@ tsv_status tsv_gdn_commit(const tsv_gdn_desc* d, const int32_t* path, const int3
 
 tsv_status tsv_gdn_scan(const tsv_gdn_desc* d, const int32_t* cu_len, int32_t max_len, int32_t* dev_status,
                         cudaStream_t stream);
+
+/*
+ * What stands ahead of the LM head, and products, in 8 bits.  The pages have no counterpart: [1185] Phase 3 quantises the
+ * head to 4 bits, and its cost model counts the projections among a verify's reads; these calls serve targets whose
+ * weights are e4m3 with one fp32 scale per block of 128 x 128.
+ *
+ * 8-bit rows: codes e4m3 [rows, H] with float scale [rows, ceil(H / 128)]; per 128 features of a row (the last group may be
+ *   shorter) scale = max |y| * (1 / 448) in fp32 (1 / 448 rounded to fp32) and code = e4m3(y / scale), the division in fp32,
+ *   the code rounded to nearest even and held to +-448.  A group of zeros, or of values so small that the scale is 0, has
+ *   scale 0 and zero codes; a NaN or an infinity among a group's values makes its scale that, and the codes follow.
+ *
+ * tsv_add_rms_norm - the residual's addition and the root-mean-square norm of every row:
+ *     h = x + residual;  y = h / sqrt(mean(h^2) + eps) * (weight_offset + weight)
+ *   x, residual, residual_out, weight, out: `dtype` (TSV_F16, TSV_BF16 or TSV_F32), [rows, H], weight [H].  residual may
+ *   be NULL (h = x).  Outputs, each optional but one at least: residual_out = h, out = y, and y as 8-bit rows in out8 (uint8 e4m3
+ *   [rows, H]) with out8_scale.  Everything between is fp32 and each output is rounded once from it: y is of the unrounded h, the codes of
+ *   the unrounded y.  A row whose squares leave fp32's range is scaled by a power of two first.  residual_out may equal residual or x,
+ *   out may equal x or residual; otherwise outputs overlap neither inputs nor each other.
+ *   1 <= H <= 32768, 1e-30 <= eps, eps and weight_offset finite.  A NaN or an infinity in a row makes that row's y NaN where it
+ *   is not zero.
+ * tsv_quantize_e4m3 - 8-bit rows of x as it is: out8, out8_scale as above (H without an upper limit).
+ */
+tsv_status tsv_add_rms_norm(const void* x, const void* residual, const void* weight, int32_t rows, int32_t H, int32_t dtype,
+                            float eps, float weight_offset, void* residual_out, void* out, void* out8, float* out8_scale,
+                            cudaStream_t stream);
+
+tsv_status tsv_quantize_e4m3(const void* x, int32_t rows, int32_t H, int32_t dtype, void* out8, float* out8_scale,
+                             cudaStream_t stream);
+
+/*
+ * tsv_matmul_e4m3 - rows in 8 bits times weights in 8 bits:
+ *     out[m, n] = sum over k of a[m, k] a_scale[m, k / 128] w[n, k] w_scale[n / 128, k / 128]
+ *   a: e4m3 [rows, K], a_scale float [rows, ceil(K / 128)] (8-bit rows as above); w: e4m3 [N, K], w_scale float
+ *   [ceil(N / 128), ceil(K / 128)]; out [rows, N] of out_dtype (TSV_BF16, TSV_F16 or TSV_F32).  The products of 128 features are summed on
+ *   the tensor cores into fp32, scaled, and summed in fp32; out is rounded once.  The same inputs give the same bits in every call.
+ *   K % 16 == 0, a and w 16-byte aligned, rows >= 0, N >= 1.
+ * tsv_matmul_e4m3_argmax - the same product with its argmax, as tsv_lm_head_argmax: argmax int32 [rows] (ties to the lowest
+ *   index), maxval float [rows] or NULL; the products are never written.  Workspace: tsv_matmul_e4m3_argmax_workspace_size.
+ *   A product that is NaN counts as larger than every number if its sign bit is clear, and as smaller if it is set.
+ * tsv_lm_head_argmax, tsv_lm_head_logits with w_dtype TSV_E4M3_B128: W as w, scales as w_scale, biases ignored; hidden (bf16) becomes 8-bit
+ *   rows in the workspace first.  H % 16 == 0.
+ */
+tsv_status tsv_matmul_e4m3(const void* a, const float* a_scale, int32_t rows, int32_t K, const void* w, const float* w_scale,
+                           int32_t N, void* out, int32_t out_dtype, cudaStream_t stream);
+
+size_t tsv_matmul_e4m3_argmax_workspace_size(int32_t rows);
+
+tsv_status tsv_matmul_e4m3_argmax(const void* a, const float* a_scale, int32_t rows, int32_t K, const void* w,
+                                  const float* w_scale, int32_t N, int32_t* argmax, float* maxval, void* workspace,
+                                  size_t ws_bytes, cudaStream_t stream);
+
+/*
+ * tsv_token_logprobs - what a user asks about emitted tokens, from one read of the logits:
+ *     z = logits / temperature;  logp(t) = z_t - log(sum exp(z));  entropy = -sum p log p with p = softmax(z)
+ *   logits [rows, V] of logits_dtype (TSV_F32, TSV_BF16 or TSV_F16; each row may start anywhere: V needs no alignment).
+ *   targets int32 [rows] or NULL; logp float [rows]: each target's log probability; rank int32 [rows] or NULL: how many
+ *   tokens have a larger logit, or an equal one and a lower index (0: the greedy choice).  With targets NULL, logp and rank are NULL too.
+ *   entropy float [rows] or NULL.  top_tokens int32, top_logp float [rows, top_k]: the top_k largest, largest first, ties to the lower
+ *   index; 0 <= top_k <= min(64, V) (0: both NULL).
+ *   A logit of -infinity has probability 0 (and adds nothing to the entropy).  A row with a NaN or +infinity, or with
+ *   nothing but -infinity, has no distribution: its floats are NaN and its rank and tokens -1.  A target outside [0, V) (the -1 that
+ *   pads emitted tokens) gets logp NaN and rank -1.  1e-6 <= temperature <= 1e6.  Sums are fp32, in a fixed order.
+ */
+size_t tsv_token_logprobs_workspace_size(int32_t rows, int32_t V, int32_t top_k);
+
+tsv_status tsv_token_logprobs(const void* logits, int32_t logits_dtype, int32_t rows, int32_t V, const int32_t* targets,
+                              float temperature, int32_t top_k, float* logp, int32_t* rank, float* entropy,
+                              int32_t* top_tokens, float* top_logp, void* workspace, size_t ws_bytes, cudaStream_t stream);
 
 #ifdef __cplusplus
 }

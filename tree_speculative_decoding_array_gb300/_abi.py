@@ -12,7 +12,7 @@ _HERE = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(_HERE, "libtsv.so")
 
 OK, EINVAL, ETOPOLOGY, EUNSUPPORTED, ECAPACITY, ECUDA = range(6)
-F16, BF16, I8_SCALED, Q4_G64, I4_G64 = range(5)
+F16, BF16, I8_SCALED, Q4_G64, I4_G64, E4M3_B128, F32 = range(7)
 DEV_OK, DEV_BAD_ROOT, DEV_BAD_PARENT, DEV_BAD_PATH, DEV_BAD_KV_LEN, DEV_TIMEOUT, DEV_BAD_SEQ_LEN = range(7)
 ATTN_AUTO, ATTN_SIMT, ATTN_TCGEN05, ATTN_TCGEN05_64, ATTN_TCGEN05_128 = range(5)
 MAX_T = 64
@@ -88,6 +88,13 @@ SIGNATURES = {
     "tsv_gdn_tree_verify": (C.c_int, [C.POINTER(GdnDesc), _vp, _vp, _vp]),
     "tsv_gdn_commit": (C.c_int, [C.POINTER(GdnDesc), _vp, _vp, _vp, _vp]),
     "tsv_gdn_scan": (C.c_int, [C.POINTER(GdnDesc), _vp, _i32, _vp, _vp]),
+    "tsv_add_rms_norm": (C.c_int, [_vp, _vp, _vp, _i32, _i32, _i32, C.c_float, C.c_float, _vp, _vp, _vp, _vp, _vp]),
+    "tsv_quantize_e4m3": (C.c_int, [_vp, _i32, _i32, _i32, _vp, _vp, _vp]),
+    "tsv_matmul_e4m3": (C.c_int, [_vp, _vp, _i32, _i32, _vp, _vp, _i32, _vp, _i32, _vp]),
+    "tsv_matmul_e4m3_argmax_workspace_size": (_sz, [_i32]),
+    "tsv_matmul_e4m3_argmax": (C.c_int, [_vp, _vp, _i32, _i32, _vp, _vp, _i32, _vp, _vp, _vp, _sz, _vp]),
+    "tsv_token_logprobs_workspace_size": (_sz, [_i32, _i32, _i32]),
+    "tsv_token_logprobs": (C.c_int, [_vp, _i32, _i32, _i32, _vp, C.c_float, _i32, _vp, _vp, _vp, _vp, _vp, _vp, _sz, _vp]),
 }
 
 _lib = None

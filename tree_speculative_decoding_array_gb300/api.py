@@ -13,8 +13,10 @@ from dataclasses import dataclass, field
 import torch
 
 from . import _abi
-from ._abi import BF16, F16, I4_G64, I8_SCALED, MAX_LAYERS, Q4_G64, AppendDesc, AttnDesc, GdnDesc, KvDesc, check, load
+from ._abi import (BF16, E4M3_B128, F16, F32, I4_G64, I8_SCALED, MAX_LAYERS, Q4_G64, AppendDesc, AttnDesc, GdnDesc, KvDesc,
+                   check, load)
 
+ROW_DTYPE = {torch.bfloat16: BF16, torch.float16: F16, torch.float32: F32}
 KV_TORCH_DTYPE = {F16: torch.float16, BF16: torch.bfloat16, I8_SCALED: torch.int8, I4_G64: torch.uint8}
 
 
@@ -197,11 +199,14 @@ def lm_head_workspace_size(rows: int, H: int, V: int, w_dtype: int) -> int:
 
 def lm_head_argmax(hidden, W, argmax, *, w_dtype, V, scales=None, biases=None, maxlogit=None, workspace=None,
                    stream=None):
-    """hidden bf16 [rows,H]; W fp16/bf16 [V,H] or uint8 [V,H/2] (+ bf16 scales/biases [V,H/64])."""
+    """hidden bf16 [rows,H]; W fp16/bf16 [V,H], uint8 [V,H/2] (+ bf16 scales/biases [V,H/64]) or, for E4M3_B128, e4m3 [V,H]
+    (+ fp32 scales [ceil(V/128),ceil(H/128)])."""
     lib = load()
     rows, H = hidden.shape
     _cuda(hidden, "hidden", torch.bfloat16)
-    if w_dtype == Q4_G64:
+    if w_dtype == E4M3_B128:
+        _e4m3_head(hidden, W, scales, V, H)
+    elif w_dtype == Q4_G64:
         _cuda(W, "W", torch.uint8, (V, H // 2))
         _cuda(scales, "scales", torch.bfloat16, (V, H // 64))
         _cuda(biases, "biases", torch.bfloat16, (V, H // 64))
@@ -221,6 +226,9 @@ def lm_head_logits(hidden, W, logits, *, w_dtype, V, scales=None, biases=None, w
     """Every logit: hidden bf16 [rows, H] -> logits fp32 [rows, V]."""
     lib = load()
     rows, H = hidden.shape
+    if w_dtype == E4M3_B128:
+        _cuda(hidden, "hidden", torch.bfloat16)
+        _e4m3_head(hidden, W, scales, V, H)
     _cuda(logits, "logits", torch.float32, (rows, V))
     if workspace is None:
         workspace = torch.empty(max(lm_head_workspace_size(rows, H, V, w_dtype), 256), dtype=torch.uint8,
@@ -364,6 +372,131 @@ def gdn_scan(desc: GdnDesc, cu_len, *, max_len, dev_status=None, stream=None):
     check(load().tsv_gdn_scan(C.byref(desc), _p(cu_len), int(max_len), _p(dev_status), _stream(stream)), "gdn_scan")
 
 
+# ----------------------------------------------------------------------------- 8-bit rows, weights and what is asked of logits
+def _blocks(n):
+    """Groups of 128 that n features (or weight rows) fall into."""
+    return -(-n // 128)
+
+
+def _here(name, dtype, shape, t):
+    """t's address, once it is known to be a contiguous tensor of that type and shape on the current device."""
+    if t.dtype != dtype or t.shape != shape or not t.is_cuda or not t.is_contiguous():
+        _cuda(t, name, dtype, shape)
+    if t.get_device() != torch.cuda.current_device():
+        raise ValueError(f"{name} is on {t.device}, the current device is cuda:{torch.cuda.current_device()}")
+    return t.data_ptr()
+
+
+def _e4m3(name, t, shape):
+    """An e4m3 buffer: torch.float8_e4m3fn, or uint8 with the same bytes."""
+    return _here(name, torch.uint8 if t.dtype == torch.uint8 else torch.float8_e4m3fn, shape, t)
+
+
+def _e4m3_head(hidden, W, scales, V, H):
+    _here("hidden", torch.bfloat16, hidden.shape, hidden)
+    _e4m3("W", W, (V, H))
+    if scales is None:
+        raise ValueError("an e4m3 head needs scales")
+    _here("scales", torch.float32, (_blocks(V), _blocks(H)), scales)
+
+
+def _row_dtype(name, t):
+    if t.dim() != 2:
+        raise ValueError(f"{name} must have two dimensions, got {tuple(t.shape)}")
+    dt = ROW_DTYPE.get(t.dtype)
+    if dt is None:
+        raise ValueError(f"{name} must be bfloat16, float16 or float32, got {t.dtype}")
+    return dt
+
+
+def add_rms_norm(x, weight, *, eps, residual=None, residual_out=None, out=None, out8=None, out8_scale=None,
+                 weight_offset=0.0, stream=None):
+    """h = x + residual; y = h / sqrt(mean(h^2) + eps) * (weight_offset + weight), row by row.
+
+    x/residual/residual_out/out [rows, H] and weight [H] of one type (bf16, fp16 or fp32).  Outputs, each optional:
+    residual_out = h, out = y, and y as 8-bit rows: out8 (float8_e4m3fn or uint8) [rows, H] with out8_scale fp32
+    [rows, ceil(H/128)].  residual_out may be residual or x, out may be x or residual.
+    """
+    dt, shape = _row_dtype("x", x), x.shape
+    rows, H = shape
+    kind = x.dtype
+    if (out8 is None) != (out8_scale is None):
+        raise ValueError("out8 and out8_scale belong together")
+    check(load().tsv_add_rms_norm(
+        _here("x", kind, shape, x), None if residual is None else _here("residual", kind, shape, residual),
+        _here("weight", kind, (H,), weight), rows, H, dt, eps, weight_offset,
+        None if residual_out is None else _here("residual_out", kind, shape, residual_out),
+        None if out is None else _here("out", kind, shape, out), None if out8 is None else _e4m3("out8", out8, shape),
+        None if out8 is None else _here("out8_scale", torch.float32, (rows, _blocks(H)), out8_scale), _stream(stream)),
+        "add_rms_norm")
+
+
+def quantize_e4m3(x, out8, out8_scale, stream=None):
+    """8-bit rows of x [rows, H] (bf16, fp16 or fp32): e4m3 codes and an fp32 scale for every 128 features."""
+    dt, (rows, H) = _row_dtype("x", x), x.shape
+    check(load().tsv_quantize_e4m3(_here("x", x.dtype, x.shape, x), rows, H, dt, _e4m3("out8", out8, x.shape),
+                                   _here("out8_scale", torch.float32, (rows, _blocks(H)), out8_scale), _stream(stream)),
+          "quantize_e4m3")
+
+
+def matmul_e4m3(a, a_scale, w, w_scale, out, stream=None):
+    """out [rows, N] (bf16, fp16 or fp32) = 8-bit rows a [rows, K], a_scale [rows, ceil(K/128)] times e4m3 weights w [N, K],
+    w_scale [ceil(N/128), ceil(K/128)]."""
+    dt = _row_dtype("out", out)
+    (rows, K), N = a.shape, w.shape[0]
+    check(load().tsv_matmul_e4m3(
+        _e4m3("a", a, (rows, K)), _here("a_scale", torch.float32, (rows, _blocks(K)), a_scale), rows, K, _e4m3("w", w, (N, K)),
+        _here("w_scale", torch.float32, (_blocks(N), _blocks(K)), w_scale), N, _here("out", out.dtype, (rows, N), out), dt,
+        _stream(stream)), "matmul_e4m3")
+
+
+def matmul_e4m3_argmax(a, a_scale, w, w_scale, argmax, *, maxval=None, workspace=None, stream=None):
+    """The same product's largest value of every row and its column: argmax int32 [rows], maxval fp32 [rows]."""
+    lib = load()
+    (rows, K), N = a.shape, w.shape[0]
+    if workspace is None:
+        workspace = torch.empty(max(lib.tsv_matmul_e4m3_argmax_workspace_size(rows), 256), dtype=torch.uint8, device=a.device)
+    check(lib.tsv_matmul_e4m3_argmax(
+        _e4m3("a", a, (rows, K)), _here("a_scale", torch.float32, (rows, _blocks(K)), a_scale), rows, K, _e4m3("w", w, (N, K)),
+        _here("w_scale", torch.float32, (_blocks(N), _blocks(K)), w_scale), N, _here("argmax", torch.int32, (rows,), argmax),
+        None if maxval is None else _here("maxval", torch.float32, (rows,), maxval), *_workspace(workspace), _stream(stream)),
+        "matmul_e4m3_argmax")
+
+
+def _workspace(t):
+    return _here("workspace", t.dtype, t.shape, t), t.numel() * t.element_size()
+
+
+def token_logprobs_workspace_size(rows: int, V: int, top_k: int) -> int:
+    return int(load().tsv_token_logprobs_workspace_size(rows, V, top_k))
+
+
+def token_logprobs(logits, targets=None, logp=None, *, rank=None, entropy=None, top_tokens=None, top_logp=None,
+                   temperature=1.0, workspace=None, stream=None):
+    """Of every row of logits [rows, V] (fp32, bf16 or fp16): the target's log probability and rank, the entropy, and the
+    likeliest tokens with their log probabilities.
+
+    targets int32 [rows] with logp fp32 [rows] and, optionally, rank int32 [rows]; entropy fp32 [rows]; top_tokens int32 and
+    top_logp fp32 [rows, k], 1 <= k <= 64.  Each part is optional, one at least is wanted.
+    """
+    dt, (rows, V) = _row_dtype("logits", logits), logits.shape
+    if (top_tokens is None) != (top_logp is None):
+        raise ValueError("top_tokens and top_logp belong together")
+    k = 0 if top_tokens is None else top_tokens.shape[-1]
+    if top_tokens is not None and k == 0:
+        raise ValueError("top_tokens has room for no token")
+    lib = load()
+    if workspace is None:
+        workspace = torch.empty(max(token_logprobs_workspace_size(rows, V, k), 256), dtype=torch.uint8, device=logits.device)
+    vec = lambda name, t, dt: None if t is None else _here(name, dt, (rows,), t)  # noqa: E731
+    check(lib.tsv_token_logprobs(
+        _here("logits", logits.dtype, logits.shape, logits), dt, rows, V, vec("targets", targets, torch.int32), temperature, k,
+        vec("logp", logp, torch.float32), vec("rank", rank, torch.int32), vec("entropy", entropy, torch.float32),
+        None if k == 0 else _here("top_tokens", torch.int32, (rows, k), top_tokens),
+        None if k == 0 else _here("top_logp", torch.float32, (rows, k), top_logp), *_workspace(workspace), _stream(stream)),
+        "token_logprobs")
+
+
 # ----------------------------------------------------------------------------- one verify round
 @dataclass
 class VerifyRound:
@@ -406,6 +539,11 @@ class VerifyRound:
     uniforms: torch.Tensor = None  # fp32 [B * T], one per node
     gdn: dict = None       # recurrent layers (optional): per-layer lists q, k, v, g, beta, state[, state_out] and
                            # gdn_desc's norm_eps and scale; outputs in outs["gdn_o"], states advanced by the round
+    norm: dict = None      # last norm (optional): x [B * T, H], weight, eps and, if wanted, residual, residual_out and
+                           # weight_offset of add_rms_norm; writes hidden (which may be None: a buffer of the round's, or
+                           # 8-bit rows in outs["hidden8"] and outs["hidden8_scale"] ahead of an e4m3 head)
+    logprobs: int = None   # log probabilities (optional): this many likeliest tokens of every node in outs["top_tokens"]
+                           # and outs["top_logp"], the node's own token's in outs["logp"], the entropy in outs["entropy"]
     outs: dict = field(default_factory=dict)
 
     def __post_init__(self):
@@ -440,17 +578,44 @@ class VerifyRound:
             self.gdesc = gdn_desc(o=self.outs["gdn_o"], **self.gdn)
             if (self.gdesc.B, self.gdesc.T) != (B, T) or self.gdesc.packed:
                 raise ValueError("the recurrent layers' inputs must be [B, T, heads, features] of this round")
+        f32 = lambda *s: torch.empty(*s, dtype=torch.float32, device=dev)
+        self.hidden8 = None  # the normed rows in 8 bits, where the norm writes them for an e4m3 head
+        if self.norm is not None:
+            H = self.norm["x"].shape[1]
+            if tuple(self.norm["x"].shape) != (BT, H):
+                raise ValueError(f"norm's x must be [B * T = {BT}, H], got {tuple(self.norm['x'].shape)}")
+            if self.w_dtype == E4M3_B128 and self.hidden is None:
+                self.hidden8 = (torch.empty(BT, H, dtype=torch.float8_e4m3fn, device=dev), f32(BT, _blocks(H)))
+                self.outs["hidden8"], self.outs["hidden8_scale"] = self.hidden8
+            elif self.hidden is None:
+                self.hidden = torch.empty(BT, H, dtype=torch.bfloat16, device=dev)
+        elif self.hidden is None:
+            raise ValueError("hidden is wanted where the round has no norm")
         self.attn_ws = torch.empty(max(attention_workspace_size(self.adesc), 256), dtype=torch.uint8, device=dev)
-        self.lm_ws = torch.empty(max(lm_head_workspace_size(B * T, self.hidden.shape[1], self.V, self.w_dtype), 256),
-                                 dtype=torch.uint8, device=dev)
-        if self.sample is not None:  # the LM stage writes every logit and draws each node's token
-            self.outs["logits"] = torch.empty(B * T, self.V, dtype=torch.float32, device=dev)
+        H = (self.hidden if self.hidden is not None else self.hidden8[0]).shape[1]
+        self.lm_ws = torch.empty(max(lm_head_workspace_size(BT, H, self.V, self.w_dtype), 256), dtype=torch.uint8, device=dev)
+        if self.logprobs is not None:
+            k = int(self.logprobs)
+            self.outs["entropy"] = f32(BT)
+            if self.sample is None:
+                k = max(k, 1)  # the greedy token is the first of them
+            else:
+                self.outs["logp"] = f32(BT)
+            if k > 0:
+                self.outs["top_tokens"], self.outs["top_logp"] = z(BT, k), f32(BT, k)
+            if self.sample is None:
+                self.outs["logp"] = self.outs["top_logp"][:, 0]
+            self.logprobs_ws = torch.empty(max(token_logprobs_workspace_size(BT, self.V, k), 256), dtype=torch.uint8, device=dev)
+        if self.sample is not None or self.logprobs is not None:  # the LM stage writes every logit
+            self.outs["logits"] = f32(BT, self.V)
+        if self.sample is not None:  # and draws each node's token
             self.sample_ws = torch.empty(max(sample_workspace_size(B * T, self.V, int(self.sample[1])), 256),
                                          dtype=torch.uint8, device=dev)
 
-    def run(self, stream=None, stages=("mask", "append", "attn", "gdn", "lm", "walk", "gather", "commit")):
+    def run(self, stream=None, stages=("mask", "append", "attn", "gdn", "norm", "lm", "walk", "gather", "commit")):
         """Issue the round's calls in order; "append" runs only when the round was built with append inputs, "gdn"
-        and "commit" (the recurrent layers and their states) only when it was built with recurrent layers."""
+        and "commit" (the recurrent layers and their states) only when it was built with recurrent layers, "norm" only
+        when it was built with the last norm."""
         o = self.outs
         B, T = self.parents.shape
         if "mask" in stages:
@@ -461,15 +626,11 @@ class VerifyRound:
             tree_verify_attention(self.adesc, self.attn_ws, dev_status=o["status"], stream=stream)
         if "gdn" in stages and self.gdesc is not None:
             gdn_tree_verify(self.gdesc, o["anc"], dev_status=o["status"], stream=stream)
-        if "lm" in stages and self.sample is None:
-            lm_head_argmax(self.hidden, self.W, o["argmax"], w_dtype=self.w_dtype, V=self.V, scales=self.w_scales,
-                           biases=self.w_biases, maxlogit=o["maxlogit"], workspace=self.lm_ws, stream=stream)
-        elif "lm" in stages:  # sampled verification: o["argmax"] receives each node's draw, the walk's input
-            t, k, p = self.sample
-            lm_head_logits(self.hidden, self.W, o["logits"], w_dtype=self.w_dtype, V=self.V, scales=self.w_scales,
-                           biases=self.w_biases, workspace=self.lm_ws, stream=stream)
-            sample_nucleus(o["logits"], self.uniforms, o["argmax"], temperature=t, top_k=k, top_p=p,
-                           workspace=self.sample_ws, stream=stream)
+        if "norm" in stages and self.norm is not None:
+            out8, out8_scale = self.hidden8 if self.hidden8 is not None else (None, None)
+            add_rms_norm(**self.norm, out=self.hidden, out8=out8, out8_scale=out8_scale, stream=stream)
+        if "lm" in stages:
+            self._lm(stream)
         if "walk" in stages:
             tree_accept_walk(o["argmax"].view(B, T), self.tokens, self.parents, o["path"], o["path_len"], o["emitted"],
                              dev_status=o["status"], stream=stream)
@@ -480,7 +641,36 @@ class VerifyRound:
             gdn_commit(self.gdesc, o["path"], o["path_len"], dev_status=o["status"], stream=stream)
         return o
 
-    def capture(self, stages=("mask", "append", "attn", "gdn", "lm", "walk", "gather", "commit")):
+    def _lm(self, stream):
+        """The LM stage: each node's token in outs["argmax"], by the argmax, by a draw, or as the likeliest of its log
+        probabilities."""
+        o = self.outs
+        if self.sample is None and self.logprobs is None:
+            if self.hidden8 is not None:
+                matmul_e4m3_argmax(*self.hidden8, self.W, self.w_scales, o["argmax"], maxval=o["maxlogit"],
+                                   workspace=self.lm_ws, stream=stream)
+            else:
+                lm_head_argmax(self.hidden, self.W, o["argmax"], w_dtype=self.w_dtype, V=self.V, scales=self.w_scales,
+                               biases=self.w_biases, maxlogit=o["maxlogit"], workspace=self.lm_ws, stream=stream)
+            return
+        if self.hidden8 is not None:
+            matmul_e4m3(*self.hidden8, self.W, self.w_scales, o["logits"], stream=stream)
+        else:
+            lm_head_logits(self.hidden, self.W, o["logits"], w_dtype=self.w_dtype, V=self.V, scales=self.w_scales,
+                           biases=self.w_biases, workspace=self.lm_ws, stream=stream)
+        if self.sample is not None:  # o["argmax"] receives each node's draw, the walk's input
+            t, k, p = self.sample
+            sample_nucleus(o["logits"], self.uniforms, o["argmax"], temperature=t, top_k=k, top_p=p,
+                           workspace=self.sample_ws, stream=stream)
+        if self.logprobs is not None:
+            drawn = self.sample is not None
+            token_logprobs(o["logits"], o["argmax"] if drawn else None, o["logp"] if drawn else None, entropy=o["entropy"],
+                           top_tokens=o.get("top_tokens"), top_logp=o.get("top_logp"), workspace=self.logprobs_ws, stream=stream)
+            if not drawn:
+                with torch.cuda.stream(stream):
+                    o["argmax"].copy_(o["top_tokens"][:, 0])
+
+    def capture(self, stages=("mask", "append", "attn", "gdn", "norm", "lm", "walk", "gather", "commit")):
         """Record ``run(stages)`` once as a CUDA graph over this round's buffers.
 
         Every call reads its per-round inputs (parents, tokens, q, hidden, kv_len, ...) from device memory and

@@ -12,7 +12,7 @@
 // hidden row.  Bests are merged with 64-bit atomic maxima on a packed key
 // (orderable fp32 logit << 32 | ~index), so ties go to the lowest index
 // regardless of the order in which CTAs finish.  A last tiny kernel unpacks.
-#include "common.cuh"
+#include "e4m3.cuh"
 
 namespace tsv {
 
@@ -290,17 +290,51 @@ bool lm_tc_applies(int rows, int H, int V, int w_dtype);
 tsv_status launch_lm_tc(const void* hidden, int rows, int H, int V, int w_dtype, const void* W, const void* scales,
                         const void* biases, unsigned long long* best, float* logits, void* extra, cudaStream_t stream);
 static size_t best_bytes(int rows) { return ((size_t)rows * sizeof(unsigned long long) + 255) & ~(size_t)255; }
+
+// The running bests, for the 8-bit product's argmax (matmul_e4m3.cu).
+size_t lm_best_bytes(int rows) { return best_bytes(rows); }
+void launch_lm_best_clear(unsigned long long* best, int rows, cudaStream_t stream) {
+    launch_pdl(lm_zero_best_kernel, std::min((rows + 255) / 256, sm_count()), 256, 0, stream, best, rows);
+}
+tsv_status launch_lm_best_unpack(const char* name, const unsigned long long* best, int rows, int32_t* argmax, float* maxval,
+                                 cudaStream_t stream) {
+    launch_pdl(lm_unpack_kernel, (rows + 127) / 128, 128, 0, stream, best, rows, argmax, maxval);
+    return check_launch(name);
+}
 }  // namespace tsv
 
 extern "C" size_t tsv_lm_head_workspace_size(int32_t rows, int32_t H, int32_t V, int32_t w_dtype) {
     using namespace tsv;
     if (rows < 1 || H < 1 || V < 1) return 0;
     size_t n = best_bytes(rows);
+    if (w_dtype == TSV_E4M3_B128) return n + e4_rows_bytes(rows, H);
     if (lm_tc_applies(rows, H, V, w_dtype)) n += lm_tc_extra_bytes(rows, H, w_dtype);
     return n;
 }
 
 namespace tsv {
+
+// 8-bit heads: hidden becomes 8-bit rows in the workspace, behind the bests; then the 8-bit product.
+static tsv_status lm_head_e4m3(const char* name, const void* hidden, int rows, int H, int V, const void* W, const void* scales,
+                               int32_t* argmax, float* maxlogit, float* logits, void* workspace, size_t ws_bytes,
+                               cudaStream_t stream) {
+    if (H % 16) return fail(TSV_EINVAL, "%s: H=%d not a multiple of 16", name, H);
+    if (!scales) return fail(TSV_EINVAL, "%s: 8-bit head without scales", name);
+    if (((uintptr_t)hidden | (uintptr_t)W | (uintptr_t)workspace) & 15)
+        return fail(TSV_EINVAL, "%s: hidden/W/workspace not 16-byte aligned", name);
+    if ((uintptr_t)scales & 3) return fail(TSV_EINVAL, "%s: scales not 4-byte aligned", name);
+    const size_t need = best_bytes(rows) + e4_rows_bytes(rows, H);
+    if (ws_bytes < need) return fail(TSV_ECAPACITY, "%s: workspace %zu < %zu bytes", name, ws_bytes, need);
+    unsigned long long* best = (unsigned long long*)workspace;
+    char* codes = (char*)workspace + best_bytes(rows);
+    float* code_scale = (float*)(codes + e4_codes_bytes(rows, H));
+    tsv_status st = launch_quantize_e4m3(hidden, rows, H, TSV_BF16, codes, code_scale, stream);
+    if (st != TSV_OK) return st;
+    if (argmax) launch_lm_best_clear(best, rows, stream);
+    const E4Product p = {codes, code_scale, W, (const float*)scales, rows, H, V, logits, TSV_F32, argmax ? best : nullptr};
+    st = launch_matmul_e4m3(name, p, stream);
+    return st != TSV_OK || !argmax ? st : launch_lm_best_unpack(name, best, rows, argmax, maxlogit, stream);
+}
 
 // Shared body of tsv_lm_head_argmax (argmax != NULL) and tsv_lm_head_logits (logits != NULL).
 static tsv_status lm_head_run(const char* name, const void* hidden, int32_t rows, int32_t H, int32_t V,
@@ -308,8 +342,10 @@ static tsv_status lm_head_run(const char* name, const void* hidden, int32_t rows
                               float* maxlogit, float* logits, void* workspace, size_t ws_bytes, cudaStream_t stream) {
     if (rows < 1 || V < 1 || H < 64) return fail(TSV_EINVAL, "%s: rows=%d V=%d H=%d", name, rows, V, H);
     if (!hidden || !W || !(argmax || logits) || !workspace) return fail(TSV_EINVAL, "%s: null pointer argument", name);
+    if (w_dtype == TSV_E4M3_B128)
+        return lm_head_e4m3(name, hidden, rows, H, V, W, scales, argmax, maxlogit, logits, workspace, ws_bytes, stream);
     if (w_dtype != TSV_F16 && w_dtype != TSV_BF16 && w_dtype != TSV_Q4_G64)
-        return fail(TSV_EUNSUPPORTED, "%s: weight format %d (fp16, bf16 or 4-bit group-64 only)", name, w_dtype);
+        return fail(TSV_EUNSUPPORTED, "%s: weight format %d (fp16, bf16, 4-bit group-64 or 8-bit block-128 only)", name, w_dtype);
     if (w_dtype == TSV_Q4_G64) {
         if (H % 64) return fail(TSV_EINVAL, "%s: H=%d not a multiple of the 64-wide group", name, H);
         if (!scales || !biases) return fail(TSV_EINVAL, "%s: 4-bit head without scales/biases", name);
