@@ -31,24 +31,89 @@ struct MmParams {
     int mtiles, ntiles;      // of 128 rows (pairs: 256), of BN weights
     int panel;               // row tiles that are walked together, so that their weights are read from L2
     int stages, stage_bytes, a_bytes;
+    bool vec;                // every 16-byte piece of an output row is aligned
 };
 
 template <int BN, bool PAIR>
 struct MmShape {
     static constexpr int kEpiWarps = BN >= 128 ? 8 : 4;
-    static constexpr int kCols = BN / (kEpiWarps / 4);     // columns of an epilogue thread
-    static constexpr int kBufs = BN == 256 ? 2 : 256 / BN;  // accumulators in TMEM
-    static constexpr int kThreads = (kEpiWarps + 2) * 32;
-    static constexpr int kPerSm = BN >= 128 ? 1 : 2;
-    static constexpr int kSmem = kPerSm == 1 ? 224 * 1024 : 110 * 1024;
+    static constexpr int kCols = BN / (kEpiWarps / 4);  // columns of an epilogue thread
+    static constexpr int kPerSm = BN >= 128 ? 1 : BN == 64 ? 2 : 3;
+    // A tile's columns are kParts MMAs of kPart columns, each with accumulators, barriers, an issuing warp and a warpgroup of its
+    // own: the shorter an accumulator's way round (products, read out, free again), the less the two of TMEM are waited for.
+    static constexpr int kParts = BN == 256 ? 2 : 1, kPart = BN / kParts;
+    static constexpr int kBufs = BN == 256 ? 2 : 4;  // accumulators of a part in TMEM
+    static constexpr int kBox = kPart / (PAIR ? 2 : 1);  // weights of a part in a CTA's shared memory
+    // 256 columns: an epilogue thread holds 128 sums, so the eight epilogue warps take registers over from a third warpgroup
+    // (producer, two issuers, scales): 256 x 208 + 128 x 88 = 384 x 168.  The third warpgroup's scale warp
+    // then reads the scales ahead of the epilogue, which has neither the registers nor the time.
+    static constexpr bool kWide = BN == 256;
+    static constexpr int kThreads = kWide ? 384 : (kEpiWarps + 2) * 32;
+    static constexpr int kScaleBytes = kWide ? 2 * 4 * 2 * 128 * 4 : 0;   // two groups of 4 blocks, two weight blocks, 128 rows
+    static constexpr int kOutBytes = kEpiWarps == 8 ? kEpiWarps * 4096 : 0;  // 32 rows x 128 bytes of output per warp
+    static constexpr int kSmem = (kPerSm == 1 ? 224 : kPerSm == 2 ? 110 : 72) * 1024;
+    static constexpr int kRing = kSmem - 1024 - kScaleBytes - kOutBytes;
 };
 
-// acc += s * d, two fp32 numbers at a time.
-__device__ __forceinline__ void fma2(unsigned long long& acc, uint32_t d0, uint32_t d1, unsigned long long s) {
-    asm("{\n .reg .b64 d;\n mov.b64 d, {%1, %2};\n fma.rn.f32x2 %0, d, %3, %0;\n}" : "+l"(acc) : "r"(d0), "r"(d1), "l"(s));
+__device__ __forceinline__ void sums8(const float* acc, float (&v)[8]) {
+#pragma unroll
+    for (int j = 0; j < 8; ++j) v[j] = acc[j];
 }
-__device__ __forceinline__ float2 unpack2(unsigned long long v) {
-    return make_float2(__uint_as_float((uint32_t)v), __uint_as_float((uint32_t)(v >> 32)));
+
+// A thread's COLS sums to `n` places of its output row.
+template <typename T, int COLS>
+__device__ __forceinline__ void store_row(T* o, const float (&acc)[COLS], int n, bool vec) {
+#pragma unroll
+    for (int c = 0; c < COLS; c += 8) {
+        float v[8];
+        sums8(acc + c, v);
+        if (vec && c + 8 <= n) store8<T, true>(o + c, 8, v);
+        else store8<T, false>(o + c, n - c, v);
+    }
+}
+
+// A warp's 32 rows of COLS sums through its 4 KB of shared memory, 128 bytes of every row at a time, so that a store covers
+// four whole 128-byte pieces (a thread's own row, written by itself, costs a 32-byte sector for every 16 bytes: 10,000 SM
+// clocks for a tile of 128 x 256 bf16, half of what its products take).  `rows`, `n`: what is left of the matrix from o on.
+template <typename T, int COLS>
+__device__ __forceinline__ void store_rows(T* o, const float (&acc)[COLS], size_t ld, int rows, int n, bool vec,
+                                           uint8_t* buf, int lane) {
+    constexpr int P = 128 / sizeof(T), V = 16 / sizeof(T);  // elements of a piece, of a 16-byte vector
+#pragma unroll
+    for (int c = 0; c < COLS; c += P) {
+        if (c >= n) break;
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+            uint4 u;
+            if constexpr (sizeof(T) == 4) {
+                const float* x = acc + c + 4 * j;
+                u = make_uint4(__float_as_uint(x[0]), __float_as_uint(x[1]), __float_as_uint(x[2]), __float_as_uint(x[3]));
+            } else {
+                float v[8];
+                sums8(acc + c + 8 * j, v);
+                u = make_uint4(RowType<T>::pack(v[0], v[1]), RowType<T>::pack(v[2], v[3]), RowType<T>::pack(v[4], v[5]),
+                               RowType<T>::pack(v[6], v[7]));
+            }
+            *reinterpret_cast<uint4*>(buf + lane * 128 + ((j ^ (lane & 7)) << 4)) = u;  // no two of 8 lanes in one bank
+        }
+        __syncwarp();
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            const int r = i * 4 + (lane >> 3), j = lane & 7, at = c + j * V;
+            const uint4 u = *reinterpret_cast<const uint4*>(buf + r * 128 + ((j ^ (r & 7)) << 4));
+            T* to = o + (size_t)r * ld + at;
+            if (r >= rows || at >= n) continue;
+            if (vec && at + V <= n) {
+                *reinterpret_cast<uint4*>(to) = u;
+            } else {
+                const T* from = reinterpret_cast<const T*>(&u);
+#pragma unroll
+                for (int k = 0; k < V; ++k)
+                    if (at + k < n) to[k] = from[k];
+            }
+        }
+        __syncwarp();
+    }
 }
 
 template <int BN, bool PAIR>
@@ -58,12 +123,14 @@ __global__ void __launch_bounds__(MmShape<BN, PAIR>::kThreads, MmShape<BN, PAIR>
     using S = MmShape<BN, PAIR>;
     constexpr int CTAS = PAIR ? 2 : 1;
     extern __shared__ uint8_t smem_raw[];
-    __shared__ uint64_t full[kMmMaxStages], empty[kMmMaxStages], acc_full[S::kBufs], acc_empty[S::kBufs], drain;
+    __shared__ uint64_t full[kMmMaxStages], empty[kMmMaxStages], acc_full[S::kBufs * S::kParts], acc_empty[S::kBufs * S::kParts], sc_full[2], sc_empty[2], drain;
     __shared__ uint32_t tmem_slot;
     __shared__ int abort_word;
     volatile int* abort_flag = &abort_word;
     uint8_t* ring = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
 
+    uint8_t* outbuf = ring + S::kRing;
+    float* scales = reinterpret_cast<float*>(outbuf + S::kOutBytes);
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const uint32_t rank = PAIR ? tc::cluster_rank() : 0;
     const int first = blockIdx.x / CTAS, step = gridDim.x / CTAS, tiles = q.mtiles * q.ntiles;
@@ -71,13 +138,18 @@ __global__ void __launch_bounds__(MmShape<BN, PAIR>::kThreads, MmShape<BN, PAIR>
     if (threadIdx.x == 0) {
         for (int s = 0; s < ST; ++s) {
             tc::mbar_init(&full[s], 1);
-            tc::mbar_init(&empty[s], 1);
+            tc::mbar_init(&empty[s], S::kParts);
         }
-        for (int b = 0; b < S::kBufs; ++b) {
+        for (int b = 0; b < S::kBufs * S::kParts; ++b) {
             tc::mbar_init(&acc_full[b], 1);
-            tc::mbar_init(&acc_empty[b], S::kEpiWarps * CTAS);
+            // of a single row tile, the warps that have rows
+            tc::mbar_init(&acc_empty[b], CTAS * S::kEpiWarps / 4 / S::kParts * (!PAIR && q.mtiles == 1 ? min(4, (q.p.rows + 31) / 32) : 4));
         }
-        tc::mbar_init(&drain, 1);
+        for (int g = 0; g < 2; ++g) {
+            tc::mbar_init(&sc_full[g], 1);
+            tc::mbar_init(&sc_empty[g], S::kEpiWarps);
+        }
+        tc::mbar_init(&drain, S::kParts);
         abort_word = 0;
         tc::fence_mbar_init();
     }
@@ -103,134 +175,185 @@ __global__ void __launch_bounds__(MmShape<BN, PAIR>::kThreads, MmShape<BN, PAIR>
         m = p0 + r - n * wide;
     };
 
-    if (warp == S::kEpiWarps) {
-        // ------------------------------------------------------------ producer
-        if (lane == 0) {
-            tc::tma_prefetch_desc(&q.amap);
-            tc::tma_prefetch_desc(&q.wmap);
+    if (warp >= S::kEpiWarps) {
+        if constexpr (S::kWide) asm volatile("setmaxnreg.dec.sync.aligned.u32 88;");
+        if (warp == S::kEpiWarps) {
+            // -------------------------------------------------------- producer
             int st = 0, issued = 0;
             uint32_t fill = 0;
             bool ok = true;
             for (int t = first; ok && t < tiles; t += step) {
                 int m, n;
                 place(t, m, n);
-                const int arow = (m * CTAS + rank) * kMmRows, wrow = n * BN + rank * (BN / CTAS);
+                const int arow = (m * CTAS + rank) * kMmRows, wrow = n * BN + rank * S::kBox;
                 for (int kb = 0; kb < KB; ++kb) {
-                    if (issued >= ST && !tc::mbar_wait(&empty[st], fill ^ 1u, abort_flag, 256)) { ok = false; break; }
+                    if (issued >= ST && !tc::mbar_wait_warp(&empty[st], fill ^ 1u, abort_flag)) { ok = false; break; }
                     uint8_t* a = ring + (size_t)st * q.stage_bytes;
-                    if constexpr (PAIR) {
-                        const uint32_t bar = tc::cluster_addr(&full[st], 0);
-                        if (rank == 0) tc::mbar_expect_tx(&full[st], 2u * q.stage_bytes);
-                        tc::tma_load_2d_pair(a, &q.amap, bar, kb * kE4Block, arow);
-                        tc::tma_load_2d_pair(a + q.a_bytes, &q.wmap, bar, kb * kE4Block, wrow);
-                    } else {
-                        tc::mbar_expect_tx(&full[st], q.stage_bytes);
-                        tc::tma_load_2d(a, &q.amap, &full[st], kb * kE4Block, arow);
-                        tc::tma_load_2d(a + q.a_bytes, &q.wmap, &full[st], kb * kE4Block, wrow);
-                    }
+                    const uint32_t bar = PAIR ? tc::cluster_addr(&full[st], 0) : tc::smem_u32(&full[st]);
+                    // a pair's bytes, of both CTAs, are expected by its first CTA
+                    tc::mbar_expect_tx_one(&full[st], rank == 0 ? CTAS * q.stage_bytes : 0u);
+                    tc::tma_load_2d_one<PAIR>(a, &q.amap, bar, kb * kE4Block, arow);
+#pragma unroll
+                    for (int h = 0; h < S::kParts; ++h)
+                        tc::tma_load_2d_one<PAIR>(a + q.a_bytes + h * S::kBox * kE4Block, &q.wmap, bar, kb * kE4Block, wrow + h * S::kPart);
                     ++issued;
                     if (++st == ST) { st = 0; fill ^= 1u; }
                 }
             }
             if (*abort_flag && rank == 0)  // let the copies in flight land (bounded) before the CTA goes away
                 for (int i = max(0, issued - ST); i < issued; ++i) tc::mbar_drain(&full[i % ST], (i / ST) & 1);
-        }
-    } else if (warp == S::kEpiWarps + 1) {
-        // ------------------------------------------------------------ MMA issuer (of a pair: its first CTA's)
-        if (lane == 0 && rank == 0) {
-            const uint32_t idesc = tc::idesc_e4m3(kMmRows * CTAS, BN);
+        } else if (warp <= S::kEpiWarps + S::kParts && rank == 0) {
+            // -------------------------------------------------------- MMA issuers (of a pair: its first CTA's)
+            const int h = warp - S::kEpiWarps - 1;
+            const uint32_t idesc = tc::idesc_e4m3(kMmRows * CTAS, S::kPart);
             const uint64_t d0 = tc::sdesc_sw128(tc::smem_u32(ring), 16, 1024);
+            const uint32_t b_off = q.a_bytes + h * S::kBox * kE4Block;
+            uint64_t *part_full = acc_full + h * S::kBufs, *part_empty = acc_empty + h * S::kBufs;
             int st = 0, buf = 0;
             uint32_t ph = 0, use = 0;  // parities of the stage's fill and of the accumulator's use
             bool ok = true, reused = false;
             for (int t = first; ok && t < tiles; t += step) {
                 for (int kb = 0; kb < KB; ++kb) {
-                    if (reused && !tc::mbar_wait_spin(&acc_empty[buf], use ^ 1u, abort_flag)) { ok = false; break; }
-                    if (!tc::mbar_wait_spin(&full[st], ph, abort_flag)) { ok = false; break; }
+                    if (reused && !tc::mbar_wait_warp(&part_empty[buf], use ^ 1u, abort_flag)) { ok = false; break; }
+                    if (!tc::mbar_wait_warp(&full[st], ph, abort_flag)) { ok = false; break; }
                     tc::tc_fence_after();
-                    const uint64_t da = tc::sdesc_add(d0, (uint32_t)st * q.stage_bytes), db = tc::sdesc_add(da, q.a_bytes);
-#pragma unroll
-                    for (int k = 0; k < kE4Block / 32; ++k)
-                        tc::mma_e4m3<PAIR>(tmem + buf * BN, tc::sdesc_add(da, k * 32), tc::sdesc_add(db, k * 32), idesc, k > 0);
-                    if constexpr (PAIR) {
-                        tc::mma_commit_pair(&empty[st]);
-                        tc::mma_commit_pair(&acc_full[buf]);
-                    } else {
-                        tc::mma_commit(&empty[st]);
-                        tc::mma_commit(&acc_full[buf]);
-                    }
+                    const uint64_t da = tc::sdesc_add(d0, (uint32_t)st * q.stage_bytes), db = tc::sdesc_add(da, b_off);
+                    tc::mma_e4m3_block<PAIR>(tmem + buf * BN + h * S::kPart, da, db, idesc, &empty[st], &part_full[buf]);
                     if (++st == ST) { st = 0; ph ^= 1u; }
                     if (++buf == S::kBufs) { buf = 0; use ^= 1u; reused = true; }
                 }
             }
-            if constexpr (PAIR) tc::mma_commit_pair(&drain);
-            else tc::mma_commit(&drain);
+            tc::mma_commit_elect<PAIR>(&drain);
             tc::mbar_drain(&drain, 0);
+        } else if (S::kWide && warp == S::kEpiWarps + 3) {
+            // -------------------------------------------------------- scales: a_scale w_scale of 128 rows, two weight blocks, 4 blocks
+            const E4Product& p = q.p;
+            const int wlast = e4_blocks(p.N) - 1;
+            int g = 0, groups = 0;
+            uint32_t use = 0;
+            bool ok = true;
+            for (int t = first; ok && t < tiles; t += step) {
+                int m, n;
+                place(t, m, n);
+                const int row0 = (m * CTAS + rank) * kMmRows + lane;
+                const float* w0 = p.w_scale + (size_t)min(n * 2, wlast) * KB;
+                const float* w1 = p.w_scale + (size_t)min(n * 2 + 1, wlast) * KB;
+                for (int kb = 0; kb < KB; kb += 4) {
+                    float a[4][4], w[2][4];
+#pragma unroll
+                    for (int r = 0; r < 4; ++r) {
+                        const float* as = p.a_scale + (size_t)min(row0 + r * 32, p.rows - 1) * KB + kb;
+#pragma unroll
+                        for (int k = 0; k < 4; ++k) a[r][k] = kb + k < KB ? __ldg(as + k) : 0.f;
+                    }
+#pragma unroll
+                    for (int k = 0; k < 4; ++k) {
+                        w[0][k] = kb + k < KB ? __ldg(w0 + kb + k) : 0.f;
+                        w[1][k] = kb + k < KB ? __ldg(w1 + kb + k) : 0.f;
+                    }
+                    if (groups >= 2 && !tc::mbar_wait_warp(&sc_empty[g], use ^ 1u, abort_flag)) { ok = false; break; }
+                    float* to = scales + g * 4 * 256 + lane;
+#pragma unroll
+                    for (int k = 0; k < 4; ++k)
+#pragma unroll
+                        for (int r = 0; r < 4; ++r) {
+                            to[k * 256 + r * 32] = a[r][k] * w[0][k];
+                            to[k * 256 + 128 + r * 32] = a[r][k] * w[1][k];
+                        }
+                    __syncwarp();
+                    tc::mbar_arrive_one(&sc_full[g]);
+                    ++groups;
+                    if (++g == 2) { g = 0; use ^= 1u; }
+                }
+            }
         }
     } else {
+        if constexpr (S::kWide) asm volatile("setmaxnreg.inc.sync.aligned.u32 208;");
         // ------------------------------------------------------------ epilogue: scale and add up, then write out
         const int quarter = warp & 3, half = warp >> 2;
         const uint32_t taddr = tmem + ((uint32_t)(quarter * 32) << 16) + half * S::kCols;
-        const uint32_t bar0 = tc::cluster_addr(&acc_empty[0], 0);
+        const uint32_t part = (S::kParts > 1 ? half * S::kBufs : 0) * 8;
+        const uint32_t full0 = tc::smem_u32(acc_full) + part, empty0 = PAIR ? tc::cluster_addr(acc_empty, 0) + part : tc::smem_u32(acc_empty) + part;
+        const uint32_t sc0 = tc::smem_u32(scales) + (half * 128 + quarter * 32 + lane) * 4;
         const E4Product& p = q.p;
-        int buf = 0;
-        uint32_t use = 0;
+        int buf = 0, g = 0;
+        uint32_t use = 0, gph = 0;
         bool ok = true;
-        for (int t = first; ok && t < tiles; t += step) {
+        // a warp without rows has no part in a single row tile's barriers
+        for (int t = !PAIR && q.mtiles == 1 && quarter * 32 >= p.rows ? tiles : first; ok && t < tiles; t += step) {
             int m, n;
             place(t, m, n);
-            const int row = (m * CTAS + rank) * kMmRows + quarter * 32 + lane, col = n * BN + half * S::kCols;
-            const bool live = row < p.rows;
-            const float* as = p.a_scale + (size_t)(live ? row : 0) * KB;
+            const int row0 = (m * CTAS + rank) * kMmRows + quarter * 32, row = row0 + lane, col = n * BN + half * S::kCols;
+            float acc[S::kCols];
+#pragma unroll
+            for (int c = 0; c < S::kCols; ++c) acc[c] = 0.f;
+            const float* as = p.a_scale + (size_t)min(row, p.rows - 1) * KB;
             const float* ws = p.w_scale + (size_t)(min(col, p.N - 1) / kE4Block) * KB;
-            unsigned long long acc[S::kCols / 2];
+            float sa = 0.f, sw = 0.f;
+            if constexpr (!S::kWide) sa = __ldg(as), sw = __ldg(ws);
+            // 16 columns are on their way out of TMEM while the 16 before them are added up, from one block to the next
+            uint32_t d[2][16];
+            ok = tc::mbar_wait_warp(full0 + buf * 8, use, abort_flag);
+            tc::tc_fence_after();
+            if (ok) tc::tmem_ld16(taddr + buf * BN, d[0]);
+            for (int kb = 0; ok && kb < KB; ++kb) {
+                float sc;
+                if constexpr (S::kWide) {
+                    if ((kb & 3) == 0) ok = tc::mbar_wait_warp(tc::smem_u32(&sc_full[g]), gph, abort_flag);
+                    asm volatile("ld.shared.f32 %0, [%1];" : "=f"(sc) : "r"(sc0 + (g * 4 + (kb & 3)) * 1024));
+                } else {
+                    sc = sa * sw;
+                    if (kb + 1 < KB) sa = __ldg(as + kb + 1), sw = __ldg(ws + kb + 1);
+                }
 #pragma unroll
-            for (int c = 0; c < S::kCols / 2; ++c) acc[c] = 0ull;
-            float sa = __ldg(as), sw = __ldg(ws);
-            for (int kb = 0; kb < KB; ++kb) {
-                const float sc = sa * sw;
-                const unsigned long long s2 = (unsigned long long)__float_as_uint(sc) << 32 | __float_as_uint(sc);
-                if (kb + 1 < KB) sa = __ldg(as + kb + 1), sw = __ldg(ws + kb + 1);
-                if (!__all_sync(0xFFFFFFFFu, tc::mbar_wait(&acc_full[buf], use, abort_flag))) { ok = false; break; }
-                tc::tc_fence_after();
-#pragma unroll
-                for (int c0 = 0; c0 < S::kCols; c0 += 32) {
-                    uint32_t d[32];
-                    tc::tmem_ld32(taddr + buf * BN + c0, d);
-                    tc::tmem_wait_ld();
-                    if (c0 + 32 == S::kCols) {
+                for (int c = 0; c < S::kCols / 16; ++c) {
+                    uint32_t(&now)[16] = d[c & 1];
+                    tc::tmem_wait_ld16(now);
+                    if (c + 1 < S::kCols / 16) {
+                        tc::tmem_ld16(taddr + buf * BN + (c + 1) * 16, d[(c + 1) & 1]);
+                    } else {
                         tc::tc_fence_before();
                         __syncwarp();
-                        if constexpr (PAIR) tc::mbar_arrive_one_cluster(bar0 + buf * 8);
-                        else tc::mbar_arrive_one(&acc_empty[buf]);
+                        if constexpr (PAIR) tc::mbar_arrive_one_cluster(empty0 + buf * 8);
+                        else tc::mbar_arrive_one(empty0 + buf * 8);
+                        if (++buf == S::kBufs) { buf = 0; use ^= 1u; }
+                        if (kb + 1 < KB) {
+                            ok = ok && tc::mbar_wait_warp(full0 + buf * 8, use, abort_flag);
+                            tc::tc_fence_after();
+                            tc::tmem_ld16(taddr + buf * BN, d[0]);
+                        }
                     }
 #pragma unroll
-                    for (int c = 0; c < 32; c += 2) fma2(acc[(c0 + c) / 2], d[c], d[c + 1], s2);
+                    for (int i = 0; i < 16; ++i) acc[c * 16 + i] = fmaf(sc, __uint_as_float(now[i]), acc[c * 16 + i]);
                 }
-                if (++buf == S::kBufs) { buf = 0; use ^= 1u; }
+                if (S::kWide && ((kb & 3) == 3 || kb + 1 == KB)) {
+                    __syncwarp();
+                    tc::mbar_arrive_one(&sc_empty[g]);
+                    if (++g == 2) { g = 0; gph ^= 1u; }
+                }
             }
-            if (!ok || !live) continue;
+            tc::tmem_wait_ld();
+            if (!ok || row0 >= p.rows || col >= p.N) continue;
             if (p.best) {
                 float best = 0.f;
                 int at = -1;
 #pragma unroll
                 for (int c = 0; c < S::kCols; ++c) {
-                    const float2 v2 = unpack2(acc[c / 2]);
-                    const float v = c & 1 ? v2.y : v2.x;
-                    if (col + c < p.N && (at < 0 || orderable(v) > orderable(best))) best = v, at = col + c;
+                    if (col + c < p.N && (at < 0 || orderable(acc[c]) > orderable(best))) best = acc[c], at = col + c;
                 }
-                if (at >= 0) atomicMax(&p.best[row], pack_best(best, (uint32_t)at));
-            } else {
-#pragma unroll
-                for (int c = 0; c < S::kCols; ++c) {
-                    const float2 v2 = unpack2(acc[c / 2]);
-                    const float v = c & 1 ? v2.y : v2.x;
-                    const size_t o = (size_t)row * p.N + col + c;
-                    if (col + c >= p.N) continue;
-                    if (p.out_dtype == TSV_F32) ((float*)p.out)[o] = v;
-                    else if (p.out_dtype == TSV_BF16) ((__nv_bfloat16*)p.out)[o] = __float2bfloat16_rn(v);
-                    else ((__half*)p.out)[o] = __float2half_rn(v);
-                }
+                if (row < p.rows) atomicMax(&p.best[row], pack_best(best, (uint32_t)at));
+            } else if constexpr (S::kOutBytes > 0) {
+                uint8_t* buf4k = outbuf + warp * 4096;
+                const size_t o = (size_t)row0 * p.N + col;
+                const int rows = p.rows - row0, cols = p.N - col;
+                if (p.out_dtype == TSV_F32) store_rows<float, S::kCols>((float*)p.out + o, acc, p.N, rows, cols, q.vec, buf4k, lane);
+                else if (p.out_dtype == TSV_BF16) store_rows<__nv_bfloat16, S::kCols>((__nv_bfloat16*)p.out + o, acc, p.N, rows, cols, q.vec, buf4k, lane);
+                else store_rows<__half, S::kCols>((__half*)p.out + o, acc, p.N, rows, cols, q.vec, buf4k, lane);
+            } else if (row < p.rows) {
+                const size_t o = (size_t)row * p.N + col;
+                if (p.out_dtype == TSV_F32) store_row<float, S::kCols>((float*)p.out + o, acc, p.N - col, q.vec);
+                else if (p.out_dtype == TSV_BF16) store_row<__nv_bfloat16, S::kCols>((__nv_bfloat16*)p.out + o, acc, p.N - col, q.vec);
+                else store_row<__half, S::kCols>((__half*)p.out + o, acc, p.N - col, q.vec);
             }
         }
     }
@@ -286,14 +409,15 @@ static tsv_status launch_mm(const char* name, const E4Product& p, cudaStream_t s
     q.panel = std::min(q.mtiles, 8);
     // rows of a in shared memory: as many as there are, in whole swizzle atoms of 8.  The MMA reads 128 rows, so a stage's
     // weights, or the next stage's bytes, stand in for missing ones and end in accumulator rows that nothing reads.
-    const int arows = std::min(kMmRows, (p.rows + 7) / 8 * 8), wrows = BN / CTAS;
+    const int arows = std::min(kMmRows, (p.rows + 7) / 8 * 8);
     q.a_bytes = arows * kE4Block;
-    q.stage_bytes = q.a_bytes + wrows * kE4Block;
+    q.stage_bytes = q.a_bytes + S::kParts * S::kBox * kE4Block;
     // the last stage's 128 rows have to end inside the ring as well
     const int slack = std::max(0, kMmRows * kE4Block - q.stage_bytes);
-    q.stages = std::min((int)kMmMaxStages, (S::kSmem - 1024 - slack) / q.stage_bytes);
-    if (!mm_map(&q.amap, p.a, p.rows, p.K, arows) || !mm_map(&q.wmap, p.w, p.N, p.K, wrows))
+    q.stages = std::min((int)kMmMaxStages, (S::kRing - slack) / q.stage_bytes);
+    if (!mm_map(&q.amap, p.a, p.rows, p.K, arows) || !mm_map(&q.wmap, p.w, p.N, p.K, S::kBox))
         return fail(TSV_ECUDA, "%s: tensor map encoding failed", name);
+    q.vec = ((uintptr_t)p.out & 15) == 0 && p.N % (p.out_dtype == TSV_F32 ? 4 : 8) == 0;
     const long long tiles = (long long)q.mtiles * q.ntiles;
     if (tiles > INT_MAX / 2) return fail(TSV_ECAPACITY, "%s: %lld tiles", name, tiles);
     const int places = sm_count() * S::kPerSm / CTAS;
@@ -306,7 +430,6 @@ static tsv_status launch_mm(const char* name, const E4Product& p, cudaStream_t s
 tsv_status launch_matmul_e4m3(const char* name, const E4Product& p, cudaStream_t stream) {
     if (p.rows > kMmRows && (long long)p.N * p.rows >= 256ll * 256 * 76) return launch_mm<256, true>(name, p, stream);
     const long long mt = (p.rows + kMmRows - 1) / kMmRows;
-    if (mt * p.N >= 256ll * sm_count() && p.rows > kMmRows) return launch_mm<256, false>(name, p, stream);
     if (mt * p.N >= 128ll * sm_count() && p.rows > 64) return launch_mm<128, false>(name, p, stream);
     if (mt * p.N >= 64ll * sm_count()) return launch_mm<64, false>(name, p, stream);
     return launch_mm<32, false>(name, p, stream);

@@ -28,14 +28,23 @@ __device__ __forceinline__ void mbar_arrive(uint64_t* bar) {
 }
 // One lane of the converged warp arrives: elect.sync plus a predicated arrive, so no divergent branch (whose
 // reconvergence costs the warp issue slots) is taken.
-__device__ __forceinline__ void mbar_arrive_one(uint64_t* bar) {
+__device__ __forceinline__ void mbar_arrive_one(uint32_t bar) {
     asm volatile(
-        "{\n .reg .pred p;\n elect.sync _|p, 0xffffffff;\n @p mbarrier.arrive.shared::cta.b64 _, [%0];\n}" ::"r"(
-            smem_u32(bar))
+        "{\n .reg .pred p;\n elect.sync _|p, 0xffffffff;\n @p mbarrier.arrive.shared::cta.b64 _, [%0];\n}" ::"r"(bar)
         : "memory");
 }
+__device__ __forceinline__ void mbar_arrive_one(uint64_t* bar) { mbar_arrive_one(smem_u32(bar)); }
 __device__ __forceinline__ void mbar_expect_tx(uint64_t* bar, uint32_t bytes) {
     asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;" ::"r"(smem_u32(bar)), "r"(bytes) : "memory");
+}
+__device__ __forceinline__ bool mbar_try_wait(uint32_t bar, uint32_t parity) {  // by its shared-memory address
+    uint32_t ok;
+    asm volatile(
+        "{\n .reg .pred p;\n mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n selp.u32 %0, 1, 0, p;\n}"
+        : "=r"(ok)
+        : "r"(bar), "r"(parity)
+        : "memory");
+    return ok != 0;
 }
 __device__ __forceinline__ bool mbar_try_wait(uint64_t* bar, uint32_t parity) {
     uint32_t ok;
@@ -113,6 +122,25 @@ __device__ __forceinline__ bool mbar_wait_spin(uint64_t* bar, uint32_t parity, v
     }
 }
 
+// A converged warp's wait on a hand-off that takes some hundred clocks: suspending tests with a vote, which keeps the loop free of
+// divergence (the same loop written with branches on each lane's own result takes three times as long), the timer and the abort
+// flag only after 1024 of them.  True in every lane, or false in every lane.
+__device__ __forceinline__ bool mbar_wait_warp(uint32_t bar, uint32_t parity, volatile int* abort) {
+    uint64_t t0 = 0;
+    for (uint32_t i = 1;; ++i) {
+        if (__all_sync(0xFFFFFFFFu, mbar_try_wait(bar, parity))) return true;
+        if ((i & 1023) == 0) {
+            const uint64_t t = globaltimer();
+            if (t0 == 0) t0 = t;
+            if (t - t0 > kWaitNs) *abort = 1;
+            if (__any_sync(0xFFFFFFFFu, *abort != 0)) return false;
+        }
+    }
+}
+__device__ __forceinline__ bool mbar_wait_warp(uint64_t* bar, uint32_t parity, volatile int* abort) {
+    return mbar_wait_warp(smem_u32(bar), parity, abort);
+}
+
 // ---------------------------------------------------------------- CTA pairs and clusters
 __device__ __forceinline__ uint32_t cluster_rank() {
     uint32_t r;
@@ -128,10 +156,11 @@ __device__ __forceinline__ uint32_t cluster_addr(const void* p, uint32_t rank) {
     asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(smem_u32(p)), "r"(rank));
     return r;
 }
-// One lane of the converged warp arrives on a barrier anywhere in the cluster.
+// One lane of the converged warp arrives on a barrier anywhere in the cluster.  Relaxed: what it tells of is TMEM reads that have
+// ended, no memory (a release would wait for every store under way, microseconds per arrival).
 __device__ __forceinline__ void mbar_arrive_one_cluster(uint32_t bar) {
     asm volatile(
-        "{\n .reg .pred p;\n elect.sync _|p, 0xffffffff;\n @p mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];\n}" ::"r"(
+        "{\n .reg .pred p;\n elect.sync _|p, 0xffffffff;\n @p mbarrier.arrive.relaxed.cluster.shared::cluster.b64 _, [%0];\n}" ::"r"(
             bar)
         : "memory");
 }
@@ -151,13 +180,32 @@ __device__ __forceinline__ void tma_load_2d(void* dst, const CUtensorMap* m, uin
         : "memory");
 }
 
-// The same into this CTA's shared memory, completing on a barrier of either CTA of the pair (`bar`: its cluster address).
-__device__ __forceinline__ void tma_load_2d_pair(void* dst, const CUtensorMap* m, uint32_t bar, int c0, int c1) {
+// One lane of a converged warp expects `bytes` (if not 0) on `bar`.
+__device__ __forceinline__ void mbar_expect_tx_one(uint64_t* bar, uint32_t bytes) {
     asm volatile(
-        "cp.async.bulk.tensor.2d.cta_group::2.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%3, %4}], "
-        "[%2];" ::"r"(smem_u32(dst)),
-        "l"((uint64_t)m), "r"(bar), "r"(c0), "r"(c1)
+        "{\n .reg .pred e;\n elect.sync _|e, 0xffffffff;\n setp.ne.and.u32 e, %1, 0, e;\n"
+        " @e mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;\n}" ::"r"(smem_u32(bar)),
+        "r"(bytes)
         : "memory");
+}
+// tma_load_2d by one lane of a converged warp.  PAIR: completing on a barrier of either CTA of the pair; `bar` is its cluster
+// address there, its own address otherwise.
+template <bool PAIR>
+__device__ __forceinline__ void tma_load_2d_one(void* dst, const CUtensorMap* m, uint32_t bar, int c0, int c1) {
+    if constexpr (PAIR)
+        asm volatile(
+            "{\n .reg .pred e;\n elect.sync _|e, 0xffffffff;\n"
+            " @e cp.async.bulk.tensor.2d.cta_group::2.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%3, %4}], [%2];\n"
+            "}" ::"r"(smem_u32(dst)),
+            "l"((uint64_t)m), "r"(bar), "r"(c0), "r"(c1)
+            : "memory");
+    else
+        asm volatile(
+            "{\n .reg .pred e;\n elect.sync _|e, 0xffffffff;\n"
+            " @e cp.async.bulk.tensor.2d.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%3, %4}], [%2];\n"
+            "}" ::"r"(smem_u32(dst)),
+            "l"((uint64_t)m), "r"(bar), "r"(c0), "r"(c1)
+            : "memory");
 }
 
 // 2^x by the SFU (approximate, flushes subnormal results to zero; 2^-inf = 0).
@@ -226,29 +274,60 @@ __host__ __device__ constexpr uint32_t idesc_e4m3(int M, int N) {
     return (1u << 4) | ((uint32_t)(N >> 3) << 17) | ((uint32_t)(M >> 4) << 24);
 }
 
-// D[tmem] (+)= A[smem] x B[smem] over 32 e4m3 features; issued by one thread.  PAIR: by the pair's first CTA, for 256 rows of A
-// (128 from each CTA's shared memory) and N rows of B (half from each), into both CTAs' TMEM.
+// D[tmem] = A[smem] x B[smem] over a block of 128 e4m3 features (four MMAs of 32, 128-byte swizzled rows), then arrivals on
+// free_bar and done_bar once they are through; issued by one lane of a converged warp, which keeps the operands uniform.  PAIR: by
+// the pair's first CTA, for 256 rows of A (128 from each CTA's shared memory) and N rows of B (half from each), into both CTAs'
+// TMEM; the arrivals reach both CTAs' copies of the barriers.
 template <bool PAIR>
-__device__ __forceinline__ void mma_e4m3(uint32_t d_tmem, uint64_t a, uint64_t b, uint32_t idesc, uint32_t accumulate) {
+__device__ __forceinline__ void mma_e4m3_block(uint32_t d_tmem, uint64_t a, uint64_t b, uint32_t idesc, uint64_t* free_bar,
+                                               uint64_t* done_bar) {
+    if constexpr (PAIR) {
+        asm volatile(
+            "{\n .reg .pred e, n, y;\n .reg .b64 a1, a2, a3, b1, b2, b3;\n elect.sync _|e, 0xffffffff;\n"
+            " setp.ne.u32 n, 0, 0;\n setp.eq.u32 y, 0, 0;\n"
+ "add.s64 a1, %1, 2;\n add.s64 b1, %2, 2;\n"
+ "add.s64 a2, %1, 4;\n add.s64 b2, %2, 4;\n"
+ "add.s64 a3, %1, 6;\n add.s64 b3, %2, 6;\n"
+ "@e tcgen05.mma.cta_group::2.kind::f8f6f4 [%0], %1, %2, %3, n;\n"
+ "@e tcgen05.mma.cta_group::2.kind::f8f6f4 [%0], a1, b1, %3, y;\n"
+ "@e tcgen05.mma.cta_group::2.kind::f8f6f4 [%0], a2, b2, %3, y;\n"
+ "@e tcgen05.mma.cta_group::2.kind::f8f6f4 [%0], a3, b3, %3, y;\n"
+            " @e tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%4], %6;\n"
+            " @e tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%5], %6;\n}" ::"r"(d_tmem),
+            "l"(a), "l"(b), "r"(idesc), "r"(smem_u32(free_bar)), "r"(smem_u32(done_bar)), "h"((uint16_t)3)
+            : "memory");
+    } else {
+        asm volatile(
+            "{\n .reg .pred e, n, y;\n .reg .b64 a1, a2, a3, b1, b2, b3;\n elect.sync _|e, 0xffffffff;\n"
+            " setp.ne.u32 n, 0, 0;\n setp.eq.u32 y, 0, 0;\n"
+ "add.s64 a1, %1, 2;\n add.s64 b1, %2, 2;\n"
+ "add.s64 a2, %1, 4;\n add.s64 b2, %2, 4;\n"
+ "add.s64 a3, %1, 6;\n add.s64 b3, %2, 6;\n"
+ "@e tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], %1, %2, %3, n;\n"
+ "@e tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], a1, b1, %3, y;\n"
+ "@e tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], a2, b2, %3, y;\n"
+ "@e tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], a3, b3, %3, y;\n"
+            " @e tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%4];\n"
+            " @e tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%5];\n}" ::"r"(d_tmem),
+            "l"(a), "l"(b), "r"(idesc), "r"(smem_u32(free_bar)), "r"(smem_u32(done_bar))
+            : "memory");
+    }
+}
+// An arrival on `bar` (PAIR: on both CTAs' copies) once every mma_e4m3_block of this warp is through.
+template <bool PAIR>
+__device__ __forceinline__ void mma_commit_elect(uint64_t* bar) {
     if constexpr (PAIR)
         asm volatile(
-            "{\n .reg .pred p;\n setp.ne.b32 p, %4, 0;\n tcgen05.mma.cta_group::2.kind::f8f6f4 [%0], %1, %2, %3, p;\n}" ::"r"(
-                d_tmem),
-            "l"(a), "l"(b), "r"(idesc), "r"(accumulate)
+            "{\n .reg .pred e;\n elect.sync _|e, 0xffffffff;\n"
+            " @e tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;\n}" ::"r"(
+                smem_u32(bar)),
+            "h"((uint16_t)3)
             : "memory");
     else
         asm volatile(
-            "{\n .reg .pred p;\n setp.ne.b32 p, %4, 0;\n tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], %1, %2, %3, p;\n}" ::"r"(
-                d_tmem),
-            "l"(a), "l"(b), "r"(idesc), "r"(accumulate)
+            "{\n .reg .pred e;\n elect.sync _|e, 0xffffffff;\n"
+            " @e tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n}" ::"r"(smem_u32(bar))
             : "memory");
-}
-// mma_commit for a pair's MMAs: arrives on both CTAs' copies of `bar`.
-__device__ __forceinline__ void mma_commit_pair(uint64_t* bar) {
-    asm volatile(
-        "tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;" ::"r"(smem_u32(bar)),
-        "h"((uint16_t)3)
-        : "memory");
 }
 
 // D[tmem] (+)= A[smem] x B[smem]; issued by one thread.
@@ -311,6 +390,15 @@ __device__ __forceinline__ void tmem_ld16(uint32_t taddr, uint32_t (&r)[16]) {
                  : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]),
                    "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
                  : "r"(taddr));
+}
+
+// tmem_wait_ld for a load that another may follow before its values are used: the values pass through the wait, so no use
+// of them moves ahead of it.
+__device__ __forceinline__ void tmem_wait_ld16(uint32_t (&r)[16]) {
+    asm volatile("tcgen05.wait::ld.sync.aligned;"
+                 : "+r"(r[0]), "+r"(r[1]), "+r"(r[2]), "+r"(r[3]), "+r"(r[4]), "+r"(r[5]), "+r"(r[6]), "+r"(r[7]),
+                   "+r"(r[8]), "+r"(r[9]), "+r"(r[10]), "+r"(r[11]), "+r"(r[12]), "+r"(r[13]), "+r"(r[14]), "+r"(r[15])
+                 :: "memory");
 }
 
 __device__ __forceinline__ void tmem_st32(uint32_t taddr, const uint32_t (&r)[32]) {
