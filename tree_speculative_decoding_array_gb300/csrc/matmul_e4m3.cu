@@ -31,6 +31,7 @@ struct MmParams {
     int mtiles, ntiles;      // of 128 rows (pairs: 256), of BN weights
     int panel;               // row tiles that are walked together, so that their weights are read from L2
     int stages, stage_bytes, a_bytes;
+    int split;               // CTAs of a cluster that share a tile's blocks (1: none; more: one tile per cluster)
     bool vec;                // every 16-byte piece of an output row is aligned
 };
 
@@ -38,20 +39,22 @@ template <int BN, bool PAIR>
 struct MmShape {
     static constexpr int kEpiWarps = BN >= 128 ? 8 : 4;
     static constexpr int kCols = BN / (kEpiWarps / 4);  // columns of an epilogue thread
-    static constexpr int kPerSm = BN >= 128 ? 1 : BN == 64 ? 2 : 3;
+    static constexpr int kPerSm = BN >= 128 ? 1 : 3;
     // A tile's columns are kParts MMAs of kPart columns, each with accumulators, barriers, an issuing warp and a warpgroup of its
     // own: the shorter an accumulator's way round (products, read out, free again), the less the two of TMEM are waited for.
     static constexpr int kParts = BN == 256 ? 2 : 1, kPart = BN / kParts;
-    static constexpr int kBufs = BN == 256 ? 2 : 4;  // accumulators of a part in TMEM
+    static constexpr int kBufs = BN == 128 ? 4 : 2;  // accumulators of a part in TMEM
     static constexpr int kBox = kPart / (PAIR ? 2 : 1);  // weights of a part in a CTA's shared memory
     // 256 columns: an epilogue thread holds 128 sums, so the eight epilogue warps take registers over from a third warpgroup
     // (producer, two issuers, scales): 256 x 208 + 128 x 88 = 384 x 168.  The third warpgroup's scale warp
     // then reads the scales ahead of the epilogue, which has neither the registers nor the time.
     static constexpr bool kWide = BN == 256;
-    static constexpr int kThreads = kWide ? 384 : (kEpiWarps + 2) * 32;
+    static constexpr int kIssuers = BN >= 128 ? 2 : 1;
+    static constexpr int kThreads = kWide ? 384 : (kEpiWarps + 1 + kIssuers) * 32;
     static constexpr int kScaleBytes = kWide ? 2 * 4 * 2 * 128 * 4 : 0;   // two groups of 4 blocks, two weight blocks, 128 rows
     static constexpr int kOutBytes = kEpiWarps == 8 ? kEpiWarps * 4096 : 0;  // 32 rows x 128 bytes of output per warp
-    static constexpr int kSmem = (kPerSm == 1 ? 224 : kPerSm == 2 ? 110 : 72) * 1024;
+    static constexpr bool kAhead = kPerSm == 1;
+    static constexpr int kSmem = (kPerSm == 1 ? 224 : 72) * 1024;
     static constexpr int kRing = kSmem - 1024 - kScaleBytes - kOutBytes;
 };
 
@@ -97,20 +100,19 @@ __device__ __forceinline__ void store_rows(T* o, const float (&acc)[COLS], size_
             *reinterpret_cast<uint4*>(buf + lane * 128 + ((j ^ (lane & 7)) << 4)) = u;  // no two of 8 lanes in one bank
         }
         __syncwarp();
+        if (vec) {
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
-            const int r = i * 4 + (lane >> 3), j = lane & 7, at = c + j * V;
-            const uint4 u = *reinterpret_cast<const uint4*>(buf + r * 128 + ((j ^ (r & 7)) << 4));
-            T* to = o + (size_t)r * ld + at;
-            if (r >= rows || at >= n) continue;
-            if (vec && at + V <= n) {
-                *reinterpret_cast<uint4*>(to) = u;
-            } else {
-                const T* from = reinterpret_cast<const T*>(&u);
-#pragma unroll
-                for (int k = 0; k < V; ++k)
-                    if (at + k < n) to[k] = from[k];
+            for (int i = 0; i < 8; ++i) {
+                const int r = i * 4 + (lane >> 3), j = lane & 7, at = c + j * V;
+                const uint4 u = *reinterpret_cast<const uint4*>(buf + r * 128 + ((j ^ (r & 7)) << 4));
+                if (r < rows && at < n) *reinterpret_cast<uint4*>(o + (size_t)r * ld + at) = u;  // n is a multiple of V
             }
+        } else {  // rows at any address: neighbouring lanes write neighbouring elements
+            for (int r = 0; r < min(rows, 32); ++r)
+#pragma unroll
+                for (int k = lane; k < P; k += 32)
+                    if (c + k < n)
+                        o[(size_t)r * ld + c + k] = *reinterpret_cast<const T*>(buf + r * 128 + (((k / V) ^ (r & 7)) << 4) + k % V * sizeof(T));
         }
         __syncwarp();
     }
@@ -133,8 +135,10 @@ __global__ void __launch_bounds__(MmShape<BN, PAIR>::kThreads, MmShape<BN, PAIR>
     float* scales = reinterpret_cast<float*>(outbuf + S::kOutBytes);
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const uint32_t rank = PAIR ? tc::cluster_rank() : 0;
-    const int first = blockIdx.x / CTAS, step = gridDim.x / CTAS, tiles = q.mtiles * q.ntiles;
+    const int split = PAIR ? 1 : q.split, share = split > 1 ? (int)tc::cluster_rank() : 0;
+    const int first = blockIdx.x / (CTAS * split), step = gridDim.x / (CTAS * split), tiles = q.mtiles * q.ntiles;
     const int KB = q.blocks, ST = q.stages;
+    const int k0 = (int)((long long)KB * share / split), k1 = (int)((long long)KB * (share + 1) / split);  // this CTA's blocks
     if (threadIdx.x == 0) {
         for (int s = 0; s < ST; ++s) {
             tc::mbar_init(&full[s], 1);
@@ -149,7 +153,7 @@ __global__ void __launch_bounds__(MmShape<BN, PAIR>::kThreads, MmShape<BN, PAIR>
             tc::mbar_init(&sc_full[g], 1);
             tc::mbar_init(&sc_empty[g], S::kEpiWarps);
         }
-        tc::mbar_init(&drain, S::kParts);
+        tc::mbar_init(&drain, S::kIssuers);
         abort_word = 0;
         tc::fence_mbar_init();
     }
@@ -186,8 +190,8 @@ __global__ void __launch_bounds__(MmShape<BN, PAIR>::kThreads, MmShape<BN, PAIR>
                 int m, n;
                 place(t, m, n);
                 const int arow = (m * CTAS + rank) * kMmRows, wrow = n * BN + rank * S::kBox;
-                for (int kb = 0; kb < KB; ++kb) {
-                    if (issued >= ST && !tc::mbar_wait_warp(&empty[st], fill ^ 1u, abort_flag)) { ok = false; break; }
+                for (int kb = k0; kb < k1; ++kb) {
+                    if (!tc::mbar_wait_warp(&empty[st], fill ^ 1u, abort_flag)) { ok = false; break; }
                     uint8_t* a = ring + (size_t)st * q.stage_bytes;
                     const uint32_t bar = PAIR ? tc::cluster_addr(&full[st], 0) : tc::smem_u32(&full[st]);
                     // a pair's bytes, of both CTAs, are expected by its first CTA
@@ -202,26 +206,29 @@ __global__ void __launch_bounds__(MmShape<BN, PAIR>::kThreads, MmShape<BN, PAIR>
             }
             if (*abort_flag && rank == 0)  // let the copies in flight land (bounded) before the CTA goes away
                 for (int i = max(0, issued - ST); i < issued; ++i) tc::mbar_drain(&full[i % ST], (i / ST) & 1);
-        } else if (warp <= S::kEpiWarps + S::kParts && rank == 0) {
+        } else if (warp <= S::kEpiWarps + S::kIssuers && rank == 0) {
             // -------------------------------------------------------- MMA issuers (of a pair: its first CTA's)
-            const int h = warp - S::kEpiWarps - 1;
+            // Waits and MMAs of a block take an issuer some 350 clocks, so there are two: with two parts, one for each; else
+            // they take turns.
+            const int i = warp - S::kEpiWarps - 1;
+            constexpr int kTurns = S::kParts > 1 ? 1 : S::kIssuers;
+            const int h = S::kParts > 1 ? i : 0;
             const uint32_t idesc = tc::idesc_e4m3(kMmRows * CTAS, S::kPart);
             const uint64_t d0 = tc::sdesc_sw128(tc::smem_u32(ring), 16, 1024);
-            const uint32_t b_off = q.a_bytes + h * S::kBox * kE4Block;
+            const uint32_t b_off = q.a_bytes + h * S::kBox * kE4Block, tm = tmem + h * S::kPart;
             uint64_t *part_full = acc_full + h * S::kBufs, *part_empty = acc_empty + h * S::kBufs;
-            int st = 0, buf = 0;
-            uint32_t ph = 0, use = 0;  // parities of the stage's fill and of the accumulator's use
-            bool ok = true, reused = false;
-            for (int t = first; ok && t < tiles; t += step) {
-                for (int kb = 0; kb < KB; ++kb) {
-                    if (reused && !tc::mbar_wait_warp(&part_empty[buf], use ^ 1u, abort_flag)) { ok = false; break; }
-                    if (!tc::mbar_wait_warp(&full[st], ph, abort_flag)) { ok = false; break; }
-                    tc::tc_fence_after();
-                    const uint64_t da = tc::sdesc_add(d0, (uint32_t)st * q.stage_bytes), db = tc::sdesc_add(da, b_off);
-                    tc::mma_e4m3_block<PAIR>(tmem + buf * BN + h * S::kPart, da, db, idesc, &empty[st], &part_full[buf]);
-                    if (++st == ST) { st = 0; ph ^= 1u; }
-                    if (++buf == S::kBufs) { buf = 0; use ^= 1u; reused = true; }
-                }
+            const long long todo = (long long)(first < tiles ? (tiles - 1 - first) / step + 1 : 0) * (k1 - k0);
+            int st = kTurns > 1 ? i % ST : 0, buf = kTurns > 1 ? i : 0;
+            uint32_t ph = kTurns > 1 ? (i / ST) & 1 : 0, use = 0;  // parities of the stage's fill and of the accumulator's use
+            for (long long g = kTurns > 1 ? i : 0; g < todo; g += kTurns) {
+                if (!tc::mbar_wait_warp(tc::smem_u32(&part_empty[buf]), use ^ 1u, tc::smem_u32(&full[st]), ph, abort_flag)) break;
+                tc::tc_fence_after();
+                const uint64_t da = tc::sdesc_add(d0, (uint32_t)st * q.stage_bytes), db = tc::sdesc_add(da, b_off);
+                tc::mma_e4m3_block<PAIR>(tm + buf * BN, da, db, idesc, &empty[st], &part_full[buf]);
+                st += kTurns;
+                if (st >= ST) { st -= ST; ph ^= 1u; }
+                buf += kTurns;
+                if (buf >= S::kBufs) { buf -= S::kBufs; use ^= 1u; }
             }
             tc::mma_commit_elect<PAIR>(&drain);
             tc::mbar_drain(&drain, 0);
@@ -290,43 +297,50 @@ __global__ void __launch_bounds__(MmShape<BN, PAIR>::kThreads, MmShape<BN, PAIR>
             const float* as = p.a_scale + (size_t)min(row, p.rows - 1) * KB;
             const float* ws = p.w_scale + (size_t)(min(col, p.N - 1) / kE4Block) * KB;
             float sa = 0.f, sw = 0.f;
-            if constexpr (!S::kWide) sa = __ldg(as), sw = __ldg(ws);
-            // 16 columns are on their way out of TMEM while the 16 before them are added up, from one block to the next
-            uint32_t d[2][16];
-            ok = tc::mbar_wait_warp(full0 + buf * 8, use, abort_flag);
-            tc::tc_fence_after();
-            if (ok) tc::tmem_ld16(taddr + buf * BN, d[0]);
-            for (int kb = 0; ok && kb < KB; ++kb) {
+            if constexpr (!S::kWide) sa = __ldg(as + k0), sw = __ldg(ws + k0);
+            // kAhead: 16 columns are on their way out of TMEM while the 16 before them are added up, from one block to the next
+            uint32_t d[S::kAhead ? 2 : 1][16];
+            if constexpr (S::kAhead) {
+                ok = tc::mbar_wait_warp(full0 + buf * 8, use, abort_flag);
+                tc::tc_fence_after();
+                if (ok) tc::tmem_ld16(taddr + buf * BN, d[0]);
+            }
+            for (int kb = k0; ok && kb < k1; ++kb) {
                 float sc;
                 if constexpr (S::kWide) {
                     if ((kb & 3) == 0) ok = tc::mbar_wait_warp(tc::smem_u32(&sc_full[g]), gph, abort_flag);
                     asm volatile("ld.shared.f32 %0, [%1];" : "=f"(sc) : "r"(sc0 + (g * 4 + (kb & 3)) * 1024));
                 } else {
                     sc = sa * sw;
-                    if (kb + 1 < KB) sa = __ldg(as + kb + 1), sw = __ldg(ws + kb + 1);
+                    if (kb + 1 < k1) sa = __ldg(as + kb + 1), sw = __ldg(ws + kb + 1);
+                }
+                if constexpr (!S::kAhead) {
+                    ok = tc::mbar_wait_warp(full0 + buf * 8, use, abort_flag);
+                    tc::tc_fence_after();
                 }
 #pragma unroll
                 for (int c = 0; c < S::kCols / 16; ++c) {
-                    uint32_t(&now)[16] = d[c & 1];
+                    uint32_t(&now)[16] = d[S::kAhead ? c & 1 : 0];
+                    if constexpr (!S::kAhead) tc::tmem_ld16(taddr + buf * BN + c * 16, now);
                     tc::tmem_wait_ld16(now);
-                    if (c + 1 < S::kCols / 16) {
-                        tc::tmem_ld16(taddr + buf * BN + (c + 1) * 16, d[(c + 1) & 1]);
-                    } else {
+                    if (c + 1 == S::kCols / 16) {
                         tc::tc_fence_before();
                         __syncwarp();
                         if constexpr (PAIR) tc::mbar_arrive_one_cluster(empty0 + buf * 8);
                         else tc::mbar_arrive_one(empty0 + buf * 8);
                         if (++buf == S::kBufs) { buf = 0; use ^= 1u; }
-                        if (kb + 1 < KB) {
+                        if (S::kAhead && kb + 1 < k1) {
                             ok = ok && tc::mbar_wait_warp(full0 + buf * 8, use, abort_flag);
                             tc::tc_fence_after();
                             tc::tmem_ld16(taddr + buf * BN, d[0]);
                         }
+                    } else if constexpr (S::kAhead) {
+                        tc::tmem_ld16(taddr + buf * BN + (c + 1) * 16, d[(c + 1) & 1]);
                     }
 #pragma unroll
                     for (int i = 0; i < 16; ++i) acc[c * 16 + i] = fmaf(sc, __uint_as_float(now[i]), acc[c * 16 + i]);
                 }
-                if (S::kWide && ((kb & 3) == 3 || kb + 1 == KB)) {
+                if (S::kWide && ((kb & 3) == 3 || kb + 1 == k1)) {
                     __syncwarp();
                     tc::mbar_arrive_one(&sc_empty[g]);
                     if (++g == 2) { g = 0; gph ^= 1u; }
@@ -334,7 +348,15 @@ __global__ void __launch_bounds__(MmShape<BN, PAIR>::kThreads, MmShape<BN, PAIR>
             }
             tc::tmem_wait_ld();
             if (!ok || row0 >= p.rows || col >= p.N) continue;
-            if (p.best) {
+            if (!PAIR && split > 1) {
+                // this CTA's sums to its own shared memory, where the stages were; 16-byte pieces swizzled against bank conflicts
+                float* to = reinterpret_cast<float*>(ring) + (quarter * 32 + lane) * BN;
+                const int c4 = half * S::kCols / 4;
+                if (row < p.rows)
+#pragma unroll
+                    for (int c = 0; c < S::kCols / 4; ++c)
+                        *reinterpret_cast<float4*>(to + (((c4 + c) ^ (lane & 7)) << 2)) = make_float4(acc[4 * c], acc[4 * c + 1], acc[4 * c + 2], acc[4 * c + 3]);
+            } else if (p.best) {
                 float best = 0.f;
                 int at = -1;
 #pragma unroll
@@ -358,6 +380,40 @@ __global__ void __launch_bounds__(MmShape<BN, PAIR>::kThreads, MmShape<BN, PAIR>
         }
     }
     __syncthreads();
+    if (!PAIR && split > 1) {
+        // every CTA of the cluster adds up, share by share, its part of the tile's columns, and writes them
+        tc::cluster_sync();
+        int m, n;
+        place(first, m, n);
+        const int row0 = m * kMmRows, rows = min(kMmRows, q.p.rows - row0), per = BN / 4 / split;
+        for (int e = threadIdx.x; e < rows * per; e += blockDim.x) {
+            const int r = e / per, c = share * per + e - r * per, col = n * BN + c * 4;
+            const float* from = reinterpret_cast<const float*>(ring) + r * BN + ((c ^ (r & 7)) << 2);
+            float4 part[8], v = make_float4(0.f, 0.f, 0.f, 0.f);  // asked for together, added up in order
+#pragma unroll
+            for (int s = 0; s < 8; ++s)
+                if (s < split) part[s] = tc::ld_cluster_f4(tc::cluster_addr(from, s));
+#pragma unroll
+            for (int s = 0; s < 8; ++s)
+                if (s < split) v = make_float4(v.x + part[s].x, v.y + part[s].y, v.z + part[s].z, v.w + part[s].w);
+            const size_t o = (size_t)(row0 + r) * q.p.N + col;
+            const float x[4] = {v.x, v.y, v.z, v.w};
+            if (q.p.best) {
+                unsigned long long key = 0ull;
+                for (int j = 0; j < 4 && col + j < q.p.N; ++j) key = max(key, pack_best(x[j], (uint32_t)(col + j)));
+                if (key) atomicMax(&q.p.best[row0 + r], key);
+                continue;
+            }
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                if (col + j >= q.p.N) break;
+                if (q.p.out_dtype == TSV_F32) ((float*)q.p.out)[o + j] = x[j];
+                else if (q.p.out_dtype == TSV_BF16) ((__nv_bfloat16*)q.p.out)[o + j] = __float2bfloat16_rn(x[j]);
+                else ((__half*)q.p.out)[o + j] = __float2half_rn(x[j]);
+            }
+        }
+        tc::cluster_sync();  // no CTA goes while another reads its sums
+    }
     // the pair's second CTA: the last arrivals of the first one's commits have to come in as well
     if (PAIR && rank == 1 && threadIdx.x == 0) tc::mbar_drain(&drain, 0);
     if constexpr (PAIR) tc::cluster_sync();  // neither CTA's memory goes while the other's copies, MMAs or arrivals use it
@@ -398,7 +454,7 @@ static bool mm_map(CUtensorMap* m, const void* base, int rows, int K, int box) {
 }
 
 template <int BN, bool PAIR>
-static tsv_status launch_mm(const char* name, const E4Product& p, cudaStream_t stream) {
+static tsv_status launch_mm(const char* name, const E4Product& p, int split, cudaStream_t stream) {
     using S = MmShape<BN, PAIR>;
     constexpr int CTAS = PAIR ? 2 : 1;
     MmParams q;
@@ -407,6 +463,7 @@ static tsv_status launch_mm(const char* name, const E4Product& p, cudaStream_t s
     q.mtiles = (p.rows + kMmRows * CTAS - 1) / (kMmRows * CTAS);
     q.ntiles = (p.N + BN - 1) / BN;
     q.panel = std::min(q.mtiles, 8);
+    q.split = split;
     // rows of a in shared memory: as many as there are, in whole swizzle atoms of 8.  The MMA reads 128 rows, so a stage's
     // weights, or the next stage's bytes, stand in for missing ones and end in accumulator rows that nothing reads.
     const int arows = std::min(kMmRows, (p.rows + 7) / 8 * 8);
@@ -421,18 +478,44 @@ static tsv_status launch_mm(const char* name, const E4Product& p, cudaStream_t s
     const long long tiles = (long long)q.mtiles * q.ntiles;
     if (tiles > INT_MAX / 2) return fail(TSV_ECAPACITY, "%s: %lld tiles", name, tiles);
     const int places = sm_count() * S::kPerSm / CTAS;
-    const int grid = (int)std::min<long long>(tiles, places) * CTAS;
+    const int grid = split > 1 ? (int)tiles * split : (int)std::min<long long>(tiles, places) * CTAS;
     cudaFuncSetAttribute(matmul_e4m3_kernel<BN, PAIR>, cudaFuncAttributeMaxDynamicSharedMemorySize, S::kSmem);
-    launch_pdl_cluster(matmul_e4m3_kernel<BN, PAIR>, grid, S::kThreads, S::kSmem, stream, CTAS, q);
+    launch_pdl_cluster(matmul_e4m3_kernel<BN, PAIR>, grid, S::kThreads, S::kSmem, stream, CTAS * split, q);
     return check_launch(name);
 }
 
+// The kernel for a product, by an estimate of each one's microseconds.  A block of 128 features takes a CTA 0.28 us (a pair: 0.5)
+// wherever its operands come from, since that is what its hand-offs and 66 bytes per SM clock from L2 cost; rounds of CTAs
+// follow one another; HBM delivers 6.5 bytes per nanosecond at most; a launch costs 3.5 us, sharing a tile's features between the CTAs of a
+// cluster 2.5 and 0.035 per row (their sums go through shared memory).  Measured (us: estimate's choice, others), K = 5120:
+//   1 x 1024: 64 columns shared by 8 6.3, by 4 7.0, 128 columns 13.2     1 x 20480: 64 columns 21.4, 128 30.1
+//   1 x 6144: 64 shared by 4 11.4, by 2 11.8, 128 13.6                   1 x 248320: 128 columns 187 (the HBM rate), 64 193
+//   512 x 5120: pairs 23.7, 128 columns 26.0                             2048 x 5120: 128 columns 57.7, pairs 62.4
+//   1024 x 5120: 128 columns 36.3, pairs 42.8                            4096 x 20480: pairs 345, 128 columns 397
 tsv_status launch_matmul_e4m3(const char* name, const E4Product& p, cudaStream_t stream) {
-    if (p.rows > kMmRows && (long long)p.N * p.rows >= 256ll * 256 * 76) return launch_mm<256, true>(name, p, stream);
-    const long long mt = (p.rows + kMmRows - 1) / kMmRows;
-    if (mt * p.N >= 128ll * sm_count() && p.rows > 64) return launch_mm<128, false>(name, p, stream);
-    if (mt * p.N >= 64ll * sm_count()) return launch_mm<64, false>(name, p, stream);
-    return launch_mm<32, false>(name, p, stream);
+    const int sms = sm_count(), blocks = e4_blocks(p.K);
+    const long long mt = (p.rows + kMmRows - 1) / kMmRows, n64 = mt * ((p.N + 63) / 64), n128 = mt * ((p.N + 127) / 128);
+    const long long pairs = (mt + 1) / 2 * ((p.N + 255) / 256);
+    const float stream_us = ((float)p.N + p.rows) * p.K / 6.5e6f;
+    const auto rounds = [](long long tiles, int places) { return (float)((tiles + places - 1) / places); };
+    float best = 1e30f;
+    int columns = 0, split = 1;
+    const auto offer = [&](float us, int c, int s) {
+        if (us < best) best = us, columns = c, split = s;
+    };
+    if (mt > 1) offer(std::max(rounds(pairs, sms / 2) * blocks * 0.5f, stream_us), 256, 1);
+    for (int s = 1; s <= 8 && s <= std::max(1, blocks / 2); s *= 2) {
+        const float share = (float)((blocks + s - 1) / s), joined = s > 1 ? 2.5f + 0.035f * std::min(p.rows, kMmRows) : 0.f;
+        if (s == 1 || n128 * s <= sms) offer(std::max(rounds(n128 * s, sms) * share * 0.28f, stream_us) + joined, 128, s);
+        if (s == 1 || n64 * s <= sms * 3) {
+            const float beside = std::min(3.f, std::max(1.f, (float)(n64 * s) / sms));  // CTAs on an SM
+            const float block = std::max(0.28f, beside * (std::min(p.rows, kMmRows) * 128 + 8192) / 85e3f);
+            offer(std::max(rounds(n64 * s, sms * 3) * share * block, stream_us) + joined, 64, s);
+        }
+    }
+    if (columns == 256) return launch_mm<256, true>(name, p, 1, stream);
+    if (columns == 128) return launch_mm<128, false>(name, p, split, stream);
+    return launch_mm<64, false>(name, p, split, stream);
 }
 
 // What both entry points ask of their operands.

@@ -140,6 +140,12 @@ __device__ __forceinline__ bool mbar_wait_warp(uint32_t bar, uint32_t parity, vo
 __device__ __forceinline__ bool mbar_wait_warp(uint64_t* bar, uint32_t parity, volatile int* abort) {
     return mbar_wait_warp(smem_u32(bar), parity, abort);
 }
+// The same for two barriers, with one vote.
+__device__ __forceinline__ bool mbar_wait_warp(uint32_t bar0, uint32_t parity0, uint32_t bar1, uint32_t parity1, volatile int* abort) {
+    const bool a = mbar_try_wait(bar0, parity0), b = mbar_try_wait(bar1, parity1);
+    if (__all_sync(0xFFFFFFFFu, a && b)) return true;
+    return mbar_wait_warp(bar0, parity0, abort) && mbar_wait_warp(bar1, parity1, abort);
+}
 
 // ---------------------------------------------------------------- CTA pairs and clusters
 __device__ __forceinline__ uint32_t cluster_rank() {
@@ -155,6 +161,12 @@ __device__ __forceinline__ uint32_t cluster_addr(const void* p, uint32_t rank) {
     uint32_t r;
     asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(smem_u32(p)), "r"(rank));
     return r;
+}
+// 16 bytes of any CTA's shared memory, by their cluster address.
+__device__ __forceinline__ float4 ld_cluster_f4(uint32_t addr) {
+    float4 v;
+    asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];" : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w) : "r"(addr) : "memory");
+    return v;
 }
 // One lane of the converged warp arrives on a barrier anywhere in the cluster.  Relaxed: what it tells of is TMEM reads that have
 // ended, no memory (a release would wait for every store under way, microseconds per arrival).
