@@ -599,7 +599,8 @@ tsv_status tsv_matmul_e4m3_argmax(const void* a, const float* a_scale, int32_t r
  *   index; 0 <= top_k <= min(64, V) (0: both NULL).
  *   A logit of -infinity has probability 0 (and adds nothing to the entropy).  A row with a NaN or +infinity, or with
  *   nothing but -infinity, has no distribution: its floats are NaN and its rank and tokens -1.  A target outside [0, V) (the -1 that
- *   pads emitted tokens) gets logp NaN and rank -1.  1e-6 <= temperature <= 1e6.  Sums are fp32, in a fixed order.
+ *   pads emitted tokens) gets logp NaN and rank -1.  1e-6 <= temperature <= 1e6.  Sums are fp32, in an order that
+ *   the sizes and the rows' offsets from 16-byte boundaries fix, so the same call gives the same bits.
  */
 size_t tsv_token_logprobs_workspace_size(int32_t rows, int32_t V, int32_t top_k);
 

@@ -117,9 +117,12 @@ def test_unaligned_rows_same_bits_twice_and_other_streams(gpu_lib):
     targets = torch.tensor([0, 1, 2, 50000], dtype=torch.int32, device=DEV)
     one = ask(gpu_lib, x, targets, 1.0, 20)
     check(one, x, targets, 1.0, 20)
-    two = ask(gpu_lib, x.clone(), targets, 1.0, 20, stream=torch.cuda.Stream())
+    two = ask(gpu_lib, x, targets, 1.0, 20, stream=torch.cuda.Stream())
     for n in one:
         assert np.array_equal(one[n], two[n]), n
+    # at another address the sums are taken in another order: each within its tolerance of the exact value
+    three = ask(gpu_lib, x.clone(), targets, 1.0, 20, stream=torch.cuda.Stream())
+    check(three, x, targets, 1.0, 20)
     same = ask(gpu_lib, x[:1].expand(300, -1).contiguous(), targets[:1].expand(300).contiguous(), 1.0, 20)
     for n in one:  # another number of rows, another split: within the tolerance, whole values equal
         assert np.allclose(same[n][7], one[n][0], rtol=1e-5, atol=1e-5), n

@@ -81,8 +81,8 @@ def no_error_left_behind():
     (logprobs, dict(targets=None), "EINVAL", b"together"), (logprobs, dict(logp=None), "EINVAL", b"together"),
     (logprobs, dict(targets=None, logp=None), "EINVAL", b"rank"), (logprobs, dict(top_tokens=None), "EINVAL", b"top_k=5"), (logprobs, dict(top_k=0), "EINVAL", b"top_k=0"),
     (logprobs, dict(targets=None, logp=None, rank=None, entropy=None, top_k=0, top_tokens=None, top_logp=None), "EINVAL", b"no output"),
-    (logprobs, dict(logits=PTR + 2), "EINVAL", b"aligned"), (logprobs, dict(ws=None), "EINVAL", b"workspace"), (logprobs, dict(ws=PTR + 8), "EINVAL", b"16-byte"),
-    (logprobs, dict(ws_bytes=0), "ECAPACITY", b"workspace"),
+    (logprobs, dict(logits=PTR + 2), "EINVAL", b"aligned"), (logprobs, dict(ws=None, V=100000), "EINVAL", b"workspace"), (logprobs, dict(ws=PTR + 8), "EINVAL", b"16-byte"),
+    (logprobs, dict(ws_bytes=0, V=100000), "ECAPACITY", b"workspace"),
 ])
 def test_refused(call, kw, status, word):
     assert call(**kw) == getattr(_abi, status)

@@ -63,6 +63,22 @@ __device__ __forceinline__ void sums8(const float* acc, float (&v)[8]) {
     for (int j = 0; j < 8; ++j) v[j] = acc[j];
 }
 
+// Bits of the largest of a thread's sums in the order of orderable(): a NaN without a sign above everything, one with a sign
+// below everything, -0 below 0.  Bits of numbers without a sign are ordered as integers; where all have one, the other way round.
+template <int COLS>
+__device__ __forceinline__ uint32_t largest(const float (&acc)[COLS]) {
+    int m = __float_as_int(acc[0]);
+#pragma unroll
+    for (int c = 1; c < COLS; ++c) m = max(m, __float_as_int(acc[c]));
+    if (__any_sync(0xFFFFFFFFu, m < 0)) {
+        uint32_t u = __float_as_uint(acc[0]);
+#pragma unroll
+        for (int c = 1; c < COLS; ++c) u = min(u, __float_as_uint(acc[c]));
+        m = m < 0 ? (int)u : m;
+    }
+    return (uint32_t)m;
+}
+
 // A thread's COLS sums to `n` places of its output row.
 template <typename T, int COLS>
 __device__ __forceinline__ void store_row(T* o, const float (&acc)[COLS], int n, bool vec) {
@@ -297,6 +313,8 @@ __global__ void __launch_bounds__(MmShape<BN, PAIR>::kThreads, MmShape<BN, PAIR>
             const float* as = p.a_scale + (size_t)min(row, p.rows - 1) * KB;
             const float* ws = p.w_scale + (size_t)(min(col, p.N - 1) / kE4Block) * KB;
             float sa = 0.f, sw = 0.f;
+            unsigned long long seen = 0ull;  // the row's best so far, or an older one
+            if (p.best && row < p.rows) seen = *(volatile unsigned long long*)&p.best[row];
             if constexpr (!S::kWide) sa = __ldg(as + k0), sw = __ldg(ws + k0);
             // kAhead: 16 columns are on their way out of TMEM while the 16 before them are added up, from one block to the next
             uint32_t d[S::kAhead ? 2 : 1][16];
@@ -357,13 +375,18 @@ __global__ void __launch_bounds__(MmShape<BN, PAIR>::kThreads, MmShape<BN, PAIR>
                     for (int c = 0; c < S::kCols / 4; ++c)
                         *reinterpret_cast<float4*>(to + (((c4 + c) ^ (lane & 7)) << 2)) = make_float4(acc[4 * c], acc[4 * c + 1], acc[4 * c + 2], acc[4 * c + 3]);
             } else if (p.best) {
-                float best = 0.f;
-                int at = -1;
+                if (col + S::kCols > p.N)  // columns behind the last one: the bits that rank below every number's
 #pragma unroll
-                for (int c = 0; c < S::kCols; ++c) {
-                    if (col + c < p.N && (at < 0 || orderable(acc[c]) > orderable(best))) best = acc[c], at = col + c;
+                    for (int c = 0; c < S::kCols; ++c) acc[c] = col + c < p.N ? acc[c] : __uint_as_float(0xFFFFFFFFu);
+                const uint32_t top = largest<S::kCols>(acc);
+                // most tiles do not hold their rows' best: `seen`, read a tile's time ago, tells
+                const bool wins = row < p.rows && orderable(__uint_as_float(top)) >= (uint32_t)(seen >> 32);
+                if (__any_sync(0xFFFFFFFFu, wins)) {
+                    int at = 0;
+#pragma unroll
+                    for (int c = S::kCols - 1; c >= 0; --c) at = __float_as_uint(acc[c]) == top ? c : at;
+                    if (wins) atomicMax(&p.best[row], pack_best(__uint_as_float(top), (uint32_t)(col + at)));
                 }
-                if (row < p.rows) atomicMax(&p.best[row], pack_best(best, (uint32_t)at));
             } else if constexpr (S::kOutBytes > 0) {
                 uint8_t* buf4k = outbuf + warp * 4096;
                 const size_t o = (size_t)row0 * p.N + col;
