@@ -3,15 +3,16 @@
 //   z = logits / T;  logp(t) = z_t - log sum exp z;  entropy = log sum exp z - sum p z
 //
 // Bound by HBM: every logit is read once.  A CTA walks a part of a row in tiles of 4096 logits, 16 in a thread's registers; a
-// row is one part where there are rows enough to fill the GPU, else up to 64, whose results a second kernel joins (one warp per
-// row).  Sums are kept per thread against the thread's own running maximum (rescaled when it rises) and joined at the end, in the
-// same order in every run.
+// row is one part where there are rows enough to fill the GPU, else up to 64, whose results a second kernel joins.  Sums are kept
+// per thread against the thread's own maximum so far (the sums are rescaled when it rises) and joined at the
+// end, in the same order in every run.
 //
-// The top k are exact.  The k-th largest of the 256 threads' maxima over the first tile is a bound below which no logit of the top k
-// lies, and at most k threads hold anything above it: at most 16 k candidates go to shared memory.  From then on a logit is a
-// candidate if it is larger than the k-th best known, which few are; the list is cut back to k whenever it might overflow, and
-// a tile in which too many logits still qualify (an ascending row) is bounded like the first one.  Candidates are 64-bit keys (value, then
-// lower index), so ties need no care.
+// The top k are exact.  Logits above a bound that k logits are known to reach go to a list in shared memory: in the first tile the
+// bound is the smallest over the 8 warps of each one's ceil(k / 8)-th largest thread maximum, then the k-th best of the list, which is
+// cut back to k between groups of 1, 1, 2, 4, 8, 8 ... tiles (no barrier inside a group: one per tile cost a third of the time).  Of
+// logits in no particular order a few hundred pass.  Where a group's do not fit (an ascending row, many equal ones), its tiles
+// are read again, each bounded by the k-th largest of the 256 threads' maxima, above which no more than 16 k logits can
+// lie.  Candidates are 64-bit keys (value, then lower index), so ties need no care.
 #include <algorithm>
 
 #include "e4m3.cuh"
@@ -25,6 +26,7 @@ constexpr int kLpTile = kLpThreads * kLpPer;
 constexpr int kLpMaxTop = 64;
 constexpr int kLpMaxParts = 64;
 constexpr int kLpList = 2048;                    // candidates; 16 x 64 + 64 at least
+constexpr int kLpGroup = 8;                      // tiles between two looks at the list
 constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
 
 struct LogprobParams {
@@ -38,8 +40,9 @@ struct LogprobParams {
     unsigned long long* part_top;    // [rows][parts][K]
 };
 
-// What is known of some of a row's logits: their maximum m, the sum of 2^d and of d 2^d with d = (x - m) log2(e) / T, and how
-// many rank ahead of the target.
+// What is known of some of a row's logits x: their maximum m, the sums of 2^d and of d 2^d with d = (x - m) c, c = log2(e) / T, and
+// how many rank ahead of the target.  (x - m) c in two steps, not x c - m c in one: a rounded m c would shift every d of a thread alike,
+// and overflow where a mask's lowest value is all there is.
 struct Sums {
     float m, s, w;
     int ahead;
@@ -96,27 +99,60 @@ __device__ __forceinline__ unsigned long long logit_key(float x, int i) { return
 __device__ __forceinline__ int key_token(unsigned long long k) { return (int)(0xFFFFFFFFu - (uint32_t)k); }
 __device__ __forceinline__ float key_logit(unsigned long long k) { return unorderable((uint32_t)(k >> 32)); }
 
-// A row's numbers, by one thread; NaN and -1 where the row has no distribution.  Returns log sum exp((x - m) / T), or NaN.
-__device__ __forceinline__ float row_results(const LogprobParams& p, size_t row, Sums v, int target, float t) {
-    const bool bad = !(v.s < INFINITY) || v.m == -INFINITY, has = target >= 0 && target < p.V;
-    const float nan = __int_as_float(0x7FFFFFFF), lse = bad ? nan : logf(v.s);
-    if (p.logp) p.logp[row] = bad || !has ? nan : (t - v.m) * p.inv_t - lse;
-    if (p.rank) p.rank[row] = bad || !has ? -1 : v.ahead;
-    if (p.entropy) p.entropy[row] = bad ? nan : lse - kLn2 * v.w / v.s;
-    return lse;
-}
+// A row's results, once its sums are known.
+struct RowResults {
+    bool bad;         // a NaN or +infinity, or nothing but -infinity: no distribution
+    float inv_t, m, lse;  // 1 / T, the largest logit, log sum exp((x - m) / T)
+    __device__ __forceinline__ RowResults(Sums v, float inv_t)
+        : bad(!(v.s < INFINITY) || v.m == -INFINITY), inv_t(inv_t), m(v.m), lse(bad ? 0.f : logf(v.s)) {}
+    __device__ __forceinline__ float logp(float x) const { return bad ? __int_as_float(0x7FFFFFFF) : (x - m) * inv_t - lse; }
+    // by one thread
+    __device__ __forceinline__ void write(const LogprobParams& p, size_t row, Sums v, int target, float t) const {
+        const bool has = target >= 0 && target < p.V;
+        const float nan = __int_as_float(0x7FFFFFFF);
+        if (p.logp) p.logp[row] = has ? logp(t) : nan;
+        if (p.rank) p.rank[row] = bad || !has ? -1 : v.ahead;
+        if (p.entropy) p.entropy[row] = bad ? nan : lse - kLn2 * v.w / v.s;
+    }
+    __device__ __forceinline__ void write_top(const LogprobParams& p, size_t row, int k, unsigned long long key) const {
+        p.top_tokens[row * p.K + k] = bad ? -1 : key_token(key);
+        p.top_logp[row * p.K + k] = logp(key_logit(key));
+    }
+};
 
 template <typename T>
 __device__ __forceinline__ float target_logit(const LogprobParams& p, size_t row, int target) {
     return target >= 0 && target < p.V ? RowType<T>::to_f32(((const T*)p.logits)[row * p.V + target]) : 0.f;
 }
 
+// A thread's 16 logits of a tile, -infinity where the row has none.
+template <typename T>
+__device__ __forceinline__ void load_tile(const T* x0, int at, int V, bool inside, float (&x)[kLpPer]) {
+    constexpr int W = 16 / sizeof(T), NV = kLpPer / W;
+    uint4 u[NV];
+    if (inside) {
+#pragma unroll
+        for (int j = 0; j < NV; ++j) u[j] = ldg_stream16(x0 + at + j * kLpThreads * W);
+#pragma unroll
+        for (int j = 0; j < NV; ++j) unpack16<T>(u[j], x + j * W);
+        return;
+    }
+#pragma unroll
+    for (int j = 0; j < NV; ++j)
+#pragma unroll
+        for (int k = 0; k < W; ++k) {
+            const int i = at + j * kLpThreads * W + k;
+            x[j * W + k] = i >= 0 && i < V ? RowType<T>::to_f32(x0[i]) : -INFINITY;
+        }
+}
+
 template <typename T>
 __global__ void __launch_bounds__(kLpThreads, 4) logprobs_kernel(const LogprobParams p) {
     griddep_begin();
-    constexpr int W = 16 / sizeof(T), NV = kLpPer / W;
+    constexpr int W = 16 / sizeof(T);
     __shared__ unsigned long long list[kLpList], maxima[kLpThreads];
     __shared__ Sums warps[kLpThreads / 32];
+    __shared__ float bounds[kLpThreads / 32];
     __shared__ int filled;
     const int tid = threadIdx.x, lane = tid & 31, K = p.K;
     const size_t row = blockIdx.x / p.parts;
@@ -130,116 +166,121 @@ __global__ void __launch_bounds__(kLpThreads, 4) logprobs_kernel(const LogprobPa
     const int target = p.targets ? p.targets[row] : -1;
     const float t = target_logit<T>(p, row, target);
     const bool ranked = p.rank && target >= 0 && target < p.V;
-    // a logit before the target ranks ahead if it is larger than `below`, the next number under t: an equal one does
+    // a logit ahead of the target outranks it if it is larger than `below`, the next number under t: an equal one does
     const float below = nextafterf(t, -INFINITY);
 
-    Sums v = {-INFINITY, 0.f, 0.f, 0};
-    float kth = -INFINITY;   // the k-th best of the list when it was last cut back
-    int room_used = 0;       // an upper bound of `filled`, the same in every thread
-    if (tid == 0) filled = 0;
-    for (int tile = t0; tile < t1; ++tile) {
-        float x[kLpPer];
-#pragma unroll
-        for (int j = 0; j < NV; ++j) {
-            const int i = tile * kLpTile + (j * kLpThreads + tid) * W - lead;
-            if (i >= 0 && i + W <= p.V) {
-                unpack16<T>(ldg_stream16(x0 + i), x + j * W);
-            } else {
-#pragma unroll
-                for (int k = 0; k < W; ++k) x[j * W + k] = i + k >= 0 && i + k < p.V ? RowType<T>::to_f32(x0[i + k]) : -INFINITY;
-            }
-        }
-        float most = x[0];
-#pragma unroll
-        for (int k = 1; k < kLpPer; ++k) most = fmaxf(most, x[k]);
-        if (most > v.m) {
-            if (v.m > -INFINITY) {
-                const float d = fmaxf((v.m - most) * c, -1000.f), f = tc::ex2_approx(d);
-                v.w = (v.w + v.s * d) * f;
-                v.s *= f;
-            }
-            v.m = most;
-        }
-        const float m = v.m > -INFINITY ? v.m : 0.f;
+    // element k of this thread's 16 in a tile is logit first(tile) + (k / W) * 256 W + k % W
+    auto first = [&](int tile) { return tile * kLpTile + tid * W - lead; };
+    auto inside = [&](int tile) { return tile * kLpTile >= lead && (tile + 1) * kLpTile - lead <= p.V; };
+    auto append = [&](const float (&x)[kLpPer], int at, auto&& wanted) {
 #pragma unroll
         for (int k = 0; k < kLpPer; ++k) {
-            const float d = (x[k] - m) * c, e = tc::ex2_approx(d);
-            v.s += e;                              // a NaN stays
-            v.w = fmaf(e, fmaxf(d, -1000.f), v.w);  // 0 for -infinity
+            const int i = at + (k / W) * kLpThreads * W + k % W;
+            if (wanted(x[k], i) && i >= 0 && i < p.V) {
+                const int to = atomicAdd(&filled, 1);
+                if (to < kLpList) list[to] = logit_key(x[k], i);
+            }
         }
-        if (ranked) {
+    };
+    Sums v = {-INFINITY, 0.f, 0.f, 0};
+    float kth = -INFINITY;  // what a logit has to exceed to be a candidate; in the first tile, to reach
+    int kept = 0;           // candidates that stood in the list, sorted, after the last cut
+    if (tid == 0) filled = 0;
+    auto cut = [&](int have) {  // the list's `have` candidates back to the best K, sorted; after a barrier
+        const int n = power_of_two(max(have, K));
+        for (int e = have + tid; e < n; e += kLpThreads) list[e] = 0ull;
+        __syncthreads();
+        sort_keys(list, n);
+        kept = min(have, K);
+        if (tid == 0) filled = kept;
+        if (have >= K) kth = key_logit(list[K - 1]);
+        __syncthreads();
+    };
+    for (int next = t0, group = 1; next < t1;) {
+        const int end = min(t1, next + group);
+        for (int tile = next; tile < end; ++tile) {
+            float x[kLpPer];
+            const int at = first(tile);
+            load_tile<T>(x0, at, p.V, inside(tile), x);
+            float most = x[0];
 #pragma unroll
-            for (int j = 0; j < NV; ++j) {
-                const int i = tile * kLpTile + (j * kLpThreads + tid) * W - lead;
-                if (i + W <= target || i > target) {
-                    const float over = i > target ? t : below;
-                    if (t > -INFINITY || i > target) {
+            for (int k = 1; k < kLpPer; ++k) most = fmaxf(most, x[k]);
+            if (most > v.m) {
+                if (v.m > -INFINITY) {
+                    const float d = fmaxf((v.m - most) * c, -1000.f), f = tc::ex2_approx(d);
+                    v.w = (v.w + v.s * d) * f;
+                    v.s *= f;
+                }
+                v.m = most;
+            }
+            const float m = v.m > -INFINITY ? v.m : 0.f;
 #pragma unroll
-                        for (int k = 0; k < W; ++k) v.ahead += x[j * W + k] > over;
-                    } else {
-                        v.ahead += W - max(0, -i);  // every logit is at least -infinity
-                    }
+            for (int k = 0; k < kLpPer; ++k) {
+                const float d = (x[k] - m) * c, e = tc::ex2_approx(d);
+                v.s += e;                               // a NaN stays
+                v.w = fmaf(e, fmaxf(d, -1000.f), v.w);  // 0 for -infinity
+            }
+            if (ranked) {
+                const bool after = tile * kLpTile - lead > target, before = (tile + 1) * kLpTile - lead <= target;
+                if (after || (before && t > -INFINITY)) {
+                    const float over = after ? t : below;
+#pragma unroll
+                    for (int k = 0; k < kLpPer; ++k) v.ahead += x[k] > over;
                 } else {
 #pragma unroll
-                    for (int k = 0; k < W; ++k)
-                        v.ahead += i + k >= 0 && i + k < p.V && (x[j * W + k] > t || (x[j * W + k] == t && i + k < target));
+                    for (int k = 0; k < kLpPer; ++k) {
+                        const int i = at + (k / W) * kLpThreads * W + k % W;
+                        v.ahead += i >= 0 && i < p.V && (x[k] > t || (x[k] == t && i < target));
+                    }
                 }
             }
-        }
-        if (K == 0) continue;
-        // ---- the top k
-        auto index = [&](int k) { return tile * kLpTile + ((k / W) * kLpThreads + tid) * W + k % W - lead; };
-        auto append = [&](auto&& wanted) {
-#pragma unroll
-            for (int k = 0; k < kLpPer; ++k) {
-                const int i = index(k);
-                if (i >= 0 && i < p.V && wanted(x[k], i)) {
-                    const int at = atomicAdd(&filled, 1);
-                    if (at < kLpList) list[at] = logit_key(x[k], i);  // more than that only where NaNs are, whose row has no top k
+            if (K == 0) continue;
+            if (tile == t0) {
+                uint32_t m = orderable(most), q = 0u;
+                for (int n = 0; n < (K + kLpThreads / 32 - 1) / (kLpThreads / 32); ++n) {
+                    q = __reduce_max_sync(0xFFFFFFFFu, m);
+                    if (lane == __ffs(__ballot_sync(0xFFFFFFFFu, m == q)) - 1) m = 0u;
                 }
-            }
-        };
-        auto cut = [&] {  // the list back to its best K, sorted
-            __syncthreads();
-            const int have = min(filled, kLpList);
-            const int n = power_of_two(max(have, K));
-            for (int e = have + tid; e < n; e += kLpThreads) list[e] = 0ull;
-            __syncthreads();
-            sort_keys(list, n);
-            if (tid == 0) filled = min(have, K);
-            room_used = min(have, K);
-            if (have >= K) kth = key_logit(list[K - 1]);
-            __syncthreads();
-        };
-        bool all_above = tile == t0;
-        if (!all_above) {
-            int holders = __syncthreads_count(most > kth);
-            if (room_used + holders * kLpPer > kLpList) {
-                cut();
-                holders = __syncthreads_count(most > kth);
-                all_above = room_used + holders * kLpPer > kLpList;
-            }
-            if (!all_above) {
-                room_used += holders * kLpPer;
-                if (most > kth) append([&](float y, int) { return y > kth; });
-            }
-        }
-        if (all_above) {
-            unsigned long long mine = 0ull;
+                if (lane == 0) bounds[tid >> 5] = q > 0u ? unorderable(q) : -INFINITY;
+                __syncthreads();
+                float bound = bounds[0];
 #pragma unroll
-            for (int k = 0; k < kLpPer; ++k) {
-                const int i = index(k);
-                if (i >= 0 && i < p.V && x[k] == x[k]) mine = max(mine, logit_key(x[k], i));
+                for (int w = 1; w < kLpThreads / 32; ++w) bound = fminf(bound, bounds[w]);
+                if (most >= bound) append(x, at, [&](float y, int) { return y >= bound; });
+            } else if (most > kth) {
+                append(x, at, [&](float y, int) { return y > kth; });
             }
-            __syncthreads();
-            maxima[tid] = mine;
-            __syncthreads();
-            sort_keys(maxima, kLpThreads);
-            const unsigned long long bound = maxima[K - 1];
-            room_used += K * kLpPer;
-            if (mine >= bound) append([&](float y, int i) { return logit_key(y, i) >= bound && y >= kth; });
-            cut();
         }
+        if (K > 0) {
+            __syncthreads();
+            const int have = filled;
+            __syncthreads();
+            if (have > kLpList) {
+                if (tid == 0) filled = kept;
+                for (int tile = next; tile < end; ++tile) {
+                    float x[kLpPer];
+                    const int at = first(tile);
+                    load_tile<T>(x0, at, p.V, inside(tile), x);
+                    unsigned long long mine = 0ull;
+#pragma unroll
+                    for (int k = 0; k < kLpPer; ++k) {
+                        const int i = at + (k / W) * kLpThreads * W + k % W;
+                        if (i >= 0 && i < p.V && x[k] == x[k]) mine = max(mine, logit_key(x[k], i));
+                    }
+                    maxima[tid] = mine;
+                    __syncthreads();
+                    sort_keys(maxima, kLpThreads);
+                    const unsigned long long bound = maxima[K - 1];
+                    if (mine >= bound) append(x, at, [&](float y, int i) { return logit_key(y, i) >= bound; });
+                    __syncthreads();
+                    cut(min(filled, kLpList));  // beyond the list only where NaNs are, and such a row has no top k
+                }
+            } else if (next == t0 || have > 2 * K) {
+                cut(have);
+            }
+        }
+        group = next == t0 ? 1 : min(kLpGroup, 2 * group);
+        next = end;
     }
     // ---- the part's results
     v = joined_warp(v, c);
@@ -248,26 +289,19 @@ __global__ void __launch_bounds__(kLpThreads, 4) logprobs_kernel(const LogprobPa
     v = warps[0];
 #pragma unroll
     for (int w = 1; w < kLpThreads / 32; ++w) v = joined(v, warps[w], c);
-    if (K > 0) {
+    if (K > 0 && filled > kept) {  // the same in every thread: the last appends lie behind barriers
+        const int have = filled;
         __syncthreads();
-        const int have = min(filled, kLpList);
-        const int n = power_of_two(max(have, K));
-        for (int e = have + tid; e < n; e += kLpThreads) list[e] = 0ull;
-        __syncthreads();
-        sort_keys(list, n);
+        cut(have);
     }
     if (p.parts > 1) {
         if (tid == 0) p.part_sums[blockIdx.x] = make_float4(v.m, v.s, v.w, __int_as_float(v.ahead));
         for (int k = tid; k < K; k += kLpThreads) p.part_top[(size_t)blockIdx.x * K + k] = list[k];
         return;
     }
-    const bool bad = !(v.s < INFINITY) || v.m == -INFINITY;
-    const float nan = __int_as_float(0x7FFFFFFF), lse = bad ? nan : logf(v.s);
-    if (tid == 0) row_results(p, row, v, target, t);
-    for (int k = tid; k < K; k += kLpThreads) {
-        p.top_tokens[row * K + k] = bad ? -1 : key_token(list[k]);
-        p.top_logp[row * K + k] = bad ? nan : (key_logit(list[k]) - v.m) * p.inv_t - lse;
-    }
+    const RowResults res(v, p.inv_t);
+    if (tid == 0) res.write(p, row, v, target, t);
+    for (int k = tid; k < K; k += kLpThreads) res.write_top(p, row, k, list[k]);
 }
 
 // Largest 64-bit key of the warp (keys are unique, but for 0).
@@ -277,14 +311,17 @@ __device__ __forceinline__ unsigned long long warp_largest(unsigned long long k)
     return ((unsigned long long)hi << 32) | lo;
 }
 
-// One warp per row joins its parts: the sums in the parts' order, the sorted lists by taking the largest head K times.  A lane
-// holds the parts `lane` and `lane + 32`.
+// A CTA per row joins its parts: the sums in the parts' order, the sorted lists (brought to shared memory first) by taking the
+// largest head K times.  Lane l of the first warp holds the parts l and l + 32.
 template <typename T>
 __global__ void __launch_bounds__(128) logprobs_join_kernel(const LogprobParams p) {
     griddep_begin();
+    __shared__ unsigned long long tops[kLpMaxParts * kLpMaxTop];
     const int lane = threadIdx.x & 31;
-    const size_t row = (size_t)blockIdx.x * (blockDim.x >> 5) + (threadIdx.x >> 5);
-    if (row >= p.rows) return;
+    const size_t row = blockIdx.x;
+    for (int e = threadIdx.x; e < p.parts * p.K; e += blockDim.x) tops[e] = p.part_top[row * p.parts * p.K + e];
+    __syncthreads();
+    if (threadIdx.x >= 32) return;
     const float c = p.inv_t * kLog2e;
     Sums v = {-INFINITY, 0.f, 0.f, 0};
 #pragma unroll
@@ -295,27 +332,27 @@ __global__ void __launch_bounds__(128) logprobs_join_kernel(const LogprobParams 
             v = h ? joined(v, u, c) : u;
         }
     v = joined_warp(v, c);
-    const bool bad = !(v.s < INFINITY) || v.m == -INFINITY;
-    const float nan = __int_as_float(0x7FFFFFFF), lse = bad ? nan : logf(v.s);
+    const RowResults res(v, p.inv_t);
     if (lane == 0) {
         const int target = p.targets ? p.targets[row] : -1;
-        row_results(p, row, v, target, target_logit<T>(p, row, target));
+        res.write(p, row, v, target, target_logit<T>(p, row, target));
     }
-    const unsigned long long* tops = p.part_top + row * p.parts * p.K;
     int at[2] = {0, 0};
     unsigned long long head[2];
 #pragma unroll
-    for (int h = 0; h < 2; ++h) head[h] = p.K > 0 && lane + h * 32 < p.parts ? tops[(size_t)(lane + h * 32) * p.K] : 0ull;
+    for (int h = 0; h < 2; ++h) head[h] = p.K > 0 && lane + h * 32 < p.parts ? tops[(lane + h * 32) * p.K] : 0ull;
+    unsigned long long mine[2] = {0ull, 0ull};  // lane l keeps the l-th and the (l + 32)-th best
     for (int k = 0; k < p.K; ++k) {
         const unsigned long long best = warp_largest(max(head[0], head[1]));
 #pragma unroll
-        for (int h = 0; h < 2; ++h)
-            if (head[h] == best && best != 0ull) head[h] = ++at[h] < p.K ? tops[(size_t)(lane + h * 32) * p.K + at[h]] : 0ull;
-        if (lane == 0) {
-            p.top_tokens[row * p.K + k] = bad ? -1 : key_token(best);
-            p.top_logp[row * p.K + k] = bad ? nan : (key_logit(best) - v.m) * p.inv_t - lse;
+        for (int h = 0; h < 2; ++h) {
+            if (head[h] == best && best != 0ull) head[h] = ++at[h] < p.K ? tops[(lane + h * 32) * p.K + at[h]] : 0ull;
+            if (k == lane + h * 32) mine[h] = best;
         }
     }
+#pragma unroll
+    for (int h = 0; h < 2; ++h)
+        if (lane + h * 32 < p.K) res.write_top(p, row, lane + h * 32, mine[h]);
 }
 
 // Parts of a row: enough CTAs for eight per SM, a tile at least in each.
@@ -327,7 +364,7 @@ static int logprob_parts(int rows, int V) {
 template <typename T>
 static void launch_logprobs(const LogprobParams& p, cudaStream_t stream) {
     launch_pdl(logprobs_kernel<T>, p.rows * p.parts, kLpThreads, 0, stream, p);
-    if (p.parts > 1) launch_pdl(logprobs_join_kernel<T>, (p.rows + 3) / 4, 128, 0, stream, p);
+    if (p.parts > 1) launch_pdl(logprobs_join_kernel<T>, p.rows, 128, 0, stream, p);
 }
 
 }  // namespace tsv
