@@ -9,7 +9,7 @@
 //
 // The top k are exact.  Logits above a bound that k logits are known to reach go to a list in shared memory: in the first tile the
 // bound is the smallest over the 8 warps of each one's ceil(k / 8)-th largest thread maximum, then the k-th best of the list, which is
-// cut back to k between groups of 1, 1, 2, 4, 8, 8 ... tiles (no barrier inside a group: one per tile cost a third of the time).  Of
+// cut back to k between groups of 1, 1, 2, 4, 8, 16, 16 ... tiles (no barrier inside a group: one per tile cost a third of the time).  Of
 // logits in no particular order a few hundred pass.  Where a group's do not fit (an ascending row, many equal ones), its tiles
 // are read again, each bounded by the k-th largest of the 256 threads' maxima, above which no more than 16 k logits can
 // lie.  Candidates are 64-bit keys (value, then lower index), so ties need no care.
@@ -26,7 +26,8 @@ constexpr int kLpTile = kLpThreads * kLpPer;
 constexpr int kLpMaxTop = 64;
 constexpr int kLpMaxParts = 64;
 constexpr int kLpList = 2048;                    // candidates; 16 x 64 + 64 at least
-constexpr int kLpGroup = 8;                      // tiles between two looks at the list
+constexpr int kLpPerSm = 5;                       // CTAs resident on an SM
+constexpr int kLpGroup = 16;                     // tiles between two looks at the list
 constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
 
 struct LogprobParams {
@@ -68,17 +69,28 @@ __device__ __forceinline__ Sums joined_warp(Sums v, float c) {
 
 __device__ __forceinline__ int power_of_two(int n) { return 1 << (32 - __clz(n - 1)); }  // at least n >= 1
 
-// Sorts n keys (a power of two) in shared memory, largest first; the whole CTA.
-__device__ __forceinline__ void sort_keys(unsigned long long* key, int n) {
+// Sorts n keys (a power of two) in shared memory, largest first: the whole CTA, or up to 128 keys its first warp alone (a barrier of
+// the CTA for each of the 21 steps of 64 keys had been a seventh of a row's instructions).  A barrier follows.
+template <int THREADS>
+__device__ __forceinline__ void sort_steps(unsigned long long* key, int n) {
     for (int size = 2; size <= n; size <<= 1)
         for (int step = size >> 1; step > 0; step >>= 1) {
-            for (int e = threadIdx.x; e < n / 2; e += kLpThreads) {
+            for (int e = threadIdx.x; e < n / 2; e += THREADS) {
                 const int i = ((e & ~(step - 1)) << 1) | (e & (step - 1)), j = i | step;
                 const unsigned long long a = key[i], b = key[j];
                 if ((a < b) == ((i & size) == 0)) key[i] = b, key[j] = a;
             }
-            __syncthreads();
+            if constexpr (THREADS == 32) __syncwarp();
+            else __syncthreads();
         }
+}
+__device__ __forceinline__ void sort_keys(unsigned long long* key, int n) {
+    if (n > 128) {
+        sort_steps<kLpThreads>(key, n);
+    } else {
+        if (threadIdx.x < 32) sort_steps<32>(key, n);
+        __syncthreads();
+    }
 }
 
 // 16 bytes of logits as fp32.
@@ -147,7 +159,7 @@ __device__ __forceinline__ void load_tile(const T* x0, int at, int V, bool insid
 }
 
 template <typename T>
-__global__ void __launch_bounds__(kLpThreads, 4) logprobs_kernel(const LogprobParams p) {
+__global__ void __launch_bounds__(kLpThreads, kLpPerSm) logprobs_kernel(const LogprobParams p) {
     griddep_begin();
     constexpr int W = 16 / sizeof(T);
     __shared__ unsigned long long list[kLpList], maxima[kLpThreads];
@@ -172,14 +184,17 @@ __global__ void __launch_bounds__(kLpThreads, 4) logprobs_kernel(const LogprobPa
     // element k of this thread's 16 in a tile is logit first(tile) + (k / W) * 256 W + k % W
     auto first = [&](int tile) { return tile * kLpTile + tid * W - lead; };
     auto inside = [&](int tile) { return tile * kLpTile >= lead && (tile + 1) * kLpTile - lead <= p.V; };
+    // candidates among a thread's 16; each is read again, rather than selected from 16 registers
     auto append = [&](const float (&x)[kLpPer], int at, auto&& wanted) {
+        uint32_t mask = 0u;
 #pragma unroll
-        for (int k = 0; k < kLpPer; ++k) {
-            const int i = at + (k / W) * kLpThreads * W + k % W;
-            if (wanted(x[k], i) && i >= 0 && i < p.V) {
-                const int to = atomicAdd(&filled, 1);
-                if (to < kLpList) list[to] = logit_key(x[k], i);
-            }
+        for (int k = 0; k < kLpPer; ++k) mask |= wanted(x[k], at + (k / W) * kLpThreads * W + k % W) ? 1u << k : 0u;
+        while (mask) {
+            const int k = __ffs(mask) - 1, i = at + (k / W) * kLpThreads * W + k % W;
+            mask &= mask - 1;
+            if (i < 0 || i >= p.V) continue;
+            const int to = atomicAdd(&filled, 1);
+            if (to < kLpList) list[to] = logit_key(RowType<T>::to_f32(x0[i]), i);
         }
     };
     Sums v = {-INFINITY, 0.f, 0.f, 0};
@@ -314,12 +329,20 @@ __device__ __forceinline__ unsigned long long warp_largest(unsigned long long k)
 // A CTA per row joins its parts: the sums in the parts' order, the sorted lists (brought to shared memory first) by taking the
 // largest head K times.  Lane l of the first warp holds the parts l and l + 32.
 template <typename T>
-__global__ void __launch_bounds__(128) logprobs_join_kernel(const LogprobParams p) {
+__global__ void __launch_bounds__(kLpThreads) logprobs_join_kernel(const LogprobParams p) {
     griddep_begin();
     __shared__ unsigned long long tops[kLpMaxParts * kLpMaxTop];
     const int lane = threadIdx.x & 31;
     const size_t row = blockIdx.x;
-    for (int e = threadIdx.x; e < p.parts * p.K; e += blockDim.x) tops[e] = p.part_top[row * p.parts * p.K + e];
+    const unsigned long long* from = p.part_top + row * p.parts * p.K;
+    for (int e = threadIdx.x; e < p.parts * p.K; e += 8 * kLpThreads) {  // eight loads under way
+        unsigned long long key[8];
+#pragma unroll
+        for (int j = 0; j < 8; ++j) key[j] = e + j * kLpThreads < p.parts * p.K ? from[e + j * kLpThreads] : 0ull;
+#pragma unroll
+        for (int j = 0; j < 8; ++j)
+            if (e + j * kLpThreads < p.parts * p.K) tops[e + j * kLpThreads] = key[j];
+    }
     __syncthreads();
     if (threadIdx.x >= 32) return;
     const float c = p.inv_t * kLog2e;
@@ -355,16 +378,16 @@ __global__ void __launch_bounds__(128) logprobs_join_kernel(const LogprobParams 
         if (lane + h * 32 < p.K) res.write_top(p, row, lane + h * 32, mine[h]);
 }
 
-// Parts of a row: enough CTAs for eight per SM, a tile at least in each.
+// Parts of a row: as many as fill the GPU once, a tile at least in each.
 static int logprob_parts(int rows, int V) {
-    const int tiles = (V + kLpTile - 1) / kLpTile, want = (int)(((long long)sm_count() * 4 + rows - 1) / rows);
+    const int tiles = (V + kLpTile - 1) / kLpTile, want = sm_count() * kLpPerSm / rows;
     return std::max(1, std::min({want, tiles, kLpMaxParts}));
 }
 
 template <typename T>
 static void launch_logprobs(const LogprobParams& p, cudaStream_t stream) {
     launch_pdl(logprobs_kernel<T>, p.rows * p.parts, kLpThreads, 0, stream, p);
-    if (p.parts > 1) launch_pdl(logprobs_join_kernel<T>, p.rows, 128, 0, stream, p);
+    if (p.parts > 1) launch_pdl(logprobs_join_kernel<T>, p.rows, kLpThreads, 0, stream, p);
 }
 
 }  // namespace tsv
