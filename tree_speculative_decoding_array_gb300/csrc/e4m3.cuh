@@ -12,8 +12,7 @@ constexpr float kE4Inv = 1.f / 448.f;  // 448: the largest e4m3 value
 
 __host__ __device__ constexpr int e4_blocks(int n) { return n / kE4Block + (n % kE4Block != 0); }
 
-// 8 consecutive features of a row as fp32, and back (rounded once).  T: uint16_t-sized bf16 / fp16 or float; `n` of the 8
-// are inside the row; VEC: all 8 are and the address is a multiple of the vector's bytes.
+// Row types: to and from fp32 (rounded once), one by one and, 16-bit types, two at a time.
 template <typename T>
 struct RowType;
 template <>
@@ -46,12 +45,10 @@ struct RowType<float> {
     static __device__ __forceinline__ float from_f32(float x) { return x; }
 };
 
-template <typename T, bool VEC>
-__device__ __forceinline__ void load8(const T* p, int n, float (&v)[8]) {
-    if constexpr (!VEC) {
-#pragma unroll
-        for (int j = 0; j < 8; ++j) v[j] = j < n ? RowType<T>::to_f32(p[j]) : 0.f;
-    } else if constexpr (sizeof(T) == 4) {
+// 8 features from an address that is a multiple of 16 bytes.
+template <typename T>
+__device__ __forceinline__ void load8(const T* p, float (&v)[8]) {
+    if constexpr (sizeof(T) == 4) {
         const float4 a = reinterpret_cast<const float4*>(p)[0], b = reinterpret_cast<const float4*>(p)[1];
         v[0] = a.x, v[1] = a.y, v[2] = a.z, v[3] = a.w, v[4] = b.x, v[5] = b.y, v[6] = b.z, v[7] = b.w;
     } else {
@@ -63,6 +60,7 @@ __device__ __forceinline__ void load8(const T* p, int n, float (&v)[8]) {
     }
 }
 
+// 8 features, VEC: to an address that is a multiple of 16 bytes; else the first n of them, one by one.
 template <typename T, bool VEC>
 __device__ __forceinline__ void store8(T* p, int n, const float (&v)[8]) {
     if constexpr (!VEC) {
@@ -78,37 +76,38 @@ __device__ __forceinline__ void store8(T* p, int n, const float (&v)[8]) {
     }
 }
 
-// The 16 lanes of a half-warp hold the 128 features of one group, 8 each (zeros past the row's end): codes and scale.
-// The maximum is taken over the bits of |y|, so that a NaN, whose bits are above infinity's, is not lost.
-__device__ __forceinline__ float group_scale(const float (&y)[8]) {
-    uint32_t m = 0u;
-#pragma unroll
-    for (int j = 0; j < 8; ++j) m = max(m, __float_as_uint(y[j]) & 0x7FFFFFFFu);
-#pragma unroll
-    for (int o = 8; o > 0; o >>= 1) m = max(m, __shfl_xor_sync(0xFFFFFFFFu, m, o));
-    return __fmul_rn(__uint_as_float(m), kE4Inv);
+// The larger magnitude of two values, with some sign; a NaN if either is one.
+__device__ __forceinline__ float larger_magnitude(float a, float b) {
+    float m;
+    asm("max.NaN.xorsign.abs.f32 %0, %1, %2;" : "=f"(m) : "f"(a), "f"(b));
+    return m;
 }
+// A group's scale from its largest magnitude.
+__device__ __forceinline__ float e4_scale(float largest) { return __fmul_rn(fabsf(largest), kE4Inv); }
+__device__ __forceinline__ bool e4_ordinary(float scale) { return scale >= 0x1p-100f && scale <= 0x1p100f; }
 
-__device__ __forceinline__ uint2 group_codes(const float (&y)[8], float scale) {
-    uint32_t w[4];
+// y / scale in fp32, rounded to nearest, for N of a group's values.  Where scale is an ordinary number the quotient is y r with one
+// residual step, r the rounded reciprocal: correctly rounded unless scale's significand is all ones (Markstein, "Computation of
+// elementary functions on the IBM RISC System/6000 processor", 1990), and three instructions where a division takes about ten.  A
+// residual that underflows belongs to a quotient far below the smallest code.
+template <int N>
+__device__ __forceinline__ void group_quotients(const float* y, float scale, float* q) {
+    if (e4_ordinary(scale) && (__float_as_uint(scale) & 0x7FFFFFu) != 0x7FFFFFu) {
+        const float r = __frcp_rn(scale);
 #pragma unroll
-    for (int j = 0; j < 4; ++j) {
-        const float2 q = scale == 0.f ? make_float2(0.f, 0.f)
-                                      : make_float2(__fdiv_rn(y[2 * j], scale), __fdiv_rn(y[2 * j + 1], scale));
-        w[j] = __nv_cvt_float2_to_fp8x2(q, __NV_SATFINITE, __NV_E4M3);
-    }
-    return make_uint2(w[0] | (w[1] << 16), w[2] | (w[3] << 16));
-}
-
-template <bool VEC>
-__device__ __forceinline__ void store_codes(uint8_t* p, int n, uint2 c) {
-    if constexpr (VEC) {
-        *reinterpret_cast<uint2*>(p) = c;
+        for (int j = 0; j < N; ++j) {
+            const float p = __fmul_rn(y[j], r);
+            q[j] = fmaf(fmaf(-p, scale, y[j]), r, p);
+        }
     } else {
 #pragma unroll
-        for (int j = 0; j < 8; ++j)
-            if (j < n) p[j] = (uint8_t)((j < 4 ? c.x >> (8 * j) : c.y >> (8 * (j - 4))) & 0xFFu);
+        for (int j = 0; j < N; ++j) q[j] = scale == 0.f ? 0.f : __fdiv_rn(y[j], scale);
     }
+}
+
+// Two quotients' codes, the first in the low byte.
+__device__ __forceinline__ uint32_t e4_pair(float a, float b) {
+    return __nv_cvt_float2_to_fp8x2(make_float2(a, b), __NV_SATFINITE, __NV_E4M3);
 }
 
 // Bytes of an 8-bit copy of `rows` rows of H features: codes, then scales, each rounded up to 256.
