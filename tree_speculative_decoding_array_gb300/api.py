@@ -378,26 +378,34 @@ def _blocks(n):
     return -(-n // 128)
 
 
-def _here(name, dtype, shape, t):
-    """t's address, once it is known to be a contiguous tensor of that type and shape on the current device."""
-    if t.dtype != dtype or t.shape != shape or not t.is_cuda or not t.is_contiguous():
-        _cuda(t, name, dtype, shape)
-    if t.get_device() != torch.cuda.current_device():
-        raise ValueError(f"{name} is on {t.device}, the current device is cuda:{torch.cuda.current_device()}")
-    return t.data_ptr()
+def _here(name, dtype, shape, t, dev):
+    """t's address, once it is known to be a contiguous tensor of that type and shape on the current device `dev`."""
+    if t.dtype is dtype and t.get_device() == dev and t.shape == shape and t.is_contiguous():
+        return t.data_ptr()
+    _cuda(t, name, dtype, shape)
+    raise ValueError(f"{name} is on {t.device}, the current device is cuda:{dev}")
 
 
-def _e4m3(name, t, shape):
+def _e4m3(name, t, shape, dev):
     """An e4m3 buffer: torch.float8_e4m3fn, or uint8 with the same bytes."""
-    return _here(name, torch.uint8 if t.dtype == torch.uint8 else torch.float8_e4m3fn, shape, t)
+    return _here(name, torch.uint8 if t.dtype is torch.uint8 else torch.float8_e4m3fn, shape, t, dev)
+
+
+def _device_stream(stream):
+    """The current device (-2, which no tensor is on, where CUDA is not in use) and the handle of a stream on it."""
+    if not torch.cuda.is_initialized():
+        return -2, None
+    dev = torch._C._cuda_getDevice()
+    return dev, torch._C._cuda_getCurrentRawStream(dev) if stream is None else stream.cuda_stream
 
 
 def _e4m3_head(hidden, W, scales, V, H):
-    _here("hidden", torch.bfloat16, hidden.shape, hidden)
-    _e4m3("W", W, (V, H))
+    dev, _ = _device_stream(None)
+    _here("hidden", torch.bfloat16, hidden.shape, hidden, dev)
+    _e4m3("W", W, (V, H), dev)
     if scales is None:
         raise ValueError("an e4m3 head needs scales")
-    _here("scales", torch.float32, (_blocks(V), _blocks(H)), scales)
+    _here("scales", torch.float32, (_blocks(V), _blocks(H)), scales, dev)
 
 
 def _row_dtype(name, t):
@@ -417,54 +425,60 @@ def add_rms_norm(x, weight, *, eps, residual=None, residual_out=None, out=None, 
     residual_out = h, out = y, and y as 8-bit rows: out8 (float8_e4m3fn or uint8) [rows, H] with out8_scale fp32
     [rows, ceil(H/128)].  residual_out may be residual or x, out may be x or residual.
     """
-    dt, shape = _row_dtype("x", x), x.shape
+    dt, shape, kind = _row_dtype("x", x), x.shape, x.dtype
     rows, H = shape
-    kind = x.dtype
     if (out8 is None) != (out8_scale is None):
         raise ValueError("out8 and out8_scale belong together")
+    dev, st = _device_stream(stream)
     check(load().tsv_add_rms_norm(
-        _here("x", kind, shape, x), None if residual is None else _here("residual", kind, shape, residual),
-        _here("weight", kind, (H,), weight), rows, H, dt, eps, weight_offset,
-        None if residual_out is None else _here("residual_out", kind, shape, residual_out),
-        None if out is None else _here("out", kind, shape, out), None if out8 is None else _e4m3("out8", out8, shape),
-        None if out8 is None else _here("out8_scale", torch.float32, (rows, _blocks(H)), out8_scale), _stream(stream)),
-        "add_rms_norm")
+        _here("x", kind, shape, x, dev), None if residual is None else _here("residual", kind, shape, residual, dev),
+        _here("weight", kind, (H,), weight, dev), rows, H, dt, eps, weight_offset,
+        None if residual_out is None else _here("residual_out", kind, shape, residual_out, dev),
+        None if out is None else _here("out", kind, shape, out, dev), None if out8 is None else _e4m3("out8", out8, shape, dev),
+        None if out8 is None else _here("out8_scale", torch.float32, (rows, -(-H // 128)), out8_scale, dev), st), "add_rms_norm")
 
 
 def quantize_e4m3(x, out8, out8_scale, stream=None):
     """8-bit rows of x [rows, H] (bf16, fp16 or fp32): e4m3 codes and an fp32 scale for every 128 features."""
     dt, (rows, H) = _row_dtype("x", x), x.shape
-    check(load().tsv_quantize_e4m3(_here("x", x.dtype, x.shape, x), rows, H, dt, _e4m3("out8", out8, x.shape),
-                                   _here("out8_scale", torch.float32, (rows, _blocks(H)), out8_scale), _stream(stream)),
-          "quantize_e4m3")
+    dev, st = _device_stream(stream)
+    check(load().tsv_quantize_e4m3(_here("x", x.dtype, x.shape, x, dev), rows, H, dt, _e4m3("out8", out8, x.shape, dev),
+                                   _here("out8_scale", torch.float32, (rows, _blocks(H)), out8_scale, dev), st), "quantize_e4m3")
+
+
+def _product(a, a_scale, w, w_scale, dev):
+    """The operands of a product as the C calls take them, and its shape."""
+    (rows, K), N = a.shape, w.shape[0]
+    kb = -(-K // 128)
+    return (_e4m3("a", a, (rows, K), dev), _here("a_scale", torch.float32, (rows, kb), a_scale, dev), rows, K, _e4m3("w", w, (N, K), dev),
+            _here("w_scale", torch.float32, (-(-N // 128), kb), w_scale, dev), N)
 
 
 def matmul_e4m3(a, a_scale, w, w_scale, out, stream=None):
     """out [rows, N] (bf16, fp16 or fp32) = 8-bit rows a [rows, K], a_scale [rows, ceil(K/128)] times e4m3 weights w [N, K],
     w_scale [ceil(N/128), ceil(K/128)]."""
     dt = _row_dtype("out", out)
-    (rows, K), N = a.shape, w.shape[0]
-    check(load().tsv_matmul_e4m3(
-        _e4m3("a", a, (rows, K)), _here("a_scale", torch.float32, (rows, _blocks(K)), a_scale), rows, K, _e4m3("w", w, (N, K)),
-        _here("w_scale", torch.float32, (_blocks(N), _blocks(K)), w_scale), N, _here("out", out.dtype, (rows, N), out), dt,
-        _stream(stream)), "matmul_e4m3")
+    dev, st = _device_stream(stream)
+    args = _product(a, a_scale, w, w_scale, dev)
+    check(load().tsv_matmul_e4m3(*args, _here("out", out.dtype, (args[2], args[6]), out, dev), dt, st), "matmul_e4m3")
 
 
 def matmul_e4m3_argmax(a, a_scale, w, w_scale, argmax, *, maxval=None, workspace=None, stream=None):
     """The same product's largest value of every row and its column: argmax int32 [rows], maxval fp32 [rows]."""
     lib = load()
-    (rows, K), N = a.shape, w.shape[0]
+    dev, st = _device_stream(stream)
+    args = _product(a, a_scale, w, w_scale, dev)
+    rows = args[2]
     if workspace is None:
         workspace = torch.empty(max(lib.tsv_matmul_e4m3_argmax_workspace_size(rows), 256), dtype=torch.uint8, device=a.device)
     check(lib.tsv_matmul_e4m3_argmax(
-        _e4m3("a", a, (rows, K)), _here("a_scale", torch.float32, (rows, _blocks(K)), a_scale), rows, K, _e4m3("w", w, (N, K)),
-        _here("w_scale", torch.float32, (_blocks(N), _blocks(K)), w_scale), N, _here("argmax", torch.int32, (rows,), argmax),
-        None if maxval is None else _here("maxval", torch.float32, (rows,), maxval), *_workspace(workspace), _stream(stream)),
+        *args, _here("argmax", torch.int32, (rows,), argmax, dev),
+        None if maxval is None else _here("maxval", torch.float32, (rows,), maxval, dev), *_workspace(workspace, dev), st),
         "matmul_e4m3_argmax")
 
 
-def _workspace(t):
-    return _here("workspace", t.dtype, t.shape, t), t.numel() * t.element_size()
+def _workspace(t, dev):
+    return _here("workspace", t.dtype, t.shape, t, dev), t.numel() * t.element_size()
 
 
 def token_logprobs_workspace_size(rows: int, V: int, top_k: int) -> int:
@@ -488,13 +502,15 @@ def token_logprobs(logits, targets=None, logp=None, *, rank=None, entropy=None, 
     lib = load()
     if workspace is None:
         workspace = torch.empty(max(token_logprobs_workspace_size(rows, V, k), 256), dtype=torch.uint8, device=logits.device)
-    vec = lambda name, t, dt: None if t is None else _here(name, dt, (rows,), t)  # noqa: E731
+    dev, st = _device_stream(stream)
+    f32, i32, each = torch.float32, torch.int32, (rows,)
     check(lib.tsv_token_logprobs(
-        _here("logits", logits.dtype, logits.shape, logits), dt, rows, V, vec("targets", targets, torch.int32), temperature, k,
-        vec("logp", logp, torch.float32), vec("rank", rank, torch.int32), vec("entropy", entropy, torch.float32),
-        None if k == 0 else _here("top_tokens", torch.int32, (rows, k), top_tokens),
-        None if k == 0 else _here("top_logp", torch.float32, (rows, k), top_logp), *_workspace(workspace), _stream(stream)),
-        "token_logprobs")
+        _here("logits", logits.dtype, logits.shape, logits, dev), dt, rows, V,
+        None if targets is None else _here("targets", i32, each, targets, dev), temperature, k,
+        None if logp is None else _here("logp", f32, each, logp, dev), None if rank is None else _here("rank", i32, each, rank, dev),
+        None if entropy is None else _here("entropy", f32, each, entropy, dev),
+        None if k == 0 else _here("top_tokens", i32, (rows, k), top_tokens, dev),
+        None if k == 0 else _here("top_logp", f32, (rows, k), top_logp, dev), *_workspace(workspace, dev), st), "token_logprobs")
 
 
 # ----------------------------------------------------------------------------- one verify round
