@@ -37,7 +37,7 @@ struct MmParams {
 
 template <int BN, bool PAIR>
 struct MmShape {
-    static constexpr int kEpiWarps = BN >= 128 ? 8 : 4;
+    static constexpr int kEpiWarps = BN == 256 ? 16 : BN == 128 ? 8 : 4;
     static constexpr int kCols = BN / (kEpiWarps / 4);  // columns of an epilogue thread
     static constexpr int kPerSm = BN >= 128 ? 1 : 3;
     // A tile's columns are kParts MMAs of kPart columns, each with accumulators, barriers, an issuing warp and a warpgroup of its
@@ -50,10 +50,11 @@ struct MmShape {
     // then reads the scales ahead of the epilogue, which has neither the registers nor the time.
     static constexpr bool kWide = BN == 256;
     static constexpr int kIssuers = BN >= 128 ? 2 : 1;
-    static constexpr int kThreads = kWide ? 384 : (kEpiWarps + 1 + kIssuers) * 32;
+    static constexpr int kThreads = (kEpiWarps + (kWide ? 4 : 1 + kIssuers)) * 32;
     static constexpr int kScaleBytes = kWide ? 2 * 4 * 2 * 128 * 4 : 0;   // two groups of 4 blocks, two weight blocks, 128 rows
-    static constexpr int kOutBytes = kEpiWarps == 8 ? kEpiWarps * 4096 : 0;  // 32 rows x 128 bytes of output per warp
-    static constexpr bool kAhead = kPerSm == 1;
+    static constexpr int kPiece = kWide ? 64 : 128;                        // bytes of an output row that a warp gathers
+    static constexpr int kOutBytes = BN >= 128 ? kEpiWarps * 32 * kPiece : 0;
+    static constexpr bool kAhead = BN == 128;
     static constexpr int kSmem = (kPerSm == 1 ? 224 : 72) * 1024;
     static constexpr int kRing = kSmem - 1024 - kScaleBytes - kOutBytes;
 };
@@ -91,44 +92,43 @@ __device__ __forceinline__ void store_row(T* o, const float (&acc)[COLS], int n,
     }
 }
 
-// A warp's 32 rows of COLS sums through its 4 KB of shared memory, 128 bytes of every row at a time, so that a store covers
-// four whole 128-byte pieces (a thread's own row, written by itself, costs a 32-byte sector for every 16 bytes: 10,000 SM
-// clocks for a tile of 128 x 256 bf16, half of what its products take).  `rows`, `n`: what is left of the matrix from o on.
-template <typename T, int COLS>
-__device__ __forceinline__ void store_rows(T* o, const float (&acc)[COLS], size_t ld, int rows, int n, bool vec,
-                                           uint8_t* buf, int lane) {
-    constexpr int P = 128 / sizeof(T), V = 16 / sizeof(T);  // elements of a piece, of a 16-byte vector
+// A warp's 32 rows of COLS sums through its shared memory, BYTES of every row at a time, so that a store covers whole 64- or 128-byte
+// pieces of rows (a thread's own row, written by itself, costs a 32-byte sector for every 16 bytes: 10,000 SM clocks for a tile of
+// 128 x 256 bf16, half of what its products take).  `rows`, `n`: what is left of the matrix from o on.
+template <typename T, int COLS, int BYTES>
+__device__ __forceinline__ void store_rows(T* o, const float (&acc)[COLS], size_t ld, int rows, int n, bool vec, uint8_t* buf, int lane) {
+    constexpr int P = BYTES / sizeof(T), V = 16 / sizeof(T), J = BYTES / 16;  // elements of a piece, of a 16-byte vector, vectors of a piece
+    // vector j of row r: no two of 8 lanes in one bank, as they write (a row each) and as they read (J to a row)
+    const auto place = [&](int r, int j) { return buf + r * BYTES + ((j ^ (r * J / 8 & (J - 1))) << 4); };
 #pragma unroll
     for (int c = 0; c < COLS; c += P) {
         if (c >= n) break;
 #pragma unroll
-        for (int j = 0; j < 8; ++j) {
+        for (int j = 0; j < J; ++j) {
             uint4 u;
             if constexpr (sizeof(T) == 4) {
                 const float* x = acc + c + 4 * j;
                 u = make_uint4(__float_as_uint(x[0]), __float_as_uint(x[1]), __float_as_uint(x[2]), __float_as_uint(x[3]));
             } else {
-                float v[8];
-                sums8(acc + c + 8 * j, v);
-                u = make_uint4(RowType<T>::pack(v[0], v[1]), RowType<T>::pack(v[2], v[3]), RowType<T>::pack(v[4], v[5]),
-                               RowType<T>::pack(v[6], v[7]));
+                const float* x = acc + c + 8 * j;
+                u = make_uint4(RowType<T>::pack(x[0], x[1]), RowType<T>::pack(x[2], x[3]), RowType<T>::pack(x[4], x[5]),
+                               RowType<T>::pack(x[6], x[7]));
             }
-            *reinterpret_cast<uint4*>(buf + lane * 128 + ((j ^ (lane & 7)) << 4)) = u;  // no two of 8 lanes in one bank
+            *reinterpret_cast<uint4*>(place(lane, j)) = u;
         }
         __syncwarp();
         if (vec) {
 #pragma unroll
-            for (int i = 0; i < 8; ++i) {
-                const int r = i * 4 + (lane >> 3), j = lane & 7, at = c + j * V;
-                const uint4 u = *reinterpret_cast<const uint4*>(buf + r * 128 + ((j ^ (r & 7)) << 4));
+            for (int i = 0; i < J; ++i) {
+                const int r = (i * 32 + lane) / J, j = lane % J, at = c + j * V;
+                const uint4 u = *reinterpret_cast<const uint4*>(place(r, j));
                 if (r < rows && at < n) *reinterpret_cast<uint4*>(o + (size_t)r * ld + at) = u;  // n is a multiple of V
             }
         } else {  // rows at any address: neighbouring lanes write neighbouring elements
             for (int r = 0; r < min(rows, 32); ++r)
 #pragma unroll
                 for (int k = lane; k < P; k += 32)
-                    if (c + k < n)
-                        o[(size_t)r * ld + c + k] = *reinterpret_cast<const T*>(buf + r * 128 + (((k / V) ^ (r & 7)) << 4) + k % V * sizeof(T));
+                    if (c + k < n) o[(size_t)r * ld + c + k] = *reinterpret_cast<const T*>(place(r, k / V) + k % V * sizeof(T));
         }
         __syncwarp();
     }
@@ -196,7 +196,7 @@ __global__ void __launch_bounds__(MmShape<BN, PAIR>::kThreads, MmShape<BN, PAIR>
     };
 
     if (warp >= S::kEpiWarps) {
-        if constexpr (S::kWide) asm volatile("setmaxnreg.dec.sync.aligned.u32 88;");
+        if constexpr (S::kWide) asm volatile("setmaxnreg.dec.sync.aligned.u32 64;");
         if (warp == S::kEpiWarps) {
             // -------------------------------------------------------- producer
             int st = 0, issued = 0;
@@ -237,7 +237,7 @@ __global__ void __launch_bounds__(MmShape<BN, PAIR>::kThreads, MmShape<BN, PAIR>
             int st = kTurns > 1 ? i % ST : 0, buf = kTurns > 1 ? i : 0;
             uint32_t ph = kTurns > 1 ? (i / ST) & 1 : 0, use = 0;  // parities of the stage's fill and of the accumulator's use
             for (long long g = kTurns > 1 ? i : 0; g < todo; g += kTurns) {
-                if (!tc::mbar_wait_warp(tc::smem_u32(&part_empty[buf]), use ^ 1u, tc::smem_u32(&full[st]), ph, abort_flag)) break;
+                if (!tc::mbar_wait_warp(tc::smem_u32(&full[st]), ph, tc::smem_u32(&part_empty[buf]), use ^ 1u, abort_flag)) break;
                 tc::tc_fence_after();
                 const uint64_t da = tc::sdesc_add(d0, (uint32_t)st * q.stage_bytes), db = tc::sdesc_add(da, b_off);
                 tc::mma_e4m3_block<PAIR>(tm + buf * BN, da, db, idesc, &empty[st], &part_full[buf]);
@@ -291,13 +291,14 @@ __global__ void __launch_bounds__(MmShape<BN, PAIR>::kThreads, MmShape<BN, PAIR>
             }
         }
     } else {
-        if constexpr (S::kWide) asm volatile("setmaxnreg.inc.sync.aligned.u32 208;");
+        if constexpr (S::kWide) asm volatile("setmaxnreg.inc.sync.aligned.u32 104;");
         // ------------------------------------------------------------ epilogue: scale and add up, then write out
         const int quarter = warp & 3, half = warp >> 2;
         const uint32_t taddr = tmem + ((uint32_t)(quarter * 32) << 16) + half * S::kCols;
-        const uint32_t part = (S::kParts > 1 ? half * S::kBufs : 0) * 8;
+        const int which = half * S::kCols / S::kPart;  // the part that this warp's columns are of
+        const uint32_t part = which * S::kBufs * 8;
         const uint32_t full0 = tc::smem_u32(acc_full) + part, empty0 = PAIR ? tc::cluster_addr(acc_empty, 0) + part : tc::smem_u32(acc_empty) + part;
-        const uint32_t sc0 = tc::smem_u32(scales) + (half * 128 + quarter * 32 + lane) * 4;
+        const uint32_t sc0 = tc::smem_u32(scales) + (which * 128 + quarter * 32 + lane) * 4;
         const E4Product& p = q.p;
         int buf = 0, g = 0;
         uint32_t use = 0, gph = 0;
@@ -324,6 +325,7 @@ __global__ void __launch_bounds__(MmShape<BN, PAIR>::kThreads, MmShape<BN, PAIR>
                 if (ok) tc::tmem_ld16(taddr + buf * BN, d[0]);
             }
             for (int kb = k0; ok && kb < k1; ++kb) {
+                bool there = false;  // the next block's sums, looked at ahead of the wait
                 float sc;
                 if constexpr (S::kWide) {
                     if ((kb & 3) == 0) ok = tc::mbar_wait_warp(tc::smem_u32(&sc_full[g]), gph, abort_flag);
@@ -339,16 +341,15 @@ __global__ void __launch_bounds__(MmShape<BN, PAIR>::kThreads, MmShape<BN, PAIR>
 #pragma unroll
                 for (int c = 0; c < S::kCols / 16; ++c) {
                     uint32_t(&now)[16] = d[S::kAhead ? c & 1 : 0];
+                    if (S::kAhead && c == S::kCols / 16 - 1) there = __all_sync(0xFFFFFFFFu, tc::mbar_test(full0 + (buf + 1 == S::kBufs ? 0 : buf + 1) * 8, buf + 1 == S::kBufs ? use ^ 1u : use));
                     if constexpr (!S::kAhead) tc::tmem_ld16(taddr + buf * BN + c * 16, now);
                     tc::tmem_wait_ld16(now);
                     if (c + 1 == S::kCols / 16) {
                         tc::tc_fence_before();
-                        __syncwarp();
-                        if constexpr (PAIR) tc::mbar_arrive_one_cluster(empty0 + buf * 8);
-                        else tc::mbar_arrive_one(empty0 + buf * 8);
+                        tc::mbar_arrive_lane0<PAIR>(empty0 + buf * 8, lane);
                         if (++buf == S::kBufs) { buf = 0; use ^= 1u; }
                         if (S::kAhead && kb + 1 < k1) {
-                            ok = ok && tc::mbar_wait_warp(full0 + buf * 8, use, abort_flag);
+                            if (!there) ok = ok && tc::mbar_wait_warp(full0 + buf * 8, use, abort_flag);
                             tc::tc_fence_after();
                             tc::tmem_ld16(taddr + buf * BN, d[0]);
                         }
@@ -388,12 +389,12 @@ __global__ void __launch_bounds__(MmShape<BN, PAIR>::kThreads, MmShape<BN, PAIR>
                     if (wins) atomicMax(&p.best[row], pack_best(__uint_as_float(top), (uint32_t)(col + at)));
                 }
             } else if constexpr (S::kOutBytes > 0) {
-                uint8_t* buf4k = outbuf + warp * 4096;
+                uint8_t* piece = outbuf + warp * 32 * S::kPiece;
                 const size_t o = (size_t)row0 * p.N + col;
                 const int rows = p.rows - row0, cols = p.N - col;
-                if (p.out_dtype == TSV_F32) store_rows<float, S::kCols>((float*)p.out + o, acc, p.N, rows, cols, q.vec, buf4k, lane);
-                else if (p.out_dtype == TSV_BF16) store_rows<__nv_bfloat16, S::kCols>((__nv_bfloat16*)p.out + o, acc, p.N, rows, cols, q.vec, buf4k, lane);
-                else store_rows<__half, S::kCols>((__half*)p.out + o, acc, p.N, rows, cols, q.vec, buf4k, lane);
+                if (p.out_dtype == TSV_F32) store_rows<float, S::kCols, S::kPiece>((float*)p.out + o, acc, p.N, rows, cols, q.vec, piece, lane);
+                else if (p.out_dtype == TSV_BF16) store_rows<__nv_bfloat16, S::kCols, S::kPiece>((__nv_bfloat16*)p.out + o, acc, p.N, rows, cols, q.vec, piece, lane);
+                else store_rows<__half, S::kCols, S::kPiece>((__half*)p.out + o, acc, p.N, rows, cols, q.vec, piece, lane);
             } else if (row < p.rows) {
                 const size_t o = (size_t)row * p.N + col;
                 if (p.out_dtype == TSV_F32) store_row<float, S::kCols>((float*)p.out + o, acc, p.N - col, q.vec);

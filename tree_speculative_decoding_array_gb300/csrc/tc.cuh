@@ -56,7 +56,17 @@ __device__ __forceinline__ bool mbar_try_wait(uint64_t* bar, uint32_t parity) {
     return ok != 0;
 }
 
-// Non-blocking test of the phase with the given parity.
+// Non-blocking test of the phase with the given parity, by the barrier's shared-memory address.
+__device__ __forceinline__ bool mbar_test(uint32_t bar, uint32_t parity) {
+    uint32_t ok;
+    asm volatile(
+        "{\n .reg .pred p;\n mbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n selp.u32 %0, 1, 0, p;\n}"
+        : "=r"(ok)
+        : "r"(bar), "r"(parity)
+        : "memory");
+    return ok != 0;
+}
+// The same.
 __device__ __forceinline__ bool mbar_test(uint64_t* bar, uint32_t parity) {
     uint32_t ok;
     asm volatile(
@@ -140,7 +150,8 @@ __device__ __forceinline__ bool mbar_wait_warp(uint32_t bar, uint32_t parity, vo
 __device__ __forceinline__ bool mbar_wait_warp(uint64_t* bar, uint32_t parity, volatile int* abort) {
     return mbar_wait_warp(smem_u32(bar), parity, abort);
 }
-// The same for two barriers, with one vote.
+// The same for two barriers, with one vote where both are through.  bar1 is the one that is waited for longer: bar0 is looked at
+// while it is not, and not after it.
 __device__ __forceinline__ bool mbar_wait_warp(uint32_t bar0, uint32_t parity0, uint32_t bar1, uint32_t parity1, volatile int* abort) {
     const bool a = mbar_try_wait(bar0, parity0), b = mbar_try_wait(bar1, parity1);
     if (__all_sync(0xFFFFFFFFu, a && b)) return true;
@@ -167,6 +178,16 @@ __device__ __forceinline__ float4 ld_cluster_f4(uint32_t addr) {
     float4 v;
     asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];" : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w) : "r"(addr) : "memory");
     return v;
+}
+// Lane 0 of the converged warp arrives, without an election; of a pair: by the barrier's cluster address, relaxed as below.
+template <bool PAIR>
+__device__ __forceinline__ void mbar_arrive_lane0(uint32_t bar, int lane) {
+    if constexpr (PAIR)
+        asm volatile("{\n .reg .pred p;\n setp.eq.s32 p, %1, 0;\n @p mbarrier.arrive.relaxed.cluster.shared::cluster.b64 _, [%0];\n}" ::"r"(bar),
+                     "r"(lane)
+                     : "memory");
+    else
+        asm volatile("{\n .reg .pred p;\n setp.eq.s32 p, %1, 0;\n @p mbarrier.arrive.shared::cta.b64 _, [%0];\n}" ::"r"(bar), "r"(lane) : "memory");
 }
 // One lane of the converged warp arrives on a barrier anywhere in the cluster.  Relaxed: what it tells of is TMEM reads that have
 // ended, no memory (a release would wait for every store under way, microseconds per arrival).
