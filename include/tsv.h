@@ -554,10 +554,10 @@ tsv_status tsv_gdn_scan(const tsv_gdn_desc* d, const int32_t* cu_len, int32_t ma
  *   x, residual, residual_out, weight, out: `dtype` (TSV_F16, TSV_BF16 or TSV_F32), [rows, H], weight [H].  residual may
  *   be NULL (h = x).  Outputs, each optional but one at least: residual_out = h, out = y, and y as 8-bit rows in out8 (uint8 e4m3
  *   [rows, H]) with out8_scale.  Everything between is fp32 and each output is rounded once from it: y is of the unrounded h, the codes of
- *   the unrounded y.  A row whose squares leave fp32's range is scaled by a power of two first.  residual_out may equal residual or x,
+ *   the unrounded y (their quotients within two units in the last place of fp32).  A row whose squares leave fp32's range is scaled by a power of two first.  residual_out may equal residual or x,
  *   out may equal x or residual; otherwise outputs overlap neither inputs nor each other.
- *   1 <= H <= 32768, 1e-30 <= eps, eps and weight_offset finite.  A NaN or an infinity in a row makes that row's y NaN where it
- *   is not zero.
+ *   1 <= H <= 32768, 1e-30 <= eps, eps and weight_offset finite.  A NaN in a row makes all of its y NaN, an infinity makes
+ *   y NaN there and 0 elsewhere.
  * tsv_quantize_e4m3 - 8-bit rows of x as it is: out8, out8_scale as above (H without an upper limit).
  */
 tsv_status tsv_add_rms_norm(const void* x, const void* residual, const void* weight, int32_t rows, int32_t H, int32_t dtype,
@@ -573,7 +573,7 @@ tsv_status tsv_quantize_e4m3(const void* x, int32_t rows, int32_t H, int32_t dty
  *   a: e4m3 [rows, K], a_scale float [rows, ceil(K / 128)] (8-bit rows as above); w: e4m3 [N, K], w_scale float
  *   [ceil(N / 128), ceil(K / 128)]; out [rows, N] of out_dtype (TSV_BF16, TSV_F16 or TSV_F32).  The products of 128 features are summed on
  *   the tensor cores into fp32, scaled, and summed in fp32; out is rounded once.  The same inputs give the same bits in every call.
- *   K % 16 == 0, a and w 16-byte aligned, rows >= 0, N >= 1.
+ *   K % 16 == 0, a and w 16-byte aligned, 0 <= rows <= 2^30, 1 <= N <= 2^30.
  * tsv_matmul_e4m3_argmax - the same product with its argmax, as tsv_lm_head_argmax: argmax int32 [rows] (ties to the lowest
  *   index), maxval float [rows] or NULL; the products are never written.  Workspace: tsv_matmul_e4m3_argmax_workspace_size.
  *   A product that is NaN counts as larger than every number if its sign bit is clear, and as smaller if it is set.

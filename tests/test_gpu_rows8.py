@@ -87,9 +87,27 @@ def test_norm_parts(gpu_lib):
     check_norm(run_norm(gpu_lib, x, w, r, shift=1), x, w, r)
     odd = torch.empty(9 * 392 + 3, dtype=torch.bfloat16, device=DEV)[3:].view(9, 392).copy_(x)
     check_norm(run_norm(gpu_lib, odd, w, r), x, w, r)
-    x2, r2 = x.clone(), r.clone()
-    gpu_lib.add_rms_norm(x2, w, eps=1e-6, residual=r2, residual_out=r2, out=x2)
-    check_norm(dict(residual_out=r2, out=x2), x, w, r)
+    for rows, H in ((9, 392), (3000, 640), (2500, 5120), (2000, 9000), (70, 17000), (1500, 333)):  # in place, more rows than are under way at once
+        x, r, w = (rnd(*s, seed=k, dtype=torch.bfloat16).to(DEV) for k, s in enumerate([(rows, H), (rows, H), (H,)]))
+        x2, r2 = x.clone(), r.clone()
+        gpu_lib.add_rms_norm(x2, w, eps=1e-6, residual=r2, residual_out=r2, out=x2)
+        check_norm(dict(residual_out=r2, out=x2), x, w, r)
+        x2, r2 = x.clone(), r.clone()
+        gpu_lib.add_rms_norm(x2, w, eps=1e-6, residual=r2, residual_out=x2, out=r2)
+        check_norm(dict(residual_out=x2, out=r2), x, w, r)
+
+
+@pytest.mark.parametrize("H", [100, 256, 512, 1032])
+def test_huge_rows_among_others(gpu_lib, H):
+    """Rows whose squares leave fp32's range beside rows whose do not, where several share a CTA."""
+    x = rnd(2001, H, seed=H)
+    x[::7] *= 1e30
+    x[5, H // 2] = float("inf")
+    x, w = x.to(DEV), rnd(H, seed=1).to(DEV)
+    o = run_norm(gpu_lib, x, w, parts=("out", "out8"))
+    fine = [i for i in range(2001) if i != 5]
+    check_norm({k: v[fine] if v.dtype != F8 else v.view(torch.uint8)[fine].view(F8) for k, v in o.items()}, x[fine], w)
+    assert torch.isnan(o["out"][5, H // 2]) and int(torch.isnan(o["out"][5]).sum()) == 1
 
 
 def test_norm_values_at_the_ends(gpu_lib):
@@ -153,7 +171,9 @@ def product_bound(a, sa, w, sw):
 
 SIZES = [(1, 16, 1), (1, 128, 128), (1, 5120, 520), (2, 272, 129), (5, 1040, 1001), (16, 2048, 640), (17, 400, 130), (33, 384, 1000), (64, 6144, 256),
          (65, 640, 77), (128, 512, 384), (129, 4112, 260), (200, 256, 3000), (257, 144, 520), (400, 1024, 1024), (1, 2560, 20000), (1000, 128, 600),
-         (3, 48, 40000), (96, 1280, 2000), (130, 20480, 130)]
+         (3, 48, 40000), (96, 1280, 2000), (130, 20480, 130),
+         # 64 columns shared by clusters of 8 and 4; CTA pairs, several rounds of them, ragged at both ends
+         (1, 2112, 2666), (33, 2112, 2666), (20, 2384, 4997), (100, 3744, 2666), (1300, 272, 9000), (2500, 1040, 4999), (4100, 400, 5003)]
 
 
 @pytest.mark.parametrize("rows, K, N", SIZES)

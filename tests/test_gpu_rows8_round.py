@@ -96,6 +96,24 @@ def test_sampled_round_captured(gpu_lib):
     assert np.allclose(vr.outs["logp"].cpu().numpy(), want["logp"], atol=1e-4)
 
 
+def test_greedy_round_with_logprobs_captured(gpu_lib):
+    vr, eager = round_of(logprobs=3), round_of(logprobs=3)
+    keep = vr.kv_len.clone(), [t.clone() for t in vr.k + vr.v]
+    vr.run()
+    torch.cuda.synchronize()
+    vr.capture()
+    vr.norm["x"].copy_(eager.norm["x"].flip(0))
+    eager.norm["x"].copy_(vr.norm["x"])
+    vr.kv_len.copy_(keep[0])
+    for t, c in zip(vr.k + vr.v, keep[1]):
+        t.copy_(c)
+    vr.replay()
+    eager.run()
+    torch.cuda.synchronize()
+    for n in ("argmax", "logp", "entropy", "top_tokens", "top_logp", "path", "emitted"):
+        assert torch.equal(vr.outs[n], eager.outs[n]), n
+
+
 def test_norm_ahead_of_a_16_bit_head(gpu_lib):
     g = torch.Generator().manual_seed(5)
     W = torch.randn(V, H, generator=g).bfloat16().to(DEV)

@@ -69,6 +69,7 @@ def no_error_left_behind():
     (matmul, dict(K=136), "EINVAL", b"multiple of 16"), (matmul, dict(dtype=tsv.I4_G64), "EUNSUPPORTED", b"output type"),
     (matmul, dict(a=PTR + 8), "EINVAL", b"16-byte"), (matmul, dict(w=PTR + 8), "EINVAL", b"16-byte"), (matmul, dict(a_scale=PTR + 2), "EINVAL", b"4-byte"),
     (matmul, dict(out=PTR + 1), "EINVAL", b"aligned"), (matmul, dict(out=None), "EINVAL", b"null"), (matmul, dict(w_scale=None), "EINVAL", b"null"),
+    (matmul, dict(rows=(1 << 30) + 1), "ECAPACITY", b"2^30"), (matmul, dict(N=(1 << 30) + 1), "ECAPACITY", b"2^30"),
     (best, dict(K=8), "EINVAL", b"multiple of 16"), (best, dict(argmax=None), "EINVAL", b"null"), (best, dict(ws=None), "EINVAL", b"null"),
     (best, dict(ws=PTR + 8), "EINVAL", b"16-byte"), (best, dict(ws_bytes=255), "ECAPACITY", b"256"),
     (head, dict(H=264), "EINVAL", b"multiple of 16"), (head, dict(scales=None), "EINVAL", b"scales"), (head, dict(scales=PTR + 2), "EINVAL", b"4-byte"),

@@ -62,7 +62,7 @@ __device__ __forceinline__ void load8(const T* p, float (&v)[8]) {
 
 // 8 features, VEC: to an address that is a multiple of 16 bytes; else the first n of them, one by one.
 template <typename T, bool VEC>
-__device__ __forceinline__ void store8(T* p, int n, const float (&v)[8]) {
+__device__ __forceinline__ void store8(T* p, int n, const float* v) {
     if constexpr (!VEC) {
 #pragma unroll
         for (int j = 0; j < 8; ++j)

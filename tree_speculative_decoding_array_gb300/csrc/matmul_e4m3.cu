@@ -45,9 +45,10 @@ struct MmShape {
     static constexpr int kParts = BN == 256 ? 2 : 1, kPart = BN / kParts;
     static constexpr int kBufs = BN == 128 ? 4 : 2;  // accumulators of a part in TMEM
     static constexpr int kBox = kPart / (PAIR ? 2 : 1);  // weights of a part in a CTA's shared memory
-    // 256 columns: an epilogue thread holds 128 sums, so the eight epilogue warps take registers over from a third warpgroup
-    // (producer, two issuers, scales): 256 x 208 + 128 x 88 = 384 x 168.  The third warpgroup's scale warp
-    // then reads the scales ahead of the epilogue, which has neither the registers nor the time.
+    // 256 columns: an epilogue thread holds 64 sums and 16 warps have to share the registers, so they take some over from the last
+    // warpgroup (producer, two issuers, scales): 512 x 104 + 128 x 64 = 640 x 96.  A warp of its own reads the scales ahead
+    // of the epilogue, which has neither the registers nor the time.  (Eight epilogue warps with 128 sums each: 346 us against 337 for
+    // 4096 x 5120 x 20480.)
     static constexpr bool kWide = BN == 256;
     static constexpr int kIssuers = BN >= 128 ? 2 : 1;
     static constexpr int kThreads = (kEpiWarps + (kWide ? 4 : 1 + kIssuers)) * 32;
@@ -59,9 +60,12 @@ struct MmShape {
     static constexpr int kRing = kSmem - 1024 - kScaleBytes - kOutBytes;
 };
 
-__device__ __forceinline__ void sums8(const float* acc, float (&v)[8]) {
-#pragma unroll
-    for (int j = 0; j < 8; ++j) v[j] = acc[j];
+// a += s x, b += s y, in one instruction.
+__device__ __forceinline__ void add_scaled(float& a, float& b, uint32_t x, uint32_t y, float s) {
+    asm("{\n .reg .b64 d, t, f;\n mov.b64 d, {%2, %3};\n mov.b64 t, {%0, %1};\n mov.b64 f, {%4, %4};\n"
+        " fma.rn.f32x2 t, d, f, t;\n mov.b64 {%0, %1}, t;\n}"
+        : "+f"(a), "+f"(b)
+        : "r"(x), "r"(y), "f"(s));
 }
 
 // Bits of the largest of a thread's sums in the order of orderable(): a NaN without a sign above everything, one with a sign
@@ -85,10 +89,8 @@ template <typename T, int COLS>
 __device__ __forceinline__ void store_row(T* o, const float (&acc)[COLS], int n, bool vec) {
 #pragma unroll
     for (int c = 0; c < COLS; c += 8) {
-        float v[8];
-        sums8(acc + c, v);
-        if (vec && c + 8 <= n) store8<T, true>(o + c, 8, v);
-        else store8<T, false>(o + c, n - c, v);
+        if (vec && c + 8 <= n) store8<T, true>(o + c, 8, acc + c);
+        else store8<T, false>(o + c, n - c, acc + c);
     }
 }
 
@@ -298,7 +300,7 @@ __global__ void __launch_bounds__(MmShape<BN, PAIR>::kThreads, MmShape<BN, PAIR>
         const int which = half * S::kCols / S::kPart;  // the part that this warp's columns are of
         const uint32_t part = which * S::kBufs * 8;
         const uint32_t full0 = tc::smem_u32(acc_full) + part, empty0 = PAIR ? tc::cluster_addr(acc_empty, 0) + part : tc::smem_u32(acc_empty) + part;
-        const uint32_t sc0 = tc::smem_u32(scales) + (which * 128 + quarter * 32 + lane) * 4;
+        const uint32_t sc0 = tc::smem_u32(scales) + (half * S::kCols / kE4Block * 128 + quarter * 32 + lane) * 4;
         const E4Product& p = q.p;
         int buf = 0, g = 0;
         uint32_t use = 0, gph = 0;
@@ -357,7 +359,7 @@ __global__ void __launch_bounds__(MmShape<BN, PAIR>::kThreads, MmShape<BN, PAIR>
                         tc::tmem_ld16(taddr + buf * BN + (c + 1) * 16, d[(c + 1) & 1]);
                     }
 #pragma unroll
-                    for (int i = 0; i < 16; ++i) acc[c * 16 + i] = fmaf(sc, __uint_as_float(now[i]), acc[c * 16 + i]);
+                    for (int i = 0; i < 16; i += 2) add_scaled(acc[c * 16 + i], acc[c * 16 + i + 1], now[i], now[i + 1], sc);
                 }
                 if (S::kWide && ((kb & 3) == 3 || kb + 1 == k1)) {
                     __syncwarp();
@@ -546,6 +548,7 @@ tsv_status launch_matmul_e4m3(const char* name, const E4Product& p, cudaStream_t
 static tsv_status check_product(const char* name, const E4Product& p) {
     if (p.rows < 0 || p.K < 1 || p.N < 1) return fail(TSV_EINVAL, "%s: rows=%d K=%d N=%d", name, p.rows, p.K, p.N);
     if (p.K % 16) return fail(TSV_EINVAL, "%s: K=%d not a multiple of 16", name, p.K);
+    if (p.rows > 1 << 30 || p.N > 1 << 30) return fail(TSV_ECAPACITY, "%s: rows=%d N=%d above 2^30", name, p.rows, p.N);
     if (p.rows == 0) return TSV_OK;
     if (!p.a || !p.a_scale || !p.w || !p.w_scale) return fail(TSV_EINVAL, "%s: null pointer argument", name);
     if (((uintptr_t)p.a | (uintptr_t)p.w) & 15) return fail(TSV_EINVAL, "%s: a or w not 16-byte aligned", name);

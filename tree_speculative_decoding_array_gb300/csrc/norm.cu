@@ -9,6 +9,7 @@
 // thread, one by one, had cost three times as much).  Either way a group's maximum needs shuffles and no shared memory.  Short rows share a
 // CTA.
 #include <algorithm>
+#include <atomic>
 
 #include "e4m3.cuh"
 
@@ -271,12 +272,11 @@ template <typename T, int VPT, int THREADS, bool VEC>
 static void launch_norm_as(const NormParams& p, int vecs, cudaStream_t stream) {
     const int threads = ((vecs + VPT - 1) / VPT + 31) / 32 * 32, together = std::max(1, 256 / threads), block = threads * together;
     const auto kernel = rms_norm_kernel<T, VPT, THREADS, VEC>;
-    static int per_sm[THREADS / 32 + 1] = {0};  // CTAs resident on an SM, by the CTA's warps (the same on every device of the build's kind)
-    int& fit = per_sm[block / 32];
+    static std::atomic<int> per_sm[THREADS / 32 + 1];  // CTAs resident on an SM, by the CTA's warps (the same on every GPU of the build's kind)
+    int fit = per_sm[block / 32].load(std::memory_order_relaxed);
     if (fit == 0) {
-        int n = 1;
-        if (cudaOccupancyMaxActiveBlocksPerMultiprocessor(&n, kernel, block, 0) != cudaSuccess || n < 1) n = 1;
-        fit = n;
+        if (cudaOccupancyMaxActiveBlocksPerMultiprocessor(&fit, kernel, block, 0) != cudaSuccess || fit < 1) fit = 1;
+        per_sm[block / 32].store(fit, std::memory_order_relaxed);
     }
     const long long ctas = ((long long)p.rows + together - 1) / together;
     launch_pdl(kernel, (int)std::min<long long>(ctas, (long long)sm_count() * fit), block, 0, stream, p, threads);
