@@ -268,6 +268,21 @@ def test_head(gpu_lib, rows, H, V):
         assert torch.equal(again, arg)
 
 
+@pytest.mark.parametrize("rows, K, N", [(128, 5120, 100000), (100, 640, 40000), (300, 1152, 3000), (2048, 640, 20000), (33, 2112, 2666)])
+def test_the_same_bits_every_time(gpu_lib, rows, K, N):
+    """Many launches, back to back, while copies land in whatever order they do: a hand-off that relies on their order shows here."""
+    g = torch.Generator(device=DEV).manual_seed(rows)
+    byte = lambda *s: torch.randint(0, 120, s, device=DEV, dtype=torch.uint8, generator=g)  # noqa: E731
+    args = byte(rows, K), torch.rand(rows, rows8.blocks(K), device=DEV, generator=g), byte(N, K), torch.rand(rows8.blocks(N), rows8.blocks(K), device=DEV, generator=g)
+    first, out = torch.empty(rows, N, device=DEV), torch.empty(rows, N, device=DEV)
+    gpu_lib.matmul_e4m3(*args, first)
+    for _ in range(12):
+        out.zero_()
+        for _ in range(8):
+            gpu_lib.matmul_e4m3(*args, out)
+        assert torch.equal(out, first)
+
+
 def test_captured_and_on_two_streams(gpu_lib):
     """A norm, a product and an argmax recorded once and replayed on new inputs, and two streams at once."""
     rows, H, N = 24, 1024, 3000

@@ -50,7 +50,7 @@ struct MmShape {
     // of the epilogue, which has neither the registers nor the time.  (Eight epilogue warps with 128 sums each: 346 us against 337 for
     // 4096 x 5120 x 20480.)
     static constexpr bool kWide = BN == 256;
-    static constexpr int kIssuers = BN >= 128 ? 2 : 1;
+    static constexpr int kIssuers = BN >= 128 ? 2 : 1, kTurns = kParts > 1 ? 1 : kIssuers;  // issuers that take turns with the blocks
     static constexpr int kThreads = (kEpiWarps + (kWide ? 4 : 1 + kIssuers)) * 32;
     static constexpr int kScaleBytes = kWide ? 2 * 4 * 2 * 128 * 4 : 0;   // two groups of 4 blocks, two weight blocks, 128 rows
     static constexpr int kPiece = kWide ? 64 : 128;                        // bytes of an output row that a warp gathers
@@ -229,15 +229,15 @@ __global__ void __launch_bounds__(MmShape<BN, PAIR>::kThreads, MmShape<BN, PAIR>
             // Waits and MMAs of a block take an issuer some 350 clocks, so there are two: with two parts, one for each; else
             // they take turns.
             const int i = warp - S::kEpiWarps - 1;
-            constexpr int kTurns = S::kParts > 1 ? 1 : S::kIssuers;
+            constexpr int kTurns = S::kTurns;
             const int h = S::kParts > 1 ? i : 0;
             const uint32_t idesc = tc::idesc_e4m3(kMmRows * CTAS, S::kPart);
             const uint64_t d0 = tc::sdesc_sw128(tc::smem_u32(ring), 16, 1024);
             const uint32_t b_off = q.a_bytes + h * S::kBox * kE4Block, tm = tmem + h * S::kPart;
             uint64_t *part_full = acc_full + h * S::kBufs, *part_empty = acc_empty + h * S::kBufs;
             const long long todo = (long long)(first < tiles ? (tiles - 1 - first) / step + 1 : 0) * (k1 - k0);
-            int st = kTurns > 1 ? i % ST : 0, buf = kTurns > 1 ? i : 0;
-            uint32_t ph = kTurns > 1 ? (i / ST) & 1 : 0, use = 0;  // parities of the stage's fill and of the accumulator's use
+            int st = kTurns > 1 ? i : 0, buf = kTurns > 1 ? i : 0;  // both counts are multiples of kTurns
+            uint32_t ph = 0, use = 0;  // parities of the stage's fill and of the accumulator's use
             for (long long g = kTurns > 1 ? i : 0; g < todo; g += kTurns) {
                 if (!tc::mbar_wait_warp(tc::smem_u32(&full[st]), ph, tc::smem_u32(&part_empty[buf]), use ^ 1u, abort_flag)) break;
                 tc::tc_fence_after();
@@ -498,6 +498,9 @@ static tsv_status launch_mm(const char* name, const E4Product& p, int split, cud
     // the last stage's 128 rows have to end inside the ring as well
     const int slack = std::max(0, kMmRows * kE4Block - q.stage_bytes);
     q.stages = std::min((int)kMmMaxStages, (S::kRing - slack) / q.stage_bytes);
+    // Issuers that take turns need every stage to be one issuer's: an issuer that comes to a stage's next filling without having waited
+    // for the one before takes the parity of the filling before that one for its own, and copies may land out of order.
+    q.stages -= q.stages % S::kTurns;
     if (!mm_map(&q.amap, p.a, p.rows, p.K, arows) || !mm_map(&q.wmap, p.w, p.N, p.K, S::kBox))
         return fail(TSV_ECUDA, "%s: tensor map encoding failed", name);
     q.vec = ((uintptr_t)p.out & 15) == 0 && p.N % (p.out_dtype == TSV_F32 ? 4 : 8) == 0;
