@@ -47,8 +47,8 @@ struct MmShape {
     static constexpr int kBox = kPart / (PAIR ? 2 : 1);  // weights of a part in a CTA's shared memory
     // 256 columns: an epilogue thread holds 64 sums and 16 warps have to share the registers, so they take some over from the last
     // warpgroup (producer, two issuers, scales): 512 x 104 + 128 x 64 = 640 x 96.  A warp of its own reads the scales ahead
-    // of the epilogue, which has neither the registers nor the time.  (Eight epilogue warps with 128 sums each: 346 us against 337 for
-    // 4096 x 5120 x 20480.)
+    // of the epilogue, which has neither the registers nor the time.  (Eight epilogue warps with 128 sums each: 346 us against
+    // 337 for 4096 x 5120 x 20480.)
     static constexpr bool kWide = BN == 256;
     static constexpr int kIssuers = BN >= 128 ? 2 : 1, kTurns = kParts > 1 ? 1 : kIssuers;  // issuers that take turns with the blocks
     static constexpr int kThreads = (kEpiWarps + (kWide ? 4 : 1 + kIssuers)) * 32;
@@ -56,7 +56,7 @@ struct MmShape {
     static constexpr int kPiece = kWide ? 64 : 128;                        // bytes of an output row that a warp gathers
     static constexpr int kOutBytes = BN >= 128 ? kEpiWarps * 32 * kPiece : 0;
     static constexpr bool kAhead = BN == 128;
-    static constexpr int kSmem = (kPerSm == 1 ? 224 : 72) * 1024;
+    static constexpr int kSmem = (kPerSm == 1 ? 225 : 72) * 1024;
     static constexpr int kRing = kSmem - 1024 - kScaleBytes - kOutBytes;
 };
 
@@ -226,8 +226,8 @@ __global__ void __launch_bounds__(MmShape<BN, PAIR>::kThreads, MmShape<BN, PAIR>
                 for (int i = max(0, issued - ST); i < issued; ++i) tc::mbar_drain(&full[i % ST], (i / ST) & 1);
         } else if (warp <= S::kEpiWarps + S::kIssuers && rank == 0) {
             // -------------------------------------------------------- MMA issuers (of a pair: its first CTA's)
-            // Waits and MMAs of a block take an issuer some 350 clocks, so there are two: with two parts, one for each; else
-            // they take turns.
+            // An issuer's waits, MMAs and commits follow one another and take as long as the MMAs of 128 columns run, so there are
+            // two: with two parts, one for each; else they take turns.
             const int i = warp - S::kEpiWarps - 1;
             constexpr int kTurns = S::kTurns;
             const int h = S::kParts > 1 ? i : 0;
@@ -498,8 +498,9 @@ static tsv_status launch_mm(const char* name, const E4Product& p, int split, cud
     // the last stage's 128 rows have to end inside the ring as well
     const int slack = std::max(0, kMmRows * kE4Block - q.stage_bytes);
     q.stages = std::min((int)kMmMaxStages, (S::kRing - slack) / q.stage_bytes);
-    // Issuers that take turns need every stage to be one issuer's: an issuer that comes to a stage's next filling without having waited
-    // for the one before takes the parity of the filling before that one for its own, and copies may land out of order.
+    // Issuers that take turns need every stage to be one issuer's: a parity does not tell a filling from the last but one, so whoever
+    // waits for a filling has to have seen the one before.  (That a freed accumulator implies the one before does not help: a
+    // suspended test of one barrier ends after the test of another that was issued behind it.)
     q.stages -= q.stages % S::kTurns;
     if (!mm_map(&q.amap, p.a, p.rows, p.K, arows) || !mm_map(&q.wmap, p.w, p.N, p.K, S::kBox))
         return fail(TSV_ECUDA, "%s: tensor map encoding failed", name);
@@ -517,10 +518,11 @@ static tsv_status launch_mm(const char* name, const E4Product& p, int split, cud
 // wherever its operands come from, since that is what its hand-offs and 66 bytes per SM clock from L2 cost; rounds of CTAs
 // follow one another; HBM delivers 6.5 bytes per nanosecond at most; a launch costs 3.5 us, sharing a tile's features between the CTAs of a
 // cluster 2.5 and 0.035 per row (their sums go through shared memory).  Measured (us: estimate's choice, others), K = 5120:
-//   1 x 1024: 64 columns shared by 8 6.3, by 4 7.0, 128 columns 13.2     1 x 20480: 64 columns 21.4, 128 30.1
-//   1 x 6144: 64 shared by 4 11.4, by 2 11.8, 128 13.6                   1 x 248320: 128 columns 187 (the HBM rate), 64 193
-//   512 x 5120: pairs 23.7, 128 columns 26.0                             2048 x 5120: 128 columns 57.7, pairs 62.4
-//   1024 x 5120: 128 columns 36.3, pairs 42.8                            4096 x 20480: pairs 345, 128 columns 397
+//   1 x 1024: 64 columns shared by 8 6.5, by 4 7.0, 128 shared by 4 7.4   1 x 20480: 64 columns 21.3, 128 27.8
+//   1 x 6144: 64 shared by 4 11.6, 128 by 2 11.2, 64 alone 13.9           1 x 248320: 128 columns 183 (the HBM rate), 64 195
+//   128 x 6144: 128 columns 14.3, 64 shared by 4 16.2                     128 x 248320: 128 columns 207, 64 273
+//   512 x 5120: pairs 23.1, 128 columns 24.0                              2048 x 5120: 128 columns 54.0, pairs 60.7
+//   1024 x 5120: 128 columns 34.0, pairs 41.6                             4096 x 20480: pairs 329, 128 columns 364
 tsv_status launch_matmul_e4m3(const char* name, const E4Product& p, cudaStream_t stream) {
     const int sms = sm_count(), blocks = e4_blocks(p.K);
     const long long mt = (p.rows + kMmRows - 1) / kMmRows, n64 = mt * ((p.N + 63) / 64), n128 = mt * ((p.N + 127) / 128);

@@ -150,8 +150,8 @@ __device__ __forceinline__ bool mbar_wait_warp(uint32_t bar, uint32_t parity, vo
 __device__ __forceinline__ bool mbar_wait_warp(uint64_t* bar, uint32_t parity, volatile int* abort) {
     return mbar_wait_warp(smem_u32(bar), parity, abort);
 }
-// The same for two barriers, with one vote where both are through.  bar1 is the one that is waited for longer: bar0 is looked at
-// while it is not, and not after it.
+// The same for two barriers, with one vote where both are through.  Both tests are under way at once, in no order: neither barrier
+// may depend on the other's wait for its parity to be the one meant.
 __device__ __forceinline__ bool mbar_wait_warp(uint32_t bar0, uint32_t parity0, uint32_t bar1, uint32_t parity1, volatile int* abort) {
     const bool a = mbar_try_wait(bar0, parity0), b = mbar_try_wait(bar1, parity1);
     if (__all_sync(0xFFFFFFFFu, a && b)) return true;
@@ -179,7 +179,8 @@ __device__ __forceinline__ float4 ld_cluster_f4(uint32_t addr) {
     asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];" : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w) : "r"(addr) : "memory");
     return v;
 }
-// Lane 0 of the converged warp arrives, without an election; of a pair: by the barrier's cluster address, relaxed as below.
+// Lane 0 of the converged warp arrives, without an election; of a pair: by the barrier's cluster address, relaxed, since what it tells
+// of is TMEM reads that have ended, no memory (a release would wait for every store under way, microseconds per arrival).
 template <bool PAIR>
 __device__ __forceinline__ void mbar_arrive_lane0(uint32_t bar, int lane) {
     if constexpr (PAIR)
@@ -188,14 +189,6 @@ __device__ __forceinline__ void mbar_arrive_lane0(uint32_t bar, int lane) {
                      : "memory");
     else
         asm volatile("{\n .reg .pred p;\n setp.eq.s32 p, %1, 0;\n @p mbarrier.arrive.shared::cta.b64 _, [%0];\n}" ::"r"(bar), "r"(lane) : "memory");
-}
-// One lane of the converged warp arrives on a barrier anywhere in the cluster.  Relaxed: what it tells of is TMEM reads that have
-// ended, no memory (a release would wait for every store under way, microseconds per arrival).
-__device__ __forceinline__ void mbar_arrive_one_cluster(uint32_t bar) {
-    asm volatile(
-        "{\n .reg .pred p;\n elect.sync _|p, 0xffffffff;\n @p mbarrier.arrive.relaxed.cluster.shared::cluster.b64 _, [%0];\n}" ::"r"(
-            bar)
-        : "memory");
 }
 
 // ---------------------------------------------------------------- TMA
