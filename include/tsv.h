@@ -552,10 +552,11 @@ tsv_status tsv_gdn_scan(const tsv_gdn_desc* d, const int32_t* cu_len, int32_t ma
  * tsv_add_rms_norm - the residual's addition and the root-mean-square norm of every row:
  *     h = x + residual;  y = h / sqrt(mean(h^2) + eps) * (weight_offset + weight)
  *   x, residual, residual_out, weight, out: `dtype` (TSV_F16, TSV_BF16 or TSV_F32), [rows, H], weight [H].  residual may
- *   be NULL (h = x).  Outputs, each optional but one at least: residual_out = h, out = y, and y as 8-bit rows in out8 (uint8 e4m3
- *   [rows, H]) with out8_scale.  Everything between is fp32 and each output is rounded once from it: y is of the unrounded h, the codes of
- *   the unrounded y (their quotients within two units in the last place of fp32).  A row whose squares leave fp32's range is scaled by a power of two first.  residual_out may equal residual or x,
- *   out may equal x or residual; otherwise outputs overlap neither inputs nor each other.
+ *   be NULL (h = x).  Outputs, each optional but one at least: residual_out = h, out = y, and y as 8-bit rows in out8
+ *   (uint8 e4m3 [rows, H]) with out8_scale.  Everything between is fp32 and each output is rounded once from it: y is of
+ *   the unrounded h, the codes of the unrounded y (their quotients within two units in the last place of fp32).  A row
+ *   whose squares leave fp32's range is scaled by a power of two first.  residual_out may equal residual or x, out may
+ *   equal x or residual; otherwise outputs overlap neither inputs nor each other.
  *   1 <= H <= 32768, 1e-30 <= eps, eps and weight_offset finite.  A NaN in a row makes all of its y NaN, an infinity makes
  *   y NaN there and 0 elsewhere.
  * tsv_quantize_e4m3 - 8-bit rows of x as it is: out8, out8_scale as above (H without an upper limit).
@@ -571,14 +572,15 @@ tsv_status tsv_quantize_e4m3(const void* x, int32_t rows, int32_t H, int32_t dty
  * tsv_matmul_e4m3 - rows in 8 bits times weights in 8 bits:
  *     out[m, n] = sum over k of a[m, k] a_scale[m, k / 128] w[n, k] w_scale[n / 128, k / 128]
  *   a: e4m3 [rows, K], a_scale float [rows, ceil(K / 128)] (8-bit rows as above); w: e4m3 [N, K], w_scale float
- *   [ceil(N / 128), ceil(K / 128)]; out [rows, N] of out_dtype (TSV_BF16, TSV_F16 or TSV_F32).  The products of 128 features are summed on
- *   the tensor cores into fp32, scaled, and summed in fp32; out is rounded once.  The same inputs give the same bits in every call.
+ *   [ceil(N / 128), ceil(K / 128)]; out [rows, N] of out_dtype (TSV_BF16, TSV_F16 or TSV_F32).  The products of 128
+ *   features are summed on the tensor cores into fp32, scaled, and summed in fp32; out is rounded once.  The same inputs
+ *   give the same bits in every call.
  *   K % 16 == 0, a and w 16-byte aligned, 0 <= rows <= 2^30, 1 <= N <= 2^30.
  * tsv_matmul_e4m3_argmax - the same product with its argmax, as tsv_lm_head_argmax: argmax int32 [rows] (ties to the lowest
  *   index), maxval float [rows] or NULL; the products are never written.  Workspace: tsv_matmul_e4m3_argmax_workspace_size.
  *   A product that is NaN counts as larger than every number if its sign bit is clear, and as smaller if it is set.
- * tsv_lm_head_argmax, tsv_lm_head_logits with w_dtype TSV_E4M3_B128: W as w, scales as w_scale, biases ignored; hidden (bf16) becomes 8-bit
- *   rows in the workspace first.  H % 16 == 0.
+ * tsv_lm_head_argmax, tsv_lm_head_logits with w_dtype TSV_E4M3_B128: W as w, scales as w_scale, biases ignored; hidden
+ *   (bf16) becomes 8-bit rows in the workspace first.  H % 16 == 0, rows and V at most 2^30.
  */
 tsv_status tsv_matmul_e4m3(const void* a, const float* a_scale, int32_t rows, int32_t K, const void* w, const float* w_scale,
                            int32_t N, void* out, int32_t out_dtype, cudaStream_t stream);
@@ -594,13 +596,13 @@ tsv_status tsv_matmul_e4m3_argmax(const void* a, const float* a_scale, int32_t r
  *     z = logits / temperature;  logp(t) = z_t - log(sum exp(z));  entropy = -sum p log p with p = softmax(z)
  *   logits [rows, V] of logits_dtype (TSV_F32, TSV_BF16 or TSV_F16; each row may start anywhere: V needs no alignment).
  *   targets int32 [rows] or NULL; logp float [rows]: each target's log probability; rank int32 [rows] or NULL: how many
- *   tokens have a larger logit, or an equal one and a lower index (0: the greedy choice).  With targets NULL, logp and rank are NULL too.
- *   entropy float [rows] or NULL.  top_tokens int32, top_logp float [rows, top_k]: the top_k largest, largest first, ties to the lower
- *   index; 0 <= top_k <= min(64, V) (0: both NULL).
+ *   tokens have a larger logit, or an equal one and a lower index (0: the greedy choice).  With targets NULL, logp and
+ *   rank are NULL too.  entropy float [rows] or NULL.  top_tokens int32, top_logp float [rows, top_k]: the top_k largest,
+ *   largest first, ties to the lower index; 0 <= top_k <= min(64, V) (0: both NULL).
  *   A logit of -infinity has probability 0 (and adds nothing to the entropy).  A row with a NaN or +infinity, or with
- *   nothing but -infinity, has no distribution: its floats are NaN and its rank and tokens -1.  A target outside [0, V) (the -1 that
- *   pads emitted tokens) gets logp NaN and rank -1.  1e-6 <= temperature <= 1e6.  Sums are fp32, in an order that
- *   the sizes and the rows' offsets from 16-byte boundaries fix, so the same call gives the same bits.
+ *   nothing but -infinity, has no distribution: its floats are NaN and its rank and tokens -1.  A target outside [0, V)
+ *   (the -1 that pads emitted tokens) gets logp NaN and rank -1.  1e-6 <= temperature <= 1e6.  Sums are fp32, in an order
+ *   that the sizes and the rows' offsets from 16-byte boundaries fix, so the same call gives the same bits.
  */
 size_t tsv_token_logprobs_workspace_size(int32_t rows, int32_t V, int32_t top_k);
 

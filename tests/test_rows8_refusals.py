@@ -75,6 +75,7 @@ def no_error_left_behind():
     (head, dict(H=264), "EINVAL", b"multiple of 16"), (head, dict(scales=None), "EINVAL", b"scales"), (head, dict(scales=PTR + 2), "EINVAL", b"4-byte"),
     (head, dict(W=PTR + 4), "EINVAL", b"16-byte"), (head, dict(ws=PTR + 8), "EINVAL", b"16-byte"), (head, dict(ws_bytes=512), "ECAPACITY", b"workspace"),
     (head, dict(dtype=tsv.F32), "EUNSUPPORTED", b"format 6"),
+    (head, dict(rows=(1 << 30) + 1), "ECAPACITY", b"2^30"), (head, dict(V=(1 << 30) + 1), "ECAPACITY", b"2^30"),
     (logprobs, dict(rows=-1), "EINVAL", b"rows"), (logprobs, dict(V=0), "EINVAL", b"V=0"), (logprobs, dict(V=(1 << 24) + 1), "EINVAL", b"2^24"),
     (logprobs, dict(dtype=tsv.I8_SCALED), "EUNSUPPORTED", b"type 2"), (logprobs, dict(top_k=65), "EUNSUPPORTED", b"top_k=65"),
     (logprobs, dict(top_k=-1), "EUNSUPPORTED", b"top_k=-1"), (logprobs, dict(V=4), "EUNSUPPORTED", b"top_k=5"), (logprobs, dict(t=0.0), "EINVAL", b"temperature"),

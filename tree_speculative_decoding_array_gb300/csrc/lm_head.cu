@@ -319,6 +319,7 @@ static tsv_status lm_head_e4m3(const char* name, const void* hidden, int rows, i
                                int32_t* argmax, float* maxlogit, float* logits, void* workspace, size_t ws_bytes,
                                cudaStream_t stream) {
     if (H % 16) return fail(TSV_EINVAL, "%s: H=%d not a multiple of 16", name, H);
+    if (rows > 1 << 30 || V > 1 << 30) return fail(TSV_ECAPACITY, "%s: rows=%d V=%d above 2^30", name, rows, V);
     if (!scales) return fail(TSV_EINVAL, "%s: 8-bit head without scales", name);
     if (((uintptr_t)hidden | (uintptr_t)W | (uintptr_t)workspace) & 15)
         return fail(TSV_EINVAL, "%s: hidden/W/workspace not 16-byte aligned", name);
