@@ -69,28 +69,32 @@ __device__ __forceinline__ Sums joined_warp(Sums v, float c) {
 
 __device__ __forceinline__ int power_of_two(int n) { return 1 << (32 - __clz(n - 1)); }  // at least n >= 1
 
-// Sorts n keys (a power of two) in shared memory, largest first: the whole CTA, or up to 128 keys its first warp alone (a barrier of
-// the CTA for each of the 21 steps of 64 keys had been a seventh of a row's instructions).  A barrier follows.
-template <int THREADS>
-__device__ __forceinline__ void sort_steps(unsigned long long* key, int n) {
+// Sorts n keys (a power of two) in shared memory, largest first.  A barrier follows.
+__device__ __forceinline__ void sort_keys(unsigned long long* key, int n) {
     for (int size = 2; size <= n; size <<= 1)
         for (int step = size >> 1; step > 0; step >>= 1) {
-            for (int e = threadIdx.x; e < n / 2; e += THREADS) {
+            for (int e = threadIdx.x; e < n / 2; e += kLpThreads) {
                 const int i = ((e & ~(step - 1)) << 1) | (e & (step - 1)), j = i | step;
                 const unsigned long long a = key[i], b = key[j];
                 if ((a < b) == ((i & size) == 0)) key[i] = b, key[j] = a;
             }
-            if constexpr (THREADS == 32) __syncwarp();
-            else __syncthreads();
+            __syncthreads();
         }
 }
-__device__ __forceinline__ void sort_keys(unsigned long long* key, int n) {
-    if (n > 128) {
-        sort_steps<kLpThreads>(key, n);
-    } else {
-        if (threadIdx.x < 32) sort_steps<32>(key, n);
-        __syncthreads();
-    }
+
+// The best K of 0 to 256 keys, no two alike, to the front, largest first, and 0 where there are fewer: each key's place is how many
+// are larger, counted by as many neighbouring lanes as there are threads for it.  (Sorting 64 keys took one warp 4600 SM clocks.)
+__device__ __forceinline__ void place_keys(unsigned long long* key, int have, int K) {
+    const int lanes = min(32, kLpThreads / power_of_two(max(have, 1))), e = threadIdx.x / lanes;
+    const unsigned long long mine = e < have ? key[e] : 0ull;
+    int larger = 0;
+    if (e < have)
+        for (int j = threadIdx.x & (lanes - 1); j < have; j += lanes) larger += key[j] > mine;
+    for (int o = lanes >> 1; o > 0; o >>= 1) larger += __shfl_xor_sync(0xFFFFFFFFu, larger, o);
+    __syncthreads();
+    if (e < have && larger < K) key[larger] = mine;  // the same from all of the key's lanes
+    if (threadIdx.x >= have && threadIdx.x < K) key[threadIdx.x] = 0ull;
+    __syncthreads();
 }
 
 // 16 bytes of logits as fp32.
@@ -202,10 +206,14 @@ __global__ void __launch_bounds__(kLpThreads, kLpPerSm) logprobs_kernel(const Lo
     int kept = 0;           // candidates that stood in the list, sorted, after the last cut
     if (tid == 0) filled = 0;
     auto cut = [&](int have) {  // the list's `have` candidates back to the best K, sorted; after a barrier
-        const int n = power_of_two(max(have, K));
-        for (int e = have + tid; e < n; e += kLpThreads) list[e] = 0ull;
-        __syncthreads();
-        sort_keys(list, n);
+        if (have <= kLpThreads) {
+            place_keys(list, have, K);
+        } else {
+            const int n = power_of_two(have);
+            for (int e = have + tid; e < n; e += kLpThreads) list[e] = 0ull;
+            __syncthreads();
+            sort_keys(list, n);
+        }
         kept = min(have, K);
         if (tid == 0) filled = kept;
         if (have >= K) kth = key_logit(list[K - 1]);
