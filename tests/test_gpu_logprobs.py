@@ -157,3 +157,16 @@ def test_long_rows_of_many(gpu_lib):
     last = x[-2:]
     check({n: v[-2:] for n, v in got.items()}, last, targets[-2:], 1.0, 2)
     assert (got["rank"][:-1] == 248319).all() and (got["top_tokens"][:-1] == [0, 1]).all()
+
+
+@pytest.mark.parametrize("rows, V, k", [(400, 9000, 20), (500, 8200, 64), (130, 12289, 33), (760, 700, 64), (761, 4100, 5)])
+def test_rows_that_share_the_gpu_unevenly(gpu_lib, rows, V, k):
+    """Parts of one or two tiles, the last of a few logits; the first tile masked but for fewer than k logits in some rows."""
+    g = torch.Generator().manual_seed(rows)
+    x = torch.randn(rows, V, generator=g)
+    x[::3, 3 : min(V, 4096)] = float("-inf")
+    x[1::5, : V - 70] = float("-inf")
+    x[2::7, 10:50] = 9.0
+    targets = torch.randint(0, V, (rows,), generator=g, dtype=torch.int32).to(DEV)
+    x = x.to(DEV)
+    check(ask(gpu_lib, x, targets, 1.0, k), x, targets, 1.0, k)

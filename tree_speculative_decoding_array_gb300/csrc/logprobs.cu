@@ -8,11 +8,13 @@
 // end, in the same order in every run.
 //
 // The top k are exact.  Logits above a bound that k logits are known to reach go to a list in shared memory: in the first tile the
-// bound is the smallest over the 8 warps of each one's ceil(k / 8)-th largest thread maximum, then the k-th best of the list, which is
-// cut back to k between groups of 1, 1, 2, 4, 8, 16, 16 ... tiles (no barrier inside a group: one per tile cost a third of the time).  Of
-// logits in no particular order a few hundred pass.  Where a group's do not fit (an ascending row, many equal ones), its tiles
-// are read again, each bounded by the k-th largest of the 256 threads' maxima, above which no more than 16 k logits can
-// lie.  Candidates are 64-bit keys (value, then lower index), so ties need no care.
+// bound is the smallest over the 8 warps of each one's ceil(k / 8)-th largest thread maximum (where there are too few, the k-th largest
+// of all 256), then the k-th best of the list, which is cut back to k between groups of 1, 1, 2, 4, 8, 16, 16 ... tiles (no barrier inside
+// a group: one per tile cost a third of the time).  Of logits in no particular order a few hundred pass.  Where a group's do not
+// fit (an ascending row, many equal ones), its tiles are read again, each bounded by the k-th largest of the 256 threads' maxima, above
+// which no more than 16 k logits can lie.  Candidates are 64-bit keys (value, then lower index), so ties need no care.
+//
+// 2048 rows of 248320 in fp32: 350 us with 20 alternatives (0.86 of HBM: the bounds, cuts and candidates are what is left), 303 without.
 #include <algorithm>
 
 #include "e4m3.cuh"
@@ -89,6 +91,7 @@ __device__ __forceinline__ void place_keys(unsigned long long* key, int have, in
     const unsigned long long mine = e < have ? key[e] : 0ull;
     int larger = 0;
     if (e < have)
+#pragma unroll 4
         for (int j = threadIdx.x & (lanes - 1); j < have; j += lanes) larger += key[j] > mine;
     for (int o = lanes >> 1; o > 0; o >>= 1) larger += __shfl_xor_sync(0xFFFFFFFFu, larger, o);
     __syncthreads();
@@ -188,7 +191,7 @@ __global__ void __launch_bounds__(kLpThreads, kLpPerSm) logprobs_kernel(const Lo
     // element k of this thread's 16 in a tile is logit first(tile) + (k / W) * 256 W + k % W
     auto first = [&](int tile) { return tile * kLpTile + tid * W - lead; };
     auto inside = [&](int tile) { return tile * kLpTile >= lead && (tile + 1) * kLpTile - lead <= p.V; };
-    // candidates among a thread's 16; each is read again, rather than selected from 16 registers
+    // candidates among a thread's 16
     auto append = [&](const float (&x)[kLpPer], int at, auto&& wanted) {
         uint32_t mask = 0u;
 #pragma unroll
@@ -197,8 +200,11 @@ __global__ void __launch_bounds__(kLpThreads, kLpPerSm) logprobs_kernel(const Lo
             const int k = __ffs(mask) - 1, i = at + (k / W) * kLpThreads * W + k % W;
             mask &= mask - 1;
             if (i < 0 || i >= p.V) continue;
+            float y = x[0];
+#pragma unroll
+            for (int j = 1; j < kLpPer; ++j) y = j == k ? x[j] : y;
             const int to = atomicAdd(&filled, 1);
-            if (to < kLpList) list[to] = logit_key(RowType<T>::to_f32(x0[i]), i);
+            if (to < kLpList) list[to] = logit_key(y, i);
         }
     };
     Sums v = {-INFINITY, 0.f, 0.f, 0};
@@ -218,6 +224,20 @@ __global__ void __launch_bounds__(kLpThreads, kLpPerSm) logprobs_kernel(const Lo
         if (tid == 0) filled = kept;
         if (have >= K) kth = key_logit(list[K - 1]);
         __syncthreads();
+    };
+    // Candidates of a tile by the K-th largest of the threads' maxima; the whole CTA.
+    auto append_bounded = [&](const float (&x)[kLpPer], int at) {
+        unsigned long long mine = tid;  // below every logit's key, and no two alike
+#pragma unroll
+        for (int k = 0; k < kLpPer; ++k) {
+            const int i = at + (k / W) * kLpThreads * W + k % W;
+            if (i >= 0 && i < p.V && x[k] == x[k]) mine = max(mine, logit_key(x[k], i));
+        }
+        maxima[tid] = mine;
+        __syncthreads();
+        place_keys(maxima, kLpThreads, K);
+        const unsigned long long bound = maxima[K - 1];
+        if (mine >= bound) append(x, at, [&](float y, int i) { return logit_key(y, i) >= bound; });
     };
     for (int next = t0, group = 1; next < t1;) {
         const int end = min(t1, next + group);
@@ -269,7 +289,8 @@ __global__ void __launch_bounds__(kLpThreads, kLpPerSm) logprobs_kernel(const Lo
                 float bound = bounds[0];
 #pragma unroll
                 for (int w = 1; w < kLpThreads / 32; ++w) bound = fminf(bound, bounds[w]);
-                if (most >= bound) append(x, at, [&](float y, int) { return y >= bound; });
+                if (bound == -INFINITY) append_bounded(x, at);  // threads without a logit, or masked ones
+                else if (most >= bound) append(x, at, [&](float y, int) { return y >= bound; });
             } else if (most > kth) {
                 append(x, at, [&](float y, int) { return y > kth; });
             }
@@ -284,17 +305,7 @@ __global__ void __launch_bounds__(kLpThreads, kLpPerSm) logprobs_kernel(const Lo
                     float x[kLpPer];
                     const int at = first(tile);
                     load_tile<T>(x0, at, p.V, inside(tile), x);
-                    unsigned long long mine = 0ull;
-#pragma unroll
-                    for (int k = 0; k < kLpPer; ++k) {
-                        const int i = at + (k / W) * kLpThreads * W + k % W;
-                        if (i >= 0 && i < p.V && x[k] == x[k]) mine = max(mine, logit_key(x[k], i));
-                    }
-                    maxima[tid] = mine;
-                    __syncthreads();
-                    sort_keys(maxima, kLpThreads);
-                    const unsigned long long bound = maxima[K - 1];
-                    if (mine >= bound) append(x, at, [&](float y, int i) { return logit_key(y, i) >= bound; });
+                    append_bounded(x, at);
                     __syncthreads();
                     cut(min(filled, kLpList));  // beyond the list only where NaNs are, and such a row has no top k
                 }
@@ -386,9 +397,11 @@ __global__ void __launch_bounds__(kLpThreads) logprobs_join_kernel(const Logprob
         if (lane + h * 32 < p.K) res.write_top(p, row, lane + h * 32, mine[h]);
 }
 
-// Parts of a row: as many as fill the GPU once, a tile at least in each.
+// Parts of a row, a tile at least in each: as many as fill the GPU once, or twice where once would leave more than a quarter of its
+// places empty (400 rows of 248320: 3 parts 98 us, one 126; 512: 2 parts 124, one 130; 300 rows, which fill 0.79: 2 parts 82, 5 parts 83).
 static int logprob_parts(int rows, int V) {
-    const int tiles = (V + kLpTile - 1) / kLpTile, want = sm_count() * kLpPerSm / rows;
+    const int places = sm_count() * kLpPerSm, once = places / rows, tiles = (V + kLpTile - 1) / kLpTile;
+    const int want = once * rows < places * 3 / 4 ? 2 * places / rows : once;
     return std::max(1, std::min({want, tiles, kLpMaxParts}));
 }
 
