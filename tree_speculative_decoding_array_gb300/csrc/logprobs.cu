@@ -51,6 +51,30 @@ struct Sums {
     int ahead;
 };
 
+// Two fp32 numbers in one register pair, and operations on both.
+__device__ __forceinline__ uint64_t pair(float a, float b) {
+    uint64_t r;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a), "f"(b));
+    return r;
+}
+__device__ __forceinline__ float first_of(uint64_t p) { return __uint_as_float((uint32_t)p); }
+__device__ __forceinline__ float second_of(uint64_t p) { return __uint_as_float((uint32_t)(p >> 32)); }
+__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
+    uint64_t r;
+    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+    return r;
+}
+__device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b) {
+    uint64_t r;
+    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+    return r;
+}
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
+    uint64_t r;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+    return r;
+}
+
 __device__ __forceinline__ Sums joined(Sums a, Sums b, float c) {
     const float m = fmaxf(a.m, b.m);
     if (m == -INFINITY) return {m, a.s + b.s, a.w + b.w, a.ahead + b.ahead};  // nothing but -infinity (or NaN, which s keeps)
@@ -257,18 +281,35 @@ __global__ void __launch_bounds__(kLpThreads, kLpPerSm) logprobs_kernel(const Lo
                 v.m = most;
             }
             const float m = v.m > -INFINITY ? v.m : 0.f;
+            // two logits at a time; a NaN stays in both sums
+            uint64_t s2 = 0ull, w2 = 0ull;
+            const uint64_t less = pair(-m, -m), scale = pair(c, c);
 #pragma unroll
-            for (int k = 0; k < kLpPer; ++k) {
-                const float d = (x[k] - m) * c, e = tc::ex2_approx(d);
-                v.s += e;                               // a NaN stays
-                v.w = fmaf(e, fmaxf(d, -1000.f), v.w);  // 0 for -infinity
+            for (int k = 0; k < kLpPer; k += 2) {
+                const uint64_t d = mul2(add2(pair(x[k], x[k + 1]), less), scale);
+                const uint64_t e = pair(tc::ex2_approx(first_of(d)), tc::ex2_approx(second_of(d)));
+                s2 = add2(s2, e);
+                w2 = fma2(e, d, w2);
             }
+            float w = first_of(w2) + second_of(w2);
+            if (w != w) {  // 0 times -infinity: such logits add nothing
+                w = 0.f;
+#pragma unroll
+                for (int k = 0; k < kLpPer; ++k) {
+                    const float d = (x[k] - m) * c;
+                    w = fmaf(tc::ex2_approx(d), fmaxf(d, -1000.f), w);
+                }
+            }
+            v.s += first_of(s2) + second_of(s2);
+            v.w += w;
             if (ranked) {
                 const bool after = tile * kLpTile - lead > target, before = (tile + 1) * kLpTile - lead <= target;
                 if (after || (before && t > -INFINITY)) {
                     const float over = after ? t : below;
+                    if (most > over) {
 #pragma unroll
-                    for (int k = 0; k < kLpPer; ++k) v.ahead += x[k] > over;
+                        for (int k = 0; k < kLpPer; ++k) v.ahead += x[k] > over;
+                    }
                 } else {
 #pragma unroll
                     for (int k = 0; k < kLpPer; ++k) {
