@@ -28,9 +28,17 @@ constexpr int kLpTile = kLpThreads * kLpPer;
 constexpr int kLpMaxTop = 64;
 constexpr int kLpMaxParts = 64;
 constexpr int kLpList = 2048;                    // candidates; 16 x 64 + 64 at least
-constexpr int kLpPerSm = 5;                       // CTAs resident on an SM
 constexpr int kLpGroup = 16;                     // tiles between two looks at the list
 constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
+
+// CTAs resident on an SM, and whether a thread asks for its next tile before it works on this one.  16-bit logits, whose tiles are 8
+// registers: four CTAs that look ahead (2048 rows of 248320: 292 us, five without 328); fp32, near HBM's rate as it is: five (346; four
+// that look ahead 401).
+template <typename T>
+struct LpShape {
+    static constexpr bool kAhead = sizeof(T) == 2;
+    static constexpr int kPerSm = kAhead ? 4 : 5;
+};
 
 struct LogprobParams {
     const void* logits;
@@ -168,16 +176,24 @@ __device__ __forceinline__ float target_logit(const LogprobParams& p, size_t row
     return target >= 0 && target < p.V ? RowType<T>::to_f32(((const T*)p.logits)[row * p.V + target]) : 0.f;
 }
 
-// A thread's 16 logits of a tile, -infinity where the row has none.
+// A thread's 16 logits of a tile as they come from memory.
 template <typename T>
-__device__ __forceinline__ void load_tile(const T* x0, int at, int V, bool inside, float (&x)[kLpPer]) {
-    constexpr int W = 16 / sizeof(T), NV = kLpPer / W;
+struct RawTile {
+    static constexpr int W = 16 / sizeof(T), NV = kLpPer / W;
     uint4 u[NV];
-    if (inside) {
+    __device__ __forceinline__ void load(const T* x0, int at) {
 #pragma unroll
         for (int j = 0; j < NV; ++j) u[j] = ldg_stream16(x0 + at + j * kLpThreads * W);
+    }
+};
+
+// As numbers, -infinity where the row has none.  inside: `raw` holds them.
+template <typename T>
+__device__ __forceinline__ void load_tile(const T* x0, int at, int V, bool inside, const RawTile<T>& raw, float (&x)[kLpPer]) {
+    constexpr int W = 16 / sizeof(T), NV = kLpPer / W;
+    if (inside) {
 #pragma unroll
-        for (int j = 0; j < NV; ++j) unpack16<T>(u[j], x + j * W);
+        for (int j = 0; j < NV; ++j) unpack16<T>(raw.u[j], x + j * W);
         return;
     }
 #pragma unroll
@@ -190,7 +206,7 @@ __device__ __forceinline__ void load_tile(const T* x0, int at, int V, bool insid
 }
 
 template <typename T>
-__global__ void __launch_bounds__(kLpThreads, kLpPerSm) logprobs_kernel(const LogprobParams p) {
+__global__ void __launch_bounds__(kLpThreads, LpShape<T>::kPerSm) logprobs_kernel(const LogprobParams p) {
     griddep_begin();
     constexpr int W = 16 / sizeof(T);
     __shared__ unsigned long long list[kLpList], maxima[kLpThreads];
@@ -263,12 +279,16 @@ __global__ void __launch_bounds__(kLpThreads, kLpPerSm) logprobs_kernel(const Lo
         const unsigned long long bound = maxima[K - 1];
         if (mine >= bound) append(x, at, [&](float y, int i) { return logit_key(y, i) >= bound; });
     };
+    RawTile<T> raw;
+    if (LpShape<T>::kAhead && inside(t0)) raw.load(x0, first(t0));
     for (int next = t0, group = 1; next < t1;) {
         const int end = min(t1, next + group);
         for (int tile = next; tile < end; ++tile) {
             float x[kLpPer];
             const int at = first(tile);
-            load_tile<T>(x0, at, p.V, inside(tile), x);
+            if (!LpShape<T>::kAhead && inside(tile)) raw.load(x0, at);
+            load_tile<T>(x0, at, p.V, inside(tile), raw, x);
+            if (LpShape<T>::kAhead && tile + 1 < t1 && inside(tile + 1)) raw.load(x0, first(tile + 1));
             float most = x[0];
 #pragma unroll
             for (int k = 1; k < kLpPer; ++k) most = fmaxf(most, x[k]);
@@ -345,7 +365,9 @@ __global__ void __launch_bounds__(kLpThreads, kLpPerSm) logprobs_kernel(const Lo
                 for (int tile = next; tile < end; ++tile) {
                     float x[kLpPer];
                     const int at = first(tile);
-                    load_tile<T>(x0, at, p.V, inside(tile), x);
+                    RawTile<T> again;
+                    if (inside(tile)) again.load(x0, at);
+                    load_tile<T>(x0, at, p.V, inside(tile), again, x);
                     append_bounded(x, at);
                     __syncthreads();
                     cut(min(filled, kLpList));  // beyond the list only where NaNs are, and such a row has no top k
@@ -440,14 +462,18 @@ __global__ void __launch_bounds__(kLpThreads) logprobs_join_kernel(const Logprob
 
 // Parts of a row, a tile at least in each: as many as fill the GPU once, or twice where once would leave more than a quarter of its
 // places empty (400 rows of 248320: 3 parts 98 us, one 126; 512: 2 parts 124, one 130; 300 rows, which fill 0.79: 2 parts 82, 5 parts 83).
+template <typename T>
 static int logprob_parts(int rows, int V) {
-    const int places = sm_count() * kLpPerSm, once = places / rows, tiles = (V + kLpTile - 1) / kLpTile;
+    const int places = sm_count() * LpShape<T>::kPerSm, once = places / rows, tiles = (V + kLpTile - 1) / kLpTile;
     const int want = once * rows < places * 3 / 4 ? 2 * places / rows : once;
     return std::max(1, std::min({want, tiles, kLpMaxParts}));
 }
 
 template <typename T>
-static void launch_logprobs(const LogprobParams& p, cudaStream_t stream) {
+static void launch_logprobs(LogprobParams p, void* workspace, cudaStream_t stream) {
+    p.parts = logprob_parts<T>(p.rows, p.V);
+    p.part_sums = (float4*)workspace;
+    p.part_top = (unsigned long long*)(p.part_sums + (size_t)p.rows * p.parts);
     launch_pdl(logprobs_kernel<T>, p.rows * p.parts, kLpThreads, 0, stream, p);
     if (p.parts > 1) launch_pdl(logprobs_join_kernel<T>, p.rows, kLpThreads, 0, stream, p);
 }
@@ -457,7 +483,7 @@ static void launch_logprobs(const LogprobParams& p, cudaStream_t stream) {
 extern "C" size_t tsv_token_logprobs_workspace_size(int32_t rows, int32_t V, int32_t top_k) {
     using namespace tsv;
     if (rows < 1 || V < 1 || top_k < 0 || top_k > kLpMaxTop) return 0;
-    const size_t parts = logprob_parts(rows, V);
+    const size_t parts = std::max(logprob_parts<float>(rows, V), logprob_parts<__half>(rows, V));  // for any type
     return parts > 1 ? (rows * parts * (16 + 8 * (size_t)top_k) + 255) & ~(size_t)255 : 0;
 }
 
@@ -486,12 +512,10 @@ extern "C" tsv_status tsv_token_logprobs(const void* logits, int32_t logits_dtyp
     if (need && !workspace) return fail(TSV_EINVAL, "token_logprobs: null workspace");
     if ((uintptr_t)workspace & 15) return fail(TSV_EINVAL, "token_logprobs: workspace not 16-byte aligned");
     if (ws_bytes < need) return fail(TSV_ECAPACITY, "token_logprobs: workspace %zu < %zu bytes", ws_bytes, need);
-    if ((long long)rows * logprob_parts(rows, V) > INT_MAX) return fail(TSV_ECAPACITY, "token_logprobs: rows=%d", rows);
-    LogprobParams p = {logits, targets, rows, V, top_k, logprob_parts(rows, V), 1.f / temperature, logp, entropy, top_logp, rank, top_tokens};
-    p.part_sums = (float4*)workspace;
-    p.part_top = (unsigned long long*)(p.part_sums + (size_t)rows * p.parts);
-    if (logits_dtype == TSV_F32) launch_logprobs<float>(p, stream);
-    else if (logits_dtype == TSV_BF16) launch_logprobs<__nv_bfloat16>(p, stream);
-    else launch_logprobs<__half>(p, stream);
+    if ((long long)rows * std::max(logprob_parts<float>(rows, V), logprob_parts<__half>(rows, V)) > INT_MAX) return fail(TSV_ECAPACITY, "token_logprobs: rows=%d", rows);
+    const LogprobParams p = {logits, targets, rows, V, top_k, 1, 1.f / temperature, logp, entropy, top_logp, rank, top_tokens};
+    if (logits_dtype == TSV_F32) launch_logprobs<float>(p, workspace, stream);
+    else if (logits_dtype == TSV_BF16) launch_logprobs<__nv_bfloat16>(p, workspace, stream);
+    else launch_logprobs<__half>(p, workspace, stream);
     return check_launch("token_logprobs");
 }
