@@ -170,3 +170,19 @@ def test_rows_that_share_the_gpu_unevenly(gpu_lib, rows, V, k):
     targets = torch.randint(0, V, (rows,), generator=g, dtype=torch.int32).to(DEV)
     x = x.to(DEV)
     check(ask(gpu_lib, x, targets, 1.0, k), x, targets, 1.0, k)
+
+
+@pytest.mark.parametrize("V, k", [(248320, 64), (30000, 64), (9000, 20), (40000, 1)])
+def test_parts_are_joined(gpu_lib, V, k):
+    """The best of many parts: spread evenly, all in one part, in a few parts whose lists are all better than the others', and few left."""
+    g = torch.Generator().manual_seed(V + k)
+    x = torch.randn(6, V, generator=g)
+    x[0, :4096] += 30                       # one part's
+    x[1, : V // 3] += 30                    # a third of the parts'
+    x[2] = torch.linspace(-9, 9, V)
+    x[3, k + 3 :] = float("-inf")           # hardly more than k left
+    x[4] = torch.randint(0, 2, (V,), generator=g).float()
+    x[4, V // 2 :] += 5
+    targets = torch.randint(0, V, (6,), generator=g, dtype=torch.int32).to(DEV)
+    x = x.to(DEV)
+    check(ask(gpu_lib, x, targets, 1.0, k), x, targets, 1.0, k)

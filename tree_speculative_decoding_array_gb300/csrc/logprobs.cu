@@ -9,7 +9,7 @@
 //
 // The top k are exact.  Logits above a bound that k logits are known to reach go to a list in shared memory: in the first tile the
 // bound is the smallest over the 8 warps of each one's ceil(k / 8)-th largest thread maximum (where there are too few, the k-th largest
-// of all 256), then the k-th best of the list, which is cut back to k between groups of 1, 1, 2, 4, 8, 16, 16 ... tiles (no barrier inside
+// of all 256), then the k-th best of the list, which is cut back to k between groups of 1, 2, 6, 16, 16 ... tiles (no barrier inside
 // a group: one per tile cost a third of the time).  Of logits in no particular order a few hundred pass.  Where a group's do not
 // fit (an ascending row, many equal ones), its tiles are read again, each bounded by the k-th largest of the 256 threads' maxima, above
 // which no more than 16 k logits can lie.  Candidates are 64-bit keys (value, then lower index), so ties need no care.
@@ -382,11 +382,11 @@ __global__ void __launch_bounds__(kLpThreads, LpShape<T>::kPerSm) logprobs_kerne
                     __syncthreads();
                     cut(min(filled, kLpList));  // beyond the list only where NaNs are, and such a row has no top k
                 }
-            } else if (next == t0 || have > 2 * K) {
+            } else if (next == t0 || have > K + K / 2) {
                 cut(have);
             }
         }
-        group = next == t0 ? 1 : min(kLpGroup, 2 * group);
+        group = next == t0 ? 2 : min(kLpGroup, 3 * group);
         next = end;
     }
     // ---- the part's results
@@ -419,7 +419,8 @@ __device__ __forceinline__ unsigned long long warp_largest(unsigned long long k)
 }
 
 // A CTA per row joins its parts: the sums in the parts' order, the sorted lists (brought to shared memory first) by taking the
-// largest head K times.  Lane l of the first warp holds the parts l and l + 32.
+// largest head K times.  Lane l of the first warp holds the parts l and l + 32.  (Counting places among the keys that reach a bound takes
+// longer up to 20 alternatives: 3 rows of 248320 with 5 9.8 us instead of 8.8; with 64 it is 16.3 instead of 18.8.)
 template <typename T>
 __global__ void __launch_bounds__(kLpThreads) logprobs_join_kernel(const LogprobParams p) {
     griddep_begin();
@@ -470,11 +471,11 @@ __global__ void __launch_bounds__(kLpThreads) logprobs_join_kernel(const Logprob
         if (lane + h * 32 < p.K) res.write_top(p, row, lane + h * 32, mine[h]);
 }
 
-// Parts of a row, a tile at least in each: as many as fill the GPU once, or twice where once would leave more than a quarter of its
+// Parts of a row, half a tile at least in each (every thread then has a logit, and the first bound comes from the warps): as many as fill the GPU once, or twice where once would leave more than a quarter of its
 // places empty (400 rows of 248320: 3 parts 98 us, one 126; 512: 2 parts 124, one 130; 300 rows, which fill 0.79: 2 parts 82, 5 parts 83).
 template <typename T>
 static int logprob_parts(int rows, int V) {
-    const int places = sm_count() * LpShape<T>::kPerSm, once = places / rows, tiles = (V + kLpTile - 1) / kLpTile;
+    const int places = sm_count() * LpShape<T>::kPerSm, once = places / rows, tiles = (V + kLpTile / 2) / kLpTile;
     const int want = once * rows < places * 3 / 4 ? 2 * places / rows : once;
     return std::max(1, std::min({want, tiles, kLpMaxParts}));
 }
