@@ -14,8 +14,9 @@
 // fit (an ascending row, many equal ones), its tiles are read again, each bounded by the k-th largest of the 256 threads' maxima, above
 // which no more than 16 k logits can lie.  Candidates are 64-bit keys (value, then lower index), so ties need no care.
 //
-// 2048 rows of 248320 with ranks: fp32 341 us with 20 alternatives (0.88 of HBM), 304 without; bf16 283 and 218, 14 instructions per logit
-// at 76 % of the issue slots.
+// 2048 rows of 248320 with ranks: fp32 343 us with 20 alternatives (0.87 of HBM), 305 without; bf16 286 and 222, 14 instructions
+// per logit at 76 % of the issue slots.  -infinity as any other logit: 2 % of them masked 347 us in fp32 (393 where a tile that has one
+// was summed again).
 #include <algorithm>
 
 #include "e4m3.cuh"
@@ -81,6 +82,13 @@ __device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b) {
 __device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
     uint64_t r;
     asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+    return r;
+}
+
+// At least -1000, whose power of two is 0 as -infinity's is, but whose product with it is a number; a NaN stays.
+__device__ __forceinline__ float clamped(float d) {
+    float r;
+    asm("max.NaN.f32 %0, %1, 0fC47A0000;" : "=f"(r) : "f"(d));
     return r;
 }
 
@@ -315,24 +323,19 @@ __global__ void __launch_bounds__(kLpThreads, LpShape<T>::kPerSm) logprobs_kerne
 #pragma unroll
             for (int k = 0; k < kLpPer; k += 2) {
                 const uint64_t d = mul2(add2(pair(x[k], x[k + 1]), less), scale);
-                const uint64_t e = pair(tc::ex2_approx(first_of(d)), tc::ex2_approx(second_of(d)));
+                const float da = clamped(first_of(d)), db = clamped(second_of(d));
+                const uint64_t e = pair(tc::ex2_approx(da), tc::ex2_approx(db));
                 s2 = add2(s2, e);
-                w2 = fma2(e, d, w2);
+                w2 = fma2(e, pair(da, db), w2);
             }
-            float w = first_of(w2) + second_of(w2);
-            if (w != w) {  // 0 times -infinity: such logits add nothing
-                w = 0.f;
-#pragma unroll
-                for (int k = 0; k < kLpPer; ++k) {
-                    const float d = (x[k] - m) * c;
-                    w = fmaf(tc::ex2_approx(d), fmaxf(d, -1000.f), w);
-                }
-            }
+            const float w = first_of(w2) + second_of(w2);
             v.s += first_of(s2) + second_of(s2);
             v.w += w;
             if (ranked) {
                 const bool after = tile * kLpTile - lead > target, before = (tile + 1) * kLpTile - lead <= target;
-                if (after || (before && t > -INFINITY)) {
+                if (before && t == -INFINITY && inside(tile)) {
+                    v.ahead += kLpPer;
+                } else if (after || (before && t > -INFINITY)) {
                     const float over = after ? t : below;
                     if (most > over) {
                         uint64_t n2 = 0ull;  // in fp32: a comparison gives 1 or 0 in one instruction
