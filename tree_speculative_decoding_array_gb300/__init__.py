@@ -2,7 +2,9 @@
 
 One verify round is five calls of the C ABI in ``include/tsv.h`` (built from
 ``csrc/`` into ``libtsv.so``): ``tree_mask`` -> ``tree_verify_attention`` ->
-``lm_head_argmax`` -> ``tree_accept_walk`` -> ``kv_gather_positions``.  This
+``lm_head_argmax`` -> ``tree_accept_walk`` -> ``kv_gather_positions``.  Ahead of
+the head stand, where a target has them, ``add_rms_norm`` and products with 8-bit
+weights (``matmul_e4m3``); ``token_logprobs`` tells about the emitted tokens.  This
 package is only the Python binding (argument marshalling over ctypes); it has
 no fallback and raises if the library is not built.
 """
