@@ -289,10 +289,15 @@ __global__ void __launch_bounds__(kLpThreads, LpShape<T>::kPerSm) logprobs_kerne
             const int i = at + (k / W) * kLpThreads * W + k % W;
             if (i >= 0 && i < p.V && x[k] == x[k]) mine = max(mine, logit_key(x[k], i));
         }
-        maxima[tid] = mine;
-        __syncthreads();
-        place_keys(maxima, kLpThreads, K);
-        const unsigned long long bound = maxima[K - 1];
+        // the threads that have a logit; up to K of them hold no more than the list takes
+        const int left = p.V - at + tid * W, holders = min(kLpThreads, (left + W - 1) / W);
+        unsigned long long bound = 0ull;
+        if (holders > K) {
+            maxima[tid] = mine;
+            __syncthreads();
+            place_keys(maxima, holders, K);
+            bound = maxima[K - 1];
+        }
         if (mine >= bound) append(x, at, [&](float y, int i) { return logit_key(y, i) >= bound; });
     };
     RawTile<T> raw;
