@@ -9,10 +9,11 @@
 //
 // The top k are exact.  Logits above a bound that k logits are known to reach go to a list in shared memory: in the first tile the
 // bound is the smallest over the 8 warps of each one's ceil(k / 8)-th largest thread maximum (where there are too few, the k-th largest
-// of all 256), then the k-th best of the list, which is cut back to k between groups of 1, 2, 6, 16, 16 ... tiles (no barrier inside
-// a group: one per tile cost a third of the time).  Of logits in no particular order a few hundred pass.  Where a group's do not
-// fit (an ascending row, many equal ones), its tiles are read again, each bounded by the k-th largest of the 256 threads' maxima, above
-// which no more than 16 k logits can lie.  Candidates are 64-bit keys (value, then lower index), so ties need no care.
+// of all 256), then the k-th best of the list as it was cut last.  The list is looked at between groups of 1, 2, 6, 16, 16 ... tiles (no
+// barrier inside a group: one per tile cost a third of the time), and cut back to k where more than k + k / 2 stand in it.  Of logits in no
+// particular order a few hundred pass.  Where a group's do not fit (an ascending row, many equal ones), what stood in the list ahead
+// of it is kept and its tiles are read again, each bounded by the k-th largest of the 256 threads' maxima, above which no more
+// than 16 k logits can lie.  Candidates are 64-bit keys (value, then lower index), so ties need no care.
 //
 // 2048 rows of 248320 with ranks: fp32 343 us with 20 alternatives (0.87 of HBM), 305 without; bf16 286 and 222, 14 instructions
 // per logit at 76 % of the issue slots.  -infinity as any other logit: 2 % of them masked 347 us in fp32 (393 where a tile that has one
@@ -29,7 +30,7 @@ constexpr int kLpPer = 16;                       // logits per thread and tile
 constexpr int kLpTile = kLpThreads * kLpPer;
 constexpr int kLpMaxTop = 64;
 constexpr int kLpMaxParts = 64;
-constexpr int kLpList = 2048;                    // candidates; 16 x 64 + 64 at least
+constexpr int kLpList = 2048;                    // candidates; 16 x 64 + 96 at least
 constexpr int kLpGroup = 16;                     // tiles between two looks at the list
 constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
 
@@ -229,6 +230,7 @@ __global__ void __launch_bounds__(kLpThreads, LpShape<T>::kPerSm) logprobs_kerne
     __shared__ Sums warps[kLpThreads / 32];
     __shared__ float bounds[kLpThreads / 32];
     __shared__ int filled;
+    __shared__ int stood;  // of the list's candidates, those of earlier groups of tiles: kept ones, and uncut ones behind them (thread 0's alone)
     const int tid = threadIdx.x, lane = tid & 31, K = p.K;
     const size_t row = blockIdx.x / p.parts;
     const int part = blockIdx.x - (int)row * p.parts;
@@ -266,7 +268,7 @@ __global__ void __launch_bounds__(kLpThreads, LpShape<T>::kPerSm) logprobs_kerne
     Sums v = {-INFINITY, 0.f, 0.f, 0};
     float kth = -INFINITY;  // what a logit has to exceed to be a candidate; in the first tile, to reach
     int kept = 0;           // candidates that stood in the list, sorted, after the last cut
-    if (tid == 0) filled = 0;
+    if (tid == 0) filled = stood = 0;
     auto cut = [&](int have) {  // the list's `have` candidates back to the best K, sorted; after a barrier
         if (have <= kLpThreads) {
             place_keys(list, have, K);
@@ -277,7 +279,7 @@ __global__ void __launch_bounds__(kLpThreads, LpShape<T>::kPerSm) logprobs_kerne
             sort_keys(list, n);
         }
         kept = min(have, K);
-        if (tid == 0) filled = kept;
+        if (tid == 0) filled = stood = kept;
         if (have >= K) kth = key_logit(list[K - 1]);
         __syncthreads();
     };
@@ -379,7 +381,7 @@ __global__ void __launch_bounds__(kLpThreads, LpShape<T>::kPerSm) logprobs_kerne
             const int have = filled;
             __syncthreads();
             if (have > kLpList) {
-                if (tid == 0) filled = kept;
+                if (tid == 0) filled = stood;  // these are still there: a group's candidates go behind them
                 for (int tile = next; tile < end; ++tile) {
                     float x[kLpPer];
                     const int at = first(tile);
@@ -392,6 +394,8 @@ __global__ void __launch_bounds__(kLpThreads, LpShape<T>::kPerSm) logprobs_kerne
                 }
             } else if (next == t0 || have > K + K / 2) {
                 cut(have);
+            } else if (tid == 0) {
+                stood = have;
             }
         }
         group = next == t0 ? 2 : min(kLpGroup, 3 * group);
