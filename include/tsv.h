@@ -261,6 +261,8 @@ tsv_status tsv_tree_verify_attention(const tsv_attn_desc* d, void* workspace, si
  *           row holds element 2j in its low nibble and 2j+1 in its high nibble;
  *           scales, biases: bf16 [V, H/64]; w = scale * q + bias, q in [0, 15].
  *   argmax  int32 [rows], out: index of the largest logit, ties -> lowest index.
+ *           A logit that is NaN counts as larger than every number if its sign
+ *           bit is clear, and as smaller if it is set.
  *   maxlogit float [rows] or NULL, out: that logit (fp32 accumulation).
  *   H % 64 == 0 (H % 256 == 0 for TSV_F16/TSV_BF16), 1 <= V < 2^31, rows >= 1.
  *   fp16 and bf16 heads with up to 4 rows stream the head once through CUDA

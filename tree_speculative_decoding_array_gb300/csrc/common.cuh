@@ -78,9 +78,12 @@ __device__ __forceinline__ float2 f16x2_to_f32x2(uint32_t u) {
 }
 
 // Monotone map of fp32 to uint32 (larger float -> larger integer), used to pack
-// (logit, index) into one 64-bit key for an atomic maximum.
+// (logit, index) into one 64-bit key for an atomic maximum.  A NaN without a sign lies above every number, one with a sign below.  The bits
+// are taken where the compiler cannot see that they are a float's: it makes a negation of the sign's flip otherwise, whose NaN has
+// other bits (those that rank as -0).
 __device__ __forceinline__ uint32_t orderable(float f) {
-    uint32_t u = __float_as_uint(f);
+    uint32_t u;
+    asm("mov.b32 %0, %1;" : "=r"(u) : "f"(f));
     return (u & 0x80000000u) ? ~u : (u | 0x80000000u);
 }
 __device__ __forceinline__ float unorderable(uint32_t o) {
