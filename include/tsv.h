@@ -612,6 +612,15 @@ tsv_status tsv_token_logprobs(const void* logits, int32_t logits_dtype, int32_t 
                               float temperature, int32_t top_k, float* logp, int32_t* rank, float* entropy,
                               int32_t* top_tokens, float* top_logp, void* workspace, size_t ws_bytes, cudaStream_t stream);
 
+/*
+ * tsv_greedy_tokens - what tsv_lm_head_argmax gives, of logits whose likeliest tokens tsv_token_logprobs has found: argmax
+ *   int32 [rows], the first of each row's top_tokens [rows, top_k], and its logit in maxlogit (float [rows] or NULL).  Rows without a
+ *   distribution, whose first token is -1, are searched: ties to the lower index, a NaN larger than every number if its
+ *   sign bit is clear and smaller if it is set.  logits float [rows, V] as in that call; top_k >= 1.
+ */
+tsv_status tsv_greedy_tokens(const float* logits, int32_t rows, int32_t V, const int32_t* top_tokens, int32_t top_k,
+                             int32_t* argmax, float* maxlogit, cudaStream_t stream);
+
 #ifdef __cplusplus
 }
 #endif

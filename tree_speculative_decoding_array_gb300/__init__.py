@@ -13,7 +13,7 @@ from ._abi import (ATTN_AUTO, ATTN_SIMT, ATTN_TCGEN05, BF16, E4M3_B128, F32, DEV
 from .api import (VerifyRound, append_desc, draft_children, tree_select, attention_workspace_size, attn_desc, gdn_commit, gdn_desc, gdn_scan, gdn_tree_verify, kv_desc, kv_gather_positions, gather_positions, lm_head_argmax,
                   lm_head_logits, lm_head_workspace_size, sample_nucleus, sample_workspace_size, sliding_band_mask, tree_accept_walk, tree_append, tree_mask,
                   tree_verify_attention,
-                  add_rms_norm, matmul_e4m3, matmul_e4m3_argmax, quantize_e4m3, token_logprobs, token_logprobs_workspace_size)
+                  add_rms_norm, greedy_tokens, matmul_e4m3, matmul_e4m3_argmax, quantize_e4m3, token_logprobs, token_logprobs_workspace_size)
 
 __all__ = [
     "load", "TsvError", "ATTN_AUTO", "ATTN_SIMT", "ATTN_TCGEN05", "DEV_TIMEOUT", "AttnDesc", "KvDesc", "F16", "BF16", "I8_SCALED", "Q4_G64", "MAX_T", "MAX_LAYERS",
@@ -22,4 +22,5 @@ __all__ = [
     "lm_head_argmax", "lm_head_logits", "sample_workspace_size", "sample_nucleus", "tree_accept_walk", "kv_desc", "kv_gather_positions", "gather_positions", "VerifyRound",
     "I4_G64", "DEV_BAD_SEQ_LEN", "GdnDesc", "gdn_desc", "gdn_tree_verify", "gdn_commit", "gdn_scan",
     "E4M3_B128", "F32", "add_rms_norm", "quantize_e4m3", "matmul_e4m3", "matmul_e4m3_argmax", "token_logprobs", "token_logprobs_workspace_size",
+    "greedy_tokens",
 ]

@@ -95,6 +95,7 @@ SIGNATURES = {
     "tsv_matmul_e4m3_argmax": (C.c_int, [_vp, _vp, _i32, _i32, _vp, _vp, _i32, _vp, _vp, _vp, _sz, _vp]),
     "tsv_token_logprobs_workspace_size": (_sz, [_i32, _i32, _i32]),
     "tsv_token_logprobs": (C.c_int, [_vp, _i32, _i32, _i32, _vp, C.c_float, _i32, _vp, _vp, _vp, _vp, _vp, _vp, _sz, _vp]),
+    "tsv_greedy_tokens": (C.c_int, [_vp, _i32, _i32, _vp, _i32, _vp, _vp, _vp]),
 }
 
 _lib = None

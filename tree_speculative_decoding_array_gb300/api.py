@@ -513,6 +513,19 @@ def token_logprobs(logits, targets=None, logp=None, *, rank=None, entropy=None, 
         None if k == 0 else _here("top_logp", f32, (rows, k), top_logp, dev), *_workspace(workspace, dev), st), "token_logprobs")
 
 
+def greedy_tokens(logits, top_tokens, argmax, *, maxlogit=None, stream=None):
+    """Each row's greedy token, argmax int32 [rows], and its logit, maxlogit fp32 [rows], as lm_head_argmax gives them: of logits fp32
+    [rows, V] and the likeliest tokens top_tokens int32 [rows, k] that token_logprobs has found."""
+    if logits.dim() != 2 or top_tokens.dim() != 2 or top_tokens.shape[1] == 0:
+        raise ValueError(f"logits must be [rows, V] and top_tokens [rows, k], got {tuple(logits.shape)} and {tuple(top_tokens.shape)}")
+    (rows, V), k = logits.shape, top_tokens.shape[1]
+    dev, st = _device_stream(stream)
+    check(load().tsv_greedy_tokens(
+        _here("logits", torch.float32, (rows, V), logits, dev), rows, V, _here("top_tokens", torch.int32, (rows, k), top_tokens, dev), k,
+        _here("argmax", torch.int32, (rows,), argmax, dev), None if maxlogit is None else _here("maxlogit", torch.float32, (rows,), maxlogit, dev), st),
+        "greedy_tokens")
+
+
 # ----------------------------------------------------------------------------- one verify round
 @dataclass
 class VerifyRound:
@@ -559,7 +572,9 @@ class VerifyRound:
                            # weight_offset of add_rms_norm; writes hidden (which may be None: a buffer of the round's, or
                            # 8-bit rows in outs["hidden8"] and outs["hidden8_scale"] ahead of an e4m3 head)
     logprobs: int = None   # log probabilities (optional): this many likeliest tokens of every node in outs["top_tokens"]
-                           # and outs["top_logp"], the node's own token's in outs["logp"], the entropy in outs["entropy"]
+                           # and outs["top_logp"], the node's own token's in outs["logp"], the entropy in outs["entropy"], all
+                           # of softmax(logits), whatever temperature sample draws at; the tokens stay as they are without
+                           # (a row without a distribution has its argmax as token, NaN as logp and -1 as top_tokens)
     outs: dict = field(default_factory=dict)
 
     def __post_init__(self):
@@ -683,8 +698,7 @@ class VerifyRound:
             token_logprobs(o["logits"], o["argmax"] if drawn else None, o["logp"] if drawn else None, entropy=o["entropy"],
                            top_tokens=o.get("top_tokens"), top_logp=o.get("top_logp"), workspace=self.logprobs_ws, stream=stream)
             if not drawn:
-                with torch.cuda.stream(stream):
-                    o["argmax"].copy_(o["top_tokens"][:, 0])
+                greedy_tokens(o["logits"], o["top_tokens"], o["argmax"], maxlogit=o["maxlogit"], stream=stream)
 
     def capture(self, stages=("mask", "append", "attn", "gdn", "norm", "lm", "walk", "gather", "commit")):
         """Record ``run(stages)`` once as a CUDA graph over this round's buffers.

@@ -483,6 +483,41 @@ __global__ void __launch_bounds__(kLpThreads) logprobs_join_kernel(const Logprob
         if (lane + h * 32 < p.K) res.write_top(p, row, lane + h * 32, mine[h]);
 }
 
+// The greedy token and its logit of every row, where the row's likeliest token is known: that one.  A row without a distribution has none, and
+// a CTA looks for the largest of its logits in the order of the LM heads' argmax (as pack_best() ranks them), so that a round's
+// tokens do not depend on whether it asks for log probabilities.  Two loads and two stores per row (2048 rows 1.9 us), but for such rows (one of
+// 248320 57 us: its CTA's loads, latency; 2048 of them 386, near HBM's rate).
+__global__ void __launch_bounds__(kLpThreads) greedy_tokens_kernel(const float* __restrict__ logits, int rows, int V,
+                                                                   const int32_t* __restrict__ top_tokens, int K,
+                                                                   int32_t* __restrict__ argmax, float* __restrict__ maxlogit) {
+    griddep_begin();
+    __shared__ unsigned long long bests[kLpThreads / 32];
+    for (int row = blockIdx.x; row < rows; row += gridDim.x) {
+        const float* x = logits + (size_t)row * V;
+        int token = top_tokens[(size_t)row * K];
+        float value;
+        if (token >= 0 && token < V) {
+            value = x[token];
+        } else {
+            unsigned long long best = 0ull;
+#pragma unroll 4
+            for (int i = threadIdx.x; i < V; i += kLpThreads) best = max(best, pack_best(x[i], (uint32_t)i));
+            best = warp_largest(best);
+            __syncthreads();  // of a row before this one, every thread has read its bests
+            if ((threadIdx.x & 31) == 0) bests[threadIdx.x >> 5] = best;
+            __syncthreads();
+#pragma unroll
+            for (int w = 0; w < kLpThreads / 32; ++w) best = max(best, bests[w]);
+            token = key_token(best);
+            value = key_logit(best);
+        }
+        if (threadIdx.x == 0) {
+            argmax[row] = token;
+            if (maxlogit) maxlogit[row] = value;
+        }
+    }
+}
+
 // Parts of a row, half a tile at least in each (every thread then has a logit, and the first bound comes from the warps): as many as fill the GPU once, or twice where once would leave more than a quarter of its
 // places empty (400 rows of 248320: 3 parts 98 us, one 126; 512: 2 parts 124, one 130; 300 rows, which fill 0.79: 2 parts 82, 5 parts 83).
 template <typename T>
@@ -541,4 +576,18 @@ extern "C" tsv_status tsv_token_logprobs(const void* logits, int32_t logits_dtyp
     else if (logits_dtype == TSV_BF16) launch_logprobs<__nv_bfloat16>(p, workspace, stream);
     else launch_logprobs<__half>(p, workspace, stream);
     return check_launch("token_logprobs");
+}
+
+extern "C" tsv_status tsv_greedy_tokens(const float* logits, int32_t rows, int32_t V, const int32_t* top_tokens, int32_t top_k,
+                                        int32_t* argmax, float* maxlogit, cudaStream_t stream) {
+    using namespace tsv;
+    clear_error();
+    if (rows < 0 || V < 1 || V > (1 << 24) || top_k < 1)
+        return fail(TSV_EINVAL, "greedy_tokens: rows=%d V=%d (1 .. 2^24) top_k=%d", rows, V, top_k);
+    if (rows == 0) return TSV_OK;
+    if (!logits || !top_tokens || !argmax) return fail(TSV_EINVAL, "greedy_tokens: null pointer argument");
+    if (((uintptr_t)logits | (uintptr_t)top_tokens | (uintptr_t)argmax | (uintptr_t)maxlogit) & 3)
+        return fail(TSV_EINVAL, "greedy_tokens: a buffer is not aligned to its elements");
+    launch_pdl(greedy_tokens_kernel, std::min(rows, sm_count() * 8), kLpThreads, 0, stream, logits, rows, V, top_tokens, top_k, argmax, maxlogit);
+    return check_launch("greedy_tokens");
 }
