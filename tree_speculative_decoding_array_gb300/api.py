@@ -32,6 +32,18 @@ def _stream(stream):
     return C.c_void_p(stream.cuda_stream)
 
 
+def _scratch(nbytes, device, stream):
+    """A workspace of the call's own, allocated on the stream that the call runs on: once it is let go, only that stream's later work gets
+    its memory."""
+    n = max(int(nbytes), 256)
+    if stream is None:
+        return torch.empty(n, dtype=torch.uint8, device=device)
+    if not isinstance(stream, torch.cuda.Stream):
+        stream = torch.cuda.ExternalStream(stream.cuda_stream, device=device)
+    with torch.cuda.stream(stream):
+        return torch.empty(n, dtype=torch.uint8, device=device)
+
+
 def _cuda(t, name, dtype=None, shape=None):
     if t is None:
         return
@@ -95,8 +107,7 @@ def draft_children(draft_logits, child_tokens, child_logp, *, top_k, workspace=N
     _cuda(child_tokens, "child_tokens", torch.int32, (rows, top_k))
     _cuda(child_logp, "child_logp", torch.float32, (rows, top_k))
     if workspace is None:
-        workspace = torch.empty(max(int(lib.tsv_draft_children_workspace_size(rows, V, top_k)), 256),
-                                dtype=torch.uint8, device=draft_logits.device)
+        workspace = _scratch(lib.tsv_draft_children_workspace_size(rows, V, top_k), draft_logits.device, stream)
     check(lib.tsv_draft_children(_p(draft_logits), rows, V, int(top_k), _p(child_tokens), _p(child_logp),
                                  _p(workspace), workspace.numel(), _stream(stream)), "draft_children")
 
@@ -216,7 +227,7 @@ def lm_head_argmax(hidden, W, argmax, *, w_dtype, V, scales=None, biases=None, m
     if maxlogit is not None:
         _cuda(maxlogit, "maxlogit", torch.float32, (rows,))
     if workspace is None:
-        workspace = torch.empty(lm_head_workspace_size(rows, H, V, w_dtype), dtype=torch.uint8, device=hidden.device)
+        workspace = _scratch(lm_head_workspace_size(rows, H, V, w_dtype), hidden.device, stream)
     ws_bytes = workspace.numel() * workspace.element_size()
     check(lib.tsv_lm_head_argmax(_p(hidden), rows, H, V, w_dtype, _p(W), _p(scales), _p(biases), _p(argmax),
                                  _p(maxlogit), _p(workspace), ws_bytes, _stream(stream)), "lm_head_argmax")
@@ -231,8 +242,7 @@ def lm_head_logits(hidden, W, logits, *, w_dtype, V, scales=None, biases=None, w
         _e4m3_head(hidden, W, scales, V, H)
     _cuda(logits, "logits", torch.float32, (rows, V))
     if workspace is None:
-        workspace = torch.empty(max(lm_head_workspace_size(rows, H, V, w_dtype), 256), dtype=torch.uint8,
-                                device=hidden.device)
+        workspace = _scratch(lm_head_workspace_size(rows, H, V, w_dtype), hidden.device, stream)
     check(lib.tsv_lm_head_logits(_p(hidden), rows, H, V, w_dtype, _p(W), _p(scales), _p(biases), _p(logits),
                                  _p(workspace), workspace.numel(), _stream(stream)), "lm_head_logits")
 
@@ -248,8 +258,7 @@ def sample_nucleus(logits, uniforms, tokens, *, temperature, top_k, top_p, works
     _cuda(uniforms, "uniforms", torch.float32, (rows,))
     _cuda(tokens, "tokens", torch.int32, (rows,))
     if workspace is None:
-        workspace = torch.empty(max(sample_workspace_size(rows, V, top_k), 256), dtype=torch.uint8,
-                                device=logits.device)
+        workspace = _scratch(sample_workspace_size(rows, V, top_k), logits.device, stream)
     check(lib.tsv_sample_nucleus(_p(logits), rows, V, float(temperature), int(top_k), float(top_p), _p(uniforms),
                                  _p(tokens), _p(workspace), workspace.numel(), _stream(stream)), "sample_nucleus")
 
@@ -470,7 +479,7 @@ def matmul_e4m3_argmax(a, a_scale, w, w_scale, argmax, *, maxval=None, workspace
     args = _product(a, a_scale, w, w_scale, dev)
     rows = args[2]
     if workspace is None:
-        workspace = torch.empty(max(lib.tsv_matmul_e4m3_argmax_workspace_size(rows), 256), dtype=torch.uint8, device=a.device)
+        workspace = _scratch(lib.tsv_matmul_e4m3_argmax_workspace_size(rows), a.device, stream)
     check(lib.tsv_matmul_e4m3_argmax(
         *args, _here("argmax", torch.int32, (rows,), argmax, dev),
         None if maxval is None else _here("maxval", torch.float32, (rows,), maxval, dev), *_workspace(workspace, dev), st),
@@ -501,7 +510,7 @@ def token_logprobs(logits, targets=None, logp=None, *, rank=None, entropy=None, 
         raise ValueError("top_tokens has room for no token")
     lib = load()
     if workspace is None:
-        workspace = torch.empty(max(token_logprobs_workspace_size(rows, V, k), 256), dtype=torch.uint8, device=logits.device)
+        workspace = _scratch(token_logprobs_workspace_size(rows, V, k), logits.device, stream)
     dev, st = _device_stream(stream)
     f32, i32, each = torch.float32, torch.int32, (rows,)
     check(lib.tsv_token_logprobs(
