@@ -578,6 +578,8 @@ tsv_status tsv_quantize_e4m3(const void* x, int32_t rows, int32_t H, int32_t dty
  *   features are summed on the tensor cores into fp32, scaled, and summed in fp32; out is rounded once.  The same inputs
  *   give the same bits in every call.
  *   K % 16 == 0, a and w 16-byte aligned, 0 <= rows <= 2^30, 1 <= N <= 2^30.
+ *   Every wait inside the kernel is bounded.  These calls have no status word: should a wait run out, the part of out that it was
+ *   for is NaN (of the argmax: those rows' maxval).
  * tsv_matmul_e4m3_argmax - the same product with its argmax, as tsv_lm_head_argmax: argmax int32 [rows] (ties to the lowest
  *   index), maxval float [rows] or NULL; the products are never written.  Workspace: tsv_matmul_e4m3_argmax_workspace_size.
  *   A product that is NaN counts as larger than every number if its sign bit is clear, and as smaller if it is set.

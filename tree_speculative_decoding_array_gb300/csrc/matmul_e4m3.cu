@@ -136,6 +136,13 @@ __device__ __forceinline__ void store_rows(T* o, const float (&acc)[COLS], size_
     }
 }
 
+// One element of the output.
+__device__ __forceinline__ void put(const E4Product& p, size_t at, float x) {
+    if (p.out_dtype == TSV_F32) ((float*)p.out)[at] = x;
+    else if (p.out_dtype == TSV_BF16) ((__nv_bfloat16*)p.out)[at] = __float2bfloat16_rn(x);
+    else ((__half*)p.out)[at] = __float2half_rn(x);
+}
+
 template <int BN, bool PAIR>
 __global__ void __launch_bounds__(MmShape<BN, PAIR>::kThreads, MmShape<BN, PAIR>::kPerSm)
     matmul_e4m3_kernel(const __grid_constant__ MmParams q) {
@@ -406,6 +413,25 @@ __global__ void __launch_bounds__(MmShape<BN, PAIR>::kThreads, MmShape<BN, PAIR>
         }
     }
     __syncthreads();
+    // A wait of this CTA ran out (its copies and MMAs have ended, or had their time to): NaN is what its tiles hold, or what it adds to
+    // the cluster's sums, so that no reader takes what is missing for a product.  By the epilogue's warps, which have registers for it.
+    if (*abort_flag && warp < S::kEpiWarps) {
+        constexpr int kThreads = S::kEpiWarps * 32;
+        const float nan = __int_as_float(0x7FFFFFFF);
+        if (!PAIR && split > 1)
+            for (int e = threadIdx.x; e < kMmRows * BN; e += kThreads) reinterpret_cast<float*>(ring)[e] = nan;
+        else
+            for (int t = first; t < tiles; t += step) {
+                int m, n;
+                place(t, m, n);
+                const int row0 = (m * CTAS + rank) * kMmRows, rows = min(kMmRows, q.p.rows - row0), cols = min(BN, q.p.N - n * BN);
+                for (int r = 0; r < rows; ++r) {
+                    if (q.p.best && threadIdx.x == 0) atomicMax(&q.p.best[row0 + r], pack_best(nan, (uint32_t)(n * BN)));
+                    if (!q.p.best)
+                        for (int c = threadIdx.x; c < cols; c += kThreads) put(q.p, (size_t)(row0 + r) * q.p.N + n * BN + c, nan);
+                }
+            }
+    }
     if (!PAIR && split > 1) {
         // every CTA of the cluster adds up, share by share, its part of the tile's columns, and writes them
         tc::cluster_sync();
@@ -433,9 +459,7 @@ __global__ void __launch_bounds__(MmShape<BN, PAIR>::kThreads, MmShape<BN, PAIR>
 #pragma unroll
             for (int j = 0; j < 4; ++j) {
                 if (col + j >= q.p.N) break;
-                if (q.p.out_dtype == TSV_F32) ((float*)q.p.out)[o + j] = x[j];
-                else if (q.p.out_dtype == TSV_BF16) ((__nv_bfloat16*)q.p.out)[o + j] = __float2bfloat16_rn(x[j]);
-                else ((__half*)q.p.out)[o + j] = __float2half_rn(x[j]);
+                put(q.p, o + j, x[j]);
             }
         }
         tc::cluster_sync();  // no CTA goes while another reads its sums
