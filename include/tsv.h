@@ -576,7 +576,8 @@ tsv_status tsv_quantize_e4m3(const void* x, int32_t rows, int32_t H, int32_t dty
  *   a: e4m3 [rows, K], a_scale float [rows, ceil(K / 128)] (8-bit rows as above); w: e4m3 [N, K], w_scale float
  *   [ceil(N / 128), ceil(K / 128)]; out [rows, N] of out_dtype (TSV_BF16, TSV_F16 or TSV_F32).  The products of 128
  *   features are summed on the tensor cores into fp32, scaled, and summed in fp32; out is rounded once.  The same inputs
- *   give the same bits in every call.
+ *   give the same bits in every call.  A block's scale is a_scale w_scale rounded to fp32 ahead of its sums: below fp32's
+ *   normal numbers (2^-126) it has fewer bits, beyond its range it is an infinity.
  *   K % 16 == 0, a and w 16-byte aligned, 0 <= rows <= 2^30, 1 <= N <= 2^30.
  *   Every wait inside the kernel is bounded.  These calls have no status word: should a wait run out, the part of out that it was
  *   for is NaN (of the argmax: those rows' maxval).
@@ -584,7 +585,7 @@ tsv_status tsv_quantize_e4m3(const void* x, int32_t rows, int32_t H, int32_t dty
  *   index), maxval float [rows] or NULL; the products are never written.  Workspace: tsv_matmul_e4m3_argmax_workspace_size.
  *   A product that is NaN counts as larger than every number if its sign bit is clear, and as smaller if it is set.
  * tsv_lm_head_argmax, tsv_lm_head_logits with w_dtype TSV_E4M3_B128: W as w, scales as w_scale, biases ignored; hidden
- *   (bf16) becomes 8-bit rows in the workspace first.  H % 16 == 0, rows and V at most 2^30.
+ *   (bf16) becomes 8-bit rows in the workspace first.  H % 16 == 0, H >= 64, rows and V at most 2^30.
  */
 tsv_status tsv_matmul_e4m3(const void* a, const float* a_scale, int32_t rows, int32_t K, const void* w, const float* w_scale,
                            int32_t N, void* out, int32_t out_dtype, cudaStream_t stream);
@@ -598,7 +599,8 @@ tsv_status tsv_matmul_e4m3_argmax(const void* a, const float* a_scale, int32_t r
 /*
  * tsv_token_logprobs - what a user asks about emitted tokens, from one read of the logits:
  *     z = logits / temperature;  logp(t) = z_t - log(sum exp(z));  entropy = -sum p log p with p = softmax(z)
- *   logits [rows, V] of logits_dtype (TSV_F32, TSV_BF16 or TSV_F16; each row may start anywhere: V needs no alignment).
+ *   logits [rows, V] of logits_dtype (TSV_F32, TSV_BF16 or TSV_F16; each row may start anywhere: V needs no alignment),
+ *   1 <= V <= 2^24.
  *   targets int32 [rows] or NULL; logp float [rows]: each target's log probability; rank int32 [rows] or NULL: how many
  *   tokens have a larger logit, or an equal one and a lower index (0: the greedy choice).  With targets NULL, logp and
  *   rank are NULL too.  entropy float [rows] or NULL.  top_tokens int32, top_logp float [rows, top_k]: the top_k largest,

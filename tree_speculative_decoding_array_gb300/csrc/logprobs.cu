@@ -518,8 +518,9 @@ __global__ void __launch_bounds__(kLpThreads) greedy_tokens_kernel(const float* 
     }
 }
 
-// Parts of a row, half a tile at least in each (every thread then has a logit, and the first bound comes from the warps): as many as fill the GPU once, or twice where once would leave more than a quarter of its
-// places empty (400 rows of 248320: 3 parts 98 us, one 126; 512: 2 parts 124, one 130; 300 rows, which fill 0.79: 2 parts 82, 5 parts 83).
+// Parts of a row, half a tile at least in each (every thread then has a logit, and the first bound comes from the warps): as many as fill the
+// GPU once, or twice where once would leave more than a quarter of its places empty (400 rows of 248320: 3 parts 98 us, one 126; 512: 2
+// parts 124, one 130; 300 rows, which fill 0.79: 2 parts 82, 5 parts 83).
 template <typename T>
 static int logprob_parts(int rows, int V) {
     const int places = sm_count() * LpShape<T>::kPerSm, once = places / rows, tiles = (V + kLpTile / 2) / kLpTile;
@@ -570,7 +571,8 @@ extern "C" tsv_status tsv_token_logprobs(const void* logits, int32_t logits_dtyp
     if (need && !workspace) return fail(TSV_EINVAL, "token_logprobs: null workspace");
     if ((uintptr_t)workspace & 15) return fail(TSV_EINVAL, "token_logprobs: workspace not 16-byte aligned");
     if (ws_bytes < need) return fail(TSV_ECAPACITY, "token_logprobs: workspace %zu < %zu bytes", ws_bytes, need);
-    if ((long long)rows * std::max(logprob_parts<float>(rows, V), logprob_parts<__half>(rows, V)) > INT_MAX) return fail(TSV_ECAPACITY, "token_logprobs: rows=%d", rows);
+    if ((long long)rows * std::max(logprob_parts<float>(rows, V), logprob_parts<__half>(rows, V)) > INT_MAX)
+        return fail(TSV_ECAPACITY, "token_logprobs: rows=%d", rows);
     const LogprobParams p = {logits, targets, rows, V, top_k, 1, 1.f / temperature, logp, entropy, top_logp, rank, top_tokens};
     if (logits_dtype == TSV_F32) launch_logprobs<float>(p, workspace, stream);
     else if (logits_dtype == TSV_BF16) launch_logprobs<__nv_bfloat16>(p, workspace, stream);

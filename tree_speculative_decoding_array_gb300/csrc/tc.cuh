@@ -46,15 +46,7 @@ __device__ __forceinline__ bool mbar_try_wait(uint32_t bar, uint32_t parity) {  
         : "memory");
     return ok != 0;
 }
-__device__ __forceinline__ bool mbar_try_wait(uint64_t* bar, uint32_t parity) {
-    uint32_t ok;
-    asm volatile(
-        "{\n .reg .pred p;\n mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n selp.u32 %0, 1, 0, p;\n}"
-        : "=r"(ok)
-        : "r"(smem_u32(bar)), "r"(parity)
-        : "memory");
-    return ok != 0;
-}
+__device__ __forceinline__ bool mbar_try_wait(uint64_t* bar, uint32_t parity) { return mbar_try_wait(smem_u32(bar), parity); }
 
 // Non-blocking test of the phase with the given parity, by the barrier's shared-memory address.
 __device__ __forceinline__ bool mbar_test(uint32_t bar, uint32_t parity) {
@@ -66,16 +58,7 @@ __device__ __forceinline__ bool mbar_test(uint32_t bar, uint32_t parity) {
         : "memory");
     return ok != 0;
 }
-// The same.
-__device__ __forceinline__ bool mbar_test(uint64_t* bar, uint32_t parity) {
-    uint32_t ok;
-    asm volatile(
-        "{\n .reg .pred p;\n mbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n selp.u32 %0, 1, 0, p;\n}"
-        : "=r"(ok)
-        : "r"(smem_u32(bar)), "r"(parity)
-        : "memory");
-    return ok != 0;
-}
+__device__ __forceinline__ bool mbar_test(uint64_t* bar, uint32_t parity) { return mbar_test(smem_u32(bar), parity); }
 
 // Waits for the phase with the given parity to complete, polling with the non-suspending test_wait (a warp
 // parked in a suspending try_wait was seen to resume microseconds after the phase completed, which puts that
@@ -311,13 +294,13 @@ __device__ __forceinline__ void mma_e4m3_block(uint32_t d_tmem, uint64_t a, uint
         asm volatile(
             "{\n .reg .pred e, n, y;\n .reg .b64 a1, a2, a3, b1, b2, b3;\n elect.sync _|e, 0xffffffff;\n"
             " setp.ne.u32 n, 0, 0;\n setp.eq.u32 y, 0, 0;\n"
- "add.s64 a1, %1, 2;\n add.s64 b1, %2, 2;\n"
- "add.s64 a2, %1, 4;\n add.s64 b2, %2, 4;\n"
- "add.s64 a3, %1, 6;\n add.s64 b3, %2, 6;\n"
- "@e tcgen05.mma.cta_group::2.kind::f8f6f4 [%0], %1, %2, %3, n;\n"
- "@e tcgen05.mma.cta_group::2.kind::f8f6f4 [%0], a1, b1, %3, y;\n"
- "@e tcgen05.mma.cta_group::2.kind::f8f6f4 [%0], a2, b2, %3, y;\n"
- "@e tcgen05.mma.cta_group::2.kind::f8f6f4 [%0], a3, b3, %3, y;\n"
+            " add.s64 a1, %1, 2;\n add.s64 b1, %2, 2;\n"
+            " add.s64 a2, %1, 4;\n add.s64 b2, %2, 4;\n"
+            " add.s64 a3, %1, 6;\n add.s64 b3, %2, 6;\n"
+            " @e tcgen05.mma.cta_group::2.kind::f8f6f4 [%0], %1, %2, %3, n;\n"
+            " @e tcgen05.mma.cta_group::2.kind::f8f6f4 [%0], a1, b1, %3, y;\n"
+            " @e tcgen05.mma.cta_group::2.kind::f8f6f4 [%0], a2, b2, %3, y;\n"
+            " @e tcgen05.mma.cta_group::2.kind::f8f6f4 [%0], a3, b3, %3, y;\n"
             " @e tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%4], %6;\n"
             " @e tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%5], %6;\n}" ::"r"(d_tmem),
             "l"(a), "l"(b), "r"(idesc), "r"(smem_u32(free_bar)), "r"(smem_u32(done_bar)), "h"((uint16_t)3)
@@ -326,13 +309,13 @@ __device__ __forceinline__ void mma_e4m3_block(uint32_t d_tmem, uint64_t a, uint
         asm volatile(
             "{\n .reg .pred e, n, y;\n .reg .b64 a1, a2, a3, b1, b2, b3;\n elect.sync _|e, 0xffffffff;\n"
             " setp.ne.u32 n, 0, 0;\n setp.eq.u32 y, 0, 0;\n"
- "add.s64 a1, %1, 2;\n add.s64 b1, %2, 2;\n"
- "add.s64 a2, %1, 4;\n add.s64 b2, %2, 4;\n"
- "add.s64 a3, %1, 6;\n add.s64 b3, %2, 6;\n"
- "@e tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], %1, %2, %3, n;\n"
- "@e tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], a1, b1, %3, y;\n"
- "@e tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], a2, b2, %3, y;\n"
- "@e tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], a3, b3, %3, y;\n"
+            " add.s64 a1, %1, 2;\n add.s64 b1, %2, 2;\n"
+            " add.s64 a2, %1, 4;\n add.s64 b2, %2, 4;\n"
+            " add.s64 a3, %1, 6;\n add.s64 b3, %2, 6;\n"
+            " @e tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], %1, %2, %3, n;\n"
+            " @e tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], a1, b1, %3, y;\n"
+            " @e tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], a2, b2, %3, y;\n"
+            " @e tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], a3, b3, %3, y;\n"
             " @e tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%4];\n"
             " @e tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%5];\n}" ::"r"(d_tmem),
             "l"(a), "l"(b), "r"(idesc), "r"(smem_u32(free_bar)), "r"(smem_u32(done_bar))
