@@ -543,7 +543,7 @@ class VerifyRound:
     Caches (k, v[, k_scale, v_scale]) and the LM head are resident state; the
     per-round inputs are parents, tokens, q (per layer), hidden and kv_len.
     The int32 results (path, path_len, emitted, argmax) are views into one
-    block, ``outs["result"]``.
+    block, ``outs["result"]``.  ``outs["maxlogit"]`` is written by greedy rounds.
     """
     T: int
     HQ: int

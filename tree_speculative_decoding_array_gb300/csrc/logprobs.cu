@@ -15,8 +15,8 @@
 // of it is kept and its tiles are read again, each bounded by the k-th largest of the 256 threads' maxima, above which no more
 // than 16 k logits can lie.  Candidates are 64-bit keys (value, then lower index), so ties need no care.
 //
-// 2048 rows of 248320 with ranks: fp32 343 us with 20 alternatives (0.87 of HBM), 305 without; bf16 286 and 222, 14 instructions
-// per logit at 76 % of the issue slots.  -infinity as any other logit: 2 % of them masked 347 us in fp32 (393 where a tile that has one
+// 2048 rows of 248320 with ranks of likely tokens: fp32 338 us with 20 alternatives (0.89 of HBM), 304 without; bf16 286 and 222, of
+// random tokens 304 and 227, 14 to 17 instructions per logit at 76 % of the issue slots.  -infinity as any other logit: 2 % of them masked 347 us in fp32 (393 where a tile that has one
 // was summed again).
 #include <algorithm>
 
