@@ -16,8 +16,8 @@
 // than 16 k logits can lie.  Candidates are 64-bit keys (value, then lower index), so ties need no care.
 //
 // 2048 rows of 248320 with ranks of likely tokens: fp32 338 us with 20 alternatives (0.89 of HBM), 304 without; bf16 286 and 222, of
-// random tokens 304 and 227, 14 to 17 instructions per logit at 76 % of the issue slots.  -infinity as any other logit: 2 % of them masked 347 us in fp32 (393 where a tile that has one
-// was summed again).
+// random tokens 304 and 227, 14 to 17 instructions per logit at 76 % of the issue slots.  -infinity as any other logit: 2 % of them
+// masked 340 us in fp32 (393 where a tile that has one was summed again).
 #include <algorithm>
 
 #include "e4m3.cuh"
